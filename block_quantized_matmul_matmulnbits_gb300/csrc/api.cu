@@ -84,7 +84,8 @@ int device_setup(int* sm_count, unsigned int** status = nullptr) {
         }
         if (mnb::gemv_prepare() != cudaSuccess || mnb::gemm_prepare() != cudaSuccess ||
             mnb::lora_down_prepare() != cudaSuccess || mnb::decode_prepare() != cudaSuccess ||
-            mnb::decode_mt_prepare() != cudaSuccess ||
+            mnb::decode_mt_prepare() != cudaSuccess || mnb::attn_prepare() != cudaSuccess ||
+            mnb::logprobs_prepare() != cudaSuccess ||
             cudaGetSymbolAddress(&st, mnb::g_status) != cudaSuccess) {
             cudaGetLastError();
             return MNB_ERR_CUDA;
@@ -218,6 +219,8 @@ int make_plan(const mnb_desc& d, int64_t batch, int64_t M, int rank, int sms, mn
 }
 
 }  // namespace
+
+int mnb::device_ready(int* sm_count, unsigned int** status) { return device_setup(sm_count, status); }
 
 extern "C" {
 

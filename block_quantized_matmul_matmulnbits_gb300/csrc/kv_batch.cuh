@@ -1,0 +1,91 @@
+// kv_batch.cuh -- the paged 8-bit cache and the batch of sequences as the
+// kernels see them, and how a kernel finds the sequence of its work item.
+#pragma once
+
+#include <stdint.h>
+
+#include "mnb_internal.h"
+
+namespace mnb {
+
+constexpr int kKvBlock = MNB_KV_BLOCK;  // tokens that share a scale
+
+struct KvArgs {
+    const int32_t* table;   // [seqs, max_pages]
+    const int32_t* kv_len;  // [seqs]
+    const int32_t* q_start; // [seqs + 1]
+    int64_t num_pages;
+    int64_t max_tokens;     // max_pages * page_size, at most 2^31 - 1
+    int seqs, max_pages, tokens;
+    int page_shift;         // log2(page_size)
+    int kv_heads, head_dim;
+};
+
+inline KvArgs kv_args(const mnb_kv_cache* c, const mnb_kv_batch* b) {
+    KvArgs a;
+    a.table = b->page_table;
+    a.kv_len = b->kv_len;
+    a.q_start = b->q_start;
+    a.num_pages = c->num_pages;
+    a.page_shift = 0;
+    while ((1 << a.page_shift) < c->page_size) ++a.page_shift;
+    a.max_tokens = (int64_t)b->max_pages << a.page_shift;
+    if (a.max_tokens > INT32_MAX) a.max_tokens = INT32_MAX;
+    a.seqs = b->seqs;
+    a.max_pages = b->max_pages;
+    a.tokens = (int)b->tokens;
+    a.kv_heads = c->kv_heads;
+    a.head_dim = c->head_dim;
+    return a;
+}
+
+// Work items of a sequence are numbered without a prefix sum over the batch:
+// sequence s owns the items from first_item(s) = (q_start[s] * mul >> 4) +
+// extra * s on.  The floor of the difference of two sums is at most one below
+// the difference of the floors, so a sequence of n tokens always owns at least
+// floor(n * mul / 16) + extra items: with extra = 1 enough for its groups of 16
+// rows, with extra = 2 for the aligned blocks of 16 positions it touches (the
+// first and the last partly).  Surplus items find nothing to do.
+__host__ __device__ inline int64_t kv_items(int64_t tokens, int seqs, int mul, int extra) {
+    return ((tokens * mul) >> 4) + (int64_t)extra * seqs;
+}
+
+// The sequence that owns item `u`, and its first item: a 32-way search by the
+// whole warp (two rounds of loads up to 1024 sequences).
+__device__ __forceinline__ int kv_find_seq(const KvArgs& a, int64_t u, int mul, int extra, int64_t* first) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0, hi = a.seqs;
+    int64_t at_lo = 0;
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 31) >> 5;
+        const int s = lo + lane * step;
+        int64_t at = INT64_MAX;
+        if (s < hi) at = (((int64_t)__ldg(a.q_start + s) * mul) >> 4) + (int64_t)extra * s;
+        const unsigned le = __ballot_sync(0xffffffffu, at <= u);
+        const int k = le ? 31 - __clz(le) : 0;  // the first item of `lo` is never past u
+        at_lo = __shfl_sync(0xffffffffu, at, k);
+        lo += k * step;
+        hi = min(hi, lo + step);
+    }
+    if (a.seqs == 1) at_lo = ((int64_t)__ldg(a.q_start) * mul) >> 4;
+    *first = at_lo;
+    return lo;
+}
+
+// Length of sequence s, and its tokens of this call: rows row0 .. row0 + n - 1 are the
+// positions len - n .. len - 1 (the first ones may lie before 0).
+__device__ __forceinline__ void kv_sequence(const KvArgs& a, int s, int* len, int* row0, int* n) {
+    const int q0 = __ldg(a.q_start + s), q1 = __ldg(a.q_start + s + 1);
+    const int l = __ldg(a.kv_len + s);
+    *len = l < 0 ? 0 : (int)min((int64_t)l, a.max_tokens);
+    *row0 = q0;
+    *n = q1 > q0 ? q1 - q0 : 0;
+}
+
+// Page of position `pos` (below max_tokens) of sequence s, or -1.
+__device__ __forceinline__ int kv_page(const KvArgs& a, int s, int pos) {
+    const int p = __ldg(a.table + (int64_t)s * a.max_pages + (pos >> a.page_shift));
+    return p >= 0 && p < a.num_pages ? p : -1;
+}
+
+}  // namespace mnb

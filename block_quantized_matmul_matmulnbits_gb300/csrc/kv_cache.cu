@@ -1,0 +1,266 @@
+// kv_cache.cu -- writing tokens into the 8-bit key/value cache and reading
+// them back (mnb_kv_write, mnb_kv_read).
+//
+// One warp takes one block of 16 positions of one kv head, keys or values: the
+// 16 rows that share a scale, 1 or 2 KB of codes that lie together in the
+// page.  All of the block's rows are loaded at once (up to eight 16-byte loads
+// a lane in flight), the largest magnitude is found with shuffles, and the
+// rows go out as 8-byte stores of whole 64- or 128-byte code rows: the tokens
+// are read once and nothing waits on another warp.  Both directions are bound
+// by memory: 2 bytes in and 1 out a value (written), 1 in and 2 out (read).
+// The alternative split, one warp a token, needs the block's scale agreed
+// between 16 warps.
+//
+// The magnitude is taken on the FP16 bit patterns without their sign, which
+// order as unsigned integers with NaN above infinity above every finite value,
+// so a non-finite value reaches the scale without a test of its own.
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "kv_batch.cuh"
+#include "mnb_internal.h"
+
+namespace mnb {
+
+namespace {
+
+constexpr int kWarps = 8;
+
+struct KvIoArgs {
+    KvArgs b;
+    int64_t items;
+    int64_t row_stride;  // halfs
+    uint8_t *k_codes, *v_codes;
+    float *k_scales, *v_scales;
+    __half *k, *v;
+};
+
+// The block of one warp: where its codes and scale lie, and which positions are the call's.
+struct KvUnit {
+    int which, head;
+    int lo, first, len;    // first position of the block; of the call's tokens; the sequence's length
+    int64_t row0;          // token row of position `first`
+    int64_t slot;          // row of the cache (page, head, row in page) of position lo
+};
+
+// False: nothing to do (the whole warp together).
+__device__ __forceinline__ bool kv_unit(const KvIoArgs& p, KvUnit& u) {
+    const KvArgs& a = p.b;
+    const int64_t w = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const int combos = 2 * a.kv_heads;
+    const int64_t item = w / combos;
+    if (item >= p.items) return false;
+    const int c = (int)(w - item * combos);
+    u.which = c >= a.kv_heads;
+    u.head = u.which ? c - a.kv_heads : c;
+    int64_t first_item;
+    const int s = kv_find_seq(a, item, 1, 2, &first_item);
+    int row0, n;
+    kv_sequence(a, s, &u.len, &row0, &n);
+    u.first = u.len - n;
+    u.row0 = row0;
+    const int64_t lo = ((int64_t)((u.first > 0 ? u.first : 0) >> 4) + (item - first_item)) * kKvBlock;
+    if (n == 0 || lo < 0 || lo >= u.len) return false;
+    u.lo = (int)lo;
+    const int page = kv_page(a, s, u.lo);
+    if (page < 0) return false;
+    const int mask = (1 << a.page_shift) - 1;
+    u.slot = (((int64_t)page * a.kv_heads + u.head) << a.page_shift) + (u.lo & mask);
+    return true;
+}
+
+__device__ __forceinline__ int quantize_code(float x, float inv) {
+    const int c = __float2int_rn(__fmul_rn(x, inv));
+    return 128 + (c > 127 ? 127 : (c < -127 ? -127 : c));
+}
+
+template <int D>
+__global__ void __launch_bounds__(kWarps * 32) kv_write_kernel(const KvIoArgs p) {
+    constexpr int LPR = D / 8;          // lanes of a row (8 values each)
+    constexpr int RPI = 32 / LPR;       // rows of an iteration
+    constexpr int NI = kKvBlock / RPI;  // iterations
+    KvUnit u;
+    if (!kv_unit(p, u)) return;
+    const int lane = threadIdx.x & 31;
+    const int r0 = lane / LPR, c8 = (lane % LPR) * 8;
+
+    const __half* x = (u.which ? p.v : p.k) + (int64_t)u.head * D + c8;
+    uint8_t* codes = (u.which ? p.v_codes : p.k_codes) + u.slot * D + c8;
+    float* scale = (u.which ? p.v_scales : p.k_scales) + (u.slot >> 4);
+    uint4 v[NI];
+    unsigned fresh = 0, kept = 0;  // bit i: this lane's row of iteration i is the call's, or older
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+        const int pos = u.lo + i * RPI + r0;
+        const int64_t row = u.row0 + (pos - u.first);
+        const bool f = pos >= u.first && pos < u.len && row >= 0 && row < p.b.tokens;
+        v[i] = f ? __ldg(reinterpret_cast<const uint4*>(x + row * p.row_stride)) : make_uint4(0, 0, 0, 0);
+        fresh |= f ? 1u << i : 0u;
+        kept |= pos < u.first ? 1u << i : 0u;
+    }
+    const bool has_old = u.first > u.lo;
+    const float s_old = has_old ? *scale : 0.f;
+    unsigned m = 0;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+        m = __vmaxu2(m, v[i].x & 0x7FFF7FFFu);
+        m = __vmaxu2(m, v[i].y & 0x7FFF7FFFu);
+        m = __vmaxu2(m, v[i].z & 0x7FFF7FFFu);
+        m = __vmaxu2(m, v[i].w & 0x7FFF7FFFu);
+    }
+    m = max(m & 0xFFFFu, m >> 16);
+    m = __reduce_max_sync(0xffffffffu, m);
+    const float s_new = __fdiv_rn(__half2float(__ushort_as_half((unsigned short)m)), 127.f);
+    // fmaxf drops a NaN: the sum keeps it
+    const float s = !has_old ? s_new : (s_old != s_old || s_new != s_new) ? s_old + s_new : fmaxf(s_old, s_new);
+    const bool good = s > 0.f && s < __int_as_float(0x7f800000);
+    const float inv = good ? __fdiv_rn(1.f, s) : 0.f;
+    const bool again = has_old && (!good || s != s_old);  // older codes follow the new scale
+    const float ratio = again && good ? __fdiv_rn(s_old, s) : 0.f;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+        uint2* dst = reinterpret_cast<uint2*>(codes + (int64_t)(i * RPI + r0) * D);
+        uint32_t out[2] = {0x80808080u, 0x80808080u};
+        if ((fresh >> i) & 1u) {
+            if (good) {
+                const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&w[2 * j]));
+                    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&w[2 * j + 1]));
+                    out[j] = (uint32_t)quantize_code(a.x, inv) | ((uint32_t)quantize_code(a.y, inv) << 8) |
+                             ((uint32_t)quantize_code(b.x, inv) << 16) | ((uint32_t)quantize_code(b.y, inv) << 24);
+                }
+            }
+            *dst = make_uint2(out[0], out[1]);
+        } else if (again && ((kept >> i) & 1u)) {
+            if (good) {
+                const uint2 q = *dst;
+                const uint32_t w[2] = {q.x, q.y};
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    out[j] = 0;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float old = (float)((int)((w[j] >> (8 * k)) & 0xFFu) - 128);
+                        out[j] |= (uint32_t)quantize_code(old, ratio) << (8 * k);
+                    }
+                }
+            }
+            *dst = make_uint2(out[0], out[1]);
+        }
+    }
+    // only now: every lane has read the old scale (the reduction above)
+    if (lane == 0) *scale = s;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kWarps * 32) kv_read_kernel(const KvIoArgs p) {
+    constexpr int LPR = D / 8, RPI = 32 / LPR, NI = kKvBlock / RPI;
+    KvUnit u;
+    if (!kv_unit(p, u)) return;
+    const int lane = threadIdx.x & 31;
+    const int r0 = lane / LPR, c8 = (lane % LPR) * 8;
+    const uint8_t* codes = (u.which ? p.v_codes : p.k_codes) + u.slot * D + c8;
+    __half* x = (u.which ? p.v : p.k) + (int64_t)u.head * D + c8;
+    uint2 q[NI];
+#pragma unroll
+    for (int i = 0; i < NI; ++i)  // the block's 16 rows are always inside its page
+        q[i] = __ldg(reinterpret_cast<const uint2*>(codes + (int64_t)(i * RPI + r0) * D));
+    const float s = __ldg((u.which ? p.v_scales : p.k_scales) + (u.slot >> 4));
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+        const int pos = u.lo + i * RPI + r0;
+        const int64_t row = u.row0 + (pos - u.first);
+        if (pos < u.first || pos >= u.len || row < 0 || row >= p.b.tokens) continue;
+        const uint32_t w[2] = {q[i].x, q[i].y};
+        uint32_t o[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t h = w[j >> 1] >> ((j & 1) * 16);
+            const __half2 t = __halves2half2(__float2half_rn(__fmul_rn((float)((int)(h & 0xFFu) - 128), s)),
+                                             __float2half_rn(__fmul_rn((float)((int)((h >> 8) & 0xFFu) - 128), s)));
+            o[j] = *reinterpret_cast<const uint32_t*>(&t);
+        }
+        *reinterpret_cast<uint4*>(x + row * p.row_stride) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+}
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+int kv_io(const mnb_kv_cache* c, const mnb_kv_batch* b, void* K, void* V, int64_t row_stride, bool write,
+          void* stream) {
+    bool empty;
+    int rc = kv_check(c, b, &empty);
+    if (rc != MNB_OK) return rc;
+    if (row_stride < (int64_t)c->kv_heads * c->head_dim) return MNB_ERR_ARG;
+    if (row_stride % 8 != 0) return MNB_ERR_ALIGN;
+    if (empty || b->max_pages == 0 || c->num_pages == 0) return MNB_OK;
+    if (!K || !V) return MNB_ERR_ARG;
+    if (!aligned(K, 16) || !aligned(V, 16)) return MNB_ERR_ALIGN;
+    KvIoArgs p;
+    p.b = kv_args(c, b);
+    p.items = kv_items(b->tokens, b->seqs, 1, 2);
+    p.row_stride = row_stride;
+    p.k_codes = static_cast<uint8_t*>(c->K);
+    p.v_codes = static_cast<uint8_t*>(c->V);
+    p.k_scales = static_cast<float*>(c->K_scales);
+    p.v_scales = static_cast<float*>(c->V_scales);
+    p.k = static_cast<__half*>(K);
+    p.v = static_cast<__half*>(V);
+    const int64_t blocks = (p.items * 2 * c->kv_heads + kWarps - 1) / kWarps;
+    if (blocks > INT32_MAX) return MNB_ERR_UNSUPPORTED;
+    int sms;
+    unsigned int* status;
+    rc = device_ready(&sms, &status);
+    if (rc != MNB_OK) return rc;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const dim3 grid((unsigned)blocks), block(kWarps * 32);
+    if (write) {
+        if (c->head_dim == 64)
+            kv_write_kernel<64><<<grid, block, 0, st>>>(p);
+        else
+            kv_write_kernel<128><<<grid, block, 0, st>>>(p);
+    } else {
+        if (c->head_dim == 64)
+            kv_read_kernel<64><<<grid, block, 0, st>>>(p);
+        else
+            kv_read_kernel<128><<<grid, block, 0, st>>>(p);
+    }
+    return cudaGetLastError() == cudaSuccess ? MNB_OK : MNB_ERR_CUDA;
+}
+
+}  // namespace
+
+int kv_check(const mnb_kv_cache* c, const mnb_kv_batch* b, bool* empty) {
+    if (!c || !b || c->num_pages < 0 || c->kv_heads <= 0 || c->reserved != 0 || b->seqs < 0 || b->max_pages < 0 ||
+        b->tokens < 0 || b->max_new < 0 || b->max_len < 0)
+        return MNB_ERR_ARG;
+    if (c->head_dim != 64 && c->head_dim != 128) return MNB_ERR_UNSUPPORTED;
+    if (c->page_size < 16 || c->page_size > 256 || (c->page_size & (c->page_size - 1)) != 0)
+        return MNB_ERR_UNSUPPORTED;
+    if (c->num_pages > INT32_MAX || c->kv_heads > 65535 || b->tokens > INT32_MAX) return MNB_ERR_UNSUPPORTED;
+    *empty = b->seqs == 0 || b->tokens == 0;
+    if (*empty) return MNB_OK;
+    if (!b->kv_len || !b->q_start) return MNB_ERR_ARG;
+    // without pages every sequence is empty, and the cache may be NULL
+    if (b->max_pages > 0 && c->num_pages > 0 &&
+        (!c->K || !c->V || !c->K_scales || !c->V_scales || !b->page_table))
+        return MNB_ERR_ARG;
+    if (!aligned(c->K, 16) || !aligned(c->V, 16) || !aligned(c->K_scales, 16) || !aligned(c->V_scales, 16) ||
+        !aligned(b->page_table, 4) || !aligned(b->kv_len, 4) || !aligned(b->q_start, 4))
+        return MNB_ERR_ALIGN;
+    return MNB_OK;
+}
+
+}  // namespace mnb
+
+extern "C" int mnb_kv_write(const mnb_kv_cache* cache, const mnb_kv_batch* batch, const void* K, const void* V,
+                            int64_t row_stride, void* stream) {
+    return mnb::kv_io(cache, batch, const_cast<void*>(K), const_cast<void*>(V), row_stride, true, stream);
+}
+
+extern "C" int mnb_kv_read(const mnb_kv_cache* cache, const mnb_kv_batch* batch, void* K, void* V,
+                           int64_t row_stride, void* stream) {
+    return mnb::kv_io(cache, batch, K, V, row_stride, false, stream);
+}

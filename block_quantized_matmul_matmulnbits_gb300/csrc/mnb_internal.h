@@ -210,4 +210,19 @@ int run_noalloc(mnb_handle h, const void* X, const void* Wq, const void* scales,
 cudaError_t dequant_launch(const uint8_t* Wq, const __half* S, const uint8_t* Z, int N, int K, int bits,
                            __half* W16, int variant, cudaStream_t st);
 
+// ---- 8-bit key/value cache, attention, log probabilities ------------------
+
+// The current device's SM count and status word (set up on first use): MNB_OK,
+// MNB_ERR_NO_DEVICE or MNB_ERR_CUDA (api.cu).
+int device_ready(int* sm_count, unsigned int** status);
+
+// The checks every cache call shares (kv_cache.cu): MNB_OK or MNB_ERR_*;
+// *empty: the call has no tokens.  A cache or table without pages is allowed:
+// every sequence is then empty.
+int kv_check(const mnb_kv_cache* c, const mnb_kv_batch* b, bool* empty);
+
+// Once per context: shared-memory limits of the kernels (hooked into the device setup).
+cudaError_t attn_prepare();
+cudaError_t logprobs_prepare();
+
 }  // namespace mnb

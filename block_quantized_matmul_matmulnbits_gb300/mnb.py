@@ -30,7 +30,8 @@ FLAG_EARLY_WEIGHTS = 1
 
 # Every symbol include/mnb.h declares (checked against the header by the tests).
 EXPORTS = ("mnb_create", "mnb_destroy", "mnb_run", "mnb_run_bias", "mnb_run_qlora", "mnb_run_multi", "mnb_transpose_dq_weight", "mnb_run_q8x", "mnb_quantize_x", "mnb_check_wait_timeout", "mnb_plan", "mnb_last_route", "mnb_sync_status",
-           "mnb_status_str", "mnb_dequant", "mnb_lora_down", "mnb_run_noalloc", "mnb_noalloc_max_rows")
+           "mnb_status_str", "mnb_dequant", "mnb_lora_down", "mnb_run_noalloc", "mnb_noalloc_max_rows",
+           "mnb_kv_write", "mnb_kv_read", "mnb_attn", "mnb_attn_workspace", "mnb_logprobs")
 
 
 class MnbDesc(ctypes.Structure):
@@ -51,6 +52,18 @@ class MnbPlanInfo(ctypes.Structure):
 class MnbProjection(ctypes.Structure):
     _fields_ = [("N", ctypes.c_int64), ("Wq", ctypes.c_void_p), ("scales", ctypes.c_void_p),
                 ("zp", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("Y", ctypes.c_void_p)]
+
+
+class MnbKvCache(ctypes.Structure):
+    _fields_ = [("num_pages", ctypes.c_int64), ("page_size", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("reserved", ctypes.c_int32), ("K", ctypes.c_void_p),
+                ("V", ctypes.c_void_p), ("K_scales", ctypes.c_void_p), ("V_scales", ctypes.c_void_p)]
+
+
+class MnbKvBatch(ctypes.Structure):
+    _fields_ = [("seqs", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("tokens", ctypes.c_int64),
+                ("max_new", ctypes.c_int32), ("max_len", ctypes.c_int32), ("page_table", ctypes.c_void_p),
+                ("kv_len", ctypes.c_void_p), ("q_start", ctypes.c_void_p)]
 
 
 class MnbError(RuntimeError):
@@ -109,6 +122,17 @@ def lib() -> ctypes.CDLL:
             L.mnb_run_noalloc.restype = ctypes.c_int
             L.mnb_noalloc_max_rows.argtypes = []
             L.mnb_noalloc_max_rows.restype = I64
+            C, B, F32 = ctypes.POINTER(MnbKvCache), ctypes.POINTER(MnbKvBatch), ctypes.c_float
+            L.mnb_kv_write.argtypes = [C, B, P, P, I64, P]
+            L.mnb_kv_write.restype = ctypes.c_int
+            L.mnb_kv_read.argtypes = [C, B, P, P, I64, P]
+            L.mnb_kv_read.restype = ctypes.c_int
+            L.mnb_attn.argtypes = [C, B, P, I64, I32, F32, I32, P, I64, P, P, I64, P]
+            L.mnb_attn.restype = ctypes.c_int
+            L.mnb_attn_workspace.argtypes = [C, B, I32, I32, I32]
+            L.mnb_attn_workspace.restype = I64
+            L.mnb_logprobs.argtypes = [P, I64, I64, I64, F32, P, I32, P, P, P, P, P]
+            L.mnb_logprobs.restype = ctypes.c_int
             _lib = L
     return _lib
 
@@ -246,6 +270,137 @@ def mnb_dequant(Wq, scales, zp, N: int, K: int, bits: int, W16, variant: int = 0
 
 def mnb_lora_down(X, A, T, Mt: int, K: int, rank: int = 32, stream=None) -> None:
     _check(lib().mnb_lora_down(_ptr(X), _ptr(A), _ptr(T), Mt, K, rank, _stream(stream)), "mnb_lora_down")
+
+
+KV_BLOCK = 16  # tokens that share a scale of the cache
+
+
+def _want(ok: bool, what: str) -> None:
+    if not ok:
+        raise ValueError(what)
+
+
+class KVCache:
+    """A paged 8-bit cache of one layer's keys and values (mnb_kv_cache), over the caller's tensors:
+    K, V uint8 [num_pages, kv_heads, page_size, head_dim]; K_scales, V_scales float32 [num_pages,
+    kv_heads, page_size // 16].  ``KVCache.empty`` makes the tensors.  The object keeps them alive."""
+
+    def __init__(self, K, V, K_scales, V_scales):
+        import torch
+        _want(K.dim() == 4 and K.dtype == V.dtype == torch.uint8 and K.shape == V.shape,
+              "K and V: uint8 [num_pages, kv_heads, page_size, head_dim]")
+        pages, heads, page, dim = K.shape
+        _want(K_scales.dtype == V_scales.dtype == torch.float32 and
+              tuple(K_scales.shape) == tuple(V_scales.shape) == (pages, heads, page // KV_BLOCK),
+              "K_scales and V_scales: float32 [num_pages, kv_heads, page_size // 16]")
+        _want(all(t.is_contiguous() for t in (K, V, K_scales, V_scales)), "the cache's tensors have to be contiguous")
+        self.K, self.V, self.K_scales, self.V_scales = K, V, K_scales, V_scales
+        self.num_pages, self.page_size, self.kv_heads, self.head_dim = pages, page, heads, dim
+        self.desc = MnbKvCache(pages, page, heads, dim, 0, K.data_ptr(), V.data_ptr(), K_scales.data_ptr(),
+                               V_scales.data_ptr())
+        self.ref = ctypes.byref(self.desc)
+
+    @classmethod
+    def empty(cls, num_pages: int, page_size: int, kv_heads: int, head_dim: int, device="cuda"):
+        import torch
+        shape = (num_pages, kv_heads, page_size, head_dim)
+        scales = (num_pages, kv_heads, page_size // KV_BLOCK)
+        return cls(*(torch.full(shape, 128, dtype=torch.uint8, device=device) for _ in range(2)),
+                   *(torch.zeros(scales, dtype=torch.float32, device=device) for _ in range(2)))
+
+
+class KVBatch:
+    """The sequences of a call (mnb_kv_batch), over int32 device tensors: page_table [seqs, max_pages],
+    kv_len [seqs], q_start [seqs + 1].  The tensors may change between calls (lengths, pages); ``tokens``
+    is the row count of the token tensors, ``max_new`` / ``max_len`` bound the new tokens and the length
+    of a sequence."""
+
+    def __init__(self, page_table, kv_len, q_start, tokens: int, max_new: int, max_len: int):
+        import torch
+        seqs = kv_len.shape[0]
+        _want(all(t.dtype == torch.int32 and t.is_contiguous() for t in (page_table, kv_len, q_start)),
+              "page_table, kv_len and q_start: contiguous int32")
+        _want(page_table.dim() == 2 and page_table.shape[0] == seqs and tuple(q_start.shape) == (seqs + 1,),
+              "page_table [seqs, max_pages], kv_len [seqs], q_start [seqs + 1]")
+        self.page_table, self.kv_len, self.q_start = page_table, kv_len, q_start
+        self.seqs, self.tokens, self.max_new, self.max_len = seqs, tokens, max_new, max_len
+        self.desc = MnbKvBatch(seqs, page_table.shape[1], tokens, max_new, max_len, page_table.data_ptr(),
+                               kv_len.data_ptr(), q_start.data_ptr())
+        self.ref = ctypes.byref(self.desc)
+
+
+def _is_half(x) -> bool:
+    import torch
+    return x.dtype is torch.float16
+
+
+def _rows(x, heads: int, dim: int, tokens: int, what: str) -> int:
+    """Row stride of a token tensor [tokens, heads, dim] or [tokens, heads * dim] (rows may be strided)."""
+    s, n = x.stride(), x.dim()
+    if n == 3 and x.shape[1] == heads and x.shape[2] == dim:
+        ok = s[2] == 1 and (s[1] == dim or heads == 1)
+    else:
+        ok = n == 2 and x.shape[1] == heads * dim and s[1] == 1
+    _want(ok and x.shape[0] == tokens and _is_half(x), f"{what}: fp16 [tokens, heads, head_dim], whole rows")
+    return s[0] if tokens > 1 else max(s[0], heads * dim)
+
+
+def mnb_kv_write(cache: KVCache, batch: KVBatch, K, V, stream=None) -> None:
+    """Quantise the batch's tokens (K, V fp16 [tokens, kv_heads, head_dim]) into the cache."""
+    stride = _rows(K, cache.kv_heads, cache.head_dim, batch.tokens, "K")
+    _want(_rows(V, cache.kv_heads, cache.head_dim, batch.tokens, "V") == stride, "K and V: one row stride")
+    _check(lib().mnb_kv_write(cache.ref, batch.ref, K.data_ptr(), V.data_ptr(), stride, _stream(stream)),
+           "mnb_kv_write")
+
+
+def mnb_kv_read(cache: KVCache, batch: KVBatch, K, V, stream=None) -> None:
+    """The batch's tokens from the cache into K, V (fp16 [tokens, kv_heads, head_dim])."""
+    stride = _rows(K, cache.kv_heads, cache.head_dim, batch.tokens, "K")
+    _want(_rows(V, cache.kv_heads, cache.head_dim, batch.tokens, "V") == stride, "K and V: one row stride")
+    _check(lib().mnb_kv_read(cache.ref, batch.ref, K.data_ptr(), V.data_ptr(), stride, _stream(stream)), "mnb_kv_read")
+
+
+def mnb_attn_workspace(cache: KVCache, batch: KVBatch, q_heads: int, window: int = 0, sm_count: int = 0) -> int:
+    """Bytes of workspace mnb_attn needs for these sizes."""
+    n = lib().mnb_attn_workspace(cache.ref, batch.ref, q_heads, window, sm_count)
+    if n < 0:
+        raise MnbError(n, "mnb_attn_workspace")
+    return n
+
+
+def attn_workspace(cache: KVCache, batch: KVBatch, q_heads: int, window: int = 0):
+    """A workspace tensor for mnb_attn (None where it needs none)."""
+    import torch
+    n = mnb_attn_workspace(cache, batch, q_heads, window)
+    return torch.empty(n, dtype=torch.uint8, device=cache.K.device) if n else None
+
+
+def mnb_attn(cache: KVCache, batch: KVBatch, Q, out, scale: Optional[float] = None, window: int = 0, lse=None, ws=None,
+             stream=None) -> None:
+    """Causal attention of the batch's tokens over the cache: Q, out fp16 [tokens, q_heads, head_dim], lse
+    float32 [tokens, q_heads] or None; scale defaults to head_dim ** -0.5.  ``ws``: attn_workspace(...)."""
+    dim = cache.head_dim
+    q_heads = Q.shape[1] if Q.dim() == 3 else Q.shape[1] // dim
+    stride = _rows(Q, q_heads, dim, batch.tokens, "Q")
+    out_stride = _rows(out, q_heads, dim, batch.tokens, "out")
+    _want(lse is None or (lse.is_contiguous() and lse.element_size() == 4 and lse.numel() == batch.tokens * q_heads),
+          "lse: float32 [tokens, q_heads]")
+    _check(lib().mnb_attn(cache.ref, batch.ref, Q.data_ptr(), stride, q_heads, dim ** -0.5 if scale is None else scale,
+                          window, out.data_ptr(), out_stride, None if lse is None else lse.data_ptr(),
+                          None if ws is None else ws.data_ptr(), 0 if ws is None else ws.nbytes, _stream(stream)),
+           "mnb_attn")
+
+
+def mnb_logprobs(logits, target=None, logprob=None, entropy=None, top_ids=None, top_logprobs=None, scale: float = 1.0,
+                 stream=None) -> None:
+    """Log probability of `target` (int64 [rows]), entropy and the top k of logits fp16 [rows, vocab] (rows may be
+    strided) into logprob, entropy (float32 [rows]), top_ids (int32 [rows, k]) and top_logprobs (float32)."""
+    rows, vocab = logits.shape
+    _want(_is_half(logits) and (logits.stride(1) == 1 or vocab == 1), "logits: fp16 [rows, vocab]")
+    k = 0 if top_ids is None else top_ids.shape[1]
+    stride = logits.stride(0) if rows > 1 else max(logits.stride(0), vocab)
+    _check(lib().mnb_logprobs(logits.data_ptr(), rows, vocab, stride, scale, _ptr(target), k, _ptr(logprob),
+                              _ptr(entropy), _ptr(top_ids), _ptr(top_logprobs), _stream(stream)), "mnb_logprobs")
 
 
 class Projection:

@@ -331,6 +331,140 @@ int mnb_run_noalloc(mnb_handle h,
 /* Largest batch * M mnb_run_noalloc accepts with an adapter. */
 int64_t mnb_noalloc_max_rows(void);
 
+/* ---- the 8-bit key/value cache ------------------------------------------ */
+
+/* A paged cache of one layer's keys and values in 8 bits.
+ *   num_pages   pages of the two code tensors
+ *   page_size   tokens a page: 16, 32, 64, 128 or 256
+ *   kv_heads    key/value heads (1 .. 65535)
+ *   head_dim    64 or 128
+ *   K, V        uint8 [num_pages, kv_heads, page_size, head_dim]
+ *   K_scales, V_scales   float [num_pages, kv_heads, page_size / 16]
+ * A block of 16 tokens of a page and head shares one scale; a code q stands
+ * for (q - 128) * scale, the map of this library's INT8 weights with their
+ * default zero point. */
+#define MNB_KV_BLOCK 16
+typedef struct {
+    int64_t num_pages;
+    int32_t page_size;
+    int32_t kv_heads;
+    int32_t head_dim;
+    int32_t reserved;     /* 0 */
+    void* K;
+    void* V;
+    void* K_scales;
+    void* V_scales;
+} mnb_kv_cache;
+
+/* The sequences of one call.
+ *   seqs        sequences
+ *   max_pages   columns of page_table
+ *   page_table  int32 [seqs, max_pages] (device): page j of sequence s holds
+ *               its positions j * page_size .. ; entries past the sequence's
+ *               length are not read
+ *   kv_len      int32 [seqs] (device): tokens of the sequence in the cache, the
+ *               call's own tokens included
+ *   q_start     int32 [seqs + 1] (device), q_start[0] = 0, ascending: the
+ *               call's tokens of sequence s are rows q_start[s] ..
+ *               q_start[s + 1] - 1 of its token tensors, and they are the LAST
+ *               positions of the sequence.  A sequence may have none.
+ *   tokens      rows of the token tensors (= q_start[seqs])
+ *   max_new     at least the largest q_start[s + 1] - q_start[s]
+ *   max_len     about the largest kv_len[s]
+ * The lengths are read on the device, so a captured call can be replayed with
+ * others.  max_new and max_len choose the launch: rows of a sequence with
+ * more than max_new may be left out; a max_len that is off costs time only.
+ * Positions before 0, rows past `tokens`, lengths past max_pages pages and
+ * page numbers outside the cache are skipped, never followed. */
+typedef struct {
+    int32_t seqs;
+    int32_t max_pages;
+    int64_t tokens;
+    int32_t max_new;
+    int32_t max_len;
+    const int32_t* page_table;
+    const int32_t* kv_len;
+    const int32_t* q_start;
+} mnb_kv_batch;
+
+/* Quantise the call's tokens into the cache.
+ *   K, V   fp16, row t at K + t * row_stride, [kv_heads, head_dim] each
+ *          (row_stride in elements, a multiple of 8, at least
+ *          kv_heads * head_dim: a slice of a fused QKV row works)
+ * For each block of 16 positions and head that gets new tokens, in binary32
+ * with every step rounded once: s_new = max |x| / 127 over the new tokens; the
+ * block's scale becomes s_new, or max(s_old, s_new) where the block already
+ * holds older tokens of the sequence (positions before the call's); codes are
+ * 128 + clamp(rint(x * (1 / scale)), -127, 127) (ties to even), and where the
+ * scale grew the older tokens' codes become 128 + rint((q - 128) * (s_old /
+ * scale)).  A scale of zero gives codes 128.  A block that receives a
+ * non-finite value gets a non-finite scale and codes 128: its 16 tokens read
+ * as NaN.  Codes of positions past the sequence's end are left as they are.
+ * Writing the same tokens at the same positions again changes nothing.  Two
+ * sequences of a call must not share a page that the call writes.
+ * Errors: MNB_ERR_ARG, MNB_ERR_UNSUPPORTED, MNB_ERR_ALIGN (K, V, codes and
+ * scales 16 bytes, the index arrays 4), MNB_ERR_NO_DEVICE, MNB_ERR_CUDA. */
+int mnb_kv_write(const mnb_kv_cache* cache, const mnb_kv_batch* batch, const void* K, const void* V,
+                 int64_t row_stride, void* stream);
+
+/* The reverse: the values of the call's tokens (the last ones of each
+ * sequence) as fp16((q - 128) * scale), one rounding, into K and V laid out as
+ * in mnb_kv_write.  Rows whose position or page does not exist are left as
+ * they are.  Errors as mnb_kv_write. */
+int mnb_kv_read(const mnb_kv_cache* cache, const mnb_kv_batch* batch, void* K, void* V, int64_t row_stride,
+                void* stream);
+
+/* Causal attention of the call's tokens over the cache (which already holds
+ * them).  Token i of sequence s has position p = kv_len[s] - n + i and sees
+ * the positions j <= p, with window > 0 only those with j > p - window:
+ *   out = sum_j softmax_j(scale * q . k_j) v_j,   k_j, v_j as the codes stand
+ *   Q      fp16, row t at Q + t * q_stride, [q_heads, head_dim]; query head h
+ *          reads kv head h / (q_heads / kv_heads)
+ *   out    fp16, row t at out + t * out_stride, [q_heads, head_dim]
+ *   lse    float [tokens, q_heads] or NULL: log of the sum of
+ *          exp(scale * q . k_j) (natural logarithm)
+ *   ws     workspace of at least mnb_attn_workspace bytes, 16-byte aligned;
+ *          may be NULL when that is 0.  It needs no clearing and holds nothing
+ *          between calls; calls that may overlap need one each.
+ * Strides are in elements, multiples of 8.  A row that sees no position gets
+ * zeros and lse -infinity.  The scores, the softmax and the sums are in binary32,
+ * the probabilities enter the second product in fp16; keys' and values' codes
+ * enter both products exactly.  Deterministic for given arguments.
+ * Errors: MNB_ERR_ARG (also a workspace that is too small),
+ * MNB_ERR_UNSUPPORTED (q_heads not a multiple of kv_heads), MNB_ERR_ALIGN,
+ * MNB_ERR_NO_DEVICE, MNB_ERR_CUDA. */
+int mnb_attn(const mnb_kv_cache* cache, const mnb_kv_batch* batch, const void* Q, int64_t q_stride,
+             int32_t q_heads, float scale, int32_t window, void* out, int64_t out_stride, float* lse,
+             void* ws, int64_t ws_bytes, void* stream);
+
+/* Workspace bytes of mnb_attn for these sizes on a GPU with `sm_count` SMs
+ * (sm_count <= 0: the current device).  Host only; negative: an error code. */
+int64_t mnb_attn_workspace(const mnb_kv_cache* cache, const mnb_kv_batch* batch, int32_t q_heads, int32_t window,
+                           int32_t sm_count);
+
+/* What is taken from a row of logits: the log probability of a given token,
+ * the entropy, and the most likely tokens.  With x = scale * logit (scale > 0,
+ * the reciprocal of a temperature) and lse = log sum exp(x) over the row:
+ *   logits        fp16, row r at logits + r * row_stride, [vocab] each; any
+ *                 vocab of 1 .. 786432 and any row_stride >= vocab
+ *   target        int64 [rows] or NULL; a target outside [0, vocab) stands for
+ *                 no token and gives logprob 0
+ *   logprob       float [rows]: x[target] - lse          (NULL without target)
+ *   entropy       float [rows] or NULL: lse - sum p x, natural units
+ *   top           0 .. 32, at most vocab
+ *   top_ids       int32 [rows, top]: by falling logit, equal ones by rising id
+ *   top_logprobs  float [rows, top]: their x - lse
+ * Logits of -infinity are tokens that cannot be drawn (they add 0); a row with
+ * nothing else gives logprob and top_logprobs -infinity and entropy 0.  A row
+ * with NaN or +infinity gives NaN for every float (its top_ids are valid ids,
+ * in no stated order).  The logits are read from memory once; sums in binary32.
+ * Errors: MNB_ERR_ARG, MNB_ERR_UNSUPPORTED (vocab, top above 32),
+ * MNB_ERR_ALIGN (logits 16 bytes, target 8, the others 4), MNB_ERR_NO_DEVICE,
+ * MNB_ERR_CUDA. */
+int mnb_logprobs(const void* logits, int64_t rows, int64_t vocab, int64_t row_stride, float scale,
+                 const int64_t* target, int32_t top, float* logprob, float* entropy, int32_t* top_ids,
+                 float* top_logprobs, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
