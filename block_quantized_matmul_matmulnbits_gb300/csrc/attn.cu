@@ -10,13 +10,19 @@
 //    2^(w_j - max w) <= 1 whatever the value scales are, so its FP16 rounding
 //    (2^-11 of each term) never meets FP16's subnormals at the large end; the
 //    denominator takes each block's sum times 1 / vs_b, in binary32.
-//  * Codes become FP16 integers (1024 + q, then - 1152): both products take them
-//    exactly, with binary32 accumulation (mma.sync m16n8k16).
-//  * 16 query rows are one MMA row tile: consecutive (token, head of the kv
-//    head's group) pairs, so the heads that share a kv head share its bytes.
+//  * Both products take the codes exactly, with binary32 accumulation (mma.sync
+//    m16n8k16).  The first one's are fed as FP16 subnormals q 2^-24 (one byte permute for
+//    two codes), the offset 128 sum_d q_d taken off the accumulator before it starts;
+//    the second one's, whose sum runs over all keys, as the integers q - 128 themselves
+//    (1024 + q less 1152), so that nothing has to cancel at the end.
+//  * Keys and values are the LEFT operands (16 keys, 16 values of d), the query rows the
+//    columns: consecutive (token, head of the kv head's group) pairs, 8 or 16 of them, so
+//    the heads that share a kv head share its bytes, and a decode step of up to
+//    eight heads a kv head wastes no half of an MMA.  The probabilities pass from the first
+//    product's result to the second one's operand with one 8 x 8 transpose a register.
 //
 // attn_split_kernel: a CTA of four warps takes one row tile, one kv head and
-// `chunk` keys.  Each warp walks its own blocks of 16 keys (4 KB of codes at head_dim
+// `chunk` keys.  Each warp walks its own stages of 32 keys (8 KB of codes at head_dim
 // 128) through a ring of cp.async copies of its own, so nothing in the loop
 // waits on another warp; the warps' results are joined once at the end, and the
 // chunks' by attn_join_kernel where a row tile has more than one.  The codes are
@@ -32,10 +38,10 @@ namespace mnb {
 
 namespace {
 
-constexpr int kRows = 16;     // query rows of a tile
 constexpr int kWarps = 4;
-constexpr int kStages = 4;    // blocks of 16 keys in a warp's ring
 constexpr int kCtasPerSm = 3;
+__host__ __device__ constexpr int ring_stages(int D) { return D == 64 ? 4 : 2; }  // stages of 32 keys in a warp's ring
+constexpr float kCodeUnit = 5.9604644775390625e-8f;           // 2^-24, FP16's smallest subnormal
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.693147180559945309417f;
 
@@ -84,6 +90,13 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
     return v;
 }
 
+// An 8 x 8 matrix of FP16 values (row g in lanes 4 g .. 4 g + 3, two columns a lane), transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
 constexpr uint32_t kBias = 0x64806480u;  // half2(1024 + 128)
 
 // Two codes (bytes `sel` of w) as exact FP16 integers q - 128.
@@ -105,51 +118,41 @@ struct Tile {
     int64_t row0;  // token row of the sequence's first token of the call
 };
 
+template <int ROWS>
 __device__ __forceinline__ bool find_tile(const AttnArgs& a, int64_t u, Tile& t) {
     int64_t first = u;
-    t.s = a.single ? (int)u : kv_find_seq(a.b, u, a.group, 1, &first);
+    t.s = a.single ? (int)u : kv_find_seq(a.b, u, a.group * (16 / ROWS), 1, &first);
     int row0;
     kv_sequence(a.b, t.s, &t.len, &row0, &t.n);
     t.row0 = row0;
-    const int64_t r0 = (u - first) * kRows;
+    const int64_t r0 = (u - first) * ROWS;
     if (r0 < 0 || r0 >= (int64_t)t.n * a.group) return false;
     t.r0 = (int)r0;
     return true;
 }
 
-template <int D>
+template <int D, int NT>
 __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) attn_split_kernel(const AttnArgs a) {
-    constexpr int KS = D / 16;           // k-steps of the first product
-    constexpr int NN = D / 8;            // column tiles of the second
+    constexpr int KS = D / 16;               // k-steps of the first product
+    constexpr int MT = D / 16;               // row tiles (values' d) of the second
+    constexpr int kRows = 8 * NT;
     constexpr int kBlockBytes = kKvBlock * D;
-    constexpr int kStageBytes = 2 * kBlockBytes;
-    constexpr int kCopies = kBlockBytes / 16 / 32;  // 16-byte copies a lane, keys or values
+    constexpr int kStageBytes = 4 * kBlockBytes;    // two blocks' keys, then their values
+    constexpr int kStages = ring_stages(D);
+    constexpr int kCopies = kBlockBytes / 16 / 32;  // 16-byte copies a lane and block, keys or values
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
+    pdl_wait();
     pdl_launch_dependents();
 
     Tile tl;
-    if (!find_tile(a, blockIdx.x, tl)) return;
+    if (!find_tile<kRows>(a, blockIdx.x, tl)) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t = lane & 3;
     const int head = blockIdx.y, split = blockIdx.z;
     const int rows = (int)min((int64_t)tl.n * a.group - tl.r0, (int64_t)kRows);
     const int first = tl.len - tl.n;  // position of the call's first token
 
-    // this lane's two rows: what they see is [lo, hi)
-    int hi[2], lo[2];
-    int64_t qoff[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int r = tl.r0 + g + 8 * i;
-        const int tok = r / a.group;
-        const int64_t row = tl.row0 + tok;
-        const bool ok = g + 8 * i < rows && row >= 0 && row < a.b.tokens;
-        const int pos = first + tok;
-        hi[i] = ok ? max(pos + 1, 0) : 0;
-        lo[i] = a.window > 0 ? max(pos - a.window + 1, 0) : 0;
-        qoff[i] = ok ? row * a.q_stride + (int64_t)(head * a.group + (r - tok * a.group)) * D : -1;
-    }
     // the tile: its last token sees furthest, its first one starts furthest back
     const int tok_a = tl.r0 / a.group, tok_b = (tl.r0 + rows - 1) / a.group;
     const int hi_t = max(first + tok_b + 1, 0);
@@ -158,64 +161,48 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) attn_split_kernel(con
     const int begin = (int)min(begin64, (int64_t)hi_t);
     // the last chunk takes what is left, however long
     const int end = split == a.splits - 1 ? hi_t : (int)min(begin64 + a.chunk, (int64_t)hi_t);
-    const int nblk = (end - begin + kKvBlock - 1) / kKvBlock;
-    const int mine = nblk > warp ? (nblk - warp + kWarps - 1) / kWarps : 0;
+    const int nstage = (end - begin + 2 * kKvBlock - 1) / (2 * kKvBlock);
+    const int mine = nstage > warp ? (nstage - warp + kWarps - 1) / kWarps : 0;
     // blocks that every row of the tile sees wholly need no mask
-    const int all_hi = max(first + tok_a + 1, 0);
+    const int all_hi = min(max(first + tok_a + 1, 0), end);
     const int all_lo = a.window > 0 ? max(first + tok_b - a.window + 1, 0) : 0;
 
-    uint32_t qf[KS][4];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const uint4* src = reinterpret_cast<const uint4*>(a.Q + (qoff[i] < 0 ? 0 : qoff[i]) + t * (D / 4));
-#pragma unroll
-        for (int j = 0; j < KS / 2; ++j) {
-            const uint4 v = qoff[i] < 0 || mine == 0 ? make_uint4(0, 0, 0, 0) : __ldg(src + j);
-            qf[2 * j][i] = v.x;
-            qf[2 * j][2 + i] = v.y;
-            qf[2 * j + 1][i] = v.z;
-            qf[2 * j + 1][2 + i] = v.w;
-        }
-    }
-
-    float o[NN][4];
-#pragma unroll
-    for (int j = 0; j < NN; ++j)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) o[j][c] = 0.f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-
+    // Where this warp's blocks lie, 32 blocks (16 stages) at a time, one a lane: the row
+    // of the cache (-1: no such page) and the two scales; `nxt` is loaded while `cur` is used.
     const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * kStages * kStageBytes);
-    // Where this warp's blocks lie, 32 blocks at a time, one a lane: the row of the
-    // cache (-1: no such page) and the two scales; `next` is loaded while `cur` is used.
     const int pmask = (1 << a.b.page_shift) - 1;
-    auto block_pos = [&](int i) { return begin + (warp + i * kWarps) * kKvBlock; };
-    auto load_page = [&](int base) { return base + lane < mine ? kv_page(a.b, tl.s, block_pos(base + lane)) : -1; };
+    auto stage_pos = [&](int i) { return begin + (warp + i * kWarps) * (2 * kKvBlock); };
+    auto lane_pos = [&](int base) { return stage_pos(base + (lane >> 1)) + (lane & 1) * kKvBlock; };
+    auto load_page = [&](int base) {
+        return base + (lane >> 1) < mine && lane_pos(base) < end ? kv_page(a.b, tl.s, lane_pos(base)) : -1;
+    };
     auto slot_of = [&](int page, int base) {
         return page < 0 ? (int64_t)-1
-                        : (((int64_t)page * a.b.kv_heads + head) << a.b.page_shift) + (block_pos(base + lane) & pmask);
+                        : (((int64_t)page * a.b.kv_heads + head) << a.b.page_shift) + (lane_pos(base) & pmask);
     };
     auto load_scales = [&](int64_t slot, float& ks, float& vs) {
-        ks = slot < 0 ? 0.f : __ldg(a.Ks + (slot >> 4));
-        vs = slot < 0 ? 1.f : __ldg(a.Vs + (slot >> 4));
+        ks = slot < 0 ? 0.f : a.Ks[slot >> 4];
+        vs = slot < 0 ? 1.f : a.Vs[slot >> 4];
     };
     int64_t slot_cur = slot_of(load_page(0), 0), slot_nxt = -1;
     int page_nxt = -1;
     float ks_cur, vs_cur, ks_nxt = 0.f, vs_nxt = 1.f;
     load_scales(slot_cur, ks_cur, vs_cur);
-    auto issue = [&](int i, int base) {  // block i of this warp into its ring; one copy group, maybe empty
+    auto issue = [&](int i, int base) {  // stage i of this warp into its ring; one copy group, maybe empty
         if (i < mine) {
-            const int64_t slot = __shfl_sync(0xffffffffu, i - base < 32 ? slot_cur : slot_nxt, i & 31);
-            if (slot >= 0) {
-                const uint32_t dst = ring + (uint32_t)((i % kStages) * kStageBytes);
-                const uint8_t* k = a.K + slot * D + lane * 16;
-                const uint8_t* v = a.V + slot * D + lane * 16;
+            const uint32_t dst = ring + (uint32_t)((i % kStages) * kStageBytes);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int64_t slot = __shfl_sync(0xffffffffu, i - base < 16 ? slot_cur : slot_nxt, 2 * (i & 15) + k);
+                if (slot < 0) continue;
+                const uint8_t* ksrc = a.K + slot * D + lane * 16;
+                const uint8_t* vsrc = a.V + slot * D + lane * 16;
 #pragma unroll
                 for (int c = 0; c < kCopies; ++c) {
                     const int id = lane + 32 * c;
-                    const uint32_t off = block_off<D>(id / (D / 16), id % (D / 16));
-                    cp_async16(dst + off, k + 512 * c);
-                    cp_async16(dst + kBlockBytes + off, v + 512 * c);
+                    const uint32_t off = (uint32_t)(k * kBlockBytes) + block_off<D>(id / (D / 16), id % (D / 16));
+                    cp_async16(dst + off, ksrc + 512 * c);
+                    cp_async16(dst + 2 * kBlockBytes + off, vsrc + 512 * c);
                 }
             }
         }
@@ -224,132 +211,205 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) attn_split_kernel(con
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) issue(i, 0);
 
+    // Queries as the first product's right operand (column g of tile nt), and the constant
+    // each column starts from: codes enter as q 2^-24, so -128 sum_d q_d 2^-24.
+    uint32_t qf[NT][KS][2];
+    float q0[NT][2];
+    int hi[NT][2], lo[NT][2];  // what rows 8 nt + 2 t, + 1 see: [lo, hi)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const int r = tl.r0 + 8 * nt + g, tok = r / a.group;
+        const int64_t row = tl.row0 + tok;
+        const bool ok = 8 * nt + g < rows && row >= 0 && row < a.b.tokens && mine > 0;
+        const uint4* src = reinterpret_cast<const uint4*>(
+            a.Q + (ok ? row * a.q_stride + (int64_t)(head * a.group + (r - tok * a.group)) * D : 0) + t * (D / 4));
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < KS / 2; ++j) {
+            const uint4 v = ok ? src[j] : make_uint4(0, 0, 0, 0);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                qf[nt][2 * j + (i >> 1)][i & 1] = w[i];
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+                sum += f.x + f.y;
+            }
+        }
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            q0[nt][b] = __shfl_sync(0xffffffffu, sum, 4 * (2 * t + b)) * (-128.f * kCodeUnit);
+            const int rr = 8 * nt + 2 * t + b;
+            const int pos = first + (tl.r0 + rr) / a.group;
+            hi[nt][b] = rr < rows ? min(max(pos + 1, 0), end) : 0;
+            lo[nt][b] = a.window > 0 ? max(pos - a.window + 1, 0) : 0;
+        }
+    }
+
+    float o[MT][NT][4];
+#pragma unroll
+    for (int j = 0; j < MT; ++j)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) o[j][nt][c] = 0.f;
+    float m[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) m[nt][0] = m[nt][1] = -INFINITY, l[nt][0] = l[nt][1] = 0.f;
+
     for (int i = 0; i < mine; ++i) {
-        const int base = i & ~31;
-        if ((i & 31) == 0) {
+        const int base = i & ~15;
+        if ((i & 15) == 0) {
             if (i > 0) {
                 slot_cur = slot_nxt;
                 ks_cur = ks_nxt;
                 vs_cur = vs_nxt;
             }
-            page_nxt = load_page(base + 32);
-        } else if ((i & 31) == 8) {  // the pages have arrived long since
-            slot_nxt = slot_of(page_nxt, base + 32);
+            page_nxt = load_page(base + 16);
+        } else if ((i & 15) == 4) {  // the pages have arrived long since
+            slot_nxt = slot_of(page_nxt, base + 16);
             load_scales(slot_nxt, ks_nxt, vs_nxt);
         }
         issue(i + kStages - 1, base);
         asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
         __syncwarp();
-        const uint32_t kb = ring + (uint32_t)((i % kStages) * kStageBytes), vb = kb + kBlockBytes;
-        const float ks = __shfl_sync(0xffffffffu, ks_cur, i & 31) * a.scale_log2;
-        const float vs0 = __shfl_sync(0xffffffffu, vs_cur, i & 31);
-        const bool here = __shfl_sync(0xffffffffu, slot_cur >= 0 ? 1 : 0, i & 31) != 0;
-        // A scale of zero has codes of zero value only: any scale gives the same products.
-        // 2^-60 lies below every other scale (2^-31), so it never lifts the maximum.
-        const float vs = vs0 == 0.f ? 8.67361738e-19f : vs0;
-        const float lv = __log2f(vs), ivs = __frcp_rn(vs);
+        const uint32_t kb = ring + (uint32_t)((i % kStages) * kStageBytes), vb = kb + 2 * kBlockBytes;
 
-        // S = Q K^T: columns 2t, 2t + 1 of the two column tiles are keys 2t, 2t + 1 (+ 8)
-        float sc[2][4];
+        float sc[2][NT][4], ivs[2];
+        bool here[2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            uint32_t w[KS];
+        for (int k = 0; k < 2; ++k) {
+            const int from = 2 * (i & 15) + k;
+            const float ks = __shfl_sync(0xffffffffu, ks_cur, from) * (a.scale_log2 * (1.f / kCodeUnit));
+            const float vs0 = __shfl_sync(0xffffffffu, vs_cur, from);
+            here[k] = __shfl_sync(0xffffffffu, slot_cur >= 0 ? 1 : 0, from) != 0;
+            // A scale of zero has codes of zero value only: any scale gives the same products.
+            // 2^-60 lies below every other scale (2^-31), so it never lifts the maximum.
+            const float vs = vs0 == 0.f ? 8.67361738e-19f : vs0;
+            const float lv = __log2f(vs);
+            ivs[k] = __frcp_rn(vs);
+            // S^T = K Q^T: rows g, g + 8 are keys, columns 2t, 2t + 1 query rows
+            uint32_t w[2][KS];
 #pragma unroll
-            for (int c = 0; c < D / 64; ++c) {
-                const uint4 v = lds128(kb + block_off<D>(g + 8 * h, t * (D / 64) + c));
-                w[4 * c] = v.x;
-                w[4 * c + 1] = v.y;
-                w[4 * c + 2] = v.z;
-                w[4 * c + 3] = v.w;
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c) {
+                    const uint4 v =
+                        lds128(kb + (uint32_t)(k * kBlockBytes) + block_off<D>(g + 8 * h, t * (D / 64) + c));
+                    w[h][4 * c] = v.x;
+                    w[h][4 * c + 1] = v.y;
+                    w[h][4 * c + 2] = v.z;
+                    w[h][4 * c + 3] = v.w;
+                }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                sc[k][nt][0] = sc[k][nt][2] = q0[nt][0];
+                sc[k][nt][1] = sc[k][nt][3] = q0[nt][1];
             }
 #pragma unroll
             for (int j = 0; j < KS; ++j) {
-                const uint32_t b0 = codes_half2<0x4140u>(w[j]), b1 = codes_half2<0x4342u>(w[j]);
-                if (j == 0)
-                    mma_16816_z(sc[h], qf[j][0], qf[j][1], qf[j][2], qf[j][3], b0, b1);
-                else
-                    mma_16816(sc[h], qf[j][0], qf[j][1], qf[j][2], qf[j][3], b0, b1);
+                const uint32_t a0 = prmt(w[0][j], 0u, 0x4140u), a1 = prmt(w[1][j], 0u, 0x4140u);
+                const uint32_t a2 = prmt(w[0][j], 0u, 0x4342u), a3 = prmt(w[1][j], 0u, 0x4342u);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) mma_16816(sc[k][nt], a0, a1, a2, a3, qf[nt][j][0], qf[nt][j][1]);
             }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) sc[k][nt][c] = fmaf(sc[k][nt][c], ks, lv);
         }
+        const int p0 = stage_pos(i);
+        if (!here[0] || !here[1] || p0 < all_lo || p0 + 2 * kKvBlock > all_hi) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+            for (int k = 0; k < 2; ++k)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) sc[h][c] = fmaf(sc[h][c], ks, lv);
-        const int p0 = block_pos(i);
-        if (!here || p0 < all_lo || p0 + kKvBlock > all_hi) {
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+                    for (int c = 0; c < 4; ++c) {
+                        const int j = p0 + 16 * k + g + 8 * (c >> 1), b = c & 1;
+                        if (!here[k] || j >= hi[nt][b] || j < lo[nt][b]) sc[k][nt][c] = -INFINITY;
+                    }
+        }
+        float f[NT][2];
+        bool move = false;
+        uint32_t pf[2][NT][2];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const int j = p0 + 8 * h + 2 * t + (c & 1), r = c >> 1;
-                    if (!here || j >= hi[r] || j < lo[r]) sc[h][c] = -INFINITY;
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                float x = fmaxf(fmaxf(sc[0][nt][b], sc[0][nt][b + 2]), fmaxf(sc[1][nt][b], sc[1][nt][b + 2]));
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+                x = fmaxf(x, m[nt][b]);
+                const float mu = x == -INFINITY ? 0.f : x;  // a row that has seen nothing yet
+                f[nt][b] = ex2(m[nt][b] - mu);
+                move |= f[nt][b] != 1.f;
+                m[nt][b] = x;
+                float sum[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    sc[k][nt][b] = ex2(sc[k][nt][b] - mu);
+                    sc[k][nt][b + 2] = ex2(sc[k][nt][b + 2] - mu);
+                    sum[k] = sc[k][nt][b] + sc[k][nt][b + 2];
                 }
-        }
-        float f[2], mu[2];
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            float x = fmaxf(fmaxf(sc[0][2 * r], sc[0][2 * r + 1]), fmaxf(sc[1][2 * r], sc[1][2 * r + 1]));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-            x = fmaxf(x, m[r]);
-            mu[r] = x == -INFINITY ? 0.f : x;  // a row that has seen nothing yet
-            f[r] = ex2(m[r] - mu[r]);
-            m[r] = x;
-        }
-        if (__any_sync(0xffffffffu, f[0] != 1.f || f[1] != 1.f)) {
-#pragma unroll
-            for (int j = 0; j < NN; ++j) {
-                o[j][0] *= f[0];
-                o[j][1] *= f[0];
-                o[j][2] *= f[1];
-                o[j][3] *= f[1];
+                l[nt][b] *= f[nt][b];
+                // a block hidden from the row may have any scale
+                if (sum[0] != 0.f) l[nt][b] = fmaf(sum[0], ivs[0], l[nt][b]);
+                if (sum[1] != 0.f) l[nt][b] = fmaf(sum[1], ivs[1], l[nt][b]);
             }
-            l[0] *= f[0];
-            l[1] *= f[1];
+        if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+            for (int j = 0; j < MT; ++j)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) o[j][nt][c] *= f[nt][c & 1];
         }
+        // P^T as the second product's right operand: columns are query rows, k the keys
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            float sum = 0.f;
+        for (int k = 0; k < 2; ++k)
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const float p = ex2(sc[h][2 * r + c] - mu[r]);
-                    sc[h][2 * r + c] = p;
-                    sum += p;
-                }
-            if (sum != 0.f) l[r] = fmaf(sum, ivs, l[r]);  // a block hidden from the row may have any scale
-        }
-        const uint32_t a0 = pack_half2(sc[0][0], sc[0][1]), a1 = pack_half2(sc[0][2], sc[0][3]);
-        const uint32_t a2 = pack_half2(sc[1][0], sc[1][1]), a3 = pack_half2(sc[1][2], sc[1][3]);
+            for (int nt = 0; nt < NT; ++nt) {
+                pf[k][nt][0] = transpose8(pack_half2(sc[k][nt][0], sc[k][nt][1]));
+                pf[k][nt][1] = transpose8(pack_half2(sc[k][nt][2], sc[k][nt][3]));
+            }
 
-        // O += P V: lane (g, t) holds the codes of keys 2t, 2t + 1, 2t + 8, 2t + 9 at
-        // d = (D / 8) g + nn, column tile nn's column g
-        uint32_t v[4][D / 32];
+        // O^T += V^T P^T: lane (g, t) holds the codes of keys 2t, 2t + 1, 2t + 8, 2t + 9 at
+        // d = (D / 8) g + e; row tile j has e = 2j in its row g and 2j + 1 in its row g + 8
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int row = 2 * t + (r & 1) + 8 * (r >> 1);
-            if constexpr (D == 128) {
-                const uint4 x = lds128(vb + block_off<D>(row, g));
-                v[r][0] = x.x;
-                v[r][1] = x.y;
-                v[r][2] = x.z;
-                v[r][3] = x.w;
-            } else {
-                const uint2 x = lds64(vb + block_off<D>(row, g >> 1) + (uint32_t)((g & 1) * 8));
-                v[r][0] = x.x;
-                v[r][1] = x.y;
+        for (int k = 0; k < 2; ++k) {
+            uint32_t v[4][D / 32];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = 2 * t + (r & 1) + 8 * (r >> 1);
+                const uint32_t at = vb + (uint32_t)(k * kBlockBytes);
+                if constexpr (D == 128) {
+                    const uint4 x = lds128(at + block_off<D>(row, g));
+                    v[r][0] = x.x;
+                    v[r][1] = x.y;
+                    v[r][2] = x.z;
+                    v[r][3] = x.w;
+                } else {
+                    const uint2 x = lds64(at + block_off<D>(row, g >> 1) + (uint32_t)((g & 1) * 8));
+                    v[r][0] = x.x;
+                    v[r][1] = x.y;
+                }
             }
-        }
 #pragma unroll
-        for (int w = 0; w < D / 32; ++w) {
-            // the two keys of a pair side by side: bytes (d, d, d + 1, d + 1)
-            const uint32_t x0 = prmt(v[0][w], v[1][w], 0x5140u), x1 = prmt(v[0][w], v[1][w], 0x7362u);
-            const uint32_t y0 = prmt(v[2][w], v[3][w], 0x5140u), y1 = prmt(v[2][w], v[3][w], 0x7362u);
-            mma_16816(o[4 * w], a0, a1, a2, a3, codes_half2<0x4140u>(x0), codes_half2<0x4140u>(y0));
-            mma_16816(o[4 * w + 1], a0, a1, a2, a3, codes_half2<0x4342u>(x0), codes_half2<0x4342u>(y0));
-            mma_16816(o[4 * w + 2], a0, a1, a2, a3, codes_half2<0x4140u>(x1), codes_half2<0x4140u>(y1));
-            mma_16816(o[4 * w + 3], a0, a1, a2, a3, codes_half2<0x4342u>(x1), codes_half2<0x4342u>(y1));
+            for (int w = 0; w < D / 32; ++w)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    // the two keys of a pair side by side: bytes (d, d, d + 1, d + 1)
+                    const uint32_t x = prmt(v[0][w], v[1][w], h ? 0x7362u : 0x5140u);
+                    const uint32_t y = prmt(v[2][w], v[3][w], h ? 0x7362u : 0x5140u);
+                    const uint32_t a0 = codes_half2<0x4140u>(x), a1 = codes_half2<0x4342u>(x);
+                    const uint32_t a2 = codes_half2<0x4140u>(y), a3 = codes_half2<0x4342u>(y);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        mma_16816(o[2 * w + h][nt], a0, a1, a2, a3, pf[k][nt][0], pf[k][nt][1]);
+                }
         }
         __syncwarp();  // the stage is read before it is filled again
     }
@@ -357,38 +417,38 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) attn_split_kernel(con
 
     // ---- join the warps
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-        if (t == 0) {
-            s_m[warp][g + 8 * r] = m[r];
-            s_l[warp][g + 8 * r] = l[r];
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) l[nt][b] += __shfl_xor_sync(0xffffffffu, l[nt][b], x);
+            if (g == 0) {
+                s_m[warp][8 * nt + 2 * t + b] = m[nt][b];
+                s_l[warp][8 * nt + 2 * t + b] = l[nt][b];
+            }
         }
-    }
     __syncthreads();  // also: every ring is free
     constexpr int kPitch = D + 4;
     float* s_o = reinterpret_cast<float*>(smem);  // [kWarps][kRows][kPitch]
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        const int row = g + 8 * r;
-        float mm = -INFINITY;
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, s_m[w][row]);
-        const float fac = ex2(m[r] - (mm == -INFINITY ? 0.f : mm));
-        // d = (D / 4) t + nn and (D / 4) t + D / 8 + nn
-        float* dst = s_o + (warp * kRows + row) * kPitch + t * (D / 4);
+        for (int b = 0; b < 2; ++b) {
+            const int row = 8 * nt + 2 * t + b;
+            float mm = -INFINITY;
 #pragma unroll
-        for (int j = 0; j < NN; j += 4) {
-            *reinterpret_cast<float4*>(dst + j) = make_float4(o[j][2 * r] * fac, o[j + 1][2 * r] * fac,
-                                                              o[j + 2][2 * r] * fac, o[j + 3][2 * r] * fac);
-            *reinterpret_cast<float4*>(dst + NN + j) =
-                make_float4(o[j][2 * r + 1] * fac, o[j + 1][2 * r + 1] * fac, o[j + 2][2 * r + 1] * fac,
-                            o[j + 3][2 * r + 1] * fac);
+            for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, s_m[w][row]);
+            const float fac = ex2(m[nt][b] - (mm == -INFINITY ? 0.f : mm));
+            float* dst = s_o + (warp * kRows + row) * kPitch + g * (D / 8);
+#pragma unroll
+            for (int j = 0; j < MT; j += 2)
+                *reinterpret_cast<float4*>(dst + 2 * j) = make_float4(o[j][nt][b] * fac, o[j][nt][b + 2] * fac,
+                                                                      o[j + 1][nt][b] * fac, o[j + 1][nt][b + 2] * fac);
         }
-    }
     __syncthreads();
-    // eight threads a row, D / 8 values each (interleaved by four)
-    const int row = threadIdx.x >> 3, part = threadIdx.x & 7;
+    // kPer threads a row, four values at a time
+    constexpr int kPer = kWarps * 32 / kRows;
+    const int row = threadIdx.x / kPer, part = threadIdx.x % kPer;
     if (row >= rows) return;
     const int r = tl.r0 + row, tok = r / a.group;
     const int64_t trow = tl.row0 + tok;
@@ -403,8 +463,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) attn_split_kernel(con
     const int64_t orow = trow * a.q_heads + qh;
     const float inv = a.splits > 1 ? 1.f : (ll == 0.f ? 0.f : __fdiv_rn(1.f, ll));
 #pragma unroll
-    for (int c = 0; c < D / 32; ++c) {
-        const int d = (c * 8 + part) * 4;
+    for (int d = part * 4; d < D; d += kPer * 4) {
         float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
@@ -476,13 +535,14 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnArgs a) {
     if (lane == 0 && a.lse) a.lse[row] = ll == 0.f ? -INFINITY : (mu + log2f(ll)) * kLn2;
 }
 
-constexpr int split_smem(int D) {
-    const int ring = kWarps * kStages * 2 * kKvBlock * D, join = kWarps * kRows * (D + 4) * 4;
+constexpr int split_smem(int D, int nt) {
+    const int ring = kWarps * ring_stages(D) * 4 * kKvBlock * D, join = kWarps * 8 * nt * (D + 4) * 4;
     return ring > join ? ring : join;
 }
 
 struct AttnPlan {
     int64_t units;
+    int rows;  // query rows of a tile
     int single, chunk, splits;
     int64_t ws_bytes;
 };
@@ -491,17 +551,18 @@ struct AttnPlan {
 // the GPU, in whole rounds of the four warps, at least 128 keys a CTA.
 int attn_plan(const mnb_kv_cache* c, const mnb_kv_batch* b, int q_heads, int window, int sms, AttnPlan* p) {
     const int G = q_heads / c->kv_heads;
-    p->single = (int64_t)b->max_new * G <= kRows;
-    p->units = p->single ? b->seqs : kv_items(b->tokens, b->seqs, G, 1);
+    p->rows = (int64_t)b->max_new * G <= 8 ? 8 : 16;
+    p->single = (int64_t)b->max_new * G <= p->rows;
+    p->units = p->single ? b->seqs : kv_items(b->tokens, b->seqs, G * (16 / p->rows), 1);
     if (p->units > INT32_MAX) return MNB_ERR_UNSUPPORTED;
     int64_t keys = b->max_len;
-    // a tile's rows lie kRows / G + 1 tokens apart at most; its range starts at a block's start
-    if (window > 0) keys = keys < (int64_t)window + kRows / G + 1 + kKvBlock ? keys : (int64_t)window + kRows / G + 1 + kKvBlock;
+    // a tile's rows lie rows / G + 1 tokens apart at most; its range starts at a block's start
+    if (window > 0) keys = keys < (int64_t)window + p->rows / G + 1 + kKvBlock ? keys : (int64_t)window + p->rows / G + 1 + kKvBlock;
     if (keys < 1) keys = 1;
     const int64_t want = (p->units * c->kv_heads * keys) / ((int64_t)sms * kCtasPerSm * 2) + 1;
-    const int64_t round = kWarps * kKvBlock;
+    const int64_t round = kWarps * 2 * kKvBlock;
     int64_t chunk = (want + round - 1) / round * round;
-    if (chunk < 2 * round) chunk = 2 * round;
+    if (chunk < round) chunk = round;
     p->splits = (int)((keys + chunk - 1) / chunk);
     if (p->splits == 1) chunk = (keys + kKvBlock - 1) / kKvBlock * kKvBlock;
     p->chunk = (int)(chunk < INT32_MAX - 64 ? chunk : INT32_MAX - 63);
@@ -513,20 +574,13 @@ bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p
 
 template <int D>
 cudaError_t launch(const AttnArgs& a, const AttnPlan& p, cudaStream_t st) {
-    attn_split_kernel<D><<<dim3((unsigned)p.units, (unsigned)a.b.kv_heads, (unsigned)p.splits), kWarps * 32,
-                           split_smem(D), st>>>(a);
-    cudaError_t e = cudaGetLastError();
+    const dim3 grid((unsigned)p.units, (unsigned)a.b.kv_heads, (unsigned)p.splits), block(kWarps * 32);
+    const cudaError_t e =
+        p.rows == 8 ? launch_pdl(attn_split_kernel<D, 1>, grid, block, split_smem(D, 1), st, a)
+                    : launch_pdl(attn_split_kernel<D, 2>, grid, block, split_smem(D, 2), st, a);
     if (e != cudaSuccess || p.splits == 1) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(((int64_t)a.b.tokens * a.q_heads + 7) / 8));
-    cfg.blockDim = dim3(256);
-    cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn_join_kernel<D>, a);
+    return launch_pdl(attn_join_kernel<D>, dim3((unsigned)(((int64_t)a.b.tokens * a.q_heads + 7) / 8)), dim3(256), 0,
+                      st, a);
 }
 
 // The checks mnb_attn and mnb_attn_workspace share.
@@ -542,9 +596,14 @@ int attn_check(const mnb_kv_cache* c, const mnb_kv_batch* b, int q_heads, int wi
 }  // namespace
 
 cudaError_t attn_prepare() {
-    cudaError_t e = cudaFuncSetAttribute(attn_split_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, split_smem(64));
-    if (e != cudaSuccess) return e;
-    return cudaFuncSetAttribute(attn_split_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, split_smem(128));
+    const auto allow = [](const void* f, int bytes) {
+        return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    };
+    cudaError_t e = allow((const void*)attn_split_kernel<64, 1>, split_smem(64, 1));
+    if (e == cudaSuccess) e = allow((const void*)attn_split_kernel<64, 2>, split_smem(64, 2));
+    if (e == cudaSuccess) e = allow((const void*)attn_split_kernel<128, 1>, split_smem(128, 1));
+    if (e == cudaSuccess) e = allow((const void*)attn_split_kernel<128, 2>, split_smem(128, 2));
+    return e;
 }
 
 }  // namespace mnb

@@ -1,5 +1,8 @@
 // kv_batch.cuh -- the paged 8-bit cache and the batch of sequences as the
 // kernels see them, and how a kernel finds the sequence of its work item.
+// The kernels start before the work ahead of them on the stream has finished
+// and wait for it (pdl_wait); what that work may have written is read with plain
+// loads, which the compiler keeps behind the wait, never with __ldg.
 #pragma once
 
 #include <stdint.h>
@@ -60,14 +63,14 @@ __device__ __forceinline__ int kv_find_seq(const KvArgs& a, int64_t u, int mul, 
         const int step = (hi - lo + 31) >> 5;
         const int s = lo + lane * step;
         int64_t at = INT64_MAX;
-        if (s < hi) at = (((int64_t)__ldg(a.q_start + s) * mul) >> 4) + (int64_t)extra * s;
+        if (s < hi) at = (((int64_t)a.q_start[s] * mul) >> 4) + (int64_t)extra * s;
         const unsigned le = __ballot_sync(0xffffffffu, at <= u);
         const int k = le ? 31 - __clz(le) : 0;  // the first item of `lo` is never past u
         at_lo = __shfl_sync(0xffffffffu, at, k);
         lo += k * step;
         hi = min(hi, lo + step);
     }
-    if (a.seqs == 1) at_lo = ((int64_t)__ldg(a.q_start) * mul) >> 4;
+    if (a.seqs == 1) at_lo = ((int64_t)a.q_start[0] * mul) >> 4;
     *first = at_lo;
     return lo;
 }
@@ -75,8 +78,8 @@ __device__ __forceinline__ int kv_find_seq(const KvArgs& a, int64_t u, int mul, 
 // Length of sequence s, and its tokens of this call: rows row0 .. row0 + n - 1 are the
 // positions len - n .. len - 1 (the first ones may lie before 0).
 __device__ __forceinline__ void kv_sequence(const KvArgs& a, int s, int* len, int* row0, int* n) {
-    const int q0 = __ldg(a.q_start + s), q1 = __ldg(a.q_start + s + 1);
-    const int l = __ldg(a.kv_len + s);
+    const int q0 = a.q_start[s], q1 = a.q_start[s + 1];
+    const int l = a.kv_len[s];
     *len = l < 0 ? 0 : (int)min((int64_t)l, a.max_tokens);
     *row0 = q0;
     *n = q1 > q0 ? q1 - q0 : 0;
@@ -84,7 +87,7 @@ __device__ __forceinline__ void kv_sequence(const KvArgs& a, int s, int* len, in
 
 // Page of position `pos` (below max_tokens) of sequence s, or -1.
 __device__ __forceinline__ int kv_page(const KvArgs& a, int s, int pos) {
-    const int p = __ldg(a.table + (int64_t)s * a.max_pages + (pos >> a.page_shift));
+    const int p = a.table[(int64_t)s * a.max_pages + (pos >> a.page_shift)];
     return p >= 0 && p < a.num_pages ? p : -1;
 }
 

@@ -79,6 +79,8 @@ __global__ void __launch_bounds__(kWarps * 32) kv_write_kernel(const KvIoArgs p)
     constexpr int LPR = D / 8;          // lanes of a row (8 values each)
     constexpr int RPI = 32 / LPR;       // rows of an iteration
     constexpr int NI = kKvBlock / RPI;  // iterations
+    pdl_wait();
+    pdl_launch_dependents();
     KvUnit u;
     if (!kv_unit(p, u)) return;
     const int lane = threadIdx.x & 31;
@@ -94,7 +96,7 @@ __global__ void __launch_bounds__(kWarps * 32) kv_write_kernel(const KvIoArgs p)
         const int pos = u.lo + i * RPI + r0;
         const int64_t row = u.row0 + (pos - u.first);
         const bool f = pos >= u.first && pos < u.len && row >= 0 && row < p.b.tokens;
-        v[i] = f ? __ldg(reinterpret_cast<const uint4*>(x + row * p.row_stride)) : make_uint4(0, 0, 0, 0);
+        v[i] = f ? *reinterpret_cast<const uint4*>(x + row * p.row_stride) : make_uint4(0, 0, 0, 0);
         fresh |= f ? 1u << i : 0u;
         kept |= pos < u.first ? 1u << i : 0u;
     }
@@ -157,6 +159,8 @@ __global__ void __launch_bounds__(kWarps * 32) kv_write_kernel(const KvIoArgs p)
 template <int D>
 __global__ void __launch_bounds__(kWarps * 32) kv_read_kernel(const KvIoArgs p) {
     constexpr int LPR = D / 8, RPI = 32 / LPR, NI = kKvBlock / RPI;
+    pdl_wait();
+    pdl_launch_dependents();
     KvUnit u;
     if (!kv_unit(p, u)) return;
     const int lane = threadIdx.x & 31;
@@ -166,8 +170,8 @@ __global__ void __launch_bounds__(kWarps * 32) kv_read_kernel(const KvIoArgs p) 
     uint2 q[NI];
 #pragma unroll
     for (int i = 0; i < NI; ++i)  // the block's 16 rows are always inside its page
-        q[i] = __ldg(reinterpret_cast<const uint2*>(codes + (int64_t)(i * RPI + r0) * D));
-    const float s = __ldg((u.which ? p.v_scales : p.k_scales) + (u.slot >> 4));
+        q[i] = *reinterpret_cast<const uint2*>(codes + (int64_t)(i * RPI + r0) * D);
+    const float s = (u.which ? p.v_scales : p.k_scales)[u.slot >> 4];
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
         const int pos = u.lo + i * RPI + r0;
@@ -216,18 +220,9 @@ int kv_io(const mnb_kv_cache* c, const mnb_kv_batch* b, void* K, void* V, int64_
     if (rc != MNB_OK) return rc;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const dim3 grid((unsigned)blocks), block(kWarps * 32);
-    if (write) {
-        if (c->head_dim == 64)
-            kv_write_kernel<64><<<grid, block, 0, st>>>(p);
-        else
-            kv_write_kernel<128><<<grid, block, 0, st>>>(p);
-    } else {
-        if (c->head_dim == 64)
-            kv_read_kernel<64><<<grid, block, 0, st>>>(p);
-        else
-            kv_read_kernel<128><<<grid, block, 0, st>>>(p);
-    }
-    return cudaGetLastError() == cudaSuccess ? MNB_OK : MNB_ERR_CUDA;
+    const auto kernel = write ? (c->head_dim == 64 ? kv_write_kernel<64> : kv_write_kernel<128>)
+                              : (c->head_dim == 64 ? kv_read_kernel<64> : kv_read_kernel<128>);
+    return launch_pdl(kernel, grid, block, 0, st, p) == cudaSuccess ? MNB_OK : MNB_ERR_CUDA;
 }
 
 }  // namespace

@@ -100,23 +100,49 @@ struct __align__(16) LpShared {
     unsigned long long bars[64];           // one a 4 KB piece
     unsigned long long list[kList];
     unsigned long long top[kMaxTop];       // this CTA's best, sorted
-    unsigned long long merged[kMaxCluster * kMaxTop];
+    unsigned long long merged[kMaxCluster * kMaxTop];  // first CTA: every CTA's best, sorted each
     unsigned long long best[kWarpCount];
     Stat warp_stat[kWarpCount];
-    Stat stat;
+    Stat stats[kMaxCluster];               // first CTA: every CTA's sums
     int count;
 };
 
-__device__ __forceinline__ unsigned long long ld_peer_u64(uint32_t addr, uint32_t rank) {
-    uint32_t remote;
-    unsigned long long v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(addr), "r"(rank));
-    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(remote));
-    return v;
+// The address that `addr` of this CTA has in the cluster's first CTA.
+__device__ __forceinline__ uint32_t in_first(uint32_t addr) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
+    return r;
 }
 
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// Pairs of binary32 values in one 64-bit register: one instruction for two.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t max_order(const uint4& q) {  // order16 of a piece's largest logit
+    const __half2 m2 = __hmax2(__hmax2(*reinterpret_cast<const __half2*>(&q.x), *reinterpret_cast<const __half2*>(&q.y)),
+                               __hmax2(*reinterpret_cast<const __half2*>(&q.z), *reinterpret_cast<const __half2*>(&q.w)));
+    return order16(__half_as_ushort(__hmax(__low2half(m2), __high2half(m2))));
 }
 
 __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LpArgs a) {
@@ -125,6 +151,9 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LpArgs a) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = (int)(blockIdx.x % a.cluster);
     const int64_t row = blockIdx.x / a.cluster;
+    if (a.cluster > 1) cluster_arrive();  // waited for before the first CTA's memory is written
+    pdl_wait();
+    pdl_launch_dependents();
     const __half* src = a.logits + row * a.row_stride;
     // The row in 16-byte pieces from the boundary at or before its start: element e of
     // piece v is token 8 v + e - skew.  Pieces that lie wholly in the row are copied in
@@ -163,7 +192,9 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LpArgs a) {
     __syncthreads();
 
     // ---- one look at the slice
-    Stat st = {-INFINITY, 0.f, 0.f};
+    float r = -INFINITY;                       // the reference
+    uint64_t z2 = 0, y2 = 0, ref2 = 0;         // both sums in two halves; -r, 0 while r is -infinity
+    const uint64_t c2 = pair(a.c, a.c);
     uint32_t best = 0;  // order16 of this thread's largest logit
     bool ok = true;
     for (int i = 0; i < pieces; ++i) {
@@ -172,34 +203,35 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LpArgs a) {
         const int v = i * kThreads + tid;
         if (v >= nv) break;
         const uint4 q = *reinterpret_cast<const uint4*>(smem + (size_t)v * 16);
-        const __half2 h[4] = {*reinterpret_cast<const __half2*>(&q.x), *reinterpret_cast<const __half2*>(&q.y),
-                              *reinterpret_cast<const __half2*>(&q.z), *reinterpret_cast<const __half2*>(&q.w)};
-        const __half2 m2 = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
-        const __half mh = __hmax(__low2half(m2), __high2half(m2));
-        best = max(best, order16(__half_as_ushort(mh)));
-        const float top = __half2float(mh) * a.c;
-        if (top > st.r + kMove || st.r == -INFINITY) {
-            if (top != -INFINITY && top == top) {
-                const Stat none = {top, 0.f, 0.f};
-                st = join(st, none);
-            }
+        const uint32_t order = max_order(q);
+        best = max(best, order);
+        const float top = __half2float(__ushort_as_half((unsigned short)unorder16(order))) * a.c;
+        if (top > r + kMove) {  // never for a NaN
+            const float f = ex2f(fmaxf(r - top, -1000.f));
+            const float2 zz = unpair(z2), yy = unpair(y2);
+            const float d = fmaxf(r - top, -1000.f);
+            z2 = pair(zz.x * f, zz.y * f);
+            y2 = pair(f * fmaf(zz.x, d, yy.x), f * fmaf(zz.y, d, yy.y));
+            r = top;
+            ref2 = pair(-top, -top);
         }
-        const float r = st.r == -INFINITY ? 0.f : st.r;
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const float2 f = __half22float2(h[j]);
-            const float y0 = max_nan(fmaf(f.x, a.c, -r), -200.f), y1 = max_nan(fmaf(f.y, a.c, -r), -200.f);
-            const float e0 = ex2f(y0), e1 = ex2f(y1);
-            st.z += e0 + e1;
-            st.y = fmaf(e0, y0, st.y);
-            st.y = fmaf(e1, y1, st.y);
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+            const float2 y = unpair(fma2(pair(f.x, f.y), c2, ref2));
+            const float y0 = max_nan(y.x, -200.f), y1 = max_nan(y.y, -200.f);
+            const uint64_t e = pair(ex2f(y0), ex2f(y1));
+            z2 = add2(z2, e);
+            y2 = fma2(e, pair(y0, y1), y2);
         }
     }
     // every copy has landed before anything below may end the CTA
     for (int i = 0; i < pieces; ++i)
         if (!mbar_wait(bars + 8u * i, 0, a.status, false)) break;
 
-    Stat ws = st;
+    const float2 zs = unpair(z2), ys = unpair(y2);
+    Stat ws = {r, zs.x + zs.y, ys.x + ys.y};
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) {
         Stat o;
@@ -214,7 +246,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LpArgs a) {
     if (tid == 0) {
         Stat s = sh.warp_stat[0];
         for (int w = 1; w < kWarpCount; ++w) s = join(s, sh.warp_stat[w]);
-        sh.stat = s;
+        sh.stats[0] = s;
     }
 
     // ---- this CTA's k best
@@ -227,11 +259,9 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LpArgs a) {
         }
         if (best >= tau && best > 0) {
             for (int v = tid; v < nv; v += kThreads) {
-                const uint4 q = *reinterpret_cast<const uint4*>(smem + (size_t)v * 16);
-                const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
+                if (max_order(*reinterpret_cast<const uint4*>(smem + (size_t)v * 16)) < tau) continue;
                 for (int e = 0; e < 8; ++e) {
-                    const uint32_t o = order16((w[e >> 1] >> ((e & 1) * 16)) & 0xFFFFu);
+                    const uint32_t o = order16(reinterpret_cast<const unsigned short*>(smem)[v * 8 + e]);
                     const int64_t id = (int64_t)(v0 + v) * 8 + e - skew;
                     if (o >= tau && id >= 0 && id < a.vocab) {
                         const int at = atomicAdd(&sh.count, 1);
@@ -277,30 +307,55 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LpArgs a) {
         }
     }
 
-    // ---- the cluster's first CTA joins
+    // ---- the cluster's first CTA joins what the others leave in its memory
     __syncthreads();
-    if (a.cluster > 1) cluster_sync();
-    if (rank == 0) {
-        const uint32_t s_top = smem_u32(sh.top), s_stat = smem_u32(&sh.stat);
-        const int nk = a.cluster * a.top;
-        for (int i = tid; i < nk; i += kThreads) sh.merged[i] = ld_peer_u64(s_top + 8u * (i % a.top), (uint32_t)(i / a.top));
-        Stat s = sh.stat;
-        for (int q = 1; q < a.cluster; ++q) {
-            Stat o;
-            o.r = ld_peer_f32(s_stat, (uint32_t)q);
-            o.z = ld_peer_f32(s_stat + 4u, (uint32_t)q);
-            o.y = ld_peer_f32(s_stat + 8u, (uint32_t)q);
-            s = join(s, o);
+    if (a.cluster > 1) {
+        cluster_wait();
+        if (rank > 0) {
+            const uint32_t dst = in_first(smem_u32(sh.merged)) + 8u * (uint32_t)(rank * a.top);
+            for (int i = tid; i < a.top; i += kThreads)
+                asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(dst + 8u * i), "l"(sh.top[i]) : "memory");
+            if (tid == 0) {
+                const uint32_t to = in_first(smem_u32(&sh.stats[rank]));
+                asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to), "f"(sh.stats[0].r) : "memory");
+                asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + 4u), "f"(sh.stats[0].z) : "memory");
+                asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + 8u), "f"(sh.stats[0].y) : "memory");
+            }
+        } else {
+            for (int i = tid; i < a.top; i += kThreads) sh.merged[i] = sh.top[i];
         }
+        cluster_arrive();
+        if (rank > 0) return;
+        cluster_wait();
+    } else {
+        for (int i = tid; i < a.top; i += kThreads) sh.merged[i] = sh.top[i];
         __syncthreads();
+    }
+    {
+        const int nk = a.cluster * a.top;
+        Stat s = sh.stats[0];
+        for (int q = 1; q < a.cluster; ++q) s = join(s, sh.stats[q]);
         const bool none = s.z == 0.f && s.r == -INFINITY;
         const float logz = log2f(s.z);
         const float bad = s.z != s.z || s.z == INFINITY ? __int_as_float(0x7fffffff) : 0.f;
         auto logp = [&](float x) { return none ? -INFINITY : (fmaf(x, a.c, -s.r) - logz) * kLn2f + bad; };
         for (int i = tid; i < nk; i += kThreads) {
+            // every list is sorted: its keys above k are found by halving, all lists at once
             const unsigned long long k = sh.merged[i];
             int above = 0;
-            for (int j = 0; j < nk; ++j) above += sh.merged[j] > k;
+#pragma unroll
+            for (int q = 0; q < kMaxCluster; ++q) {
+                if (q >= a.cluster) break;
+                int lo = 0, hi = a.top;
+                while (lo < hi) {
+                    const int mid = (lo + hi) >> 1;
+                    if (sh.merged[q * a.top + mid] > k)
+                        lo = mid + 1;
+                    else
+                        hi = mid;
+                }
+                above += lo;
+            }
             if (k != 0 && above < a.top) {
                 a.top_ids[row * a.top + above] = (int32_t)~(uint32_t)k;
                 a.top_logprobs[row * a.top + above] =
@@ -315,7 +370,6 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LpArgs a) {
             }
         }
     }
-    if (a.cluster > 1) cluster_sync();  // the peers' lists stay until they are read
 }
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -372,12 +426,14 @@ extern "C" int mnb_logprobs(const void* logits, int64_t rows, int64_t vocab, int
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = (size_t)a.slice_vecs * 16;
     cfg.stream = reinterpret_cast<cudaStream_t>(stream);
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = (unsigned)a.cluster;
     at[0].val.clusterDim.y = 1;
     at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, logprobs_kernel, a) == cudaSuccess ? MNB_OK : MNB_ERR_CUDA;
 }

@@ -145,10 +145,17 @@ def _ptr(x) -> Optional[int]:
     return x.data_ptr()
 
 
+def _current_stream() -> int:
+    import torch
+    try:  # the handle alone, without a Stream object around it (3 us less a call)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    except AttributeError:
+        return torch.cuda.current_stream().cuda_stream
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -329,19 +336,26 @@ class KVBatch:
         self.ref = ctypes.byref(self.desc)
 
 
+_half = None  # torch.float16, once torch is there
+
+
 def _is_half(x) -> bool:
-    import torch
-    return x.dtype is torch.float16
+    global _half
+    if _half is None:
+        import torch
+        _half = torch.float16
+    return x.dtype is _half
 
 
 def _rows(x, heads: int, dim: int, tokens: int, what: str) -> int:
     """Row stride of a token tensor [tokens, heads, dim] or [tokens, heads * dim] (rows may be strided)."""
-    s, n = x.stride(), x.dim()
-    if n == 3 and x.shape[1] == heads and x.shape[2] == dim:
-        ok = s[2] == 1 and (s[1] == dim or heads == 1)
+    shape, s = x.shape, x.stride()
+    if len(shape) == 3:
+        ok = shape[1] == heads and shape[2] == dim and s[2] == 1 and (s[1] == dim or heads == 1)
     else:
-        ok = n == 2 and x.shape[1] == heads * dim and s[1] == 1
-    _want(ok and x.shape[0] == tokens and _is_half(x), f"{what}: fp16 [tokens, heads, head_dim], whole rows")
+        ok = len(shape) == 2 and shape[1] == heads * dim and s[1] == 1
+    if not ok or shape[0] != tokens or not _is_half(x):
+        raise ValueError(f"{what}: fp16 [tokens, heads, head_dim], whole rows")
     return s[0] if tokens > 1 else max(s[0], heads * dim)
 
 
