@@ -1,27 +1,29 @@
 // logprobs.cu -- log probability of a given token, entropy and the most likely
 // tokens of each row of logits (mnb_logprobs).
 //
-// One thread-block cluster takes a row; each CTA copies a slice of it into
-// shared memory (bulk copies of 4 KB, one barrier each) and reads it as the
-// pieces arrive.  Every thread keeps sum 2^(x c - r) and sum 2^(x c - r) (x c - r),
+// One thread-block cluster takes a row, each of its CTAs a slice, each thread
+// every 256th 16-byte piece of it, straight from memory into registers (four
+// loads in flight a thread).  Every thread keeps sum 2^y and sum 2^y y of y = x c - r,
 // c = scale log2(e), with a reference r of its own: any r near the row's
-// maximum serves, so it is moved only when a value passes it by 2^4 (what the
-// entropy's difference of two terms can lose to it stays at 4 roundings of 1),
-// and the threads' sums are brought to a common one at the end:
-//     lse = ln 2 (M + log2 Z),   entropy = ln 2 (log2 Z - (sum 2^y y) / Z),   y = x c - M.
+// maximum serves, so it is set 2^4 above the largest value seen and moved only when a
+// value passes it by 2^4 (what the entropy's difference of two terms can lose to
+// it stays at a few roundings of 1), and the threads' sums are brought to a
+// common one at the end:
+//     lse = ln 2 (M + log2 Z),   entropy = ln 2 (log2 Z - (sum 2^y y) / Z).
+// A thread's fixed work (joining, selecting) costs as much as about 100 logits,
+// so a row gets no more CTAs than the GPU needs to be full.
 //
 // The k most likely: the k-th largest of the threads' own maxima is a value
-// that at least k of the CTA's logits reach, so only the few threads whose
-// maximum reaches it look at their logits again (in shared memory) and collect
-// those that do; ranks among the collected are counted directly.  FP16
-// logits tie often; the keys order equal ones by rising id.  Where more are collected
-// than the list holds (long runs of equal logits), the CTA takes its maximum k
-// times instead.  The cluster's first CTA merges the CTAs' lists through
-// distributed shared memory.
+// that at least k of the CTA's logits reach.  Each thread remembers which
+// piece held its maximum and the largest of its other pieces, so the few threads whose
+// maximum reaches that value look at one piece again, at all of theirs only
+// where a second one reaches it too; what reaches it is collected, and ranks among
+// the collected are counted directly.  FP16 logits tie often; the keys order
+// equal ones by rising id.  Where more are collected than the list holds (long
+// runs of equal logits), the CTA takes its maximum k times instead.  The cluster's
+// first CTA merges the lists that the others leave in its shared memory.
 //
-// Bound by memory: 2 bytes a logit, read once.  A slice is at most 40 KB where
-// eight CTAs a cluster allow it, so that several CTAs share an SM and one's
-// selection runs under the others' copies.
+// Bound by memory: 2 bytes a logit, read once.
 #include <cuda_fp16.h>
 
 #include "common.cuh"
@@ -36,8 +38,8 @@ constexpr int kWarpCount = kThreads / 32;
 constexpr int kMaxTop = 32;
 constexpr int kMaxCluster = 8;
 constexpr int kList = 512;              // candidates of a CTA
-constexpr int64_t kMaxVocab = 786432;   // eight slices of 192 KB
-constexpr uint32_t kSliceTarget = 40960;
+constexpr int kMaxVocab = 1 << 24;
+constexpr int kUnroll = 4;              // pieces of a thread in flight
 constexpr float kMove = 4.f;
 constexpr float kLn2f = 0.693147180559945309417f;
 
@@ -45,12 +47,10 @@ struct LpArgs {
     const __half* logits;
     int64_t rows, row_stride;
     int vocab, top, cluster;
-    int slice_vecs;  // 16-byte pieces of shared memory a CTA
-    float c;         // scale * log2(e)
+    float c;  // scale * log2(e)
     const int64_t* target;
     float *logprob, *entropy, *top_logprobs;
     int32_t* top_ids;
-    unsigned int* status;
 };
 
 __device__ __forceinline__ float ex2f(float x) {
@@ -96,8 +96,15 @@ __device__ __forceinline__ Stat join(Stat a, Stat b) {
     return s;
 }
 
+__device__ __forceinline__ Stat from_lane(const Stat& s, int x) {  // of lane ^ x
+    Stat o;
+    o.r = __shfl_xor_sync(0xffffffffu, s.r, x);
+    o.z = __shfl_xor_sync(0xffffffffu, s.z, x);
+    o.y = __shfl_xor_sync(0xffffffffu, s.y, x);
+    return o;
+}
+
 struct __align__(16) LpShared {
-    unsigned long long bars[64];           // one a 4 KB piece
     unsigned long long list[kList];
     unsigned long long top[kMaxTop];       // this CTA's best, sorted
     unsigned long long merged[kMaxCluster * kMaxTop];  // first CTA: every CTA's best, sorted each
@@ -139,81 +146,44 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     return r;
 }
 
-__device__ __forceinline__ uint32_t max_order(const uint4& q) {  // order16 of a piece's largest logit
+__device__ __forceinline__ float max_of(const uint4& q) {  // largest of a piece's logits
     const __half2 m2 = __hmax2(__hmax2(*reinterpret_cast<const __half2*>(&q.x), *reinterpret_cast<const __half2*>(&q.y)),
                                __hmax2(*reinterpret_cast<const __half2*>(&q.z), *reinterpret_cast<const __half2*>(&q.w)));
-    return order16(__half_as_ushort(__hmax(__low2half(m2), __high2half(m2))));
+    return __half2float(__hmax(__low2half(m2), __high2half(m2)));
 }
 
-__global__ void __launch_bounds__(kThreads) logprobs_kernel(const LpArgs a) {
-    extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ LpShared sh;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int rank = (int)(blockIdx.x % a.cluster);
-    const int64_t row = blockIdx.x / a.cluster;
-    if (a.cluster > 1) cluster_arrive();  // waited for before the first CTA's memory is written
-    pdl_wait();
-    pdl_launch_dependents();
-    const __half* src = a.logits + row * a.row_stride;
-    // The row in 16-byte pieces from the boundary at or before its start: element e of
-    // piece v is token 8 v + e - skew.  Pieces that lie wholly in the row are copied in
-    // bulk, the ragged ones at its ends element by element.
-    const int skew = (int)((reinterpret_cast<uintptr_t>(src) & 15u) >> 1);
-    const int vecs = (a.vocab + skew + 7) >> 3;
-    const int v0 = (int)((int64_t)rank * vecs / a.cluster), v1 = (int)((int64_t)(rank + 1) * vecs / a.cluster);
-    const int nv = v1 - v0;
-    const int f0 = max(v0, skew > 0 ? 1 : 0), f1 = min(v1, (a.vocab + skew) >> 3);  // whole pieces
-    const int pieces = (nv + kThreads - 1) / kThreads;
-    const uint32_t sbase = smem_u32(smem), bars = smem_u32(sh.bars);
-    if (tid == 0) {
-        for (int i = 0; i < pieces; ++i) mbar_init(bars + 8u * i, 1);
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        sh.count = 0;
-        for (int i = 0; i < pieces; ++i) {
-            const int p0 = max(v0 + i * kThreads, f0), p1 = min(v0 + (i + 1) * kThreads, f1);
-            if (p1 > p0) {
-                mbar_arrive_tx(bars + 8u * i, (uint32_t)(p1 - p0) * 16u);
-                bulk_load(sbase + (uint32_t)(p0 - v0) * 16u, src + ((int64_t)p0 * 8 - skew), (uint32_t)(p1 - p0) * 16u,
-                          bars + 8u * i);
-            } else {
-                mbar_arrive(bars + 8u * i);
-            }
-        }
-    }
-    // the ragged pieces: at most the row's first and last, with -infinity around the row
-    if (warp == 1 && lane < 16) {
-        const int v = lane < 8 ? v0 : v1 - 1, e = lane & 7;
-        if (nv > 0 && (v < f0 || v >= f1) && (lane < 8 || v1 - 1 > v0)) {
-            const int64_t id = (int64_t)v * 8 + e - skew;
-            const __half x = id >= 0 && id < a.vocab ? src[id] : __ushort_as_half((unsigned short)0xFC00u);
-            reinterpret_cast<__half*>(smem)[(v - v0) * 8 + e] = x;
-        }
-    }
-    __syncthreads();
+__device__ __forceinline__ uint32_t order_of(float x) { return order16(__half_as_ushort(__float2half_rn(x))); }
 
-    // ---- one look at the slice
-    float r = -INFINITY;                       // the reference
-    uint64_t z2 = 0, y2 = 0, ref2 = 0;         // both sums in two halves; -r, 0 while r is -infinity
-    const uint64_t c2 = pair(a.c, a.c);
-    uint32_t best = 0;  // order16 of this thread's largest logit
-    bool ok = true;
-    for (int i = 0; i < pieces; ++i) {
-        ok = ok && mbar_wait(bars + 8u * i, 0, a.status);
-        if (!ok) break;
-        const int v = i * kThreads + tid;
-        if (v >= nv) break;
-        const uint4 q = *reinterpret_cast<const uint4*>(smem + (size_t)v * 16);
-        const uint32_t order = max_order(q);
-        best = max(best, order);
-        const float top = __half2float(__ushort_as_half((unsigned short)unorder16(order))) * a.c;
+__device__ __forceinline__ uint4 ld_stream(const void* p) {  // once, from memory
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p)
+                 : "memory");
+    return v;
+}
+
+// The running sums and the largest logits of one thread.
+struct Look {
+    float r = -INFINITY;                // reference
+    uint64_t z2 = 0, y2 = 0, ref2 = 0;  // both sums in two halves; (-r, -r), 0 while r is -infinity
+    float best = -INFINITY, second = -INFINITY;  // largest logit; largest outside its piece
+    int at = -1;                        // piece of the largest logit
+
+    __device__ __forceinline__ void add(const uint4& q, int v, float c, uint64_t c2) {
+        const float x = max_of(q);
+        second = fmaxf(second, fminf(best, x));
+        at = x > best ? v : at;
+        best = fmaxf(best, x);
+        const float top = x * c;
         if (top > r + kMove) {  // never for a NaN
-            const float f = ex2f(fmaxf(r - top, -1000.f));
+            const float to = top + kMove;
+            const float d = fmaxf(r - to, -1000.f), f = ex2f(d);
             const float2 zz = unpair(z2), yy = unpair(y2);
-            const float d = fmaxf(r - top, -1000.f);
             z2 = pair(zz.x * f, zz.y * f);
             y2 = pair(f * fmaf(zz.x, d, yy.x), f * fmaf(zz.y, d, yy.y));
-            r = top;
-            ref2 = pair(-top, -top);
+            r = to;
+            ref2 = pair(-to, -to);
         }
         const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
@@ -226,50 +196,106 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LpArgs a) {
             y2 = fma2(e, pair(y0, y1), y2);
         }
     }
-    // every copy has landed before anything below may end the CTA
-    for (int i = 0; i < pieces; ++i)
-        if (!mbar_wait(bars + 8u * i, 0, a.status, false)) break;
+};
 
-    const float2 zs = unpair(z2), ys = unpair(y2);
-    Stat ws = {r, zs.x + zs.y, ys.x + ys.y};
+__global__ void __launch_bounds__(kThreads, 6) logprobs_kernel(const LpArgs a) {
+    __shared__ LpShared sh;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = (int)(blockIdx.x % a.cluster);
+    const int64_t row = blockIdx.x / a.cluster;
+    if (a.cluster > 1) cluster_arrive();  // waited for before the first CTA's memory is written
+    if (tid == 0) sh.count = 0;
+    pdl_wait();
+    pdl_launch_dependents();
+    const __half* src = a.logits + row * a.row_stride;
+    // The row in 16-byte pieces from the boundary at or before its start: element e of
+    // piece v is token 8 v + e - skew.  Pieces f0 .. f1 - 1 of this CTA's v0 .. v1 - 1 lie wholly
+    // in the row; at most one at either end of the row is ragged.
+    const int skew = (int)((reinterpret_cast<uintptr_t>(src) & 15u) >> 1);
+    const int vecs = (a.vocab + skew + 7) >> 3;
+    const int v0 = (int)((int64_t)rank * vecs / a.cluster), v1 = (int)((int64_t)(rank + 1) * vecs / a.cluster);
+    const int f0 = max(v0, skew > 0 ? 1 : 0), f1 = min(v1, (a.vocab + skew) >> 3);
+    const __half* pieces = src - skew;
+    auto token = [&](int v, int e) { return (int64_t)v * 8 + e - skew; };
+    auto logit = [&](int64_t id) {  // -infinity outside the row
+        return id >= 0 && id < a.vocab ? (uint32_t)__half_as_ushort(src[id]) : 0xFC00u;
+    };
+    auto piece = [&](int v) {
+        if (v >= f0 && v < f1) return ld_stream(pieces + (int64_t)v * 8);
+        uint32_t w[4];
 #pragma unroll
-    for (int x = 16; x > 0; x >>= 1) {
-        Stat o;
-        o.r = __shfl_xor_sync(0xffffffffu, ws.r, x);
-        o.z = __shfl_xor_sync(0xffffffffu, ws.z, x);
-        o.y = __shfl_xor_sync(0xffffffffu, ws.y, x);
-        ws = join(ws, o);
+        for (int j = 0; j < 4; ++j) w[j] = logit(token(v, 2 * j)) | (logit(token(v, 2 * j + 1)) << 16);
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    };
+    // the orders of a piece's tokens that are in the row and reach `least`
+    auto each = [&](int v, uint32_t least, auto&& take) {
+        const uint4 q = piece(v);
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int64_t id = token(v, e);
+            const uint32_t o = order16((w[e >> 1] >> ((e & 1) * 16)) & 0xFFFFu);
+            if (o >= least && id >= 0 && id < a.vocab) take(key_of(o, (uint32_t)id));
+        }
+    };
+
+    // ---- one look at the slice
+    Look look;
+    const uint64_t c2 = pair(a.c, a.c);
+    bool any = f0 + tid < f1;  // this thread has a piece
+    // the ragged pieces: the slice's first belongs to thread 0 too, its last to thread 1
+    const int edge = tid == 0 ? v0 : v1 - 1;
+    const bool ragged = tid < 2 && v1 > v0 && (edge < f0 || edge >= f1) && (tid == 0 || v1 - 1 > v0);
+    if (ragged) {
+        look.add(piece(edge), edge, a.c, c2);
+        any = true;
     }
+    int v = f0 + tid;
+    for (; v + (kUnroll - 1) * kThreads < f1; v += kUnroll * kThreads) {
+        uint4 q[kUnroll];
+#pragma unroll
+        for (int j = 0; j < kUnroll; ++j) q[j] = ld_stream(pieces + (int64_t)(v + j * kThreads) * 8);
+#pragma unroll
+        for (int j = 0; j < kUnroll; ++j) look.add(q[j], v + j * kThreads, a.c, c2);
+    }
+    for (; v < f1; v += kThreads) look.add(ld_stream(pieces + (int64_t)v * 8), v, a.c, c2);
+
+    const float2 zs = unpair(look.z2), ys = unpair(look.y2);
+    Stat ws = {look.r, zs.x + zs.y, ys.x + ys.y};
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) ws = join(ws, from_lane(ws, x));
     if (lane == 0) sh.warp_stat[warp] = ws;
     if (tid < kMaxTop) sh.top[tid] = 0;
     __syncthreads();
-    if (tid == 0) {
-        Stat s = sh.warp_stat[0];
-        for (int w = 1; w < kWarpCount; ++w) s = join(s, sh.warp_stat[w]);
-        sh.stats[0] = s;
+    if (warp == 0) {
+        Stat s = sh.warp_stat[lane % kWarpCount];
+#pragma unroll
+        for (int x = kWarpCount / 2; x > 0; x >>= 1) s = join(s, from_lane(s, x));
+        if (lane == 0) sh.stats[0] = s;
     }
 
     // ---- this CTA's k best
     if (a.top > 0) {
         uint32_t tau = 0;  // the k-th largest of the threads' maxima, bit by bit
+        const uint32_t best = any ? order_of(look.best) : 0u;
 #pragma unroll
         for (int bit = 15; bit >= 0; --bit) {
             const uint32_t t = tau | (1u << bit);
             if (__syncthreads_count(best >= t) >= a.top) tau = t;
         }
-        if (best >= tau && best > 0) {
-            for (int v = tid; v < nv; v += kThreads) {
-                if (max_order(*reinterpret_cast<const uint4*>(smem + (size_t)v * 16)) < tau) continue;
-                for (int e = 0; e < 8; ++e) {
-                    const uint32_t o = order16(reinterpret_cast<const unsigned short*>(smem)[v * 8 + e]);
-                    const int64_t id = (int64_t)(v0 + v) * 8 + e - skew;
-                    if (o >= tau && id >= 0 && id < a.vocab) {
-                        const int at = atomicAdd(&sh.count, 1);
-                        if (at < kList) sh.list[at] = key_of(o, (uint32_t)id);
-                    }
-                }
-            }
-        }
+        auto collect = [&](int v) {
+            each(v, tau, [&](unsigned long long k) {
+                const int at = atomicAdd(&sh.count, 1);
+                if (at < kList) sh.list[at] = k;
+            });
+        };
+        const bool reach = any && best >= tau;
+        const bool all = reach && (look.at < 0 || order_of(look.second) >= tau);
+        if (reach && !all) collect(look.at);
+        if (all && tid < 2 && ragged) collect(edge);
+        // a thread's whole pieces are looked at by its warp, one a lane
+        for (unsigned left = __ballot_sync(0xffffffffu, all); left; left &= left - 1)
+            for (int v = f0 + warp * 32 + (__ffs(left) - 1) + lane * kThreads; v < f1; v += 32 * kThreads) collect(v);
         __syncthreads();
         const int n = sh.count;
         if (n <= kList) {  // the order of the list does not matter: the keys differ
@@ -283,14 +309,8 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LpArgs a) {
             unsigned long long last = ~0ull;
             for (int j = 0; j < a.top; ++j) {
                 unsigned long long mine = 0;
-                for (int v = tid; v < nv; v += kThreads) {
-                    for (int e = 0; e < 8; ++e) {
-                        const uint32_t o = order16(reinterpret_cast<const unsigned short*>(smem)[v * 8 + e]);
-                        const int64_t id = (int64_t)(v0 + v) * 8 + e - skew;
-                        const unsigned long long k = key_of(o, (uint32_t)id);
-                        if (id >= 0 && id < a.vocab && k < last && k > mine) mine = k;
-                    }
-                }
+                for (int v = v0 + tid; v < v1; v += kThreads)
+                    each(v, 0u, [&](unsigned long long k) { mine = k < last && k > mine ? k : mine; });
 #pragma unroll
                 for (int x = 16; x > 0; x >>= 1) {
                     const unsigned long long o = __shfl_xor_sync(0xffffffffu, mine, x);
@@ -374,21 +394,14 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LpArgs a) {
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-// CTAs of a row: enough for slices of at most 40 KB, and while the rows leave
-// SMs idle as many as eight with 1 KB each.
+// CTAs of a row: as many as fill the SMs with four each, of at least 2048 logits.
 int cluster_for(int64_t rows, int64_t vocab, int sms) {
     int c = 1;
-    while (c < kMaxCluster && vocab * 2 > (int64_t)c * kSliceTarget) c *= 2;
-    while (c < kMaxCluster && rows * c * 2 <= sms && vocab * 2 >= (int64_t)c * 2 * 1024) c *= 2;
+    while (c < kMaxCluster && rows * c < (int64_t)sms * 4 && vocab >= (int64_t)c * 2 * 2048) c *= 2;
     return c;
 }
 
 }  // namespace
-
-cudaError_t logprobs_prepare() {
-    return cudaFuncSetAttribute(logprobs_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (int)(kMaxVocab / kMaxCluster * 2 + 64));
-}
 
 }  // namespace mnb
 
@@ -405,16 +418,16 @@ extern "C" int mnb_logprobs(const void* logits, int64_t rows, int64_t vocab, int
         !aligned(top_ids, 4) || !aligned(top_logprobs, 4))
         return MNB_ERR_ALIGN;
     int sms;
-    LpArgs a;
-    const int rc = device_ready(&sms, &a.status);
+    unsigned int* status;
+    const int rc = device_ready(&sms, &status);
     if (rc != MNB_OK) return rc;
+    LpArgs a;
     a.logits = static_cast<const __half*>(logits);
     a.rows = rows;
     a.row_stride = row_stride;
     a.vocab = (int)vocab;
     a.top = top;
     a.cluster = cluster_for(rows, vocab, sms);
-    a.slice_vecs = (int)(((vocab + 7 + 7) / 8 + a.cluster - 1) / a.cluster);
     a.c = scale * 1.44269504088896340736f;
     a.target = target;
     a.logprob = logprob;
@@ -424,7 +437,6 @@ extern "C" int mnb_logprobs(const void* logits, int64_t rows, int64_t vocab, int
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(rows * a.cluster));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = (size_t)a.slice_vecs * 16;
     cfg.stream = reinterpret_cast<cudaStream_t>(stream);
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;

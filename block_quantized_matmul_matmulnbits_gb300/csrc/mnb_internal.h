@@ -223,6 +223,5 @@ int kv_check(const mnb_kv_cache* c, const mnb_kv_batch* b, bool* empty);
 
 // Once per context: shared-memory limits of the kernels (hooked into the device setup).
 cudaError_t attn_prepare();
-cudaError_t logprobs_prepare();
 
 }  // namespace mnb
