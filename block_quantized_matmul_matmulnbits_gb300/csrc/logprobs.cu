@@ -41,6 +41,7 @@ constexpr int kList = 512;              // candidates of a CTA
 constexpr int kMaxVocab = 1 << 24;
 constexpr int kUnroll = 4;              // pieces of a thread in flight
 constexpr float kMove = 4.f;
+
 constexpr float kLn2f = 0.693147180559945309417f;
 
 struct LpArgs {
@@ -84,24 +85,24 @@ struct Stat {  // sums about the reference r (in units of log2)
     float r, z, y;
 };
 
-__device__ __forceinline__ Stat join(Stat a, Stat b) {
-    Stat s;
-    s.r = fmaxf(a.r, b.r);
-    const float u = s.r == -INFINITY ? 0.f : s.r;
-    // a reference of -infinity comes with sums of 0 (or NaN): no shift of its own
-    const float da = fmaxf(a.r - u, -1000.f), db = fmaxf(b.r - u, -1000.f);
-    const float fa = ex2f(da), fb = ex2f(db);
-    s.z = a.z * fa + b.z * fb;
-    s.y = fa * (a.y + a.z * da) + fb * (b.y + b.z * db);
-    return s;
+// The same sums about another reference, not below r.  One of -infinity comes with sums of
+// 0 (or NaN) and has no shift of its own.
+__device__ __forceinline__ Stat about(const Stat& s, float r) {
+    const float d = fmaxf(s.r - (r == -INFINITY ? 0.f : r), -1000.f), f = ex2f(d);
+    return {r, s.z * f, f * fmaf(s.z, d, s.y)};
 }
 
-__device__ __forceinline__ Stat from_lane(const Stat& s, int x) {  // of lane ^ x
-    Stat o;
-    o.r = __shfl_xor_sync(0xffffffffu, s.r, x);
-    o.z = __shfl_xor_sync(0xffffffffu, s.z, x);
-    o.y = __shfl_xor_sync(0xffffffffu, s.y, x);
-    return o;
+__device__ __forceinline__ Stat warp_join(Stat s) {
+    float r = s.r;
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) r = fmaxf(r, __shfl_xor_sync(0xffffffffu, r, x));
+    s = about(s, r);
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) {
+        s.z += __shfl_xor_sync(0xffffffffu, s.z, x);
+        s.y += __shfl_xor_sync(0xffffffffu, s.y, x);
+    }
+    return s;
 }
 
 struct __align__(16) LpShared {
@@ -146,10 +147,10 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     return r;
 }
 
-__device__ __forceinline__ float max_of(const uint4& q) {  // largest of a piece's logits
-    const __half2 m2 = __hmax2(__hmax2(*reinterpret_cast<const __half2*>(&q.x), *reinterpret_cast<const __half2*>(&q.y)),
-                               __hmax2(*reinterpret_cast<const __half2*>(&q.z), *reinterpret_cast<const __half2*>(&q.w)));
-    return __half2float(__hmax(__low2half(m2), __high2half(m2)));
+__device__ __forceinline__ __half2 as_half2(uint32_t x) { return *reinterpret_cast<const __half2*>(&x); }
+
+__device__ __forceinline__ __half2 max_of(const uint4& q) {
+    return __hmax2(__hmax2(as_half2(q.x), as_half2(q.y)), __hmax2(as_half2(q.z), as_half2(q.w)));
 }
 
 __device__ __forceinline__ uint32_t order_of(float x) { return order16(__half_as_ushort(__float2half_rn(x))); }
@@ -163,15 +164,20 @@ __device__ __forceinline__ uint4 ld_stream(const void* p) {  // once, from memor
     return v;
 }
 
-// The running sums and the largest logits of one thread.
+// The running sums and the largest logits of one thread, a group of up to kUnroll pieces
+// at a time.
 struct Look {
     float r = -INFINITY;                // reference
     uint64_t z2 = 0, y2 = 0, ref2 = 0;  // both sums in two halves; (-r, -r), 0 while r is -infinity
-    float best = -INFINITY, second = -INFINITY;  // largest logit; largest outside its piece
-    int at = -1;                        // piece of the largest logit
+    float best = -INFINITY, second = -INFINITY;  // largest logit; largest outside its group
+    int at = -1;                        // first piece of the largest logit's group
 
-    __device__ __forceinline__ void add(const uint4& q, int v, float c, uint64_t c2) {
-        const float x = max_of(q);
+    template <int N>
+    __device__ __forceinline__ void add(const uint4 (&q)[N], int v, float c, uint64_t c2) {
+        __half2 m2 = max_of(q[0]);
+#pragma unroll
+        for (int i = 1; i < N; ++i) m2 = __hmax2(m2, max_of(q[i]));
+        const float x = __half2float(__hmax(__low2half(m2), __high2half(m2)));
         second = fmaxf(second, fminf(best, x));
         at = x > best ? v : at;
         best = fmaxf(best, x);
@@ -185,20 +191,35 @@ struct Look {
             r = to;
             ref2 = pair(-to, -to);
         }
-        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+        // 0 times -infinity has to stay 0.  Where FP16's lowest value adds nothing (2^-160 of
+        // the reference), -infinity is replaced by it, two logits at a time; else the
+        // exponents are held at -200 one by one.
+        if (r >= fmaf(-65504.f, c, 160.f))
+            sum<false>(q, c2);
+        else
+            sum<true>(q, c2);
+    }
+
+    template <bool LOW, int N>
+    __device__ __forceinline__ void sum(const uint4 (&q)[N], uint64_t c2) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
-            const float2 y = unpair(fma2(pair(f.x, f.y), c2, ref2));
-            const float y0 = max_nan(y.x, -200.f), y1 = max_nan(y.y, -200.f);
-            const uint64_t e = pair(ex2f(y0), ex2f(y1));
-            z2 = add2(z2, e);
-            y2 = fma2(e, pair(y0, y1), y2);
+        for (int i = 0; i < N; ++i) {
+            const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const __half2 h = LOW ? as_half2(w[j]) : __hmax2_nan(as_half2(w[j]), as_half2(0xFBFFFBFFu));
+                const float2 f = __half22float2(h);
+                float2 y = unpair(fma2(pair(f.x, f.y), c2, ref2));
+                if (LOW) y = make_float2(max_nan(y.x, -200.f), max_nan(y.y, -200.f));
+                const uint64_t e = pair(ex2f(y.x), ex2f(y.y));
+                z2 = add2(z2, e);
+                y2 = fma2(e, pair(y.x, y.y), y2);
+            }
         }
     }
 };
 
-__global__ void __launch_bounds__(kThreads, 6) logprobs_kernel(const LpArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LpArgs a) {
     __shared__ LpShared sh;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = (int)(blockIdx.x % a.cluster);
@@ -229,8 +250,10 @@ __global__ void __launch_bounds__(kThreads, 6) logprobs_kernel(const LpArgs a) {
     };
     // the orders of a piece's tokens that are in the row and reach `least`
     auto each = [&](int v, uint32_t least, auto&& take) {
-        const uint4 q = piece(v);
-        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+        const uint4 x = piece(v);
+        const __half2 m2 = max_of(x);
+        if (order16(__half_as_ushort(__hmax(__low2half(m2), __high2half(m2)))) < least) return;
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const int64_t id = token(v, e);
@@ -247,30 +270,44 @@ __global__ void __launch_bounds__(kThreads, 6) logprobs_kernel(const LpArgs a) {
     const int edge = tid == 0 ? v0 : v1 - 1;
     const bool ragged = tid < 2 && v1 > v0 && (edge < f0 || edge >= f1) && (tid == 0 || v1 - 1 > v0);
     if (ragged) {
-        look.add(piece(edge), edge, a.c, c2);
+        const uint4 one[1] = {piece(edge)};
+        look.add(one, edge, a.c, c2);
         any = true;
     }
     int v = f0 + tid;
-    for (; v + (kUnroll - 1) * kThreads < f1; v += kUnroll * kThreads) {
-        uint4 q[kUnroll];
+    constexpr int kStep = kUnroll * kThreads;
+    uint4 q[2][kUnroll];  // a group, and the next one on its way
+    auto fetch = [&](uint4(&to)[kUnroll], int v) {
+        if (v + (kUnroll - 1) * kThreads < f1) {
 #pragma unroll
-        for (int j = 0; j < kUnroll; ++j) q[j] = ld_stream(pieces + (int64_t)(v + j * kThreads) * 8);
-#pragma unroll
-        for (int j = 0; j < kUnroll; ++j) look.add(q[j], v + j * kThreads, a.c, c2);
+            for (int j = 0; j < kUnroll; ++j) to[j] = ld_stream(pieces + (int64_t)(v + j * kThreads) * 8);
+        }
+    };
+    fetch(q[0], v);
+    while (v + (kUnroll - 1) * kThreads < f1) {
+        fetch(q[1], v + kStep);
+        look.add(q[0], v, a.c, c2);
+        v += kStep;
+        if (v + (kUnroll - 1) * kThreads >= f1) break;
+        fetch(q[0], v + kStep);
+        look.add(q[1], v, a.c, c2);
+        v += kStep;
     }
-    for (; v < f1; v += kThreads) look.add(ld_stream(pieces + (int64_t)v * 8), v, a.c, c2);
+    for (; v < f1; v += kThreads) {
+        const uint4 one[1] = {ld_stream(pieces + (int64_t)v * 8)};
+        look.add(one, v, a.c, c2);
+    }
 
     const float2 zs = unpair(look.z2), ys = unpair(look.y2);
     Stat ws = {look.r, zs.x + zs.y, ys.x + ys.y};
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) ws = join(ws, from_lane(ws, x));
+    ws = warp_join(ws);
     if (lane == 0) sh.warp_stat[warp] = ws;
     if (tid < kMaxTop) sh.top[tid] = 0;
     __syncthreads();
     if (warp == 0) {
-        Stat s = sh.warp_stat[lane % kWarpCount];
-#pragma unroll
-        for (int x = kWarpCount / 2; x > 0; x >>= 1) s = join(s, from_lane(s, x));
+        Stat s = {-INFINITY, 0.f, 0.f};
+        if (lane < kWarpCount) s = sh.warp_stat[lane];
+        s = warp_join(s);
         if (lane == 0) sh.stats[0] = s;
     }
 
@@ -291,8 +328,11 @@ __global__ void __launch_bounds__(kThreads, 6) logprobs_kernel(const LpArgs a) {
         };
         const bool reach = any && best >= tau;
         const bool all = reach && (look.at < 0 || order_of(look.second) >= tau);
-        if (reach && !all) collect(look.at);
-        if (all && tid < 2 && ragged) collect(edge);
+        if (reach && !all) {  // the group (a single piece at the slice's end, where the others are past it)
+            const int group = look.at >= f0 && look.at + (kUnroll - 1) * kThreads < f1 ? kUnroll : 1;
+            for (int j = 0; j < group; ++j) collect(look.at + j * kThreads);
+        }
+        if (all && ragged) collect(edge);
         // a thread's whole pieces are looked at by its warp, one a lane
         for (unsigned left = __ballot_sync(0xffffffffu, all); left; left &= left - 1)
             for (int v = f0 + warp * 32 + (__ffs(left) - 1) + lane * kThreads; v < f1; v += 32 * kThreads) collect(v);
@@ -353,8 +393,9 @@ __global__ void __launch_bounds__(kThreads, 6) logprobs_kernel(const LpArgs a) {
     }
     {
         const int nk = a.cluster * a.top;
-        Stat s = sh.stats[0];
-        for (int q = 1; q < a.cluster; ++q) s = join(s, sh.stats[q]);
+        Stat s = {-INFINITY, 0.f, 0.f};
+        if (lane < a.cluster) s = sh.stats[lane];
+        s = warp_join(s);
         const bool none = s.z == 0.f && s.r == -INFINITY;
         const float logz = log2f(s.z);
         const float bad = s.z != s.z || s.z == INFINITY ? __int_as_float(0x7fffffff) : 0.f;
@@ -394,10 +435,10 @@ __global__ void __launch_bounds__(kThreads, 6) logprobs_kernel(const LpArgs a) {
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-// CTAs of a row: as many as fill the SMs with four each, of at least 2048 logits.
+// CTAs of a row: enough for two on every SM (four fit), of at least 2048 logits each.
 int cluster_for(int64_t rows, int64_t vocab, int sms) {
     int c = 1;
-    while (c < kMaxCluster && rows * c < (int64_t)sms * 4 && vocab >= (int64_t)c * 2 * 2048) c *= 2;
+    while (c < kMaxCluster && rows * c < (int64_t)sms * 2 && vocab >= (int64_t)c * 2 * 2048) c *= 2;
     return c;
 }
 

@@ -106,6 +106,19 @@ def test_masked_tokens_and_empty_rows():
     check(x, [8001, 4, 4, 1, 5], 10)
 
 
+@pytest.mark.parametrize("scale", [1.0, 1e-5, 8.0])
+def test_lowest_values_beside_masked_tokens(scale):
+    # FP16's lowest value is a logit, -infinity is none, whatever the scale
+    x = np.full((4, 9001), -np.inf, np.float16)
+    x[0, ::3] = -65504
+    x[1, :10] = -65504
+    x[1, 10:20] = -65472
+    x[2] = -65504
+    x[3, ::2] = -65504
+    x[3, 7] = 1.0
+    check(x, [3, 11, 9000, 7], 12, scale=scale)
+
+
 def test_non_finite_rows_and_targets_of_no_token():
     r = np.random.default_rng(4)
     x = r.standard_normal((5, 3001)).astype(np.float16)

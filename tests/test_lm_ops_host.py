@@ -100,7 +100,7 @@ def child_logprobs_checks():
                dict(scale=float("nan")), dict(scale=float("inf")), dict(top=-1), dict(top=101), dict(logits=None),
                dict(logprob=None), dict(ids=None), dict(tops=None)):
         assert logprobs(**kw) == E.MNB_ERR_ARG, kw
-    for kw in (dict(vocab=786433, stride=800000), dict(top=33), dict(rows=1 << 40)):
+    for kw in (dict(vocab=(1 << 24) + 1, stride=1 << 25), dict(top=33), dict(rows=1 << 40)):
         assert logprobs(**kw) == E.MNB_ERR_UNSUPPORTED, kw
     for kw in (dict(logits=A + 2), dict(target=A + 4), dict(logprob=A + 2), dict(ids=A + 1), dict(tops=A + 2),
                dict(entropy=A + 2)):
