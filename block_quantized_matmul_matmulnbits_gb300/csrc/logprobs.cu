@@ -248,9 +248,8 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LpArgs a) {
         for (int j = 0; j < 4; ++j) w[j] = logit(token(v, 2 * j)) | (logit(token(v, 2 * j + 1)) << 16);
         return make_uint4(w[0], w[1], w[2], w[3]);
     };
-    // the orders of a piece's tokens that are in the row and reach `least`
-    auto each = [&](int v, uint32_t least, auto&& take) {
-        const uint4 x = piece(v);
+    // the keys of a piece's tokens that are in the row and reach `least`
+    auto each = [&](const uint4& x, int v, uint32_t least, auto&& take) {
         const __half2 m2 = max_of(x);
         if (order16(__half_as_ushort(__hmax(__low2half(m2), __high2half(m2)))) < least) return;
         const uint32_t w[4] = {x.x, x.y, x.z, x.w};
@@ -320,22 +319,38 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LpArgs a) {
             const uint32_t t = tau | (1u << bit);
             if (__syncthreads_count(best >= t) >= a.top) tau = t;
         }
-        auto collect = [&](int v) {
-            each(v, tau, [&](unsigned long long k) {
+        auto collect = [&](const uint4& x, int v) {
+            each(x, v, tau, [&](unsigned long long k) {
                 const int at = atomicAdd(&sh.count, 1);
                 if (at < kList) sh.list[at] = k;
             });
         };
         const bool reach = any && best >= tau;
         const bool all = reach && (look.at < 0 || order_of(look.second) >= tau);
-        if (reach && !all) {  // the group (a single piece at the slice's end, where the others are past it)
-            const int group = look.at >= f0 && look.at + (kUnroll - 1) * kThreads < f1 ? kUnroll : 1;
-            for (int j = 0; j < group; ++j) collect(look.at + j * kThreads);
+        if (reach && !all) {  // the group, or the single piece at the slice's end; loads first
+            const bool group = look.at >= f0 && look.at + (kUnroll - 1) * kThreads < f1;
+            uint4 x[kUnroll];
+            x[0] = piece(look.at);
+#pragma unroll
+            for (int j = 1; j < kUnroll; ++j)
+                if (group) x[j] = ld_stream(pieces + (int64_t)(look.at + j * kThreads) * 8);
+            collect(x[0], look.at);
+            if (group)
+#pragma unroll
+                for (int j = 1; j < kUnroll; ++j) collect(x[j], look.at + j * kThreads);
         }
-        if (all && ragged) collect(edge);
-        // a thread's whole pieces are looked at by its warp, one a lane
-        for (unsigned left = __ballot_sync(0xffffffffu, all); left; left &= left - 1)
-            for (int v = f0 + warp * 32 + (__ffs(left) - 1) + lane * kThreads; v < f1; v += 32 * kThreads) collect(v);
+        if (all && ragged) collect(piece(edge), edge);
+        // a thread's whole pieces are looked at by its warp, two a lane at a time
+        for (unsigned left = __ballot_sync(0xffffffffu, all); left; left &= left - 1) {
+            int v = f0 + warp * 32 + (__ffs(left) - 1) + lane * kThreads;
+            for (; v < f1; v += 64 * kThreads) {
+                const int w = v + 32 * kThreads;
+                const uint4 x = ld_stream(pieces + (int64_t)v * 8);
+                const uint4 y = w < f1 ? ld_stream(pieces + (int64_t)w * 8) : x;
+                collect(x, v);
+                if (w < f1) collect(y, w);
+            }
+        }
         __syncthreads();
         const int n = sh.count;
         if (n <= kList) {  // the order of the list does not matter: the keys differ
@@ -350,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LpArgs a) {
             for (int j = 0; j < a.top; ++j) {
                 unsigned long long mine = 0;
                 for (int v = v0 + tid; v < v1; v += kThreads)
-                    each(v, 0u, [&](unsigned long long k) { mine = k < last && k > mine ? k : mine; });
+                    each(piece(v), v, 0u, [&](unsigned long long k) { mine = k < last && k > mine ? k : mine; });
 #pragma unroll
                 for (int x = 16; x > 0; x >>= 1) {
                     const unsigned long long o = __shfl_xor_sync(0xffffffffu, mine, x);
