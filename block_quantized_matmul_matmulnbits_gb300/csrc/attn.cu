@@ -28,11 +28,7 @@
 // chunks' by attn_join_kernel where a row tile has more than one.  The codes are
 // stored with their 16-byte chunks permuted by the row, so that both products'
 // operand reads are free of bank conflicts.
-#include <cuda_fp16.h>
-
-#include "common.cuh"
-#include "kv_batch.cuh"
-#include "mnb_internal.h"
+#include "attn_common.cuh"
 
 namespace mnb {
 
@@ -42,38 +38,6 @@ constexpr int kWarps = 4;
 constexpr int kCtasPerSm = 3;
 __host__ __device__ constexpr int ring_stages(int D) { return D == 64 ? 4 : 2; }  // stages of 32 keys in a warp's ring
 constexpr float kCodeUnit = 5.9604644775390625e-8f;           // 2^-24, FP16's smallest subnormal
-constexpr float kLog2e = 1.44269504088896340736f;
-constexpr float kLn2 = 0.693147180559945309417f;
-
-struct AttnArgs {
-    KvArgs b;
-    const uint8_t *K, *V;
-    const float *Ks, *Vs;
-    const __half* Q;
-    __half* out;
-    float* lse;          // [tokens, q_heads] or nullptr
-    int64_t q_stride, out_stride;
-    int q_heads, group;  // group: query heads of a kv head
-    float scale_log2;    // scale * log2(e)
-    int window;
-    int single;          // every sequence has at most one row tile: tile u is sequence u's
-    int chunk, splits;   // keys of a CTA, CTAs of a row tile
-    float* part;         // [tokens * q_heads, splits, head_dim] (splits > 1)
-    float* ml;           // [tokens * q_heads, splits, 2]: maximum of w, denominator
-};
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -97,38 +61,10 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     return y;
 }
 
-constexpr uint32_t kBias = 0x64806480u;  // half2(1024 + 128)
-
-// Two codes (bytes `sel` of w) as exact FP16 integers q - 128.
-template <uint32_t SEL>
-__device__ __forceinline__ uint32_t codes_half2(uint32_t w) {
-    return hsub2_rn(prmt(w, 0x64646464u, SEL), kBias);
-}
-
 // Byte offset of 16-byte chunk c of row r in a block of 16 rows of D codes.
 template <int D>
 __device__ __forceinline__ uint32_t block_off(int r, int c) {
     return D == 128 ? (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)) : (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
-}
-
-// The rows of one tile: sequence, and the tile's first row among the sequence's
-// n * group rows; false where the work item has no rows.
-struct Tile {
-    int s, len, n, r0;
-    int64_t row0;  // token row of the sequence's first token of the call
-};
-
-template <int ROWS>
-__device__ __forceinline__ bool find_tile(const AttnArgs& a, int64_t u, Tile& t) {
-    int64_t first = u;
-    t.s = a.single ? (int)u : kv_find_seq(a.b, u, a.group * (16 / ROWS), 1, &first);
-    int row0;
-    kv_sequence(a.b, t.s, &t.len, &row0, &t.n);
-    t.row0 = row0;
-    const int64_t r0 = (u - first) * ROWS;
-    if (r0 < 0 || r0 >= (int64_t)t.n * a.group) return false;
-    t.r0 = (int)r0;
-    return true;
 }
 
 template <int D, int NT>
@@ -146,7 +82,8 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) attn_split_kernel(con
     pdl_launch_dependents();
 
     Tile tl;
-    if (!find_tile<kRows>(a, blockIdx.x, tl)) return;
+    if (!find_tile(a, blockIdx.x, NT == 1 ? 3 : 4, tl)) return;
+    if ((int64_t)tl.n * a.group > a.most_rows) return;  // the prompt kernel's
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t = lane & 3;
     const int head = blockIdx.y, split = blockIdx.z;
@@ -541,31 +478,56 @@ constexpr int split_smem(int D, int nt) {
 }
 
 struct AttnPlan {
-    int64_t units;
-    int rows;  // query rows of a tile
-    int single, chunk, splits;
+    int split_rows;      // split kernel: query rows of a tile, 8 or 16; 0: not launched
+    int row_tiles;       // prompt kernel: tiles of 128 rows a CTA, 1 or 2; 0: not launched
+    int64_t split_units, prompt_units;
+    int split_single, prompt_single;  // every sequence of the kernel has at most one tile
+    int chunk, splits;   // both kernels'
     int64_t ws_bytes;
 };
 
-// How the keys are dealt out: about two CTAs' worth of work for every CTA slot of
-// the GPU, in whole rounds of the four warps, at least 128 keys a CTA.
+int64_t round_up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
+
+// Which kernels run, and how the keys are dealt out.  A sequence with at most 16 rows
+// (tokens x heads of a kv head) is the split kernel's.  Where the batch has longer ones, they are the
+// prompt kernel's, and the split kernel takes the rest if there can be any.
 int attn_plan(const mnb_kv_cache* c, const mnb_kv_batch* b, int q_heads, int window, int sms, AttnPlan* p) {
-    const int G = q_heads / c->kv_heads;
-    p->rows = (int64_t)b->max_new * G <= 8 ? 8 : 16;
-    p->single = (int64_t)b->max_new * G <= p->rows;
-    p->units = p->single ? b->seqs : kv_items(b->tokens, b->seqs, G * (16 / p->rows), 1);
-    if (p->units > INT32_MAX) return MNB_ERR_UNSUPPORTED;
+    const int G = q_heads / c->kv_heads, H = c->kv_heads;
+    const int64_t most = (int64_t)b->max_new * G;
+    *p = AttnPlan{};
+    const bool prompt = most > 16;
+    if (!prompt)
+        p->split_rows = most <= 8 ? 8 : 16;
+    else if (b->seqs > 1 && G <= 16 && b->tokens < (int64_t)b->seqs * b->max_new)
+        p->split_rows = G <= 8 ? 8 : 16;
+    p->split_units = b->seqs;  // one tile each
+    p->split_single = 1;
+    int span = p->split_rows / G + 1;  // tokens a tile's rows can lie apart
+    if (prompt) {
+        p->row_tiles = most <= kPromptTile ? 1 : 2;
+        p->prompt_single = most <= (int64_t)p->row_tiles * kPromptTile;
+        p->prompt_units = p->prompt_single ? b->seqs : kv_items(b->tokens, b->seqs, {G, p->row_tiles == 1 ? 7 : 8, 1});
+        span = p->row_tiles * kPromptTile / G + 1;
+    }
+    if (p->prompt_units > INT32_MAX) return MNB_ERR_UNSUPPORTED;
     int64_t keys = b->max_len;
-    // a tile's rows lie rows / G + 1 tokens apart at most; its range starts at a block's start
-    if (window > 0) keys = keys < (int64_t)window + p->rows / G + 1 + kKvBlock ? keys : (int64_t)window + p->rows / G + 1 + kKvBlock;
+    // with a window a tile sees its tokens' windows, from a block's start
+    if (window > 0 && keys > (int64_t)window + span + kKvBlock) keys = (int64_t)window + span + kKvBlock;
     if (keys < 1) keys = 1;
-    const int64_t want = (p->units * c->kv_heads * keys) / ((int64_t)sms * kCtasPerSm * 2) + 1;
-    const int64_t round = kWarps * 2 * kKvBlock;
-    int64_t chunk = (want + round - 1) / round * round;
-    if (chunk < round) chunk = round;
+    int64_t chunk;
+    if (prompt) {
+        // a CTA an SM: split only where there are fewer tiles than SMs, at least 512 keys each
+        const int64_t tiles = p->prompt_units * H;
+        chunk = tiles >= sms ? keys : round_up((tiles * keys + sms - 1) / sms, 128);
+        if (chunk < 512) chunk = 512;
+        if (p->split_rows && chunk > 8192) chunk = 8192;  // a single token's CTA walks its chunk alone
+    } else {
+        // about two CTAs' worth of work for every CTA slot, whole rounds of the four warps
+        chunk = round_up((p->split_units * H * keys) / ((int64_t)sms * kCtasPerSm * 2) + 1, kWarps * 2 * kKvBlock);
+    }
     p->splits = (int)((keys + chunk - 1) / chunk);
-    if (p->splits == 1) chunk = (keys + kKvBlock - 1) / kKvBlock * kKvBlock;
-    p->chunk = (int)(chunk < INT32_MAX - 64 ? chunk : INT32_MAX - 63);
+    chunk = round_up(chunk, 128);
+    p->chunk = (int)(chunk < INT32_MAX - 128 ? chunk : INT32_MAX - 127);
     p->ws_bytes = p->splits > 1 ? (int64_t)b->tokens * q_heads * p->splits * (c->head_dim + 2) * 4 : 0;
     return MNB_OK;
 }
@@ -573,11 +535,20 @@ int attn_plan(const mnb_kv_cache* c, const mnb_kv_batch* b, int q_heads, int win
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 template <int D>
-cudaError_t launch(const AttnArgs& a, const AttnPlan& p, cudaStream_t st) {
-    const dim3 grid((unsigned)p.units, (unsigned)a.b.kv_heads, (unsigned)p.splits), block(kWarps * 32);
-    const cudaError_t e =
-        p.rows == 8 ? launch_pdl(attn_split_kernel<D, 1>, grid, block, split_smem(D, 1), st, a)
-                    : launch_pdl(attn_split_kernel<D, 2>, grid, block, split_smem(D, 2), st, a);
+cudaError_t launch(AttnArgs a, const AttnPlan& p, unsigned int* status, cudaStream_t st) {
+    cudaError_t e = cudaSuccess;
+    if (p.row_tiles) {
+        a.single = p.prompt_single;
+        a.skip_rows = p.split_rows;
+        e = attn_prompt_launch(a, p.row_tiles, p.prompt_units, status, st);
+    }
+    if (e == cudaSuccess && p.split_rows) {
+        a.single = p.split_single;
+        a.most_rows = p.row_tiles ? p.split_rows : INT64_MAX;
+        const dim3 grid((unsigned)p.split_units, (unsigned)a.b.kv_heads, (unsigned)p.splits), block(kWarps * 32);
+        e = p.split_rows == 8 ? launch_pdl(attn_split_kernel<D, 1>, grid, block, split_smem(D, 1), st, a)
+                              : launch_pdl(attn_split_kernel<D, 2>, grid, block, split_smem(D, 2), st, a);
+    }
     if (e != cudaSuccess || p.splits == 1) return e;
     return launch_pdl(attn_join_kernel<D>, dim3((unsigned)(((int64_t)a.b.tokens * a.q_heads + 7) / 8)), dim3(256), 0,
                       st, a);
@@ -589,7 +560,7 @@ int attn_check(const mnb_kv_cache* c, const mnb_kv_batch* b, int q_heads, int wi
     if (rc != MNB_OK) return rc;
     if (q_heads <= 0 || window < 0) return MNB_ERR_ARG;
     if (q_heads % c->kv_heads != 0 || q_heads > 65535) return MNB_ERR_UNSUPPORTED;
-    if ((int64_t)b->tokens * q_heads > (int64_t)1 << 40) return MNB_ERR_UNSUPPORTED;
+    if ((int64_t)b->tokens * q_heads > INT32_MAX) return MNB_ERR_UNSUPPORTED;
     return MNB_OK;
 }
 
@@ -603,6 +574,7 @@ cudaError_t attn_prepare() {
     if (e == cudaSuccess) e = allow((const void*)attn_split_kernel<64, 2>, split_smem(64, 2));
     if (e == cudaSuccess) e = allow((const void*)attn_split_kernel<128, 1>, split_smem(128, 1));
     if (e == cudaSuccess) e = allow((const void*)attn_split_kernel<128, 2>, split_smem(128, 2));
+    if (e == cudaSuccess) e = attn_prompt_prepare();
     return e;
 }
 
@@ -658,12 +630,14 @@ extern "C" int mnb_attn(const mnb_kv_cache* cache, const mnb_kv_batch* batch, co
     a.group = q_heads / cache->kv_heads;
     a.scale_log2 = scale * mnb::kLog2e;
     a.window = window;
-    a.single = p.single;
+    a.single = 0;
+    a.skip_rows = 0;
+    a.most_rows = INT64_MAX;
     a.chunk = p.chunk;
     a.splits = p.splits;
     a.part = static_cast<float*>(ws);
     a.ml = a.part ? a.part + batch->tokens * (int64_t)q_heads * p.splits * cache->head_dim : nullptr;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    const cudaError_t e = cache->head_dim == 64 ? mnb::launch<64>(a, p, st) : mnb::launch<128>(a, p, st);
+    const cudaError_t e = cache->head_dim == 64 ? mnb::launch<64>(a, p, status, st) : mnb::launch<128>(a, p, status, st);
     return e == cudaSuccess ? MNB_OK : MNB_ERR_CUDA;
 }

@@ -11,6 +11,23 @@
 
 namespace mnb {
 
+// Launch that may start before the preceding kernel on the stream has finished; the
+// kernel waits for it (pdl_wait) before it reads or writes anything.
+template <typename A>
+inline cudaError_t launch_pdl(void (*kernel)(A), dim3 grid, dim3 block, size_t smem, cudaStream_t st, const A& args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args);
+}
+
 constexpr int kKvBlock = MNB_KV_BLOCK;  // tokens that share a scale
 
 struct KvArgs {
@@ -43,19 +60,24 @@ inline KvArgs kv_args(const mnb_kv_cache* c, const mnb_kv_batch* b) {
 }
 
 // Work items of a sequence are numbered without a prefix sum over the batch:
-// sequence s owns the items from first_item(s) = (q_start[s] * mul >> 4) +
+// sequence s owns the items from first_item(s) = (q_start[s] * mul >> shift) +
 // extra * s on.  The floor of the difference of two sums is at most one below
 // the difference of the floors, so a sequence of n tokens always owns at least
-// floor(n * mul / 16) + extra items: with extra = 1 enough for its groups of 16
-// rows, with extra = 2 for the aligned blocks of 16 positions it touches (the
-// first and the last partly).  Surplus items find nothing to do.
-__host__ __device__ inline int64_t kv_items(int64_t tokens, int seqs, int mul, int extra) {
-    return ((tokens * mul) >> 4) + (int64_t)extra * seqs;
+// floor(n * mul / 2^shift) + extra items: with extra = 1 enough for its groups of
+// 2^shift rows (mul rows a token), with extra = 2, mul = 1 and shift = 4 for the aligned
+// blocks of 16 positions it touches (the first and the last partly).  Surplus items find
+// nothing to do.
+struct KvSplit {
+    int mul, shift, extra;
+};
+
+__host__ __device__ inline int64_t kv_items(int64_t tokens, int seqs, KvSplit k) {
+    return ((tokens * k.mul) >> k.shift) + (int64_t)k.extra * seqs;
 }
 
 // The sequence that owns item `u`, and its first item: a 32-way search by the
 // whole warp (two rounds of loads up to 1024 sequences).
-__device__ __forceinline__ int kv_find_seq(const KvArgs& a, int64_t u, int mul, int extra, int64_t* first) {
+__device__ __forceinline__ int kv_find_seq(const KvArgs& a, int64_t u, KvSplit k, int64_t* first) {
     const int lane = threadIdx.x & 31;
     int lo = 0, hi = a.seqs;
     int64_t at_lo = 0;
@@ -63,14 +85,14 @@ __device__ __forceinline__ int kv_find_seq(const KvArgs& a, int64_t u, int mul, 
         const int step = (hi - lo + 31) >> 5;
         const int s = lo + lane * step;
         int64_t at = INT64_MAX;
-        if (s < hi) at = (((int64_t)a.q_start[s] * mul) >> 4) + (int64_t)extra * s;
+        if (s < hi) at = kv_items(a.q_start[s], s, k);
         const unsigned le = __ballot_sync(0xffffffffu, at <= u);
-        const int k = le ? 31 - __clz(le) : 0;  // the first item of `lo` is never past u
-        at_lo = __shfl_sync(0xffffffffu, at, k);
-        lo += k * step;
+        const int last = le ? 31 - __clz(le) : 0;  // the first item of `lo` is never past u
+        at_lo = __shfl_sync(0xffffffffu, at, last);
+        lo += last * step;
         hi = min(hi, lo + step);
     }
-    if (a.seqs == 1) at_lo = ((int64_t)a.q_start[0] * mul) >> 4;
+    if (a.seqs == 1) at_lo = kv_items(a.q_start[0], 0, k);
     *first = at_lo;
     return lo;
 }

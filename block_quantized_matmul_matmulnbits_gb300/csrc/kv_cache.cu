@@ -25,6 +25,7 @@ namespace mnb {
 namespace {
 
 constexpr int kWarps = 8;
+constexpr KvSplit kBlocks = {1, 4, 2};  // the blocks of 16 positions that a sequence's tokens touch
 
 struct KvIoArgs {
     KvArgs b;
@@ -54,7 +55,7 @@ __device__ __forceinline__ bool kv_unit(const KvIoArgs& p, KvUnit& u) {
     u.which = c >= a.kv_heads;
     u.head = u.which ? c - a.kv_heads : c;
     int64_t first_item;
-    const int s = kv_find_seq(a, item, 1, 2, &first_item);
+    const int s = kv_find_seq(a, item, kBlocks, &first_item);
     int row0, n;
     kv_sequence(a, s, &u.len, &row0, &n);
     u.first = u.len - n;
@@ -204,7 +205,7 @@ int kv_io(const mnb_kv_cache* c, const mnb_kv_batch* b, void* K, void* V, int64_
     if (!aligned(K, 16) || !aligned(V, 16)) return MNB_ERR_ALIGN;
     KvIoArgs p;
     p.b = kv_args(c, b);
-    p.items = kv_items(b->tokens, b->seqs, 1, 2);
+    p.items = kv_items(b->tokens, b->seqs, kBlocks);
     p.row_stride = row_stride;
     p.k_codes = static_cast<uint8_t*>(c->K);
     p.v_codes = static_cast<uint8_t*>(c->V);

@@ -446,7 +446,7 @@ int64_t mnb_attn_workspace(const mnb_kv_cache* cache, const mnb_kv_batch* batch,
  * the entropy, and the most likely tokens.  With x = scale * logit (scale > 0,
  * the reciprocal of a temperature) and lse = log sum exp(x) over the row:
  *   logits        fp16, row r at logits + r * row_stride, [vocab] each; any
- *                 vocab of 1 .. 786432 and any row_stride >= vocab
+ *                 vocab of 1 .. 2^24 and any row_stride >= vocab
  *   target        int64 [rows] or NULL; a target outside [0, vocab) stands for
  *                 no token and gives logprob 0
  *   logprob       float [rows]: x[target] - lse          (NULL without target)
