@@ -12,13 +12,12 @@
 //    FP16 integers into shared memory (128-byte swizzle), keys and values in
 //    two stages each, and the tile's scales into a small ring.  Values stay [key][d]:
 //    the second product reads its right operand with d contiguous (MN-major).
-//  * warp 12 issues S_q = Q_q K^T for both row tiles, then O_q += P_q V for both.
-//    The order keeps the tensor core busy while a tile's probabilities are made:
-//    S_1 runs under the softmax of S_0, O_0 under that of S_1.
+//  * warp 12 issues O_0 += P_0 V, the next S_0 = Q_0 K^T, then the same for row tile 1:
+//    a row tile's softmax runs under the other one's products.
 //  * warps 0..3 and 4..7 own a row tile each, a thread a row: scores from tensor
-//    memory, maximum, 2^x, and the probabilities back over the scores
-//    (two FP16 values a column) as the second product's left operand.  The scores are read
-//    twice instead of held: 128 registers less a thread.  The accumulator is rescaled only when a
+//    memory into registers (which the other warps give up), maximum, 2^x, and the
+//    probabilities back over the scores (two FP16 values a column) as the second
+//    product's left operand.  The accumulator is rescaled only when a
 //    row's maximum has grown by more than 2^8 since the last time: FP16 holds
 //    probabilities up to 2^8 as exactly as up to 1, and the denominator is binary32.
 // Both row tiles share the unpacked keys and values: unpacking costs an eighth of
@@ -126,8 +125,27 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
         "%15, %16};" ::"r"(taddr),
         "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-        : "memory");
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]));
+}
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(taddr));
+}
+
+// Registers a thread of the calling warpgroup holds from here on.
+template <int N>
+__device__ __forceinline__ void give_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void take_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -181,7 +199,12 @@ struct Layout {
     static constexpr int kBytes = kBars + 256 + 1024;     // and the alignment of the swizzle atoms
     // tensor memory: NQ score tiles of 128 columns, then NQ accumulators of D
     static constexpr int kCols = NQ * (128 + D) <= 256 ? 256 : 512;
-    static constexpr int kThreads = 32 * (NQ * kSoftWarps + kUnpackWarps + 1);
+    // whole warpgroups (the last one issues the products); 128 or 168 registers a thread at
+    // launch, dealt out again to softmax, unpacking and the rest
+    static constexpr int kThreads = 128 * (NQ + 2);
+    static constexpr int kLaunchRegs = NQ == 2 ? 128 : 168;
+    static constexpr int kSoftRegs = NQ == 2 ? 176 : 232, kUnpackRegs = NQ == 2 ? 112 : 152, kOtherRegs = NQ == 2 ? 48 : 80;
+    static_assert(NQ * kSoftRegs + kUnpackRegs + kOtherRegs <= (NQ + 2) * kLaunchRegs, "within the launch's registers");
 };
 
 template <int D, int NQ>
@@ -250,40 +273,45 @@ __global__ void __launch_bounds__(Layout<D, NQ>::kThreads, 1) attn_prompt_kernel
     fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sptr + (tmem_slot - base));
 
-    if (warp == kMmaWarp) {
+    if (warp >= kMmaWarp) {
         // ---------------------------------------------------------------- products
-        if (lane == 0) {
+        give_registers<L::kOtherRegs>();
+        if (warp == kMmaWarp && lane == 0) {
             bool ok = mbar_wait(q_full, 0, status);
-            for (int j = 0; ok && j < nj; ++j) {
-                const int st = j & 1;
-                const uint32_t ph = (uint32_t)(j >> 1) & 1u;
-                if (!(ok = mbar_wait(k_full(st), ph, status))) break;
-                for (int q = 0; ok && q < NQ; ++q) {
-                    // the probabilities lie over the scores: the product that read them is done
-                    if (j > 0 && !(ok = mbar_wait(o_done(q), (uint32_t)(j - 1) & 1u, status))) break;
-                    fence_after();
-                    const uint32_t qs = base + L::kQ + q * L::kOperand, ks = base + L::kK + st * L::kOperand;
+            auto scores = [&](int q, int j) {  // S_q = Q_q K^T of tile j
+                const uint32_t qs = base + L::kQ + q * L::kOperand, ks = base + L::kK + (j & 1) * L::kOperand;
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        const uint32_t off = (uint32_t)(k / 4 * kSlab + k % 4 * 32);
-                        mma_ss(tmem + q * 128, operand(qs + off, 0), operand(ks + off, 0), idesc(kTileKeys, false), k > 0);
-                    }
-                    commit(s_full(q));
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint32_t off = (uint32_t)(k / 4 * kSlab + k % 4 * 32);
+                    mma_ss(tmem + q * 128, operand(qs + off, 0), operand(ks + off, 0), idesc(kTileKeys, false), k > 0);
                 }
-                if (!ok) break;
-                commit(k_empty(st));
-                if (!(ok = mbar_wait(v_full(st), ph, status))) break;
-                for (int q = 0; ok && q < NQ; ++q) {
+                commit(s_full(q));
+                if (q == NQ - 1) commit(k_empty(j & 1));
+            };
+            auto phase = [](int j) { return (uint32_t)(j >> 1) & 1u; };
+            if (ok && nj > 0 && (ok = mbar_wait(k_full(0), 0, status))) {
+                fence_after();
+                for (int q = 0; q < NQ; ++q) scores(q, 0);
+            }
+            for (int j = 0; ok && j < nj; ++j) {
+                for (int q = 0; q < NQ; ++q) {
                     if (!(ok = mbar_wait(p_full(q), (uint32_t)j & 1u, status))) break;
+                    if (q == 0 && !(ok = mbar_wait(v_full(j & 1), phase(j), status))) break;
                     fence_after();
-                    const uint32_t vs = base + L::kV + st * L::kOperand;
+                    const uint32_t vs = base + L::kV + (j & 1) * L::kOperand;
 #pragma unroll
-                    for (int k = 0; k < kTileKeys / 16; ++k)
+                    for (int k = 0; k < kTileKeys / 16; ++k)  // O_q += P_q V
                         mma_ts(tmem + NQ * 128 + q * D, tmem + q * 128 + 8 * k, operand(vs + k * 2048, kSlab),
                                idesc(D, true), (j | k) != 0);
                     commit(o_done(q));
+                    if (q == NQ - 1) commit(v_empty(j & 1));
+                    if (j + 1 == nj) continue;
+                    if (q == 0 && !(ok = mbar_wait(k_full((j + 1) & 1), phase(j + 1), status))) break;
+                    // the probabilities lie over the scores: the product that reads them is done
+                    if (!(ok = mbar_wait(o_done(q), (uint32_t)j & 1u, status))) break;
+                    fence_after();
+                    scores(q, j + 1);
                 }
-                if (ok) commit(v_empty(st));
             }
             commit(drain);  // tensor memory is freed only after every issued product has finished
             mbar_wait(drain, 0, status, false);
@@ -294,6 +322,7 @@ __global__ void __launch_bounds__(Layout<D, NQ>::kThreads, 1) attn_prompt_kernel
         // A load instruction of the four warps covers 16 rows (D = 128) or 32 (D = 64); the
         // eight lanes of a store phase hold four chunks of two rows, whose swizzled places
         // are eight different 16-byte columns.
+        give_registers<L::kUnpackRegs>();
         constexpr int kLoads = D / 16;  // 16-byte pieces a thread and tile
         const int uw = warp - kUnpack0;
         const int chunk = D == 128 ? (lane & 3) + ((lane >> 1) & 4) : lane & 3;
@@ -374,6 +403,7 @@ __global__ void __launch_bounds__(Layout<D, NQ>::kThreads, 1) attn_prompt_kernel
         }
     } else {
         // ---------------------------------------------------------------- softmax
+        take_registers<L::kSoftRegs>();
         const int q = warp / kSoftWarps, sub = warp & 3;  // row tile, quarter of its tensor-memory lanes
         const int r = q * kPromptTile + sub * 32 + lane;  // row of the CTA
         const int tok = (tl.r0 + r) / a.group, qh = head * a.group + (tl.r0 + r - tok * a.group);
@@ -403,81 +433,83 @@ __global__ void __launch_bounds__(Layout<D, NQ>::kThreads, 1) attn_prompt_kernel
         auto tile = [&](int j, auto masked) {
             constexpr bool MASK = decltype(masked)::value;
             const TileScales& t = scales[j & (kScaleRing - 1)];
+            float x[4][32];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_ld32(s_at + 32 * c, x[c]);
             const int p0 = begin + j * kTileKeys;
             auto sees = [&](int i) { return p0 + i < hi && p0 + i >= lo; };
+#pragma unroll
+            for (int c = 0; c < 4; ++c) landed(x[c]);
             float top = -INFINITY;
-            float v[2][32];
-            tmem_ld32(s_at, v[0]);
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                float(&x)[32] = v[c & 1];
-                landed(x);
-                if (c < 3) tmem_ld32(s_at + 32 * (c + 1), v[(c + 1) & 1]);
+                if (MASK) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) x[c][i] = sees(32 * c + i) ? x[c][i] : -INFINITY;
+                }
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
-                    float mx = -INFINITY;
+                    float mx[4];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        mx = fmaxf(mx, !MASK || sees(32 * c + 16 * b + i) ? x[16 * b + i] : -INFINITY);
-                    top = fmaxf(top, fmaf(mx, t.ks[2 * c + b], t.lv[2 * c + b]));
+                    for (int i = 0; i < 4; ++i) {
+                        const float* y = &x[c][16 * b + 4 * i];
+                        mx[i] = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
+                    }
+                    const float w = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    top = fmaxf(top, fmaf(w, t.ks[2 * c + b], t.lv[2 * c + b]));
                 }
             }
-            tmem_ld32(s_at, v[0]);
             const bool grown = top > m + kMoveBy || m == -INFINITY;
             const float to = grown ? top : m;
             const float f = grown && m != -INFINITY ? ex2(m - to) : 1.f;
             if (__any_sync(0xffffffffu, f != 1.f)) {  // then j > 0: a tile has been added up
-                landed(v[0]);  // (and read again below)
                 ok = __all_sync(0xffffffffu, mbar_wait(o_done(q), (uint32_t)(j - 1) & 1u, status));
                 if (!ok) return;
                 fence_after();
+#pragma unroll 1
+                for (int c = 0; c < D; c += 16) {
+                    uint32_t o[16];
+                    tmem_ld16(o_at + c, o);
 #pragma unroll
-                for (int c = 0; c < D / 32; ++c) {
-                    float o[32];
-                    tmem_ld32(o_at + 32 * c, o);
-                    landed(o);
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t w[16];
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(o[16 * h + i] * f);
-                        tmem_st16(o_at + 32 * c + 16 * h, w);
-                    }
+                    for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                    tmem_st16(o_at + c, o);
                 }
                 l *= f;
-                tmem_ld32(s_at, v[0]);
             }
             m = to;
             const float mu = to == -INFINITY ? 0.f : to;
+            float add = 0.f;
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                float(&x)[32] = v[c & 1];
-                landed(x);
-                if (c < 3) tmem_ld32(s_at + 32 * (c + 1), v[(c + 1) & 1]);
                 uint32_t p[16];
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
                     const float ks = t.ks[2 * c + b], lv = t.lv[2 * c + b] - mu;
                     const uint64_t ks2 = pair(ks, ks), lv2 = pair(lv, lv);
-                    uint64_t sum2 = 0;
+                    uint64_t sum2[2] = {0, 0};
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        float2 w = unpair(fma2(pair(x[16 * b + 2 * i], x[16 * b + 2 * i + 1]), ks2, lv2));
+                        const float* y = &x[c][16 * b + 2 * i];
+                        float2 w = unpair(fma2(pair(y[0], y[1]), ks2, lv2));
                         w.x = ex2(w.x);
                         w.y = ex2(w.y);
-                        if (MASK) {
-                            w.x = sees(32 * c + 16 * b + 2 * i) ? w.x : 0.f;
-                            w.y = sees(32 * c + 16 * b + 2 * i + 1) ? w.y : 0.f;
+                        if (MASK) {  // a hidden block may have any scale
+                            w.x = y[0] == -INFINITY ? 0.f : w.x;
+                            w.y = y[1] == -INFINITY ? 0.f : w.y;
                         }
-                        sum2 = add2(sum2, pair(w.x, w.y));
+                        sum2[i & 1] = add2(sum2[i & 1], pair(w.x, w.y));
                         p[8 * b + i] = pack_half2(w.x, w.y);
                     }
-                    const float2 s = unpair(sum2);
+                    const float2 s = unpair(add2(sum2[0], sum2[1]));
                     const float sum = s.x + s.y;
-                    if (sum != 0.f) l = fmaf(sum, t.ivs[2 * c + b], l);  // a hidden block may have any scale
+                    if (MASK)
+                        add = sum != 0.f ? fmaf(sum, t.ivs[2 * c + b], add) : add;
+                    else
+                        add = fmaf(sum, t.ivs[2 * c + b], add);
                 }
-                tmem_st16(s_at + 16 * c, p);  // over scores that have been read
+                tmem_st16(s_at + 16 * c, p);  // over scores that are in registers
             }
+            l += add;
         };
         for (int j = 0; j < nj; ++j) {
             ok = __all_sync(0xffffffffu, mbar_wait(s_full(q), (uint32_t)j & 1u, status));
