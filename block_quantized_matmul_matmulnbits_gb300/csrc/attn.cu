@@ -509,7 +509,7 @@ int attn_plan(const mnb_kv_cache* c, const mnb_kv_batch* b, int q_heads, int win
         p->prompt_units = p->prompt_single ? b->seqs : kv_items(b->tokens, b->seqs, {G, p->row_tiles == 1 ? 7 : 8, 1});
         span = p->row_tiles * kPromptTile / G + 1;
     }
-    if (p->prompt_units > INT32_MAX) return MNB_ERR_UNSUPPORTED;
+    if (p->prompt_units * H > INT32_MAX || p->split_units > INT32_MAX) return MNB_ERR_UNSUPPORTED;
     int64_t keys = b->max_len;
     // with a window a tile sees its tokens' windows, from a block's start
     if (window > 0 && keys > (int64_t)window + span + kKvBlock) keys = (int64_t)window + span + kKvBlock;
@@ -525,6 +525,7 @@ int attn_plan(const mnb_kv_cache* c, const mnb_kv_batch* b, int q_heads, int win
         // about two CTAs' worth of work for every CTA slot, whole rounds of the four warps
         chunk = round_up((p->split_units * H * keys) / ((int64_t)sms * kCtasPerSm * 2) + 1, kWarps * 2 * kKvBlock);
     }
+    if (keys / chunk >= 65535) chunk = round_up(keys / 65535 + 1, 128);
     p->splits = (int)((keys + chunk - 1) / chunk);
     chunk = round_up(chunk, 128);
     p->chunk = (int)(chunk < INT32_MAX - 128 ? chunk : INT32_MAX - 127);

@@ -17,9 +17,11 @@
 //  * warps 0..3 and 4..7 own a row tile each, a thread a row: scores from tensor
 //    memory into registers (which the other warps give up), maximum, 2^x, and the
 //    probabilities back over the scores (two FP16 values a column) as the second
-//    product's left operand.  The accumulator is rescaled only when a
-//    row's maximum has grown by more than 2^8 since the last time: FP16 holds
-//    probabilities up to 2^8 as exactly as up to 1, and the denominator is binary32.
+//    product's left operand.  The reference m of a row is its maximum as of the last time
+//    that mattered: FP16 holds probabilities up to 2^15 as exactly as up to 1, and the
+//    denominator is binary32.  So a tile's probabilities are first made about the old
+//    reference, without a maximum; only where a row's sum passes 2^15 is the maximum
+//    taken, the accumulator rescaled and the tile's probabilities made again.
 // Both row tiles share the unpacked keys and values: unpacking costs an eighth of
 // what the products do.
 //
@@ -36,14 +38,12 @@ constexpr int kTileKeys = 128;
 constexpr int kTileBlocks = kTileKeys / kKvBlock;
 constexpr int kSlab = kTileKeys * 128;  // 128 rows of 64 FP16 values
 constexpr int kScaleRing = 4;
-constexpr float kMoveBy = 8.f;   // a maximum that grew by no more (log2) stays the reference
-
-struct TileScales {   // of one 16-key block: w = s * ks + lv, denominator += sum * ivs
-    float ks[kTileBlocks], lv[kTileBlocks], ivs[kTileBlocks];
-};
+constexpr float kMoveBy = 8.f;       // a maximum that grew by no more (log2) stays the reference
+constexpr float kMostSum = 32768.f;  // of a row's 128 probabilities: each fits FP16
 
 struct PromptArgs {
     AttnArgs a;
+    int64_t units;
     unsigned int* status;
 };
 
@@ -195,7 +195,7 @@ struct Layout {
     static constexpr int kK = kQ + NQ * kOperand;         // two stages
     static constexpr int kV = kK + 2 * kOperand;          // two stages
     static constexpr int kScales = kV + 2 * kOperand;
-    static constexpr int kBars = kScales + kScaleRing * (int)sizeof(TileScales);
+    static constexpr int kBars = kScales + kScaleRing * kTileBlocks * 16;
     static constexpr int kBytes = kBars + 256 + 1024;     // and the alignment of the swizzle atoms
     // tensor memory: NQ score tiles of 128 columns, then NQ accumulators of D
     static constexpr int kCols = NQ * (128 + D) <= 256 ? 256 : 512;
@@ -217,12 +217,12 @@ __global__ void __launch_bounds__(Layout<D, NQ>::kThreads, 1) attn_prompt_kernel
     pdl_wait();
     pdl_launch_dependents();
 
-    // later tiles of a sequence see more keys: the long ones start first
+    // later tiles of a sequence see more keys: the long ones of every head start first
+    const int head = blockIdx.x % a.b.kv_heads, split = blockIdx.y;
     Tile tl;
-    if (!find_tile(a, (int64_t)gridDim.x - 1 - blockIdx.x, NQ == 1 ? 7 : 8, tl)) return;
+    if (!find_tile(a, P.units - 1 - blockIdx.x / a.b.kv_heads, NQ == 1 ? 7 : 8, tl)) return;
     if ((int64_t)tl.n * a.group <= a.skip_rows) return;  // the split kernel's
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int head = blockIdx.y, split = blockIdx.z;
     const int rows = (int)min((int64_t)tl.n * a.group - tl.r0, (int64_t)kRows);
     const int first = tl.len - tl.n;
     const int tok_a = tl.r0 / a.group, tok_b = (tl.r0 + rows - 1) / a.group;
@@ -237,7 +237,8 @@ __global__ void __launch_bounds__(Layout<D, NQ>::kThreads, 1) attn_prompt_kernel
 
     const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
     unsigned char* sptr = smem_raw + (base - raw);
-    TileScales* scales = reinterpret_cast<TileScales*>(sptr + L::kScales);
+    // of a tile's blocks: w = s * .x + .y, denominator += sum * .z
+    float4* scales = reinterpret_cast<float4*>(sptr + L::kScales);
     const uint32_t bars = base + L::kBars;
     auto k_full = [&](int s) { return bars + 8u * s; };
     auto k_empty = [&](int s) { return bars + 16u + 8u * s; };
@@ -380,10 +381,9 @@ __global__ void __launch_bounds__(Layout<D, NQ>::kThreads, 1) attn_prompt_kernel
             if (uw == 0 && lane < kTileBlocks) {
                 // no such page, or past the end: exponent -infinity, whatever the stage holds
                 const float v = vs == 0.f ? 8.67361738e-19f : vs;  // 2^-60: see attn_split_kernel
-                TileScales& t = scales[j & (kScaleRing - 1)];
-                t.ks[lb] = slot < 0 ? 0.f : ks * a.scale_log2;
-                t.lv[lb] = slot < 0 ? -INFINITY : __log2f(v);
-                t.ivs[lb] = slot < 0 ? 1.f : __frcp_rn(v);
+                scales[(j & (kScaleRing - 1)) * kTileBlocks + lb] =
+                    slot < 0 ? make_float4(0.f, -INFINITY, 1.f, 0.f)
+                             : make_float4(ks * a.scale_log2, __log2f(v), __frcp_rn(v), 0.f);
             }
             fence_async_proxy();
             __syncwarp();
@@ -432,7 +432,7 @@ __global__ void __launch_bounds__(Layout<D, NQ>::kThreads, 1) attn_prompt_kernel
         // One tile of keys; MASK: some row does not see all of it.
         auto tile = [&](int j, auto masked) {
             constexpr bool MASK = decltype(masked)::value;
-            const TileScales& t = scales[j & (kScaleRing - 1)];
+            const float4* t = scales + (j & (kScaleRing - 1)) * kTileBlocks;
             float x[4][32];
 #pragma unroll
             for (int c = 0; c < 4; ++c) tmem_ld32(s_at + 32 * c, x[c]);
@@ -440,25 +440,64 @@ __global__ void __launch_bounds__(Layout<D, NQ>::kThreads, 1) attn_prompt_kernel
             auto sees = [&](int i) { return p0 + i < hi && p0 + i >= lo; };
 #pragma unroll
             for (int c = 0; c < 4; ++c) landed(x[c]);
-            float top = -INFINITY;
+            if (MASK) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                if (MASK) {
+                for (int c = 0; c < 4; ++c)
 #pragma unroll
                     for (int i = 0; i < 32; ++i) x[c][i] = sees(32 * c + i) ? x[c][i] : -INFINITY;
+            }
+            float add;  // to the denominator
+            // The probabilities about a reference, over the scores (which are in registers); their sum.
+            auto probabilities = [&](float mu) {
+                float all = 0.f;
+                add = 0.f;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t p[16];
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        const float4 k = t[2 * c + b];
+                        const float lv = k.y - mu;
+                        const uint64_t ks2 = pair(k.x, k.x), lv2 = pair(lv, lv);
+                        uint64_t sum2[2] = {0, 0};
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float* y = &x[c][16 * b + 2 * i];
+                            float2 w = unpair(fma2(pair(y[0], y[1]), ks2, lv2));
+                            w.x = ex2(w.x);
+                            w.y = ex2(w.y);
+                            if (MASK) {  // a hidden block may have any scale
+                                w.x = y[0] == -INFINITY ? 0.f : w.x;
+                                w.y = y[1] == -INFINITY ? 0.f : w.y;
+                            }
+                            sum2[i & 1] = add2(sum2[i & 1], pair(w.x, w.y));
+                            p[8 * b + i] = pack_half2(w.x, w.y);
+                        }
+                        const float2 s = unpair(add2(sum2[0], sum2[1]));
+                        const float sum = s.x + s.y;
+                        all += sum;
+                        if (!MASK || sum != 0.f) add = fmaf(sum, k.z, add);
+                    }
+                    tmem_st16(s_at + 16 * c, p);
                 }
+                return all;
+            };
+            // The reference holds for most tiles: their sum says so.  A row that has none yet, or
+            // one that passes it too far (or is NaN), takes the warp through the maximum.
+            if (__all_sync(0xffffffffu, m != -INFINITY) && __all_sync(0xffffffffu, probabilities(m) <= kMostSum)) {
+                l += add;
+                return;
+            }
+            float top = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
-                    float mx[4];
+                    float w = -INFINITY;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float* y = &x[c][16 * b + 4 * i];
-                        mx[i] = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
-                    }
-                    const float w = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                    top = fmaxf(top, fmaf(w, t.ks[2 * c + b], t.lv[2 * c + b]));
+                    for (int i = 0; i < 16; ++i) w = fmaxf(w, x[c][16 * b + i]);
+                    top = fmaxf(top, fmaf(w, t[2 * c + b].x, t[2 * c + b].y));
                 }
-            }
             const bool grown = top > m + kMoveBy || m == -INFINITY;
             const float to = grown ? top : m;
             const float f = grown && m != -INFINITY ? ex2(m - to) : 1.f;
@@ -477,38 +516,7 @@ __global__ void __launch_bounds__(Layout<D, NQ>::kThreads, 1) attn_prompt_kernel
                 l *= f;
             }
             m = to;
-            const float mu = to == -INFINITY ? 0.f : to;
-            float add = 0.f;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                uint32_t p[16];
-#pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    const float ks = t.ks[2 * c + b], lv = t.lv[2 * c + b] - mu;
-                    const uint64_t ks2 = pair(ks, ks), lv2 = pair(lv, lv);
-                    uint64_t sum2[2] = {0, 0};
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float* y = &x[c][16 * b + 2 * i];
-                        float2 w = unpair(fma2(pair(y[0], y[1]), ks2, lv2));
-                        w.x = ex2(w.x);
-                        w.y = ex2(w.y);
-                        if (MASK) {  // a hidden block may have any scale
-                            w.x = y[0] == -INFINITY ? 0.f : w.x;
-                            w.y = y[1] == -INFINITY ? 0.f : w.y;
-                        }
-                        sum2[i & 1] = add2(sum2[i & 1], pair(w.x, w.y));
-                        p[8 * b + i] = pack_half2(w.x, w.y);
-                    }
-                    const float2 s = unpair(add2(sum2[0], sum2[1]));
-                    const float sum = s.x + s.y;
-                    if (MASK)
-                        add = sum != 0.f ? fmaf(sum, t.ivs[2 * c + b], add) : add;
-                    else
-                        add = fmaf(sum, t.ivs[2 * c + b], add);
-                }
-                tmem_st16(s_at + 16 * c, p);  // over scores that are in registers
-            }
+            probabilities(to == -INFINITY ? 0.f : to);
             l += add;
         };
         for (int j = 0; j < nj; ++j) {
@@ -585,8 +593,8 @@ cudaError_t allow() {
 }
 
 template <int D, int NQ>
-cudaError_t launch(const PromptArgs& p, int64_t units, cudaStream_t st) {
-    return launch_pdl(attn_prompt_kernel<D, NQ>, dim3((unsigned)units, (unsigned)p.a.b.kv_heads, (unsigned)p.a.splits),
+cudaError_t launch(const PromptArgs& p, cudaStream_t st) {
+    return launch_pdl(attn_prompt_kernel<D, NQ>, dim3((unsigned)(p.units * p.a.b.kv_heads), (unsigned)p.a.splits),
                       dim3(Layout<D, NQ>::kThreads), Layout<D, NQ>::kBytes, st, p);
 }
 
@@ -601,9 +609,9 @@ cudaError_t attn_prompt_prepare() {
 }
 
 cudaError_t attn_prompt_launch(const AttnArgs& a, int row_tiles, int64_t units, unsigned int* status, cudaStream_t st) {
-    const PromptArgs p = {a, status};
-    if (a.b.head_dim == 64) return row_tiles == 1 ? launch<64, 1>(p, units, st) : launch<64, 2>(p, units, st);
-    return row_tiles == 1 ? launch<128, 1>(p, units, st) : launch<128, 2>(p, units, st);
+    const PromptArgs p = {a, units, status};
+    if (a.b.head_dim == 64) return row_tiles == 1 ? launch<64, 1>(p, st) : launch<64, 2>(p, st);
+    return row_tiles == 1 ? launch<128, 1>(p, st) : launch<128, 2>(p, st);
 }
 
 }  // namespace mnb
