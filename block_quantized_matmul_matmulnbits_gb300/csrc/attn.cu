@@ -36,6 +36,8 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kCtasPerSm = 3;
+constexpr int kJoinOneWarp = 8;     // chunks that one warp joins
+constexpr int kSplitMostRows = 48;  // of a sequence
 __host__ __device__ constexpr int ring_stages(int D) { return D == 64 ? 4 : 2; }  // stages of 32 keys in a warp's ring
 constexpr float kCodeUnit = 5.9604644775390625e-8f;           // 2^-24, FP16's smallest subnormal
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
@@ -424,42 +426,75 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) attn_split_kernel(con
     }
 }
 
-// The chunks of a row joined in their order: out = sum_c 2^(m_c - m) o_c / sum_c 2^(m_c - m) l_c.
-// One warp a row (token, query head).
-template <int D>
+// The chunks of a row (token, query head) joined: out = sum_c 2^(m_c - m) o_c / sum_c 2^(m_c - m) l_c.
+// WARPS warps a row take the chunks in turn, four loads in flight each, and are added in
+// their order.  One warp a row while there are few chunks; with more, a row's loads one behind the
+// other are what the call waits for (one warp a row of 114 chunks: 68 us; eight: 5 us).
+template <int D, int WARPS>
 __global__ void __launch_bounds__(256) attn_join_kernel(const AttnArgs a) {
-    const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
+    constexpr int kRowsPerCta = 8 / WARPS;
+    constexpr int V = D / 32;  // values a lane
+    __shared__ float s_acc[8][D], s_l[8];
     pdl_wait();
-    if (row >= (int64_t)a.b.tokens * a.q_heads) return;
+    pdl_launch_dependents();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t row = (int64_t)blockIdx.x * kRowsPerCta + warp / WARPS;
+    const int w = warp % WARPS;
+    const bool ok = row < (int64_t)a.b.tokens * a.q_heads;
+    const int splits = ok ? a.splits : 0;
     const float2* ml = reinterpret_cast<const float2*>(a.ml) + row * a.splits;
     float mm = -INFINITY;
-    for (int c = lane; c < a.splits; c += 32) mm = fmaxf(mm, ml[c].x);
+    for (int c = lane; c < splits; c += 32) mm = fmaxf(mm, ml[c].x);
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, x));
     const float mu = mm == -INFINITY ? 0.f : mm;
-    constexpr int V = D / 32;  // values a lane
     float acc[V], ll = 0.f;
 #pragma unroll
     for (int j = 0; j < V; ++j) acc[j] = 0.f;
     const float* part = a.part + row * a.splits * D + lane * V;
-    for (int c = 0; c < a.splits; ++c) {
-        const float2 x = ml[c];
-        const float f = ex2(x.x - mu);
-        ll = fmaf(x.y, f, ll);
-        if (x.x == -INFINITY && x.y == 0.f) continue;  // a chunk with nothing to see: its sums are zeros
+    auto load = [&](int c, float (&v)[V]) {
         if constexpr (V == 4) {
             const float4 p = *reinterpret_cast<const float4*>(part + (int64_t)c * D);
-            acc[0] = fmaf(p.x, f, acc[0]);
-            acc[1] = fmaf(p.y, f, acc[1]);
-            acc[2] = fmaf(p.z, f, acc[2]);
-            acc[3] = fmaf(p.w, f, acc[3]);
+            v[0] = p.x, v[1] = p.y, v[2] = p.z, v[3] = p.w;
         } else {
             const float2 p = *reinterpret_cast<const float2*>(part + (int64_t)c * D);
-            acc[0] = fmaf(p.x, f, acc[0]);
-            acc[1] = fmaf(p.y, f, acc[1]);
+            v[0] = p.x, v[1] = p.y;
+        }
+    };
+    constexpr int kAhead = 4;
+    for (int c0 = w; c0 < splits; c0 += WARPS * kAhead) {
+        float v[kAhead][V];
+        float2 x[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int c = min(c0 + i * WARPS, splits - 1);
+            load(c, v[i]);
+            x[i] = ml[c];
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            // a chunk that saw nothing has sums of zero and m = -infinity: factor 0
+            const float f = c0 + i * WARPS < splits ? ex2(x[i].x - mu) : 0.f;
+            if (c0 + i * WARPS < splits) ll = fmaf(x[i].y, f, ll);
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                if (c0 + i * WARPS < splits) acc[j] = fmaf(v[i][j], f, acc[j]);
         }
     }
+    if constexpr (WARPS > 1) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) s_acc[warp][lane * V + j] = acc[j];
+        if (lane == 0) s_l[warp] = ll;
+        __syncthreads();
+        if (w != 0) return;
+#pragma unroll
+        for (int i = 1; i < WARPS; ++i) {
+            ll += s_l[warp + i];
+#pragma unroll
+            for (int j = 0; j < V; ++j) acc[j] += s_acc[warp + i][lane * V + j];
+        }
+    }
+    if (!ok) return;
     const float inv = ll == 0.f ? 0.f : __fdiv_rn(1.f, ll);
     const int64_t tok = row / a.q_heads;
     const int qh = (int)(row - tok * a.q_heads);
@@ -488,20 +523,23 @@ struct AttnPlan {
 
 int64_t round_up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
 
-// Which kernels run, and how the keys are dealt out.  A sequence with at most 16 rows
-// (tokens x heads of a kv head) is the split kernel's.  Where the batch has longer ones, they are the
-// prompt kernel's, and the split kernel takes the rest if there can be any.
+// Which kernels run, and how the keys are dealt out.  Up to 48 rows (tokens x heads of a kv
+// head) a sequence the split kernel is faster, in tiles of 8 or 16 rows that each read the keys
+// (35 rows: 13.4 against 17.8 us at 16 x 4,000 keys and 2 kv heads of 64, 20 rows: 110
+// against 144 us at 3 x 131,070 and 8 of 128), above it the prompt kernel (64 rows: 153
+// against 234 us there).  Where a batch may hold both long prompts and single tokens, the
+// sequences of one split tile (8 rows, or 16 with more than 8 heads a kv head) go to the split kernel.
 int attn_plan(const mnb_kv_cache* c, const mnb_kv_batch* b, int q_heads, int window, int sms, AttnPlan* p) {
     const int G = q_heads / c->kv_heads, H = c->kv_heads;
     const int64_t most = (int64_t)b->max_new * G;
     *p = AttnPlan{};
-    const bool prompt = most > 16;
+    const bool prompt = most > kSplitMostRows;
     if (!prompt)
         p->split_rows = most <= 8 ? 8 : 16;
     else if (b->seqs > 1 && G <= 16 && b->tokens < (int64_t)b->seqs * b->max_new)
         p->split_rows = G <= 8 ? 8 : 16;
-    p->split_units = b->seqs;  // one tile each
-    p->split_single = 1;
+    p->split_single = prompt || most <= p->split_rows;
+    p->split_units = p->split_single ? b->seqs : kv_items(b->tokens, b->seqs, {G, p->split_rows == 8 ? 3 : 4, 1});
     int span = p->split_rows / G + 1;  // tokens a tile's rows can lie apart
     if (prompt) {
         p->row_tiles = most <= kPromptTile ? 1 : 2;
@@ -551,8 +589,10 @@ cudaError_t launch(AttnArgs a, const AttnPlan& p, unsigned int* status, cudaStre
                               : launch_pdl(attn_split_kernel<D, 2>, grid, block, split_smem(D, 2), st, a);
     }
     if (e != cudaSuccess || p.splits == 1) return e;
-    return launch_pdl(attn_join_kernel<D>, dim3((unsigned)(((int64_t)a.b.tokens * a.q_heads + 7) / 8)), dim3(256), 0,
-                      st, a);
+    const int64_t rows = (int64_t)a.b.tokens * a.q_heads;
+    if (p.splits <= kJoinOneWarp)
+        return launch_pdl(attn_join_kernel<D, 1>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, st, a);
+    return launch_pdl(attn_join_kernel<D, 8>, dim3((unsigned)rows), dim3(256), 0, st, a);
 }
 
 // The checks mnb_attn and mnb_attn_workspace share.

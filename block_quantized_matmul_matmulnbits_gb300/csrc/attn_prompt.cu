@@ -70,7 +70,14 @@ __host__ __device__ constexpr uint32_t idesc(int n, bool n_major) {
     return (1u << 4) | (n_major ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 }
 
+__device__ __forceinline__ bool elected() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+    if (!elected()) return;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
@@ -80,6 +87,7 @@ __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint3
 }
 
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
+    if (!elected()) return;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
@@ -89,6 +97,7 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
 }
 
 __device__ __forceinline__ void commit(uint32_t bar) {
+    if (!elected()) return;
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 
@@ -138,6 +147,20 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
         : "r"(taddr));
 }
 
+// Bounded wait for the phase of `parity` (as mbar_wait), with a plain test first: the wait
+// with a suspend time takes 95 cycles even where the phase is complete, the test 15.
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, unsigned int* status, bool abortable = true) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return r != 0 || mbar_wait(bar, parity, status, abortable);
+}
+
 // Registers a thread of the calling warpgroup holds from here on.
 template <int N>
 __device__ __forceinline__ void give_registers() {
@@ -156,6 +179,15 @@ __device__ __forceinline__ uint32_t swizzled(int row, int chunk) {
 
 __device__ __forceinline__ void sts128(uint32_t at, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(at)
+                 : "memory");
+    return v;
 }
 
 __device__ __forceinline__ uint4 ldg128(const void* p) {
@@ -277,8 +309,8 @@ __global__ void __launch_bounds__(Layout<D, NQ>::kThreads, 1) attn_prompt_kernel
     if (warp >= kMmaWarp) {
         // ---------------------------------------------------------------- products
         give_registers<L::kOtherRegs>();
-        if (warp == kMmaWarp && lane == 0) {
-            bool ok = mbar_wait(q_full, 0, status);
+        if (warp == kMmaWarp) {
+            bool ok = __all_sync(0xffffffffu, bar_wait(q_full, 0, status));
             auto scores = [&](int q, int j) {  // S_q = Q_q K^T of tile j
                 const uint32_t qs = base + L::kQ + q * L::kOperand, ks = base + L::kK + (j & 1) * L::kOperand;
 #pragma unroll
@@ -290,14 +322,14 @@ __global__ void __launch_bounds__(Layout<D, NQ>::kThreads, 1) attn_prompt_kernel
                 if (q == NQ - 1) commit(k_empty(j & 1));
             };
             auto phase = [](int j) { return (uint32_t)(j >> 1) & 1u; };
-            if (ok && nj > 0 && (ok = mbar_wait(k_full(0), 0, status))) {
+            if (ok && nj > 0 && (ok = __all_sync(0xffffffffu, bar_wait(k_full(0), 0, status)))) {
                 fence_after();
                 for (int q = 0; q < NQ; ++q) scores(q, 0);
             }
-            for (int j = 0; ok && j < nj; ++j) {
+            for (int j = 0; __all_sync(0xffffffffu, ok && j < nj); ++j) {
                 for (int q = 0; q < NQ; ++q) {
-                    if (!(ok = mbar_wait(p_full(q), (uint32_t)j & 1u, status))) break;
-                    if (q == 0 && !(ok = mbar_wait(v_full(j & 1), phase(j), status))) break;
+                    if (!(ok = __all_sync(0xffffffffu, bar_wait(p_full(q), (uint32_t)j & 1u, status)))) break;
+                    if (q == 0 && !(ok = __all_sync(0xffffffffu, bar_wait(v_full(j & 1), phase(j), status)))) break;
                     fence_after();
                     const uint32_t vs = base + L::kV + (j & 1) * L::kOperand;
 #pragma unroll
@@ -306,10 +338,10 @@ __global__ void __launch_bounds__(Layout<D, NQ>::kThreads, 1) attn_prompt_kernel
                                idesc(D, true), (j | k) != 0);
                     commit(o_done(q));
                     if (q == NQ - 1) commit(v_empty(j & 1));
-                    if (j + 1 == nj) continue;
-                    if (q == 0 && !(ok = mbar_wait(k_full((j + 1) & 1), phase(j + 1), status))) break;
+                    if (__all_sync(0xffffffffu, j + 1 == nj)) continue;
+                    if (q == 0 && !(ok = __all_sync(0xffffffffu, bar_wait(k_full((j + 1) & 1), phase(j + 1), status)))) break;
                     // the probabilities lie over the scores: the product that reads them is done
-                    if (!(ok = mbar_wait(o_done(q), (uint32_t)j & 1u, status))) break;
+                    if (!(ok = __all_sync(0xffffffffu, bar_wait(o_done(q), (uint32_t)j & 1u, status)))) break;
                     fence_after();
                     scores(q, j + 1);
                 }
@@ -412,13 +444,16 @@ __global__ void __launch_bounds__(Layout<D, NQ>::kThreads, 1) attn_prompt_kernel
         const int pos = first + tok;
         const int hi = ok_row ? min(max(pos + 1, 0), end) : 0;
         const int lo = a.window > 0 ? max(pos - a.window + 1, 0) : 0;
-        {
-            const uint4* src = reinterpret_cast<const uint4*>(a.Q + (ok_row ? trow * a.q_stride + (int64_t)qh * D : 0));
+        {  // the warp's 32 rows into the operand, 16 bytes a lane, whole rows side by side
+            constexpr int kLanes = D / 8;
             const uint32_t to = base + L::kQ + q * L::kOperand;
-#pragma unroll
-            for (int c = 0; c < D / 8; ++c) {
-                const uint4 v = ok_row && nj > 0 ? src[c] : make_uint4(0, 0, 0, 0);
-                sts128(to + (uint32_t)((c >> 3) * kSlab) + swizzled(r & (kPromptTile - 1), c & 7), v.x, v.y, v.z, v.w);
+            const int c = lane % kLanes;
+#pragma unroll 8
+            for (int i = 0; i < kLanes; ++i) {
+                const int from = i * (32 / kLanes) + lane / kLanes;
+                const int64_t at = __shfl_sync(0xffffffffu, ok_row ? trow * a.q_stride + (int64_t)qh * D : -1, from);
+                const uint4 v = at >= 0 && nj > 0 ? *reinterpret_cast<const uint4*>(a.Q + at + c * 8) : make_uint4(0, 0, 0, 0);
+                sts128(to + (uint32_t)((c >> 3) * kSlab) + swizzled(sub * 32 + from, c & 7), v.x, v.y, v.z, v.w);
             }
             fence_async_proxy();
             __syncwarp();
@@ -541,31 +576,48 @@ __global__ void __launch_bounds__(Layout<D, NQ>::kThreads, 1) attn_prompt_kernel
         if (ok) {
             const int64_t orow = trow * a.q_heads + qh;
             const float inv = a.splits > 1 ? 1.f : (l == 0.f ? 0.f : __fdiv_rn(1.f, l));
+            const bool nothing = nj == 0 || l == 0.f;  // the accumulator holds zeros, or was never written
+            // The warp's 32 rows pass through its rows of the query tile (every product that read
+            // them is done), kOutBytes of each at a time, so that whole rows are written side by side.
+            constexpr int kOutBytes = D == 128 ? 256 : 128;
+            constexpr int kOutLanes = kOutBytes / 16;
+            const uint32_t mine = base + L::kQ + q * L::kOperand + (uint32_t)(sub * 32 * kOutBytes);
+            auto spot = [&](int row, int c) { return mine + (uint32_t)(row * kOutBytes + ((c ^ (row & 7)) << 4)); };
+            const bool parts = a.splits > 1;
+            const int per = kOutBytes / (parts ? 4 : 2);  // values of a row at a time
+#pragma unroll 1
+            for (int d0 = 0; d0 < D; d0 += per) {
+#pragma unroll 1
+                for (int c = 0; c < per; c += 16) {
+                    uint32_t o[16];
+                    if (nj > 0) tmem_ld16(o_at + d0 + c, o);
+                    float f[16];
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-                float o[32];
-                if (nj > 0) {
-                    tmem_ld32(o_at + 32 * c, o);
-                    landed(o);
+                    for (int i = 0; i < 16; ++i) f[i] = nothing ? 0.f : __uint_as_float(o[i]) * inv;
+                    if (parts) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            sts128(spot(lane, c / 4 + i), __float_as_uint(f[4 * i]), __float_as_uint(f[4 * i + 1]),
+                                   __float_as_uint(f[4 * i + 2]), __float_as_uint(f[4 * i + 3]));
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            sts128(spot(lane, c / 8 + i), pack_half2(f[8 * i], f[8 * i + 1]),
+                                   pack_half2(f[8 * i + 2], f[8 * i + 3]), pack_half2(f[8 * i + 4], f[8 * i + 5]),
+                                   pack_half2(f[8 * i + 6], f[8 * i + 7]));
+                    }
                 }
-                if (!ok_row) continue;
-                if (nj == 0 || l == 0.f) {  // saw nothing: the accumulator holds zeros, or was never written
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] = 0.f;
+                __syncwarp();
+#pragma unroll 4
+                for (int i = 0; i < kOutLanes; ++i) {
+                    const int row = i * (32 / kOutLanes) + lane / kOutLanes, c = lane % kOutLanes;
+                    char* to = reinterpret_cast<char*>(parts ? reinterpret_cast<uintptr_t>(a.part + (orow * a.splits + split) * D + d0)
+                                                             : reinterpret_cast<uintptr_t>(a.out + trow * a.out_stride + (int64_t)qh * D + d0));
+                    to = reinterpret_cast<char*>(__shfl_sync(0xffffffffu, ok_row ? reinterpret_cast<unsigned long long>(to) : 0ull, row));
+                    const uint4 v = lds128(spot(row, c));
+                    if (to) *reinterpret_cast<uint4*>(to + c * 16) = v;
                 }
-                if (a.splits > 1) {
-                    float4* dst = reinterpret_cast<float4*>(a.part + (orow * a.splits + split) * D + 32 * c);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-                } else {
-                    uint4* dst = reinterpret_cast<uint4*>(a.out + trow * a.out_stride + (int64_t)qh * D + 32 * c);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        dst[i] = make_uint4(pack_half2(o[8 * i] * inv, o[8 * i + 1] * inv),
-                                            pack_half2(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
-                                            pack_half2(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
-                                            pack_half2(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
-                }
+                __syncwarp();
             }
             if (ok_row) {
                 if (a.splits > 1)
