@@ -195,7 +195,13 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) attn_split_kernel(con
             for (int c = 0; c < 4; ++c) o[j][nt][c] = 0.f;
     float m[NT][2], l[NT][2];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) m[nt][0] = m[nt][1] = -INFINITY, l[nt][0] = l[nt][1] = 0.f;
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            // columns without a row: a reference that always holds
+            m[nt][b] = 8 * nt + 2 * t + b < rows ? -INFINITY : 0.f;
+            l[nt][b] = 0.f;
+        }
 
     for (int i = 0; i < mine; ++i) {
         const int base = i & ~15;
@@ -241,6 +247,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) attn_split_kernel(con
                     w[h][4 * c + 2] = v.z;
                     w[h][4 * c + 3] = v.w;
                 }
+            float odd[NT][4];  // a second accumulator: half the way through dependent products
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 sc[k][nt][0] = sc[k][nt][2] = q0[nt][0];
@@ -251,12 +258,17 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) attn_split_kernel(con
                 const uint32_t a0 = prmt(w[0][j], 0u, 0x4140u), a1 = prmt(w[1][j], 0u, 0x4140u);
                 const uint32_t a2 = prmt(w[0][j], 0u, 0x4342u), a3 = prmt(w[1][j], 0u, 0x4342u);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) mma_16816(sc[k][nt], a0, a1, a2, a3, qf[nt][j][0], qf[nt][j][1]);
+                for (int nt = 0; nt < NT; ++nt) {
+                    if (j == 1)
+                        mma_16816_z(odd[nt], a0, a1, a2, a3, qf[nt][j][0], qf[nt][j][1]);
+                    else
+                        mma_16816(j & 1 ? odd[nt] : sc[k][nt], a0, a1, a2, a3, qf[nt][j][0], qf[nt][j][1]);
+                }
             }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) sc[k][nt][c] = fmaf(sc[k][nt][c], ks, lv);
+                for (int c = 0; c < 4; ++c) sc[k][nt][c] = fmaf(sc[k][nt][c] + odd[nt][c], ks, lv);
         }
         const int p0 = stage_pos(i);
         if (!here[0] || !here[1] || p0 < all_lo || p0 + 2 * kKvBlock > all_hi) {
@@ -270,49 +282,65 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) attn_split_kernel(con
                         if (!here[k] || j >= hi[nt][b] || j < lo[nt][b]) sc[k][nt][c] = -INFINITY;
                     }
         }
-        float f[NT][2];
-        bool move = false;
-        uint32_t pf[2][NT][2];
+        // The reference m holds for most stages: FP16 takes probabilities up to 2^15 about it as
+        // exactly as up to 1, and a lane's sum says so.  Else the warp goes through the maximum.
+        float pr[2][NT][4];
+        float sum[2][NT][2];
+        auto probabilities = [&]() {
+            bool holds = true;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                float x = fmaxf(fmaxf(sc[0][nt][b], sc[0][nt][b + 2]), fmaxf(sc[1][nt][b], sc[1][nt][b + 2]));
-                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-                x = fmaxf(x, m[nt][b]);
-                const float mu = x == -INFINITY ? 0.f : x;  // a row that has seen nothing yet
-                f[nt][b] = ex2(m[nt][b] - mu);
-                move |= f[nt][b] != 1.f;
-                m[nt][b] = x;
-                float sum[2];
+                for (int b = 0; b < 2; ++b) {
+                    const float mu = m[nt][b] == -INFINITY ? 0.f : m[nt][b];  // a row that has seen nothing yet
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    sc[k][nt][b] = ex2(sc[k][nt][b] - mu);
-                    sc[k][nt][b + 2] = ex2(sc[k][nt][b + 2] - mu);
-                    sum[k] = sc[k][nt][b] + sc[k][nt][b + 2];
+                    for (int k = 0; k < 2; ++k) {
+                        pr[k][nt][b] = ex2(sc[k][nt][b] - mu);
+                        pr[k][nt][b + 2] = ex2(sc[k][nt][b + 2] - mu);
+                        sum[k][nt][b] = pr[k][nt][b] + pr[k][nt][b + 2];
+                    }
+                    holds = holds && m[nt][b] != -INFINITY && sum[0][nt][b] + sum[1][nt][b] <= 32768.f;
                 }
-                l[nt][b] *= f[nt][b];
-                // a block hidden from the row may have any scale
-                if (sum[0] != 0.f) l[nt][b] = fmaf(sum[0], ivs[0], l[nt][b]);
-                if (sum[1] != 0.f) l[nt][b] = fmaf(sum[1], ivs[1], l[nt][b]);
-            }
-        if (__any_sync(0xffffffffu, move)) {
+            return holds;
+        };
+        if (!__all_sync(0xffffffffu, probabilities())) {
+            float f[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    float x = fmaxf(fmaxf(sc[0][nt][b], sc[0][nt][b + 2]), fmaxf(sc[1][nt][b], sc[1][nt][b + 2]));
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+                    x = fmaxf(x, m[nt][b]);
+                    f[nt][b] = ex2(m[nt][b] - (x == -INFINITY ? 0.f : x));
+                    m[nt][b] = x;
+                    l[nt][b] *= f[nt][b];
+                }
 #pragma unroll
             for (int j = 0; j < MT; ++j)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int c = 0; c < 4; ++c) o[j][nt][c] *= f[nt][c & 1];
+            probabilities();
         }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int k = 0; k < 2; ++k)  // a block hidden from the row may have any scale
+                    if (sum[k][nt][b] != 0.f) l[nt][b] = fmaf(sum[k][nt][b], ivs[k], l[nt][b]);
         // P^T as the second product's right operand: columns are query rows, k the keys
+        uint32_t pf[2][NT][2];
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                pf[k][nt][0] = transpose8(pack_half2(sc[k][nt][0], sc[k][nt][1]));
-                pf[k][nt][1] = transpose8(pack_half2(sc[k][nt][2], sc[k][nt][3]));
+                pf[k][nt][0] = transpose8(pack_half2(pr[k][nt][0], pr[k][nt][1]));
+                pf[k][nt][1] = transpose8(pack_half2(pr[k][nt][2], pr[k][nt][3]));
             }
 
         // O^T += V^T P^T: lane (g, t) holds the codes of keys 2t, 2t + 1, 2t + 8, 2t + 9 at
