@@ -457,7 +457,8 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) attn_split_kernel(con
 // The chunks of a row (token, query head) joined: out = sum_c 2^(m_c - m) o_c / sum_c 2^(m_c - m) l_c.
 // WARPS warps a row take the chunks in turn, four loads in flight each, and are added in
 // their order.  One warp a row while there are few chunks; with more, a row's loads one behind the
-// other are what the call waits for (one warp a row of 114 chunks: 68 us; eight: 5 us).
+// other would be what the call waits for (131,071 keys in 114 chunks: 89 us with one warp a
+// row, 53 with eight).
 template <int D, int WARPS>
 __global__ void __launch_bounds__(256) attn_join_kernel(const AttnArgs a) {
     constexpr int kRowsPerCta = 8 / WARPS;
@@ -588,8 +589,12 @@ int attn_plan(const mnb_kv_cache* c, const mnb_kv_batch* b, int q_heads, int win
         if (chunk < 512) chunk = 512;
         if (p->split_rows && chunk > 8192) chunk = 8192;  // a single token's CTA walks its chunk alone
     } else {
-        // about two CTAs' worth of work for every CTA slot, whole rounds of the four warps
-        chunk = round_up((p->split_units * H * keys) / ((int64_t)sms * kCtasPerSm * 2) + 1, kWarps * 2 * kKvBlock);
+        // Whole rounds of the four warps.  One sequence: a CTA for every slot (131,071 keys: 49.5
+        // against 52.7 us with two).  Several, of lengths that are not known here: twice as many, so that
+        // the short ones' slots find work (3 uneven ones of up to 131,071 keys: 75 us with
+        // one, 59 with two, 67 with three; 64 of up to 8,192: 77, 66 and 64).
+        const int64_t ctas = (int64_t)sms * kCtasPerSm * (b->seqs == 1 ? 1 : 2);
+        chunk = round_up((p->split_units * H * keys + ctas - 1) / ctas, kWarps * 2 * kKvBlock);
     }
     if (keys / chunk >= 65535) chunk = round_up(keys / 65535 + 1, 128);
     p->splits = (int)((keys + chunk - 1) / chunk);

@@ -104,7 +104,7 @@ __device__ __forceinline__ void kv_sequence(const KvArgs& a, int s, int* len, in
     const int l = a.kv_len[s];
     *len = l < 0 ? 0 : (int)min((int64_t)l, a.max_tokens);
     *row0 = q0;
-    *n = q1 > q0 ? q1 - q0 : 0;
+    *n = q1 > q0 ? min(q1 - q0, a.tokens) : 0;
 }
 
 // Page of position `pos` (below max_tokens) of sequence s, or -1.
