@@ -66,16 +66,16 @@ int device_setup(int* sm_count, unsigned int** status = nullptr) {
         cudaGetLastError();
         return MNB_ERR_NO_DEVICE;
     }
-    int major = 0;
-    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess) {
-        cudaGetLastError();
-        return MNB_ERR_NO_DEVICE;
-    }
-    if (major != 10) return MNB_ERR_NO_DEVICE;  // built for sm_103a only
     unsigned long long ctx = 0;
     if (mnb::current_context_id(&ctx) != cudaSuccess) return MNB_ERR_CUDA;
     std::lock_guard<std::mutex> lk(g_init_mu);
     if (g_setup_ctx[dev] != ctx) {
+        int major = 0;
+        if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess) {
+            cudaGetLastError();
+            return MNB_ERR_NO_DEVICE;
+        }
+        if (major != 10) return MNB_ERR_NO_DEVICE;  // built for sm_103a only
         int sms = 0;
         void* st = nullptr;
         if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {

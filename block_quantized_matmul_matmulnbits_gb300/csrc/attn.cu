@@ -36,6 +36,7 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kCtasPerSm = 3;
+constexpr int kMaxCluster = 8;
 constexpr int kJoinOneWarp = 8;     // chunks that one warp joins
 constexpr int kSplitMostRows = 48;  // of a sequence
 __host__ __device__ constexpr int ring_stages(int D) { return D == 64 ? 4 : 2; }  // stages of 32 keys in a warp's ring
@@ -61,6 +62,20 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     uint32_t y;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
+}
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ float4 ld_peer_f32x4(uint32_t local_addr, uint32_t rank) {
+    uint32_t remote;
+    float4 v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local_addr), "r"(rank));
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(remote));
+    return v;
 }
 
 // Byte offset of 16-byte chunk c of row r in a block of 16 rows of D codes.
@@ -416,21 +431,18 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) attn_split_kernel(con
     // kPer threads a row, four values at a time
     constexpr int kPer = kWarps * 32 / kRows;
     const int row = threadIdx.x / kPer, part = threadIdx.x % kPer;
-    if (row >= rows) return;
-    const int r = tl.r0 + row, tok = r / a.group;
-    const int64_t trow = tl.row0 + tok;
-    if (trow < 0 || trow >= a.b.tokens) return;
-    const int qh = head * a.group + (r - tok * a.group);
     float mm = -INFINITY, ll = 0.f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, s_m[w][row]);
     const float mu = mm == -INFINITY ? 0.f : mm;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) ll += s_l[w][row] * ex2(s_m[w][row] - mu);
+    const int r = tl.r0 + row, tok = r / a.group;
+    const int64_t trow = tl.row0 + tok;
+    const bool ok = row < rows && trow >= 0 && trow < a.b.tokens;
+    const int qh = head * a.group + (r - tok * a.group);
     const int64_t orow = trow * a.q_heads + qh;
-    const float inv = a.splits > 1 ? 1.f : (ll == 0.f ? 0.f : __fdiv_rn(1.f, ll));
-#pragma unroll
-    for (int d = part * 4; d < D; d += kPer * 4) {
+    auto warps_sum = [&](int d) {
         float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
@@ -440,18 +452,81 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) attn_split_kernel(con
             sum.z += x.z;
             sum.w += x.w;
         }
-        if (a.splits > 1)
-            *reinterpret_cast<float4*>(a.part + (orow * a.splits + split) * D + d) = sum;
-        else
-            *reinterpret_cast<uint2*>(a.out + trow * a.out_stride + (int64_t)qh * D + d) =
-                make_uint2(pack_half2(sum.x * inv, sum.y * inv), pack_half2(sum.z * inv, sum.w * inv));
+        return sum;
+    };
+    auto put = [&](int d, float4 x, float inv) {
+        *reinterpret_cast<uint2*>(a.out + trow * a.out_stride + (int64_t)qh * D + d) =
+            make_uint2(pack_half2(x.x * inv, x.y * inv), pack_half2(x.z * inv, x.w * inv));
+    };
+    auto put_lse = [&](float ref, float den) {
+        if (a.lse) a.lse[orow] = den == 0.f ? -INFINITY : (ref + log2f(den)) * kLn2;
+    };
+    if (!a.cluster) {
+        if (!ok) return;
+        const float inv = a.splits > 1 ? 1.f : (ll == 0.f ? 0.f : __fdiv_rn(1.f, ll));
+#pragma unroll
+        for (int d = part * 4; d < D; d += kPer * 4) {
+            const float4 sum = warps_sum(d);
+            if (a.splits > 1)
+                *reinterpret_cast<float4*>(a.part + (orow * a.splits + split) * D + d) = sum;
+            else
+                put(d, sum, inv);
+        }
+        if (part == 0) {
+            if (a.splits > 1)
+                *reinterpret_cast<float2*>(a.ml + (orow * a.splits + split) * 2) = make_float2(mm, ll);
+            else
+                put_lse(mu, ll);
+        }
+        return;
     }
+    // Up to eight chunks are one cluster: the CTAs leave their sums in their own shared memory,
+    // and each joins every splits-th piece of four values, the chunks in their order.
+    float* c_o = s_o + kWarps * kRows * kPitch;  // [kRows][D]
+    float* c_m = c_o + kRows * D;                // [kRows][2]
+#pragma unroll
+    for (int d = part * 4; d < D; d += kPer * 4) *reinterpret_cast<float4*>(c_o + row * D + d) = warps_sum(d);
     if (part == 0) {
-        if (a.splits > 1)
-            *reinterpret_cast<float2*>(a.ml + (orow * a.splits + split) * 2) = make_float2(mm, ll);
-        else if (a.lse)
-            a.lse[orow] = ll == 0.f ? -INFINITY : (mu + log2f(ll)) * kLn2;
+        c_m[2 * row] = mm;
+        c_m[2 * row + 1] = ll;
     }
+    cluster_sync();
+    if (ok) {
+        const uint32_t m_at = smem_u32(c_m + 2 * row), o_at = smem_u32(c_o + row * D);
+        float cm[kMaxCluster], cl[kMaxCluster], ref = -INFINITY, den = 0.f;
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c) {
+            cm[c] = c < a.splits ? ld_peer_f32(m_at, (uint32_t)c) : -INFINITY;
+            cl[c] = c < a.splits ? ld_peer_f32(m_at + 4u, (uint32_t)c) : 0.f;
+        }
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c) ref = fmaxf(ref, cm[c]);
+        const float u = ref == -INFINITY ? 0.f : ref;
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c) {
+            cm[c] = ex2(cm[c] - u);
+            if (c < a.splits) den = fmaf(cl[c], cm[c], den);
+        }
+        const float inv = den == 0.f ? 0.f : __fdiv_rn(1.f, den);
+        for (int i = split; part + i * kPer < D / 4; i += a.splits) {
+            const int d = (part + i * kPer) * 4;
+            float4 x[kMaxCluster], sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int c = 0; c < kMaxCluster; ++c)
+                if (c < a.splits) x[c] = ld_peer_f32x4(o_at + (uint32_t)d * 4u, (uint32_t)c);
+#pragma unroll
+            for (int c = 0; c < kMaxCluster; ++c)
+                if (c < a.splits) {
+                    sum.x = fmaf(x[c].x, cm[c], sum.x);
+                    sum.y = fmaf(x[c].y, cm[c], sum.y);
+                    sum.z = fmaf(x[c].z, cm[c], sum.z);
+                    sum.w = fmaf(x[c].w, cm[c], sum.w);
+                }
+            put(d, sum, inv);
+        }
+        if (part == 0 && split == 0) put_lse(u, den);
+    }
+    cluster_sync();  // the sums stay until every CTA has read them
 }
 
 // The chunks of a row (token, query head) joined: out = sum_c 2^(m_c - m) o_c / sum_c 2^(m_c - m) l_c.
@@ -537,7 +612,8 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnArgs a) {
 }
 
 constexpr int split_smem(int D, int nt) {
-    const int ring = kWarps * ring_stages(D) * 4 * kKvBlock * D, join = kWarps * 8 * nt * (D + 4) * 4;
+    const int ring = kWarps * ring_stages(D) * 4 * kKvBlock * D;
+    const int join = (kWarps * 8 * nt * (D + 4) + 8 * nt * (D + 2)) * 4;  // the warps' sums, the cluster's
     return ring > join ? ring : join;
 }
 
@@ -547,6 +623,7 @@ struct AttnPlan {
     int64_t split_units, prompt_units;
     int split_single, prompt_single;  // every sequence of the kernel has at most one tile
     int chunk, splits;   // both kernels'
+    int cluster;         // split kernel alone: the CTAs of a row tile are a cluster and join themselves
     int64_t ws_bytes;
 };
 
@@ -600,7 +677,13 @@ int attn_plan(const mnb_kv_cache* c, const mnb_kv_batch* b, int q_heads, int win
     p->splits = (int)((keys + chunk - 1) / chunk);
     chunk = round_up(chunk, 128);
     p->chunk = (int)(chunk < INT32_MAX - 128 ? chunk : INT32_MAX - 127);
-    p->ws_bytes = p->splits > 1 ? (int64_t)b->tokens * q_heads * p->splits * (c->head_dim + 2) * 4 : 0;
+    // Few chunks that all run at once join through shared memory: no second kernel (577 keys of 3
+    // heads: 4.6 against 5.8 us).  Not with more CTAs than slots: a cluster waits for its
+    // longest chunk, and starts only when there is room for all (64 uneven sequences: 83
+    // against 66 us).
+    p->cluster = !prompt && p->splits > 1 && p->splits <= kMaxCluster &&
+                 p->split_units * H * p->splits <= (int64_t)sms * kCtasPerSm;
+    p->ws_bytes = p->splits > 1 && !p->cluster ? (int64_t)b->tokens * q_heads * p->splits * (c->head_dim + 2) * 4 : 0;
     return MNB_OK;
 }
 
@@ -618,10 +701,11 @@ cudaError_t launch(AttnArgs a, const AttnPlan& p, unsigned int* status, cudaStre
         a.single = p.split_single;
         a.most_rows = p.row_tiles ? p.split_rows : INT64_MAX;
         const dim3 grid((unsigned)p.split_units, (unsigned)a.b.kv_heads, (unsigned)p.splits), block(kWarps * 32);
-        e = p.split_rows == 8 ? launch_pdl(attn_split_kernel<D, 1>, grid, block, split_smem(D, 1), st, a)
-                              : launch_pdl(attn_split_kernel<D, 2>, grid, block, split_smem(D, 2), st, a);
+        const int cluster = p.cluster ? p.splits : 1;
+        e = p.split_rows == 8 ? launch_pdl(attn_split_kernel<D, 1>, grid, block, split_smem(D, 1), st, a, cluster)
+                              : launch_pdl(attn_split_kernel<D, 2>, grid, block, split_smem(D, 2), st, a, cluster);
     }
-    if (e != cudaSuccess || p.splits == 1) return e;
+    if (e != cudaSuccess || p.splits == 1 || p.cluster) return e;
     const int64_t rows = (int64_t)a.b.tokens * a.q_heads;
     if (p.splits <= kJoinOneWarp)
         return launch_pdl(attn_join_kernel<D, 1>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, st, a);
@@ -709,6 +793,7 @@ extern "C" int mnb_attn(const mnb_kv_cache* cache, const mnb_kv_batch* batch, co
     a.most_rows = INT64_MAX;
     a.chunk = p.chunk;
     a.splits = p.splits;
+    a.cluster = p.cluster;
     a.part = static_cast<float*>(ws);
     a.ml = a.part ? a.part + batch->tokens * (int64_t)q_heads * p.splits * cache->head_dim : nullptr;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

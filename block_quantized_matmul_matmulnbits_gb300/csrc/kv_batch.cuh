@@ -14,17 +14,22 @@ namespace mnb {
 // Launch that may start before the preceding kernel on the stream has finished; the
 // kernel waits for it (pdl_wait) before it reads or writes anything.
 template <typename A>
-inline cudaError_t launch_pdl(void (*kernel)(A), dim3 grid, dim3 block, size_t smem, cudaStream_t st, const A& args) {
+inline cudaError_t launch_pdl(void (*kernel)(A), dim3 grid, dim3 block, size_t smem, cudaStream_t st, const A& args,
+                              int cluster_z = 1) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = block;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = 1;
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = (unsigned)cluster_z;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster_z > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, args);
 }
 

@@ -292,9 +292,17 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LpArgs a) {
         look.add(q[1], v, a.c, c2);
         v += kStep;
     }
-    for (; v < f1; v += kThreads) {
-        const uint4 one[1] = {ld_stream(pieces + (int64_t)v * 8)};
-        look.add(one, v, a.c, c2);
+    {  // fewer than a group are left: all on their way before the first is looked at
+        uint4 rest[kUnroll - 1];
+#pragma unroll
+        for (int j = 0; j < kUnroll - 1; ++j)
+            if (v + j * kThreads < f1) rest[j] = ld_stream(pieces + (int64_t)(v + j * kThreads) * 8);
+#pragma unroll
+        for (int j = 0; j < kUnroll - 1; ++j)
+            if (v + j * kThreads < f1) {
+                const uint4 one[1] = {rest[j]};
+                look.add(one, v + j * kThreads, a.c, c2);
+            }
     }
 
     const float2 zs = unpair(look.z2), ys = unpair(look.y2);

@@ -145,12 +145,19 @@ def _ptr(x) -> Optional[int]:
     return x.data_ptr()
 
 
+_raw_stream = None  # () -> handle of torch's current stream
+
+
 def _current_stream() -> int:
-    import torch
-    try:  # the handle alone, without a Stream object around it (3 us less a call)
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
-    except AttributeError:
-        return torch.cuda.current_stream().cuda_stream
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        try:  # the handle alone, without a Stream object around it (3 us less a call)
+            of, device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+            _raw_stream = lambda: of(device())  # noqa: E731
+        except AttributeError:
+            _raw_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+    return _raw_stream()
 
 
 def _stream(stream) -> Optional[int]:
@@ -359,19 +366,27 @@ def _rows(x, heads: int, dim: int, tokens: int, what: str) -> int:
     return s[0] if tokens > 1 else max(s[0], heads * dim)
 
 
+def _kv_rows(cache, batch, K, V) -> int:
+    stride = _rows(K, cache.kv_heads, cache.head_dim, batch.tokens, "K")
+    if V.shape != K.shape or V.stride() != K.stride() or V.dtype is not K.dtype:
+        raise ValueError("V: shape, strides and type of K")
+    return stride
+
+
 def mnb_kv_write(cache: KVCache, batch: KVBatch, K, V, stream=None) -> None:
     """Quantise the batch's tokens (K, V fp16 [tokens, kv_heads, head_dim]) into the cache."""
-    stride = _rows(K, cache.kv_heads, cache.head_dim, batch.tokens, "K")
-    _want(_rows(V, cache.kv_heads, cache.head_dim, batch.tokens, "V") == stride, "K and V: one row stride")
-    _check(lib().mnb_kv_write(cache.ref, batch.ref, K.data_ptr(), V.data_ptr(), stride, _stream(stream)),
-           "mnb_kv_write")
+    rc = (_lib or lib()).mnb_kv_write(cache.ref, batch.ref, K.data_ptr(), V.data_ptr(), _kv_rows(cache, batch, K, V),
+                                      _current_stream() if stream is None else _stream(stream))
+    if rc:
+        raise MnbError(rc, "mnb_kv_write")
 
 
 def mnb_kv_read(cache: KVCache, batch: KVBatch, K, V, stream=None) -> None:
     """The batch's tokens from the cache into K, V (fp16 [tokens, kv_heads, head_dim])."""
-    stride = _rows(K, cache.kv_heads, cache.head_dim, batch.tokens, "K")
-    _want(_rows(V, cache.kv_heads, cache.head_dim, batch.tokens, "V") == stride, "K and V: one row stride")
-    _check(lib().mnb_kv_read(cache.ref, batch.ref, K.data_ptr(), V.data_ptr(), stride, _stream(stream)), "mnb_kv_read")
+    rc = (_lib or lib()).mnb_kv_read(cache.ref, batch.ref, K.data_ptr(), V.data_ptr(), _kv_rows(cache, batch, K, V),
+                                     _current_stream() if stream is None else _stream(stream))
+    if rc:
+        raise MnbError(rc, "mnb_kv_read")
 
 
 def mnb_attn_workspace(cache: KVCache, batch: KVBatch, q_heads: int, window: int = 0, sm_count: int = 0) -> int:
@@ -397,12 +412,16 @@ def mnb_attn(cache: KVCache, batch: KVBatch, Q, out, scale: Optional[float] = No
     q_heads = Q.shape[1] if Q.dim() == 3 else Q.shape[1] // dim
     stride = _rows(Q, q_heads, dim, batch.tokens, "Q")
     out_stride = _rows(out, q_heads, dim, batch.tokens, "out")
-    _want(lse is None or (lse.is_contiguous() and lse.element_size() == 4 and lse.numel() == batch.tokens * q_heads),
-          "lse: float32 [tokens, q_heads]")
-    _check(lib().mnb_attn(cache.ref, batch.ref, Q.data_ptr(), stride, q_heads, dim ** -0.5 if scale is None else scale,
-                          window, out.data_ptr(), out_stride, None if lse is None else lse.data_ptr(),
-                          None if ws is None else ws.data_ptr(), 0 if ws is None else ws.nbytes, _stream(stream)),
-           "mnb_attn")
+    if lse is not None and not (lse.is_contiguous() and lse.element_size() == 4 and
+                                lse.numel() == batch.tokens * q_heads):
+        raise ValueError("lse: float32 [tokens, q_heads]")
+    rc = (_lib or lib()).mnb_attn(cache.ref, batch.ref, Q.data_ptr(), stride, q_heads,
+                                  dim ** -0.5 if scale is None else scale, window, out.data_ptr(), out_stride,
+                                  None if lse is None else lse.data_ptr(), None if ws is None else ws.data_ptr(),
+                                  0 if ws is None else ws.nbytes,
+                                  _current_stream() if stream is None else _stream(stream))
+    if rc:
+        raise MnbError(rc, "mnb_attn")
 
 
 def mnb_logprobs(logits, target=None, logprob=None, entropy=None, top_ids=None, top_logprobs=None, scale: float = 1.0,
