@@ -12,8 +12,9 @@
 //    FP16 integers into shared memory (128-byte swizzle), keys and values in
 //    two stages each, and the tile's scales into a small ring.  Values stay [key][d]:
 //    the second product reads its right operand with d contiguous (MN-major).
-//  * warp 12 issues O_0 += P_0 V, the next S_0 = Q_0 K^T, then the same for row tile 1:
-//    a row tile's softmax runs under the other one's products.
+//  * warp 12 issues O_0 += P_0 V, the next S_0 = Q_0 K^T, then the same for row tile 1
+//    (O_1 before S_0 where P_1 is there by then): a row tile's softmax runs under the other
+//    one's products.
 //  * warps 0..3 and 4..7 own a row tile each, a thread a row: scores from tensor
 //    memory into registers (which the other warps give up), maximum, 2^x, and the
 //    probabilities back over the scores (two FP16 values a column) as the second
@@ -22,8 +23,15 @@
 //    denominator is binary32.  So a tile's probabilities are first made about the old
 //    reference, without a maximum; only where a row's sum passes 2^15 is the maximum
 //    taken, the accumulator rescaled and the tile's probabilities made again.
-// Both row tiles share the unpacked keys and values: unpacking costs an eighth of
-// what the products do.
+// Both row tiles share the unpacked keys and values.
+//
+// Bound by the tensor core, 4 d operations a query row and key: 1.09 PFLOP/s at a prompt of 4,096
+// tokens behind 4,096 and one of 395 behind 182, 32 query heads on 8 kv heads of 128 (382 us).
+// What stands between: a row tile's scores cannot be made before the product that reads the
+// probabilities over them has ended (some 300 cycles each time that nothing else is queued),
+// the softmax of 128 x 128 scores takes 1,200 cycles where the two row tiles share the
+// schedulers, as much as its products, and the tiles of a grid end unevenly (an eighth).
+// With the softmax or the unpacking left out the same call takes 305 or 339 us, with neither 272.
 //
 // Every wait is bounded (common.cuh): a role that gives up records a timeout and the others follow.
 #include "attn_common.cuh"
@@ -55,14 +63,12 @@ __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::aft
 
 // Shared-memory operand in 128-byte swizzled atoms of 8 rows x 128 bytes (1024 bytes apart).
 // K-major: the rows are M or N, K runs along the 128 bytes.  MN-major: the rows are K, N
-// runs along the 128 bytes and on to the next slab of 64 values, `lead` bytes away.
-__device__ __forceinline__ uint64_t operand(uint32_t saddr, uint32_t lead) {
-    uint64_t d = (uint64_t)((saddr & 0x3FFFFu) >> 4);
-    d |= (uint64_t)((lead ? lead >> 4 : 1u) & 0x3FFFu) << 16;
-    d |= (uint64_t)(1024 >> 4) << 32;
-    d |= (uint64_t)1 << 46;
-    d |= (uint64_t)2 << 61;
-    return d;
+// runs along the 128 bytes and on to the next slab of 64 values, `lead` bytes away.  The low
+// word of its descriptor; the high one is the same for all: stride 1024 bytes, version 1,
+// 128-byte swizzle.
+constexpr uint32_t kOperandHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t operand_low(uint32_t saddr, uint32_t lead) {
+    return ((saddr & 0x3FFFFu) >> 4) | ((lead ? lead >> 4 : 1u) & 0x3FFFu) << 16;
 }
 
 // kind::f16 instruction descriptor: FP32 accumulate, FP16 operands, M = 128.
@@ -70,29 +76,39 @@ __host__ __device__ constexpr uint32_t idesc(int n, bool n_major) {
     return (1u << 4) | (n_major ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 }
 
+// The warp that issues stays together and one lane is elected for each product: the operands'
+// addresses then stay in uniform registers.  With one lane on a path of its own they are
+// moved there for every product, and beside busy warps on the same scheduler a round
+// of 32 products took 3,300 cycles instead of 2,200 (2,050 are the tensor core's).
 __device__ __forceinline__ bool elected() {
     uint32_t r;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
     return r != 0;
 }
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t acc) {
     if (!elected()) return;
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+        "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(id), "r"(acc)
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(id), "r"(acc), "r"(kOperandHigh)
         : "memory");
 }
 
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t acc) {
     if (!elected()) return;
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\t"
+        "mov.b64 db, {%2, %5};\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(id), "r"(acc)
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(id), "r"(acc), "r"(kOperandHigh)
         : "memory");
 }
 
@@ -147,9 +163,8 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
         : "r"(taddr));
 }
 
-// Bounded wait for the phase of `parity` (as mbar_wait), with a plain test first: the wait
-// with a suspend time takes 95 cycles even where the phase is complete, the test 15.
-__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, unsigned int* status, bool abortable = true) {
+// Whether the phase of `parity` is complete.
+__device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity) {
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
@@ -158,7 +173,13 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, unsigned
         : "=r"(r)
         : "r"(bar), "r"(parity)
         : "memory");
-    return r != 0 || mbar_wait(bar, parity, status, abortable);
+    return r != 0;
+}
+
+// Bounded wait for it (as mbar_wait), with the plain test first: the wait with a suspend time
+// takes 95 cycles even where the phase is complete, the test 15.
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, unsigned int* status) {
+    return bar_test(bar, parity) || mbar_wait(bar, parity, status);
 }
 
 // Registers a thread of the calling warpgroup holds from here on.
@@ -310,40 +331,73 @@ __global__ void __launch_bounds__(Layout<D, NQ>::kThreads, 1) attn_prompt_kernel
         // ---------------------------------------------------------------- products
         give_registers<L::kOtherRegs>();
         if (warp == kMmaWarp) {
-            bool ok = __all_sync(0xffffffffu, bar_wait(q_full, 0, status));
-            auto scores = [&](int q, int j) {  // S_q = Q_q K^T of tile j
-                const uint32_t qs = base + L::kQ + q * L::kOperand, ks = base + L::kK + (j & 1) * L::kOperand;
+            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+            const uint32_t q0 = operand_low(base + L::kQ, 0), k0 = operand_low(base + L::kK, 0);
+            const uint32_t v0 = operand_low(base + L::kV, kSlab);
+            constexpr uint32_t kStep = L::kOperand >> 4;  // descriptors count in 16 bytes
+            auto phase = [](int j) { return (uint32_t)(j >> 1) & 1u; };
+            // every branch goes by a vote: then the compiler knows that the warp stays together
+            auto vote = [](bool v) { return __all_sync(0xffffffffu, v) != 0; };
+            auto scores = [&](auto qc, int j) {  // S_q = Q_q K^T of tile j
+                constexpr int q = decltype(qc)::value;
+                const uint32_t ks = k0 + (uint32_t)(j & 1) * kStep;
+                fence_after();
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
-                    const uint32_t off = (uint32_t)(k / 4 * kSlab + k % 4 * 32);
-                    mma_ss(tmem + q * 128, operand(qs + off, 0), operand(ks + off, 0), idesc(kTileKeys, false), k > 0);
+                    const uint32_t off = (uint32_t)((k / 4 * kSlab + k % 4 * 32) >> 4);
+                    mma_ss(tm + q * 128, q0 + q * kStep + off, ks + off, idesc(kTileKeys, false), k > 0);
                 }
                 commit(s_full(q));
                 if (q == NQ - 1) commit(k_empty(j & 1));
             };
-            auto phase = [](int j) { return (uint32_t)(j >> 1) & 1u; };
-            if (ok && nj > 0 && (ok = __all_sync(0xffffffffu, bar_wait(k_full(0), 0, status)))) {
+            auto add_up = [&](auto qc, int j) {  // O_q += P_q V
+                constexpr int q = decltype(qc)::value;
+                const uint32_t vs = v0 + (uint32_t)(j & 1) * kStep;
                 fence_after();
-                for (int q = 0; q < NQ; ++q) scores(q, 0);
-            }
-            for (int j = 0; __all_sync(0xffffffffu, ok && j < nj); ++j) {
-                for (int q = 0; q < NQ; ++q) {
-                    if (!(ok = __all_sync(0xffffffffu, bar_wait(p_full(q), (uint32_t)j & 1u, status)))) break;
-                    if (q == 0 && !(ok = __all_sync(0xffffffffu, bar_wait(v_full(j & 1), phase(j), status)))) break;
-                    fence_after();
-                    const uint32_t vs = base + L::kV + (j & 1) * L::kOperand;
 #pragma unroll
-                    for (int k = 0; k < kTileKeys / 16; ++k)  // O_q += P_q V
-                        mma_ts(tmem + NQ * 128 + q * D, tmem + q * 128 + 8 * k, operand(vs + k * 2048, kSlab),
-                               idesc(D, true), (j | k) != 0);
-                    commit(o_done(q));
-                    if (q == NQ - 1) commit(v_empty(j & 1));
-                    if (__all_sync(0xffffffffu, j + 1 == nj)) continue;
-                    if (q == 0 && !(ok = __all_sync(0xffffffffu, bar_wait(k_full((j + 1) & 1), phase(j + 1), status)))) break;
-                    // the probabilities lie over the scores: the product that reads them is done
-                    if (!(ok = __all_sync(0xffffffffu, bar_wait(o_done(q), (uint32_t)j & 1u, status)))) break;
-                    fence_after();
-                    scores(q, j + 1);
+                for (int k = 0; k < kTileKeys / 16; ++k)
+                    mma_ts(tm + NQ * 128 + q * D, tm + q * 128 + 8 * k, vs + (uint32_t)(k * 2048 >> 4), idesc(D, true),
+                           (j | k) != 0);
+                commit(o_done(q));
+                if (q == NQ - 1) commit(v_empty(j & 1));
+            };
+            using First = std::integral_constant<int, 0>;
+            using Last = std::integral_constant<int, NQ - 1>;
+            bool ok = vote(nj == 0 || bar_wait(q_full, 0, status));
+            if (vote(ok && nj > 0)) {
+                ok = vote(bar_wait(k_full(0), 0, status));
+                if (ok) {
+                    scores(First{}, 0);
+                    if (NQ == 2) scores(Last{}, 0);
+                }
+            }
+            for (int j = 0; vote(ok && j < nj); ++j) {
+                const uint32_t odd = (uint32_t)j & 1u;
+                ok = vote(bar_wait(v_full(j & 1), phase(j), status)) && vote(bar_wait(p_full(0), odd, status));
+                if (!ok) break;
+                add_up(First{}, j);
+                const bool more = !vote(j + 1 == nj);
+                // The other row tile's probabilities may be there already: then its product runs
+                // while this one's end is waited for.
+                const bool early = NQ == 2 && vote(bar_test(p_full(NQ - 1), odd));
+                if (early) add_up(Last{}, j);
+                if (more) {
+                    // the probabilities lie over the scores: the product that reads them has to be done
+                    ok = vote(bar_wait(k_full((j + 1) & 1), phase(j + 1), status)) && vote(bar_wait(o_done(0), odd, status));
+                    if (!ok) break;
+                    scores(First{}, j + 1);
+                }
+                if (NQ == 2) {
+                    if (!early) {
+                        ok = vote(bar_wait(p_full(NQ - 1), odd, status));
+                        if (!ok) break;
+                        add_up(Last{}, j);
+                    }
+                    if (more) {
+                        ok = vote(bar_wait(o_done(NQ - 1), odd, status));
+                        if (!ok) break;
+                        scores(Last{}, j + 1);
+                    }
                 }
             }
             commit(drain);  // tensor memory is freed only after every issued product has finished
