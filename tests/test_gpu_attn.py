@@ -207,3 +207,42 @@ def test_offsets_past_32_bits():
     mnb.mnb_attn(cache, batch, qd, out, ws=mnb.attn_workspace(cache, batch, 8))
     torch.cuda.synchronize()
     assert np.all(np.abs(out.float().cpu().numpy() - want) <= tol)
+
+
+@pytest.mark.parametrize("dim,window", [(64, 0), (128, 0), (128, 50)])
+@pytest.mark.parametrize("max_len", [None, 60000])
+def test_prompts_among_single_tokens(dim, window, max_len):
+    # rows of both kernels in one call: a prompt, one over and one at the split kernel's 48 rows, single
+    # tokens, an idle slot; a large length bound cuts the keys into many chunks
+    c = Case(40, [310, 80, 97, 40, 0, 700], [170, 13, 12, 1, 0, 1], 2, dim, 32)
+    check(c, 8, window, max_len=max_len)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("news", [[1], [9], [200]])
+def test_scores_that_rise_along_the_keys(dim, news):
+    # the reference of the sum has to move again and again, in the end by more than binary32's range of 2^x
+    c = Case(41, [700], news, 1, dim, 16)
+    r = np.random.default_rng(41)
+    grow = np.linspace(0.0, 0.2, c.table.shape[1])
+    for b, p in enumerate(c.table[0]):
+        if p >= 0:
+            c.codes[0][p] = r.integers(200, 256, c.codes[0][p].shape, dtype=np.uint8)
+            c.scales[0][p] = grow[b]
+    q = np.abs(queries(c, 2))
+    want, want_lse, tol = attn_ref(c, q, 0.3)
+    out, lse = run(c, q, 0.3)
+    assert np.all(np.abs(out - want) <= tol)
+    assert np.all(np.abs(lse - want_lse) <= 2e-4 + 1e-6 * np.abs(want_lse))
+
+
+@pytest.mark.parametrize("news", [[4], [60]])
+def test_a_bad_query_row_stays_alone(news):
+    c = Case(42, [150], news, 1, 64, 16)
+    q = queries(c, 3)
+    want, _, tol = attn_ref(c, q, 0.125)
+    q[1, 0, 5], q[2, 2, 7] = np.nan, np.inf
+    out, _ = run(c, q, 0.125)
+    good = np.ones(q.shape[:2], bool)
+    good[1, 0] = good[2, 2] = False
+    assert np.all((np.abs(out - want) <= tol)[good]) and np.all(np.isnan(out[1, 0]))
