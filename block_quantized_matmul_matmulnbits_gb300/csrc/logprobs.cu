@@ -14,10 +14,10 @@
 // so a row gets no more CTAs than the GPU needs to be full.
 //
 // The k most likely: the k-th largest of the threads' own maxima is a value
-// that at least k of the CTA's logits reach.  Each thread remembers which
-// piece held its maximum and the largest of its other pieces, so the few threads whose
-// maximum reaches that value look at one piece again, at all of theirs only
-// where a second one reaches it too; what reaches it is collected, and ranks among
+// that at least k of the CTA's logits reach.  Each thread remembers which two
+// groups of pieces held its largest logits and the largest of the others, so few groups
+// have to be looked at again, a piece a thread, and all of a thread's only where a third
+// one reaches that value too; what reaches it is collected, and ranks among
 // the collected are counted directly.  FP16 logits tie often; the keys order
 // equal ones by rising id.  Where more are collected than the list holds (long
 // runs of equal logits), the CTA takes its maximum k times instead.  The cluster's
@@ -112,7 +112,8 @@ struct __align__(16) LpShared {
     unsigned long long best[kWarpCount];
     Stat warp_stat[kWarpCount];
     Stat stats[kMaxCluster];               // first CTA: every CTA's sums
-    int count;
+    int work[2 * kThreads];                // first pieces of groups to look at again
+    int count, works;
 };
 
 // The address that `addr` of this CTA has in the cluster's first CTA.
@@ -169,8 +170,8 @@ __device__ __forceinline__ uint4 ld_stream(const void* p) {  // once, from memor
 struct Look {
     float r = -INFINITY;                // reference
     uint64_t z2 = 0, y2 = 0, ref2 = 0;  // both sums in two halves; (-r, -r), 0 while r is -infinity
-    float best = -INFINITY, second = -INFINITY;  // largest logit; largest outside its group
-    int at = -1;                        // first piece of the largest logit's group
+    float best = -INFINITY, second = -INFINITY, third = -INFINITY;  // the three largest of the groups' maxima
+    int at = -1, second_at = -1;        // first pieces of the first two's groups
 
     template <int N>
     __device__ __forceinline__ void add(const uint4 (&q)[N], int v, float c, uint64_t c2) {
@@ -178,6 +179,8 @@ struct Look {
 #pragma unroll
         for (int i = 1; i < N; ++i) m2 = __hmax2(m2, max_of(q[i]));
         const float x = __half2float(__hmax(__low2half(m2), __high2half(m2)));
+        third = fmaxf(third, fminf(second, x));
+        second_at = x > best ? at : (x > second ? v : second_at);
         second = fmaxf(second, fminf(best, x));
         at = x > best ? v : at;
         best = fmaxf(best, x);
@@ -225,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LpArgs a) {
     const int rank = (int)(blockIdx.x % a.cluster);
     const int64_t row = blockIdx.x / a.cluster;
     if (a.cluster > 1) cluster_arrive();  // waited for before the first CTA's memory is written
-    if (tid == 0) sh.count = 0;
+    if (tid == 0) sh.count = sh.works = 0;
     pdl_wait();
     pdl_launch_dependents();
     const __half* src = a.logits + row * a.row_stride;
@@ -334,18 +337,18 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LpArgs a) {
             });
         };
         const bool reach = any && best >= tau;
-        const bool all = reach && (look.at < 0 || order_of(look.second) >= tau);
-        if (reach && !all) {  // the group, or the single piece at the slice's end; loads first
-            const bool group = look.at >= f0 && look.at + (kUnroll - 1) * kThreads < f1;
-            uint4 x[kUnroll];
-            x[0] = piece(look.at);
-#pragma unroll
-            for (int j = 1; j < kUnroll; ++j)
-                if (group) x[j] = ld_stream(pieces + (int64_t)(look.at + j * kThreads) * 8);
-            collect(x[0], look.at);
-            if (group)
-#pragma unroll
-                for (int j = 1; j < kUnroll; ++j) collect(x[j], look.at + j * kThreads);
+        const bool two = order_of(look.second) >= tau;
+        const bool all = reach && (look.at < 0 || order_of(look.third) >= tau || (two && look.second_at < 0));
+        if (reach && !all) {
+            const int i = atomicAdd(&sh.works, two ? 2 : 1);
+            sh.work[i] = look.at;
+            if (two) sh.work[i + 1] = look.second_at;
+        }
+        __syncthreads();
+        // a piece a thread; an entry is a whole group, or the single piece at an end of the slice
+        for (int i = tid; i < sh.works * kUnroll; i += kThreads) {
+            const int from = sh.work[i / kUnroll], v = from + i % kUnroll * kThreads;
+            if (v == from || (from >= f0 && from + (kUnroll - 1) * kThreads < f1)) collect(piece(v), v);
         }
         if (all && ragged) collect(piece(edge), edge);
         // a thread's whole pieces are looked at by its warp, two a lane at a time
