@@ -64,10 +64,11 @@ struct Tile {
 
 __device__ __forceinline__ bool find_tile(const AttnArgs& a, int64_t u, int row_shift, Tile& t) {
     int64_t first = u;
-    t.s = a.single ? (int)u : kv_find_seq(a.b, u, {a.group, row_shift, 1}, &first);
-    int row0;
-    kv_sequence(a.b, t.s, &t.len, &row0, &t.n);
-    t.row0 = row0;
+    const KvSeq q = a.single ? kv_sequence(a.b, (int)u) : kv_find_seq(a.b, u, {a.group, row_shift, 1}, &first);
+    t.s = q.s;
+    t.len = q.len;
+    t.n = q.n;
+    t.row0 = q.row0;
     const int64_t r0 = (u - first) << row_shift;
     if (r0 < 0 || r0 >= (int64_t)t.n * a.group) return false;
     t.r0 = (int)r0;

@@ -80,36 +80,50 @@ __host__ __device__ inline int64_t kv_items(int64_t tokens, int seqs, KvSplit k)
     return ((tokens * k.mul) >> k.shift) + (int64_t)k.extra * seqs;
 }
 
-// The sequence that owns item `u`, and its first item: a 32-way search by the
-// whole warp (two rounds of loads up to 1024 sequences).
-__device__ __forceinline__ int kv_find_seq(const KvArgs& a, int64_t u, KvSplit k, int64_t* first) {
+// One sequence of the batch: its length, and its tokens of this call: rows row0 .. row0 + n - 1
+// are the positions len - n .. len - 1 (the first ones may lie before 0).
+struct KvSeq {
+    int s, len, row0, n;
+};
+
+__device__ __forceinline__ KvSeq kv_sequence(const KvArgs& a, int s, int q0, int q1, int l) {
+    return {s, l < 0 ? 0 : (int)min((int64_t)l, a.max_tokens), q0, q1 > q0 ? min(q1 - q0, a.tokens) : 0};
+}
+
+__device__ __forceinline__ KvSeq kv_sequence(const KvArgs& a, int s) {
+    return kv_sequence(a, s, a.q_start[s], a.q_start[s + 1], a.kv_len[s]);
+}
+
+// The sequence that owns item `u`, and its first item: a 32-way search by the whole warp (two
+// rounds of loads up to 1024 sequences).  The last round's lanes hold single sequences, and
+// load all there is to know of them at once: loads one behind the other are what a
+// small call consists of.
+__device__ __forceinline__ KvSeq kv_find_seq(const KvArgs& a, int64_t u, KvSplit k, int64_t* first) {
     const int lane = threadIdx.x & 31;
     int lo = 0, hi = a.seqs;
-    int64_t at_lo = 0;
-    while (hi - lo > 1) {
+    for (;;) {
         const int step = (hi - lo + 31) >> 5;
         const int s = lo + lane * step;
         int64_t at = INT64_MAX;
-        if (s < hi) at = kv_items(a.q_start[s], s, k);
+        int q0 = 0, q1 = 0, l = 0;
+        if (s < hi) {
+            q0 = a.q_start[s];
+            if (step == 1) {
+                q1 = a.q_start[s + 1];
+                l = a.kv_len[s];
+            }
+            at = kv_items(q0, s, k);
+        }
         const unsigned le = __ballot_sync(0xffffffffu, at <= u);
         const int last = le ? 31 - __clz(le) : 0;  // the first item of `lo` is never past u
-        at_lo = __shfl_sync(0xffffffffu, at, last);
+        if (step == 1) {
+            *first = __shfl_sync(0xffffffffu, at, last);
+            return kv_sequence(a, lo + last, __shfl_sync(0xffffffffu, q0, last), __shfl_sync(0xffffffffu, q1, last),
+                               __shfl_sync(0xffffffffu, l, last));
+        }
         lo += last * step;
         hi = min(hi, lo + step);
     }
-    if (a.seqs == 1) at_lo = kv_items(a.q_start[0], 0, k);
-    *first = at_lo;
-    return lo;
-}
-
-// Length of sequence s, and its tokens of this call: rows row0 .. row0 + n - 1 are the
-// positions len - n .. len - 1 (the first ones may lie before 0).
-__device__ __forceinline__ void kv_sequence(const KvArgs& a, int s, int* len, int* row0, int* n) {
-    const int q0 = a.q_start[s], q1 = a.q_start[s + 1];
-    const int l = a.kv_len[s];
-    *len = l < 0 ? 0 : (int)min((int64_t)l, a.max_tokens);
-    *row0 = q0;
-    *n = q1 > q0 ? min(q1 - q0, a.tokens) : 0;
 }
 
 // Page of position `pos` (below max_tokens) of sequence s, or -1.

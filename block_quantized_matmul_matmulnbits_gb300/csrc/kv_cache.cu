@@ -47,23 +47,22 @@ struct KvUnit {
 // False: nothing to do (the whole warp together).
 __device__ __forceinline__ bool kv_unit(const KvIoArgs& p, KvUnit& u) {
     const KvArgs& a = p.b;
-    const int64_t w = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    const int combos = 2 * a.kv_heads;
-    const int64_t item = w / combos;
+    const unsigned w = blockIdx.x * kWarps + (threadIdx.x >> 5);  // below 2^32: kv_io
+    const unsigned combos = 2u * (unsigned)a.kv_heads;
+    const unsigned item = w / combos;
     if (item >= p.items) return false;
     const int c = (int)(w - item * combos);
     u.which = c >= a.kv_heads;
     u.head = u.which ? c - a.kv_heads : c;
     int64_t first_item;
-    const int s = kv_find_seq(a, item, kBlocks, &first_item);
-    int row0, n;
-    kv_sequence(a, s, &u.len, &row0, &n);
-    u.first = u.len - n;
-    u.row0 = row0;
-    const int64_t lo = ((int64_t)((u.first > 0 ? u.first : 0) >> 4) + (item - first_item)) * kKvBlock;
-    if (n == 0 || lo < 0 || lo >= u.len) return false;
+    const KvSeq q = kv_find_seq(a, item, kBlocks, &first_item);
+    u.len = q.len;
+    u.first = q.len - q.n;
+    u.row0 = q.row0;
+    const int64_t lo = ((int64_t)((u.first > 0 ? u.first : 0) >> 4) + ((int64_t)item - first_item)) * kKvBlock;
+    if (q.n == 0 || lo < 0 || lo >= u.len) return false;
     u.lo = (int)lo;
-    const int page = kv_page(a, s, u.lo);
+    const int page = kv_page(a, q.s, u.lo);
     if (page < 0) return false;
     const int mask = (1 << a.page_shift) - 1;
     u.slot = (((int64_t)page * a.kv_heads + u.head) << a.page_shift) + (u.lo & mask);
@@ -214,7 +213,7 @@ int kv_io(const mnb_kv_cache* c, const mnb_kv_batch* b, void* K, void* V, int64_
     p.k = static_cast<__half*>(K);
     p.v = static_cast<__half*>(V);
     const int64_t blocks = (p.items * 2 * c->kv_heads + kWarps - 1) / kWarps;
-    if (blocks > INT32_MAX) return MNB_ERR_UNSUPPORTED;
+    if (blocks > INT32_MAX / kWarps) return MNB_ERR_UNSUPPORTED;  // 4 TB of values
     int sms;
     unsigned int* status;
     rc = device_ready(&sms, &status);
