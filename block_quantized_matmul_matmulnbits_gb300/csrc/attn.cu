@@ -39,6 +39,7 @@ constexpr int kCtasPerSm = 3;
 constexpr int kMaxCluster = 8;
 constexpr int kJoinOneWarp = 8;     // chunks that one warp joins
 constexpr int kSplitMostRows = 48;  // of a sequence
+constexpr int kShortChunk = 512;    // keys
 __host__ __device__ constexpr int ring_stages(int D) { return D == 64 ? 4 : 2; }  // stages of 32 keys in a warp's ring
 constexpr float kCodeUnit = 5.9604644775390625e-8f;           // 2^-24, FP16's smallest subnormal
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
@@ -669,9 +670,15 @@ int attn_plan(const mnb_kv_cache* c, const mnb_kv_batch* b, int q_heads, int win
         // Whole rounds of the four warps.  One sequence: a CTA for every slot (131,071 keys: 49.5
         // against 52.7 us with two).  Several, of lengths that are not known here: twice as many, so that
         // the short ones' slots find work (3 uneven ones of up to 131,071 keys: 75 us with
-        // one, 59 with two, 67 with three; 64 of up to 8,192: 77, 66 and 64).
-        const int64_t ctas = (int64_t)sms * kCtasPerSm * (b->seqs == 1 ? 1 : 2);
-        chunk = round_up((p->split_units * H * keys + ctas - 1) / ctas, kWarps * 2 * kKvBlock);
+        // one, 59 with two, 67 with three; 64 of up to 8,192: 77, 66 and 64).  But no chunk
+        // under 512 keys for that, four stages a warp: what a chunk costs by itself is more
+        // then (8 kv heads, 8 sequences of up to 2,000 keys: 9.0 against 10.0 us; 5 tokens of 2 of up to
+        // 8,000, 2 kv heads of 64: 9.0 against 13.4), and from there on it is less (32 of 8,000,
+        // 8 heads: 35 against 48).
+        const int64_t slots = (int64_t)sms * kCtasPerSm, all = p->split_units * H * keys;
+        chunk = (all + slots - 1) / slots;
+        if (b->seqs > 1 && chunk > kShortChunk) chunk = max((all + 2 * slots - 1) / (2 * slots), (int64_t)kShortChunk);
+        chunk = round_up(chunk, kWarps * 2 * kKvBlock);
     }
     if (keys / chunk >= 65535) chunk = round_up(keys / 65535 + 1, 128);
     p->splits = (int)((keys + chunk - 1) / chunk);
