@@ -11,11 +11,13 @@
 // The alternative split, one warp a token, needs the block's scale agreed
 // between 16 warps.
 //
-// Reading 8 kv heads of 128 for 12 sequences of up to 16,384 tokens (356 MB) takes 55.8 us,
+// Reading 8 kv heads of 128 for 12 sequences of up to 16,384 tokens (356 MB) takes 55.5 us,
 // 6.4 TB/s.  Writing and then reading four prompts' 8,146 tokens (100 MB, less than the L2
-// cache) takes 21.0 us, 4.8 TB/s: each call loads all there is at once and then
+// cache) takes 19.1 us, 5.2 TB/s: each call loads all there is at once and then
 // stores it, and the look for the sequence, its page and its rows comes before.  CTAs of four
-// warps: a step of 128 sequences takes 9.2 us, with eight 10.5, with one 10.5.
+// warps: writing and reading a step of 128 sequences took 9.2 us, with eight 10.5, with one
+// 10.5 (now 8.2: four codes in 12 instructions, a step and the prompts above had been held
+// up by 16 a value).
 //
 // The magnitude is taken on the FP16 bit patterns without their sign, which
 // order as unsigned integers with NaN above infinity above every finite value,
@@ -75,6 +77,52 @@ __device__ __forceinline__ bool kv_unit(const KvIoArgs& p, KvUnit& u) {
     return true;
 }
 
+// Two binary32 values in one 64-bit register: one instruction for both.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ uint2 halves(uint64_t v) {
+    uint2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=r"(r.x), "=r"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// Codes of four new values.  |x * inv| stays below 127.5 (inv is 1 / s to a rounding, and 127 s
+// is no less than any of them to another), so nothing has to be clamped; adding 1.5 * 2^23 + 128
+// rounds to the nearest integer, ties to even, and leaves the code in the low byte.  The products
+// are scalar ones: a packed product and sum become one operation, rounded once, and ties differ.
+__device__ __forceinline__ uint32_t new_codes(uint32_t w0, uint32_t w1, float inv) {
+    const uint64_t magic = pair(12583040.f, 12583040.f);
+    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&w0));
+    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&w1));
+    const uint2 p = halves(add2(pair(__fmul_rn(a.x, inv), __fmul_rn(a.y, inv)), magic));
+    const uint2 q = halves(add2(pair(__fmul_rn(b.x, inv), __fmul_rn(b.y, inv)), magic));
+    return prmt(prmt(p.x, p.y, 0x0040u), prmt(q.x, q.y, 0x0040u), 0x5410u);
+}
+
+// (q - 128) * s of two codes (bytes `sel` of w) as FP16: the code joins the bits of 2^23, which
+// is taken off again with the 128.
+template <uint32_t LO, uint32_t HI>
+__device__ __forceinline__ uint32_t values_half2(uint32_t w, uint64_t s2) {
+    const uint64_t t = pair(__uint_as_float(prmt(w, 0x4B000000u, LO)), __uint_as_float(prmt(w, 0x4B000000u, HI)));
+    const uint2 v = halves(mul2(add2(t, pair(-8388736.f, -8388736.f)), s2));
+    const __half2 h = __floats2half2_rn(__uint_as_float(v.x), __uint_as_float(v.y));
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// A code of an older token under a scale that grew by 1 / ratio.
 __device__ __forceinline__ int quantize_code(float x, float inv) {
     const int c = __float2int_rn(__fmul_rn(x, inv));
     return 128 + (c > 127 ? 127 : (c < -127 ? -127 : c));
@@ -131,14 +179,8 @@ __global__ void __launch_bounds__(kWarps * 32) kv_write_kernel(const KvIoArgs p)
         uint32_t out[2] = {0x80808080u, 0x80808080u};
         if ((fresh >> i) & 1u) {
             if (good) {
-                const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&w[2 * j]));
-                    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&w[2 * j + 1]));
-                    out[j] = (uint32_t)quantize_code(a.x, inv) | ((uint32_t)quantize_code(a.y, inv) << 8) |
-                             ((uint32_t)quantize_code(b.x, inv) << 16) | ((uint32_t)quantize_code(b.y, inv) << 24);
-                }
+                out[0] = new_codes(v[i].x, v[i].y, inv);
+                out[1] = new_codes(v[i].z, v[i].w, inv);
             }
             *dst = make_uint2(out[0], out[1]);
         } else if (again && ((kept >> i) & 1u)) {
@@ -178,21 +220,15 @@ __global__ void __launch_bounds__(kWarps * 32) kv_read_kernel(const KvIoArgs p) 
     for (int i = 0; i < NI; ++i)  // the block's 16 rows are always inside its page
         q[i] = *reinterpret_cast<const uint2*>(codes + (int64_t)(i * RPI + r0) * D);
     const float s = (u.which ? p.v_scales : p.k_scales)[u.slot >> 4];
+    const uint64_t s2 = pair(s, s);
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
         const int pos = u.lo + i * RPI + r0;
         const int64_t row = u.row0 + (pos - u.first);
         if (pos < u.first || pos >= u.len || row < 0 || row >= p.b.tokens) continue;
-        const uint32_t w[2] = {q[i].x, q[i].y};
-        uint32_t o[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint32_t h = w[j >> 1] >> ((j & 1) * 16);
-            const __half2 t = __halves2half2(__float2half_rn(__fmul_rn((float)((int)(h & 0xFFu) - 128), s)),
-                                             __float2half_rn(__fmul_rn((float)((int)((h >> 8) & 0xFFu) - 128), s)));
-            o[j] = *reinterpret_cast<const uint32_t*>(&t);
-        }
-        *reinterpret_cast<uint4*>(x + row * p.row_stride) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4*>(x + row * p.row_stride) =
+            make_uint4(values_half2<0x7440u, 0x7441u>(q[i].x, s2), values_half2<0x7442u, 0x7443u>(q[i].x, s2),
+                       values_half2<0x7440u, 0x7441u>(q[i].y, s2), values_half2<0x7442u, 0x7443u>(q[i].y, s2));
     }
 }
 
