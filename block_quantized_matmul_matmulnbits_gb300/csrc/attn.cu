@@ -25,9 +25,17 @@
 // `chunk` keys.  Each warp walks its own stages of 32 keys (8 KB of codes at head_dim
 // 128) through a ring of cp.async copies of its own, so nothing in the loop
 // waits on another warp; the warps' results are joined once at the end, and the
-// chunks' by attn_join_kernel where a row tile has more than one.  The codes are
+// chunks' by attn_join_kernel where a row tile has more than one, or in the cluster that
+// the chunks of a tile form where they are few.  The codes are
 // stored with their 16-byte chunks permuted by the row, so that both products'
 // operand reads are free of bank conflicts.
+//
+// Bound by memory, head_dim + 4 / 16 bytes a key, twice: one sequence of 131,071 keys and 8 kv heads
+// of 128 takes 49.5 us, 5.5 TB/s.  64 uneven sequences of up to 8,192 take 65 us, 5.0 TB/s: at
+// their end few CTAs have work left.  (Chunks of equal work over all sequences ended
+// together and took 67: each CTA has more to look up and to join.)  Short calls wait for
+// their loads one behind the other (lengths, page, scales and codes, then the join): 577 keys
+// of 3 heads of 64 take 4.6 us behind another call.
 #include "attn_common.cuh"
 
 namespace mnb {

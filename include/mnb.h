@@ -397,7 +397,9 @@ typedef struct {
  * holds older tokens of the sequence (positions before the call's); codes are
  * 128 + clamp(rint(x * (1 / scale)), -127, 127) (ties to even), and where the
  * scale grew the older tokens' codes become 128 + rint((q - 128) * (s_old /
- * scale)).  A scale of zero gives codes 128.  A block that receives a
+ * scale)): a token that arrives alone is rounded again, by half a step at
+ * most, each time that one of the 15 after it raises the block's scale.  A
+ * scale of zero gives codes 128.  A block that receives a
  * non-finite value gets a non-finite scale and codes 128: its 16 tokens read
  * as NaN.  Codes of positions past the sequence's end are left as they are.
  * Writing the same tokens at the same positions again changes nothing.  Two
