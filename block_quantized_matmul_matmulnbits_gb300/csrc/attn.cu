@@ -48,6 +48,7 @@ constexpr int kMaxCluster = 8;
 constexpr int kJoinOneWarp = 8;     // chunks that one warp joins
 constexpr int kSplitMostRows = 48;  // of a sequence
 constexpr int kShortChunk = 512;    // keys
+constexpr int kLongWalk = 1536;     // keys
 __host__ __device__ constexpr int ring_stages(int D) { return D == 64 ? 4 : 2; }  // stages of 32 keys in a warp's ring
 constexpr float kCodeUnit = 5.9604644775390625e-8f;           // 2^-24, FP16's smallest subnormal
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
@@ -107,12 +108,13 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) attn_split_kernel(con
     pdl_wait();
     pdl_launch_dependents();
 
+    const int unit = (int)(blockIdx.x / (unsigned)a.b.kv_heads), head = (int)(blockIdx.x % (unsigned)a.b.kv_heads);
+    const int split = a.by_length ? a.splits - 1 - (int)blockIdx.z : (int)blockIdx.z;
     Tile tl;
-    if (!find_tile(a, blockIdx.x, NT == 1 ? 3 : 4, tl)) return;
+    if (!find_tile(a, a.by_length ? kv_by_length(a.b, unit) : unit, NT == 1 ? 3 : 4, tl)) return;
     if ((int64_t)tl.n * a.group > a.most_rows) return;  // the prompt kernel's
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t = lane & 3;
-    const int head = blockIdx.y, split = blockIdx.z;
     const int rows = (int)min((int64_t)tl.n * a.group - tl.r0, (int64_t)kRows);
     const int first = tl.len - tl.n;  // position of the call's first token
 
@@ -632,6 +634,7 @@ struct AttnPlan {
     int64_t split_units, prompt_units;
     int split_single, prompt_single;  // every sequence of the kernel has at most one tile
     int chunk, splits;   // both kernels'
+    int by_length;       // split kernel alone: long sequences first
     int cluster;         // split kernel alone: the CTAs of a row tile are a cluster and join themselves
     int64_t ws_bytes;
 };
@@ -662,7 +665,7 @@ int attn_plan(const mnb_kv_cache* c, const mnb_kv_batch* b, int q_heads, int win
         p->prompt_units = p->prompt_single ? b->seqs : kv_items(b->tokens, b->seqs, {G, p->row_tiles == 1 ? 7 : 8, 1});
         span = p->row_tiles * kPromptTile / G + 1;
     }
-    if (p->prompt_units * H > INT32_MAX || p->split_units > INT32_MAX) return MNB_ERR_UNSUPPORTED;
+    if (p->prompt_units * H > INT32_MAX || p->split_units * H > INT32_MAX) return MNB_ERR_UNSUPPORTED;
     int64_t keys = b->max_len;
     // with a window a tile sees its tokens' windows, from a block's start
     if (window > 0 && keys > (int64_t)window + span + kKvBlock) keys = (int64_t)window + span + kKvBlock;
@@ -698,6 +701,13 @@ int attn_plan(const mnb_kv_cache* c, const mnb_kv_batch* b, int q_heads, int win
     // against 66 us).
     p->cluster = !prompt && p->splits > 1 && p->splits <= kMaxCluster &&
                  p->split_units * H * p->splits <= (int64_t)sms * kCtasPerSm;
+    // Of many CTAs the long ones start first, so that the last ones are short: 128 sequences of up to
+    // 8,000 keys, 8 kv heads of 128: 96 against 109 us, 256 of them 161 against 189.  Finding the
+    // u-th longest costs a CTA half a microsecond: not for short walks (256 of up to 1,000: 41.5
+    // against 38.7), nor where few CTAs share a slot (96 of up to 4,000, 2 kv heads of 64: 18.7
+    // against 15.8).
+    p->by_length = !prompt && p->split_single && b->seqs <= kKvSortMost &&
+                   2 * p->split_units * H >= 3 * (int64_t)sms * kCtasPerSm && min(chunk, keys) >= kLongWalk;
     p->ws_bytes = p->splits > 1 && !p->cluster ? (int64_t)b->tokens * q_heads * p->splits * (c->head_dim + 2) * 4 : 0;
     return MNB_OK;
 }
@@ -715,7 +725,8 @@ cudaError_t launch(AttnArgs a, const AttnPlan& p, unsigned int* status, cudaStre
     if (e == cudaSuccess && p.split_rows) {
         a.single = p.split_single;
         a.most_rows = p.row_tiles ? p.split_rows : INT64_MAX;
-        const dim3 grid((unsigned)p.split_units, (unsigned)a.b.kv_heads, (unsigned)p.splits), block(kWarps * 32);
+        a.by_length = p.by_length;
+        const dim3 grid((unsigned)(p.split_units * a.b.kv_heads), 1, (unsigned)p.splits), block(kWarps * 32);
         const int cluster = p.cluster ? p.splits : 1;
         e = p.split_rows == 8 ? launch_pdl(attn_split_kernel<D, 1>, grid, block, split_smem(D, 1), st, a, cluster)
                               : launch_pdl(attn_split_kernel<D, 2>, grid, block, split_smem(D, 2), st, a, cluster);
@@ -809,6 +820,7 @@ extern "C" int mnb_attn(const mnb_kv_cache* cache, const mnb_kv_batch* batch, co
     a.chunk = p.chunk;
     a.splits = p.splits;
     a.cluster = p.cluster;
+    a.by_length = 0;
     a.part = static_cast<float*>(ws);
     a.ml = a.part ? a.part + batch->tokens * (int64_t)q_heads * p.splits * cache->head_dim : nullptr;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

@@ -28,6 +28,7 @@ struct AttnArgs {
     int window;
     int single;          // every sequence has at most one row tile: tile u is sequence u's
     int chunk, splits;   // keys of a CTA, CTAs of a row tile
+    int by_length;       // split kernel: tile u is that of the u-th longest sequence
     int cluster;         // split kernel: the CTAs of a row tile are a cluster, which joins the chunks
     int64_t skip_rows;   // prompt kernel: sequences with at most so many rows are the split kernel's
     int64_t most_rows;   // split kernel: those with more are the prompt kernel's

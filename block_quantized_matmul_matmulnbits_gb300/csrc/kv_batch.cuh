@@ -126,6 +126,42 @@ __device__ __forceinline__ KvSeq kv_find_seq(const KvArgs& a, int64_t u, KvSplit
     }
 }
 
+// The u-th longest sequence of up to kKvSortMost, by length in steps of 128 tokens, ties by number.
+// The whole warp, one bit of the wanted length at a time.
+constexpr int kKvSortMost = 256;
+__device__ __forceinline__ int kv_by_length(const KvArgs& a, int u) {
+    constexpr int kEach = kKvSortMost / 32;
+    const int lane = threadIdx.x & 31;
+    int len[kEach], most = 0;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        const int s = i * 32 + lane;
+        len[i] = s < a.seqs ? max(a.kv_len[s], 0) >> 7 : -1;
+        most = max(most, len[i]);
+    }
+    most = __reduce_max_sync(0xffffffffu, most);
+    auto count = [&](int t) {
+        int n = 0;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) n += len[i] >= t;
+        return (int)__reduce_add_sync(0xffffffffu, (unsigned)n);
+    };
+    int t = 0;  // the length of the u-th: the largest that more than u sequences reach
+    for (int bit = 31 - __clz(most | 1); bit >= 0; --bit)
+        if (count(t | (1 << bit)) > u) t |= 1 << bit;
+    int left = u - count(t + 1);
+    int found = 0;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        const unsigned same = __ballot_sync(0xffffffffu, len[i] == t);
+        const int n = __popc(same);
+        const unsigned it = __ballot_sync(0xffffffffu, len[i] == t && __popc(same & ((1u << lane) - 1u)) == left);
+        if (left >= 0 && left < n) found = i * 32 + __ffs(it) - 1;
+        left -= n;
+    }
+    return found;
+}
+
 // Page of position `pos` (below max_tokens) of sequence s, or -1.
 __device__ __forceinline__ int kv_page(const KvArgs& a, int s, int pos) {
     const int p = a.table[(int64_t)s * a.max_pages + (pos >> a.page_shift)];

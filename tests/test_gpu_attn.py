@@ -246,3 +246,14 @@ def test_a_bad_query_row_stays_alone(news):
     good = np.ones(q.shape[:2], bool)
     good[1, 0] = good[2, 2] = False
     assert np.all((np.abs(out - want) <= tol)[good]) and np.all(np.isnan(out[1, 0]))
+
+
+@pytest.mark.parametrize("seqs,max_len", [(90, 2000), (90, 6000), (256, 5000), (257, 5000)])
+def test_many_single_tokens_with_long_bounds(seqs, max_len):
+    # tokens of many sequences, which the kernel takes longest first: equal lengths, idle slots and empty ones
+    r = np.random.default_rng(seqs)
+    lens = [int(x) for x in r.choice([0, 1, 16, 40, 150, 300], seqs)]
+    news = [int(n > 0 and x > 0.1) for n, x in zip(lens, r.random(seqs))]
+    news[5], lens[5] = 1, 0  # a token without a position
+    c = Case(44, lens, news, 8, 64, 16)
+    check(c, 8, max_len=max_len)
