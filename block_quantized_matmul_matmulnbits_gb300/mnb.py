@@ -346,31 +346,35 @@ class KVBatch:
 _half = None  # torch.float16, once torch is there
 
 
-def _is_half(x) -> bool:
+def _fp16():
     global _half
-    if _half is None:
-        import torch
-        _half = torch.float16
-    return x.dtype is _half
+    import torch
+    _half = torch.float16
+    return _half
 
 
-def _rows(x, heads: int, dim: int, tokens: int, what: str) -> int:
-    """Row stride of a token tensor [tokens, heads, dim] or [tokens, heads * dim] (rows may be strided)."""
-    shape, s = x.shape, x.stride()
+def _rows(x, shape, s, heads: int, dim: int, tokens: int, what: str) -> int:
+    """Row stride of a token tensor x of this shape and these strides, [tokens, heads, dim] or [tokens, heads * dim]
+    (rows may be strided)."""
     if len(shape) == 3:
         ok = shape[1] == heads and shape[2] == dim and s[2] == 1 and (s[1] == dim or heads == 1)
     else:
         ok = len(shape) == 2 and shape[1] == heads * dim and s[1] == 1
-    if not ok or shape[0] != tokens or not _is_half(x):
+    if not ok or shape[0] != tokens or x.dtype is not (_half or _fp16()):
         raise ValueError(f"{what}: fp16 [tokens, heads, head_dim], whole rows")
     return s[0] if tokens > 1 else max(s[0], heads * dim)
 
 
 def _kv_rows(cache, batch, K, V) -> int:
-    stride = _rows(K, cache.kv_heads, cache.head_dim, batch.tokens, "K")
-    if V.shape != K.shape or V.stride() != K.stride() or V.dtype is not K.dtype:
+    shape, s = K.shape, K.stride()
+    stride = _rows(K, shape, s, cache.kv_heads, cache.head_dim, batch.tokens, "K")
+    if V.shape != shape or V.stride() != s or V.dtype is not _half:
         raise ValueError("V: shape, strides and type of K")
     return stride
+
+
+def _filled(x, nbytes: int) -> bool:
+    return x.nbytes == nbytes and x.is_contiguous()
 
 
 def mnb_kv_write(cache: KVCache, batch: KVBatch, K, V, stream=None) -> None:
@@ -409,11 +413,11 @@ def mnb_attn(cache: KVCache, batch: KVBatch, Q, out, scale: Optional[float] = No
     """Causal attention of the batch's tokens over the cache: Q, out fp16 [tokens, q_heads, head_dim], lse
     float32 [tokens, q_heads] or None; scale defaults to head_dim ** -0.5.  ``ws``: attn_workspace(...)."""
     dim = cache.head_dim
-    q_heads = Q.shape[1] if Q.dim() == 3 else Q.shape[1] // dim
-    stride = _rows(Q, q_heads, dim, batch.tokens, "Q")
-    out_stride = _rows(out, q_heads, dim, batch.tokens, "out")
-    if lse is not None and not (lse.is_contiguous() and lse.element_size() == 4 and
-                                lse.numel() == batch.tokens * q_heads):
+    shape = Q.shape
+    q_heads = shape[1] if len(shape) == 3 else shape[1] // dim
+    stride = _rows(Q, shape, Q.stride(), q_heads, dim, batch.tokens, "Q")
+    out_stride = _rows(out, out.shape, out.stride(), q_heads, dim, batch.tokens, "out")
+    if lse is not None and not _filled(lse, 4 * batch.tokens * q_heads):
         raise ValueError("lse: float32 [tokens, q_heads]")
     rc = (_lib or lib()).mnb_attn(cache.ref, batch.ref, Q.data_ptr(), stride, q_heads,
                                   dim ** -0.5 if scale is None else scale, window, out.data_ptr(), out_stride,
@@ -429,11 +433,20 @@ def mnb_logprobs(logits, target=None, logprob=None, entropy=None, top_ids=None, 
     """Log probability of `target` (int64 [rows]), entropy and the top k of logits fp16 [rows, vocab] (rows may be
     strided) into logprob, entropy (float32 [rows]), top_ids (int32 [rows, k]) and top_logprobs (float32)."""
     rows, vocab = logits.shape
-    _want(_is_half(logits) and (logits.stride(1) == 1 or vocab == 1), "logits: fp16 [rows, vocab]")
+    _want(logits.dtype is (_half or _fp16()) and (logits.stride(1) == 1 or vocab == 1), "logits: fp16 [rows, vocab]")
     k = 0 if top_ids is None else top_ids.shape[1]
+    if not ((target is None or _filled(target, 8 * rows)) and (logprob is None or _filled(logprob, 4 * rows)) and
+            (entropy is None or _filled(entropy, 4 * rows)) and
+            (top_ids is None or _filled(top_ids, 4 * rows * k)) and
+            (top_logprobs is None or _filled(top_logprobs, 4 * rows * k))):
+        raise ValueError("target: int64 [rows]; logprob, entropy: float32 [rows]; top_ids int32, top_logprobs float32 "
+                         "[rows, k]; all contiguous")
     stride = logits.stride(0) if rows > 1 else max(logits.stride(0), vocab)
-    _check(lib().mnb_logprobs(logits.data_ptr(), rows, vocab, stride, scale, _ptr(target), k, _ptr(logprob),
-                              _ptr(entropy), _ptr(top_ids), _ptr(top_logprobs), _stream(stream)), "mnb_logprobs")
+    rc = (_lib or lib()).mnb_logprobs(logits.data_ptr(), rows, vocab, stride, scale, _ptr(target), k, _ptr(logprob),
+                                      _ptr(entropy), _ptr(top_ids), _ptr(top_logprobs),
+                                      _current_stream() if stream is None else _stream(stream))
+    if rc:
+        raise MnbError(rc, "mnb_logprobs")
 
 
 class Projection:

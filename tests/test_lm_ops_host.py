@@ -140,3 +140,16 @@ def test_the_binding_checks_its_tensors():
         mnb.mnb_attn(c, b, h(4, 4, 64), h(4, 4, 64), lse=torch.zeros(4, 2), stream=0)
     with pytest.raises(ValueError):
         mnb.mnb_logprobs(torch.zeros(2, 5), stream=0)
+
+
+@pytest.mark.parametrize("bad", [dict(target="int32"), dict(logprob="float16"), dict(entropy="rows"),
+                                 dict(top_ids="strided"), dict(top_logprobs="k")])
+def test_the_binding_checks_what_log_probabilities_go_into(bad):
+    torch = pytest.importorskip("torch")
+    given = dict(target=torch.zeros(3, dtype=torch.int64), logprob=torch.zeros(3), entropy=torch.zeros(3),
+                 top_ids=torch.zeros(3, 2, dtype=torch.int32), top_logprobs=torch.zeros(3, 2))
+    wrong = dict(int32=torch.zeros(3, dtype=torch.int32), float16=torch.zeros(3, dtype=torch.float16),
+                 rows=torch.zeros(2), strided=torch.zeros(3, 4, dtype=torch.int32)[:, ::2], k=torch.zeros(3, 1))
+    name, how = next(iter(bad.items()))
+    with pytest.raises(ValueError):
+        mnb.mnb_logprobs(torch.zeros(3, 9, dtype=torch.float16), **{**given, name: wrong[how]}, stream=0)
