@@ -658,26 +658,59 @@ int attn_plan(const mnb_kv_cache* c, const mnb_kv_batch* b, int q_heads, int win
         p->split_rows = G <= 8 ? 8 : 16;
     p->split_single = prompt || most <= p->split_rows;
     p->split_units = p->split_single ? b->seqs : kv_items(b->tokens, b->seqs, {G, p->split_rows == 8 ? 3 : 4, 1});
-    int span = p->split_rows / G + 1;  // tokens a tile's rows can lie apart
+    // Keys that a tile of so many rows sees at most: all, or with a window its tokens' windows,
+    // from a block's start.
+    auto keys_of = [&](int rows) {
+        int64_t keys = b->max_len > 1 ? b->max_len : 1;
+        if (window > 0) keys = min(keys, (int64_t)window + rows / G + 1 + kKvBlock);
+        return keys;
+    };
+    int64_t keys = keys_of(p->split_rows), chunk = 0;
     if (prompt) {
-        p->row_tiles = most <= kPromptTile ? 1 : 2;
-        p->prompt_single = most <= (int64_t)p->row_tiles * kPromptTile;
-        p->prompt_units = p->prompt_single ? b->seqs : kv_items(b->tokens, b->seqs, {G, p->row_tiles == 1 ? 7 : 8, 1});
-        span = p->row_tiles * kPromptTile / G + 1;
+        // One row tile a CTA or two, and keys enough a CTA to fill the SMs, at least 256, 512 or 1024:
+        // whichever ends first by this count, in eighths of the time of a step of 128 keys with two
+        // tiles (with one it takes 6, a CTA's start and end 22, the join 24): the longest CTA, or
+        // all of them over the SMs.  Over 90 sizes (1 to 4 sequences, 40 to 4,096 tokens behind 1 to
+        // 8,000, 8 heads of 128 and 2 of 64) what it takes is 1% from the best of them on average, 16%
+        // at worst; always two tiles and 512 keys, 11% on average.  600 tokens, 8 heads of 128: 16 us
+        // with one tile, 26 with two in two chunks; 4,096 behind 8,000: 895 and 605; 40 behind 1,000: 16
+        // and 19.
+        int64_t least = INT64_MAX;
+        for (int i = 0; i < (most <= kPromptTile ? 3 : 6); ++i) {
+            const int q = 1 + i / 3, rows = q * kPromptTile;
+            const int64_t k = keys_of(rows);
+            const bool single = most <= rows;
+            const int64_t units = single         ? b->seqs
+                                  : b->seqs == 1 ? ((int64_t)b->tokens * G + rows - 1) / rows
+                                                 : kv_items(b->tokens, b->seqs, {G, q == 1 ? 7 : 8, 1});
+            const int64_t tiles = units * H;
+            if (tiles > INT32_MAX) continue;
+            int64_t each = tiles >= sms ? k : round_up((tiles * k + sms - 1) / sms, 128);
+            each = max(each, (int64_t)(256 << i % 3));
+            if (p->split_rows) each = min(each, (int64_t)8192);  // a single token's CTA walks its chunk alone
+            auto time = [&](int64_t walk) { return (walk + 127) / 128 * (q == 1 ? 6 : 8) + 22; };
+            // causal tiles see fewer and fewer of the new tokens, half of them on average
+            const int64_t whole = k / each, rest = k % each, last = max(min(each, k - b->max_new / 2), (int64_t)1);
+            int64_t all, cost;
+            if (each >= k) {
+                all = time(last);
+                cost = time(k);
+            } else {
+                all = (whole - 1) * time(each) + (rest ? time(each) + time(rest) : time(last));
+                cost = time(each);
+            }
+            cost = max(cost, tiles * all / sms) + (each < k ? 24 : 0);
+            if (cost >= least) continue;
+            least = cost;
+            keys = k;
+            chunk = each;
+            p->row_tiles = q;
+            p->prompt_single = single;
+            p->prompt_units = units;
+        }
     }
-    if (p->prompt_units * H > INT32_MAX || p->split_units * H > INT32_MAX) return MNB_ERR_UNSUPPORTED;
-    int64_t keys = b->max_len;
-    // with a window a tile sees its tokens' windows, from a block's start
-    if (window > 0 && keys > (int64_t)window + span + kKvBlock) keys = (int64_t)window + span + kKvBlock;
-    if (keys < 1) keys = 1;
-    int64_t chunk;
-    if (prompt) {
-        // a CTA an SM: split only where there are fewer tiles than SMs, at least 512 keys each
-        const int64_t tiles = p->prompt_units * H;
-        chunk = tiles >= sms ? keys : round_up((tiles * keys + sms - 1) / sms, 128);
-        if (chunk < 512) chunk = 512;
-        if (p->split_rows && chunk > 8192) chunk = 8192;  // a single token's CTA walks its chunk alone
-    } else {
+    if ((prompt && !p->row_tiles) || p->split_units * H > INT32_MAX) return MNB_ERR_UNSUPPORTED;
+    if (!prompt) {
         // Whole rounds of the four warps.  One sequence: a CTA for every slot (131,071 keys: 49.5
         // against 52.7 us with two).  Several, of lengths that are not known here: twice as many, so that
         // the short ones' slots find work (3 uneven ones of up to 131,071 keys: 75 us with
