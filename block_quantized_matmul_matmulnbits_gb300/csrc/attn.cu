@@ -47,6 +47,8 @@ constexpr int kCtasPerSm = 3;
 constexpr int kMaxCluster = 8;
 constexpr int kJoinOneWarp = 8;     // chunks that one warp joins
 constexpr int kSplitMostRows = 48;  // of a sequence
+constexpr double kSplitMostBytes = 30e6;  // of the keys and values that its tiles read
+constexpr int kLongPart = 3072;     // keys
 constexpr int kShortChunk = 512;    // keys
 constexpr int kLongWalk = 1536;     // keys
 __host__ __device__ constexpr int ring_stages(int D) { return D == 64 ? 4 : 2; }  // stages of 32 keys in a warp's ring
@@ -645,13 +647,16 @@ int64_t round_up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
 // head) a sequence the split kernel is faster, in tiles of 8 or 16 rows that each read the keys
 // (35 rows: 13.4 against 17.8 us at 16 x 4,000 keys and 2 kv heads of 64, 20 rows: 110
 // against 144 us at 3 x 131,070 and 8 of 128), above it the prompt kernel (64 rows: 153
-// against 234 us there).  Where a batch may hold both long prompts and single tokens, the
+// against 234 us there), from 129 rows on or where the split kernel's tiles read more than 30 MB (96
+// rows, 8 heads of 128: 500 keys 10.3 against 15.3 us, 4,000 keys 16.8 against 14.6).  Where a batch may hold both long prompts and single tokens, the
 // sequences of one split tile (8 rows, or 16 with more than 8 heads a kv head) go to the split kernel.
 int attn_plan(const mnb_kv_cache* c, const mnb_kv_batch* b, int q_heads, int window, int sms, AttnPlan* p) {
     const int G = q_heads / c->kv_heads, H = c->kv_heads;
     const int64_t most = (int64_t)b->max_new * G;
+    // bytes that the split kernel's tiles of 16 rows read (sizes may be absurd: not in integers)
+    const double reread = 2.0 * b->seqs * (double)((most + 15) / 16) * H * b->max_len * c->head_dim;
     *p = AttnPlan{};
-    const bool prompt = most > kSplitMostRows;
+    const bool prompt = most > kSplitMostRows && (most > kPromptTile || reread > kSplitMostBytes);
     if (!prompt)
         p->split_rows = most <= 8 ? 8 : 16;
     else if (b->seqs > 1 && G <= 16 && b->tokens < (int64_t)b->seqs * b->max_new)
@@ -674,10 +679,14 @@ int attn_plan(const mnb_kv_cache* c, const mnb_kv_batch* b, int q_heads, int win
         // 8,000, 8 heads of 128 and 2 of 64) what it takes is 1% from the best of them on average, 16%
         // at worst; always two tiles and 512 keys, 11% on average.  600 tokens, 8 heads of 128: 16 us
         // with one tile, 26 with two in two chunks; 4,096 behind 8,000: 895 and 605; 40 behind 1,000: 16
-        // and 19.
+        // and 19.  Several sequences of few tiles and long walks may also get twice the chunks, of
+        // which the shorter sequences leave some empty (16 tokens of 4 of up to 30,000 keys: 93 to 58
+        // us; with many tiles it costs: 2,000 of 4 behind 8,000, 2 heads of 64: 129 to 146).
         int64_t least = INT64_MAX;
-        for (int i = 0; i < (most <= kPromptTile ? 3 : 6); ++i) {
-            const int q = 1 + i / 3, rows = q * kPromptTile;
+        const int folds = b->seqs > 1 ? 2 : 1;
+        for (int i = 0; i < (most <= kPromptTile ? 3 : 6) * folds; ++i) {
+            const bool fold = i / 3 % folds == 1;
+            const int q = 1 + i / (3 * folds), rows = q * kPromptTile, slots = fold ? 2 * sms : sms;
             const int64_t k = keys_of(rows);
             const bool single = most <= rows;
             const int64_t units = single         ? b->seqs
@@ -685,8 +694,9 @@ int attn_plan(const mnb_kv_cache* c, const mnb_kv_batch* b, int q_heads, int win
                                                  : kv_items(b->tokens, b->seqs, {G, q == 1 ? 7 : 8, 1});
             const int64_t tiles = units * H;
             if (tiles > INT32_MAX) continue;
-            int64_t each = tiles >= sms ? k : round_up((tiles * k + sms - 1) / sms, 128);
+            int64_t each = tiles >= slots ? k : round_up((tiles * k + slots - 1) / slots, 128);
             each = max(each, (int64_t)(256 << i % 3));
+            if (fold && (2 * tiles > sms || each < kLongPart)) continue;
             if (p->split_rows) each = min(each, (int64_t)8192);  // a single token's CTA walks its chunk alone
             auto time = [&](int64_t walk) { return (walk + 127) / 128 * (q == 1 ? 6 : 8) + 22; };
             // causal tiles see fewer and fewer of the new tokens, half of them on average
@@ -699,7 +709,7 @@ int attn_plan(const mnb_kv_cache* c, const mnb_kv_batch* b, int q_heads, int win
                 all = (whole - 1) * time(each) + (rest ? time(each) + time(rest) : time(last));
                 cost = time(each);
             }
-            cost = max(cost, tiles * all / sms) + (each < k ? 24 : 0);
+            cost = max(cost, tiles * all * (fold ? 7 : 8) / (8 * (int64_t)sms)) + (each < k ? 24 : 0);
             if (cost >= least) continue;
             least = cost;
             keys = k;

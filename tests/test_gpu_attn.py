@@ -257,3 +257,12 @@ def test_many_single_tokens_with_long_bounds(seqs, max_len):
     news[5], lens[5] = 1, 0  # a token without a position
     c = Case(44, lens, news, 8, 64, 16)
     check(c, 8, max_len=max_len)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("max_len", [None, 40000])
+def test_rows_between_the_kernels(dim, max_len):
+    # 49 to 128 rows a sequence: a short bound goes to the split kernel in tiles of 16 rows, a long one to the
+    # prompt kernel, with more chunks than the sequences have keys for
+    check(Case(45, [400, 33, 16, 210], [16, 9, 16, 1], 2, dim, 32), 16, max_len=max_len)
+    check(Case(46, [301], [7], 2, dim, 16), 14, window=60, max_len=max_len)
