@@ -16,8 +16,8 @@
 // cache) takes 19.1 us, 5.2 TB/s: each call loads all there is at once and then
 // stores it, and the look for the sequence, its page and its rows comes before.  CTAs of four
 // warps: writing and reading a step of 128 sequences took 9.2 us, with eight 10.5, with one
-// 10.5 (now 8.2: four codes in 12 instructions, a step and the prompts above had been held
-// up by 16 a value).
+// 10.5; 12.4 instead of 15.6 instructions a value (new_codes below) then made it 8.2, and the
+// prompts above 19.1 instead of 20.9.
 //
 // The magnitude is taken on the FP16 bit patterns without their sign, which
 // order as unsigned integers with NaN above infinity above every finite value,
