@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(Layout<D, NQ>::kThreads, 1) attn_prompt_kernel
     const int rows = (int)min((int64_t)tl.n * a.group - tl.r0, (int64_t)kRows);
     const int first = tl.len - tl.n;
     const int tok_a = tl.r0 / a.group, tok_b = (tl.r0 + rows - 1) / a.group;
-    const int hi_t = max(first + tok_b + 1, 0);
+    const int hi_t = min(max(first + tok_b + 1, 0), a.b.max_tokens);  // past the table are no keys
     const int lo_t = a.window > 0 ? max(first + tok_a - a.window + 1, 0) : 0;
     const int64_t begin64 = (int64_t)(lo_t & ~(kKvBlock - 1)) + (int64_t)split * a.chunk;
     const int begin = (int)min(begin64, (int64_t)hi_t);

@@ -40,7 +40,7 @@ struct KvArgs {
     const int32_t* kv_len;  // [seqs]
     const int32_t* q_start; // [seqs + 1]
     int64_t num_pages;
-    int64_t max_tokens;     // max_pages * page_size, at most 2^31 - 1
+    int max_tokens;         // positions that the table has pages for
     int seqs, max_pages, tokens;
     int page_shift;         // log2(page_size)
     int kv_heads, head_dim;
@@ -54,8 +54,8 @@ inline KvArgs kv_args(const mnb_kv_cache* c, const mnb_kv_batch* b) {
     a.num_pages = c->num_pages;
     a.page_shift = 0;
     while ((1 << a.page_shift) < c->page_size) ++a.page_shift;
-    a.max_tokens = (int64_t)b->max_pages << a.page_shift;
-    if (a.max_tokens > INT32_MAX) a.max_tokens = INT32_MAX;
+    const int64_t most = (int64_t)b->max_pages << a.page_shift;
+    a.max_tokens = most > INT32_MAX ? INT32_MAX : (int)most;
     a.seqs = b->seqs;
     a.max_pages = b->max_pages;
     a.tokens = (int)b->tokens;
@@ -81,13 +81,14 @@ __host__ __device__ inline int64_t kv_items(int64_t tokens, int seqs, KvSplit k)
 }
 
 // One sequence of the batch: its length, and its tokens of this call: rows row0 .. row0 + n - 1
-// are the positions len - n .. len - 1 (the first ones may lie before 0).
+// are the positions len - n .. len - 1.  The first ones may lie before 0, and the last ones past
+// the table: positions from max_tokens on have no page, whatever the length says.
 struct KvSeq {
     int s, len, row0, n;
 };
 
 __device__ __forceinline__ KvSeq kv_sequence(const KvArgs& a, int s, int q0, int q1, int l) {
-    return {s, l < 0 ? 0 : (int)min((int64_t)l, a.max_tokens), q0, q1 > q0 ? min(q1 - q0, a.tokens) : 0};
+    return {s, max(l, 0), q0, q1 > q0 ? min(q1 - q0, a.tokens) : 0};
 }
 
 __device__ __forceinline__ KvSeq kv_sequence(const KvArgs& a, int s) {

@@ -47,7 +47,7 @@ struct KvIoArgs {
 // The block of one warp: where its codes and scale lie, and which positions are the call's.
 struct KvUnit {
     int which, head;
-    int lo, first, len;    // first position of the block; of the call's tokens; the sequence's length
+    int lo, first, end;    // first position of the block; of the call's tokens; the sequence's end in the table
     int64_t row0;          // token row of position `first`
     int64_t slot;          // row of the cache (page, head, row in page) of position lo
 };
@@ -64,11 +64,11 @@ __device__ __forceinline__ bool kv_unit(const KvIoArgs& p, KvUnit& u) {
     u.head = u.which ? c - a.kv_heads : c;
     int64_t first_item;
     const KvSeq q = kv_find_seq(a, item, kBlocks, &first_item);
-    u.len = q.len;
+    u.end = min(q.len, a.max_tokens);
     u.first = q.len - q.n;
     u.row0 = q.row0;
     const int64_t lo = ((int64_t)((u.first > 0 ? u.first : 0) >> 4) + ((int64_t)item - first_item)) * kKvBlock;
-    if (q.n == 0 || lo < 0 || lo >= u.len) return false;
+    if (q.n == 0 || lo < 0 || lo >= u.end) return false;
     u.lo = (int)lo;
     const int page = kv_page(a, q.s, u.lo);
     if (page < 0) return false;
@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(kWarps * 32) kv_write_kernel(const KvIoArgs p)
     for (int i = 0; i < NI; ++i) {
         const int pos = u.lo + i * RPI + r0;
         const int64_t row = u.row0 + (pos - u.first);
-        const bool f = pos >= u.first && pos < u.len && row >= 0 && row < p.b.tokens;
+        const bool f = pos >= u.first && pos < u.end && row >= 0 && row < p.b.tokens;
         v[i] = f ? *reinterpret_cast<const uint4*>(x + row * p.row_stride) : make_uint4(0, 0, 0, 0);
         fresh |= f ? 1u << i : 0u;
         kept |= pos < u.first ? 1u << i : 0u;
@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(kWarps * 32) kv_read_kernel(const KvIoArgs p) 
     for (int i = 0; i < NI; ++i) {
         const int pos = u.lo + i * RPI + r0;
         const int64_t row = u.row0 + (pos - u.first);
-        if (pos < u.first || pos >= u.len || row < 0 || row >= p.b.tokens) continue;
+        if (pos < u.first || pos >= u.end || row < 0 || row >= p.b.tokens) continue;
         *reinterpret_cast<uint4*>(x + row * p.row_stride) =
             make_uint4(values_half2<0x7440u, 0x7441u>(q[i].x, s2), values_half2<0x7442u, 0x7443u>(q[i].x, s2),
                        values_half2<0x7440u, 0x7441u>(q[i].y, s2), values_half2<0x7442u, 0x7443u>(q[i].y, s2));

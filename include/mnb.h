@@ -374,8 +374,10 @@ typedef struct {
  * The lengths are read on the device, so a captured call can be replayed with
  * others.  max_new and max_len choose the launch: rows of a sequence with
  * more than max_new may be left out; a max_len that is off costs time only.
- * Positions before 0, rows past `tokens`, lengths past max_pages pages and
- * page numbers outside the cache are skipped, never followed. */
+ * Positions before 0 or past max_pages pages, rows past `tokens` and page
+ * numbers outside the cache are skipped, never followed: a token without a
+ * place is neither written nor read back, its attention sees those keys of its
+ * context that have one, and the other tokens keep their positions. */
 typedef struct {
     int32_t seqs;
     int32_t max_pages;

@@ -117,3 +117,55 @@ def attn_ref(c, q, scale, window=0):
                 tol[t, h] += (2.0 ** -11 + 2 * ds) * spread + 2.0 ** -11 * np.abs(out[t, h]) \
                     + 2.0 ** -25 * len(x) * np.abs(vh).max()
     return out, lse, tol
+
+
+def past_the_table(c, over):
+    """Lengths of `over[s]` positions past the last page of the table, which gets no spare column.  Returns the
+    table that a call is given; c keeps one with columns of missing pages for the references: a position past
+    the table is one whose page does not exist."""
+    full = c.table[:, :-1].copy()
+    cap = full.shape[1] * c.P
+    c.lens = [cap + o for o in over]
+    more = -(-max(max(over), 0) // c.P)
+    c.table = np.concatenate([full, np.full((len(c.lens), more + 1), -1, np.int32)], 1)
+    return full
+
+
+def attn_ref_rows(c, q, scale, window=0):
+    """attn_ref for many rows: the same definition and tolerance, a sequence and head at a time."""
+    T, Hq, D = q.shape
+    G = Hq // c.H
+    out, lse, tol = np.zeros(q.shape), np.full((T, Hq), -np.inf), np.full(q.shape, 2.0 ** -25)
+    for s, (n, length) in enumerate(zip(c.news, c.lens)):
+        if not n or length <= 0:
+            continue
+        j = np.arange(length)
+        page = c.table[s, j // c.P].astype(np.int64)
+        there = (page >= 0) & (page < c.pages)
+        page = np.where(there, page, 0)
+        pos = length - n + np.arange(n)
+        sees = there & (j <= pos[:, None])
+        if window:
+            sees &= j > pos[:, None] - window
+        rows = slice(c.q_start[s], c.q_start[s] + n)
+        for h in range(Hq):
+            k, v = ((c.codes[w][page, h // G, j % c.P].astype(np.float64) - 128)
+                    * c.scales[w][page, h // G, j % c.P // BLOCK].astype(np.float64)[:, None] for w in (0, 1))
+            k, v = np.where(there[:, None], k, 0), np.where(there[:, None], v, 0)
+            qh = q[rows, h].astype(np.float64)
+            x = np.where(sees, qh @ k.T * scale, -np.inf)
+            some = sees.any(1)
+            m = np.where(some, x.max(1), 0.0)
+            e = np.exp(x - m[:, None])
+            den = np.where(some, e.sum(1), 1.0)
+            o = e @ v / den[:, None]
+            with np.errstate(divide="ignore"):
+                lse[rows, h] = np.where(some, m + np.log(den), -np.inf)
+            out[rows, h] = o
+            ds = 2.0 ** -24 * (D + 8) * np.where(sees, np.abs(qh) @ np.abs(k).T * abs(scale), 0).max(1) + 2.0 ** -21
+            spread = e @ np.abs(v) / den[:, None]
+            far = np.array([np.abs(v[row]).max() if row.any() else 0.0 for row in sees])
+            add = (2.0 ** -11 + 2 * ds)[:, None] * spread + 2.0 ** -11 * np.abs(o) \
+                + (2.0 ** -25 * sees.sum(1) * far)[:, None]
+            tol[rows, h] += np.where(some[:, None], add, 0)
+    return out, lse, tol

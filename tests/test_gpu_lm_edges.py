@@ -1,0 +1,95 @@
+"""Calls at the edges of the cache, attention and log probabilities: lengths past the page table."""
+import numpy as np
+import pytest
+
+from lm_helpers import Case, attn_ref_rows, past_the_table, write_ref
+from test_gpu_attn import queries, run
+from test_gpu_kv_cache import read_ref, run_write, tokens
+
+torch = pytest.importorskip("torch")
+from block_quantized_matmul_matmulnbits_gb300 import mnb  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+
+# ---- lengths past the table: the positions keep their numbers, those without a page are missing
+
+PAST = [  # positions past the table by sequence, new tokens
+    ([1], [1]),
+    ([2], [5]),
+    ([16, -3, 0], [16, 1, 9]),
+    ([5, -40, 33], [1, 7, 40]),
+    ([500, 1], [3, 300]),          # no new token of the first has a page
+]
+
+
+@pytest.mark.parametrize("over,news", PAST)
+def test_tokens_past_the_table_are_not_written(over, news):
+    c = Case(60, [128] * len(over), news, 2, 64, 16)
+    short = past_the_table(c, over)
+    k, v = tokens(c, 6)
+    want = write_ref(c, k, v)
+    c.table = short
+    got = run_write(c, k, v)
+    for w in (0, 1):
+        np.testing.assert_array_equal(got[0][w], want[0][w])
+        np.testing.assert_array_equal(got[1][w], want[1][w])
+
+
+@pytest.mark.parametrize("over,news", PAST)
+def test_tokens_past_the_table_are_not_read(over, news):
+    c = Case(61, [128] * len(over), news, 2, 128, 32)
+    short = past_the_table(c, over)
+    want = read_ref(c, 9)
+    c.table = short
+    cache, batch = c.upload(torch, mnb)
+    k, v = (torch.full((c.T, c.H, c.D), 9.0, dtype=torch.float16, device="cuda") for _ in range(2))
+    mnb.mnb_kv_read(cache, batch, k, v)
+    torch.cuda.synchronize()
+    np.testing.assert_array_equal(k.cpu().numpy(), want[0])
+    np.testing.assert_array_equal(v.cpu().numpy(), want[1])
+
+
+@pytest.mark.parametrize("window", [0, 40])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("over,news", PAST + [([1, 60], [300, 300])])
+def test_attention_of_tokens_past_the_table(over, news, dim, window):
+    c = Case(62, [256] * len(over), news, 1, dim, 32)
+    short = past_the_table(c, over)
+    q = queries(c, 3)
+    want = attn_ref_rows(c, q, 0.1, window)
+    c.table = short
+    out, lse = run(c, q, 0.1, window)
+    assert np.all(np.abs(out - want[0]) <= want[2])
+    empty = np.isinf(want[1])
+    assert np.all(lse[empty] == -np.inf)
+    assert np.all(np.abs(lse - want[1])[~empty] <= 2e-4 + 1e-6 * np.abs(want[1][~empty]))
+
+
+def test_a_decode_step_replayed_past_the_table():
+    c = Case(63, [62], [1], 2, 64, 32)
+    c.table = c.table[:, :2].copy()
+    cache, batch = c.upload(torch, mnb)
+    g = torch.Generator("cuda").manual_seed(63)
+    k, v = (torch.randn(1, 2, 64, device="cuda", generator=g).half() for _ in range(2))
+    q = torch.randn(1, 4, 64, device="cuda", generator=g).half()
+    out = torch.empty_like(q)
+    ws = mnb.attn_workspace(cache, batch, 4)
+    step = lambda: (batch.kv_len.add_(1), mnb.mnb_kv_write(cache, batch, k, v),  # noqa: E731
+                    mnb.mnb_attn(cache, batch, q, out, ws=ws))
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    graph.replay()  # position 63, the table's last
+    torch.cuda.synchronize()
+    held = [t.clone() for t in (cache.K, cache.V, cache.K_scales, cache.V_scales)]
+    full = out.clone()
+    for _ in range(3):
+        k.mul_(3)
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(held, (cache.K, cache.V, cache.K_scales, cache.V_scales)):
+            assert torch.equal(a, b)
+        assert torch.equal(out, full)  # the same 64 keys
