@@ -35,6 +35,10 @@ inline cudaError_t launch_pdl(void (*kernel)(A), dim3 grid, dim3 block, size_t s
 
 constexpr int kKvBlock = MNB_KV_BLOCK;  // tokens that share a scale
 
+// Positions of a sequence that are ever visited: a kernel's tiles and stages reach past the last
+// one by less than 4,096, and their positions stay 32-bit integers.
+constexpr int kKvMostTokens = INT32_MAX - 4095;
+
 struct KvArgs {
     const int32_t* table;   // [seqs, max_pages]
     const int32_t* kv_len;  // [seqs]
@@ -55,7 +59,7 @@ inline KvArgs kv_args(const mnb_kv_cache* c, const mnb_kv_batch* b) {
     a.page_shift = 0;
     while ((1 << a.page_shift) < c->page_size) ++a.page_shift;
     const int64_t most = (int64_t)b->max_pages << a.page_shift;
-    a.max_tokens = most > INT32_MAX ? INT32_MAX : (int)most;
+    a.max_tokens = most > kKvMostTokens ? kKvMostTokens : (int)most;
     a.seqs = b->seqs;
     a.max_pages = b->max_pages;
     a.tokens = (int)b->tokens;

@@ -358,7 +358,7 @@ typedef struct {
 
 /* The sequences of one call.
  *   seqs        sequences
- *   max_pages   columns of page_table
+ *   max_pages   columns of page_table; of its positions the first 2^31 - 4096 exist
  *   page_table  int32 [seqs, max_pages] (device): page j of sequence s holds
  *               its positions j * page_size .. ; entries past the sequence's
  *               length are not read

@@ -93,3 +93,51 @@ def test_a_decode_step_replayed_past_the_table():
         for a, b in zip(held, (cache.K, cache.V, cache.K_scales, cache.V_scales)):
             assert torch.equal(a, b)
         assert torch.equal(out, full)  # the same 64 keys
+
+
+# ---- positions next to 2^31: one page, over and over
+
+FULL = 2 ** 31 - 4096  # positions that exist
+
+
+def repeated_page(kv_len, tokens, max_new):
+    c = Case(68, [256], [1], 1, 64, 256, spare=0)
+    c.table[:] = 0
+    cache, _ = c.upload(torch, mnb)
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    table = torch.zeros(1, 2 ** 23, dtype=torch.int32, device="cuda")
+    return c, cache, mnb.KVBatch(table, i32(kv_len), i32(0, tokens), tokens, max_new, 2 ** 31 - 1)
+
+
+@pytest.mark.parametrize("n", [1, 150])
+def test_attention_next_to_the_last_position(n):
+    # every key of the page counts 2^23 - 16 times (for the later tokens too, whose positions do not exist): the page's own
+    # result.  A warp adds 2^31 / 456 / 4 / 16 products one after the other, a CTA of the prompt kernel 2^31 / 152 / 16
+    kv_len = 2 ** 31 - 1
+    c, cache, batch = repeated_page(kv_len, n, n)
+    q = np.random.default_rng(68).standard_normal((n, 1, 64)).astype(np.float16)
+    qd = torch.from_numpy(q).cuda()
+    out, lse = torch.empty_like(qd), torch.empty(n, 1, device="cuda")
+    mnb.mnb_attn(cache, batch, qd, out, lse=lse, ws=mnb.attn_workspace(cache, batch, 1))
+    torch.cuda.synchronize()
+    c.news, c.q_start = [n], np.array([0, n])
+    c.lens = [256 + n]  # every token sees the whole page, and none of what follows it
+    c.table = np.array([[0, -1, -1]], np.int32)
+    want, want_lse, tol = attn_ref_rows(c, q, 0.125)
+    adds = 2 ** 31 / (456 * 64 if n == 1 else 152 * 16)
+    v = np.abs((c.codes[1][0, 0].astype(float) - 128) * c.scales[1][0, 0].repeat(16)[:, None]).max()
+    assert np.all(np.abs(out.double().cpu().numpy() - want) <= tol + adds * 2.0 ** -23 * v)
+    assert np.all(np.abs(lse.double().cpu().numpy() - want_lse - np.log(2 ** 23 - 16)) <= 2e-4 + adds * 2.0 ** -23)
+
+
+def test_writing_and_reading_next_to_the_last_position():
+    c, cache, batch = repeated_page(FULL + 2, 5, 5)
+    held = cache.K.clone()
+    k = torch.randn(5, 1, 64, device="cuda").half()
+    mnb.mnb_kv_write(cache, batch, k, k)
+    back = [torch.full_like(k, 9.0) for _ in range(2)]
+    mnb.mnb_kv_read(cache, batch, *back)
+    torch.cuda.synchronize()
+    step = cache.K_scales[0, 0, 15].item()
+    assert (back[0][:3] - k[:3]).abs().max().item() <= 0.51 * step + 2e-3 and torch.all(back[0][3:] == 9)
+    assert torch.equal(cache.K[:, :, :240], held[:, :, :240])
