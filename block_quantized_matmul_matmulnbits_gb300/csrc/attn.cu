@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) attn_split_kernel(con
     // the tile: its last token sees furthest, its first one starts furthest back
     const int tok_a = tl.r0 / a.group, tok_b = (tl.r0 + rows - 1) / a.group;
     const int hi_t = min(max(first + tok_b + 1, 0), a.b.max_tokens);  // past the table are no keys
-    const int lo_t = a.window > 0 ? max(first + tok_a - a.window + 1, 0) : 0;
+    const int lo_t = window_start(a, first + tok_a);
     const int64_t begin64 = (int64_t)(lo_t & ~(kKvBlock - 1)) + (int64_t)split * a.chunk;
     const int begin = (int)min(begin64, (int64_t)hi_t);
     // the last chunk takes what is left, however long
@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) attn_split_kernel(con
     const int mine = nstage > warp ? (nstage - warp + kWarps - 1) / kWarps : 0;
     // blocks that every row of the tile sees wholly need no mask
     const int all_hi = min(max(first + tok_a + 1, 0), end);
-    const int all_lo = a.window > 0 ? max(first + tok_b - a.window + 1, 0) : 0;
+    const int all_lo = window_start(a, first + tok_b);
 
     // Where this warp's blocks lie, 32 blocks (16 stages) at a time, one a lane: the row
     // of the cache (-1: no such page) and the two scales; `nxt` is loaded while `cur` is used.
@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) attn_split_kernel(con
             const int rr = 8 * nt + 2 * t + b;
             const int pos = first + (tl.r0 + rr) / a.group;
             hi[nt][b] = rr < rows ? min(max(pos + 1, 0), end) : 0;
-            lo[nt][b] = a.window > 0 ? max(pos - a.window + 1, 0) : 0;
+            lo[nt][b] = window_start(a, pos);
         }
     }
 

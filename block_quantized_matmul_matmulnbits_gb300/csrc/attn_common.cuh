@@ -76,6 +76,11 @@ __device__ __forceinline__ bool find_tile(const AttnArgs& a, int64_t u, int row_
     return true;
 }
 
+// First position that a token at `pos` (before 0, too) sees; any window, the largest int among them.
+__device__ __forceinline__ int window_start(const AttnArgs& a, int pos) {
+    return a.window > 0 ? max(max(pos, 0) - a.window + 1, 0) : 0;
+}
+
 constexpr int kPromptTile = 128;  // rows of one tile of the prompt kernel (attn_prompt.cu)
 cudaError_t attn_prompt_prepare();
 // row_tiles: 1 or 2 tiles a CTA; units: its row groups (kv_items)

@@ -280,13 +280,13 @@ __global__ void __launch_bounds__(Layout<D, NQ>::kThreads, 1) attn_prompt_kernel
     const int first = tl.len - tl.n;
     const int tok_a = tl.r0 / a.group, tok_b = (tl.r0 + rows - 1) / a.group;
     const int hi_t = min(max(first + tok_b + 1, 0), a.b.max_tokens);  // past the table are no keys
-    const int lo_t = a.window > 0 ? max(first + tok_a - a.window + 1, 0) : 0;
+    const int lo_t = window_start(a, first + tok_a);
     const int64_t begin64 = (int64_t)(lo_t & ~(kKvBlock - 1)) + (int64_t)split * a.chunk;
     const int begin = (int)min(begin64, (int64_t)hi_t);
     const int end = split == a.splits - 1 ? hi_t : (int)min(begin64 + a.chunk, (int64_t)hi_t);
     const int nj = (int)(((int64_t)end - begin + kTileKeys - 1) / kTileKeys);
     const int all_hi = min(max(first + tok_a + 1, 0), end);
-    const int all_lo = a.window > 0 ? max(first + tok_b - a.window + 1, 0) : 0;
+    const int all_lo = window_start(a, first + tok_b);
 
     const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
     unsigned char* sptr = smem_raw + (base - raw);
@@ -497,7 +497,7 @@ __global__ void __launch_bounds__(Layout<D, NQ>::kThreads, 1) attn_prompt_kernel
         const bool ok_row = r < rows && trow >= 0 && trow < a.b.tokens;
         const int pos = first + tok;
         const int hi = ok_row ? min(max(pos + 1, 0), end) : 0;
-        const int lo = a.window > 0 ? max(pos - a.window + 1, 0) : 0;
+        const int lo = window_start(a, pos);
         {  // the warp's 32 rows into the operand, 16 bytes a lane, whole rows side by side
             constexpr int kLanes = D / 8;
             const uint32_t to = base + L::kQ + q * L::kOperand;

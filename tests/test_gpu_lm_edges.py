@@ -1,4 +1,5 @@
-"""Calls at the edges of the cache, attention and log probabilities: lengths past the page table."""
+"""Calls at the edges of the cache, attention and log probabilities: lengths past the page table, positions next to
+2^31, windows of any size."""
 import numpy as np
 import pytest
 
@@ -10,6 +11,20 @@ torch = pytest.importorskip("torch")
 from block_quantized_matmul_matmulnbits_gb300 import mnb  # noqa: E402
 
 pytestmark = pytest.mark.gpu
+
+
+def agree(c, heads, scale, window=0, q=None, **kw):
+    """mnb_attn against the definition; returns what it gave."""
+    q = queries(c, heads) if q is None else q
+    want, want_lse, tol = attn_ref_rows(c, q, scale, window)
+    out, lse = run(c, q, scale, window, **kw)
+    assert np.all(np.isfinite(out))
+    worst = np.max(np.abs(out - want) / tol)
+    assert worst <= 1, f"worst error is {worst:.3g} of its tolerance"
+    empty = np.isinf(want_lse)
+    assert np.all(lse[empty] == -np.inf) and np.all(out[empty] == 0)
+    assert np.all(np.abs(lse[~empty] - want_lse[~empty]) <= 2e-4 + 1e-6 * np.abs(want_lse[~empty]))
+    return out, lse
 
 
 # ---- lengths past the table: the positions keep their numbers, those without a page are missing
@@ -141,3 +156,13 @@ def test_writing_and_reading_next_to_the_last_position():
     step = cache.K_scales[0, 0, 15].item()
     assert (back[0][:3] - k[:3]).abs().max().item() <= 0.51 * step + 2e-3 and torch.all(back[0][3:] == 9)
     assert torch.equal(cache.K[:, :, :240], held[:, :, :240])
+
+
+# ---- windows
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("lens,news", [([3], [8]), ([100], [200]), ([40], [41])])
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 60])
+def test_the_largest_windows(dim, lens, news, window):
+    c = Case(66, lens, news, 1, dim, 16)
+    agree(c, 2, 0.125, window)
