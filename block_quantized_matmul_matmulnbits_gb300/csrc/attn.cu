@@ -828,7 +828,8 @@ extern "C" int mnb_attn(const mnb_kv_cache* cache, const mnb_kv_batch* batch, co
     int rc = mnb::attn_check(cache, batch, q_heads, window, &empty);
     if (rc != MNB_OK) return rc;
     const int64_t width = (int64_t)q_heads * cache->head_dim;
-    if (q_stride < width || out_stride < width || ws_bytes < 0) return MNB_ERR_ARG;
+    // the scale meets key scales and 2^24 in binary32
+    if (q_stride < width || out_stride < width || ws_bytes < 0 || !(fabsf(scale) <= 1e27f)) return MNB_ERR_ARG;
     if (q_stride % 8 != 0 || out_stride % 8 != 0) return MNB_ERR_ALIGN;
     if (empty) return MNB_OK;
     if (!Q || !out) return MNB_ERR_ARG;

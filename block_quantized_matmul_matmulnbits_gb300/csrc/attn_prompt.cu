@@ -469,7 +469,7 @@ __global__ void __launch_bounds__(Layout<D, NQ>::kThreads, 1) attn_prompt_kernel
                 const float v = vs == 0.f ? 8.67361738e-19f : vs;  // 2^-60: see attn_split_kernel
                 scales[(j & (kScaleRing - 1)) * kTileBlocks + lb] =
                     slot < 0 ? make_float4(0.f, -INFINITY, 1.f, 0.f)
-                             : make_float4(ks * a.scale_log2, __log2f(v), __frcp_rn(v), 0.f);
+                             : make_float4(ks * fabsf(a.scale_log2), __log2f(v), __frcp_rn(v), 0.f);
             }
             fence_async_proxy();
             __syncwarp();
@@ -499,6 +499,9 @@ __global__ void __launch_bounds__(Layout<D, NQ>::kThreads, 1) attn_prompt_kernel
         const int hi = ok_row ? min(max(pos + 1, 0), end) : 0;
         const int lo = window_start(a, pos);
         {  // the warp's 32 rows into the operand, 16 bytes a lane, whole rows side by side
+            // A negative scale turns the queries' signs instead: a block's largest score then has its
+            // largest exponent, whatever the sign.
+            const uint32_t turn = a.scale_log2 < 0.f ? 0x80008000u : 0u;
             constexpr int kLanes = D / 8;
             const uint32_t to = base + L::kQ + q * L::kOperand;
             const int c = lane % kLanes;
@@ -507,7 +510,8 @@ __global__ void __launch_bounds__(Layout<D, NQ>::kThreads, 1) attn_prompt_kernel
                 const int from = i * (32 / kLanes) + lane / kLanes;
                 const int64_t at = __shfl_sync(0xffffffffu, ok_row ? trow * a.q_stride + (int64_t)qh * D : -1, from);
                 const uint4 v = at >= 0 && nj > 0 ? *reinterpret_cast<const uint4*>(a.Q + at + c * 8) : make_uint4(0, 0, 0, 0);
-                sts128(to + (uint32_t)((c >> 3) * kSlab) + swizzled(sub * 32 + from, c & 7), v.x, v.y, v.z, v.w);
+                sts128(to + (uint32_t)((c >> 3) * kSlab) + swizzled(sub * 32 + from, c & 7), v.x ^ turn, v.y ^ turn, v.z ^ turn,
+                       v.w ^ turn);
             }
             fence_async_proxy();
             __syncwarp();

@@ -342,7 +342,8 @@ int64_t mnb_noalloc_max_rows(void);
  *   K_scales, V_scales   float [num_pages, kv_heads, page_size / 16]
  * A block of 16 tokens of a page and head shares one scale; a code q stands
  * for (q - 128) * scale, the map of this library's INT8 weights with their
- * default zero point. */
+ * default zero point.  Scales are not negative (mnb_kv_write makes them 0, 2^-31
+ * to 516, or not finite); a cache filled otherwise keeps to that. */
 #define MNB_KV_BLOCK 16
 typedef struct {
     int64_t num_pages;
@@ -424,6 +425,7 @@ int mnb_kv_read(const mnb_kv_cache* cache, const mnb_kv_batch* batch, void* K, v
  *   out = sum_j softmax_j(scale * q . k_j) v_j,   k_j, v_j as the codes stand
  *   Q      fp16, row t at Q + t * q_stride, [q_heads, head_dim]; query head h
  *          reads kv head h / (q_heads / kv_heads)
+ *   scale  any of either sign, at most 1e27 in size (0 too: the mean of the values)
  *   out    fp16, row t at out + t * out_stride, [q_heads, head_dim]
  *   lse    float [tokens, q_heads] or NULL: log of the sum of
  *          exp(scale * q . k_j) (natural logarithm)

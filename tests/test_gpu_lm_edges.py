@@ -1,5 +1,5 @@
 """Calls at the edges of the cache, attention and log probabilities: lengths past the page table, positions next to
-2^31, windows of any size."""
+2^31, windows of any size, scales of either sign."""
 import numpy as np
 import pytest
 
@@ -166,3 +166,13 @@ def test_writing_and_reading_next_to_the_last_position():
 def test_the_largest_windows(dim, lens, news, window):
     c = Case(66, lens, news, 1, dim, 16)
     agree(c, 2, 0.125, window)
+
+
+# ---- scales
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("news,window", [([5], 0), ([100], 0), ([200], 0), ([200], 50), ([1], 0)])
+@pytest.mark.parametrize("scale", [-0.125, 0.0, -2.0])
+def test_scales_of_either_sign(dim, news, window, scale):
+    c = Case(64, [230], news, 1, dim, 32)
+    agree(c, 2, scale, window)
