@@ -147,8 +147,11 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) attn_split_kernel(con
         return page < 0 ? (int64_t)-1
                         : (((int64_t)page * a.b.kv_heads + head) << a.b.page_shift) + (lane_pos(base) & pmask);
     };
+    // An infinite key scale becomes NaN: its codes stand for no number, but the scores they give
+    // here are zero to a few roundings of either sign, which would make the key count as hidden.
     auto load_scales = [&](int64_t slot, float& ks, float& vs) {
         ks = slot < 0 ? 0.f : a.Ks[slot >> 4];
+        ks = fmaf(0.f, ks, ks);
         vs = slot < 0 ? 1.f : a.Vs[slot >> 4];
     };
     int64_t slot_cur = slot_of(load_page(0), 0), slot_nxt = -1;

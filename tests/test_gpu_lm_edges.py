@@ -1,5 +1,5 @@
 """Calls at the edges of the cache, attention and log probabilities: lengths past the page table, positions next to
-2^31, windows of any size, scales of either sign."""
+2^31, windows of any size, scales of either sign and infinite ones."""
 import numpy as np
 import pytest
 
@@ -176,3 +176,18 @@ def test_the_largest_windows(dim, lens, news, window):
 def test_scales_of_either_sign(dim, news, window, scale):
     c = Case(64, [230], news, 1, dim, 32)
     agree(c, 2, scale, window)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("news", [[1], [5], [100], [200]])
+@pytest.mark.parametrize("which,max_len", [(0, None), (1, None), (0, 20000), (1, 20000)])
+def test_an_infinite_key_or_value_is_seen(dim, news, which, max_len):
+    # FP16's infinity among the keys or values: its block's scale is infinite, and whoever sees it gets NaN
+    c = Case(65, [230], news, 2, dim, 16)
+    b = 224 // 16 - (6 if news == [200] else 1)
+    p = c.table[0, b]
+    c.scales[which][p], c.codes[which][p] = np.inf, 128
+    out, lse = run(c, queries(c, 8), dim ** -0.5, max_len=max_len)
+    pos = 230 - news[0] + np.arange(news[0])
+    assert np.all(np.isnan(out[pos >= b * 16])) and np.all(np.isnan(lse[pos >= b * 16]))
+    assert np.all(np.isfinite(out[pos < b * 16]))
