@@ -541,7 +541,11 @@ __global__ void __launch_bounds__(Layout<D, NQ>::kThreads, 1) attn_prompt_kernel
             }
             float add;  // to the denominator
             // The probabilities about a reference, over the scores (which are in registers); their sum.
-            auto probabilities = [&](float mu) {
+            // About a new reference the exponents are rounded as its maximum was, so that none
+            // is above it; about the old one in a single step, whose difference from that (half
+            // a unit in the last place of the score) only matters where it is so large that the sum tells.
+            auto probabilities = [&](float mu, auto fresh) {
+                constexpr bool FRESH = decltype(fresh)::value;
                 float all = 0.f;
                 add = 0.f;
 #pragma unroll
@@ -550,13 +554,15 @@ __global__ void __launch_bounds__(Layout<D, NQ>::kThreads, 1) attn_prompt_kernel
 #pragma unroll
                     for (int b = 0; b < 2; ++b) {
                         const float4 k = t[2 * c + b];
-                        const float lv = k.y - mu;
-                        const uint64_t ks2 = pair(k.x, k.x), lv2 = pair(lv, lv);
+                        const float lv = FRESH ? k.y : k.y - mu;
+                        const uint64_t ks2 = pair(k.x, k.x), lv2 = pair(lv, lv), mu2 = pair(-mu, -mu);
                         uint64_t sum2[2] = {0, 0};
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             const float* y = &x[c][16 * b + 2 * i];
-                            float2 w = unpair(fma2(pair(y[0], y[1]), ks2, lv2));
+                            uint64_t w2 = fma2(pair(y[0], y[1]), ks2, lv2);
+                            if (FRESH) w2 = add2(w2, mu2);
+                            float2 w = unpair(w2);
                             w.x = ex2(w.x);
                             w.y = ex2(w.y);
                             if (MASK) {  // a hidden block may have any scale
@@ -577,7 +583,7 @@ __global__ void __launch_bounds__(Layout<D, NQ>::kThreads, 1) attn_prompt_kernel
             };
             // The reference holds for most tiles: their sum says so.  A row that has none yet, or
             // one that passes it too far (or is NaN), takes the warp through the maximum.
-            if (__all_sync(0xffffffffu, m != -INFINITY) && __all_sync(0xffffffffu, probabilities(m) <= kMostSum)) {
+            if (__all_sync(0xffffffffu, m != -INFINITY) && __all_sync(0xffffffffu, probabilities(m, std::false_type{}) <= kMostSum)) {
                 l += add;
                 return;
             }
@@ -609,7 +615,7 @@ __global__ void __launch_bounds__(Layout<D, NQ>::kThreads, 1) attn_prompt_kernel
                 l *= f;
             }
             m = to;
-            probabilities(to == -INFINITY ? 0.f : to);
+            probabilities(to == -INFINITY ? 0.f : to, std::true_type{});
             l += add;
         };
         for (int j = 0; j < nj; ++j) {

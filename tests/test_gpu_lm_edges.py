@@ -1,5 +1,6 @@
 """Calls at the edges of the cache, attention and log probabilities: lengths past the page table, positions next to
-2^31, windows of any size, scales of either sign and infinite ones."""
+2^31, windows of any size, scales of either sign and infinite ones,
+scores of any size."""
 import numpy as np
 import pytest
 
@@ -191,3 +192,30 @@ def test_an_infinite_key_or_value_is_seen(dim, news, which, max_len):
     pos = 230 - news[0] + np.arange(news[0])
     assert np.all(np.isnan(out[pos >= b * 16])) and np.all(np.isnan(lse[pos >= b * 16]))
     assert np.all(np.isfinite(out[pos < b * 16]))
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("news", [[1], [5], [150]])
+@pytest.mark.parametrize("size", [1e4, 6e4])
+def test_scores_of_any_size(dim, news, size):
+    # keys and queries at the end of FP16's range: nearly every row has one key that no rounding of the scores brings
+    # down to the next one, and its value is the result
+    c = Case(67, [150], news, 1, dim, 16)
+    c.scales[0][:] *= np.float32(1e4)
+    q = np.clip(queries(c, 2).astype(np.float64) * size, -65504, 65504).astype(np.float16)
+    want, want_lse, _ = attn_ref_rows(c, q, 1.0)
+    out, lse = run(c, q, 1.0)
+    assert np.all(np.isfinite(out))
+    assert np.all(np.abs(lse - want_lse) <= 1e-6 * np.abs(want_lse).max())
+    k, v = ([c.value(w, 0, j)[0] for j in range(150)] for w in (0, 1))
+    clear = 0
+    for t in range(c.T):
+        seen = 150 - c.T + t + 1
+        for h in range(2):
+            x = np.array(k[:seen]) @ q[t, h].astype(np.float64)
+            step = 2.0 ** -24 * (dim + 8) * (np.abs(k[:seen]) @ np.abs(q[t, h].astype(np.float64))).max()
+            best = int(x.argmax())
+            if np.sort(x)[-2:-1].max(initial=-np.inf) < x[best] - 4 * step - 40:
+                clear += 1
+                assert np.all(np.abs(out[t, h] - v[best]) <= 2.0 ** -10 * np.abs(v[best]))
+    assert clear >= 0.9 * 2 * c.T
