@@ -615,6 +615,7 @@ __global__ void __launch_bounds__(Layout<D, NQ>::kThreads, 1) attn_prompt_kernel
                 l *= f;
             }
             m = to;
+            tmem_wait_st();  // the first try's probabilities go to the same columns
             probabilities(to == -INFINITY ? 0.f : to, std::true_type{});
             l += add;
         };
