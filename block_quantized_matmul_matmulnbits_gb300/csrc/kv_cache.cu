@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kWarps * 32) kv_write_kernel(const KvIoArgs p)
             *dst = make_uint2(out[0], out[1]);
         }
     }
-    // only now: every lane has read the old scale (the reduction above)
+    __syncwarp();  // every lane has read the old scale
     if (lane == 0) *scale = s;
 }
 
