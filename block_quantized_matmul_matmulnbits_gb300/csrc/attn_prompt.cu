@@ -268,7 +268,6 @@ __global__ void __launch_bounds__(Layout<D, NQ>::kThreads, 1) attn_prompt_kernel
     unsigned int* status = P.status;
     extern __shared__ unsigned char smem_raw[];
     pdl_wait();
-    pdl_launch_dependents();
 
     // later tiles of a sequence see more keys: the long ones of every head start first
     const int head = blockIdx.x % a.b.kv_heads, split = blockIdx.y;
@@ -325,6 +324,10 @@ __global__ void __launch_bounds__(Layout<D, NQ>::kThreads, 1) attn_prompt_kernel
     fence_before();
     __syncthreads();
     fence_after();
+    // Only now may the next kernel start: the prefill matmul takes its tensor memory before it waits for
+    // this one, and must not take it from a CTA that has none yet.  (The registers of these CTAs leave
+    // no room for another beside them; this does not rest on that.)
+    pdl_launch_dependents();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sptr + (tmem_slot - base));
 
     if (warp >= kMmaWarp) {
