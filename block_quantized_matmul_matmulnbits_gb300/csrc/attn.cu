@@ -794,6 +794,18 @@ int attn_check(const mnb_kv_cache* c, const mnb_kv_batch* b, int q_heads, int wi
     return MNB_OK;
 }
 
+// The plan on a GPU of so many SMs (<= 0: the current one); without tokens all zeros.
+int attn_plan_for(const mnb_kv_cache* c, const mnb_kv_batch* b, int q_heads, int window, int sms, AttnPlan* p) {
+    bool empty;
+    int rc = attn_check(c, b, q_heads, window, &empty);
+    if (rc != MNB_OK) return rc;
+    *p = AttnPlan{};
+    if (empty) return MNB_OK;
+    unsigned int* status;
+    if (sms <= 0 && (rc = device_ready(&sms, &status)) != MNB_OK) return rc;
+    return attn_plan(c, b, q_heads, window, sms, p);
+}
+
 }  // namespace
 
 cudaError_t attn_prepare() {
@@ -812,16 +824,19 @@ cudaError_t attn_prepare() {
 
 extern "C" int64_t mnb_attn_workspace(const mnb_kv_cache* cache, const mnb_kv_batch* batch, int32_t q_heads,
                                       int32_t window, int32_t sm_count) {
-    bool empty;
-    int rc = mnb::attn_check(cache, batch, q_heads, window, &empty);
-    if (rc != MNB_OK) return rc;
-    if (empty) return 0;
-    int sms = sm_count;
-    unsigned int* status;
-    if (sms <= 0 && (rc = mnb::device_ready(&sms, &status)) != MNB_OK) return rc;
     mnb::AttnPlan p;
-    rc = mnb::attn_plan(cache, batch, q_heads, window, sms, &p);
+    const int rc = mnb::attn_plan_for(cache, batch, q_heads, window, sm_count, &p);
     return rc != MNB_OK ? rc : p.ws_bytes;
+}
+
+extern "C" int mnb_attn_plan(const mnb_kv_cache* cache, const mnb_kv_batch* batch, int32_t q_heads, int32_t window,
+                             int32_t sm_count, mnb_attn_plan_info* out) {
+    if (!out) return MNB_ERR_ARG;
+    mnb::AttnPlan p;
+    const int rc = mnb::attn_plan_for(cache, batch, q_heads, window, sm_count, &p);
+    if (rc != MNB_OK) return rc;
+    *out = {p.row_tiles * mnb::kPromptTile, p.split_rows, p.chunk, p.splits, p.cluster, p.by_length};
+    return MNB_OK;
 }
 
 extern "C" int mnb_attn(const mnb_kv_cache* cache, const mnb_kv_batch* batch, const void* Q, int64_t q_stride,

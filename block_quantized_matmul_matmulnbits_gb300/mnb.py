@@ -31,7 +31,7 @@ FLAG_EARLY_WEIGHTS = 1
 # Every symbol include/mnb.h declares (checked against the header by the tests).
 EXPORTS = ("mnb_create", "mnb_destroy", "mnb_run", "mnb_run_bias", "mnb_run_qlora", "mnb_run_multi", "mnb_transpose_dq_weight", "mnb_run_q8x", "mnb_quantize_x", "mnb_check_wait_timeout", "mnb_plan", "mnb_last_route", "mnb_sync_status",
            "mnb_status_str", "mnb_dequant", "mnb_lora_down", "mnb_run_noalloc", "mnb_noalloc_max_rows",
-           "mnb_kv_write", "mnb_kv_read", "mnb_attn", "mnb_attn_workspace", "mnb_logprobs")
+           "mnb_kv_write", "mnb_kv_read", "mnb_attn", "mnb_attn_workspace", "mnb_attn_plan", "mnb_logprobs")
 
 
 class MnbDesc(ctypes.Structure):
@@ -64,6 +64,14 @@ class MnbKvBatch(ctypes.Structure):
     _fields_ = [("seqs", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("tokens", ctypes.c_int64),
                 ("max_new", ctypes.c_int32), ("max_len", ctypes.c_int32), ("page_table", ctypes.c_void_p),
                 ("kv_len", ctypes.c_void_p), ("q_start", ctypes.c_void_p)]
+
+
+class MnbAttnPlanInfo(ctypes.Structure):
+    _fields_ = [("prompt_rows", ctypes.c_int32), ("split_rows", ctypes.c_int32), ("chunk", ctypes.c_int32),
+                ("splits", ctypes.c_int32), ("cluster", ctypes.c_int32), ("by_length", ctypes.c_int32)]
+
+    def as_dict(self):
+        return {name: getattr(self, name) for name, _ in self._fields_}
 
 
 class MnbError(RuntimeError):
@@ -131,6 +139,8 @@ def lib() -> ctypes.CDLL:
             L.mnb_attn.restype = ctypes.c_int
             L.mnb_attn_workspace.argtypes = [C, B, I32, I32, I32]
             L.mnb_attn_workspace.restype = I64
+            L.mnb_attn_plan.argtypes = [C, B, I32, I32, I32, ctypes.POINTER(MnbAttnPlanInfo)]
+            L.mnb_attn_plan.restype = ctypes.c_int
             L.mnb_logprobs.argtypes = [P, I64, I64, I64, F32, P, I32, P, P, P, P, P]
             L.mnb_logprobs.restype = ctypes.c_int
             _lib = L
@@ -399,6 +409,13 @@ def mnb_attn_workspace(cache: KVCache, batch: KVBatch, q_heads: int, window: int
     if n < 0:
         raise MnbError(n, "mnb_attn_workspace")
     return n
+
+
+def mnb_attn_plan(cache: KVCache, batch: KVBatch, q_heads: int, window: int = 0, sm_count: int = 0) -> dict:
+    """How mnb_attn deals out these sizes: rows of a CTA of its two kernels, keys of a CTA, CTAs of a tile."""
+    info = MnbAttnPlanInfo()
+    _check(lib().mnb_attn_plan(cache.ref, batch.ref, q_heads, window, sm_count, ctypes.byref(info)), "mnb_attn_plan")
+    return info.as_dict()
 
 
 def attn_workspace(cache: KVCache, batch: KVBatch, q_heads: int, window: int = 0):

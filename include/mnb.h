@@ -448,6 +448,23 @@ int mnb_attn(const mnb_kv_cache* cache, const mnb_kv_batch* batch, const void* Q
 int64_t mnb_attn_workspace(const mnb_kv_cache* cache, const mnb_kv_batch* batch, int32_t q_heads, int32_t window,
                            int32_t sm_count);
 
+/* How mnb_attn deals out a call (host only). */
+typedef struct {
+    int32_t prompt_rows; /* query rows (tokens x heads of a kv head) of a CTA of the kernel for
+                            prompts, 128 or 256; 0: not launched */
+    int32_t split_rows;  /* query rows of a CTA of the kernel for few rows, 8 or 16; 0: not
+                            launched.  Where both are, it takes the sequences with no more */
+    int32_t chunk;       /* keys of a CTA ... */
+    int32_t splits;      /* ... and CTAs that share a tile's keys; the last takes what is left */
+    int32_t cluster;     /* 1: those CTAs join their results in a cluster, without workspace */
+    int32_t by_length;   /* 1: the longest sequences' CTAs start first */
+} mnb_attn_plan_info;
+
+/* The plan of mnb_attn for these sizes on a GPU with `sm_count` SMs (sm_count <= 0: the current
+ * device).  A call without tokens launches nothing: all zeros. */
+int mnb_attn_plan(const mnb_kv_cache* cache, const mnb_kv_batch* batch, int32_t q_heads, int32_t window,
+                  int32_t sm_count, mnb_attn_plan_info* out);
+
 /* What is taken from a row of logits: the log probability of a given token,
  * the entropy, and the most likely tokens.  With x = scale * logit (scale > 0,
  * the reciprocal of a temperature) and lse = log sum exp(x) over the row:

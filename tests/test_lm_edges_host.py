@@ -5,6 +5,7 @@ import pytest
 
 from test_abi_host import run_without_gpu
 from test_lm_ops_host import A, batch, cache
+import prompt_cases
 
 from block_quantized_matmul_matmulnbits_gb300 import build as mnb_build
 from block_quantized_matmul_matmulnbits_gb300 import mnb
@@ -30,3 +31,35 @@ def child_attn_scale():
 
 def test_attention_refuses_scales_that_are_not_finite():
     run_without_gpu(child_attn_scale)
+
+
+# What tests/test_gpu_prompt_tiles.py and others rely on: which kernel, with how many row tiles and chunks, takes a case.
+def plan(dim, kv_heads, group, lens, news, page=32, window=0, max_len=None, sms=152):
+    c = cache(page_size=page, kv_heads=kv_heads, head_dim=dim)
+    b = batch(seqs=len(lens), tokens=sum(news), max_new=max(news), max_len=max_len or max(lens))
+    info = mnb.MnbAttnPlanInfo()
+    rc = mnb.lib().mnb_attn_plan(ctypes.byref(c), ctypes.byref(b), kv_heads * group, window, sms, ctypes.byref(info))
+    assert rc == mnb.MNB_OK
+    return info.as_dict()
+
+
+def test_the_plan_and_the_workspace():
+    assert plan(64, 3, 3, [577], [1]) == dict(prompt_rows=0, split_rows=8, chunk=128, splits=5, cluster=1, by_length=0)
+    p = plan(128, 8, 4, [131071], [1])
+    assert p["split_rows"] == 8 and p["splits"] > 8 and not p["cluster"]
+    b = batch(seqs=1, tokens=1, max_new=1, max_len=131071)
+    c = cache(page_size=32, kv_heads=8, head_dim=128)
+    assert mnb.lib().mnb_attn_workspace(ctypes.byref(c), ctypes.byref(b), 32, 0, 152) == 32 * p["splits"] * 130 * 4
+    assert plan(64, 1, 1, [5], [0]) == dict.fromkeys(p, 0)  # nothing to launch
+    info = mnb.MnbAttnPlanInfo()
+    L = mnb.lib()
+    assert L.mnb_attn_plan(None, ctypes.byref(b), 4, 0, 152, ctypes.byref(info)) == mnb.MNB_ERR_ARG
+    assert L.mnb_attn_plan(ctypes.byref(c), ctypes.byref(b), 32, 0, 152, None) == mnb.MNB_ERR_ARG
+    assert L.mnb_attn_plan(ctypes.byref(c), ctypes.byref(b), 12, 0, 152, ctypes.byref(info)) == mnb.MNB_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("case", prompt_cases.CASES, ids=lambda c: c.name)
+@pytest.mark.parametrize("dim", [64, 128])
+def test_cases_of_the_prompt_kernel_keep_their_plan(case, dim):
+    p = plan(dim, case.kv_heads, case.group, case.lens, case.news, window=case.window, max_len=case.max_len)
+    assert (p["prompt_rows"], p["splits"] > 1, p["split_rows"] > 0) == (case.rows, case.chunks, case.singles), p
