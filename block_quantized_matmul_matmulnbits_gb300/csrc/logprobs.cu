@@ -28,6 +28,12 @@
 // so what follows the last logit (the k-th largest bit by bit, the second look, the
 // ranks) is not hidden by another row's loads; more CTAs a row, that would hide it,
 // cost more than that in fixed work (two a row: 41 us).
+//
+// With a scale so large that a place of FP32 below 65504 c is worth more than half a unit, the
+// reference cannot be told apart from its neighbours (from 2^31 on the largest term alone would be
+// 2^64 or more).  There the reference is a logit, one that was seen, and y = (x - r) c:
+// two roundings a logit instead of one, and no distance kept (36.2 us in the case above; the
+// first form with the largest scale it takes 33.6).
 #include <cuda_fp16.h>
 
 #include "common.cuh"
@@ -45,6 +51,7 @@ constexpr int kList = 512;              // candidates of a CTA
 constexpr int kMaxVocab = 1 << 24;
 constexpr int kUnroll = 3;              // pieces of a group; two groups in registers
 constexpr float kMove = 4.f;
+constexpr float kMostScale = 256.f;     // c of the first form: half a place below 65504 * 256 is 1/2
 
 constexpr float kLn2f = 0.693147180559945309417f;
 
@@ -85,22 +92,22 @@ __device__ __forceinline__ unsigned long long key_of(uint32_t order, uint32_t id
     return ((unsigned long long)order << 32) | (uint32_t)~id;
 }
 
-struct Stat {  // sums about the reference r (in units of log2)
+struct Stat {  // sums about the reference r (times `unit`: in units of log2)
     float r, z, y;
 };
 
 // The same sums about another reference, not below r.  One of -infinity comes with sums of
 // 0 (or NaN) and has no shift of its own.
-__device__ __forceinline__ Stat about(const Stat& s, float r) {
-    const float d = fmaxf(s.r - (r == -INFINITY ? 0.f : r), -1000.f), f = ex2f(d);
+__device__ __forceinline__ Stat about(const Stat& s, float r, float unit) {
+    const float d = fmaxf((s.r - (r == -INFINITY ? 0.f : r)) * unit, -1000.f), f = ex2f(d);
     return {r, s.z * f, f * fmaf(s.z, d, s.y)};
 }
 
-__device__ __forceinline__ Stat warp_join(Stat s) {
+__device__ __forceinline__ Stat warp_join(Stat s, float unit) {
     float r = s.r;
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) r = fmaxf(r, __shfl_xor_sync(0xffffffffu, r, x));
-    s = about(s, r);
+    s = about(s, r, unit);
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) {
         s.z += __shfl_xor_sync(0xffffffffu, s.z, x);
@@ -152,6 +159,12 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     return r;
 }
 
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
 __device__ __forceinline__ __half2 as_half2(uint32_t x) { return *reinterpret_cast<const __half2*>(&x); }
 
 __device__ __forceinline__ __half2 max_of(const uint4& q) {
@@ -170,7 +183,8 @@ __device__ __forceinline__ uint4 ld_stream(const void* p) {  // once, from memor
 }
 
 // The running sums and the largest logits of one thread, a group of up to kUnroll pieces
-// at a time.
+// at a time.  FINE: the reference is a logit and c its unit; else it is in units of log2.
+template <bool FINE>
 struct Look {
     float r = -INFINITY;                // reference
     uint64_t z2 = 0, y2 = 0, ref2 = 0;  // both sums in two halves; (-r, -r), 0 while r is -infinity
@@ -188,10 +202,10 @@ struct Look {
         second = fmaxf(second, fminf(best, x));
         at = x > best ? v : at;
         best = fmaxf(best, x);
-        const float top = x * c;
-        if (top > r + kMove) {  // never for a NaN
-            const float to = top + kMove;
-            const float d = fmaxf(r - to, -1000.f), f = ex2f(d);
+        const float top = FINE ? x : x * c;
+        if (top > (FINE ? r : r + kMove)) {  // never for a NaN
+            const float to = FINE ? top : top + kMove;
+            const float d = fmaxf(FINE ? (r - to) * c : r - to, -1000.f), f = ex2f(d);
             const float2 zz = unpair(z2), yy = unpair(y2);
             z2 = pair(zz.x * f, zz.y * f);
             y2 = pair(f * fmaf(zz.x, d, yy.x), f * fmaf(zz.y, d, yy.y));
@@ -201,7 +215,7 @@ struct Look {
         // 0 times -infinity has to stay 0.  Where FP16's lowest value adds nothing (2^-160 of
         // the reference), -infinity is replaced by it, two logits at a time; else the
         // exponents are held at -200 one by one.
-        if (r >= fmaf(-65504.f, c, 160.f))
+        if (!FINE && r >= fmaf(-65504.f, c, 160.f))
             sum<false>(q, c2);
         else
             sum<true>(q, c2);
@@ -216,7 +230,7 @@ struct Look {
             for (int j = 0; j < 4; ++j) {
                 const __half2 h = LOW ? as_half2(w[j]) : __hmax2_nan(as_half2(w[j]), as_half2(0xFBFFFBFFu));
                 const float2 f = __half22float2(h);
-                float2 y = unpair(fma2(pair(f.x, f.y), c2, ref2));
+                float2 y = unpair(FINE ? mul2(add2(pair(f.x, f.y), ref2), c2) : fma2(pair(f.x, f.y), c2, ref2));
                 if (LOW) y = make_float2(max_nan(y.x, -200.f), max_nan(y.y, -200.f));
                 const uint64_t e = pair(ex2f(y.x), ex2f(y.y));
                 z2 = add2(z2, e);
@@ -226,6 +240,7 @@ struct Look {
     }
 };
 
+template <bool FINE>
 __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LpArgs a) {
     __shared__ LpShared sh;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -269,7 +284,8 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LpArgs a) {
     };
 
     // ---- one look at the slice
-    Look look;
+    Look<FINE> look;
+    const float unit = FINE ? a.c : 1.f;
     const uint64_t c2 = pair(a.c, a.c);
     bool any = f0 + tid < f1;  // this thread has a piece
     // the ragged pieces: the slice's first belongs to thread 0 too, its last to thread 1
@@ -314,14 +330,14 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LpArgs a) {
 
     const float2 zs = unpair(look.z2), ys = unpair(look.y2);
     Stat ws = {look.r, zs.x + zs.y, ys.x + ys.y};
-    ws = warp_join(ws);
+    ws = warp_join(ws, unit);
     if (lane == 0) sh.warp_stat[warp] = ws;
     if (tid < kMaxTop) sh.top[tid] = 0;
     __syncthreads();
     if (warp == 0) {
         Stat s = {-INFINITY, 0.f, 0.f};
         if (lane < kWarpCount) s = sh.warp_stat[lane];
-        s = warp_join(s);
+        s = warp_join(s, unit);
         if (lane == 0) sh.stats[0] = s;
     }
 
@@ -425,11 +441,14 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LpArgs a) {
         const int nk = a.cluster * a.top;
         Stat s = {-INFINITY, 0.f, 0.f};
         if (lane < a.cluster) s = sh.stats[lane];
-        s = warp_join(s);
+        s = warp_join(s, unit);
         const bool none = s.z == 0.f && s.r == -INFINITY;
         const float logz = log2f(s.z);
         const float bad = s.z != s.z || s.z == INFINITY ? __int_as_float(0x7fffffff) : 0.f;
-        auto logp = [&](float x) { return none ? -INFINITY : (fmaf(x, a.c, -s.r) - logz) * kLn2f + bad; };
+        auto logp = [&](float x) {
+            const float y = FINE ? (x - s.r) * a.c : fmaf(x, a.c, -s.r);
+            return none ? -INFINITY : (y - logz) * kLn2f + bad;
+        };
         for (int i = tid; i < nk; i += kThreads) {
             // every list is sorted: its keys above k are found by halving, all lists at once
             const unsigned long long k = sh.merged[i];
@@ -482,7 +501,7 @@ extern "C" int mnb_logprobs(const void* logits, int64_t rows, int64_t vocab, int
                             const int64_t* target, int32_t top, float* logprob, float* entropy, int32_t* top_ids,
                             float* top_logprobs, void* stream) {
     using namespace mnb;
-    if (rows < 0 || vocab < 1 || row_stride < vocab || top < 0 || top > vocab || !(scale > 0.f) || scale > 3e38f)
+    if (rows < 0 || vocab < 1 || row_stride < vocab || top < 0 || top > vocab || !(scale > 0.f) || scale > 2e38f)
         return MNB_ERR_ARG;
     if (vocab > kMaxVocab || top > kMaxTop || rows > INT32_MAX / kMaxCluster) return MNB_ERR_UNSUPPORTED;
     if (rows == 0) return MNB_OK;
@@ -520,5 +539,6 @@ extern "C" int mnb_logprobs(const void* logits, int64_t rows, int64_t vocab, int
     at[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, logprobs_kernel, a) == cudaSuccess ? MNB_OK : MNB_ERR_CUDA;
+    const auto kernel = a.c > kMostScale ? logprobs_kernel<true> : logprobs_kernel<false>;
+    return cudaLaunchKernelEx(&cfg, kernel, a) == cudaSuccess ? MNB_OK : MNB_ERR_CUDA;
 }

@@ -466,8 +466,8 @@ int mnb_attn_plan(const mnb_kv_cache* cache, const mnb_kv_batch* batch, int32_t 
                   int32_t sm_count, mnb_attn_plan_info* out);
 
 /* What is taken from a row of logits: the log probability of a given token,
- * the entropy, and the most likely tokens.  With x = scale * logit (scale > 0,
- * the reciprocal of a temperature) and lse = log sum exp(x) over the row:
+ * the entropy, and the most likely tokens.  With x = scale * logit (scale > 0
+ * and at most 2e38, the reciprocal of a temperature) and lse = log sum exp(x) over the row:
  *   logits        fp16, row r at logits + r * row_stride, [vocab] each; any
  *                 vocab of 1 .. 2^24 and any row_stride >= vocab
  *   target        int64 [rows] or NULL; a target outside [0, vocab) stands for

@@ -4,7 +4,7 @@ import ctypes
 import pytest
 
 from test_abi_host import run_without_gpu
-from test_lm_ops_host import A, batch, cache
+from test_lm_ops_host import A, batch, cache, logprobs
 import prompt_cases
 
 from block_quantized_matmul_matmulnbits_gb300 import build as mnb_build
@@ -31,6 +31,18 @@ def child_attn_scale():
 
 def test_attention_refuses_scales_that_are_not_finite():
     run_without_gpu(child_attn_scale)
+
+
+
+def child_logprobs_scale():
+    for scale in (2.1e38, 3e38, 3.4e38, -0.0):
+        assert logprobs(scale=scale) == mnb.MNB_ERR_ARG, scale
+    for scale in (2e38, 1e-40):
+        assert logprobs(scale=scale) == mnb.MNB_ERR_NO_DEVICE, scale
+
+
+def test_log_probabilities_refuse_scales_past_binary32():
+    run_without_gpu(child_logprobs_scale)
 
 
 # What tests/test_gpu_prompt_tiles.py and others rely on: which kernel, with how many row tiles and chunks, takes a case.
