@@ -353,13 +353,13 @@ class KVBatch:
         self.ref = ctypes.byref(self.desc)
 
 
-_half = None  # torch.float16, once torch is there
+_half = _fp32 = _int32 = _int64 = None  # torch's types, once torch is there
 
 
 def _fp16():
-    global _half
+    global _half, _fp32, _int32, _int64
     import torch
-    _half = torch.float16
+    _half, _fp32, _int32, _int64 = torch.float16, torch.float32, torch.int32, torch.int64
     return _half
 
 
@@ -383,8 +383,8 @@ def _kv_rows(cache, batch, K, V) -> int:
     return stride
 
 
-def _filled(x, nbytes: int) -> bool:
-    return x.nbytes == nbytes and x.is_contiguous()
+def _filled(x, count: int, dtype) -> bool:
+    return x.dtype is dtype and x.numel() == count and x.is_contiguous()
 
 
 def mnb_kv_write(cache: KVCache, batch: KVBatch, K, V, stream=None) -> None:
@@ -434,7 +434,7 @@ def mnb_attn(cache: KVCache, batch: KVBatch, Q, out, scale: Optional[float] = No
     q_heads = shape[1] if len(shape) == 3 else shape[1] // dim
     stride = _rows(Q, shape, Q.stride(), q_heads, dim, batch.tokens, "Q")
     out_stride = _rows(out, out.shape, out.stride(), q_heads, dim, batch.tokens, "out")
-    if lse is not None and not _filled(lse, 4 * batch.tokens * q_heads):
+    if lse is not None and not _filled(lse, batch.tokens * q_heads, _fp32):
         raise ValueError("lse: float32 [tokens, q_heads]")
     rc = (_lib or lib()).mnb_attn(cache.ref, batch.ref, Q.data_ptr(), stride, q_heads,
                                   dim ** -0.5 if scale is None else scale, window, out.data_ptr(), out_stride,
@@ -452,10 +452,11 @@ def mnb_logprobs(logits, target=None, logprob=None, entropy=None, top_ids=None, 
     rows, vocab = logits.shape
     _want(logits.dtype is (_half or _fp16()) and (logits.stride(1) == 1 or vocab == 1), "logits: fp16 [rows, vocab]")
     k = 0 if top_ids is None else top_ids.shape[1]
-    if not ((target is None or _filled(target, 8 * rows)) and (logprob is None or _filled(logprob, 4 * rows)) and
-            (entropy is None or _filled(entropy, 4 * rows)) and
-            (top_ids is None or _filled(top_ids, 4 * rows * k)) and
-            (top_logprobs is None or _filled(top_logprobs, 4 * rows * k))):
+    if not ((target is None or _filled(target, rows, _int64)) and
+            (logprob is None or _filled(logprob, rows, _fp32)) and
+            (entropy is None or _filled(entropy, rows, _fp32)) and
+            (top_ids is None or _filled(top_ids, rows * k, _int32)) and
+            (top_logprobs is None or _filled(top_logprobs, rows * k, _fp32))):
         raise ValueError("target: int64 [rows]; logprob, entropy: float32 [rows]; top_ids int32, top_logprobs float32 "
                          "[rows, k]; all contiguous")
     stride = logits.stride(0) if rows > 1 else max(logits.stride(0), vocab)

@@ -45,6 +45,37 @@ def test_log_probabilities_refuse_scales_past_binary32():
     run_without_gpu(child_logprobs_scale)
 
 
+
+@pytest.mark.parametrize("name,dtype,shape", [("target", "float64", (3,)), ("target", "int32", (3, 2)),
+                                              ("logprob", "int32", (3,)), ("logprob", "float16", (3, 2)),
+                                              ("entropy", "int32", (3,)), ("top_ids", "float32", (3, 2)),
+                                              ("top_ids", "int64", (3, 1)), ("top_logprobs", "int32", (3, 2))])
+def test_the_binding_checks_types_of_the_same_size(name, dtype, shape):
+    torch = pytest.importorskip("torch")
+    given = dict(target=torch.zeros(3, dtype=torch.int64), logprob=torch.zeros(3), entropy=torch.zeros(3),
+                 top_ids=torch.zeros(3, 2, dtype=torch.int32), top_logprobs=torch.zeros(3, 2))
+    if name == "top_ids" and dtype == "int64":
+        given["top_logprobs"] = torch.zeros(3, 1)
+    given[name] = torch.zeros(*shape, dtype=getattr(torch, dtype))
+    with pytest.raises(ValueError):
+        mnb.mnb_logprobs(torch.zeros(3, 9, dtype=torch.float16), **given, stream=0)
+
+
+def host_cache(torch, heads=2, dim=64):
+    codes, scales = torch.zeros(4, heads, 32, dim, dtype=torch.uint8), torch.zeros(4, heads, 2)
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
+    return mnb.KVCache(codes, codes.clone(), scales, scales.clone()), mnb.KVBatch(i32(2, 3), i32(2), i32(3), 4, 2, 50)
+
+
+@pytest.mark.parametrize("dtype,shape", [("int32", (4, 4)), ("float16", (4, 8)), ("float64", (4, 2))])
+def test_the_binding_checks_the_type_of_the_sums(dtype, shape):
+    torch = pytest.importorskip("torch")
+    c, b = host_cache(torch)
+    q = torch.zeros(4, 4, 64, dtype=torch.float16)
+    with pytest.raises(ValueError):
+        mnb.mnb_attn(c, b, q, q.clone(), lse=torch.zeros(*shape, dtype=getattr(torch, dtype)), stream=0)
+
+
 # What tests/test_gpu_prompt_tiles.py and others rely on: which kernel, with how many row tiles and chunks, takes a case.
 def plan(dim, kv_heads, group, lens, news, page=32, window=0, max_len=None, sms=152):
     c = cache(page_size=page, kv_heads=kv_heads, head_dim=dim)
