@@ -372,14 +372,15 @@ def _rows(x, shape, s, heads: int, dim: int, tokens: int, what: str) -> int:
         ok = len(shape) == 2 and shape[1] == heads * dim and s[1] == 1
     if not ok or shape[0] != tokens or x.dtype is not (_half or _fp16()):
         raise ValueError(f"{what}: fp16 [tokens, heads, head_dim], whole rows")
-    return s[0] if tokens > 1 else max(s[0], heads * dim)
+    return s[0] if tokens > 1 else heads * dim  # a single row has no stride
 
 
 def _kv_rows(cache, batch, K, V) -> int:
     shape, s = K.shape, K.stride()
     stride = _rows(K, shape, s, cache.kv_heads, cache.head_dim, batch.tokens, "K")
-    if V.shape != shape or V.stride() != s or V.dtype is not _half:
-        raise ValueError("V: shape, strides and type of K")
+    if V.shape != shape or V.dtype is not _half or (V.stride() != s and stride != _rows(
+            V, V.shape, V.stride(), cache.kv_heads, cache.head_dim, batch.tokens, "V")):
+        raise ValueError("V: shape, row stride and type of K")
     return stride
 
 

@@ -1,6 +1,6 @@
 """Calls at the edges of the cache, attention and log probabilities: lengths past the page table, positions next to
 2^31, windows of any size, scales of either sign and infinite ones,
-scores of any size."""
+scores of any size, single rows of any stride."""
 import numpy as np
 import pytest
 
@@ -219,3 +219,29 @@ def test_scores_of_any_size(dim, news, size):
                 clear += 1
                 assert np.all(np.abs(out[t, h] - v[best]) <= 2.0 ** -10 * np.abs(v[best]))
     assert clear >= 0.9 * 2 * c.T
+
+
+# ---- single rows
+
+def test_a_single_row_has_no_stride():
+    # a row of a matrix whose rows are not 16 bytes apart, keys and values from different ones
+    c = Case(69, [40], [1], 2, 64, 16)
+    k, v = tokens(c, 7)
+    want = write_ref(c, k, v)
+    q = queries(c, 4)
+    cache, batch = c.upload(torch, mnb)
+    wide = lambda a, n: torch.zeros(1, n, dtype=torch.float16, device="cuda")[:, :a.size].copy_(  # noqa: E731
+        torch.from_numpy(a).cuda().view(1, -1))
+    mnb.mnb_kv_write(cache, batch, wide(k, 131), wide(v, 133))
+    c.codes, c.scales = want
+    back = [torch.zeros(1, n, dtype=torch.float16, device="cuda")[:, :128] for n in (141, 143)]
+    mnb.mnb_kv_read(cache, batch, *back)
+    out = torch.zeros(1, 259, dtype=torch.float16, device="cuda")[:, :256]
+    mnb.mnb_attn(cache, batch, wide(q, 261), out)
+    torch.cuda.synchronize()
+    np.testing.assert_array_equal(cache.K.cpu().numpy(), want[0][0])
+    np.testing.assert_array_equal(cache.V.cpu().numpy(), want[0][1])
+    for w in (0, 1):
+        np.testing.assert_array_equal(back[w].cpu().numpy().reshape(1, 2, 64), read_ref(c)[w])
+    want_out, _, tol = attn_ref_rows(c, q, 0.125)
+    assert np.all(np.abs(out.float().cpu().numpy().reshape(1, 4, 64) - want_out) <= tol)
