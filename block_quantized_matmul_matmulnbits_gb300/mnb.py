@@ -318,6 +318,9 @@ class KVCache:
               tuple(K_scales.shape) == tuple(V_scales.shape) == (pages, heads, page // KV_BLOCK),
               "K_scales and V_scales: float32 [num_pages, kv_heads, page_size // 16]")
         _want(all(t.is_contiguous() for t in (K, V, K_scales, V_scales)), "the cache's tensors have to be contiguous")
+        self.device = K.get_device()  # -1: host tensors, which no call takes
+        _want(self.device == V.get_device() == K_scales.get_device() == V_scales.get_device(),
+              "the cache's tensors have to be on one device")
         self.K, self.V, self.K_scales, self.V_scales = K, V, K_scales, V_scales
         self.num_pages, self.page_size, self.kv_heads, self.head_dim = pages, page, heads, dim
         self.desc = MnbKvCache(pages, page, heads, dim, 0, K.data_ptr(), V.data_ptr(), K_scales.data_ptr(),
@@ -346,6 +349,9 @@ class KVBatch:
               "page_table, kv_len and q_start: contiguous int32")
         _want(page_table.dim() == 2 and page_table.shape[0] == seqs and tuple(q_start.shape) == (seqs + 1,),
               "page_table [seqs, max_pages], kv_len [seqs], q_start [seqs + 1]")
+        self.device = kv_len.get_device()
+        _want(self.device == page_table.get_device() == q_start.get_device(),
+              "page_table, kv_len and q_start have to be on one device")
         self.page_table, self.kv_len, self.q_start = page_table, kv_len, q_start
         self.seqs, self.tokens, self.max_new, self.max_len = seqs, tokens, max_new, max_len
         self.desc = MnbKvBatch(seqs, page_table.shape[1], tokens, max_new, max_len, page_table.data_ptr(),
@@ -366,11 +372,8 @@ def _fp16():
 def _rows(x, shape, s, heads: int, dim: int, tokens: int, what: str) -> int:
     """Row stride of a token tensor x of this shape and these strides, [tokens, heads, dim] or [tokens, heads * dim]
     (rows may be strided)."""
-    if len(shape) == 3:
-        ok = shape[1] == heads and shape[2] == dim and s[2] == 1 and (s[1] == dim or heads == 1)
-    else:
-        ok = len(shape) == 2 and shape[1] == heads * dim and s[1] == 1
-    if not ok or shape[0] != tokens or x.dtype is not (_half or _fp16()):
+    if not (shape == (tokens, heads, dim) and s[2] == 1 and (s[1] == dim or heads == 1) or
+            shape == (tokens, heads * dim) and s[1] == 1) or x.dtype is not (_half or _fp16()):
         raise ValueError(f"{what}: fp16 [tokens, heads, head_dim], whole rows")
     return s[0] if tokens > 1 else heads * dim  # a single row has no stride
 
@@ -381,11 +384,17 @@ def _kv_rows(cache, batch, K, V) -> int:
     if V.shape != shape or V.dtype is not _half or (V.stride() != s and stride != _rows(
             V, V.shape, V.stride(), cache.kv_heads, cache.head_dim, batch.tokens, "V")):
         raise ValueError("V: shape, row stride and type of K")
+    if not 0 <= cache.device == batch.device == K.get_device() == V.get_device():
+        raise _not_there("K, V")
     return stride
 
 
 def _filled(x, count: int, dtype) -> bool:
     return x.dtype is dtype and x.numel() == count and x.is_contiguous()
+
+
+def _not_there(what: str) -> MnbError:
+    return MnbError(MNB_ERR_ARG, f"{what}: every tensor has to be on the same GPU")
 
 
 def mnb_kv_write(cache: KVCache, batch: KVBatch, K, V, stream=None) -> None:
@@ -437,6 +446,10 @@ def mnb_attn(cache: KVCache, batch: KVBatch, Q, out, scale: Optional[float] = No
     out_stride = _rows(out, out.shape, out.stride(), q_heads, dim, batch.tokens, "out")
     if lse is not None and not _filled(lse, batch.tokens * q_heads, _fp32):
         raise ValueError("lse: float32 [tokens, q_heads]")
+    if not (0 <= cache.device == batch.device == Q.get_device() == out.get_device() and
+            (lse is None or lse.get_device() == cache.device) and
+            (ws is None or (ws.get_device() == cache.device and ws.is_contiguous()))):
+        raise _not_there("mnb_attn")
     rc = (_lib or lib()).mnb_attn(cache.ref, batch.ref, Q.data_ptr(), stride, q_heads,
                                   dim ** -0.5 if scale is None else scale, window, out.data_ptr(), out_stride,
                                   None if lse is None else lse.data_ptr(), None if ws is None else ws.data_ptr(),
@@ -460,7 +473,14 @@ def mnb_logprobs(logits, target=None, logprob=None, entropy=None, top_ids=None, 
             (top_logprobs is None or _filled(top_logprobs, rows * k, _fp32))):
         raise ValueError("target: int64 [rows]; logprob, entropy: float32 [rows]; top_ids int32, top_logprobs float32 "
                          "[rows, k]; all contiguous")
-    stride = logits.stride(0) if rows > 1 else max(logits.stride(0), vocab)
+    device = logits.get_device()
+    if not (device >= 0 and (target is None or target.get_device() == device) and
+            (logprob is None or logprob.get_device() == device) and
+            (entropy is None or entropy.get_device() == device) and
+            (top_ids is None or top_ids.get_device() == device) and
+            (top_logprobs is None or top_logprobs.get_device() == device)):
+        raise _not_there("mnb_logprobs")
+    stride = logits.stride(0) if rows > 1 else vocab
     rc = (_lib or lib()).mnb_logprobs(logits.data_ptr(), rows, vocab, stride, scale, _ptr(target), k, _ptr(logprob),
                                       _ptr(entropy), _ptr(top_ids), _ptr(top_logprobs),
                                       _current_stream() if stream is None else _stream(stream))

@@ -76,6 +76,47 @@ def test_the_binding_checks_the_type_of_the_sums(dtype, shape):
         mnb.mnb_attn(c, b, q, q.clone(), lse=torch.zeros(*shape, dtype=getattr(torch, dtype)), stream=0)
 
 
+
+def refused(call):
+    with pytest.raises(mnb.MnbError) as e:
+        call()
+    return e.value.code == mnb.MNB_ERR_ARG and "on the same GPU" in str(e.value)
+
+
+def test_host_tensors_never_reach_a_kernel():
+    torch = pytest.importorskip("torch")
+    c, b = host_cache(torch)
+    kv, q = torch.zeros(4, 2, 64, dtype=torch.float16), torch.zeros(4, 4, 64, dtype=torch.float16)
+    for fn in (mnb.mnb_kv_write, mnb.mnb_kv_read):
+        assert refused(lambda: fn(c, b, kv, kv.clone(), stream=0))
+    assert refused(lambda: mnb.mnb_attn(c, b, q, q.clone(), stream=0))
+    assert refused(lambda: mnb.mnb_logprobs(torch.zeros(2, 9, dtype=torch.float16), entropy=torch.zeros(2), stream=0))
+
+
+@pytest.mark.gpu
+def test_tensors_of_two_places_never_reach_a_kernel():
+    torch = pytest.importorskip("torch")
+    host, _ = host_cache(torch)
+    on = lambda x: x.cuda()  # noqa: E731
+    codes = [on(x) for x in (host.K, host.V, host.K_scales, host.V_scales)]
+    with pytest.raises(ValueError):
+        mnb.KVCache(*codes[:3], host.V_scales)
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32, device="cuda")  # noqa: E731
+    with pytest.raises(ValueError):
+        mnb.KVBatch(i32(2, 3), i32(2), i32(3).cpu(), 4, 2, 50)
+    c, b = mnb.KVCache(*codes), mnb.KVBatch(i32(2, 3), i32(2), i32(3), 4, 2, 50)
+    kv, q = (torch.zeros(4, h, 64, dtype=torch.float16, device="cuda") for h in (2, 4))
+    lse, ws = torch.zeros(4, 4, device="cuda"), torch.zeros(4096, dtype=torch.uint8, device="cuda")
+    for fn in (mnb.mnb_kv_write, mnb.mnb_kv_read):
+        assert refused(lambda: fn(c, b, kv.cpu(), kv)) and refused(lambda: fn(c, b, kv, kv.cpu()))
+        assert refused(lambda: fn(host, b, kv, kv.clone()))
+    for bad in (dict(Q=q.cpu()), dict(out=q.cpu()), dict(lse=lse.cpu()), dict(ws=ws.cpu()), dict(ws=ws[:1].expand(4096))):
+        assert refused(lambda: mnb.mnb_attn(c, b, **{**dict(Q=q, out=q.clone(), lse=lse, ws=ws), **bad})), bad
+    x, t = torch.zeros(2, 9, dtype=torch.float16, device="cuda"), torch.zeros(2, dtype=torch.int64)
+    assert refused(lambda: mnb.mnb_logprobs(x, t, lse[0, :2].contiguous()))
+    assert refused(lambda: mnb.mnb_logprobs(x, entropy=torch.zeros(2)))
+
+
 # What tests/test_gpu_prompt_tiles.py and others rely on: which kernel, with how many row tiles and chunks, takes a case.
 def plan(dim, kv_heads, group, lens, news, page=32, window=0, max_len=None, sms=152):
     c = cache(page_size=page, kv_heads=kv_heads, head_dim=dim)
