@@ -4,11 +4,12 @@
 // One thread-block cluster takes a row, each of its CTAs a slice, each thread
 // every 256th 16-byte piece of it, straight from memory into registers, in groups of
 // three pieces of which the next is on its way (32.7 us in the case below; four a group 34.3, two 35.2).  Every thread keeps sum 2^y and sum 2^y y of y = x c - r,
-// c = scale log2(e), with a reference r of its own: any r near the row's
-// maximum serves, so it is set 2^4 above the largest value seen and moved only when a
-// value passes it by 2^4 (what the entropy's difference of two terms can lose to
-// it stays at a few roundings of 1), and the threads' sums are brought to a
-// common one at the end:
+// c = scale log2(e), with a reference r of its own: the largest value seen, which moves only when
+// a value passes it by 2^5.75.  Any r near the row's maximum serves the sums, but the entropy is a
+// difference of two terms, each as far from it as r from the maximum: with the maximum itself, which a
+// row with one likely token has for r, it loses nothing (a reference 2^4 above the
+// maximum: four times the error over 30 such rows).  The threads' sums are brought to a
+// common reference at the end:
 //     lse = ln 2 (M + log2 Z),   entropy = ln 2 (log2 Z - (sum 2^y y) / Z).
 // A thread's fixed work (joining, selecting) costs as much as about 100 logits,
 // so a row gets no more CTAs than the GPU needs to be full.
@@ -50,7 +51,7 @@ constexpr int kMaxCluster = 8;
 constexpr int kList = 512;              // candidates of a CTA
 constexpr int kMaxVocab = 1 << 24;
 constexpr int kUnroll = 3;              // pieces of a group; two groups in registers
-constexpr float kMove = 4.f;
+constexpr float kMove = 5.75f;          // 4 in natural units
 constexpr float kMostScale = 256.f;     // c of the first form: half a place below 65504 * 256 is 1/2
 
 constexpr float kLn2f = 0.693147180559945309417f;
@@ -204,7 +205,7 @@ struct Look {
         best = fmaxf(best, x);
         const float top = FINE ? x : x * c;
         if (top > (FINE ? r : r + kMove)) {  // never for a NaN
-            const float to = FINE ? top : top + kMove;
+            const float to = top;
             const float d = fmaxf(FINE ? (r - to) * c : r - to, -1000.f), f = ex2f(d);
             const float2 zz = unpair(z2), yy = unpair(y2);
             z2 = pair(zz.x * f, zz.y * f);

@@ -1,5 +1,5 @@
 """mnb_logprobs with scales from the largest binary32 takes down to a hundredth: the definition in 64 bits on
-differences of logits, whose size does not matter then."""
+differences of logits, whose size does not matter then.  And what the sums lose where one token is likely."""
 import numpy as np
 import pytest
 
@@ -34,3 +34,16 @@ def test_scales_of_any_size(scale):
                 assert got < -2.3e38, (i, got, want)
             else:
                 assert abs(got - want) <= EPS + 2.0 ** -22 * abs(want), (i, got, want)
+
+
+def test_the_entropy_of_rows_with_one_likely_token():
+    # log Z and the mean of y are about zero then: what is left are the roundings of a sum near 1, at most 12 a thread
+    # and 11 of the joins, 2^-23 / sqrt(12) each
+    r = np.random.default_rng(10)
+    x = (r.standard_normal((40, 49152)) * 2).astype(np.float16)
+    x[np.arange(40), r.integers(0, 49152, 40)] = r.uniform(16, 19, 40).astype(np.float16)
+    h = run(torch.from_numpy(x).cuda(), scale=1.0)[1].astype(np.float64)
+    y = x.astype(np.float64)
+    y -= np.log(np.exp(y).sum(1))[:, None]
+    want = -(np.exp(y) * y).sum(1)
+    assert np.sqrt(((h - want) ** 2).mean()) <= 23 ** 0.5 * 2.0 ** -23 / 12 ** 0.5
