@@ -3,13 +3,15 @@
 // Per query row, with codes k_jd, v_jd (exact integers after subtracting 128)
 // and one scale a block of 16 tokens:
 //     s_j = scale * ks_b * sum_d q_d k_jd,     o = sum_j e^(s_j - m) vs_b v_j / sum_j e^(s_j - m)
-// in one pass over the keys with a running maximum.
+// in one pass over the keys with a running reference.
 //
 //  * The value scale goes into the exponent: w_j = s_j log2(e) + log2(vs_b), and
-//    the running maximum is that of w.  The second product's left operand is then
-//    2^(w_j - max w) <= 1 whatever the value scales are, so its FP16 rounding
-//    (2^-11 of each term) never meets FP16's subnormals at the large end; the
-//    denominator takes each block's sum times 1 / vs_b, in binary32.
+//    the reference m is a row's maximum of w as of the last time that mattered: it moves
+//    when a lane's part of 32 keys (of 128 in the prompt kernel a row's) sums up to more than
+//    2^15.  The second product's operand is then 2^(w_j - m) <= 2^15 whatever the value scales
+//    are, and rounded to FP16: 2^-11 of each term, and for terms more than 2^14 below the reference,
+//    which are subnormal, 2^-25 of it.  The denominator takes each block's sum times 1 / vs_b,
+//    in binary32.
 //  * Both products take the codes exactly, with binary32 accumulation (mma.sync
 //    m16n8k16).  The first one's are fed as FP16 subnormals q 2^-24 (one byte permute for
 //    two codes), the offset 128 sum_d q_d taken off the accumulator before it starts;
@@ -31,7 +33,7 @@
 // operand reads are free of bank conflicts.
 //
 // Bound by memory, head_dim + 4 / 16 bytes a key, twice: one sequence of 131,071 keys and 8 kv heads
-// of 128 takes 49.5 us, 5.5 TB/s.  64 uneven sequences of up to 8,192 take 65 us, 5.0 TB/s: at
+// of 128 takes 49.5 us, 5.4 TB/s.  64 uneven sequences of up to 8,192 take 65 us, 5.0 TB/s: at
 // their end few CTAs have work left.  (Chunks of equal work over all sequences ended
 // together and took 67: each CTA has more to look up and to join.)  Short calls wait for
 // their loads one behind the other (lengths, page, scales and codes, then the join): 577 keys

@@ -26,7 +26,7 @@
 // Both row tiles share the unpacked keys and values.
 //
 // Bound by the tensor core, 4 d operations a query row and key: 1.09 PFLOP/s at a prompt of 4,096
-// tokens behind 4,096 and one of 395 behind 182, 32 query heads on 8 kv heads of 128 (382 us).
+// tokens behind 4,096 and one of 395 behind 182, 32 query heads on 8 kv heads of 128 (379 us).
 // What stands between: a row tile's scores cannot be made before the product that reads the
 // probabilities over them has ended (some 300 cycles each time that nothing else is queued),
 // the softmax of 128 x 128 scores takes 1,200 cycles where the two row tiles share the

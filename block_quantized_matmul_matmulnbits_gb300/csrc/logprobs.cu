@@ -3,12 +3,13 @@
 //
 // One thread-block cluster takes a row, each of its CTAs a slice, each thread
 // every 256th 16-byte piece of it, straight from memory into registers, in groups of
-// three pieces of which the next is on its way (32.7 us in the case below; four a group 34.3, two 35.2).  Every thread keeps sum 2^y and sum 2^y y of y = x c - r,
+// three pieces of which the next is on its way (32.7 us in the case below when this was chosen, four a
+// group 34.3, two 35.2).  Every thread keeps sum 2^y and sum 2^y y of y = x c - r,
 // c = scale log2(e), with a reference r of its own: the largest value seen, which moves only when
-// a value passes it by 2^5.75.  Any r near the row's maximum serves the sums, but the entropy is a
+// a value passes it by 5.75 (moving at once, 33.5 us; by 8, 32.7).  Any r near the row's maximum serves the sums, but the entropy is a
 // difference of two terms, each as far from it as r from the maximum: with the maximum itself, which a
-// row with one likely token has for r, it loses nothing (a reference 2^4 above the
-// maximum: four times the error over 30 such rows).  The threads' sums are brought to a
+// row with one likely token has for r, it loses nothing (with one 4 above
+// the maximum four times the error, over 40 such rows).  The threads' sums are brought to a
 // common reference at the end:
 //     lse = ln 2 (M + log2 Z),   entropy = ln 2 (log2 Z - (sum 2^y y) / Z).
 // A thread's fixed work (joining, selecting) costs as much as about 100 logits,
@@ -25,16 +26,16 @@
 // first CTA merges the lists that the others leave in its shared memory.
 //
 // Bound by memory: 2 bytes a logit, read once.  512 rows of 151,936 with the 20 most likely:
-// 32.7 us, 4.8 TB/s; without them 29.2 us, 5.3 TB/s.  All rows end at about the same time,
+// 33.1 us, 4.7 TB/s; without them 29.5 us, 5.3 TB/s.  All rows end at about the same time,
 // so what follows the last logit (the k-th largest bit by bit, the second look, the
 // ranks) is not hidden by another row's loads; more CTAs a row, that would hide it,
 // cost more than that in fixed work (two a row: 41 us).
 //
-// With a scale so large that a place of FP32 below 65504 c is worth more than half a unit, the
-// reference cannot be told apart from its neighbours (from 2^31 on the largest term alone would be
-// 2^64 or more).  There the reference is a logit, one that was seen, and y = (x - r) c:
-// two roundings a logit instead of one, and no distance kept (36.2 us in the case above; the
-// first form with the largest scale it takes 33.6).
+// With a scale so large that a place of FP32 at 65504 c is worth more than a unit, r = x c is no
+// longer the largest logit's (from 2^31 on that one's term could be 2^64 and more).  There the
+// reference is the logit itself and y = (x - r) c:
+// two roundings a logit instead of one, and no distance kept (35.8 us in the case above; the
+// first form with the largest scale it takes 33.0).
 #include <cuda_fp16.h>
 
 #include "common.cuh"
@@ -52,7 +53,7 @@ constexpr int kList = 512;              // candidates of a CTA
 constexpr int kMaxVocab = 1 << 24;
 constexpr int kUnroll = 3;              // pieces of a group; two groups in registers
 constexpr float kMove = 5.75f;          // 4 in natural units
-constexpr float kMostScale = 256.f;     // c of the first form: half a place below 65504 * 256 is 1/2
+constexpr float kMostScale = 256.f;     // c of the first form: a place of FP32 below 65504 * 256 is a unit
 
 constexpr float kLn2f = 0.693147180559945309417f;
 
