@@ -1,0 +1,252 @@
+// qk_rope.cu -- root-mean-square norms of query and key heads and their rotation by
+// position, in one pass (mnb_qk_rope).
+//
+//     x' = x w / sqrt(mean(x^2) + eps);   (a, b) -> (a cos - b sin, b cos + a sin),  angle = p f_i
+//
+// Eight values a thread (16 bytes), a head in 8 or 16 neighbouring threads: the mean square
+// is a few shuffles, and the other value of a pair is in the same thread (interleaved) or
+// one shuffle away, so a head is read and written once.  A thread keeps its place in the head
+// for all heads of a token, so cosines, sines and weights are multiplied once a token.
+//
+// The angle: far positions need more places than FP32 has (position 10^6 times
+// a frequency of 1: the FP32 product is off by 0.06 radians).  f / 2 pi is held as a 64-bit
+// fraction of a turn, and position times that, modulo 2^64, is the angle's turn: one integer
+// product, exact to 2^-32 turns at the largest position.
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "kv_batch.cuh"
+#include "mnb_internal.h"
+
+namespace mnb {
+
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kEach = 4;  // 16-byte pieces a thread has in flight
+
+struct RopeArgs {
+    KvArgs b;                  // q_start, kv_len, seqs, tokens (where positions is NULL)
+    const int32_t* positions;
+    const float* inv_freq;
+    const __half *q_weight, *k_weight;
+    float eps;
+    int tokens, q_heads, heads, rotary;  // heads: query and key heads
+    int interleaved;
+    const __half *q, *k;
+    __half *q_out, *k_out;
+    int64_t q_stride, k_stride, q_out_stride, k_out_stride;
+};
+
+// f / 2 pi as a fraction of a turn, times 2^64.
+__device__ __forceinline__ unsigned long long turn_of(float f) {
+    const double d = (double)f, hi = 0.15915494309189534561, lo = -9.839338337591243e-18;  // 1 / 2 pi
+    const double p = d * hi;
+    const double e = fma(d, hi, -p) + d * lo;
+    return __double2ull_rz((p - floor(p)) * 18446744073709551616.0) +
+           (unsigned long long)__double2ll_rn(e * 18446744073709551616.0);
+}
+
+// Position of token t, or -1.  The whole warp.
+__device__ __forceinline__ int position_of(const RopeArgs& a, int t) {
+    if (a.positions) return a.positions[t];
+    int64_t first;
+    const KvSeq s = kv_find_seq(a.b, t, KvSplit{1, 0, 0}, &first);
+    const int i = t - s.row0;
+    return i >= 0 && i < s.n ? s.len - s.n + i : -1;
+}
+
+template <int D, bool NORM>
+__global__ void __launch_bounds__(kThreads) qk_rope_kernel(const RopeArgs a) {
+    constexpr int LPH = D / 8, STEP = kThreads / LPH;  // threads of a head, heads at once
+    __shared__ float2 turn[2][D / 2];                  // cosine and sine of a token's pairs
+    const int tid = threadIdx.x, j = tid % LPH, h0 = tid / LPH;
+    const int half = a.rotary >> 1, lanes = a.rotary >> 4;  // pairs; threads of half of the turned values
+    pdl_wait();
+    pdl_launch_dependents();
+    const unsigned long long r = tid < half ? turn_of(a.inv_freq[tid]) : 0;
+    const bool turned = j * 8 < a.rotary, second = !a.interleaved && j >= lanes;
+    // the thread that holds the other values of this one's pairs
+    const int other = (tid & 31) + (a.interleaved || !turned ? 0 : second ? -lanes : lanes);
+    const int pair0 = a.interleaved ? j * 4 : (second ? j - lanes : j) * 8;
+    uint4 gain[2][2] = {};  // weights of the thread's values and of the others, of queries and of keys
+    if (NORM) {
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            const __half* g = w ? a.k_weight : a.q_weight;
+            if (!g) continue;
+            gain[w][0] = *reinterpret_cast<const uint4*>(g + j * 8);
+            const int oj = j + other - (tid & 31);
+            gain[w][1] = *reinterpret_cast<const uint4*>(g + oj * 8);
+        }
+    }
+    int buf = 0;
+    for (int t = blockIdx.x; t < a.tokens; t += gridDim.x) {
+        const __half* q = a.q + (int64_t)t * a.q_stride + j * 8;
+        const __half* k = a.k + (int64_t)t * a.k_stride + j * 8;
+        const int pos = position_of(a, t);  // the same in all warps
+        if (pos < 0) continue;
+        if (tid < half) {
+            const int x = (int)(((unsigned long long)(unsigned)pos * r) >> 32);
+            float s, c;
+            sincospif((float)x * 4.656612873077392578125e-10f, &s, &c);  // x 2^-31: half turns
+            turn[buf][tid] = make_float2(c, s);
+        }
+        __syncthreads();
+        float c[8], s[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            c[i] = 1.f;
+            s[i] = 0.f;
+        }
+        if (turned) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float2 cs = turn[buf][pair0 + (a.interleaved ? i >> 1 : i)];
+                c[i] = cs.x;
+                s[i] = (a.interleaved ? (i & 1) : second) ? cs.y : -cs.y;
+            }
+        }
+        buf ^= 1;  // the next token's table, which no thread reads before all are done with this one's
+        for (int h = h0; h < ((a.heads + STEP - 1) / STEP) * STEP; h += STEP * kEach) {
+            uint4 x[kEach];
+#pragma unroll
+            for (int u = 0; u < kEach; ++u) {
+                const int hh = h + u * STEP;
+                x[u] = make_uint4(0, 0, 0, 0);
+                if (hh < a.heads)
+                    x[u] = *reinterpret_cast<const uint4*>(hh < a.q_heads ? q + hh * D : k + (hh - a.q_heads) * D);
+            }
+#pragma unroll
+            for (int u = 0; u < kEach; ++u) {
+                const int hh = h + u * STEP;
+                const bool key = hh >= a.q_heads;
+                uint4 y;  // the other values of the pairs
+                if (a.interleaved) {
+                    y = make_uint4(prmt(x[u].x, 0, 0x1032), prmt(x[u].y, 0, 0x1032), prmt(x[u].z, 0, 0x1032),
+                                   prmt(x[u].w, 0, 0x1032));
+                } else {
+                    y.x = __shfl_sync(0xffffffffu, x[u].x, other);
+                    y.y = __shfl_sync(0xffffffffu, x[u].y, other);
+                    y.z = __shfl_sync(0xffffffffu, x[u].z, other);
+                    y.w = __shfl_sync(0xffffffffu, x[u].w, other);
+                }
+                if (!turned) y = make_uint4(0, 0, 0, 0);  // not an infinity times 0
+                float v[8], o[8];
+                const __half2* xp = reinterpret_cast<const __half2*>(&x[u]);
+                const __half2* yp = reinterpret_cast<const __half2*>(&y);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 f = __half22float2(xp[i]), g = __half22float2(yp[i]);
+                    v[2 * i] = f.x, v[2 * i + 1] = f.y;
+                    o[2 * i] = g.x, o[2 * i + 1] = g.y;
+                }
+                float rms = 1.f;
+                if (NORM) {
+                    float sum = 0.f;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) sum = fmaf(v[i], v[i], sum);
+#pragma unroll
+                    for (int m = LPH / 2; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+                    if (key ? a.k_weight != nullptr : a.q_weight != nullptr) {
+                        rms = rsqrtf(fmaf(sum, 1.f / D, a.eps));
+                        const uint4 g0 = key ? gain[1][0] : gain[0][0], g1 = key ? gain[1][1] : gain[0][1];
+                        const __half2* gp = reinterpret_cast<const __half2*>(&g0);
+                        const __half2* op = reinterpret_cast<const __half2*>(&g1);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float2 f = __half22float2(gp[i]);
+                            const float2 g = a.interleaved ? make_float2(f.y, f.x) : __half22float2(op[i]);
+                            v[2 * i] *= f.x, v[2 * i + 1] *= f.y;
+                            o[2 * i] *= g.x, o[2 * i + 1] *= g.y;
+                        }
+                    }
+                }
+                if (hh >= a.heads) continue;
+                uint32_t out[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float lo = rms * fmaf(v[2 * i], c[2 * i], o[2 * i] * s[2 * i]);
+                    const float hi = rms * fmaf(v[2 * i + 1], c[2 * i + 1], o[2 * i + 1] * s[2 * i + 1]);
+                    const __half2 p = __floats2half2_rn(lo, hi);
+                    out[i] = *reinterpret_cast<const uint32_t*>(&p);
+                }
+                __half* to = key ? a.k_out + (int64_t)t * a.k_out_stride + (hh - a.q_heads) * D
+                                 : a.q_out + (int64_t)t * a.q_out_stride + hh * D;
+                *reinterpret_cast<uint4*>(to + j * 8) = make_uint4(out[0], out[1], out[2], out[3]);
+            }
+        }
+    }
+}
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+}  // namespace
+
+}  // namespace mnb
+
+extern "C" int mnb_qk_rope(const mnb_rope* rope, const mnb_kv_batch* batch, const int32_t* positions, int64_t tokens,
+                           const void* Q, int64_t q_stride, int32_t q_heads, const void* K, int64_t k_stride,
+                           int32_t kv_heads, void* Q_out, int64_t q_out_stride, void* K_out, int64_t k_out_stride,
+                           void* stream) {
+    using namespace mnb;
+    if (!rope || tokens < 0 || q_heads < 0 || kv_heads < 0 || rope->rotary_dim < 0 ||
+        (rope->interleaved != 0 && rope->interleaved != 1) || !(rope->eps >= 0.f) || rope->eps > 3e38f ||
+        (batch && (batch->tokens != tokens || batch->seqs < 0)))
+        return MNB_ERR_ARG;
+    const int dim = rope->head_dim;
+    if (dim != 64 && dim != 128) return MNB_ERR_UNSUPPORTED;
+    if (rope->rotary_dim > dim) return MNB_ERR_ARG;
+    if (rope->rotary_dim % 16 != 0 || tokens > INT32_MAX || q_heads > 65536 - kv_heads) return MNB_ERR_UNSUPPORTED;
+    if ((q_heads && (q_stride < (int64_t)q_heads * dim || q_out_stride < (int64_t)q_heads * dim)) ||
+        (kv_heads && (k_stride < (int64_t)kv_heads * dim || k_out_stride < (int64_t)kv_heads * dim)))
+        return MNB_ERR_ARG;
+    if ((q_heads && (q_stride % 8 != 0 || q_out_stride % 8 != 0)) ||
+        (kv_heads && (k_stride % 8 != 0 || k_out_stride % 8 != 0)))
+        return MNB_ERR_ALIGN;
+    if (tokens == 0 || q_heads + kv_heads == 0 || (batch && batch->seqs == 0)) return MNB_OK;
+    if ((q_heads && (!Q || !Q_out)) || (kv_heads && (!K || !K_out)) || (rope->rotary_dim && !rope->inv_freq) ||
+        (batch ? !batch->kv_len || !batch->q_start : !positions))
+        return MNB_ERR_ARG;
+    if ((q_heads && (!aligned(Q, 16) || !aligned(Q_out, 16))) || (kv_heads && (!aligned(K, 16) || !aligned(K_out, 16))) ||
+        !aligned(rope->q_weight, 16) || !aligned(rope->k_weight, 16) || !aligned(rope->inv_freq, 4) ||
+        (batch ? !aligned(batch->kv_len, 4) || !aligned(batch->q_start, 4) : !aligned(positions, 4)))
+        return MNB_ERR_ALIGN;
+    int sms;
+    unsigned int* status;
+    const int rc = device_ready(&sms, &status);
+    if (rc != MNB_OK) return rc;
+    RopeArgs a = {};
+    if (batch) {
+        a.b.kv_len = batch->kv_len;
+        a.b.q_start = batch->q_start;
+        a.b.seqs = batch->seqs;
+        a.b.tokens = (int)tokens;
+    } else {
+        a.positions = positions;
+    }
+    a.inv_freq = rope->inv_freq;
+    a.q_weight = static_cast<const __half*>(rope->q_weight);
+    a.k_weight = static_cast<const __half*>(rope->k_weight);
+    a.eps = rope->eps;
+    a.tokens = (int)tokens;
+    a.q_heads = q_heads;
+    a.heads = q_heads + kv_heads;
+    a.rotary = rope->rotary_dim;
+    a.interleaved = rope->interleaved;
+    a.q = static_cast<const __half*>(Q);
+    a.k = static_cast<const __half*>(K);
+    a.q_out = static_cast<__half*>(Q_out);
+    a.k_out = static_cast<__half*>(K_out);
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.q_out_stride = q_out_stride;
+    a.k_out_stride = k_out_stride;
+    const int64_t most = (int64_t)sms * 16;
+    const dim3 grid((unsigned)(tokens < most ? tokens : most)), block(kThreads);
+    const bool norm = a.q_weight || a.k_weight;
+    const auto kernel = dim == 64 ? (norm ? qk_rope_kernel<64, true> : qk_rope_kernel<64, false>)
+                                  : (norm ? qk_rope_kernel<128, true> : qk_rope_kernel<128, false>);
+    return launch_pdl(kernel, grid, block, 0, reinterpret_cast<cudaStream_t>(stream), a) == cudaSuccess ? MNB_OK
+                                                                                                        : MNB_ERR_CUDA;
+}

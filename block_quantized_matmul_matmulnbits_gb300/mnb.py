@@ -31,7 +31,8 @@ FLAG_EARLY_WEIGHTS = 1
 # Every symbol include/mnb.h declares (checked against the header by the tests).
 EXPORTS = ("mnb_create", "mnb_destroy", "mnb_run", "mnb_run_bias", "mnb_run_qlora", "mnb_run_multi", "mnb_transpose_dq_weight", "mnb_run_q8x", "mnb_quantize_x", "mnb_check_wait_timeout", "mnb_plan", "mnb_last_route", "mnb_sync_status",
            "mnb_status_str", "mnb_dequant", "mnb_lora_down", "mnb_run_noalloc", "mnb_noalloc_max_rows",
-           "mnb_kv_write", "mnb_kv_read", "mnb_attn", "mnb_attn_workspace", "mnb_attn_plan", "mnb_logprobs")
+           "mnb_kv_write", "mnb_kv_read", "mnb_attn", "mnb_attn_workspace", "mnb_attn_plan", "mnb_logprobs",
+           "mnb_qk_rope", "mnb_moe", "mnb_moe_workspace", "mnb_sample")
 
 
 class MnbDesc(ctypes.Structure):
@@ -72,6 +73,20 @@ class MnbAttnPlanInfo(ctypes.Structure):
 
     def as_dict(self):
         return {name: getattr(self, name) for name, _ in self._fields_}
+
+
+class MnbRope(ctypes.Structure):
+    _fields_ = [("head_dim", ctypes.c_int32), ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("inv_freq", ctypes.c_void_p), ("q_weight", ctypes.c_void_p),
+                ("k_weight", ctypes.c_void_p)]
+
+
+class MnbMoeLayer(ctypes.Structure):
+    _fields_ = [("hidden", ctypes.c_int32), ("inter", ctypes.c_int32), ("experts", ctypes.c_int32),
+                ("top_k", ctypes.c_int32), ("bits", ctypes.c_int32), ("flags", ctypes.c_int32),
+                ("router", ctypes.c_void_p), ("up_Wq", ctypes.c_void_p), ("up_scales", ctypes.c_void_p),
+                ("up_zp", ctypes.c_void_p), ("down_Wq", ctypes.c_void_p), ("down_scales", ctypes.c_void_p),
+                ("down_zp", ctypes.c_void_p)]
 
 
 class MnbError(RuntimeError):
@@ -143,6 +158,14 @@ def lib() -> ctypes.CDLL:
             L.mnb_attn_plan.restype = ctypes.c_int
             L.mnb_logprobs.argtypes = [P, I64, I64, I64, F32, P, I32, P, P, P, P, P]
             L.mnb_logprobs.restype = ctypes.c_int
+            L.mnb_qk_rope.argtypes = [ctypes.POINTER(MnbRope), B, P, I64, P, I64, I32, P, I64, I32, P, I64, P, I64, P]
+            L.mnb_qk_rope.restype = ctypes.c_int
+            L.mnb_moe.argtypes = [ctypes.POINTER(MnbMoeLayer), P, I64, P, P, P, P, I64, P]
+            L.mnb_moe.restype = ctypes.c_int
+            L.mnb_moe_workspace.argtypes = [ctypes.POINTER(MnbMoeLayer), I64]
+            L.mnb_moe_workspace.restype = I64
+            L.mnb_sample.argtypes = [P, I64, I64, I64, P, P, P, P, P, P, P, P]
+            L.mnb_sample.restype = ctypes.c_int
             _lib = L
     return _lib
 
@@ -486,6 +509,158 @@ def mnb_logprobs(logits, target=None, logprob=None, entropy=None, top_ids=None, 
                                       _current_stream() if stream is None else _stream(stream))
     if rc:
         raise MnbError(rc, "mnb_logprobs")
+
+
+class Rope:
+    """How query and key heads are normed and turned (mnb_rope): inv_freq float32 [rotary_dim / 2] (None: norms
+    only), q_weight, k_weight fp16 [head_dim] or None; ``interleaved`` pairs neighbouring values.  The object keeps the
+    tensors alive."""
+
+    def __init__(self, head_dim: int, inv_freq=None, interleaved: bool = False, q_weight=None, k_weight=None,
+                 eps: float = 1e-6):
+        half = _fp16()
+        _want(inv_freq is None or (inv_freq.dtype is _fp32 and inv_freq.dim() == 1 and inv_freq.is_contiguous()),
+              "inv_freq: contiguous float32 [rotary_dim / 2]")
+        _want(all(w is None or (w.dtype is half and tuple(w.shape) == (head_dim,) and w.is_contiguous())
+                  for w in (q_weight, k_weight)), "q_weight, k_weight: contiguous fp16 [head_dim]")
+        self.kept = [t for t in (inv_freq, q_weight, k_weight) if t is not None]
+        devices = {t.get_device() for t in self.kept}
+        _want(len(devices) <= 1, "inv_freq, q_weight and k_weight have to be on one device")
+        self.device = devices.pop() if devices else None
+        self.head_dim = head_dim
+        self.desc = MnbRope(head_dim, 0 if inv_freq is None else 2 * inv_freq.numel(), 1 if interleaved else 0, eps,
+                            _ptr(inv_freq), _ptr(q_weight), _ptr(k_weight))
+        self.ref = ctypes.byref(self.desc)
+
+
+def _heads(x, out, tokens: int, dim: int, device: int, what: str):
+    """(address, stride, heads, address, stride) of token tensors, zeros without one."""
+    if x is None:
+        _want(out is None, f"{what}_out without {what}")
+        return None, 0, 0, None, 0
+    shape = x.shape
+    _want(len(shape) in (2, 3) and (len(shape) == 3 or shape[1] % dim == 0), f"{what}: [tokens, heads, head_dim]")
+    heads = shape[1] if len(shape) == 3 else shape[1] // dim
+    stride = _rows(x, shape, x.stride(), heads, dim, tokens, what)
+    if x.get_device() != device:
+        raise _not_there("mnb_qk_rope")
+    if out is None or out is x:
+        return x.data_ptr(), stride, heads, x.data_ptr(), stride
+    out_stride = _rows(out, out.shape, out.stride(), heads, dim, tokens, what + "_out")
+    if out.get_device() != device:
+        raise _not_there("mnb_qk_rope")
+    return x.data_ptr(), stride, heads, out.data_ptr(), out_stride
+
+
+def mnb_qk_rope(rope: Rope, where, Q, K=None, Q_out=None, K_out=None, stream=None) -> None:
+    """Norm and rotate heads by their tokens' positions: Q fp16 [tokens, q_heads, head_dim], K alike (either may be
+    None), into Q_out, K_out (None: in place).  ``where``: a KVBatch, or int32 positions [tokens] (negative: left
+    as they are)."""
+    device = where.device if isinstance(where, KVBatch) else where.get_device()
+    if device < 0 or (rope.device is not None and rope.device != device):
+        raise _not_there("mnb_qk_rope")
+    if isinstance(where, KVBatch):
+        batch, positions, tokens = where.ref, None, where.tokens
+    else:
+        _fp16()
+        _want(where.dtype is _int32 and where.dim() == 1 and where.is_contiguous(),
+              "positions: contiguous int32 [tokens]")
+        batch, positions, tokens = None, where.data_ptr(), where.shape[0]
+    q, qs, qh, qo, qos = _heads(Q, Q_out, tokens, rope.head_dim, device, "Q")
+    k, ks, kh, ko, kos = _heads(K, K_out, tokens, rope.head_dim, device, "K")
+    rc = (_lib or lib()).mnb_qk_rope(rope.ref, batch, positions, tokens, q, qs, qh, k, ks, kh, qo, qos, ko, kos,
+                                     _current_stream() if stream is None else _stream(stream))
+    if rc:
+        raise MnbError(rc, "mnb_qk_rope")
+
+
+class MoE:
+    """A mixture-of-experts layer (mnb_moe_layer) over the caller's tensors: router fp16 [experts, hidden]; up_Wq
+    uint8 [experts, 2 * inter, hidden / 32, 32 * bits / 8] (gate rows first), up_scales fp16 and up_zp uint8 or None
+    [experts, 2 * inter, hidden / 32]; down_* [experts, hidden, inter / 32, ...] alike.  The object keeps them alive."""
+
+    def __init__(self, router, up_Wq, up_scales, down_Wq, down_scales, top_k: int, bits: int = 4, up_zp=None,
+                 down_zp=None, normalize: bool = True):
+        import torch
+        half = _fp16()
+        _want(router.dim() == 2 and router.dtype is half, "router: fp16 [experts, hidden]")
+        experts, hidden = router.shape
+        _want(down_scales.dim() == 3, "down_scales: fp16 [experts, hidden, inter / 32]")
+        inter, byte = down_scales.shape[2] * 32, 4 * bits
+        for codes, scales, zp, rows, cols, what in ((up_Wq, up_scales, up_zp, 2 * inter, hidden, "up"),
+                                                    (down_Wq, down_scales, down_zp, hidden, inter, "down")):
+            shape = (experts, rows, cols // 32)
+            _want(codes.dtype is torch.uint8 and codes.numel() == experts * rows * (cols // 32) * byte and
+                  codes.shape[0] == experts and scales.dtype is half and tuple(scales.shape) == shape and
+                  (zp is None or (zp.dtype is torch.uint8 and tuple(zp.shape) == shape)),
+                  f"{what}_Wq uint8 [experts, rows, blocks, {byte}], {what}_scales fp16 and {what}_zp uint8 "
+                  "[experts, rows, blocks]")
+        self.kept = [t for t in (router, up_Wq, up_scales, up_zp, down_Wq, down_scales, down_zp) if t is not None]
+        _want(all(t.is_contiguous() for t in self.kept), "the layer's tensors have to be contiguous")
+        self.device = router.get_device()
+        _want(all(t.get_device() == self.device for t in self.kept), "the layer's tensors have to be on one device")
+        self.hidden, self.inter, self.experts, self.top_k, self.bits = hidden, inter, experts, top_k, bits
+        self.torch_device = router.device
+        self.desc = MnbMoeLayer(hidden, inter, experts, top_k, bits, 1 if normalize else 0, _ptr(router), _ptr(up_Wq),
+                                _ptr(up_scales), _ptr(up_zp), _ptr(down_Wq), _ptr(down_scales), _ptr(down_zp))
+        self.ref = ctypes.byref(self.desc)
+
+
+def mnb_moe_workspace(layer: MoE, tokens: int) -> int:
+    """Bytes of workspace mnb_moe needs for so many tokens."""
+    n = lib().mnb_moe_workspace(layer.ref, tokens)
+    if n < 0:
+        raise MnbError(n, "mnb_moe_workspace")
+    return n
+
+
+def moe_workspace(layer: MoE, tokens: int):
+    """A workspace tensor for mnb_moe."""
+    import torch
+    return torch.empty(mnb_moe_workspace(layer, tokens), dtype=torch.uint8, device=layer.torch_device)
+
+
+def mnb_moe(layer: MoE, X, Y, ids=None, weights=None, ws=None, stream=None) -> None:
+    """The layer for up to 16 tokens: X, Y fp16 [tokens, hidden], contiguous; the experts taken and their weights into
+    ids int32 and weights float32 [tokens, top_k] (or None).  ``ws``: moe_workspace(...)."""
+    _want(X.dim() == 2 and X.shape[1] == layer.hidden and X.dtype is _half and X.is_contiguous() and
+          Y.shape == X.shape and Y.dtype is _half and Y.is_contiguous(), "X, Y: contiguous fp16 [tokens, hidden]")
+    tokens, picks = X.shape[0], X.shape[0] * layer.top_k
+    _want((ids is None or _filled(ids, picks, _int32)) and (weights is None or _filled(weights, picks, _fp32)),
+          "ids: int32, weights: float32 [tokens, top_k]")
+    device = layer.device
+    if not (0 <= device == X.get_device() == Y.get_device() and (ids is None or ids.get_device() == device) and
+            (weights is None or weights.get_device() == device) and
+            (ws is None or (ws.get_device() == device and ws.is_contiguous()))):
+        raise _not_there("mnb_moe")
+    rc = (_lib or lib()).mnb_moe(layer.ref, X.data_ptr(), tokens, Y.data_ptr(), _ptr(ids), _ptr(weights), _ptr(ws),
+                                 0 if ws is None else ws.nbytes, _current_stream() if stream is None else _stream(stream))
+    if rc:
+        raise MnbError(rc, "mnb_moe")
+
+
+def mnb_sample(logits, u, token, logprob=None, temperature=None, top_k=None, top_p=None, min_p=None,
+               stream=None) -> None:
+    """Draw a token from each row of logits fp16 [rows, vocab] (rows may be strided) with the random numbers u (float32
+    [rows], 0 .. 1) into token (int64 [rows]) and the log of its probability into logprob (float32 [rows]).
+    temperature, top_p, min_p: float32 [rows], top_k: int32 [rows], or None; all are read on the device."""
+    rows, vocab = logits.shape
+    _want(logits.dtype is (_half or _fp16()) and (logits.stride(1) == 1 or vocab == 1), "logits: fp16 [rows, vocab]")
+    device = logits.get_device()
+    given = ((u, _fp32), (token, _int64), (logprob, _fp32), (temperature, _fp32), (top_k, _int32), (top_p, _fp32),
+             (min_p, _fp32))
+    for x, dtype in given:
+        if x is not None and not _filled(x, rows, dtype):
+            raise ValueError("u, logprob, temperature, top_p, min_p: float32, top_k: int32, token: int64; all "
+                             "contiguous [rows]")
+        if device < 0 or (x is not None and x.get_device() != device):
+            raise _not_there("mnb_sample")
+    stride = logits.stride(0) if rows > 1 else vocab
+    rc = (_lib or lib()).mnb_sample(logits.data_ptr(), rows, vocab, stride, u.data_ptr(), _ptr(temperature),
+                                    _ptr(top_k), _ptr(top_p), _ptr(min_p), token.data_ptr(), _ptr(logprob),
+                                    _current_stream() if stream is None else _stream(stream))
+    if rc:
+        raise MnbError(rc, "mnb_sample")
 
 
 class Projection:

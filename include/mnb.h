@@ -488,6 +488,133 @@ int mnb_logprobs(const void* logits, int64_t rows, int64_t vocab, int64_t row_st
                  const int64_t* target, int32_t top, float* logprob, float* entropy, int32_t* top_ids,
                  float* top_logprobs, void* stream);
 
+/* ---- around the projections of a decode step ----------------------------- */
+
+/* How query and key heads are normed and turned by their positions.
+ *   head_dim      64 or 128
+ *   rotary_dim    the first values of a head that are turned: 0 .. head_dim, a
+ *                 multiple of 16
+ *   interleaved   0: values i and i + rotary_dim / 2 make pair i; 1: 2i and 2i + 1
+ *   eps           added to the mean square, at least 0
+ *   inv_freq      float [rotary_dim / 2] (device), finite: pair i of a token at
+ *                 position p is turned by p * inv_freq[i] radians (NULL without pairs)
+ *   q_weight, k_weight   fp16 [head_dim] (device) or NULL: heads that have one
+ *                 are multiplied by weight / sqrt(mean(x^2) + eps) first */
+typedef struct {
+    int32_t head_dim;
+    int32_t rotary_dim;
+    int32_t interleaved;
+    float eps;
+    const float* inv_freq;
+    const void* q_weight;
+    const void* k_weight;
+} mnb_rope;
+
+/* Norm and rotate the call's query and key heads, between the projection that
+ * made them and mnb_kv_write / mnb_attn.
+ *   batch       the sequences: token i of sequence s has position
+ *               kv_len[s] - n + i, as in mnb_attn (its page table is not read); or NULL:
+ *   positions   int32 [tokens] (device), used where batch is NULL.  A row
+ *               with a negative position, and with a batch a row that no sequence owns,
+ *               is not read and its outputs are left as they are.
+ *   tokens      rows of Q and K (batch->tokens where there is a batch)
+ *   Q, K        fp16, row t at Q + t * q_stride, [q_heads, head_dim] (K alike);
+ *               heads may be 0, the pointers then NULL.  q_heads + kv_heads <= 65536
+ *   Q_out, K_out   the same with strides of their own; each may be its input
+ *               (in place) and overlaps nothing else of the call
+ * Strides are in elements, multiples of 8, at least heads * head_dim; the sums of
+ * squares are in binary32, the angle's turns are exact to 2^-32 at every position, one
+ * rounding to fp16 at the end.  Values from rotary_dim on are normed only.
+ * Errors: MNB_ERR_ARG, MNB_ERR_UNSUPPORTED (head_dim, rotary_dim not a multiple
+ * of 16, too many heads or tokens), MNB_ERR_ALIGN (rows and weights 16
+ * bytes, the others 4), MNB_ERR_NO_DEVICE, MNB_ERR_CUDA. */
+int mnb_qk_rope(const mnb_rope* rope, const mnb_kv_batch* batch, const int32_t* positions, int64_t tokens,
+                const void* Q, int64_t q_stride, int32_t q_heads, const void* K, int64_t k_stride, int32_t kv_heads,
+                void* Q_out, int64_t q_out_stride, void* K_out, int64_t k_out_stride, void* stream);
+
+/* A mixture-of-experts layer whose experts are gated MLPs of block-quantized
+ * weights (4 or 8 bits, blocks of 32 along the inputs, codes, scales and zero points
+ * as in mnb_run, one expert behind the other):
+ *   logit_e = x . router[e],  S = the top_k largest (equal ones by rising number)
+ *   w_e     = exp(logit_e) / sum over S (MNB_MOE_NORMALIZE) or over all experts
+ *   y       = sum over S of w_e * down_e (silu(gate_e x) * (up_e x))
+ *   hidden       inputs and outputs of the layer, a multiple of 32, at most 32768
+ *   inter        width of an expert, a multiple of 32, at most 65536
+ *   experts      1 .. 256;  top_k 1 .. 16, at most experts
+ *   router       fp16 [experts, hidden]
+ *   up_Wq        [experts, 2 * inter, hidden / 32, 32 * bits / 8] codes: rows 0 ..
+ *                inter - 1 of an expert are its gate, the others its up projection
+ *   up_scales    fp16 [experts, 2 * inter, hidden / 32]
+ *   up_zp        uint8, like up_scales, or NULL (2^(bits - 1))
+ *   down_*       [experts, hidden, inter / 32, ...] alike */
+#define MNB_MOE_NORMALIZE 1
+#define MNB_MOE_MAX_TOKENS 16
+typedef struct {
+    int32_t hidden;
+    int32_t inter;
+    int32_t experts;
+    int32_t top_k;
+    int32_t bits;
+    int32_t flags;
+    const void* router;
+    const void* up_Wq;
+    const void* up_scales;
+    const void* up_zp;
+    const void* down_Wq;
+    const void* down_scales;
+    const void* down_zp;
+} mnb_moe_layer;
+
+/* The layer for a few tokens (a decode step): each expert that some token takes is read
+ * once (twice beyond 8 tokens of one expert).
+ *   X        fp16 [M, hidden], M at most MNB_MOE_MAX_TOKENS
+ *   Y        fp16 [M, hidden]; not X
+ *   ids      int32 [M, top_k] or NULL: the experts taken, by falling logit
+ *   weights  float [M, top_k] or NULL: their w_e
+ *   ws       workspace of at least mnb_moe_workspace bytes, 16-byte aligned; it needs no
+ *            clearing and holds nothing between calls; calls that may overlap need one each
+ * Router logits are sums of exact products held to more than 64-bit floating point needs to
+ * tell two experts apart by 2^-40 of their terms; the expert sums are in binary32 with
+ * exact codes, the products silu(gate) * up enter the down projection in fp16 scaled by
+ * a power of two per 32.  Each token's result is independent of the others in the call.
+ * A token with NaN or infinity takes some valid experts and gives NaN or infinity.
+ * Deterministic.  Errors: MNB_ERR_ARG (also a workspace that is too small),
+ * MNB_ERR_UNSUPPORTED (sizes beyond the above, bits, M), MNB_ERR_ALIGN (16 bytes; zero
+ * points, ids and weights 4), MNB_ERR_NO_DEVICE, MNB_ERR_CUDA. */
+int mnb_moe(const mnb_moe_layer* layer, const void* X, int64_t M, void* Y, int32_t* ids, float* weights, void* ws,
+            int64_t ws_bytes, void* stream);
+
+/* Workspace bytes of mnb_moe for M tokens.  Host only; negative: an error code. */
+int64_t mnb_moe_workspace(const mnb_moe_layer* layer, int64_t M);
+
+/* Draw a token from each row of logits with given random numbers.  Of a row's
+ * tokens by falling logit, equal ones by rising id, with weights
+ * exp(logit / temperature):
+ *   top_k   the first top_k are kept,
+ *   top_p   of these the fewest whose weights reach top_p of theirs,
+ *   min_p   of these those of at least min_p times the largest;
+ * the token is the first of the kept, in that order, at which their cumulative
+ * weight passes u times their sum.
+ *   logits       fp16, row r at logits + r * row_stride, [vocab] each; any vocab
+ *                of 1 .. 2^24 and any row_stride >= vocab
+ *   u            float [rows]; numbers below 0 and NaN count as 0, from 1 on the last is taken
+ *   temperature  float [rows] or NULL (1); 0, below and NaN take the most likely token
+ *   top_k        int32 [rows] or NULL; 0 and below: no limit
+ *   top_p        float [rows] or NULL; 1, above and NaN: no limit; the first is always kept
+ *   min_p        float [rows] or NULL; 0, below and NaN: no limit; the first is always kept
+ *   token        int64 [rows]
+ *   logprob      float [rows] or NULL: log of its weight over the sum of the kept
+ * All are device arrays, read when the call runs: a captured call can be replayed
+ * with other settings.  Logits of -infinity are never drawn; a row of nothing else
+ * gives token -1 and logprob -infinity, a row with NaN or +infinity -1 and NaN.
+ * The token is the one that 64-bit sums choose, to 2^-40 of the weights, whatever the
+ * sizes and the other rows of the call.
+ * Errors: MNB_ERR_ARG, MNB_ERR_UNSUPPORTED (vocab, rows), MNB_ERR_ALIGN (logits
+ * 16 bytes, token 8, the others 4), MNB_ERR_NO_DEVICE, MNB_ERR_CUDA. */
+int mnb_sample(const void* logits, int64_t rows, int64_t vocab, int64_t row_stride, const float* u,
+               const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
+               int64_t* token, float* logprob, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
