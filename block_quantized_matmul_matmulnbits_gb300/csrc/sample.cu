@@ -29,7 +29,7 @@ namespace mnb {
 
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kMaxVocab = 1 << 24;
@@ -39,36 +39,40 @@ constexpr uint32_t kLowest = 0x0400;     // order of -65504, the lowest logit th
 constexpr uint32_t kInfinite = 0xFC00;   // order of +infinity; NaN lies above
 constexpr int kAll = INT32_MAX;          // no limit
 constexpr int kBeyond = kAll - 1;        // a limit somewhere below the window
+constexpr uint32_t kFull = 0xffffffffu;
+
+typedef unsigned long long u64;
 
 struct SampleArgs {
     const __half* logits;
     int64_t rows, row_stride;
     int vocab, cluster;
+    int places;  // binary places of a weight: vocab weights of 1 stay below 2^62
     const float *u, *temperature, *top_p, *min_p;
     const int32_t* top_k;
     int64_t* token;
     float* logprob;
 };
 
-// 2^(j / 64), j = -32 .. 32
-__constant__ double kRoots[65] = {
-    0x1.6a09e667f3bcdp-1, 0x1.6dfb23c651a2fp-1, 0x1.71f75e8ec5f74p-1, 0x1.75feb564267c9p-1,
-    0x1.7a11473eb0187p-1, 0x1.7e2f336cf4e62p-1, 0x1.82589994cce13p-1, 0x1.868d99b4492edp-1,
-    0x1.8ace5422aa0dbp-1, 0x1.8f1ae99157736p-1, 0x1.93737b0cdc5e5p-1, 0x1.97d829fde4e50p-1,
-    0x1.9c49182a3f090p-1, 0x1.a0c667b5de565p-1, 0x1.a5503b23e255dp-1, 0x1.a9e6b5579fdbfp-1,
-    0x1.ae89f995ad3adp-1, 0x1.b33a2b84f15fbp-1, 0x1.b7f76f2fb5e47p-1, 0x1.bcc1e904bc1d2p-1,
-    0x1.c199bdd85529cp-1, 0x1.c67f12e57d14bp-1, 0x1.cb720dcef9069p-1, 0x1.d072d4a07897cp-1,
-    0x1.d5818dcfba487p-1, 0x1.da9e603db3285p-1, 0x1.dfc97337b9b5fp-1, 0x1.e502ee78b3ff6p-1,
-    0x1.ea4afa2a490dap-1, 0x1.efa1bee615a27p-1, 0x1.f50765b6e4540p-1, 0x1.fa7c1819e90d8p-1,
-    0x1.0000000000000p+0, 0x1.02c9a3e778061p+0, 0x1.059b0d3158574p+0, 0x1.0874518759bc8p+0,
-    0x1.0b5586cf9890fp+0, 0x1.0e3ec32d3d1a2p+0, 0x1.11301d0125b51p+0, 0x1.1429aaea92de0p+0,
-    0x1.172b83c7d517bp+0, 0x1.1a35beb6fcb75p+0, 0x1.1d4873168b9aap+0, 0x1.2063b88628cd6p+0,
-    0x1.2387a6e756238p+0, 0x1.26b4565e27cddp+0, 0x1.29e9df51fdee1p+0, 0x1.2d285a6e4030bp+0,
-    0x1.306fe0a31b715p+0, 0x1.33c08b26416ffp+0, 0x1.371a7373aa9cbp+0, 0x1.3a7db34e59ff7p+0,
-    0x1.3dea64c123422p+0, 0x1.4160a21f72e2ap+0, 0x1.44e086061892dp+0, 0x1.486a2b5c13cd0p+0,
-    0x1.4bfdad5362a27p+0, 0x1.4f9b2769d2ca7p+0, 0x1.5342b569d4f82p+0, 0x1.56f4736b527dap+0,
-    0x1.5ab07dd485429p+0, 0x1.5e76f15ad2148p+0, 0x1.6247eb03a5585p+0, 0x1.6623882552225p+0,
-    0x1.6a09e667f3bcdp+0,
+// 2^(j / 64) 2^62, j = -32 .. 32
+__constant__ u64 kRoots[65] = {
+    0x2d413cccfe779921ull, 0x2dbf6478ca345de4ull, 0x2e3eebd1d8bee7baull, 0x2ebfd6ac84cf917full,
+    0x2f4228e7d6030db0ull, 0x2fc5e66d9e9cc421ull, 0x304b1332999c2516ull, 0x30d1b3368925d902ull,
+    0x3159ca845541b6b7ull, 0x31e35d322aee6c57ull, 0x326e6f619b8bc9e9ull, 0x32fb053fbc9c9f17ull,
+    0x3389230547e12039ull, 0x3418ccf6bbcac965ull, 0x34aa07647c4ab917ull, 0x353cd6aaf3fb7e88ull,
+    0x35d13f32b5a75abdull, 0x366745709e2bf5edull, 0x36feede5f6bc8dd5ull, 0x37983d209783a449ull,
+    0x383337bb0aa53844ull, 0x38cfe25cafa29694ull, 0x396e41b9df20d22aull, 0x3a0e5a940f12f71aull,
+    0x3ab031b9f7490e4cull, 0x3b53cc07b6650ae1ull, 0x3bf92e66f736bd73ull, 0x3ca05dcf167fec4eull,
+    0x3d495f454921b30bull, 0x3df437dcc2b44eeeull, 0x3ea0ecb6dc8a80cfull, 0x3f4f83033d21b05dull,
+    0x4000000000000000ull, 0x40b268f9de0183baull, 0x4166c34c5615d0ecull, 0x421d1461d66f2023ull,
+    0x42d561b3e6243d8aull, 0x438fb0cb4f468808ull, 0x444c0740496d4294ull, 0x450a6abaa4b77ecdull,
+    0x45cae0f1f545eb73ull, 0x468d6fadbf2dd4f3ull, 0x47521cc5a2e6a9e0ull, 0x4818ee218a3358eeull,
+    0x48e1e9b9d588e19bull, 0x49ad159789f37496ull, 0x4a7a77d47f7b84b1ull, 0x4b4a169b900c2d00ull,
+    0x4c1bf828c6dc54b8ull, 0x4cf022c9905bfd32ull, 0x4dc69cdceaa72a9cull, 0x4e9f6cd3967fdba8ull,
+    0x4f7a993048d088d7ull, 0x50582887dcb8a7e1ull, 0x513821818624b40cull, 0x521a8ad704f3404full,
+    0x52ff6b54d8a89c75ull, 0x53e6c9da74b29ab5ull, 0x54d0ad5a753e077cull, 0x55bd1cdad49f699cull,
+    0x56ac1f752150a563ull, 0x579dbc56b48521baull, 0x5891fac0e95612c8ull, 0x5988e20954889245ull,
+    0x5a827999fcef3242ull,
 };
 
 // FP16 bits as an unsigned value in the same order: -0 as +0, NaN the largest.
@@ -90,9 +94,14 @@ __device__ __forceinline__ float ex2f(float x) {
     return y;
 }
 
-// What a row's weights are taken with: 2^(c (logit - top)), c = log2(e) / temperature.
+// ---- weights --------------------------------------------------------------------
+//
+// A weight 2^(c (logit - top)), c = log2(e) / temperature, is an integer multiple of 2^-places: sums of them are
+// exact, whatever their order, and FP64 (two operations a clock and SM here) is not needed.
+
 struct Scale {
     float top, c, c_low;  // c in two words
+    int places;
 };
 
 // log2 of the weight of a logit, in two words.
@@ -104,27 +113,60 @@ __device__ __forceinline__ float2 power_of(const Scale& k, float logit) {
     return make_float2(p, __fmaf_rn(s, k.c, -p) + __fmaf_rn(s, k.c_low, __fmul_rn(e, k.c)));
 }
 
-// 2^(p.x + p.y) to 2^-40: 2^n times a root of two from a table times the exponential series of what is left
+// 2^(p.x + p.y) = m 2^(n - 60), to 2^-40: a root of two from the table times the exponential series of what is left
 // (at most ln 2 / 128), whose first term is kept in two words.
-__device__ __forceinline__ double exp2_of(float2 p) {
-    if (!(p.x > -1000.f)) return 0.0;
+struct Power {
+    u64 m;
+    int n;
+};
+__device__ __forceinline__ Power exp2_of(float2 p) {
     const float n = rintf(p.x), f = p.x - n;  // exact
     const float j = rintf(f * 64.f), g = __fmaf_rn(j, -0.015625f, f);  // exact
     const float h = __fmul_rn(g, 0.6931471824645996f);
-    const float l = __fmaf_rn(g, 0.6931471824645996f, -h) + __fmaf_rn(g, -1.9046542121259336e-09f, __fmul_rn(p.y, 0.6931471824645996f));
+    const float l = __fmaf_rn(g, 0.6931471824645996f, -h) +
+                    __fmaf_rn(g, -1.9046542121259336e-09f, __fmul_rn(p.y, 0.6931471824645996f));
     const float z = h + l;
     const float q = z * z * (0.5f + z * (0.16666667f + z * (0.041666668f + z * 0.008333334f)));
-    const double r = kRoots[(int)j + 32] * (1.0 + (double)h + (double)(l + q));
-    return r * __longlong_as_double((long long)((int)n + 1023) << 52);
+    const u64 x = (1ull << 62) + (u64)(__float2ll_rn(h * 0x1p62f) + __float2ll_rn((l + q) * 0x1p62f));
+    return {__umul64hi(kRoots[(int)j + 32], x), (int)n};
 }
 
-__device__ __forceinline__ double weight_of(const Scale& k, uint32_t order) {
-    return exp2_of(power_of(k, value_of(order)));
+__device__ __forceinline__ u64 weight_of(const Scale& k, uint32_t order) {
+    const float2 p = power_of(k, value_of(order));
+    if (!(p.x > -70.f)) return 0;
+    const Power w = exp2_of(p);
+    const int shift = 60 - k.places - w.n;
+    return shift > 62 ? 0 : shift > 0 ? (w.m + (1ull << (shift - 1))) >> shift : w.m;
 }
 
-// The lowest order of a window from `high` down.
-__device__ __forceinline__ uint32_t window_low(uint32_t high) {
-    return high >= kLowest + kBins ? high - (kBins - 1) : kLowest;
+// Whether a logit's weight is at least m times the largest's.
+__device__ __forceinline__ bool at_least(const Scale& k, uint32_t order, float m) {
+    const float2 p = power_of(k, value_of(order));
+    if (!(p.x > -200.f)) return false;
+    const Power w = exp2_of(p);
+    return (double)w.m * __longlong_as_double((long long)(w.n - 60 + 1023) << 52) >= (double)m;
+}
+
+// log2 of s 2^-places, to FP32's places and more: log2f, and one step of Newton's method about it.
+__device__ __forceinline__ double log2_of(u64 s, int places) {
+    const int lead = 63 - __clzll((long long)s);
+    const u64 m = lead >= 60 ? s >> (lead - 60) : s << (60 - lead);  // in [2^60, 2^61)
+    const float y = log2f((float)m * 0x1p-60f);
+    const Power w = exp2_of(make_float2(y, 0.f));
+    const long long d = (long long)(m - (w.n > 0 ? w.m << 1 : w.m));
+    return (double)(lead - places) + (double)y + (double)((float)d / (float)m * 1.44269504f);
+}
+
+// floor or ceiling of f s for a factor in [0, 1).
+__device__ __forceinline__ u64 times(float f, u64 s, bool up) {
+    const int e = (int)(__float_as_uint(f) >> 23);  // no sign
+    const u64 m = e ? (__float_as_uint(f) & 0x7FFFFFu) | 0x800000u : __float_as_uint(f);
+    const int shift = 150 - (e ? e : 1);  // f = m 2^-shift, shift >= 24
+    const u64 hi = __umul64hi(s, m), lo = s * m;
+    if (shift >= 128) return up && (hi | lo) ? 1 : 0;
+    const u64 q = shift >= 64 ? (shift > 64 ? hi >> (shift - 64) : hi) : (hi << (64 - shift)) | (lo >> shift);
+    const bool left = shift >= 64 ? (lo != 0 || (shift > 64 && (hi << (128 - shift)) != 0)) : (lo << (64 - shift)) != 0;
+    return q + (up && left ? 1 : 0);
 }
 
 // ---- cluster ------------------------------------------------------------------
@@ -137,8 +179,14 @@ __device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
 __device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t v) {
     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
-__device__ __forceinline__ void st_cluster(uint32_t addr, double v) {
-    asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(addr), "d"(v) : "memory");
+__device__ __forceinline__ void st_cluster(uint32_t addr, u64 v) {
+    asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
+}
+__device__ __forceinline__ uint4 ld_cluster(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
 }
 __device__ __forceinline__ void add_cluster(uint32_t addr, uint32_t v) {
     asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
@@ -146,46 +194,50 @@ __device__ __forceinline__ void add_cluster(uint32_t addr, uint32_t v) {
 __device__ __forceinline__ void min_cluster(uint32_t addr, uint32_t v) {
     asm volatile("red.relaxed.cluster.shared::cluster.min.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
+__device__ __forceinline__ void add_shared(uint32_t addr) {
+    asm volatile("red.relaxed.cta.shared::cta.add.u32 [%0], %1;" ::"r"(addr), "r"(1u) : "memory");
+}
 __device__ __forceinline__ void cluster_sync() {
     __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// The lowest order of a window from `high` down.
+__device__ __forceinline__ uint32_t window_low(uint32_t high) {
+    return high >= kLowest + kBins ? high - (kBins - 1) : kLowest;
+}
+
 // ---- shared state ---------------------------------------------------------------
 
-enum { kDone, kWindow, kTie, kScan };
+enum { kDone, kFirst, kWindow, kTie, kScan };
 
 struct Command {
-    uint32_t op;
-    uint32_t high, low;  // kWindow: the orders from `high` down to `low`
-    uint32_t rest;       // kWindow: whether what lies below is summed
+    uint32_t op;         // kFirst: the first window, its counts and lowest ids gathered in the first CTA; kWindow: another,
+                         // counts in each CTA; kTie, kScan: the drawn logit's tokens
+    uint32_t high, low;  // the orders from `high` down to `low`
+    uint32_t rest;       // whether what lies below is summed
     uint32_t order;      // kTie, kScan: the order looked for
-    uint32_t skip;       // kScan: of its tokens in this CTA's warp, the one after so many ...
-    uint32_t who;        // ... in this warp of the cluster
-};
-
-struct Found {      // a place in the order
-    int n;          // tokens up to and with it (0: not in the window)
-    uint32_t order; // its logit
-    int tie;        // tokens of that logit before it
-    double sum;     // weight up to and with it
-    double weight;  // its own
+    uint32_t skip;       // kTie: of its tokens the one after so many; kScan: of those in this warp ...
+    uint32_t who;        // ... of the cluster
 };
 
 struct __align__(16) SampleShared {
     uint32_t count[kBins];
     uint32_t lowest[kBins];
-    double warp_sum[kWarps];
+    u64 sum_to[kThreads];               // weight and tokens up to each thread's last bin
+    int count_to[kThreads];
+    u64 warp_sum[kWarps];
     int warp_count[kWarps];
-    double rest[kMaxCluster];           // first CTA: every CTA's sum below the window
+    u64 rest[kMaxCluster];              // first CTA: every CTA's sum below the window
     uint32_t below[kMaxCluster];        // ... and the largest order there
     uint32_t top[kMaxCluster], reach[kMaxCluster];  // all CTAs: every CTA's largest order, its n-th largest thread
     uint32_t ties[kMaxCluster * kWarps];
     uint32_t warp_word[kWarps];
-    Command cmd;
-    Found found[4];                     // the k-th or last kept, two places by weight, min-p's
-    double win_sum[kMaxWindows];        // the search to the end: weight and tokens above each window,
+    Command cmd, next;
+    u64 before_sum;                     // weight and tokens above the window that is loaded
+    int before_count;
+    u64 win_sum[kMaxWindows];           // the search to the end: weight and tokens above each window,
     int win_count[kMaxWindows];         // and its bounds
     uint32_t win_high[kMaxWindows], win_low[kMaxWindows];
 };
@@ -239,253 +291,222 @@ __device__ __forceinline__ void each_piece(const Slice& s, F f) {
     }
 }
 
+__device__ __forceinline__ uint32_t word_at(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+
 __device__ __forceinline__ uint32_t half_at(const uint4& v, int i) {
-    const uint32_t w = i < 2 ? v.x : i < 4 ? v.y : i < 6 ? v.z : v.w;
+    const uint32_t w = word_at(v, i >> 1);
     return i & 1 ? w >> 16 : w & 0xFFFFu;
 }
 
 __device__ __forceinline__ __half2 as_half2(uint32_t w) { return *reinterpret_cast<const __half2*>(&w); }
 
-__device__ __forceinline__ __half2 max_nan2(__half2 a, __half2 b) { return __hmax2_nan(a, b); }
-
 __device__ __forceinline__ uint32_t block_max(SampleShared& sh, uint32_t v) {
-    v = __reduce_max_sync(0xffffffffu, v);
+    v = __reduce_max_sync(kFull, v);
     if ((threadIdx.x & 31) == 0) sh.warp_word[threadIdx.x >> 5] = v;
     __syncthreads();
-    return __reduce_max_sync(0xffffffffu, sh.warp_word[threadIdx.x & (kWarps - 1)]);
+    return __reduce_max_sync(kFull, sh.warp_word[threadIdx.x & (kWarps - 1)]);
 }
 
 // ---- the first CTA's search in the window -----------------------------------------
 
-// A thread's bins with what lies before them.
-struct Bins {
-    int lo, hi;       // bins [lo, hi) of the window, largest logits first
-    int before, n;    // tokens before them, and in them
-    double above, end;  // the weight before them, and with them
+// The window as the search sees it: bins from `high` down, `own` of them a thread, and what lies before.
+struct Window {
+    uint32_t high, low;
+    int own, before, count;  // tokens before it, and up to its end
+    u64 above, sum;          // weights
 };
 
-// Sums of every thread's bins; *count, *sum: tokens and weight up to the window's end.
-__device__ Bins window_bins(SampleShared& sh, const Scale& k, uint32_t high, uint32_t low, int before, double above,
-                            int* count, double* sum) {
+// Sums up to every thread's bins. The whole CTA.
+__device__ Window window_sums(SampleShared& sh, const Scale& k, uint32_t high, uint32_t low, int before, u64 above) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int bins = (int)(high - low) + 1, own = (bins + kThreads - 1) / kThreads;
-    Bins b;
-    b.lo = min(tid * own, bins);
-    b.hi = min(b.lo + own, bins);
-    b.n = 0;
-    double w = 0.0;
-    for (int i = b.lo; i < b.hi; ++i)
-        if (sh.count[i]) {
-            b.n += (int)sh.count[i];
-            w += (double)sh.count[i] * weight_of(k, high - i);
+    const int lo = min(tid * own, bins), hi = min(lo + own, bins);
+    int n = 0;
+    u64 w = 0;
+    for (int i = lo; i < hi; ++i) {
+        const uint32_t c = sh.count[i];
+        if (c) {
+            n += (int)c;
+            w += c * weight_of(k, high - i);
         }
-    int n = b.n;
+    }
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        const int pn = __shfl_up_sync(0xffffffffu, n, d);
-        const double pw = __shfl_up_sync(0xffffffffu, w, d);
+        const int pn = __shfl_up_sync(kFull, n, d);
+        const u64 pw = __shfl_up_sync(kFull, w, d);
         if (lane >= d) n += pn, w += pw;
     }
     if (lane == 31) sh.warp_count[warp] = n, sh.warp_sum[warp] = w;
     __syncthreads();
-    int wn = before, tn = before;
-    double ws = above, ts = above;
+    Window o = {high, low, own, before, before, above, above};
 #pragma unroll
     for (int i = 0; i < kWarps; ++i) {
-        if (i == warp) wn = tn, ws = ts;
-        tn += sh.warp_count[i];
-        ts += sh.warp_sum[i];
+        if (i == warp) n += o.count, w += o.sum;
+        o.count += sh.warp_count[i];
+        o.sum += sh.warp_sum[i];
     }
-    b.before = wn + n - b.n;
-    const double pw = __shfl_up_sync(0xffffffffu, w, 1);
-    b.above = ws + (lane ? pw : 0.0);  // the same sums as the end of the thread before
-    b.end = ws + w;
-    *count = tn;
-    *sum = ts;
-    return b;
+    sh.count_to[tid] = n;
+    sh.sum_to[tid] = w;
+    __syncthreads();
+    return o;
 }
 
-// Walks a thread's bins to the first place where `stop(tokens, weight)` with the bin's tokens holds; there
-// take(tokens before, weight before, bin's tokens, weight of one) gives how many of the bin's tokens, 1 ..
-template <typename Stop, typename Take>
-__device__ __forceinline__ void walk(const SampleShared& sh, const Scale& k, const Bins& b, uint32_t high, Found* out,
-                                     Stop stop, Take take) {
-    int n = b.before;
-    double w = b.above;
-    Found f = {};
-    for (int i = b.lo; i < b.hi; ++i) {
-        const int c = (int)sh.count[i];
-        if (!c) continue;
-        const double one = weight_of(k, high - i), to = w + (double)c * one;
-        const bool here = stop(n + c, to);
-        const int m = here ? take(n, w, c, one) : c;
-        f = {n + m, high - (uint32_t)i, m - 1, w + (double)m * one, one};  // the last one where none stops
-        if (here) break;
-        n += c;
-        w = to;
+struct Found {      // a place in the order
+    int n;          // tokens up to and with it (0: not in the window)
+    uint32_t order; // its logit
+    int tie;        // tokens of that logit before it
+    u64 sum;        // weight up to and with it
+};
+
+enum { kByCount, kReach, kPass };  // the n-th token; the first at which the weight reaches, or passes, s
+
+// The whole of one warp.
+template <int HOW>
+__device__ Found find(const SampleShared& sh, const Scale& k, const Window& w, int n, u64 s) {
+    const int lane = threadIdx.x & 31;
+    auto there = [&](int count, u64 sum) { return HOW == kByCount ? count >= n : HOW == kReach ? sum >= s : sum > s; };
+    if (!there(w.count, w.sum)) return {};
+    // the thread, then its bin
+    constexpr int kStride = kThreads / 32;
+    const int last = (lane + 1) * kStride - 1;
+    const int group = __ffs(__ballot_sync(kFull, there(sh.count_to[last], sh.sum_to[last]))) - 1;
+    const int one = group * kStride + (lane & (kStride - 1));
+    const int thread = group * kStride + __ffs(__ballot_sync(kFull, there(sh.count_to[one], sh.sum_to[one]))) - 1;
+    const int n0 = thread ? sh.count_to[thread - 1] : w.before;
+    const u64 s0 = thread ? sh.sum_to[thread - 1] : w.above;
+    const int bins = (int)(w.high - w.low) + 1, i = thread * w.own + lane;
+    const int c = lane < w.own && i < bins ? (int)sh.count[i] : 0;  // own is 16 at most
+    const u64 weight = c ? weight_of(k, w.high - i) : 0;
+    int ni = c;
+    u64 si = c * weight;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int pn = __shfl_up_sync(kFull, ni, d);
+        const u64 ps = __shfl_up_sync(kFull, si, d);
+        if (lane >= d) ni += pn, si += ps;
     }
-    *out = f;
+    ni += n0;
+    si += s0;
+    const int at = __ffs(__ballot_sync(kFull, there(ni, si))) - 1;
+    const int cb = __shfl_sync(kFull, c, at), from_n = __shfl_sync(kFull, ni, at) - cb;
+    const u64 wb = __shfl_sync(kFull, weight, at), from_s = __shfl_sync(kFull, si, at) - cb * wb;
+    int m;
+    if (HOW == kByCount)
+        m = n - from_n;
+    else if (HOW == kReach)
+        m = wb ? (int)((s - from_s + wb - 1) / wb) : 1;  // s is past from_s: the bin has a weight, or s is 0
+    else
+        m = (int)((s - from_s) / wb) + 1;
+    m = max(m, 1);
+    return {from_n + m, w.high - (uint32_t)(thread * w.own + at), m - 1, from_s + m * wb};
 }
 
-// The n-th token.
-__device__ __forceinline__ void find_count(SampleShared& sh, const Scale& k, const Bins& b, uint32_t high, int n,
-                                           Found* out) {
-    if (b.n && b.before < n && n <= b.before + b.n)
-        walk(sh, k, b, high, out, [&](int to, double) { return to >= n; },
-             [&](int from, double, int, double) { return n - from; });
-}
-
-// The first token at which the weight reaches (or, PASS, passes) the target.
-template <bool PASS>
-__device__ __forceinline__ void find_weight(SampleShared& sh, const Scale& k, const Bins& b, uint32_t high, int first,
-                                            double target, Found* out) {
-    const bool mine = PASS ? b.above <= target && target < b.end
-                           : (b.above < target || b.before == first) && target <= b.end;
-    if (b.n && mine)
-        walk(sh, k, b, high, out, [&](int, double to) { return PASS ? to > target : to >= target; },
-             [&](int, double from, int c, double one) {
-                 const double m = (target - from) / one;
-                 const double i = PASS ? floor(m) + 1.0 : ceil(m);
-                 return (int)fmin(fmax(i, 1.0), (double)c);
-             });
+// The last token of at least m times the largest weight (n: w.before where the window has none): its bins are cut
+// by halving, 32 at once. *end: the window's last logit is still kept.  The whole of one warp.
+__device__ Found find_min(const SampleShared& sh, const Scale& k, const Window& w, float m, bool* end) {
+    const int lane = threadIdx.x & 31, bins = (int)(w.high - w.low) + 1;
+    int lo = 0, hi = bins;  // the first bin that is not kept lies in [lo, hi]
+    while (lo < hi) {
+        const int step = (hi - lo + 31) >> 5, i = lo + lane * step;
+        const unsigned kept = __ballot_sync(kFull, i < hi && at_least(k, w.high - i, m));
+        const int n = __popc(kept);  // the kept ones come first
+        if (n == 0) {
+            hi = lo;
+        } else {
+            const int first = lo + (n - 1) * step + 1;
+            hi = min(hi, lo + n * step);
+            lo = first;
+        }
+    }
+    *end = lo == bins;
+    const int thread = lo / w.own, i = thread * w.own + lane;
+    int n = thread ? sh.count_to[thread - 1] : w.before;
+    u64 s = thread ? sh.sum_to[thread - 1] : w.above;
+    const int c = i < lo && lane < w.own ? (int)sh.count[i] : 0;
+    u64 si = c ? c * weight_of(k, w.high - i) : 0;
+    n += (int)__reduce_add_sync(kFull, (unsigned)c);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) si += __shfl_xor_sync(kFull, si, d);
+    return {n, 0, 0, s + si};
 }
 
 // What a row asks for.
 struct Wish {
-    int k;         // kAll: no limit
-    double p, m;   // 1 and above: no top-p; 0: no min-p
-    double u;      // 1 and above: the last
+    int k;     // kAll: no limit
+    float p;   // 1: no top-p
+    float m;   // 0: no min-p
+    float u;   // 1: the last
 };
 
-// The last token of at least min_p times the largest weight; n = kAll where the window's last logit still is, and
-// there is more below.
-__device__ __forceinline__ void find_min_p(SampleShared& sh, const Scale& k, const Bins& b, uint32_t high, uint32_t low,
-                                           bool more, double m, Found* out) {
-    // the bin whose logits are kept and whose next bin's are not: one thread's, empty or not
-    if (threadIdx.x == 0) {
-        if (more && weight_of(k, low) >= m) *out = {kAll, 0, 0, 0.0, 0.0};
-    }
-    int n = b.before;
-    double w = b.above;
-    Found f = {};
-    for (int i = b.lo; i < b.hi; ++i) {
-        const int c = (int)sh.count[i];
-        if (!c) continue;
-        const double one = weight_of(k, high - i);
-        if (!(one >= m) && one < 1.0) break;
-        n += c;
-        w += (double)c * one;
-        f = {n, high - (uint32_t)i, c - 1, w, one};
-    }
-    // the last thread that keeps any: the tokens behind it are not kept
-    const bool any = f.n > 0;
-    const uint32_t last = block_max(sh, any ? (uint32_t)threadIdx.x + 1 : 0u);
-    if (any && last == threadIdx.x + 1 && out->n != kAll) *out = f;
+__device__ __forceinline__ Found find_top_p(const SampleShared& sh, const Scale& k, const Window& w, float p, u64 sum) {
+    const u64 s = times(p, sum, true);
+    return s ? find<kReach>(sh, k, w, 0, s) : find<kByCount>(sh, k, w, 1, 0);  // the first is always kept
 }
 
-// One try with the window [high, low] from the row's maximum on: true and *at, *total (the drawn place, the kept
-// weight) where it is certain.  rest, error: the weight below the window and its bound.
-__device__ bool decide(SampleShared& sh, const Scale& k, const Wish& wish, uint32_t high, uint32_t low, bool more,
-                       double rest, double error, Found* at, double* total) {
-    int count;
-    double sum;
-    const Bins b = window_bins(sh, k, high, low, 0, 0.0, &count, &sum);
-    if (threadIdx.x < 4) sh.found[threadIdx.x] = {};
-    __syncthreads();
-    int kept = kAll;          // tokens kept, kAll: all of the row
-    double low_sum, high_sum; // bounds of the kept weight
-    if (!more) rest = error = 0.0;
-    // top-k
-    if (wish.k <= count || !more) {
-        kept = min(wish.k, count);
-        find_count(sh, k, b, high, kept, &sh.found[0]);
-        __syncthreads();
-        low_sum = high_sum = sh.found[0].sum;
+// One try with the window from the row's maximum down: true and *at, *total (the drawn place, the kept
+// weight) where it is certain.  rest, error: the weight below the window and its bound.  One warp.
+__device__ bool decide(const SampleShared& sh, const Scale& k, const Wish& wish, const Window& w, bool more, u64 rest,
+                       u64 error, Found* at, u64* total) {
+    int kept = kAll;  // tokens kept, kAll: all of the row
+    u64 low_sum, high_sum;  // bounds of the kept weight
+    if (wish.k <= w.count || !more) {
+        kept = min(wish.k, w.count);
+        low_sum = high_sum = find<kByCount>(sh, k, w, kept, 0).sum;
     } else if (wish.k == kAll) {
-        low_sum = sum + rest - error;
-        high_sum = sum + rest + error;
+        low_sum = w.sum + (rest > error ? rest - error : 0);
+        high_sum = w.sum + rest + error;
     } else {
         return false;  // the k-th lies below
     }
-    // top-p: the place for both ends of the bound
     int kept_low = kept, kept_high = kept;
-    if (wish.p < 1.0) {
-        find_weight<false>(sh, k, b, high, 0, wish.p * low_sum, &sh.found[1]);
-        find_weight<false>(sh, k, b, high, 0, wish.p * high_sum, &sh.found[2]);
-        __syncthreads();
-        const Found f1 = sh.found[1], f2 = sh.found[2];
-        if (f1.n) {
-            kept_low = min(kept, f1.n);
-            if (f1.n <= kept) low_sum = f1.sum;
-        } else if (more && kept == kAll) {
-            kept_low = kBeyond;
-        }
-        if (f2.n) {
-            kept_high = min(kept, f2.n);
-            if (f2.n <= kept) high_sum = f2.sum;
-        } else if (more && kept == kAll) {
-            kept_high = kBeyond;
-        }
-        __syncthreads();
-        if (threadIdx.x < 4) sh.found[threadIdx.x] = {};
-        __syncthreads();
+    if (wish.p < 1.f) {
+        const Found f1 = find_top_p(sh, k, w, wish.p, low_sum);
+        const Found f2 = low_sum == high_sum ? f1 : find_top_p(sh, k, w, wish.p, high_sum);
+        if (!f1.n) kept_low = kBeyond;
+        else if (f1.n <= kept) kept_low = f1.n, low_sum = f1.sum;
+        if (!f2.n) kept_high = kBeyond;
+        else if (f2.n <= kept) kept_high = f2.n, high_sum = f2.sum;
     }
-    if (wish.m > 0.0) {
-        find_min_p(sh, k, b, high, low, more, wish.m, &sh.found[3]);
-        __syncthreads();
-        const Found f = sh.found[3];
-        if (f.n != kAll && f.n > 0) {
+    if (wish.m > 0.f) {
+        bool end;
+        Found f = find_min(sh, k, w, wish.m, &end);
+        if (f.n == 0) f = find<kByCount>(sh, k, w, 1, 0);  // the first is always kept
+        if (!(end && more)) {
             if (f.n < kept_low) kept_low = f.n, low_sum = f.sum;
             if (f.n < kept_high) kept_high = f.n, high_sum = f.sum;
         }
     }
     if (kept_low != kept_high || kept_low == kBeyond) return false;
-    if (kept_low != kAll) {
-        find_count(sh, k, b, high, kept_low, &sh.found[0]);  // the last that is kept
+    Found f1 = {}, f2 = {};
+    if (wish.u < 1.f) {
+        f1 = find<kPass>(sh, k, w, 0, times(wish.u, low_sum, false));
+        f2 = low_sum == high_sum ? f1 : find<kPass>(sh, k, w, 0, times(wish.u, high_sum, false));
     }
-    if (wish.u < 1.0) {
-        find_weight<true>(sh, k, b, high, 0, wish.u * low_sum, &sh.found[1]);
-        find_weight<true>(sh, k, b, high, 0, wish.u * high_sum, &sh.found[2]);
-    }
-    __syncthreads();
-    const Found last = sh.found[0];
-    Found f1 = sh.found[1], f2 = sh.found[2];
-    if (kept_low != kAll) {
+    if (kept_low != kAll && (!f1.n || f1.n > kept_low || !f2.n || f2.n > kept_low)) {
+        const Found last = find<kByCount>(sh, k, w, kept_low, 0);
         if (!f1.n || f1.n > kept_low) f1 = last;
         if (!f2.n || f2.n > kept_low) f2 = last;
     }
     if (!f1.n || f1.n != f2.n) return false;
     *at = f1;
-    *total = 0.5 * (low_sum + high_sum);
+    *total = low_sum + (high_sum - low_sum) / 2;
     return true;
 }
 
-__device__ __forceinline__ void send(SampleShared& sh, int cluster, const Command& c) {
-    // every thread of the first CTA holds the same command; the words go to all CTAs
-    constexpr int kWords = sizeof(Command) / 4;
-    const int tid = threadIdx.x;
-    if (tid < cluster * kWords) {
-        const int word = tid % kWords;
-        const uint32_t v = word == 0 ? c.op : word == 1 ? c.high : word == 2 ? c.low : word == 3 ? c.rest
-                         : word == 4 ? c.order : word == 5 ? c.skip : c.who;
-        st_cluster(in_cta(smem_u32(&sh.cmd) + word * 4, tid / kWords), v);
-    }
-}
+// ---- the kernel ---------------------------------------------------------------------
 
-__device__ __forceinline__ void clear(SampleShared& sh, int bins) {
-    for (int i = threadIdx.x; i < bins; i += kThreads) {
-        sh.count[i] = 0;
-        sh.lowest[i] = 0xFFFFFFFFu;
-    }
-}
-
-__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a) {
-    extern __shared__ __align__(16) char smem[];
-    SampleShared& sh = *reinterpret_cast<SampleShared*>(smem);
+__global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a) {
+    __shared__ SampleShared sh;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t rank = a.cluster > 1 ? cluster_rank() : 0;
     const int64_t row = blockIdx.x / (unsigned)a.cluster;
-    if (rank == 0) clear(sh, kBins);
+    auto clear = [&](int bins) {
+        for (int i = tid; i < bins; i += kThreads) sh.count[i] = 0;
+    };
+    if (rank == 0) {
+        clear(kBins);
+        for (int i = tid; i < kBins; i += kThreads) sh.lowest[i] = 0xFFFFFFFFu;
+    }
     pdl_wait();
     pdl_launch_dependents();
 
@@ -508,30 +529,27 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     if (wish.k <= 0 || wish.k >= a.vocab) wish.k = kAll;
     if (greedy) wish.k = 1;
     const float p = a.top_p ? a.top_p[row] : 1.f, m = a.min_p ? a.min_p[row] : 0.f, u = a.u[row];
-    wish.p = p < 1.f ? fmax((double)p, 0.0) : 1.0;
-    wish.m = m > 0.f ? (double)m : 0.0;
-    wish.u = u > 0.f ? (double)u : 0.0;
+    wish.p = p < 1.f ? fmaxf(p, 0.f) : 1.f;
+    wish.m = m > 0.f ? m : 0.f;
+    wish.u = u > 0.f ? fminf(u, 1.f) : 0.f;
 
     // look 1
-    __half2 m2[4];
+    uint32_t mine;
     {
         const __half2 none = as_half2(0xFC00FC00u);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) m2[i] = none;
+        __half2 m2[4] = {none, none, none, none};
         each_piece(s, [&](const uint4& v, int) {
-            m2[0] = max_nan2(m2[0], as_half2(v.x));
-            m2[1] = max_nan2(m2[1], as_half2(v.y));
-            m2[2] = max_nan2(m2[2], as_half2(v.z));
-            m2[3] = max_nan2(m2[3], as_half2(v.w));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) m2[i] = __hmax2_nan(m2[i], as_half2(word_at(v, i)));
         });
-        m2[0] = max_nan2(max_nan2(m2[0], m2[1]), max_nan2(m2[2], m2[3]));
+        m2[0] = __hmax2_nan(__hmax2_nan(m2[0], m2[1]), __hmax2_nan(m2[2], m2[3]));
+        mine = max(order16(__half_as_ushort(__low2half(m2[0]))), order16(__half_as_ushort(__high2half(m2[0]))));
     }
-    const uint32_t mine = max(order16(__half_as_ushort(__low2half(m2[0]))), order16(__half_as_ushort(__high2half(m2[0]))));
     const uint32_t cta_top = block_max(sh, mine);
     // The window's reach: with a top-k the k-th largest of the threads' maxima (k logits reach it at least), else the
     // 128th, which holds the likely tokens of a trained model's row; without any limit, and for more than there are
     // threads, all of the histogram.
-    const bool all = wish.k == kAll && !(wish.p < 1.0) && !(wish.m > 0.0);
+    const bool all = wish.k == kAll && !(wish.p < 1.f) && !(wish.m > 0.f);
     const int want = ((wish.k != kAll ? min(wish.k, kThreads * a.cluster + 1) : 128) + a.cluster - 1) / a.cluster;
     uint32_t reach = 0;
     if (greedy) {
@@ -563,70 +581,88 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     }
     Scale k;
     k.top = value_of(top);
+    k.places = a.places;
     {
         // beyond 2^100 all but the largest logit have no weight, below 2^-100 all have the same
         const double c = fmin(fmax(1.4426950408889634074 / (greedy ? 1.0 : (double)temperature), 0x1p-100), 0x1p100);
         k.c = (float)c;
         k.c_low = (float)(c - (double)k.c);
     }
-    Command cmd = {kWindow, top, max(low, window_low(top)), wish.k == kAll, 0, 0, 0};
+    Command cmd = {kFirst, top, max(low, window_low(top)), wish.k == kAll, 0, 0, 0};
+    // many logits are counted in each CTA and gathered then, few where they are wanted
+    if (cmd.low == window_low(top) && !greedy) cmd.op = kWindow;
 
-    // first CTA: where the search is
-    enum { kTry, kWide, kCollect, kTopP, kMinP, kPick };
-    int stage = cmd.low == window_low(top) ? kWide : kTry;
+    if (tid == 0) sh.before_count = 0, sh.before_sum = 0;
+
+    // first CTA, first warp: where the search is
+    enum { kTry, kCollect, kTopP, kMinP, kPick };
+    int stage = kTry;
     int windows = 0, kept = kAll, win = 0;  // win: the window that is loaded
-    double kept_sum = 0.0;
+    u64 kept_sum = 0;
 
     for (;;) {
-        if (cmd.op == kWindow) {
+        if (cmd.op == kFirst || cmd.op == kWindow) {
+            if (cmd.op == kWindow) {
+                clear((int)(cmd.high - cmd.low) + 1);
+                __syncthreads();
+            }
             const __half low_h = __ushort_as_half((unsigned short)unorder16(cmd.low));
             const __half2 low2 = __halves2half2(low_h, low_h);
-            const uint32_t counts = in_cta(smem_u32(sh.count), 0), ids = in_cta(smem_u32(sh.lowest), 0);
+            const bool first = cmd.op == kFirst;
+            const uint32_t own = smem_u32(sh.count), counts = in_cta(own, 0), ids = in_cta(smem_u32(sh.lowest), 0);
+            const float c = k.c, t = k.top;
             __half2 b2 = as_half2(0xFC00FC00u);
             float sum = 0.f;
             each_piece(s, [&](const uint4& v, int id) {
                 const uint32_t any = __hge2_mask(as_half2(v.x), low2) | __hge2_mask(as_half2(v.y), low2) |
                                      __hge2_mask(as_half2(v.z), low2) | __hge2_mask(as_half2(v.w), low2);
-                if (!any) {
-                    b2 = __hmax2(b2, __hmax2(__hmax2(as_half2(v.x), as_half2(v.y)), __hmax2(as_half2(v.z), as_half2(v.w))));
-                    if (cmd.rest) {
-                        float e[8];
+                float e[8];
+                if (cmd.rest) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float2 f = __half22float2(as_half2(i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w));
-                            e[2 * i] = ex2f((f.x - k.top) * k.c);
-                            e[2 * i + 1] = ex2f((f.y - k.top) * k.c);
-                        }
-                        sum += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 f = __half22float2(as_half2(word_at(v, i)));
+                        e[2 * i] = ex2f((f.x - t) * c);
+                        e[2 * i + 1] = ex2f((f.y - t) * c);
                     }
                 } else {
-                    float part = 0.f;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) e[i] = 0.f;
+                }
+                if (!any) {
+                    b2 = __hmax2(b2, __hmax2(__hmax2(as_half2(v.x), as_half2(v.y)), __hmax2(as_half2(v.z), as_half2(v.w))));
+                } else {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const uint32_t h = half_at(v, i), o = order16(h);
                         if (o >= cmd.low) {
+                            e[i] = 0.f;
+                            const uint32_t at = (cmd.high - o) * 4;
                             if (o <= cmd.high) {
-                                add_cluster(counts + (cmd.high - o) * 4, 1u);
-                                min_cluster(ids + (cmd.high - o) * 4, (uint32_t)(id + i));
+                                if (first) {
+                                    add_cluster(counts + at, 1u);
+                                    min_cluster(ids + at, (uint32_t)(id + i));
+                                } else {
+                                    add_shared(own + at);
+                                }
                             }
                         } else {
                             const __half x = __ushort_as_half((unsigned short)h);
                             b2 = __hmax2(b2, __halves2half2(x, x));
-                            if (cmd.rest) part += ex2f((__half2float(x) - k.top) * k.c);
                         }
                     }
-                    sum += part;
                 }
+                sum += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
             });
             const uint32_t below = block_max(sh, max(order16(__half_as_ushort(__low2half(b2))),
                                                      order16(__half_as_ushort(__high2half(b2)))));
-            double d = (double)sum;
+            u64 d = __float2ull_rn(sum * __uint_as_float((uint32_t)(k.places + 127) << 23));
 #pragma unroll
-            for (int x = 16; x > 0; x >>= 1) d += __shfl_xor_sync(0xffffffffu, d, x);
+            for (int x = 16; x > 0; x >>= 1) d += __shfl_xor_sync(kFull, d, x);
             if (lane == 0) sh.warp_sum[warp] = d;
             __syncthreads();
             if (tid == 0) {
-                d = 0.0;
+                d = 0;
+#pragma unroll
                 for (int i = 0; i < kWarps; ++i) d += sh.warp_sum[i];
                 st_cluster(in_cta(smem_u32(&sh.rest[rank]), 0), d);
                 st_cluster(in_cta(smem_u32(&sh.below[rank]), 0), below);
@@ -636,10 +672,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
                       w1 = s.p0 + (int)((int64_t)n * (warp + 1) / kWarps);
             const bool edge0 = s.first && s.head && warp == 0, edge1 = s.last && s.tail && warp == kWarps - 1;
             const bool scan = cmd.op == kScan;
+            const __half want_h = __ushort_as_half((unsigned short)unorder16(cmd.order));
+            const __half2 want2 = __halves2half2(want_h, want_h);
             if (!scan || cmd.who == rank * kWarps + warp) {
                 int left = (int)cmd.skip, total = 0;
                 const uint4* pc = reinterpret_cast<const uint4*>(s.row + s.head);
-                // pieces -1 and w1 stand for the row's ends
+                // pieces w0 - 1 and w1 stand for the row's ends
                 for (int base = w0 - 1; base <= w1; base += 32) {
                     const int i = base + lane;
                     int id = s.head + i * 8;
@@ -650,30 +688,32 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
                         v = edge_piece(s, 0, &id);
                     else if (i == w1 && edge1)
                         v = edge_piece(s, 1, &id);
-                    uint32_t hit = 0;
+                    uint32_t hit = 0;  // equal: -0 and +0 are
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) hit |= (uint32_t)(order16(half_at(v, j)) == cmd.order) << j;
-                    int c = __popc(hit), run = c;
+                    for (int j = 0; j < 4; ++j)
+                        hit |= (__heq2_mask(as_half2(word_at(v, j)), want2) & 0x00010002u) << (2 * j);
+                    hit = (hit & 0xFFFFu) >> 1 | hit >> 15;
+                    const int c = __popc(hit);
                     if (!scan) {
                         total += c;
                         continue;
                     }
+                    int run = c;
 #pragma unroll
                     for (int d = 1; d < 32; d <<= 1) {
-                        const int q = __shfl_up_sync(0xffffffffu, run, d);
+                        const int q = __shfl_up_sync(kFull, run, d);
                         if (lane >= d) run += q;
                     }
-                    const int all_hits = __shfl_sync(0xffffffffu, run, 31);
                     int skip = left - (run - c);
                     if (skip >= 0 && skip < c) {
                         for (; skip > 0; --skip) hit &= hit - 1;
                         a.token[row] = id + __ffs(hit) - 1;
                     }
-                    left -= all_hits;
+                    left -= __shfl_sync(kFull, run, 31);
                     if (left < 0) break;
                 }
                 if (!scan) {
-                    total = (int)__reduce_add_sync(0xffffffffu, (unsigned)total);
+                    total = (int)__reduce_add_sync(kFull, (unsigned)total);
                     if (lane == 0) st_cluster(in_cta(smem_u32(&sh.ties[rank * kWarps + warp]), 0), (uint32_t)total);
                 }
             }
@@ -691,151 +731,149 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
                 next.skip = at;
                 next.who = who;
             } else {
+                if (cmd.op == kWindow && a.cluster > 1) {  // the other CTAs' counts
+                    const int quads = ((int)(cmd.high - cmd.low) + 4) >> 2;
+                    for (int i = tid; i < quads; i += kThreads) {
+                        uint4 v = reinterpret_cast<uint4*>(sh.count)[i];
+#pragma unroll
+                        for (int r = 1; r < kMaxCluster; ++r) {
+                            if (r >= a.cluster) break;
+                            const uint4 o = ld_cluster(in_cta(smem_u32(sh.count) + i * 16, r));
+                            v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+                        }
+                        reinterpret_cast<uint4*>(sh.count)[i] = v;
+                    }
+                    __syncthreads();
+                }
                 uint32_t below = 0;
-                double rest = 0.0;
+                u64 rest = 0;
                 for (int i = 0; i < a.cluster; ++i) {
                     below = max(below, sh.below[i]);
                     rest += sh.rest[i];
                 }
                 const bool more = below >= kLowest;
-                Found at = {};
-                double total = 0.0;
-                bool done = false;
-                if (stage <= kWide) {
-                    // A weight below the window is off by 2^-24 for each of: the sums of its thread's pieces, 3 |t|
-                    // ln 2 of its exponent t (60 at most, below which all of them together are under 2^-36 of the
-                    // largest's) and 4 of the power itself.
-                    const double error = rest * ((double)((s.p1 - s.p0) / kThreads + 160) * 0x1p-24) +
-                                         (double)a.vocab * 0x1p-60;
-                    done = decide(sh, k, wish, cmd.high, cmd.low, more, rest, error, &at, &total);
-                    if (!done && stage == kTry) {
-                        stage = kWide;
-                        next = {kWindow, top, window_low(top), wish.k == kAll, 0, 0, 0};
-                    } else if (!done) {
-                        stage = kCollect;
-                        windows = 0;
-                    }
-                }
-                if (!done && stage >= kCollect) {
-                    // Window by window to the end, or to the k-th token: nothing is left inexact.  Then the places of
-                    // top-p, min-p and the drawn token, each in the window that holds it.
-                    int count;
-                    double sum;
-                    const int w = stage == kCollect ? windows : win;
-                    const int before = w ? sh.win_count[w] : 0;
-                    const double above = w ? sh.win_sum[w] : 0.0;
-                    const Bins b = window_bins(sh, k, cmd.high, cmd.low, before, above, &count, &sum);
-                    __syncthreads();
-                    if (tid < 4) sh.found[tid] = {};
-                    __syncthreads();
-                    int need = -1;  // the window wanted next
-                    if (stage == kCollect) {
-                        if (tid == 0) {
-                            sh.win_high[w] = cmd.high;
-                            sh.win_low[w] = cmd.low;
-                            sh.win_count[w + 1] = count;
-                            sh.win_sum[w + 1] = sum;
-                        }
-                        windows = w + 1;
-                        win = w;
-                        __syncthreads();
-                        if (more && count < wish.k) {
-                            next = {kWindow, below, window_low(below), 0, 0, 0, 0};
-                        } else {
-                            kept = min(wish.k, count);
-                            find_count(sh, k, b, cmd.high, kept, &sh.found[0]);
-                            __syncthreads();
-                            kept_sum = sh.found[0].sum;
-                            stage = kTopP;
-                            need = w;
+                const Window w = window_sums(sh, k, cmd.high, cmd.low, sh.before_count, sh.before_sum);
+                if (warp == 0) {  // the search is one warp's
+                    Found at = {};
+                    u64 total = 0;
+                    bool done = false;
+                    if (stage == kTry) {
+                        // A weight below the window is off by 2^-24 for each of: the sums of its thread's pieces, 3 |t|
+                        // ln 2 of its exponent t (60 at most, below which all of them together are under 2^-36 of the
+                        // largest's) and 4 of the power itself; and by a place of its thread's sum.
+                        const u64 units = (u64)((s.p1 - s.p0) / kThreads + 160);
+                        const u64 error = more ? (rest >> 24) * units + units + kThreads * kMaxCluster +
+                                                     ((u64)a.vocab >> (60 - k.places)) : 0;
+                        done = decide(sh, k, wish, w, more, more ? rest : 0, error, &at, &total);
+                        if (!done && cmd.low > window_low(top)) {
+                            next = {kWindow, top, window_low(top), wish.k == kAll, 0, 0, 0};
+                        } else if (!done) {
+                            stage = kCollect;
                         }
                     }
-                    while (next.op == kDone && !done) {
-                        if (stage == kTopP) {
-                            if (!(wish.p < 1.0)) {
+                    if (stage >= kCollect) {
+                        // Window by window to the end, or to the k-th token: nothing is left inexact.  Then the places
+                        // of top-p, min-p and the drawn token, each in the window that holds it.
+                        int need = -1;  // the window wanted next
+                        if (stage == kCollect) {
+                            sh.win_high[windows] = cmd.high;
+                            sh.win_low[windows] = cmd.low;
+                            sh.win_count[windows + 1] = w.count;
+                            sh.win_sum[windows + 1] = w.sum;
+                            __syncwarp();
+                            win = windows++;
+                            if (more && w.count < wish.k) {
+                                next = {kWindow, below, window_low(below), 0, 0, 0, 0};
+                            } else {
+                                kept = min(wish.k, w.count);
+                                kept_sum = find<kByCount>(sh, k, w, kept, 0).sum;
+                                stage = kTopP;
+                            }
+                        }
+                        while (next.op == kDone && !done && need < 0) {
+                            if (stage == kTopP) {
+                                if (!(wish.p < 1.f)) {
+                                    stage = kMinP;
+                                    continue;
+                                }
+                                const u64 target = times(wish.p, kept_sum, true);
+                                int v = 0;
+                                while (v + 1 < windows && sh.win_sum[v + 1] < target) ++v;
+                                if (v != win) {
+                                    need = v;
+                                    continue;
+                                }
+                                const Found f = find_top_p(sh, k, w, wish.p, kept_sum);
+                                if (f.n && f.n <= kept) kept = f.n, kept_sum = f.sum;
                                 stage = kMinP;
-                                continue;
-                            }
-                            const double target = wish.p * kept_sum;
-                            int v = 0;
-                            while (v + 1 < windows && sh.win_sum[v + 1] < target) ++v;
-                            if (v != win) {
-                                need = v;
-                                break;
-                            }
-                            __syncthreads();
-                            if (tid == 0) sh.found[1] = {};
-                            __syncthreads();
-                            find_weight<false>(sh, k, b, cmd.high, v ? sh.win_count[v] : 0, target, &sh.found[1]);
-                            __syncthreads();
-                            const Found f = sh.found[1];
-                            if (f.n && f.n <= kept) kept = f.n, kept_sum = f.sum;
-                            stage = kMinP;
-                        } else if (stage == kMinP) {
-                            if (!(wish.m > 0.0)) {
+                            } else if (stage == kMinP) {
+                                if (!(wish.m > 0.f)) {
+                                    stage = kPick;
+                                    continue;
+                                }
+                                int v = 0;
+                                while (v + 1 < windows && at_least(k, sh.win_high[v + 1], wish.m)) ++v;
+                                if (v != win) {
+                                    need = v;
+                                    continue;
+                                }
+                                bool end;
+                                Found f = find_min(sh, k, w, wish.m, &end);
+                                if (f.n == 0) f = find<kByCount>(sh, k, w, 1, 0);
+                                if (f.n < kept) kept = f.n, kept_sum = f.sum;
                                 stage = kPick;
-                                continue;
+                            } else {
+                                const u64 target = times(wish.u, kept_sum, false);
+                                int v_last = 0, v = 0;
+                                while (v_last + 1 < windows && sh.win_count[v_last + 1] < kept) ++v_last;
+                                while (v < v_last && sh.win_sum[v + 1] <= target) ++v;
+                                if (!(wish.u < 1.f)) v = v_last;
+                                if (v != win) {
+                                    need = v;
+                                    continue;
+                                }
+                                if (wish.u < 1.f) at = find<kPass>(sh, k, w, 0, target);
+                                if (!at.n || at.n > kept) at = find<kByCount>(sh, k, w, min(kept, w.count), 0);
+                                total = kept_sum;
+                                done = true;
                             }
-                            int v = 0;
-                            while (v + 1 < windows && weight_of(k, sh.win_high[v + 1]) >= wish.m) ++v;
-                            if (v != win) {
-                                need = v;
-                                break;
-                            }
-                            __syncthreads();
-                            if (tid == 0) sh.found[1] = {};
-                            __syncthreads();
-                            find_min_p(sh, k, b, cmd.high, cmd.low, false, wish.m, &sh.found[1]);
-                            __syncthreads();
-                            const Found f = sh.found[1];
-                            if (f.n && f.n < kept) kept = f.n, kept_sum = f.sum;
-                            stage = kPick;
-                        } else {
-                            const double target = wish.u * kept_sum;
-                            int v = 0;
-                            if (wish.u < 1.0)
-                                while (v + 1 < windows && sh.win_sum[v + 1] <= target) ++v;
-                            int v_last = 0;
-                            while (v_last + 1 < windows && sh.win_count[v_last + 1] < kept) ++v_last;
-                            if (!(wish.u < 1.0) || v > v_last) v = v_last;
-                            if (v != win) {
-                                need = v;
-                                break;
-                            }
-                            __syncthreads();
-                            if (tid < 2) sh.found[tid] = {};
-                            __syncthreads();
-                            if (wish.u < 1.0)
-                                find_weight<true>(sh, k, b, cmd.high, v ? sh.win_count[v] : 0, target, &sh.found[1]);
-                            find_count(sh, k, b, cmd.high, min(kept, count), &sh.found[0]);
-                            __syncthreads();
-                            at = sh.found[1];
-                            if (!at.n || at.n > kept) at = sh.found[0];
-                            total = kept_sum;
-                            done = true;
+                        }
+                        if (need >= 0) {
+                            win = need;
+                            next = {kWindow, sh.win_high[need], sh.win_low[need], 0, 0, 0, 0};
                         }
                     }
-                    if (!done && next.op == kDone) {
-                        win = need;
-                        next = {kWindow, sh.win_high[need], sh.win_low[need], 0, 0, 0, 0};
-                    }
-                }
-                if (done) {
-                    if (tid == 0 && a.logprob) {
-                        const float2 t = power_of(k, value_of(at.order));
-                        a.logprob[row] = fminf((float)(((double)t.x + (double)t.y) * 0.69314718055994530942 - log(total)), 0.f);
-                    }
-                    if (at.tie == 0) {
-                        if (tid == 0) a.token[row] = (int64_t)sh.lowest[cmd.high - at.order];
-                        next.op = kDone;
-                    } else {
-                        next = {kTie, 0, 0, 0, at.order, (uint32_t)at.tie, 0};
+                    if (done) {
+                        if (lane == 0 && a.logprob) {
+                            const float2 t = power_of(k, value_of(at.order));
+                            a.logprob[row] = fminf((float)((((double)t.x + (double)t.y) - log2_of(total, k.places)) *
+                                                           0.69314718055994530942), 0.f);
+                        }
+                        if (cmd.op == kFirst && at.tie == 0) {
+                            if (lane == 0) a.token[row] = (int64_t)sh.lowest[cmd.high - at.order];
+                        } else {
+                            next = {kTie, 0, 0, 0, at.order, (uint32_t)at.tie, 0};
+                        }
                     }
                 }
             }
+            // the first warp's command, to every CTA
+            if (warp == 0) {
+                constexpr int kWords = sizeof(Command) / 4;
+                if (lane == 0) {
+                    sh.next = next;
+                    if (next.op == kWindow) {
+                        const int v = stage == kTry ? 0 : stage == kCollect ? windows : win;
+                        sh.before_count = v ? sh.win_count[v] : 0;
+                        sh.before_sum = v ? sh.win_sum[v] : 0;
+                    }
+                }
+                __syncwarp();
+                for (int i = lane; i < a.cluster * kWords; i += 32)
+                    st_cluster(in_cta(smem_u32(&sh.cmd) + i % kWords * 4, i / kWords),
+                               reinterpret_cast<const uint32_t*>(&sh.next)[i % kWords]);
+            }
             __syncthreads();
-            if (next.op == kWindow) clear(sh, (int)(next.high - next.low) + 1);
-            send(sh, a.cluster, next);
         }
         cluster_sync();
         cmd = sh.cmd;
@@ -845,18 +883,18 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-// CTAs of a row: enough to fill the GPU, and of at least 4096 logits each.
+// CTAs of a row: enough to fill the GPU, of at least 4096 logits each; and so many that the rows in work
+// (four CTAs an SM) stay in the L2 cache between the looks.
 int cluster_for(int64_t rows, int64_t vocab, int sms) {
+    const int64_t slots = (int64_t)sms * 4, cache = 48 << 20;
     int c = 1;
-    while (c < kMaxCluster && rows * c < (int64_t)sms * 2 && vocab >= (int64_t)c * 2 * 4096) c *= 2;
+    while (c < kMaxCluster && vocab >= (int64_t)c * 2 * 4096 &&
+           (rows * c < slots / 2 || (rows * c < slots ? rows * c : slots) / c * vocab * 2 > cache))
+        c *= 2;
     return c;
 }
 
 }  // namespace
-
-cudaError_t sample_prepare() {
-    return cudaFuncSetAttribute(sample_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(SampleShared));
-}
 
 }  // namespace mnb
 
@@ -881,6 +919,9 @@ extern "C" int mnb_sample(const void* logits, int64_t rows, int64_t vocab, int64
     a.row_stride = row_stride;
     a.vocab = (int)vocab;
     a.cluster = cluster_for(rows, vocab, sms);
+    a.places = 62;
+    while ((vocab - 1) >> (62 - a.places)) --a.places;
+    if (a.places > 60) a.places = 60;
     a.u = u;
     a.temperature = temperature;
     a.top_k = top_k;
@@ -891,7 +932,6 @@ extern "C" int mnb_sample(const void* logits, int64_t rows, int64_t vocab, int64
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(rows * a.cluster));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = sizeof(SampleShared);
     cfg.stream = reinterpret_cast<cudaStream_t>(stream);
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;
