@@ -211,12 +211,13 @@ __device__ __forceinline__ uint32_t window_low(uint32_t high) {
 // ---- shared state ---------------------------------------------------------------
 
 enum { kDone, kFirst, kWindow, kTie, kScan };
+enum { kNoRest, kRest, kExactRest };  // what lies below a window: left out, summed in FP32, or as the search's weights
 
 struct Command {
     uint32_t op;         // kFirst: the first window, its counts and lowest ids gathered in the first CTA; kWindow: another,
                          // counts in each CTA; kTie, kScan: the drawn logit's tokens
     uint32_t high, low;  // the orders from `high` down to `low`
-    uint32_t rest;       // whether what lies below is summed
+    uint32_t rest;       // kWindow: what is done with what lies below
     uint32_t order;      // kTie, kScan: the order looked for
     uint32_t skip;       // kTie: of its tokens the one after so many; kScan: of those in this warp ...
     uint32_t who;        // ... of the cluster
@@ -229,12 +230,14 @@ struct __align__(16) SampleShared {
     int count_to[kThreads];
     u64 warp_sum[kWarps];
     int warp_count[kWarps];
-    u64 rest[kMaxCluster];              // first CTA: every CTA's sum below the window
+    u64 rest[kMaxCluster];              // first CTA: every CTA's sum below the window (kFirst: of all its logits)
     uint32_t below[kMaxCluster];        // ... and the largest order there
     uint32_t top[kMaxCluster], reach[kMaxCluster];  // all CTAs: every CTA's largest order, its n-th largest thread
     uint32_t ties[kMaxCluster * kWarps];
     uint32_t warp_word[kWarps];
     Command cmd, next;
+    int work[2 * kThreads];             // first pieces of groups to look at again
+    int works;
     u64 before_sum;                     // weight and tokens above the window that is loaded
     int before_count;
     u64 win_sum[kMaxWindows];           // the search to the end: weight and tokens above each window,
@@ -265,6 +268,82 @@ __device__ __forceinline__ uint4 edge_piece(const Slice& s, int which, int* id) 
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// Pairs of FP32 values in one 64-bit register: one instruction for two.
+__device__ __forceinline__ u64 pair(float lo, float hi) {
+    u64 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 unpair(u64 v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c) {
+    u64 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ u64 add2(u64 a, u64 b) {
+    u64 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t word_at(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+__device__ __forceinline__ __half2 as_half2(uint32_t w) { return *reinterpret_cast<const __half2*>(&w); }
+__device__ __forceinline__ uint32_t as_word(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
+
+__device__ __forceinline__ __half2 max_of(const uint4& q) {
+    return __hmax2_nan(__hmax2_nan(as_half2(q.x), as_half2(q.y)), __hmax2_nan(as_half2(q.z), as_half2(q.w)));
+}
+
+// What a thread keeps of the first look: the largest of its groups of pieces and where the two best were, and the sum
+// of 2^(c x - r) about a reference r that moves when a value passes it by kMove.
+constexpr int kGroup = 3;
+constexpr int kHead = -2, kTail = -3, kNone = -1;  // the row's ends as groups
+constexpr float kMove = 8.f;
+
+struct Look {
+    float best = -INFINITY, second = -INFINITY, third = -INFINITY;
+    int at = kNone, second_at = kNone;
+    float r = -INFINITY;
+    u64 z = 0;
+    bool bad = false;  // NaN
+
+    // sum: whether the weights are wanted; low: -infinity has to be told from FP16's lowest value
+    template <int N>
+    __device__ __forceinline__ void add(const uint4 (&q)[N], int v, bool sum, bool low, float c) {
+        __half2 m2 = max_of(q[0]);
+#pragma unroll
+        for (int i = 1; i < N; ++i) m2 = __hmax2_nan(m2, max_of(q[i]));
+        const float x = __half2float(__hmax_nan(__low2half(m2), __high2half(m2)));
+        bad |= x != x;
+        third = fmaxf(third, fminf(second, x));
+        second_at = x > best ? at : (x > second ? v : second_at);
+        second = fmaxf(second, fminf(best, x));
+        at = x > best ? v : at;
+        best = fmaxf(best, x);
+        if (!sum) return;
+        const float to = x * c;
+        if (to > r + kMove) {
+            const float2 zz = unpair(z);
+            const float f = ex2f(r - to);
+            z = pair(zz.x * f, zz.y * f);
+            r = to;
+        }
+        const float ref = r == -INFINITY ? 0.f : -r;
+        const u64 r2 = pair(ref, ref), c2 = pair(c, c);
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 f = __half22float2(as_half2(word_at(q[i], j)));
+                const float2 y = unpair(fma2(pair(f.x, f.y), c2, r2));
+                z = add2(z, pair(ex2f(y.x), ex2f(y.y)));
+            }
+    }
+};
+
 // f(piece, id of its first logit) for all of the slice, several pieces in flight a thread.
 template <typename F>
 __device__ __forceinline__ void each_piece(const Slice& s, F f) {
@@ -291,14 +370,10 @@ __device__ __forceinline__ void each_piece(const Slice& s, F f) {
     }
 }
 
-__device__ __forceinline__ uint32_t word_at(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
-
 __device__ __forceinline__ uint32_t half_at(const uint4& v, int i) {
     const uint32_t w = word_at(v, i >> 1);
     return i & 1 ? w >> 16 : w & 0xFFFFu;
 }
-
-__device__ __forceinline__ __half2 as_half2(uint32_t w) { return *reinterpret_cast<const __half2*>(&w); }
 
 __device__ __forceinline__ uint32_t block_max(SampleShared& sh, uint32_t v) {
     v = __reduce_max_sync(kFull, v);
@@ -488,6 +563,7 @@ __device__ bool decide(const SampleShared& sh, const Scale& k, const Wish& wish,
         if (!f2.n || f2.n > kept_low) f2 = last;
     }
     if (!f1.n || f1.n != f2.n) return false;
+    if (high_sum - low_sum > low_sum >> 14) return false;  // the probability would be off
     *at = f1;
     *total = low_sum + (high_sum - low_sum) / 2;
     return true;
@@ -533,23 +609,63 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
     wish.m = m > 0.f ? m : 0.f;
     wish.u = u > 0.f ? fminf(u, 1.f) : 0.f;
 
+    double cd = fmin(fmax(1.4426950408889634074 / (greedy ? 1.0 : (double)temperature), 0x1p-100), 0x1p100);
+    Scale k;  // beyond 2^100 all but the largest logit have no weight, below 2^-100 all have the same
+    k.c = (float)cd;
+    k.c_low = (float)(cd - (double)k.c);
+    k.places = a.places;
+
     // look 1
-    uint32_t mine;
+    const bool all = wish.k == kAll && !(wish.p < 1.f) && !(wish.m > 0.f);
+    const bool sum = wish.k == kAll && wish.p < 1.f;
+    Look look;
     {
-        const __half2 none = as_half2(0xFC00FC00u);
-        __half2 m2[4] = {none, none, none, none};
-        each_piece(s, [&](const uint4& v, int) {
+        const uint4* pc = reinterpret_cast<const uint4*>(s.row + s.head);
+        const float c = fminf(k.c, 1e30f);  // times a logit it stays finite
+        int id;
+        if (s.first && s.head && tid == kThreads - 1) {
+            const uint4 one[1] = {edge_piece(s, 0, &id)};
+            look.add(one, kHead, sum, false, c);
+        }
+        if (s.last && s.tail && tid == kThreads - 2) {
+            const uint4 one[1] = {edge_piece(s, 1, &id)};
+            look.add(one, kTail, sum, false, c);
+        }
+        constexpr int kStep = kGroup * kThreads;
+        uint4 q[2][kGroup];  // a group, and the next one on its way
+        auto fetch = [&](uint4(&to)[kGroup], int v) {
+            if (v + (kGroup - 1) * kThreads < s.p1) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) m2[i] = __hmax2_nan(m2[i], as_half2(word_at(v, i)));
-        });
-        m2[0] = __hmax2_nan(__hmax2_nan(m2[0], m2[1]), __hmax2_nan(m2[2], m2[3]));
-        mine = max(order16(__half_as_ushort(__low2half(m2[0]))), order16(__half_as_ushort(__high2half(m2[0]))));
+                for (int j = 0; j < kGroup; ++j) to[j] = pc[v + j * kThreads];
+            }
+        };
+        int v = s.p0 + tid;
+        fetch(q[0], v);
+        while (v + (kGroup - 1) * kThreads < s.p1) {
+            fetch(q[1], v + kStep);
+            look.add(q[0], v, sum, false, c);
+            v += kStep;
+            if (v + (kGroup - 1) * kThreads >= s.p1) break;
+            fetch(q[0], v + kStep);
+            look.add(q[1], v, sum, false, c);
+            v += kStep;
+        }
+        uint4 rest[kGroup - 1];  // fewer than a group are left
+#pragma unroll
+        for (int j = 0; j < kGroup - 1; ++j)
+            if (v + j * kThreads < s.p1) rest[j] = pc[v + j * kThreads];
+#pragma unroll
+        for (int j = 0; j < kGroup - 1; ++j)
+            if (v + j * kThreads < s.p1) {
+                const uint4 one[1] = {rest[j]};
+                look.add(one, v + j * kThreads, sum, false, c);
+            }
     }
+    const uint32_t mine = look.bad ? 0xFFFFu : order16(__half_as_ushort(__float2half_rn(look.best)));
     const uint32_t cta_top = block_max(sh, mine);
     // The window's reach: with a top-k the k-th largest of the threads' maxima (k logits reach it at least), else the
     // 128th, which holds the likely tokens of a trained model's row; without any limit, and for more than there are
     // threads, all of the histogram.
-    const bool all = wish.k == kAll && !(wish.p < 1.f) && !(wish.m > 0.f);
     const int want = ((wish.k != kAll ? min(wish.k, kThreads * a.cluster + 1) : 128) + a.cluster - 1) / a.cluster;
     uint32_t reach = 0;
     if (greedy) {
@@ -579,20 +695,14 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
         }
         return;
     }
-    Scale k;
     k.top = value_of(top);
-    k.places = a.places;
-    {
-        // beyond 2^100 all but the largest logit have no weight, below 2^-100 all have the same
-        const double c = fmin(fmax(1.4426950408889634074 / (greedy ? 1.0 : (double)temperature), 0x1p-100), 0x1p100);
-        k.c = (float)c;
-        k.c_low = (float)(c - (double)k.c);
-    }
-    Command cmd = {kFirst, top, max(low, window_low(top)), wish.k == kAll, 0, 0, 0};
+    Command cmd = {kFirst, top, max(low, window_low(top)), kNoRest, 0, 0, 0};
+    const uint32_t rest_of = wish.k == kAll ? kRest : kNoRest;
     // many logits are counted in each CTA and gathered then, few where they are wanted
-    if (cmd.low == window_low(top) && !greedy) cmd.op = kWindow;
+    if (cmd.low == window_low(top) && !greedy) cmd.op = kWindow, cmd.rest = rest_of;
 
-    if (tid == 0) sh.before_count = 0, sh.before_sum = 0;
+    if (tid == 0) sh.before_count = 0, sh.before_sum = 0, sh.works = 0;
+    __syncthreads();
 
     // first CTA, first warp: where the search is
     enum { kTry, kCollect, kTopP, kMinP, kPick };
@@ -600,29 +710,107 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
     int windows = 0, kept = kAll, win = 0;  // win: the window that is loaded
     u64 kept_sum = 0;
 
+    // the weight below the window (a thread's, in FP32 and as it is) and the largest order there, to the first CTA
+    auto send_rest = [&](float part, u64 exact, uint32_t below) {
+        below = block_max(sh, below);
+        exact += __float2ull_rn(part * __uint_as_float((uint32_t)(k.places + 127) << 23));
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) exact += __shfl_xor_sync(kFull, exact, x);
+        if (lane == 0) sh.warp_sum[warp] = exact;
+        __syncthreads();
+        if (tid == 0) {
+            exact = 0;
+#pragma unroll
+            for (int i = 0; i < kWarps; ++i) exact += sh.warp_sum[i];
+            st_cluster(in_cta(smem_u32(&sh.rest[rank]), 0), exact);
+            st_cluster(in_cta(smem_u32(&sh.below[rank]), 0), below);
+        }
+    };
+
     for (;;) {
-        if (cmd.op == kFirst || cmd.op == kWindow) {
-            if (cmd.op == kWindow) {
-                clear((int)(cmd.high - cmd.low) + 1);
-                __syncthreads();
+        if (cmd.op == kFirst) {
+            // The groups that hold logits of the window, a piece a thread; all of a thread's pieces where a third of its
+            // groups does.
+            const uint32_t counts = in_cta(smem_u32(sh.count), 0), ids = in_cta(smem_u32(sh.lowest), 0);
+            const uint4* pc = reinterpret_cast<const uint4*>(s.row + s.head);
+            auto take = [&](const uint4& v, int id) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t o = order16(half_at(v, i));
+                    if (o >= cmd.low) {
+                        add_cluster(counts + (cmd.high - o) * 4, 1u);
+                        min_cluster(ids + (cmd.high - o) * 4, (uint32_t)(id + i));
+                    }
+                }
+            };
+            const float least = value_of(cmd.low);
+            const bool reaches = look.best >= least, two = look.second >= least, three = look.third >= least;
+            if (reaches && !three) {
+                const int i = atomicAdd(&sh.works, two ? 2 : 1);
+                sh.work[i] = look.at;
+                if (two) sh.work[i + 1] = look.second_at;
             }
+            __syncthreads();
+            for (int i = tid; i < sh.works * kGroup; i += kThreads) {
+                const int from = sh.work[i / kGroup], j = i % kGroup;
+                int id;
+                if (from < 0) {
+                    if (j) continue;
+                    const uint4 v = edge_piece(s, from == kTail, &id);
+                    take(v, id);
+                } else if (j == 0 || from + (kGroup - 1) * kThreads < s.p1) {  // an entry is a group, or one of the last pieces
+                    take(pc[from + j * kThreads], s.head + (from + j * kThreads) * 8);
+                }
+            }
+            for (unsigned left = __ballot_sync(kFull, three); left; left &= left - 1) {  // by its warp
+                const int from = warp * 32 + __ffs(left) - 1;
+                for (int v = s.p0 + from + lane * kThreads; v < s.p1; v += 32 * kThreads) take(pc[v], s.head + v * 8);
+                int id;
+                if (lane == 0 && from == kThreads - 1 && s.first && s.head) {
+                    const uint4 v = edge_piece(s, 0, &id);
+                    take(v, id);
+                }
+                if (lane == 0 && from == kThreads - 2 && s.last && s.tail) {
+                    const uint4 v = edge_piece(s, 1, &id);
+                    take(v, id);
+                }
+            }
+            if (sum) {
+                const float2 z = unpair(look.z);
+                send_rest((z.x + z.y) * ex2f(fmaxf(look.r - k.top * fminf(k.c, 1e30f), -1000.f)), 0, kLowest);
+            }
+        } else if (cmd.op == kWindow) {
+            clear((int)(cmd.high - cmd.low) + 1);
+            __syncthreads();
             const __half low_h = __ushort_as_half((unsigned short)unorder16(cmd.low));
             const __half2 low2 = __halves2half2(low_h, low_h);
-            const bool first = cmd.op == kFirst;
-            const uint32_t own = smem_u32(sh.count), counts = in_cta(own, 0), ids = in_cta(smem_u32(sh.lowest), 0);
-            const float c = k.c, t = k.top;
+            const uint32_t own = smem_u32(sh.count), span = cmd.high - cmd.low;
+            // t = (logit - top) c in three roundings of its own size: both factors' low words are kept
+            const float tc = __fmul_rn(k.top, k.c), tl = __fmaf_rn(k.top, k.c, -tc) + k.top * k.c_low;
+            const u64 c2 = pair(k.c, k.c), cl2 = pair(k.c_low, k.c_low), t2 = pair(-tc, -tc), tl2 = pair(-tl, -tl);
+            // -infinity stands for FP16's lowest value where that has no weight, two logits at a time; else its weight is
+            // taken off one by one
+            const bool apart = (-65504.f - k.top) * k.c > -200.f;
             __half2 b2 = as_half2(0xFC00FC00u);
-            float sum = 0.f;
-            each_piece(s, [&](const uint4& v, int id) {
+            float part = 0.f;
+            u64 exact = 0;
+            each_piece(s, [&](const uint4& v, int) {
                 const uint32_t any = __hge2_mask(as_half2(v.x), low2) | __hge2_mask(as_half2(v.y), low2) |
                                      __hge2_mask(as_half2(v.z), low2) | __hge2_mask(as_half2(v.w), low2);
                 float e[8];
-                if (cmd.rest) {
+                if (cmd.rest == kRest) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const float2 f = __half22float2(as_half2(word_at(v, i)));
-                        e[2 * i] = ex2f((f.x - t) * c);
-                        e[2 * i + 1] = ex2f((f.y - t) * c);
+                        const __half2 h = __hmax2(as_half2(word_at(v, i)), as_half2(0xFBFFFBFFu));
+                        const float2 f = __half22float2(h);
+                        const u64 x = pair(f.x, f.y);
+                        const float2 t = unpair(add2(fma2(x, c2, t2), fma2(x, cl2, tl2)));
+                        e[2 * i] = ex2f(t.x);
+                        e[2 * i + 1] = ex2f(t.y);
+                        if (apart) {
+                            if ((word_at(v, i) & 0xFFFFu) == 0xFC00u) e[2 * i] = 0.f;
+                            if (word_at(v, i) >> 16 == 0xFC00u) e[2 * i + 1] = 0.f;
+                        }
                     }
                 } else {
 #pragma unroll
@@ -631,42 +819,32 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
                 if (!any) {
                     b2 = __hmax2(b2, __hmax2(__hmax2(as_half2(v.x), as_half2(v.y)), __hmax2(as_half2(v.z), as_half2(v.w))));
                 } else {
+                    uint32_t under = 0;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const uint32_t h = half_at(v, i), o = order16(h);
-                        if (o >= cmd.low) {
-                            e[i] = 0.f;
-                            const uint32_t at = (cmd.high - o) * 4;
-                            if (o <= cmd.high) {
-                                if (first) {
-                                    add_cluster(counts + at, 1u);
-                                    min_cluster(ids + at, (uint32_t)(id + i));
-                                } else {
-                                    add_shared(own + at);
-                                }
-                            }
-                        } else {
-                            const __half x = __ushort_as_half((unsigned short)h);
-                            b2 = __hmax2(b2, __halves2half2(x, x));
+                    for (int i = 0; i < 4; ++i) {
+                        // the orders of two logits: -0 as +0, then the sign bit and, under it, the others turned
+                        const uint32_t h = as_word(__hadd2_rn(as_half2(word_at(v, i)), as_half2(0u)));
+                        const uint32_t o2 = h ^ (((h >> 15) & 0x00010001u) * 0xFFFFu | 0x80008000u);
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const uint32_t o = j ? o2 >> 16 : o2 & 0xFFFFu, d = cmd.high - o;
+                            if (d <= span) add_shared(own + d * 4);
+                            if (o >= cmd.low) e[2 * i + j] = 0.f;
+                            under = max(under, o >= cmd.low ? 0u : o);
                         }
                     }
+                    if (under) b2 = __hmax2(b2, __half2half2(__ushort_as_half((unsigned short)unorder16(under))));
                 }
-                sum += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+                part += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+                if (cmd.rest == kExactRest) {
+#pragma unroll 1
+                    for (int i = 0; i < 8; ++i) {
+                        const uint32_t o = order16(half_at(v, i));
+                        if (o < cmd.low && o >= kLowest) exact += weight_of(k, o);
+                    }
+                }
             });
-            const uint32_t below = block_max(sh, max(order16(__half_as_ushort(__low2half(b2))),
-                                                     order16(__half_as_ushort(__high2half(b2)))));
-            u64 d = __float2ull_rn(sum * __uint_as_float((uint32_t)(k.places + 127) << 23));
-#pragma unroll
-            for (int x = 16; x > 0; x >>= 1) d += __shfl_xor_sync(kFull, d, x);
-            if (lane == 0) sh.warp_sum[warp] = d;
-            __syncthreads();
-            if (tid == 0) {
-                d = 0;
-#pragma unroll
-                for (int i = 0; i < kWarps; ++i) d += sh.warp_sum[i];
-                st_cluster(in_cta(smem_u32(&sh.rest[rank]), 0), d);
-                st_cluster(in_cta(smem_u32(&sh.below[rank]), 0), below);
-            }
+            send_rest(part, exact, max(order16(__half_as_ushort(__low2half(b2))), order16(__half_as_ushort(__high2half(b2)))));
         } else {  // tokens of one logit, warp by warp in the order of their ids
             const int n = s.p1 - s.p0, w0 = s.p0 + (int)((int64_t)n * warp / kWarps),
                       w1 = s.p0 + (int)((int64_t)n * (warp + 1) / kWarps);
@@ -747,28 +925,44 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
                 }
                 uint32_t below = 0;
                 u64 rest = 0;
-                for (int i = 0; i < a.cluster; ++i) {
-                    below = max(below, sh.below[i]);
-                    rest += sh.rest[i];
-                }
-                const bool more = below >= kLowest;
+                if (cmd.op == kWindow || sum)
+                    for (int i = 0; i < a.cluster; ++i) {
+                        below = max(below, sh.below[i]);
+                        rest += sh.rest[i];
+                    }
                 const Window w = window_sums(sh, k, cmd.high, cmd.low, sh.before_count, sh.before_sum);
                 if (warp == 0) {  // the search is one warp's
                     Found at = {};
                     u64 total = 0;
                     bool done = false;
+                    bool more = below >= kLowest;
                     if (stage == kTry) {
-                        // A weight below the window is off by 2^-24 for each of: the sums of its thread's pieces, 3 |t|
-                        // ln 2 of its exponent t (60 at most, below which all of them together are under 2^-36 of the
-                        // largest's) and 4 of the power itself; and by a place of its thread's sum.
-                        const u64 units = (u64)((s.p1 - s.p0) / kThreads + 160);
-                        const u64 error = more ? (rest >> 24) * units + units + kThreads * kMaxCluster +
-                                                     ((u64)a.vocab >> (60 - k.places)) : 0;
-                        done = decide(sh, k, wish, w, more, more ? rest : 0, error, &at, &total);
-                        if (!done && cmd.low > window_low(top)) {
-                            next = {kWindow, top, window_low(top), wish.k == kAll, 0, 0, 0};
-                        } else if (!done) {
-                            stage = kCollect;
+                        // The error of a weight, in steps of 2^-24: of the sums of its thread's pieces; of its exponent t
+                        // (three roundings of |t| ln 2, 60 at most: all weights under 2^-60 together are under 2^-36 of
+                        // the largest's); of the power, 4; and a place of its thread's sum.  In the first look there is
+                        // a reference in place of the largest, and one rounding of its size and of the logit's
+                        // in the exponent: 2 |c top| and |c logit|, 60 more, ln 2 each.
+                        u64 error = 0;
+                        const u64 spare = kThreads * kMaxCluster + ((u64)a.vocab >> (60 - k.places));
+                        u64 units = (u64)((s.p1 - s.p0) / kThreads + 4 + 6 + 42 + 42 + 42);
+                        if (cmd.op == kFirst) {
+                            more = w.count < a.vocab;
+                            units += (u64)(3.f * fminf(fabsf(k.top) * k.c, 1e9f)) + 300;
+                            error = sum ? (rest >> 24) * units + units + spare : 1ull << 61;  // (not known)
+                            rest = !sum ? error : rest > w.sum ? rest - w.sum : 0;
+                        } else if (cmd.rest == kRest) {
+                            error = (rest >> 24) * units + units + spare;
+                        }
+                        if (!more) rest = error = 0;
+                        done = decide(sh, k, wish, w, more, rest, error, &at, &total);
+                        if (!done) {
+                            // all of the histogram, then what lies below it exactly
+                            if (cmd.op == kFirst)
+                                next = {kWindow, top, window_low(top), rest_of, 0, 0, 0};
+                            else if (cmd.rest == kRest && more)
+                                next = {kWindow, top, window_low(top), kExactRest, 0, 0, 0};
+                            else
+                                stage = kCollect;
                         }
                     }
                     if (stage >= kCollect) {
