@@ -34,6 +34,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kMaxVocab = 1 << 24;
 constexpr int kBins = 4096;              // places of the window
+constexpr int kList = 1024;              // logits of the first window whose ids are kept
 constexpr int kMaxWindows = 65536 / kBins + 2;
 constexpr uint32_t kLowest = 0x0400;     // order of -65504, the lowest logit that can be drawn
 constexpr uint32_t kInfinite = 0xFC00;   // order of +infinity; NaN lies above
@@ -131,7 +132,8 @@ __device__ __forceinline__ Power exp2_of(float2 p) {
     return {__umul64hi(kRoots[(int)j + 32], x), (int)n};
 }
 
-__device__ __forceinline__ u64 weight_of(const Scale& k, uint32_t order) {
+// (One copy: what the search costs is mostly the way of its instructions into the SM.)
+__device__ __noinline__ u64 weight_of(Scale k, uint32_t order) {
     const float2 p = power_of(k, value_of(order));
     if (!(p.x > -70.f)) return 0;
     const Power w = exp2_of(p);
@@ -140,7 +142,7 @@ __device__ __forceinline__ u64 weight_of(const Scale& k, uint32_t order) {
 }
 
 // Whether a logit's weight is at least m times the largest's.
-__device__ __forceinline__ bool at_least(const Scale& k, uint32_t order, float m) {
+__device__ __noinline__ bool at_least(Scale k, uint32_t order, float m) {
     const float2 p = power_of(k, value_of(order));
     if (!(p.x > -200.f)) return false;
     const Power w = exp2_of(p);
@@ -191,8 +193,10 @@ __device__ __forceinline__ uint4 ld_cluster(uint32_t addr) {
 __device__ __forceinline__ void add_cluster(uint32_t addr, uint32_t v) {
     asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
-__device__ __forceinline__ void min_cluster(uint32_t addr, uint32_t v) {
-    asm volatile("red.relaxed.cluster.shared::cluster.min.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+__device__ __forceinline__ uint32_t next_cluster(uint32_t addr) {
+    uint32_t v;
+    asm volatile("atom.relaxed.cluster.shared::cluster.add.u32 %0, [%1], 1;" : "=r"(v) : "r"(addr) : "memory");
+    return v;
 }
 __device__ __forceinline__ void add_shared(uint32_t addr) {
     asm volatile("red.relaxed.cta.shared::cta.add.u32 [%0], %1;" ::"r"(addr), "r"(1u) : "memory");
@@ -214,7 +218,7 @@ enum { kDone, kFirst, kWindow, kTie, kScan };
 enum { kNoRest, kRest, kExactRest };  // what lies below a window: left out, summed in FP32, or as the search's weights
 
 struct Command {
-    uint32_t op;         // kFirst: the first window, its counts and lowest ids gathered in the first CTA; kWindow: another,
+    uint32_t op;         // kFirst: the first window, its counts and logits gathered in the first CTA; kWindow: another,
                          // counts in each CTA; kTie, kScan: the drawn logit's tokens
     uint32_t high, low;  // the orders from `high` down to `low`
     uint32_t rest;       // kWindow: what is done with what lies below
@@ -223,9 +227,30 @@ struct Command {
     uint32_t who;        // ... of the cluster
 };
 
+// The window as the search sees it: bins from `high` down, `own` of them a thread, and what lies before.
+struct Window {
+    uint32_t high, low;
+    int own, before, count;  // tokens before it, and up to its end
+    u64 above, sum;          // weights
+};
+
+struct Found {      // a place in the order
+    int n;          // tokens up to and with it (0: not in the window)
+    uint32_t order; // its logit
+    int tie;        // tokens of that logit before it
+    u64 sum;        // weight up to and with it
+};
+
+struct Ending {     // what one end of the bound gives
+    int ok, kept;
+    u64 total;      // the kept weight
+    Found at;       // the drawn place
+};
+
 struct __align__(16) SampleShared {
     uint32_t count[kBins];
-    uint32_t lowest[kBins];
+    uint2 list[kList];                  // the first window's logits: order and id
+    uint32_t listed;
     u64 sum_to[kThreads];               // weight and tokens up to each thread's last bin
     int count_to[kThreads];
     u64 warp_sum[kWarps];
@@ -236,10 +261,15 @@ struct __align__(16) SampleShared {
     uint32_t ties[kMaxCluster * kWarps];
     uint32_t warp_word[kWarps];
     Command cmd, next;
+    Scale scale;                        // what the search works with
+    Window window;
+    Found found[4];                     // two ends of a bound: a place, the last kept
+    Ending ending[2];
     int work[2 * kThreads];             // first pieces of groups to look at again
     int works;
     u64 before_sum;                     // weight and tokens above the window that is loaded
     int before_count;
+    int trying;                         // whether the window is a try's
     u64 win_sum[kMaxWindows];           // the search to the end: weight and tokens above each window,
     int win_count[kMaxWindows];         // and its bounds
     uint32_t win_high[kMaxWindows], win_low[kMaxWindows];
@@ -382,17 +412,74 @@ __device__ __forceinline__ uint32_t block_max(SampleShared& sh, uint32_t v) {
     return __reduce_max_sync(kFull, sh.warp_word[threadIdx.x & (kWarps - 1)]);
 }
 
+// One look of a CTA for a window: counts of the orders from `high` down to `low` (cleared before) by shared-memory atomics;
+// returns the largest order below, a thread's, and adds the weight there to *weight.  The orders and what is
+// masked for the sum are worked out two logits at a time.
+template <int REST, bool APART>
+__device__ __forceinline__ uint32_t count_window(const Slice& s, const Scale& k, uint32_t high, uint32_t low,
+                                                 uint32_t counts, u64* weight) {
+    const __half low_h = __ushort_as_half((unsigned short)unorder16(low));
+    const __half2 low2 = __halves2half2(low_h, low_h);
+    const uint32_t span = high - low;
+    // t = (logit - top) c in two roundings of its own size: both factors' low words are kept
+    const float tc = __fmul_rn(k.top, k.c), tl = __fmaf_rn(k.top, k.c, -tc) + k.top * k.c_low;
+    const u64 c2 = pair(k.c, k.c), cl2 = pair(k.c_low, k.c_low), t2 = pair(-tc, -tc), tl2 = pair(-tl, -tl);
+    const float unit = __uint_as_float((uint32_t)(k.places + 127) << 23);
+    __half2 b2 = as_half2(0xFC00FC00u);
+    u64 sum = 0;
+    each_piece(s, [&](const uint4& v, int) {
+        u64 part = 0;
+        uint32_t in[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t w = word_at(v, i);
+            in[i] = __hge2_mask(as_half2(w), low2);
+            const uint32_t under = (w & ~in[i]) | (in[i] & 0xFC00FC00u);  // -infinity in place of the window's
+            b2 = __hmax2(b2, as_half2(under));
+            if (REST == kRest) {
+                const float2 f = __half22float2(__hmax2(as_half2(under), as_half2(0xFBFFFBFFu)));
+                const u64 x = pair(f.x, f.y);
+                const float2 t = unpair(add2(fma2(x, c2, t2), fma2(x, cl2, tl2)));
+                float2 e = make_float2(ex2f(t.x), ex2f(t.y));
+                if (APART) {
+                    if ((under & 0xFFFFu) == 0xFC00u) e.x = 0.f;
+                    if (under >> 16 == 0xFC00u) e.y = 0.f;
+                }
+                part = i ? add2(part, pair(e.x, e.y)) : pair(e.x, e.y);
+            }
+            if (REST == kExactRest) {
+#pragma unroll 1
+                for (int j = 0; j < 2; ++j) {
+                    const uint32_t o = order16((under >> (16 * j)) & 0xFFFFu);
+                    if (o >= kLowest) sum += weight_of(k, o);
+                }
+            }
+        }
+        if (REST == kRest) {
+            const float2 f = unpair(part);
+            sum += __float2ull_rn((f.x + f.y) * unit);
+        }
+        if ((in[0] | in[1]) | (in[2] | in[3])) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                // the orders of two logits: -0 as +0, then the sign bit and, under it, the others turned
+                const uint32_t h = as_word(__hadd2_rn(as_half2(word_at(v, i)), as_half2(0u)));
+                const uint32_t o = h ^ ((((h >> 15) & 0x00010001u) * 0xFFFFu) | 0x80008000u);
+                const uint32_t d0 = high - (o & 0xFFFFu), d1 = high - (o >> 16);
+                if (d0 <= span) add_shared(counts + d0 * 4);
+                if (d1 <= span) add_shared(counts + d1 * 4);
+            }
+        }
+    });
+    *weight += sum;
+    return max(order16(as_word(b2) & 0xFFFFu), order16(as_word(b2) >> 16));
+}
+
 // ---- the first CTA's search in the window -----------------------------------------
 
-// The window as the search sees it: bins from `high` down, `own` of them a thread, and what lies before.
-struct Window {
-    uint32_t high, low;
-    int own, before, count;  // tokens before it, and up to its end
-    u64 above, sum;          // weights
-};
-
 // Sums up to every thread's bins. The whole CTA.
-__device__ Window window_sums(SampleShared& sh, const Scale& k, uint32_t high, uint32_t low, int before, u64 above) {
+__device__ __forceinline__ void window_sums(SampleShared& sh, uint32_t high, uint32_t low, int before, u64 above) {
+    const Scale k = sh.scale;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int bins = (int)(high - low) + 1, own = (bins + kThreads - 1) / kThreads;
     const int lo = min(tid * own, bins), hi = min(lo + own, bins);
@@ -422,25 +509,22 @@ __device__ Window window_sums(SampleShared& sh, const Scale& k, uint32_t high, u
     }
     sh.count_to[tid] = n;
     sh.sum_to[tid] = w;
+    if (tid == 0) sh.window = o;
     __syncthreads();
-    return o;
 }
-
-struct Found {      // a place in the order
-    int n;          // tokens up to and with it (0: not in the window)
-    uint32_t order; // its logit
-    int tie;        // tokens of that logit before it
-    u64 sum;        // weight up to and with it
-};
 
 enum { kByCount, kReach, kPass };  // the n-th token; the first at which the weight reaches, or passes, s
 
-// The whole of one warp.
-template <int HOW>
-__device__ Found find(const SampleShared& sh, const Scale& k, const Window& w, int n, u64 s) {
+// The whole of one warp; n = 0 in *out where the window has no such place.
+__device__ __noinline__ void find(const SampleShared& sh, int how, int n, u64 s, Found* out) {
     const int lane = threadIdx.x & 31;
-    auto there = [&](int count, u64 sum) { return HOW == kByCount ? count >= n : HOW == kReach ? sum >= s : sum > s; };
-    if (!there(w.count, w.sum)) return {};
+    const Window w = sh.window;
+    auto there = [&](int count, u64 sum) { return how == kByCount ? count >= n : how == kReach ? sum >= s : sum > s; };
+    if (!there(w.count, w.sum)) {
+        if (lane == 0) out->n = 0;
+        __syncwarp();
+        return;
+    }
     // the thread, then its bin
     constexpr int kStride = kThreads / 32;
     const int last = (lane + 1) * kStride - 1;
@@ -451,11 +535,11 @@ __device__ Found find(const SampleShared& sh, const Scale& k, const Window& w, i
     const u64 s0 = thread ? sh.sum_to[thread - 1] : w.above;
     const int bins = (int)(w.high - w.low) + 1, i = thread * w.own + lane;
     const int c = lane < w.own && i < bins ? (int)sh.count[i] : 0;  // own is 16 at most
-    const u64 weight = c ? weight_of(k, w.high - i) : 0;
+    const u64 weight = c ? weight_of(sh.scale, w.high - i) : 0;
     int ni = c;
     u64 si = c * weight;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
+#pragma unroll 1
+    for (int d = 1; d < 16; d <<= 1) {
         const int pn = __shfl_up_sync(kFull, ni, d);
         const u64 ps = __shfl_up_sync(kFull, si, d);
         if (lane >= d) ni += pn, si += ps;
@@ -463,27 +547,27 @@ __device__ Found find(const SampleShared& sh, const Scale& k, const Window& w, i
     ni += n0;
     si += s0;
     const int at = __ffs(__ballot_sync(kFull, there(ni, si))) - 1;
-    const int cb = __shfl_sync(kFull, c, at), from_n = __shfl_sync(kFull, ni, at) - cb;
-    const u64 wb = __shfl_sync(kFull, weight, at), from_s = __shfl_sync(kFull, si, at) - cb * wb;
-    int m;
-    if (HOW == kByCount)
-        m = n - from_n;
-    else if (HOW == kReach)
-        m = wb ? (int)((s - from_s + wb - 1) / wb) : 1;  // s is past from_s: the bin has a weight, or s is 0
-    else
-        m = (int)((s - from_s) / wb) + 1;
-    m = max(m, 1);
-    return {from_n + m, w.high - (uint32_t)(thread * w.own + at), m - 1, from_s + m * wb};
+    if (lane == at) {
+        const int from_n = ni - c;
+        const u64 from_s = si - c * weight;
+        // with a target by weight the bin has one, or the target is 0
+        int m = n - from_n;
+        if (how != kByCount) m = weight ? (int)((s - from_s + (how == kReach ? weight - 1 : weight)) / weight) : 1;
+        m = max(m, 1);
+        *out = {from_n + m, w.high - (uint32_t)i, m - 1, from_s + m * weight};
+    }
+    __syncwarp();
 }
 
-// The last token of at least m times the largest weight (n: w.before where the window has none): its bins are cut
-// by halving, 32 at once. *end: the window's last logit is still kept.  The whole of one warp.
-__device__ Found find_min(const SampleShared& sh, const Scale& k, const Window& w, float m, bool* end) {
+// The last token of at least m times the largest weight, the first in any case: its bins are cut by halving, 32 at
+// once.  Only tokens and weight; returns whether the window's last logit is still kept.  The whole of one warp.
+__device__ __noinline__ bool find_min(const SampleShared& sh, float m, Found* out) {
+    const Window w = sh.window;
     const int lane = threadIdx.x & 31, bins = (int)(w.high - w.low) + 1;
     int lo = 0, hi = bins;  // the first bin that is not kept lies in [lo, hi]
     while (lo < hi) {
         const int step = (hi - lo + 31) >> 5, i = lo + lane * step;
-        const unsigned kept = __ballot_sync(kFull, i < hi && at_least(k, w.high - i, m));
+        const unsigned kept = __ballot_sync(kFull, i < hi && at_least(sh.scale, w.high - i, m));
         const int n = __popc(kept);  // the kept ones come first
         if (n == 0) {
             hi = lo;
@@ -493,16 +577,21 @@ __device__ Found find_min(const SampleShared& sh, const Scale& k, const Window& 
             lo = first;
         }
     }
-    *end = lo == bins;
     const int thread = lo / w.own, i = thread * w.own + lane;
     int n = thread ? sh.count_to[thread - 1] : w.before;
     u64 s = thread ? sh.sum_to[thread - 1] : w.above;
     const int c = i < lo && lane < w.own ? (int)sh.count[i] : 0;
-    u64 si = c ? c * weight_of(k, w.high - i) : 0;
+    u64 si = c ? c * weight_of(sh.scale, w.high - i) : 0;
     n += (int)__reduce_add_sync(kFull, (unsigned)c);
-#pragma unroll
+#pragma unroll 1
     for (int d = 16; d > 0; d >>= 1) si += __shfl_xor_sync(kFull, si, d);
-    return {n, 0, 0, s + si};
+    if (n == 0) {
+        find(sh, kByCount, 1, 0, out);
+    } else {
+        if (lane == 0) *out = {n, 0, 0, s + si};
+        __syncwarp();
+    }
+    return lo == bins;
 }
 
 // What a row asks for.
@@ -513,60 +602,47 @@ struct Wish {
     float u;   // 1: the last
 };
 
-__device__ __forceinline__ Found find_top_p(const SampleShared& sh, const Scale& k, const Window& w, float p, u64 sum) {
+__device__ __forceinline__ void find_top_p(const SampleShared& sh, float p, u64 sum, Found* out) {
     const u64 s = times(p, sum, true);
-    return s ? find<kReach>(sh, k, w, 0, s) : find<kByCount>(sh, k, w, 1, 0);  // the first is always kept
+    find(sh, s ? kReach : kByCount, 1, s, out);  // the first is always kept
 }
 
-// One try with the window from the row's maximum down: true and *at, *total (the drawn place, the kept
-// weight) where it is certain.  rest, error: the weight below the window and its bound.  One warp.
-__device__ bool decide(const SampleShared& sh, const Scale& k, const Wish& wish, const Window& w, bool more, u64 rest,
-                       u64 error, Found* at, u64* total) {
+// What the window from the row's maximum down gives, `below` being the weight that lies under it (more: anything
+// does): ok = 0 where it does not say.  One warp, with two places of its own.
+__device__ __noinline__ void decide(SampleShared& sh, const Wish& wish, bool more, u64 below, Found* f, Ending* out) {
+    const int lane = threadIdx.x & 31;
+    const int count = sh.window.count;
+    if (lane == 0) out->ok = 0;
     int kept = kAll;  // tokens kept, kAll: all of the row
-    u64 low_sum, high_sum;  // bounds of the kept weight
-    if (wish.k <= w.count || !more) {
-        kept = min(wish.k, w.count);
-        low_sum = high_sum = find<kByCount>(sh, k, w, kept, 0).sum;
-    } else if (wish.k == kAll) {
-        low_sum = w.sum + (rest > error ? rest - error : 0);
-        high_sum = w.sum + rest + error;
-    } else {
-        return false;  // the k-th lies below
+    u64 total = sh.window.sum + below;
+    if (wish.k <= count || !more) {
+        kept = min(wish.k, count);
+        find(sh, kByCount, kept, 0, &f[1]);
+        total = f[1].sum;
+    } else if (wish.k != kAll) {
+        return;  // the k-th lies below
     }
-    int kept_low = kept, kept_high = kept;
     if (wish.p < 1.f) {
-        const Found f1 = find_top_p(sh, k, w, wish.p, low_sum);
-        const Found f2 = low_sum == high_sum ? f1 : find_top_p(sh, k, w, wish.p, high_sum);
-        if (!f1.n) kept_low = kBeyond;
-        else if (f1.n <= kept) kept_low = f1.n, low_sum = f1.sum;
-        if (!f2.n) kept_high = kBeyond;
-        else if (f2.n <= kept) kept_high = f2.n, high_sum = f2.sum;
+        find_top_p(sh, wish.p, total, &f[0]);
+        const int n = f[0].n;
+        if (!n) kept = kBeyond;
+        else if (n <= kept) kept = n, total = f[0].sum;
     }
     if (wish.m > 0.f) {
-        bool end;
-        Found f = find_min(sh, k, w, wish.m, &end);
-        if (f.n == 0) f = find<kByCount>(sh, k, w, 1, 0);  // the first is always kept
-        if (!(end && more)) {
-            if (f.n < kept_low) kept_low = f.n, low_sum = f.sum;
-            if (f.n < kept_high) kept_high = f.n, high_sum = f.sum;
-        }
+        const bool end = find_min(sh, wish.m, &f[0]);
+        if (!(end && more) && f[0].n < kept) kept = f[0].n, total = f[0].sum;
     }
-    if (kept_low != kept_high || kept_low == kBeyond) return false;
-    Found f1 = {}, f2 = {};
-    if (wish.u < 1.f) {
-        f1 = find<kPass>(sh, k, w, 0, times(wish.u, low_sum, false));
-        f2 = low_sum == high_sum ? f1 : find<kPass>(sh, k, w, 0, times(wish.u, high_sum, false));
+    if (kept == kBeyond) return;
+    __syncwarp();
+    if (lane == 0) f[0].n = 0;
+    __syncwarp();
+    if (wish.u < 1.f) find(sh, kPass, 0, times(wish.u, total, false), &f[0]);
+    if (kept != kAll && (!f[0].n || f[0].n > kept)) {
+        __syncwarp();
+        find(sh, kByCount, kept, 0, &f[0]);
     }
-    if (kept_low != kAll && (!f1.n || f1.n > kept_low || !f2.n || f2.n > kept_low)) {
-        const Found last = find<kByCount>(sh, k, w, kept_low, 0);
-        if (!f1.n || f1.n > kept_low) f1 = last;
-        if (!f2.n || f2.n > kept_low) f2 = last;
-    }
-    if (!f1.n || f1.n != f2.n) return false;
-    if (high_sum - low_sum > low_sum >> 14) return false;  // the probability would be off
-    *at = f1;
-    *total = low_sum + (high_sum - low_sum) / 2;
-    return true;
+    if (lane == 0) *out = {f[0].n != 0, kept, total, f[0]};
+    __syncwarp();
 }
 
 // ---- the kernel ---------------------------------------------------------------------
@@ -581,7 +657,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
     };
     if (rank == 0) {
         clear(kBins);
-        for (int i = tid; i < kBins; i += kThreads) sh.lowest[i] = 0xFFFFFFFFu;
+        if (tid == 0) sh.listed = 0;
     }
     pdl_wait();
     pdl_launch_dependents();
@@ -609,11 +685,15 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
     wish.m = m > 0.f ? m : 0.f;
     wish.u = u > 0.f ? fminf(u, 1.f) : 0.f;
 
-    double cd = fmin(fmax(1.4426950408889634074 / (greedy ? 1.0 : (double)temperature), 0x1p-100), 0x1p100);
-    Scale k;  // beyond 2^100 all but the largest logit have no weight, below 2^-100 all have the same
-    k.c = (float)cd;
-    k.c_low = (float)(cd - (double)k.c);
-    k.places = a.places;
+    Scale k;
+    {
+        // log2(e) / temperature in two words; beyond 2^100 all but the largest logit have no weight, below 2^-100
+        // all have the same
+        const float t = greedy ? 1.f : fminf(fmaxf(temperature, 0x1p-99f), 0x1p99f);
+        k.c = __fdiv_rn(1.44269502162933349609f, t);
+        k.c_low = __fdiv_rn(__fmaf_rn(-k.c, t, 1.44269502162933349609f) + 1.9259629911266174681e-8f, t);
+        k.places = a.places;
+    }
 
     // look 1
     const bool all = wish.k == kAll && !(wish.p < 1.f) && !(wish.m > 0.f);
@@ -622,15 +702,6 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
     {
         const uint4* pc = reinterpret_cast<const uint4*>(s.row + s.head);
         const float c = fminf(k.c, 1e30f);  // times a logit it stays finite
-        int id;
-        if (s.first && s.head && tid == kThreads - 1) {
-            const uint4 one[1] = {edge_piece(s, 0, &id)};
-            look.add(one, kHead, sum, false, c);
-        }
-        if (s.last && s.tail && tid == kThreads - 2) {
-            const uint4 one[1] = {edge_piece(s, 1, &id)};
-            look.add(one, kTail, sum, false, c);
-        }
         constexpr int kStep = kGroup * kThreads;
         uint4 q[2][kGroup];  // a group, and the next one on its way
         auto fetch = [&](uint4(&to)[kGroup], int v) {
@@ -650,16 +721,27 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
             look.add(q[1], v, sum, false, c);
             v += kStep;
         }
-        uint4 rest[kGroup - 1];  // fewer than a group are left
+        // fewer than a group are left, and the row's ends
+        uint4 rest[kGroup + 1];
+        int at[kGroup + 1], id;
 #pragma unroll
-        for (int j = 0; j < kGroup - 1; ++j)
-            if (v + j * kThreads < s.p1) rest[j] = pc[v + j * kThreads];
+        for (int j = 0; j < kGroup - 1; ++j) {
+            at[j] = v + j * kThreads < s.p1 ? v + j * kThreads : kNone;
+            if (at[j] != kNone) rest[j] = pc[at[j]];
+        }
+        at[kGroup - 1] = s.first && s.head && tid == kThreads - 1 ? kHead : kNone;
+        at[kGroup] = s.last && s.tail && tid == kThreads - 2 ? kTail : kNone;
+        if (at[kGroup - 1] != kNone) rest[kGroup - 1] = edge_piece(s, 0, &id);
+        if (at[kGroup] != kNone) rest[kGroup] = edge_piece(s, 1, &id);
+#pragma unroll 1
+        for (int j = 0; j <= kGroup; ++j) {
+            uint4 one[1] = {rest[0]};
+            int from = at[0];
 #pragma unroll
-        for (int j = 0; j < kGroup - 1; ++j)
-            if (v + j * kThreads < s.p1) {
-                const uint4 one[1] = {rest[j]};
-                look.add(one, v + j * kThreads, sum, false, c);
-            }
+            for (int i = 1; i <= kGroup; ++i)
+                if (j == i) one[0] = rest[i], from = at[i];
+            if (from != kNone) look.add(one, from, sum, false, c);
+        }
     }
     const uint32_t mine = look.bad ? 0xFFFFu : order16(__half_as_ushort(__float2half_rn(look.best)));
     const uint32_t cta_top = block_max(sh, mine);
@@ -701,19 +783,19 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
     // many logits are counted in each CTA and gathered then, few where they are wanted
     if (cmd.low == window_low(top) && !greedy) cmd.op = kWindow, cmd.rest = rest_of;
 
-    if (tid == 0) sh.before_count = 0, sh.before_sum = 0, sh.works = 0;
+    if (tid == 0) sh.before_count = 0, sh.before_sum = 0, sh.works = 0, sh.trying = 1, sh.scale = k;
     __syncthreads();
 
     // first CTA, first warp: where the search is
     enum { kTry, kCollect, kTopP, kMinP, kPick };
     int stage = kTry;
     int windows = 0, kept = kAll, win = 0;  // win: the window that is loaded
+    u64 whole = 0;                          // the row's weight, where that is known exactly
     u64 kept_sum = 0;
 
-    // the weight below the window (a thread's, in FP32 and as it is) and the largest order there, to the first CTA
-    auto send_rest = [&](float part, u64 exact, uint32_t below) {
+    // the weight below the window and the largest order there, a thread's, to the first CTA
+    auto send_rest = [&](u64 exact, uint32_t below) {
         below = block_max(sh, below);
-        exact += __float2ull_rn(part * __uint_as_float((uint32_t)(k.places + 127) << 23));
 #pragma unroll
         for (int x = 16; x > 0; x >>= 1) exact += __shfl_xor_sync(kFull, exact, x);
         if (lane == 0) sh.warp_sum[warp] = exact;
@@ -731,7 +813,8 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
         if (cmd.op == kFirst) {
             // The groups that hold logits of the window, a piece a thread; all of a thread's pieces where a third of its
             // groups does.
-            const uint32_t counts = in_cta(smem_u32(sh.count), 0), ids = in_cta(smem_u32(sh.lowest), 0);
+            const uint32_t counts = in_cta(smem_u32(sh.count), 0), list = in_cta(smem_u32(sh.list), 0),
+                           listed = in_cta(smem_u32(&sh.listed), 0);
             const uint4* pc = reinterpret_cast<const uint4*>(s.row + s.head);
             auto take = [&](const uint4& v, int id) {
 #pragma unroll
@@ -739,7 +822,8 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
                     const uint32_t o = order16(half_at(v, i));
                     if (o >= cmd.low) {
                         add_cluster(counts + (cmd.high - o) * 4, 1u);
-                        min_cluster(ids + (cmd.high - o) * 4, (uint32_t)(id + i));
+                        const uint32_t at = next_cluster(listed);
+                        if (at < kList) st_cluster(list + at * 8, (u64)(uint32_t)(id + i) << 32 | o);
                     }
                 }
             };
@@ -777,74 +861,24 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
             }
             if (sum) {
                 const float2 z = unpair(look.z);
-                send_rest((z.x + z.y) * ex2f(fmaxf(look.r - k.top * fminf(k.c, 1e30f), -1000.f)), 0, kLowest);
+                const float f = (z.x + z.y) * ex2f(fmaxf(look.r - k.top * fminf(k.c, 1e30f), -1000.f));
+                send_rest(__float2ull_rn(f * __uint_as_float((uint32_t)(k.places + 127) << 23)), kLowest);
             }
         } else if (cmd.op == kWindow) {
             clear((int)(cmd.high - cmd.low) + 1);
             __syncthreads();
-            const __half low_h = __ushort_as_half((unsigned short)unorder16(cmd.low));
-            const __half2 low2 = __halves2half2(low_h, low_h);
-            const uint32_t own = smem_u32(sh.count), span = cmd.high - cmd.low;
-            // t = (logit - top) c in three roundings of its own size: both factors' low words are kept
-            const float tc = __fmul_rn(k.top, k.c), tl = __fmaf_rn(k.top, k.c, -tc) + k.top * k.c_low;
-            const u64 c2 = pair(k.c, k.c), cl2 = pair(k.c_low, k.c_low), t2 = pair(-tc, -tc), tl2 = pair(-tl, -tl);
-            // -infinity stands for FP16's lowest value where that has no weight, two logits at a time; else its weight is
-            // taken off one by one
-            const bool apart = (-65504.f - k.top) * k.c > -200.f;
-            __half2 b2 = as_half2(0xFC00FC00u);
-            float part = 0.f;
             u64 exact = 0;
-            each_piece(s, [&](const uint4& v, int) {
-                const uint32_t any = __hge2_mask(as_half2(v.x), low2) | __hge2_mask(as_half2(v.y), low2) |
-                                     __hge2_mask(as_half2(v.z), low2) | __hge2_mask(as_half2(v.w), low2);
-                float e[8];
-                if (cmd.rest == kRest) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const __half2 h = __hmax2(as_half2(word_at(v, i)), as_half2(0xFBFFFBFFu));
-                        const float2 f = __half22float2(h);
-                        const u64 x = pair(f.x, f.y);
-                        const float2 t = unpair(add2(fma2(x, c2, t2), fma2(x, cl2, tl2)));
-                        e[2 * i] = ex2f(t.x);
-                        e[2 * i + 1] = ex2f(t.y);
-                        if (apart) {
-                            if ((word_at(v, i) & 0xFFFFu) == 0xFC00u) e[2 * i] = 0.f;
-                            if (word_at(v, i) >> 16 == 0xFC00u) e[2 * i + 1] = 0.f;
-                        }
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) e[i] = 0.f;
-                }
-                if (!any) {
-                    b2 = __hmax2(b2, __hmax2(__hmax2(as_half2(v.x), as_half2(v.y)), __hmax2(as_half2(v.z), as_half2(v.w))));
-                } else {
-                    uint32_t under = 0;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        // the orders of two logits: -0 as +0, then the sign bit and, under it, the others turned
-                        const uint32_t h = as_word(__hadd2_rn(as_half2(word_at(v, i)), as_half2(0u)));
-                        const uint32_t o2 = h ^ (((h >> 15) & 0x00010001u) * 0xFFFFu | 0x80008000u);
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            const uint32_t o = j ? o2 >> 16 : o2 & 0xFFFFu, d = cmd.high - o;
-                            if (d <= span) add_shared(own + d * 4);
-                            if (o >= cmd.low) e[2 * i + j] = 0.f;
-                            under = max(under, o >= cmd.low ? 0u : o);
-                        }
-                    }
-                    if (under) b2 = __hmax2(b2, __half2half2(__ushort_as_half((unsigned short)unorder16(under))));
-                }
-                part += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
-                if (cmd.rest == kExactRest) {
-#pragma unroll 1
-                    for (int i = 0; i < 8; ++i) {
-                        const uint32_t o = order16(half_at(v, i));
-                        if (o < cmd.low && o >= kLowest) exact += weight_of(k, o);
-                    }
-                }
-            });
-            send_rest(part, exact, max(order16(__half_as_ushort(__low2half(b2))), order16(__half_as_ushort(__high2half(b2)))));
+            uint32_t under;
+            // -infinity stands for FP16's lowest value where that has no weight; else it is told apart
+            const bool apart = (-65504.f - k.top) * k.c > -200.f;
+            if (cmd.rest == kRest)
+                under = apart ? count_window<kRest, true>(s, k, cmd.high, cmd.low, smem_u32(sh.count), &exact)
+                              : count_window<kRest, false>(s, k, cmd.high, cmd.low, smem_u32(sh.count), &exact);
+            else if (cmd.rest == kExactRest)
+                under = count_window<kExactRest, false>(s, k, cmd.high, cmd.low, smem_u32(sh.count), &exact);
+            else
+                under = count_window<kNoRest, false>(s, k, cmd.high, cmd.low, smem_u32(sh.count), &exact);
+            send_rest(exact, under);
         } else {  // tokens of one logit, warp by warp in the order of their ids
             const int n = s.p1 - s.p0, w0 = s.p0 + (int)((int64_t)n * warp / kWarps),
                       w1 = s.p0 + (int)((int64_t)n * (warp + 1) / kWarps);
@@ -856,39 +890,48 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
                 int left = (int)cmd.skip, total = 0;
                 const uint4* pc = reinterpret_cast<const uint4*>(s.row + s.head);
                 // pieces w0 - 1 and w1 stand for the row's ends
-                for (int base = w0 - 1; base <= w1; base += 32) {
-                    const int i = base + lane;
-                    int id = s.head + i * 8;
-                    uint4 v = make_uint4(0xFC00FC00u, 0xFC00FC00u, 0xFC00FC00u, 0xFC00FC00u);
-                    if (i >= w0 && i < w1)
-                        v = pc[i];
-                    else if (i == w0 - 1 && edge0)
-                        v = edge_piece(s, 0, &id);
-                    else if (i == w1 && edge1)
-                        v = edge_piece(s, 1, &id);
-                    uint32_t hit = 0;  // equal: -0 and +0 are
+                auto hits = [&](const uint4& v) {  // equal: -0 and +0 are
+                    uint32_t hit = 0;
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         hit |= (__heq2_mask(as_half2(word_at(v, j)), want2) & 0x00010002u) << (2 * j);
-                    hit = (hit & 0xFFFFu) >> 1 | hit >> 15;
-                    const int c = __popc(hit);
-                    if (!scan) {
-                        total += c;
-                        continue;
-                    }
-                    int run = c;
+                    return (hit & 0xFFFFu) >> 1 | hit >> 15;
+                };
+                constexpr int kU = 4;
+                for (int base = w0 - 1; base <= w1 && left >= 0; base += 32 * kU) {
+                    uint4 v[kU];
 #pragma unroll
-                    for (int d = 1; d < 32; d <<= 1) {
-                        const int q = __shfl_up_sync(kFull, run, d);
-                        if (lane >= d) run += q;
+                    for (int q = 0; q < kU; ++q) {
+                        const int i = base + q * 32 + lane;
+                        v[q] = make_uint4(0xFC00FC00u, 0xFC00FC00u, 0xFC00FC00u, 0xFC00FC00u);
+                        if (i >= w0 && i < w1) v[q] = pc[i];
                     }
-                    int skip = left - (run - c);
-                    if (skip >= 0 && skip < c) {
-                        for (; skip > 0; --skip) hit &= hit - 1;
-                        a.token[row] = id + __ffs(hit) - 1;
+                    int id;
+                    if (edge0 && base == w0 - 1 && lane == 0) v[0] = edge_piece(s, 0, &id);
+#pragma unroll
+                    for (int q = 0; q < kU; ++q) {
+                        const int i = base + q * 32 + lane;
+                        if (edge1 && i == w1) v[q] = edge_piece(s, 1, &id);
+                        uint32_t hit = hits(v[q]);
+                        const int c = __popc(hit);
+                        if (!scan) {
+                            total += c;
+                            continue;
+                        }
+                        if (!__ballot_sync(kFull, c > 0)) continue;
+                        int run = c;
+#pragma unroll
+                        for (int d = 1; d < 32; d <<= 1) {
+                            const int o = __shfl_up_sync(kFull, run, d);
+                            if (lane >= d) run += o;
+                        }
+                        int skip = left - (run - c);
+                        if (skip >= 0 && skip < c) {
+                            for (; skip > 0; --skip) hit &= hit - 1;
+                            a.token[row] = s.head + i * 8 + __ffs(hit) - 1;
+                        }
+                        left -= __shfl_sync(kFull, run, 31);
                     }
-                    left -= __shfl_sync(kFull, run, 31);
-                    if (left < 0) break;
                 }
                 if (!scan) {
                     total = (int)__reduce_add_sync(kFull, (unsigned)total);
@@ -930,31 +973,52 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
                         below = max(below, sh.below[i]);
                         rest += sh.rest[i];
                     }
-                const Window w = window_sums(sh, k, cmd.high, cmd.low, sh.before_count, sh.before_sum);
+                window_sums(sh, cmd.high, cmd.low, sh.before_count, sh.before_sum);
+                const Window& w = sh.window;
+                // the first tries: the two ends of the bound, a warp each
+                bool more = below >= kLowest;
+                if (cmd.op == kFirst) more = w.count < a.vocab;
+                const bool trying = sh.trying;
+                if (trying) {
+                    // The error of a weight below the window, in steps of 2^-24: of a piece's sum, 3; of the power, 4; of
+                    // its exponent t, two roundings of half a step of |t| ln 2: 17 for |t| up to 24, and for
+                    // smaller weights (2^-24 at most, vocab of them) up to 42, all those under 2^-60 together being
+                    // under 2^-36 of the largest's; and a place for each piece.  In the first look a thread's sums
+                    // of its pieces come in place of one piece's, and the exponent's roundings are those of c logit
+                    // and c top, |c top| + 60 at most.
+                    u64 error = 0;
+                    const u64 spare = ((u64)a.vocab << k.places >> 42) + ((u64)a.vocab >> (60 - k.places)) +
+                                      (u64)s.pieces + kThreads * kMaxCluster + 64;
+                    if (cmd.op == kFirst) {
+                        const u64 units = (u64)((s.p1 - s.p0) / kThreads + 3.f * fminf(fabsf(k.top) * k.c, 1e9f)) + 400;
+                        error = sum ? (rest >> 24) * units + units + spare : 1ull << 61;  // (not known)
+                        rest = !sum ? error : rest > w.sum ? rest - w.sum : 0;
+                    } else if (cmd.rest == kRest) {
+                        error = (rest >> 24) * 24 + spare;
+                    }
+                    if (!more) rest = error = 0;
+                    if (warp < 2 && (warp == 0 || error))
+                        decide(sh, wish, more, warp ? rest + error : rest > error ? rest - error : 0, &sh.found[2 * warp],
+                               &sh.ending[warp]);
+                    __syncthreads();
+                    if (tid == 0 && error) {
+                        const Ending x = sh.ending[0], y = sh.ending[1];
+                        // the same kept tokens, the same place, and a probability that is certain enough
+                        const u64 apart = x.total > y.total ? x.total - y.total : y.total - x.total;
+                        sh.ending[0].ok = x.ok && y.ok && x.kept == y.kept && x.at.n == y.at.n && apart <= x.total >> 14;
+                        sh.ending[0].total = min(x.total, y.total) + apart / 2;
+                    }
+                    __syncwarp();
+                }
                 if (warp == 0) {  // the search is one warp's
                     Found at = {};
                     u64 total = 0;
                     bool done = false;
-                    bool more = below >= kLowest;
+                    Found* const f = sh.found;
                     if (stage == kTry) {
-                        // The error of a weight, in steps of 2^-24: of the sums of its thread's pieces; of its exponent t
-                        // (three roundings of |t| ln 2, 60 at most: all weights under 2^-60 together are under 2^-36 of
-                        // the largest's); of the power, 4; and a place of its thread's sum.  In the first look there is
-                        // a reference in place of the largest, and one rounding of its size and of the logit's
-                        // in the exponent: 2 |c top| and |c logit|, 60 more, ln 2 each.
-                        u64 error = 0;
-                        const u64 spare = kThreads * kMaxCluster + ((u64)a.vocab >> (60 - k.places));
-                        u64 units = (u64)((s.p1 - s.p0) / kThreads + 4 + 6 + 42 + 42 + 42);
-                        if (cmd.op == kFirst) {
-                            more = w.count < a.vocab;
-                            units += (u64)(3.f * fminf(fabsf(k.top) * k.c, 1e9f)) + 300;
-                            error = sum ? (rest >> 24) * units + units + spare : 1ull << 61;  // (not known)
-                            rest = !sum ? error : rest > w.sum ? rest - w.sum : 0;
-                        } else if (cmd.rest == kRest) {
-                            error = (rest >> 24) * units + units + spare;
-                        }
-                        if (!more) rest = error = 0;
-                        done = decide(sh, k, wish, w, more, rest, error, &at, &total);
+                        done = sh.ending[0].ok;
+                        at = sh.ending[0].at;
+                        total = sh.ending[0].total;
                         if (!done) {
                             // all of the histogram, then what lies below it exactly
                             if (cmd.op == kFirst)
@@ -963,11 +1027,13 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
                                 next = {kWindow, top, window_low(top), kExactRest, 0, 0, 0};
                             else
                                 stage = kCollect;
+                            if (cmd.rest == kExactRest || !more) whole = w.sum + rest;
                         }
                     }
                     if (stage >= kCollect) {
-                        // Window by window to the end, or to the k-th token: nothing is left inexact.  Then the places
-                        // of top-p, min-p and the drawn token, each in the window that holds it.
+                        // Window by window, to the k-th token or as far as the row's weight, which is exact now, says
+                        // that a limit or the drawn token lies.  Then the places of top-p, min-p and the drawn token,
+                        // each in the window that holds it.
                         int need = -1;  // the window wanted next
                         if (stage == kCollect) {
                             sh.win_high[windows] = cmd.high;
@@ -976,11 +1042,17 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
                             sh.win_sum[windows + 1] = w.sum;
                             __syncwarp();
                             win = windows++;
-                            if (more && w.count < wish.k) {
+                            bool on = more && w.count < wish.k;
+                            if (on && wish.k == kAll) {
+                                if (wish.p < 1.f) on = w.sum < times(wish.p, whole, true);
+                                else if (!(wish.m > 0.f)) on = !(wish.u < 1.f) || w.sum <= times(wish.u, whole, false);
+                                on = on && !(wish.m > 0.f && !at_least(k, cmd.low, wish.m));
+                            }
+                            if (on) {
                                 next = {kWindow, below, window_low(below), 0, 0, 0, 0};
                             } else {
-                                kept = min(wish.k, w.count);
-                                kept_sum = find<kByCount>(sh, k, w, kept, 0).sum;
+                                kept = wish.k <= w.count || !more ? min(wish.k, w.count) : kAll;
+                                kept_sum = kept == kAll ? whole : (find(sh, kByCount, kept, 0, f), f->sum);
                                 stage = kTopP;
                             }
                         }
@@ -997,8 +1069,9 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
                                     need = v;
                                     continue;
                                 }
-                                const Found f = find_top_p(sh, k, w, wish.p, kept_sum);
-                                if (f.n && f.n <= kept) kept = f.n, kept_sum = f.sum;
+                                find_top_p(sh, wish.p, kept_sum, f);
+                                if (f->n && f->n <= kept) kept = f->n, kept_sum = f->sum;
+                                __syncwarp();
                                 stage = kMinP;
                             } else if (stage == kMinP) {
                                 if (!(wish.m > 0.f)) {
@@ -1011,10 +1084,9 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
                                     need = v;
                                     continue;
                                 }
-                                bool end;
-                                Found f = find_min(sh, k, w, wish.m, &end);
-                                if (f.n == 0) f = find<kByCount>(sh, k, w, 1, 0);
-                                if (f.n < kept) kept = f.n, kept_sum = f.sum;
+                                find_min(sh, wish.m, f);
+                                if (f->n < kept) kept = f->n, kept_sum = f->sum;
+                                __syncwarp();
                                 stage = kPick;
                             } else {
                                 const u64 target = times(wish.u, kept_sum, false);
@@ -1026,8 +1098,9 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
                                     need = v;
                                     continue;
                                 }
-                                if (wish.u < 1.f) at = find<kPass>(sh, k, w, 0, target);
-                                if (!at.n || at.n > kept) at = find<kByCount>(sh, k, w, min(kept, w.count), 0);
+                                if (wish.u < 1.f) find(sh, kPass, 0, target, f), at = *f;
+                                __syncwarp();
+                                if (!at.n || at.n > kept) find(sh, kByCount, min(kept, w.count), 0, f), at = *f;
                                 total = kept_sum;
                                 done = true;
                             }
@@ -1043,8 +1116,16 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
                             a.logprob[row] = fminf((float)((((double)t.x + (double)t.y) - log2_of(total, k.places)) *
                                                            0.69314718055994530942), 0.f);
                         }
-                        if (cmd.op == kFirst && at.tie == 0) {
-                            if (lane == 0) a.token[row] = (int64_t)sh.lowest[cmd.high - at.order];
+                        if (cmd.op == kFirst && sh.listed <= kList) {
+                            // the id that so many of the same logit lie before
+                            const int n = (int)sh.listed;
+                            for (int i = lane; i < n; i += 32) {
+                                if (sh.list[i].x != at.order) continue;
+                                int before = 0;
+                                for (int j = 0; j < n; ++j)
+                                    before += sh.list[j].x == at.order && sh.list[j].y < sh.list[i].y;
+                                if (before == at.tie) a.token[row] = (int64_t)sh.list[i].y;
+                            }
                         } else {
                             next = {kTie, 0, 0, 0, at.order, (uint32_t)at.tie, 0};
                         }
@@ -1057,6 +1138,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
                 if (lane == 0) {
                     sh.next = next;
                     if (next.op == kWindow) {
+                        sh.trying = stage == kTry;
                         const int v = stage == kTry ? 0 : stage == kCollect ? windows : win;
                         sh.before_count = v ? sh.win_count[v] : 0;
                         sh.before_sum = v ? sh.win_sum[v] : 0;
@@ -1077,14 +1159,10 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-// CTAs of a row: enough to fill the GPU, of at least 4096 logits each; and so many that the rows in work
-// (four CTAs an SM) stay in the L2 cache between the looks.
+// CTAs of a row: enough for two on every SM (four fit), of at least 4096 logits each.
 int cluster_for(int64_t rows, int64_t vocab, int sms) {
-    const int64_t slots = (int64_t)sms * 4, cache = 48 << 20;
     int c = 1;
-    while (c < kMaxCluster && vocab >= (int64_t)c * 2 * 4096 &&
-           (rows * c < slots / 2 || (rows * c < slots ? rows * c : slots) / c * vocab * 2 > cache))
-        c *= 2;
+    while (c < kMaxCluster && rows * c < (int64_t)sms * 2 && vocab >= (int64_t)c * 2 * 4096) c *= 2;
     return c;
 }
 
