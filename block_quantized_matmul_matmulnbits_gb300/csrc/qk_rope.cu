@@ -23,7 +23,8 @@ namespace mnb {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kEach = 4;  // 16-byte pieces a thread has in flight
+constexpr int kRing = 4;   // 16-byte pieces a thread has on their way
+constexpr int kChunk = 8;  // tokens of a CTA, at most
 
 struct RopeArgs {
     KvArgs b;                  // q_start, kv_len, seqs, tokens (where positions is NULL)
@@ -31,7 +32,7 @@ struct RopeArgs {
     const float* inv_freq;
     const __half *q_weight, *k_weight;
     float eps;
-    int tokens, q_heads, heads, rotary;  // heads: query and key heads
+    int tokens, chunk, q_heads, heads, rotary;  // chunk: tokens of a CTA; heads: query and key heads
     int interleaved;
     const __half *q, *k;
     __half *q_out, *k_out;
@@ -57,124 +58,135 @@ __device__ __forceinline__ int position_of(const RopeArgs& a, int t) {
 }
 
 template <int D, bool NORM>
-__global__ void __launch_bounds__(kThreads) qk_rope_kernel(const RopeArgs a) {
-    constexpr int LPH = D / 8, STEP = kThreads / LPH;  // threads of a head, heads at once
-    __shared__ float2 turn[2][D / 2];                  // cosine and sine of a token's pairs
-    const int tid = threadIdx.x, j = tid % LPH, h0 = tid / LPH;
+__global__ void __launch_bounds__(kThreads, 6) qk_rope_kernel(const RopeArgs a) {
+    constexpr int LPH = D / 8, STEP = kThreads / LPH;  // threads of a head, heads of a pass
+    __shared__ float2 turn[kChunk][D / 2];             // cosine and sine of a token's pairs
+    __shared__ unsigned long long step[D / 2];
+    __shared__ float gain[2][D];                       // weights of queries and of keys
+    __shared__ int position[kChunk];
+    const int tid = threadIdx.x, warp = tid >> 5, j = tid % LPH, h0 = tid / LPH;
     const int half = a.rotary >> 1, lanes = a.rotary >> 4;  // pairs; threads of half of the turned values
+    const int t0 = blockIdx.x * a.chunk, nt = min(a.chunk, a.tokens - t0);
     pdl_wait();
     pdl_launch_dependents();
-    const unsigned long long r = tid < half ? turn_of(a.inv_freq[tid]) : 0;
+
+    // passes of STEP heads, a token's behind the other's; their pieces are on their way kRing ahead
+    const int per = (a.heads + STEP - 1) / STEP, passes = nt * per;
+    uint4 x[kRing];
+    int lt = 0, lh = h0;  // what is loaded next
+    auto fetch = [&](uint4& v) {
+        if (lt < nt && lh < a.heads) {
+            const int t = t0 + lt;
+            v = *reinterpret_cast<const uint4*>((lh < a.q_heads ? a.q + (int64_t)t * a.q_stride + lh * D
+                                                                : a.k + (int64_t)t * a.k_stride + (lh - a.q_heads) * D) +
+                                                j * 8);
+        }
+        lh += STEP;
+        if (lh >= h0 + per * STEP) lh = h0, ++lt;
+    };
+#pragma unroll
+    for (int i = 0; i < kRing; ++i) {
+        x[i] = make_uint4(0, 0, 0, 0);
+        fetch(x[i]);
+    }
+    if (tid < half) step[tid] = turn_of(a.inv_freq[tid]);
+    if (NORM) {
+        for (int i = tid; i < 2 * D; i += kThreads) {
+            const __half* g = i < D ? a.q_weight : a.k_weight;
+            gain[i / D][i % D] = g ? __half2float(g[i % D]) : 1.f;
+        }
+    }
+    for (int i = warp; i < nt; i += kThreads / 32) {
+        const int pos = position_of(a, t0 + i);
+        if ((tid & 31) == 0) position[i] = pos;
+    }
+    __syncthreads();
+    for (int i = tid; i < nt * half; i += kThreads) {
+        const int t = i / half, p = i - t * half;
+        const int r = (int)(((unsigned long long)(unsigned)position[t] * step[p]) >> 32);
+        float s, c;
+        sincospif((float)r * 4.656612873077392578125e-10f, &s, &c);  // r 2^-31: half turns
+        turn[t][p] = make_float2(c, s);
+    }
+    __syncthreads();
+
     const bool turned = j * 8 < a.rotary, second = !a.interleaved && j >= lanes;
     // the thread that holds the other values of this one's pairs
     const int other = (tid & 31) + (a.interleaved || !turned ? 0 : second ? -lanes : lanes);
     const int pair0 = a.interleaved ? j * 4 : (second ? j - lanes : j) * 8;
-    uint4 gain[2][2] = {};  // weights of the thread's values and of the others, of queries and of keys
-    if (NORM) {
+    const int other8 = (j + other - (tid & 31)) * 8;
+    float c[8], s[8];  // what a value and its other one are multiplied with, weights included
+    int have = -1;     // for which token and kind of head
+    int t = 0, h = h0;
+    for (int q = 0; q < passes; q += kRing) {
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {
-            const __half* g = w ? a.k_weight : a.q_weight;
-            if (!g) continue;
-            gain[w][0] = *reinterpret_cast<const uint4*>(g + j * 8);
-            const int oj = j + other - (tid & 31);
-            gain[w][1] = *reinterpret_cast<const uint4*>(g + oj * 8);
-        }
-    }
-    int buf = 0;
-    for (int t = blockIdx.x; t < a.tokens; t += gridDim.x) {
-        const __half* q = a.q + (int64_t)t * a.q_stride + j * 8;
-        const __half* k = a.k + (int64_t)t * a.k_stride + j * 8;
-        const int pos = position_of(a, t);  // the same in all warps
-        if (pos < 0) continue;
-        if (tid < half) {
-            const int x = (int)(((unsigned long long)(unsigned)pos * r) >> 32);
-            float s, c;
-            sincospif((float)x * 4.656612873077392578125e-10f, &s, &c);  // x 2^-31: half turns
-            turn[buf][tid] = make_float2(c, s);
-        }
-        __syncthreads();
-        float c[8], s[8];
+        for (int u = 0; u < kRing; ++u) {
+            if (q + u >= passes) break;
+            const int pos = position[t];
+            const bool key = h >= a.q_heads, normed = NORM && (key ? a.k_weight != nullptr : a.q_weight != nullptr);
+            if (have != 2 * t + key) {
+                have = 2 * t + key;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            c[i] = 1.f;
-            s[i] = 0.f;
-        }
-        if (turned) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float2 cs = turn[buf][pair0 + (a.interleaved ? i >> 1 : i)];
-                c[i] = cs.x;
-                s[i] = (a.interleaved ? (i & 1) : second) ? cs.y : -cs.y;
-            }
-        }
-        buf ^= 1;  // the next token's table, which no thread reads before all are done with this one's
-        for (int h = h0; h < ((a.heads + STEP - 1) / STEP) * STEP; h += STEP * kEach) {
-            uint4 x[kEach];
-#pragma unroll
-            for (int u = 0; u < kEach; ++u) {
-                const int hh = h + u * STEP;
-                x[u] = make_uint4(0, 0, 0, 0);
-                if (hh < a.heads)
-                    x[u] = *reinterpret_cast<const uint4*>(hh < a.q_heads ? q + hh * D : k + (hh - a.q_heads) * D);
-            }
-#pragma unroll
-            for (int u = 0; u < kEach; ++u) {
-                const int hh = h + u * STEP;
-                const bool key = hh >= a.q_heads;
-                uint4 y;  // the other values of the pairs
-                if (a.interleaved) {
-                    y = make_uint4(prmt(x[u].x, 0, 0x1032), prmt(x[u].y, 0, 0x1032), prmt(x[u].z, 0, 0x1032),
-                                   prmt(x[u].w, 0, 0x1032));
-                } else {
-                    y.x = __shfl_sync(0xffffffffu, x[u].x, other);
-                    y.y = __shfl_sync(0xffffffffu, x[u].y, other);
-                    y.z = __shfl_sync(0xffffffffu, x[u].z, other);
-                    y.w = __shfl_sync(0xffffffffu, x[u].w, other);
-                }
-                if (!turned) y = make_uint4(0, 0, 0, 0);  // not an infinity times 0
-                float v[8], o[8];
-                const __half2* xp = reinterpret_cast<const __half2*>(&x[u]);
-                const __half2* yp = reinterpret_cast<const __half2*>(&y);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 f = __half22float2(xp[i]), g = __half22float2(yp[i]);
-                    v[2 * i] = f.x, v[2 * i + 1] = f.y;
-                    o[2 * i] = g.x, o[2 * i + 1] = g.y;
-                }
-                float rms = 1.f;
-                if (NORM) {
-                    float sum = 0.f;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) sum = fmaf(v[i], v[i], sum);
-#pragma unroll
-                    for (int m = LPH / 2; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-                    if (key ? a.k_weight != nullptr : a.q_weight != nullptr) {
-                        rms = rsqrtf(fmaf(sum, 1.f / D, a.eps));
-                        const uint4 g0 = key ? gain[1][0] : gain[0][0], g1 = key ? gain[1][1] : gain[0][1];
-                        const __half2* gp = reinterpret_cast<const __half2*>(&g0);
-                        const __half2* op = reinterpret_cast<const __half2*>(&g1);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float2 f = __half22float2(gp[i]);
-                            const float2 g = a.interleaved ? make_float2(f.y, f.x) : __half22float2(op[i]);
-                            v[2 * i] *= f.x, v[2 * i + 1] *= f.y;
-                            o[2 * i] *= g.x, o[2 * i + 1] *= g.y;
-                        }
+                for (int i = 0; i < 8; ++i) {
+                    c[i] = 1.f;
+                    s[i] = 0.f;
+                    if (turned) {
+                        const float2 cs = turn[t][pair0 + (a.interleaved ? i >> 1 : i)];
+                        c[i] = cs.x;
+                        s[i] = (a.interleaved ? (i & 1) : second) ? cs.y : -cs.y;
+                    }
+                    if (NORM) {
+                        c[i] *= gain[key][j * 8 + i];
+                        if (turned) s[i] *= gain[key][a.interleaved ? j * 8 + (i ^ 1) : other8 + i];
                     }
                 }
-                if (hh >= a.heads) continue;
-                uint32_t out[4];
+            }
+            uint4 y;  // the other values of the pairs
+            if (a.interleaved) {
+                y = make_uint4(prmt(x[u].x, 0, 0x1032), prmt(x[u].y, 0, 0x1032), prmt(x[u].z, 0, 0x1032),
+                               prmt(x[u].w, 0, 0x1032));
+            } else {
+                y.x = __shfl_sync(0xffffffffu, x[u].x, other);
+                y.y = __shfl_sync(0xffffffffu, x[u].y, other);
+                y.z = __shfl_sync(0xffffffffu, x[u].z, other);
+                y.w = __shfl_sync(0xffffffffu, x[u].w, other);
+            }
+            if (!turned) y = make_uint4(0, 0, 0, 0);  // not an infinity times 0
+            float v[8];
+            const __half2* xp = reinterpret_cast<const __half2*>(&x[u]);
+            const __half2* yp = reinterpret_cast<const __half2*>(&y);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float lo = rms * fmaf(v[2 * i], c[2 * i], o[2 * i] * s[2 * i]);
-                    const float hi = rms * fmaf(v[2 * i + 1], c[2 * i + 1], o[2 * i + 1] * s[2 * i + 1]);
-                    const __half2 p = __floats2half2_rn(lo, hi);
-                    out[i] = *reinterpret_cast<const uint32_t*>(&p);
-                }
-                __half* to = key ? a.k_out + (int64_t)t * a.k_out_stride + (hh - a.q_heads) * D
-                                 : a.q_out + (int64_t)t * a.q_out_stride + hh * D;
+            for (int i = 0; i < 4; ++i) {
+                const float2 f = __half22float2(xp[i]);
+                v[2 * i] = f.x, v[2 * i + 1] = f.y;
+            }
+            float rms = 1.f;
+            if (NORM) {
+                float sum = 0.f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) sum = fmaf(v[i], v[i], sum);
+#pragma unroll
+                for (int m = LPH / 2; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+                if (normed) rms = rsqrtf(fmaf(sum, 1.f / D, a.eps));
+            }
+            uint32_t out[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 o = __half22float2(yp[i]);
+                const float lo = rms * fmaf(v[2 * i], c[2 * i], o.x * s[2 * i]);
+                const float hi = rms * fmaf(v[2 * i + 1], c[2 * i + 1], o.y * s[2 * i + 1]);
+                const __half2 p = __floats2half2_rn(lo, hi);
+                out[i] = *reinterpret_cast<const uint32_t*>(&p);
+            }
+            if (h < a.heads && pos >= 0) {
+                const int64_t row = t0 + t;
+                __half* to = key ? a.k_out + row * a.k_out_stride + (h - a.q_heads) * D
+                                 : a.q_out + row * a.q_out_stride + h * D;
                 *reinterpret_cast<uint4*>(to + j * 8) = make_uint4(out[0], out[1], out[2], out[3]);
             }
+            fetch(x[u]);
+            h += STEP;
+            if (h >= h0 + per * STEP) h = h0, ++t;
         }
     }
 }
@@ -242,8 +254,10 @@ extern "C" int mnb_qk_rope(const mnb_rope* rope, const mnb_kv_batch* batch, cons
     a.k_stride = k_stride;
     a.q_out_stride = q_out_stride;
     a.k_out_stride = k_out_stride;
-    const int64_t most = (int64_t)sms * 16;
-    const dim3 grid((unsigned)(tokens < most ? tokens : most)), block(kThreads);
+    // tokens of a CTA: eight where that leaves six CTAs an SM and more
+    a.chunk = (int)(tokens / ((int64_t)sms * 6));
+    a.chunk = a.chunk < 1 ? 1 : a.chunk > kChunk ? kChunk : a.chunk;
+    const dim3 grid((unsigned)((tokens + a.chunk - 1) / a.chunk)), block(kThreads);
     const bool norm = a.q_weight || a.k_weight;
     const auto kernel = dim == 64 ? (norm ? qk_rope_kernel<64, true> : qk_rope_kernel<64, false>)
                                   : (norm ? qk_rope_kernel<128, true> : qk_rope_kernel<128, false>);
