@@ -4,18 +4,23 @@
 //   router   logits x . r_e, one CTA an expert and four tokens.  Which expert comes first decides the
 //            output, so the sums are held in two FP32 words each (products of FP16 are exact).
 //   up       every CTA picks the experts again from the logits (a warp a token), makes the
-//            list of (expert, up to 8 of its tokens) and takes units of 32 features of one
-//            item: gate and up rows, eight warps of 16 rows by half of the inputs.
-//   down     a CTA takes 16 outputs over all items, so the sum over experts stays in it.
+//            list of (expert, some of its tokens) and takes units of 32 features of one
+//            item: gate and up rows, a warp 16 rows by a slice of the inputs.
+//   down     a cluster takes 16 outputs over all items, so the sum over experts stays in it.
 //
-// The weights are streamed from memory into registers, 16 bytes a lane: a quad's lanes hold
-// four neighbouring blocks of 32 inputs of a row.  A lane takes the zero point of its own
+// Every warp streams its own weights and inputs into a ring of steps in shared memory (cp.async: prefetched in
+// registers, 16 warps an SM waited for loads half of the time, since a short load's scoreboard is the
+// long ones' too).  A lane takes 16 bytes of codes a row: a quad's lanes hold four neighbouring blocks of 32 inputs.  A lane takes the zero point of its own
 // block off (exact in FP16) and the rows go to the MMA (m16n8k16) as its left operand.
 // A step's columns are two tokens by the quad's four blocks: the right operand is zero
 // but where a column's block is the lane's own, so each column sums one block of one
 // token, exact codes times FP16 inputs in FP32, and the block's scale multiplies its sum in FP32.
 // No code is rounded and no sum over K is needed for the zero points.  Two tokens a
 // step use a quarter of the MMA's work; an expert of a few tokens' step has one or two.
+//
+// The inputs lie in the workspace as the MMA takes them (router and up kernel write them so): 256 bytes
+// a step, first the quad's first quarter blocks and so on, each in the order of the codes, a
+// row of zeros for the lanes that have none, zeros up to a whole step.
 #include <cuda_fp16.h>
 
 #include "common.cuh"
@@ -29,12 +34,8 @@ namespace {
 constexpr int kTokens = MNB_MOE_MAX_TOKENS;
 constexpr int kMaxExperts = 256;
 constexpr int kMaxTop = 16;
-constexpr int kItem = 8;                   // tokens of an item
-constexpr int kPairs = kItem / 2;
+constexpr int kMostItem = 8;               // tokens of an item, at most
 constexpr int kMaxItems = kTokens * kMaxTop;
-// steps (of four blocks) that a warp's loads run ahead: as many as the registers hold
-template <int BITS> constexpr int kAhead = BITS == 4 ? 4 : 2;
-constexpr int kUpWarps = 8;
 constexpr int kTile = 32;                  // features of a unit of the up kernel
 
 struct MoeWeight {
@@ -43,15 +44,25 @@ struct MoeWeight {
     const uint8_t* z;
 };
 
+// The items of a call: an expert and some of its tokens each.
+struct MoeTable {
+    int count;
+    uint16_t expert[kMaxItems];
+    uint16_t n[kMaxItems];                 // tokens of the item
+    uint16_t row[kMaxItems][kMostItem];    // token | slot << 8
+};
+
 struct MoeArgs {
-    int hidden, inter, experts, top_k, tokens, normalize;
+    int hidden, inter, experts, top_k, tokens, normalize, bits;
     const __half* x;
     const __half* router;
     MoeWeight up, down;
+    int item;             // tokens of an item
     double* logits;       // [tokens, experts]
-    int32_t* sel;         // [tokens, top_k]
-    __half* h;            // [tokens * top_k, inter]: silu(gate) up / 2^e, e of each 32
-    float* he;            // [tokens * top_k, inter / 32]: weight * 2^e
+    MoeTable* table;      // the items, for the down kernel
+    char* xs;             // [tokens + 1] rows of x, the last of zeros
+    char* h;              // [tokens * top_k + 1] rows of silu(gate) up / 2^e, e of each 32; the last of zeros
+    float* he;            // [tokens * top_k, 4 steps]: weight * 2^e
     __half* y;
     int32_t* ids;
     float* weights;
@@ -69,12 +80,39 @@ __device__ __forceinline__ void add2(float& s, float& e, float p) {
     s = t;
 }
 
+// Bytes of a row of `cols` values as the MMA takes them.
+__host__ __device__ __forceinline__ int64_t row_bytes(int cols) { return (int64_t)((cols + 127) >> 7) * 256; }
+
+// Where eight values from 8 i on go, and in which order (4-bit codes: 0 4 1 5 2 6 3 7).
+__device__ __forceinline__ int piece_at(int i) { return (i >> 4) * 256 + (i & 3) * 64 + ((i >> 2) & 3) * 16; }
+__device__ __forceinline__ uint4 in_order(const uint4& v, int bits) {
+    return bits == 8 ? v : make_uint4(prmt(v.x, v.z, 0x5410u), prmt(v.x, v.z, 0x7632u), prmt(v.y, v.w, 0x5410u),
+                                      prmt(v.y, v.w, 0x7632u));
+}
+
 __global__ void __launch_bounds__(kRouterThreads) moe_router_kernel(const MoeArgs a) {
     __shared__ double part[kRouterThreads / 32][kRouterTokens];
     const int tid = threadIdx.x, lane = tid & 31, e = blockIdx.x, t0 = blockIdx.y * kRouterTokens;
     pdl_wait();
     pdl_launch_dependents();
     const int n = min(a.tokens - t0, kRouterTokens), pieces = a.hidden >> 3;
+    if (e == a.experts) {  // the inputs, once for all
+        const int all = (int)(row_bytes(a.hidden) >> 4);
+        for (int t = 0; t <= n; ++t) {
+            if (t == n && blockIdx.y != 0) break;
+            const int row = t == n ? a.tokens : t0 + t;
+            for (int i = tid; i < all; i += kRouterThreads) {
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (t < n && i < pieces)
+                    v = in_order(reinterpret_cast<const uint4*>(a.x + (int64_t)row * a.hidden)[i], a.bits);
+                *reinterpret_cast<uint4*>(a.xs + row * row_bytes(a.hidden) + piece_at(i)) = v;
+            }
+        }
+        if (blockIdx.y == 0)
+            for (int i = tid; i < (int)(row_bytes(a.inter) >> 4); i += kRouterThreads)
+                reinterpret_cast<uint4*>(a.h + (int64_t)a.tokens * a.top_k * row_bytes(a.inter))[i] = make_uint4(0, 0, 0, 0);
+        return;
+    }
     const uint4* r = reinterpret_cast<const uint4*>(a.router + (int64_t)e * a.hidden);
     float s[kRouterTokens] = {}, c[kRouterTokens] = {};
     for (int i = tid; i < pieces; i += kRouterThreads) {
@@ -113,10 +151,7 @@ __global__ void __launch_bounds__(kRouterThreads) moe_router_kernel(const MoeArg
 // ---- the choice of experts, and the items ----------------------------------
 
 struct MoeItems {
-    int count;
-    uint16_t expert[kMaxItems];
-    uint8_t n[kMaxItems];                  // tokens of the item
-    uint16_t row[kMaxItems][kItem];        // token | slot << 8
+    MoeTable t;
     uint32_t mask[kMaxExperts];            // tokens of an expert
     uint16_t first[kMaxExperts];           // its first item
     int32_t sel[kTokens * kMaxTop];
@@ -185,7 +220,7 @@ __device__ void moe_choose(const MoeArgs& a, int token, int32_t* sel, float* wei
     if (lane < a.top_k) weight[lane] = __fdiv_rn(w, sum);
 }
 
-// The items of the chosen experts (sel in place): by expert number, eight tokens each. Whole CTA.
+// The items of the chosen experts (sel in place): by expert number, a.item tokens each. Whole CTA.
 __device__ void moe_items(const MoeArgs& a, MoeItems& it) {
     const int tid = threadIdx.x, lane = tid & 31, picks = a.tokens * a.top_k;
     for (int e = tid; e < a.experts; e += blockDim.x) it.mask[e] = 0;
@@ -195,52 +230,84 @@ __device__ void moe_items(const MoeArgs& a, MoeItems& it) {
     if (tid < 32) {
         int at = 0;
         for (int e0 = 0; e0 < a.experts; e0 += 32) {
-            const int e = e0 + lane, n = e < a.experts ? __popc(it.mask[e]) : 0;
-            const unsigned one = __ballot_sync(0xffffffffu, n > 0), two = __ballot_sync(0xffffffffu, n > kItem);
-            const unsigned below = (1u << lane) - 1u;
-            const int first = at + __popc(one & below) + __popc(two & below);
-            if (n > 0) {
-                it.first[e] = (uint16_t)first;
-                it.expert[first] = (uint16_t)e;
-                it.n[first] = (uint8_t)min(n, kItem);
-                if (n > kItem) {
-                    it.expert[first + 1] = (uint16_t)e;
-                    it.n[first + 1] = (uint8_t)(n - kItem);
-                }
+            const int e = e0 + lane;
+            int n = e < a.experts ? __popc(it.mask[e]) : 0;
+            const int items = (n + a.item - 1) / a.item;
+            int run = items;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int o = __shfl_up_sync(0xffffffffu, run, d);
+                if (lane >= d) run += o;
             }
-            at += __popc(one) + __popc(two);
+            const int first = at + run - items;
+            if (e < a.experts) it.first[e] = (uint16_t)first;
+            for (int i = 0; i < items; ++i, n -= a.item) {
+                it.t.expert[first + i] = (uint16_t)e;
+                it.t.n[first + i] = (uint16_t)min(n, a.item);
+            }
+            at += __shfl_sync(0xffffffffu, run, 31);
         }
-        if (lane == 0) it.count = at;
+        if (lane == 0) it.t.count = at;
     }
     __syncthreads();
     if (tid < picks) {
         const int t = tid / a.top_k, e = it.sel[tid];
         const int at = __popc(it.mask[e] & ((1u << t) - 1u));
-        it.row[it.first[e] + at / kItem][at % kItem] = (uint16_t)(t | (tid - t * a.top_k) << 8);
+        it.t.row[it.first[e] + at / a.item][at % a.item] = (uint16_t)(t | (tid - t * a.top_k) << 8);
     }
     __syncthreads();
 }
 
 // ---- 16 rows of weights times an item's tokens -------------------------------
 
-__device__ __forceinline__ uint4 ld_stream(const void* p) {  // read once: no place in L1
+// Asynchronous copies into shared memory; `there` = false fills with zeros.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there) {  // read once: past L1
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy16_l1(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool there) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(there ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+template <int OFF = 0>
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
     uint4 v;
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p)
-                 : "memory");
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4+%5];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a), "n"(OFF));
+    return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ float2 lds_float2(uint32_t a) {
+    float2 v;
+    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
     return v;
 }
 
-// A lane's block of rows g and g + 8: codes, scales (two FP16) and zero points.
-template <int BITS>
-struct Raw {
-    uint4 a[BITS / 4], b[BITS / 4];
-    uint32_t s;
-    uint32_t za, zb;
+// A step in the ring: 16 rows by four blocks of codes (each lane's pieces behind one another's), scales [16][4], zero points
+// [16][4], inputs (256 bytes a token), the tokens' factors [4].
+template <int BITS, int NP>
+struct Slot {
+    static constexpr int kScales = 256 * BITS, kZeros = kScales + 128, kInputs = kZeros + 64,
+                         kFactors = kInputs + NP * 512, kBytes = kFactors + NP * 32;
 };
 
-// Where a lane's blocks of a row tile lie.
+// Where a tile's rows lie, for the lane's copies: its codes' block of row lane / 4, two scales of row lane / 2, four zero
+// points of row lane (lanes 0 to 15).
 struct TilePtr {
     const uint8_t* q;
     const __half* s;
@@ -250,33 +317,39 @@ struct TilePtr {
 template <int BITS>
 __device__ __forceinline__ TilePtr tile_at(const MoeWeight& w, int64_t row, int nblk) {
     const int lane = threadIdx.x & 31;
-    const int64_t at = (row + (lane >> 2)) * nblk + (lane & 3);
-    return {w.q + at * (4 * BITS), w.s + at, w.z ? w.z + at : nullptr};
+    return {w.q + ((row + (lane >> 2)) * nblk + (lane & 3)) * (4 * BITS), w.s + (row + (lane >> 1)) * nblk + (lane & 1) * 2,
+            w.z ? w.z + (row + (lane & 15)) * nblk : nullptr};
 }
 
-template <int BITS>
-__device__ __forceinline__ void load_step(Raw<BITS>& r, const TilePtr& p, int step, int nblk) {
-    const bool there = step * 4 + (int)(threadIdx.x & 3) < nblk;
-    if (there) {
-        const uint8_t* q = p.q + (int64_t)step * (16 * BITS);
-        const int64_t eight = (int64_t)nblk * 8;
+// Copies of a step's weights.  Blocks past the row's end are zeros.
+template <int BITS, int NP>
+__device__ __forceinline__ void copy_weights(uint32_t slot, const TilePtr& p, int step, int nblk) {
+    using S = Slot<BITS, NP>;
+    const int lane = threadIdx.x & 31, left = nblk - step * 4;  // blocks from the step on
+    const bool there = (lane & 3) < left;
+    const uint8_t* q = p.q + (there ? step * (16 * BITS) : 0);
 #pragma unroll
-        for (int i = 0; i < BITS / 4; ++i) {
-            r.a[i] = ld_stream(q + i * 16);
-            r.b[i] = ld_stream(q + eight * (4 * BITS) + i * 16);
+    for (int i = 0; i < BITS / 4; ++i) {
+        copy16(slot + lane * 16 + i * 1024, q + i * 16, there);
+        copy16(slot + lane * 16 + i * 1024 + 512, q + (int64_t)nblk * (32 * BITS) + i * 16, there);
+    }
+    const int b = (lane & 1) * 2;
+    const __half* s = p.s + step * 4;
+    if (!(nblk & 1)) {
+        copy4(slot + S::kScales + lane * 4, b < left ? s : p.s, b < left);
+    } else {  // rows that begin between two words
+        const uint32_t lo = b < left ? __half_as_ushort(s[0]) : 0, hi = b + 1 < left ? __half_as_ushort(s[1]) : 0;
+        asm volatile("st.shared.u32 [%0], %1;" ::"r"(slot + S::kScales + lane * 4), "r"(lo | hi << 16) : "memory");
+    }
+    if (p.z && lane < 16) {
+        const uint8_t* z = p.z + step * 4;
+        if (!(nblk & 3)) {
+            copy4(slot + S::kZeros + lane * 4, z, true);
+        } else {
+            uint32_t v = 0;
+            for (int i = 0; i < 4 && i < left; ++i) v |= (uint32_t)z[i] << (8 * i);
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(slot + S::kZeros + lane * 4), "r"(v) : "memory");
         }
-        const unsigned short* s = reinterpret_cast<const unsigned short*>(p.s) + step * 4;
-        r.s = (uint32_t)s[0] | (uint32_t)s[eight] << 16;
-        r.za = r.zb = 1u << (BITS - 1);
-        if (p.z) {
-            r.za = p.z[step * 4];
-            r.zb = p.z[step * 4 + eight];
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < BITS / 4; ++i) r.a[i] = r.b[i] = make_uint4(0, 0, 0, 0);
-        r.s = 0;
-        r.za = r.zb = 0;
     }
 }
 
@@ -300,135 +373,158 @@ __device__ __forceinline__ void codes8(uint32_t lo, uint32_t hi, uint32_t c, uin
     o[3] = hsub2_rn(prmt(hi, 0x64646464u, 0x4342u), c);
 }
 
-// Adds one step (four blocks of 16 rows) times up to eight tokens: y[p][0], y[p][1] are rows g and
-// g + 8 of token 2 p + (lane & 3) / 2, blocks 2 (lane & 1) and the one behind it.  x[p]: where in xs
-// the row begins whose values this lane hands to the MMA (-1: none); e[p]: where in es the factors of the
-// token's blocks begin (-1: no token).
-template <int BITS, bool FACTORS>
-__device__ __forceinline__ void do_step(const Raw<BITS>& r, int step, int nblk, int pairs, const __half* xs,
-                                        const int* x, const float* es, const int* e, float (*y)[2]) {
-    const int t = threadIdx.x & 3, block = step * 4 + t;
-    const bool there = block < nblk;
-    const uint32_t ca = kMagic1024x2 | r.za * 0x00010001u, cb = kMagic1024x2 | r.zb * 0x00010001u;
-    const uint32_t da = hsub2_rn(kHalf960x2, ca), db = hsub2_rn(kHalf960x2, cb);
-    float c[kPairs][4];
+// Adds a step (four blocks of 16 rows) times up to 2 NP tokens: y[p][0], y[p][1] are rows g and
+// g + 8 of token 2 p + (lane & 3) / 2, blocks 2 (lane & 1) and the one behind it.  zeros: NP * 512 bytes of zeros, the inputs of
+// lanes that have none: column g = lane / 4 is token g / 4, block g % 4, and only the lanes that hold that block have any.
+template <int BITS, int NP, bool FACTORS>
+__device__ __forceinline__ void do_step(uint32_t slot, uint32_t zeros, bool zp, int pairs, float (*y)[2]) {
+    using S = Slot<BITS, NP>;
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    uint32_t za = 1u << (BITS - 1), zb = za;
+    if (zp) {
+        za = lds8(slot + S::kZeros + lane);
+        zb = lds8(slot + S::kZeros + 32 + lane);
+    }
+    uint4 ra[BITS / 4], rb[BITS / 4];
 #pragma unroll
-    for (int p = 0; p < kPairs; ++p) c[p][0] = c[p][1] = c[p][2] = c[p][3] = 0.f;
+    for (int i = 0; i < BITS / 4; ++i) {
+        ra[i] = lds128(slot + lane * 16 + i * 1024);
+        rb[i] = lds128<512>(slot + lane * 16 + i * 1024);
+    }
+    const uint32_t x = (g & 3) == t ? slot + S::kInputs + (g >> 2) * 256 + t * 16 : zeros;
+    const uint32_t ca = kMagic1024x2 | za * 0x00010001u, cb = kMagic1024x2 | zb * 0x00010001u;
+    const uint32_t da = hsub2_rn(kHalf960x2, ca), db = hsub2_rn(kHalf960x2, cb);
+    float c[NP][4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         uint32_t A[4], B[4];
         if (BITS == 4) {
-            codes4(word(r.a[0], j), ca, da, A);
-            codes4(word(r.b[0], j), cb, db, B);
+            codes4(word(ra[0], j), ca, da, A);
+            codes4(word(rb[0], j), cb, db, B);
         } else {
             constexpr int kHi = BITS / 4 - 1;
-            codes8(word(r.a[j / 2 * kHi], 2 * j % 4), word(r.a[j / 2 * kHi], (2 * j + 1) % 4), ca, A);
-            codes8(word(r.b[j / 2 * kHi], 2 * j % 4), word(r.b[j / 2 * kHi], (2 * j + 1) % 4), cb, B);
+            codes8(word(ra[j / 2 * kHi], 2 * j % 4), word(ra[j / 2 * kHi], (2 * j + 1) % 4), ca, A);
+            codes8(word(rb[j / 2 * kHi], 2 * j % 4), word(rb[j / 2 * kHi], (2 * j + 1) % 4), cb, B);
         }
 #pragma unroll
-        for (int p = 0; p < kPairs; ++p) {
+        for (int p = 0; p < NP; ++p) {
             if (p >= pairs) break;
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (x[p] >= 0 && there) v = *reinterpret_cast<const uint4*>(xs + (x[p] + block * 32 + j * 8));
-            if (BITS == 4) {  // the codes' order: 0 4, 1 5, 2 6, 3 7
-                mma_16816(c[p], A[0], B[0], A[1], B[1], prmt(v.x, v.z, 0x5410u), prmt(v.x, v.z, 0x7632u));
-                mma_16816(c[p], A[2], B[2], A[3], B[3], prmt(v.y, v.w, 0x5410u), prmt(v.y, v.w, 0x7632u));
-            } else {
+            const uint4 v = lds128(x + p * 512 + j * 64);
+            if (j == 0)
+                mma_16816_z(c[p], A[0], B[0], A[1], B[1], v.x, v.y);
+            else
                 mma_16816(c[p], A[0], B[0], A[1], B[1], v.x, v.y);
-                mma_16816(c[p], A[2], B[2], A[3], B[3], v.z, v.w);
-            }
+            mma_16816(c[p], A[2], B[2], A[3], B[3], v.z, v.w);
         }
     }
     // scales of the two blocks that this lane holds sums of
-    const int from = (threadIdx.x & 28) | (t & 1) * 2;
-    const uint32_t s0 = __shfl_sync(0xffffffffu, r.s, from), s1 = __shfl_sync(0xffffffffu, r.s, from + 1);
+    const uint32_t s0 = lds32(slot + S::kScales + g * 8 + (t & 1) * 4), s1 = lds32(slot + S::kScales + 64 + g * 8 + (t & 1) * 4);
     const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&s0));
     const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&s1));
-    const int first = step * 4 + (t & 1) * 2;
 #pragma unroll
-    for (int p = 0; p < kPairs; ++p) {
+    for (int p = 0; p < NP; ++p) {
         if (p >= pairs) break;
-        float e0 = 1.f, e1 = 1.f;
         if (FACTORS) {
-            e0 = e[p] >= 0 && first < nblk ? es[e[p] + first] : 0.f;
-            e1 = e[p] >= 0 && first + 1 < nblk ? es[e[p] + first + 1] : 0.f;
+            const float2 f = lds_float2(slot + S::kFactors + (2 * p + (t >> 1)) * 16 + (t & 1) * 8);
+            y[p][0] = fmaf(f0.y * f.y, c[p][1], fmaf(f0.x * f.x, c[p][0], y[p][0]));
+            y[p][1] = fmaf(f1.y * f.y, c[p][3], fmaf(f1.x * f.x, c[p][2], y[p][1]));
+        } else {
+            y[p][0] = fmaf(f0.y, c[p][1], fmaf(f0.x, c[p][0], y[p][0]));
+            y[p][1] = fmaf(f1.y, c[p][3], fmaf(f1.x, c[p][2], y[p][1]));
         }
-        y[p][0] = fmaf(f1.x * e1, c[p][1], fmaf(f0.x * e0, c[p][0], y[p][0]));
-        y[p][1] = fmaf(f1.y * e1, c[p][3], fmaf(f0.y * e0, c[p][2], y[p][1]));
     }
 }
 
 // ---- gate and up -------------------------------------------------------------
 
-constexpr int kRedPitch = kItem + 1;
-
-template <int BITS>
-__global__ void __launch_bounds__(kUpWarps * 32, 2) moe_up_kernel(const MoeArgs a) {
+// Variants: NP, pairs of tokens of an item, and SLICES, warps that share a row's inputs; RING steps in shared memory.
+template <int BITS, int NP, int SLICES, int RING, int CTAS>
+__global__ void __launch_bounds__(SLICES * 128, CTAS) moe_up_kernel(const MoeArgs a) {
+    using S = Slot<BITS, NP>;
+    extern __shared__ __align__(16) uint8_t ring[];
     __shared__ MoeItems it;
-    __shared__ float red[2][2][4][16][kRedPitch];
+    __shared__ float red[2][SLICES][4][16][2 * NP + 1];
+    __shared__ uint4 zero[NP * 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid < NP * 32) zero[tid] = make_uint4(0, 0, 0, 0);
     pdl_wait();
     pdl_launch_dependents();
-    for (int t = warp; t < a.tokens; t += kUpWarps)
+    for (int t = warp; t < a.tokens; t += SLICES * 4)
         moe_choose(a, t, it.sel + t * a.top_k, it.weight + t * a.top_k);
     __syncthreads();
     if (blockIdx.x == 0 && tid < a.tokens * a.top_k) {
-        a.sel[tid] = it.sel[tid];
         if (a.ids) a.ids[tid] = it.sel[tid];
         if (a.weights) a.weights[tid] = it.weight[tid];
     }
     moe_items(a, it);
+    if (blockIdx.x == 0) {
+        const uint32_t* from = reinterpret_cast<const uint32_t*>(&it.t);
+        for (int i = tid; i < (int)sizeof(MoeTable) / 4; i += SLICES * 128) reinterpret_cast<uint32_t*>(a.table)[i] = from[i];
+    }
 
     const int nblk = a.hidden >> 5, steps = (nblk + 3) >> 2, tiles = a.inter / kTile;
-    const int units = it.count * tiles;
-    const int q = warp & 3, slice = warp >> 2;  // gate, gate + 16, up, up + 16; half of the inputs
-    const int s0 = slice ? (steps + 1) >> 1 : 0, s1 = slice ? steps : (steps + 1) >> 1;
-    const int chunks = (((steps + 1) >> 1) + kAhead<BITS> - 1) / kAhead<BITS>;
+    const int units = it.t.count * tiles;
+    const int q = warp & 3, slice = warp >> 2;  // gate, gate + 16, up, up + 16; which part of the inputs
+    const int s0 = steps * slice / SLICES, s1 = steps * (slice + 1) / SLICES;
+    const int64_t pitch = row_bytes(a.hidden), hpitch = row_bytes(a.inter);
     auto tile_of = [&](int u) {
         const int item = u / tiles, tile = u - item * tiles;
-        return tile_at<BITS>(a.up, (int64_t)it.expert[item] * 2 * a.inter + (q >> 1) * a.inter + tile * kTile +
+        return tile_at<BITS>(a.up, (int64_t)it.t.expert[item] * 2 * a.inter + (q >> 1) * a.inter + tile * kTile +
                                        (q & 1) * 16, nblk);
     };
-    Raw<BITS> raw[kAhead<BITS>];
-    int lu = blockIdx.x, lc = 0;  // what is loaded next
+    const uint32_t base = smem_u32(ring) + warp * (RING * S::kBytes), zeros = smem_u32(zero);
+    int lu = blockIdx.x, ls = s0, lpairs = 0;  // what is copied next
+    uint32_t lslot = base;
     TilePtr lp = {};
-    if (lu < units) lp = tile_of(lu);
-    auto issue = [&](int i) {
-        const int s = s0 + lc * kAhead<BITS> + i;
-        if (lu < units && s < s1) load_step<BITS>(raw[i], lp, s, nblk);
-    };
-    auto advance = [&] {
-        if (++lc == chunks) {
-            lc = 0;
-            lu += gridDim.x;
-            if (lu < units) lp = tile_of(lu);
+    const char* lx[NP];
+    auto aim = [&] {
+        if (lu >= units) return;
+        lp = tile_of(lu);
+        const int item = lu / tiles, n = it.t.n[item];
+        lpairs = (n + 1) >> 1;
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+            const int i = 2 * p + (lane >> 4);
+            lx[p] = a.xs + (i < n ? it.t.row[item][i] & 255 : a.tokens) * pitch + (lane & 15) * 16;
         }
     };
+    auto issue = [&] {
+        if (lu < units) {
+            copy_weights<BITS, NP>(lslot, lp, ls, nblk);
 #pragma unroll
-    for (int i = 0; i < kAhead<BITS>; ++i) issue(i);
-    advance();
-    int buf = 0;
-    for (int u = blockIdx.x; u < units; u += gridDim.x, buf ^= 1) {
-        const int item = u / tiles, tile = u - item * tiles, n = it.n[item], pairs = (n + 1) >> 1;
-        int x[kPairs];
-        float y[kPairs][2];
-#pragma unroll
-        for (int p = 0; p < kPairs; ++p) {
-            const int i = 2 * p + (lane >> 4);  // column g: token g / 4, block g % 4
-            x[p] = i < n && ((lane >> 2) & 3) == (lane & 3) ? (it.row[item][i] & 255) * a.hidden : -1;
-            y[p][0] = y[p][1] = 0.f;
-        }
-        for (int c = 0; c < chunks; ++c) {
-#pragma unroll
-            for (int i = 0; i < kAhead<BITS>; ++i) {
-                const int s = s0 + c * kAhead<BITS> + i;
-                if (s < s1) do_step<BITS, false>(raw[i], s, nblk, pairs, a.x, x, nullptr, nullptr, y);
-                issue(i);
+            for (int p = 0; p < NP; ++p) {
+                if (p >= lpairs) break;
+                copy16_l1(lslot + S::kInputs + p * 512 + lane * 16, lx[p] + ls * 256);
             }
-            advance();
+            if (++ls == s1) {
+                ls = s0;
+                lu += gridDim.x;
+                aim();
+            }
+        }
+        copies_end();
+        lslot = lslot == base + (RING - 1) * S::kBytes ? base : lslot + S::kBytes;
+    };
+    if (s0 == s1) lu = units;  // no steps for this warp
+    aim();
+#pragma unroll
+    for (int i = 0; i < RING - 1; ++i) issue();
+    int buf = 0;
+    uint32_t slot = base;
+    for (int u = blockIdx.x; u < units; u += gridDim.x, buf ^= 1) {
+        const int item = u / tiles, tile = u - item * tiles, n = it.t.n[item], pairs = (n + 1) >> 1;
+        float y[NP][2];
+#pragma unroll
+        for (int p = 0; p < NP; ++p) y[p][0] = y[p][1] = 0.f;
+        for (int s = s0; s < s1; ++s) {
+            copies_wait<RING - 2>();
+            __syncwarp();  // everyone's copies are there, and the slot before is read
+            issue();
+            do_step<BITS, NP, false>(slot, zeros, a.up.z != nullptr, pairs, y);
+            slot = slot == base + (RING - 1) * S::kBytes ? base : slot + S::kBytes;
         }
 #pragma unroll
-        for (int p = 0; p < kPairs; ++p) {
+        for (int p = 0; p < NP; ++p) {
             if (p >= pairs) break;
             const float v0 = y[p][0] + __shfl_xor_sync(0xffffffffu, y[p][0], 1);
             const float v1 = y[p][1] + __shfl_xor_sync(0xffffffffu, y[p][1], 1);
@@ -438,10 +534,14 @@ __global__ void __launch_bounds__(kUpWarps * 32, 2) moe_up_kernel(const MoeArgs 
             }
         }
         __syncthreads();
-        if (warp < n) {  // a warp a token, a lane a feature
+        for (int w = warp; w < n; w += SLICES * 4) {  // a warp a token, a lane a feature
             const int f = lane;
-            const float gate = red[buf][0][f >> 4][f & 15][warp] + red[buf][1][f >> 4][f & 15][warp];
-            const float up = red[buf][0][2 + (f >> 4)][f & 15][warp] + red[buf][1][2 + (f >> 4)][f & 15][warp];
+            float gate = 0.f, up = 0.f;
+#pragma unroll
+            for (int i = 0; i < SLICES; ++i) {
+                gate += red[buf][i][f >> 4][f & 15][w];
+                up += red[buf][i][2 + (f >> 4)][f & 15][w];
+            }
             const float h = gate / (1.f + expf(-gate)) * up;
             float m = fabsf(h);
 #pragma unroll
@@ -449,70 +549,105 @@ __global__ void __launch_bounds__(kUpWarps * 32, 2) moe_up_kernel(const MoeArgs 
             // FP16 holds the block about its largest value, whatever that is: 2^e <= m < 2^(e + 1)
             uint32_t e = __float_as_uint(m) & 0x7F800000u;
             e = e == 0 || e >= 0x7F000000u ? 0x3F800000u : e;
-            const int row = it.row[item][warp], at = (row & 255) * a.top_k + (row >> 8);
-            a.h[(int64_t)at * a.inter + tile * kTile + f] = __float2half_rn(h * __uint_as_float(0x7F000000u - e));
-            if (lane == 0) a.he[(int64_t)at * tiles + tile] = it.weight[at] * __uint_as_float(e);
+            const int row = it.t.row[item][w], at = (row & 255) * a.top_k + (row >> 8);
+            // feature f of the tile's block, as the MMA takes it
+            char* to = a.h + at * hpitch + (tile >> 2) * 256 + (f >> 3) * 64 + (tile & 3) * 16;
+            const int in = BITS == 8 ? f & 7 : (f & 3) * 2 + ((f >> 2) & 1);
+            reinterpret_cast<__half*>(to)[in] = __float2half_rn(h * __uint_as_float(0x7F000000u - e));
+            float* fe = a.he + (int64_t)at * ((tiles + 3) & ~3);
+            if (lane == 0) fe[tile] = it.weight[at] * __uint_as_float(e);
+            if (tile == tiles - 1)  // zeros up to a whole step
+                for (int b = tiles; b < ((tiles + 3) & ~3); ++b) {
+                    if (lane < 4)
+                        *reinterpret_cast<uint4*>(a.h + at * hpitch + (b >> 2) * 256 + lane * 64 + (b & 3) * 16) =
+                            make_uint4(0, 0, 0, 0);
+                    if (lane == 0) fe[b] = 0.f;
+                }
         }
     }
 }
 
 // ---- down ----------------------------------------------------------------------
 
-template <int BITS, int WARPS>
-__global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) moe_down_kernel(const MoeArgs a) {
-    __shared__ MoeItems it;
-    __shared__ float acc[WARPS][kTokens][17];
+constexpr int kDownWarps = 4;
+
+template <int BITS, int NP, int RING, int CTAS>
+__global__ void __launch_bounds__(kDownWarps * 32, CTAS) moe_down_kernel(const MoeArgs a) {
+    using S = Slot<BITS, NP>;
+    extern __shared__ __align__(16) uint8_t ring[];
+    __shared__ float acc[kDownWarps][kTokens][17];
+    __shared__ uint4 zero[NP * 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid < NP * 32) zero[tid] = make_uint4(0, 0, 0, 0);
+    // a cluster (along z) takes 16 rows; its warps share the steps of all items
+    const int parts = gridDim.z, worker = blockIdx.z * kDownWarps + warp;
     for (int i = lane; i < kTokens * 17; i += 32) acc[warp][0][i] = 0.f;
     pdl_wait();
     pdl_launch_dependents();
-    if (tid < a.tokens * a.top_k) it.sel[tid] = a.sel[tid];
-    __syncthreads();
-    moe_items(a, it);
-
+    const MoeTable& it = *a.table;
     const int nblk = a.inter >> 5, steps = (nblk + 3) >> 2, row0 = blockIdx.x * 16;
-    const int total = it.count * steps;  // of all items; a warp takes a run of them
-    const int f0 = (int)((int64_t)total * warp / WARPS), f1 = (int)((int64_t)total * (warp + 1) / WARPS);
-    Raw<BITS> raw[kAhead<BITS>];
-    int li = f0 / max(steps, 1), ls = f0 - li * steps, lf = f0;  // what is loaded next
+    const int64_t pitch = row_bytes(a.inter);
+    const int total = it.count * steps;
+    const int f0 = (int)((int64_t)total * worker / (parts * kDownWarps)),
+              f1 = (int)((int64_t)total * (worker + 1) / (parts * kDownWarps));
+    __syncthreads();  // the zeros
+    const uint32_t base = smem_u32(ring) + warp * (RING * S::kBytes), zeros = smem_u32(zero);
+    int li = f0 / steps, ls = f0 - li * steps, lf = f0, lpairs = 0;  // what is copied next
+    uint32_t lslot = base;
     TilePtr lp = {};
-    auto tile_of = [&](int item) {
-        return tile_at<BITS>(a.down, (int64_t)it.expert[item] * a.hidden + row0, nblk);
+    const char* lx[NP];
+    const float* le = nullptr;  // factors of token `lane` of the item
+    auto aim = [&] {
+        if (lf >= f1) return;
+        lp = tile_at<BITS>(a.down, (int64_t)it.expert[li] * a.hidden + row0, nblk);
+        const int n = it.n[li];
+        lpairs = (n + 1) >> 1;
+        auto at = [&](int i) {
+            const int row = it.row[li][i];
+            return (row & 255) * a.top_k + (row >> 8);
+        };
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+            const int i = 2 * p + (lane >> 4);
+            lx[p] = a.h + (i < n ? at(i) : a.tokens * a.top_k) * pitch + (lane & 15) * 16;
+        }
+        // (a token that is not there: any factors, its sums are not used)
+        le = a.he + (int64_t)at(lane < n ? lane : 0) * steps * 4;
     };
-    if (f0 < f1) lp = tile_of(li);
-    auto issue = [&](int i) {
+    auto issue = [&] {
         if (lf < f1) {
-            load_step<BITS>(raw[i], lp, ls, nblk);
+            copy_weights<BITS, NP>(lslot, lp, ls, nblk);
+#pragma unroll
+            for (int p = 0; p < NP; ++p) {
+                if (p >= lpairs) break;
+                copy16(lslot + S::kInputs + p * 512 + lane * 16, lx[p] + ls * 256, true);
+            }
+            if (lane < 2 * lpairs) copy16(lslot + S::kFactors + lane * 16, le + ls * 4, true);
             ++lf;
             if (++ls == steps) {
                 ls = 0;
                 ++li;
-                if (lf < f1) lp = tile_of(li);
+                aim();
             }
         }
+        copies_end();
+        lslot = lslot == base + (RING - 1) * S::kBytes ? base : lslot + S::kBytes;
     };
+    aim();
 #pragma unroll
-    for (int i = 0; i < kAhead<BITS>; ++i) issue(i);
-    int item = f0 / max(steps, 1), step = f0 - item * steps, n = 0, pairs = 0;
-    int x[kPairs], e[kPairs];
-    float y[kPairs][2];
+    for (int i = 0; i < RING - 1; ++i) issue();
+    int item = f0 / steps, step = f0 - item * steps, n = 0, pairs = 0;
+    float y[NP][2];
     auto begin = [&] {
         n = it.n[item];
         pairs = (n + 1) >> 1;
 #pragma unroll
-        for (int p = 0; p < kPairs; ++p) {
-            const int i = 2 * p + (lane >> 4), k = 2 * p + ((lane & 3) >> 1);
-            const int ri = it.row[item][i], rk = it.row[item][k];
-            x[p] = i < n && ((lane >> 2) & 3) == (lane & 3)
-                       ? ((ri & 255) * a.top_k + (ri >> 8)) * a.inter : -1;
-            e[p] = k < n ? ((rk & 255) * a.top_k + (rk >> 8)) * nblk : -1;
-            y[p][0] = y[p][1] = 0.f;
-        }
+        for (int p = 0; p < NP; ++p) y[p][0] = y[p][1] = 0.f;
     };
     auto finish = [&] {
         __syncwarp();
 #pragma unroll
-        for (int p = 0; p < kPairs; ++p) {
+        for (int p = 0; p < NP; ++p) {
             if (p >= pairs) break;
             const float v0 = y[p][0] + __shfl_xor_sync(0xffffffffu, y[p][0], 1);
             const float v1 = y[p][1] + __shfl_xor_sync(0xffffffffu, y[p][1], 1);
@@ -525,29 +660,45 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) moe_down_kernel(const 
         }
     };
     if (f0 < f1) begin();
-    for (int f = f0; f < f1; f += kAhead<BITS>) {
-#pragma unroll
-        for (int i = 0; i < kAhead<BITS>; ++i) {
-            if (f + i < f1) {
-                do_step<BITS, true>(raw[i], step, nblk, pairs, a.h, x, a.he, e, y);
-                if (++step == steps) {
-                    finish();
-                    step = 0;
-                    ++item;
-                    if (f + i + 1 < f1) begin();
-                }
-            }
-            issue(i);
+    uint32_t slot = base;
+    for (int f = f0; f < f1; ++f) {
+        copies_wait<RING - 2>();
+        __syncwarp();  // everyone's copies are there, and the slot before is read
+        issue();
+        do_step<BITS, NP, true>(slot, zeros, a.down.z != nullptr, pairs, y);
+        slot = slot == base + (RING - 1) * S::kBytes ? base : slot + S::kBytes;
+        if (++step == steps) {
+            finish();
+            step = 0;
+            ++item;
+            if (f + 1 < f1) begin();
         }
     }
     if (f0 < f1 && step != 0) finish();
     __syncthreads();
-    for (int i = tid; i < a.tokens * 16; i += WARPS * 32) {
+    // the warps' sums in order, then the CTAs'
+    for (int i = tid; i < a.tokens * 16; i += kDownWarps * 32) {
         const int t = i >> 4, r = i & 15;
         float v = acc[0][t][r];
 #pragma unroll
-        for (int w = 1; w < WARPS; ++w) v += acc[w][t][r];
-        a.y[(int64_t)t * a.hidden + row0 + r] = __float2half_rn(v);
+        for (int w = 1; w < kDownWarps; ++w) v += acc[w][t][r];
+        acc[0][t][r] = v;
+        if (parts == 1) a.y[(int64_t)t * a.hidden + row0 + r] = __float2half_rn(v);
+    }
+    if (parts > 1) {
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+        if (blockIdx.z == 0) {
+            for (int i = tid; i < a.tokens * 16; i += kDownWarps * 32) {
+                const int t = i >> 4, r = i & 15;
+                float v = acc[0][t][r];
+                for (int c = 1; c < parts; ++c) v += ld_peer_f32(smem_u32(&acc[0][t][r]), c);
+                a.y[(int64_t)t * a.hidden + row0 + r] = __float2half_rn(v);
+            }
+        }
+        __syncwarp();
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     }
 }
 
@@ -555,16 +706,17 @@ bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p
 
 // Offsets of the workspace's parts, 256-byte aligned.
 struct MoeLayout {
-    int64_t sel, h, he, bytes;
+    int64_t table, xs, h, he, bytes;
 };
 
 MoeLayout moe_layout(const mnb_moe_layer* l, int64_t M) {
     auto up = [](int64_t n) { return (n + 255) & ~(int64_t)255; };
     MoeLayout o;
-    o.sel = up(M * l->experts * 8);
-    o.h = o.sel + up(M * l->top_k * 4);
-    o.he = o.h + up(M * l->top_k * l->inter * 2);
-    o.bytes = o.he + up(M * l->top_k * (l->inter / 32) * 4);
+    o.table = up(M * l->experts * 8);
+    o.xs = o.table + up(sizeof(MoeTable));
+    o.h = o.xs + (M + 1) * row_bytes(l->hidden);
+    o.he = o.h + (M * l->top_k + 1) * row_bytes(l->inter);
+    o.bytes = o.he + up(M * l->top_k * (row_bytes(l->inter) / 64) * 4);
     return o;
 }
 
@@ -578,22 +730,73 @@ int moe_check(const mnb_moe_layer* l, int64_t M) {
     return MNB_OK;
 }
 
+// Dynamic shared memory of the rings; above 48 KB a kernel has to be allowed it (moe_prepare).
+template <int BITS, int NP, int WARPS, int RING>
+constexpr size_t kRingBytes = (size_t)WARPS * RING * Slot<BITS, NP>::kBytes;
+
+// The up kernel's grid: as many CTAs as run at once, or as there can be units.
+template <int BITS, int NP, int SLICES, int RING, int CTAS>
+cudaError_t up_launch(const MoeArgs* a, int64_t units, int sms, cudaStream_t st) {
+    constexpr size_t smem = kRingBytes<BITS, NP, SLICES * 4, RING>;
+    const auto kernel = moe_up_kernel<BITS, NP, SLICES, RING, CTAS>;
+    if (!a) return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const int64_t slots = (int64_t)CTAS * sms;
+    return launch_pdl(kernel, dim3((unsigned)(units < slots ? units : slots)), dim3(SLICES * 128), smem, st, *a);
+}
+
+template <int BITS, int NP, int RING, int CTAS>
+cudaError_t down_launch(const MoeArgs* a, int sms, cudaStream_t st) {
+    constexpr size_t smem = kRingBytes<BITS, NP, kDownWarps, RING>;
+    const auto kernel = moe_down_kernel<BITS, NP, RING, CTAS>;
+    if (!a) return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const int tiles = a->hidden / 16;
+    int parts = CTAS * sms / tiles;  // CTAs of 16 rows: as many as fit, at most eight
+    parts = parts < 1 ? 1 : parts > 8 ? 8 : parts;
+    return launch_pdl(kernel, dim3(tiles, 1, parts), dim3(kDownWarps * 32), smem, st, *a, parts);
+}
+
+// The two kernels for items of `item` tokens; without arguments, what has to be set up for them.
 template <int BITS>
-cudaError_t moe_launch(const MoeArgs& a, int sms, cudaStream_t st) {
-    cudaError_t e = launch_pdl(moe_router_kernel, dim3(a.experts, (a.tokens + kRouterTokens - 1) / kRouterTokens),
-                               dim3(kRouterThreads), 0, st, a);
+cudaError_t moe_kernels(const MoeArgs* a, int item, bool few, int64_t units, int sms, cudaStream_t st) {
+    cudaError_t e;
+    if (item == 2) {
+        // few units: four warps share a row's inputs, so that there are loads enough on their way
+        e = few ? up_launch<BITS, 1, 4, 3, BITS == 4 ? 2 : 1>(a, units, sms, st)
+                : up_launch<BITS, 1, 2, BITS == 4 ? 4 : 3, BITS == 4 ? 3 : 2>(a, units, sms, st);
+        return e != cudaSuccess ? e : down_launch<BITS, 1, 4, BITS == 4 ? 6 : 4>(a, sms, st);
+    }
+    if (item == 4) {
+        e = up_launch<BITS, 2, 2, 3, BITS == 4 ? 3 : 2>(a, units, sms, st);
+        return e != cudaSuccess ? e : down_launch<BITS, 2, 3, BITS == 4 ? 6 : 4>(a, sms, st);
+    }
+    e = up_launch<BITS, 4, 2, 3, BITS == 4 ? 2 : 1>(a, units, sms, st);
+    return e != cudaSuccess ? e : down_launch<BITS, 4, 3, BITS == 4 ? 4 : 3>(a, sms, st);
+}
+
+cudaError_t moe_launch(MoeArgs& a, int sms, cudaStream_t st) {
+    const cudaError_t e = launch_pdl(moe_router_kernel, dim3(a.experts + 1, (a.tokens + kRouterTokens - 1) / kRouterTokens),
+                                     dim3(kRouterThreads), 0, st, a);
     if (e != cudaSuccess) return e;
-    // at most this many items, of which as many as fit run at once
-    const int64_t items = (int64_t)a.tokens * a.top_k, units = items * (a.inter / kTile);
-    const int64_t slots = 2 * (int64_t)sms;
-    e = launch_pdl(moe_up_kernel<BITS>, dim3((unsigned)(units < slots ? units : slots)), dim3(kUpWarps * 32), 0, st, a);
-    if (e != cudaSuccess) return e;
-    const int tiles = a.hidden / 16;
-    if (tiles <= sms) return launch_pdl(moe_down_kernel<BITS, 16>, dim3(tiles), dim3(512), 0, st, a);
-    return launch_pdl(moe_down_kernel<BITS, 8>, dim3(tiles), dim3(256), 0, st, a);
+    // tokens of an item: two where there are no more; four where an expert gets two on average, since more cost
+    // registers and a rare expert of many is read again from the cache; else eight
+    const int picks = a.tokens * a.top_k;
+    a.item = a.tokens <= 2 ? 2 : picks <= 2 * a.experts ? 4 : 8;
+    const int64_t units = (int64_t)picks * (a.inter / kTile);
+    const bool few = units <= 2 * (int64_t)sms;
+    return a.bits == 4 ? moe_kernels<4>(&a, a.item, few, units, sms, st) : moe_kernels<8>(&a, a.item, few, units, sms, st);
 }
 
 }  // namespace
+
+cudaError_t moe_prepare() {
+    for (int item = 2; item <= 8; item *= 2)
+        for (int few = 0; few <= (item == 2); ++few) {
+            cudaError_t e = moe_kernels<4>(nullptr, item, few != 0, 0, 0, nullptr);
+            if (e == cudaSuccess) e = moe_kernels<8>(nullptr, item, few != 0, 0, 0, nullptr);
+            if (e != cudaSuccess) return e;
+        }
+    return cudaSuccess;
+}
 
 }  // namespace mnb
 
@@ -629,6 +832,7 @@ extern "C" int mnb_moe(const mnb_moe_layer* layer, const void* X, int64_t M, voi
     a.top_k = l.top_k;
     a.tokens = (int)M;
     a.normalize = l.flags & MNB_MOE_NORMALIZE;
+    a.bits = l.bits;
     a.x = static_cast<const __half*>(X);
     a.router = static_cast<const __half*>(l.router);
     a.up = {static_cast<const uint8_t*>(l.up_Wq), static_cast<const __half*>(l.up_scales),
@@ -636,13 +840,13 @@ extern "C" int mnb_moe(const mnb_moe_layer* layer, const void* X, int64_t M, voi
     a.down = {static_cast<const uint8_t*>(l.down_Wq), static_cast<const __half*>(l.down_scales),
               static_cast<const uint8_t*>(l.down_zp)};
     a.logits = reinterpret_cast<double*>(w);
-    a.sel = reinterpret_cast<int32_t*>(w + o.sel);
-    a.h = reinterpret_cast<__half*>(w + o.h);
+    a.table = reinterpret_cast<MoeTable*>(w + o.table);
+    a.xs = w + o.xs;
+    a.h = w + o.h;
     a.he = reinterpret_cast<float*>(w + o.he);
     a.y = static_cast<__half*>(Y);
     a.ids = ids;
     a.weights = weights;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    const cudaError_t e = l.bits == 4 ? moe_launch<4>(a, sms, st) : moe_launch<8>(a, sms, st);
-    return e == cudaSuccess ? MNB_OK : MNB_ERR_CUDA;
+    return moe_launch(a, sms, st) == cudaSuccess ? MNB_OK : MNB_ERR_CUDA;
 }
