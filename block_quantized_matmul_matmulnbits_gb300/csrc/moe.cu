@@ -181,6 +181,7 @@ __device__ void moe_choose(const MoeArgs& a, int token, int32_t* sel, float* wei
         const int e = i * 32 + lane;
         key[i] = 0;
         v[i] = 0.0;
+        if (i * 32 >= a.experts) continue;
         if (e < a.experts) {
             v[i] = l[e];
             key[i] = order64(v[i]);
@@ -192,8 +193,10 @@ __device__ void moe_choose(const MoeArgs& a, int token, int32_t* sel, float* wei
         double bv = v[0];
         int be = lane;
 #pragma unroll
-        for (int i = 1; i < kEach; ++i)
+        for (int i = 1; i < kEach; ++i) {
+            if (i * 32 >= a.experts) break;
             if (key[i] > best) best = key[i], bv = v[i], be = i * 32 + lane;
+        }
         const unsigned hi = (unsigned)(best >> 32), m = __reduce_max_sync(0xffffffffu, hi);
         const unsigned lo = hi == m ? (unsigned)best : 0u, m2 = __reduce_max_sync(0xffffffffu, lo);
         const int e = __reduce_min_sync(0xffffffffu, hi == m && lo == m2 ? be : INT32_MAX);
@@ -204,16 +207,20 @@ __device__ void moe_choose(const MoeArgs& a, int token, int32_t* sel, float* wei
             sel[r] = e;
         }
 #pragma unroll
-        for (int i = 0; i < kEach; ++i)
+        for (int i = 0; i < kEach; ++i) {
+            if (i * 32 >= a.experts) break;
             if (e == i * 32 + lane) key[i] = 0;
+        }
     }
     float w = lane < a.top_k ? exp_of(mine - top) : 0.f, sum = 0.f;
     if (a.normalize) {
         sum = w;
     } else {
 #pragma unroll
-        for (int i = 0; i < kEach; ++i)
+        for (int i = 0; i < kEach; ++i) {
+            if (i * 32 >= a.experts) break;
             if (i * 32 + lane < a.experts) sum += exp_of(v[i] - top);
+        }
     }
 #pragma unroll
     for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
@@ -267,37 +274,14 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there
 __device__ __forceinline__ void copy16_l1(uint32_t dst, const void* src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool there) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(there ? 4 : 0) : "memory");
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void copies_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-template <int OFF = 0>
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4+%5];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a), "n"(OFF));
-    return v;
-}
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-    uint32_t v;
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
-    return v;
-}
-__device__ __forceinline__ float2 lds_float2(uint32_t a) {
-    float2 v;
-    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a));
-    return v;
-}
-__device__ __forceinline__ uint32_t lds8(uint32_t a) {
-    uint32_t v;
-    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
-    return v;
-}
-
 // A step in the ring: 16 rows by four blocks of codes (each lane's pieces behind one another's), scales [16][4], zero points
 // [16][4], inputs (256 bytes a token), the tokens' factors [4].
 template <int BITS, int NP>
@@ -306,51 +290,57 @@ struct Slot {
                          kFactors = kInputs + NP * 512, kBytes = kFactors + NP * 32;
 };
 
-// Where a tile's rows lie, for the lane's copies: its codes' block of row lane / 4, two scales of row lane / 2, four zero
-// points of row lane (lanes 0 to 15).
+// Where a lane's copies of a tile come from, moved on step by step: its codes' block of row lane / 4 and of the one eight
+// behind, two scales of row lane / 2, four zero points of row lane (lanes 0 to 15).
 struct TilePtr {
-    const uint8_t* q;
-    const __half* s;
-    const uint8_t* z;
+    const uint8_t *q, *q8, *s, *z;
 };
 
 template <int BITS>
-__device__ __forceinline__ TilePtr tile_at(const MoeWeight& w, int64_t row, int nblk) {
+__device__ __forceinline__ TilePtr tile_at(const MoeWeight& w, int64_t row, int step, int nblk) {
     const int lane = threadIdx.x & 31;
-    return {w.q + ((row + (lane >> 2)) * nblk + (lane & 3)) * (4 * BITS), w.s + (row + (lane >> 1)) * nblk + (lane & 1) * 2,
-            w.z ? w.z + (row + (lane & 15)) * nblk : nullptr};
+    const uint8_t* q = w.q + ((row + (lane >> 2)) * nblk + step * 4 + (lane & 3)) * (4 * BITS);
+    return {q, q + nblk * (32 * BITS),
+            reinterpret_cast<const uint8_t*>(w.s + (row + (lane >> 1)) * nblk + step * 4 + (lane & 1) * 2),
+            w.z + (w.z ? (row + (lane & 15)) * nblk + step * 4 : 0)};
 }
 
-// Copies of a step's weights.  Blocks past the row's end are zeros.
+// Copies of a step's weights; blocks past the row's end (`left` of them are there) are zeros.  words: rows of scales and zero
+// points begin at a word, and all steps are whole.
 template <int BITS, int NP>
-__device__ __forceinline__ void copy_weights(uint32_t slot, const TilePtr& p, int step, int nblk) {
+__device__ __forceinline__ void copy_weights(uint32_t slot, TilePtr& p, bool words, int left) {
     using S = Slot<BITS, NP>;
-    const int lane = threadIdx.x & 31, left = nblk - step * 4;  // blocks from the step on
-    const bool there = (lane & 3) < left;
-    const uint8_t* q = p.q + (there ? step * (16 * BITS) : 0);
+    const int lane = threadIdx.x & 31;
+    if (words) {
 #pragma unroll
-    for (int i = 0; i < BITS / 4; ++i) {
-        copy16(slot + lane * 16 + i * 1024, q + i * 16, there);
-        copy16(slot + lane * 16 + i * 1024 + 512, q + (int64_t)nblk * (32 * BITS) + i * 16, there);
-    }
-    const int b = (lane & 1) * 2;
-    const __half* s = p.s + step * 4;
-    if (!(nblk & 1)) {
-        copy4(slot + S::kScales + lane * 4, b < left ? s : p.s, b < left);
-    } else {  // rows that begin between two words
+        for (int i = 0; i < BITS / 4; ++i) {
+            copy16(slot + lane * 16 + i * 1024, p.q + i * 16, true);
+            copy16(slot + lane * 16 + i * 1024 + 512, p.q8 + i * 16, true);
+        }
+        copy4(slot + S::kScales + lane * 4, p.s);
+        if (p.z) copy4(slot + S::kZeros + (lane & 15) * 4, p.z);  // (twice the same)
+    } else {
+        const bool there = (lane & 3) < left;
+        const int64_t back = there ? 0 : -(int64_t)(lane & 3) * (4 * BITS);  // a block that is there
+#pragma unroll
+        for (int i = 0; i < BITS / 4; ++i) {
+            copy16(slot + lane * 16 + i * 1024, p.q + back + i * 16, there);
+            copy16(slot + lane * 16 + i * 1024 + 512, p.q8 + back + i * 16, there);
+        }
+        const int b = (lane & 1) * 2;
+        const __half* s = reinterpret_cast<const __half*>(p.s);
         const uint32_t lo = b < left ? __half_as_ushort(s[0]) : 0, hi = b + 1 < left ? __half_as_ushort(s[1]) : 0;
         asm volatile("st.shared.u32 [%0], %1;" ::"r"(slot + S::kScales + lane * 4), "r"(lo | hi << 16) : "memory");
-    }
-    if (p.z && lane < 16) {
-        const uint8_t* z = p.z + step * 4;
-        if (!(nblk & 3)) {
-            copy4(slot + S::kZeros + lane * 4, z, true);
-        } else {
+        if (p.z && lane < 16) {
             uint32_t v = 0;
-            for (int i = 0; i < 4 && i < left; ++i) v |= (uint32_t)z[i] << (8 * i);
+            for (int i = 0; i < 4 && i < left; ++i) v |= (uint32_t)p.z[i] << (8 * i);
             asm volatile("st.shared.u32 [%0], %1;" ::"r"(slot + S::kZeros + lane * 4), "r"(v) : "memory");
         }
     }
+    p.q += 16 * BITS;
+    p.q8 += 16 * BITS;
+    p.s += 8;
+    if (p.z) p.z += 4;
 }
 
 __device__ __forceinline__ uint32_t word(const uint4& v, int i) {
@@ -373,28 +363,29 @@ __device__ __forceinline__ void codes8(uint32_t lo, uint32_t hi, uint32_t c, uin
     o[3] = hsub2_rn(prmt(hi, 0x64646464u, 0x4342u), c);
 }
 
-// Adds a step (four blocks of 16 rows) times up to 2 NP tokens: y[p][0], y[p][1] are rows g and
+// Adds a step (four blocks of 16 rows) times 2 P tokens: y[p][0], y[p][1] are rows g and
 // g + 8 of token 2 p + (lane & 3) / 2, blocks 2 (lane & 1) and the one behind it.  zeros: NP * 512 bytes of zeros, the inputs of
 // lanes that have none: column g = lane / 4 is token g / 4, block g % 4, and only the lanes that hold that block have any.
-template <int BITS, int NP, bool FACTORS>
-__device__ __forceinline__ void do_step(uint32_t slot, uint32_t zeros, bool zp, int pairs, float (*y)[2]) {
+template <int BITS, int NP, int P, bool FACTORS>
+__device__ __forceinline__ void step_of(const uint8_t* slot, const uint8_t* zeros, bool zp, float (*y)[2]) {
     using S = Slot<BITS, NP>;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     uint32_t za = 1u << (BITS - 1), zb = za;
     if (zp) {
-        za = lds8(slot + S::kZeros + lane);
-        zb = lds8(slot + S::kZeros + 32 + lane);
+        za = slot[S::kZeros + lane];
+        zb = slot[S::kZeros + 32 + lane];
     }
+    const uint4* codes = reinterpret_cast<const uint4*>(slot) + lane;
     uint4 ra[BITS / 4], rb[BITS / 4];
 #pragma unroll
     for (int i = 0; i < BITS / 4; ++i) {
-        ra[i] = lds128(slot + lane * 16 + i * 1024);
-        rb[i] = lds128<512>(slot + lane * 16 + i * 1024);
+        ra[i] = codes[i * 64];
+        rb[i] = codes[i * 64 + 32];
     }
-    const uint32_t x = (g & 3) == t ? slot + S::kInputs + (g >> 2) * 256 + t * 16 : zeros;
+    const uint8_t* x = (g & 3) == t ? slot + S::kInputs + (g >> 2) * 256 + t * 16 : zeros;
     const uint32_t ca = kMagic1024x2 | za * 0x00010001u, cb = kMagic1024x2 | zb * 0x00010001u;
     const uint32_t da = hsub2_rn(kHalf960x2, ca), db = hsub2_rn(kHalf960x2, cb);
-    float c[NP][4];
+    float c[P][4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         uint32_t A[4], B[4];
@@ -407,9 +398,8 @@ __device__ __forceinline__ void do_step(uint32_t slot, uint32_t zeros, bool zp, 
             codes8(word(rb[j / 2 * kHi], 2 * j % 4), word(rb[j / 2 * kHi], (2 * j + 1) % 4), cb, B);
         }
 #pragma unroll
-        for (int p = 0; p < NP; ++p) {
-            if (p >= pairs) break;
-            const uint4 v = lds128(x + p * 512 + j * 64);
+        for (int p = 0; p < P; ++p) {
+            const uint4 v = *reinterpret_cast<const uint4*>(x + p * 512 + j * 64);
             if (j == 0)
                 mma_16816_z(c[p], A[0], B[0], A[1], B[1], v.x, v.y);
             else
@@ -418,14 +408,12 @@ __device__ __forceinline__ void do_step(uint32_t slot, uint32_t zeros, bool zp, 
         }
     }
     // scales of the two blocks that this lane holds sums of
-    const uint32_t s0 = lds32(slot + S::kScales + g * 8 + (t & 1) * 4), s1 = lds32(slot + S::kScales + 64 + g * 8 + (t & 1) * 4);
-    const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&s0));
-    const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&s1));
+    const __half2* scales = reinterpret_cast<const __half2*>(slot + S::kScales + g * 8 + (t & 1) * 4);
+    const float2 f0 = __half22float2(scales[0]), f1 = __half22float2(scales[16]);
 #pragma unroll
-    for (int p = 0; p < NP; ++p) {
-        if (p >= pairs) break;
+    for (int p = 0; p < P; ++p) {
         if (FACTORS) {
-            const float2 f = lds_float2(slot + S::kFactors + (2 * p + (t >> 1)) * 16 + (t & 1) * 8);
+            const float2 f = *reinterpret_cast<const float2*>(slot + S::kFactors + (2 * p + (t >> 1)) * 16 + (t & 1) * 8);
             y[p][0] = fmaf(f0.y * f.y, c[p][1], fmaf(f0.x * f.x, c[p][0], y[p][0]));
             y[p][1] = fmaf(f1.y * f.y, c[p][3], fmaf(f1.x * f.x, c[p][2], y[p][1]));
         } else {
@@ -433,6 +421,17 @@ __device__ __forceinline__ void do_step(uint32_t slot, uint32_t zeros, bool zp, 
             y[p][1] = fmaf(f1.y, c[p][3], fmaf(f1.x, c[p][2], y[p][1]));
         }
     }
+}
+
+// The step for so many pairs (three are done as four): one branch, not one at every product.
+template <int BITS, int NP, bool FACTORS>
+__device__ __forceinline__ void do_step(const uint8_t* slot, const uint8_t* zeros, bool zp, int pairs, float (*y)[2]) {
+    if (NP == 1 || pairs == 1)
+        step_of<BITS, NP, 1, FACTORS>(slot, zeros, zp, y);
+    else if (NP == 2 || pairs == 2)
+        step_of<BITS, NP, (NP < 2 ? NP : 2), FACTORS>(slot, zeros, zp, y);
+    else
+        step_of<BITS, NP, NP, FACTORS>(slot, zeros, zp, y);
 }
 
 // ---- gate and up -------------------------------------------------------------
@@ -463,56 +462,66 @@ __global__ void __launch_bounds__(SLICES * 128, CTAS) moe_up_kernel(const MoeArg
     }
 
     const int nblk = a.hidden >> 5, steps = (nblk + 3) >> 2, tiles = a.inter / kTile;
-    const int units = it.t.count * tiles;
     const int q = warp & 3, slice = warp >> 2;  // gate, gate + 16, up, up + 16; which part of the inputs
     const int s0 = steps * slice / SLICES, s1 = steps * (slice + 1) / SLICES;
     const int64_t pitch = row_bytes(a.hidden), hpitch = row_bytes(a.inter);
-    auto tile_of = [&](int u) {
-        const int item = u / tiles, tile = u - item * tiles;
-        return tile_at<BITS>(a.up, (int64_t)it.t.expert[item] * 2 * a.inter + (q >> 1) * a.inter + tile * kTile +
-                                       (q & 1) * 16, nblk);
+    const bool words = !(nblk & 3);
+    // the CTA's units, one every gridDim.x: item and tile without a division each
+    const int by_item = gridDim.x / tiles, by_tile = gridDim.x - by_item * tiles;
+    struct Unit {
+        int item, tile;
     };
-    const uint32_t base = smem_u32(ring) + warp * (RING * S::kBytes), zeros = smem_u32(zero);
-    int lu = blockIdx.x, ls = s0, lpairs = 0;  // what is copied next
+    const Unit first = {(int)blockIdx.x / tiles, (int)blockIdx.x % tiles};
+    auto next = [&](Unit& u) {
+        u.item += by_item;
+        u.tile += by_tile;
+        if (u.tile >= tiles) u.tile -= tiles, ++u.item;
+    };
+    const int64_t row0 = (int64_t)(q >> 1) * a.inter + (q & 1) * 16;
+    uint8_t* const own = ring + warp * (RING * S::kBytes);
+    const uint32_t base = smem_u32(own);
+    const uint8_t* const zeros = reinterpret_cast<const uint8_t*>(zero);
+    Unit lu = first;  // what is copied next
+    int ls = s0, lpairs = 0;
+    bool more = s0 < s1 && lu.item < it.t.count;
     uint32_t lslot = base;
-    TilePtr lp = {};
+    TilePtr lp;
     const char* lx[NP];
     auto aim = [&] {
-        if (lu >= units) return;
-        lp = tile_of(lu);
-        const int item = lu / tiles, n = it.t.n[item];
+        lp = tile_at<BITS>(a.up, (int64_t)it.t.expert[lu.item] * 2 * a.inter + row0 + lu.tile * kTile, s0, nblk);
+        const int n = it.t.n[lu.item];
         lpairs = (n + 1) >> 1;
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
             const int i = 2 * p + (lane >> 4);
-            lx[p] = a.xs + (i < n ? it.t.row[item][i] & 255 : a.tokens) * pitch + (lane & 15) * 16;
+            lx[p] = a.xs + (i < n ? it.t.row[lu.item][i] & 255 : a.tokens) * pitch + s0 * 256 + (lane & 15) * 16;
         }
     };
     auto issue = [&] {
-        if (lu < units) {
-            copy_weights<BITS, NP>(lslot, lp, ls, nblk);
+        if (more) {
+            copy_weights<BITS, NP>(lslot, lp, words, nblk - ls * 4);
 #pragma unroll
             for (int p = 0; p < NP; ++p) {
-                if (p >= lpairs) break;
-                copy16_l1(lslot + S::kInputs + p * 512 + lane * 16, lx[p] + ls * 256);
+                if (p < lpairs) copy16_l1(lslot + S::kInputs + p * 512 + lane * 16, lx[p]);
+                lx[p] += 256;
             }
             if (++ls == s1) {
                 ls = s0;
-                lu += gridDim.x;
-                aim();
+                next(lu);
+                more = lu.item < it.t.count;
+                if (more) aim();
             }
         }
         copies_end();
         lslot = lslot == base + (RING - 1) * S::kBytes ? base : lslot + S::kBytes;
     };
-    if (s0 == s1) lu = units;  // no steps for this warp
-    aim();
+    if (more) aim();
 #pragma unroll
     for (int i = 0; i < RING - 1; ++i) issue();
     int buf = 0;
-    uint32_t slot = base;
-    for (int u = blockIdx.x; u < units; u += gridDim.x, buf ^= 1) {
-        const int item = u / tiles, tile = u - item * tiles, n = it.t.n[item], pairs = (n + 1) >> 1;
+    const uint8_t* slot = own;
+    for (Unit u = first; u.item < it.t.count; next(u), buf ^= 1) {
+        const int item = u.item, tile = u.tile, n = it.t.n[item], pairs = (n + 1) >> 1;
         float y[NP][2];
 #pragma unroll
         for (int p = 0; p < NP; ++p) y[p][0] = y[p][1] = 0.f;
@@ -521,7 +530,7 @@ __global__ void __launch_bounds__(SLICES * 128, CTAS) moe_up_kernel(const MoeArg
             __syncwarp();  // everyone's copies are there, and the slot before is read
             issue();
             do_step<BITS, NP, false>(slot, zeros, a.up.z != nullptr, pairs, y);
-            slot = slot == base + (RING - 1) * S::kBytes ? base : slot + S::kBytes;
+            slot = slot == own + (RING - 1) * S::kBytes ? own : slot + S::kBytes;
         }
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
@@ -591,15 +600,18 @@ __global__ void __launch_bounds__(kDownWarps * 32, CTAS) moe_down_kernel(const M
     const int f0 = (int)((int64_t)total * worker / (parts * kDownWarps)),
               f1 = (int)((int64_t)total * (worker + 1) / (parts * kDownWarps));
     __syncthreads();  // the zeros
-    const uint32_t base = smem_u32(ring) + warp * (RING * S::kBytes), zeros = smem_u32(zero);
+    const bool words = !(nblk & 3);
+    uint8_t* const own = ring + warp * (RING * S::kBytes);
+    const uint32_t base = smem_u32(own);
+    const uint8_t* const zeros = reinterpret_cast<const uint8_t*>(zero);
     int li = f0 / steps, ls = f0 - li * steps, lf = f0, lpairs = 0;  // what is copied next
     uint32_t lslot = base;
-    TilePtr lp = {};
+    TilePtr lp;
     const char* lx[NP];
-    const float* le = nullptr;  // factors of token `lane` of the item
+    const float* le;  // factors of token `lane` of the item
     auto aim = [&] {
         if (lf >= f1) return;
-        lp = tile_at<BITS>(a.down, (int64_t)it.expert[li] * a.hidden + row0, nblk);
+        lp = tile_at<BITS>(a.down, (int64_t)it.expert[li] * a.hidden + row0, ls, nblk);
         const int n = it.n[li];
         lpairs = (n + 1) >> 1;
         auto at = [&](int i) {
@@ -609,20 +621,21 @@ __global__ void __launch_bounds__(kDownWarps * 32, CTAS) moe_down_kernel(const M
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
             const int i = 2 * p + (lane >> 4);
-            lx[p] = a.h + (i < n ? at(i) : a.tokens * a.top_k) * pitch + (lane & 15) * 16;
+            lx[p] = a.h + (i < n ? at(i) : a.tokens * a.top_k) * pitch + ls * 256 + (lane & 15) * 16;
         }
         // (a token that is not there: any factors, its sums are not used)
-        le = a.he + (int64_t)at(lane < n ? lane : 0) * steps * 4;
+        le = a.he + ((int64_t)at(lane < n ? lane : 0) * steps + ls) * 4;
     };
     auto issue = [&] {
         if (lf < f1) {
-            copy_weights<BITS, NP>(lslot, lp, ls, nblk);
+            copy_weights<BITS, NP>(lslot, lp, words, nblk - ls * 4);
 #pragma unroll
             for (int p = 0; p < NP; ++p) {
-                if (p >= lpairs) break;
-                copy16(lslot + S::kInputs + p * 512 + lane * 16, lx[p] + ls * 256, true);
+                if (p < lpairs) copy16(lslot + S::kInputs + p * 512 + lane * 16, lx[p], true);
+                lx[p] += 256;
             }
-            if (lane < 2 * lpairs) copy16(lslot + S::kFactors + lane * 16, le + ls * 4, true);
+            if (lane < 2 * lpairs) copy16(lslot + S::kFactors + lane * 16, le, true);
+            le += 4;
             ++lf;
             if (++ls == steps) {
                 ls = 0;
@@ -660,13 +673,13 @@ __global__ void __launch_bounds__(kDownWarps * 32, CTAS) moe_down_kernel(const M
         }
     };
     if (f0 < f1) begin();
-    uint32_t slot = base;
+    const uint8_t* slot = own;
     for (int f = f0; f < f1; ++f) {
         copies_wait<RING - 2>();
         __syncwarp();  // everyone's copies are there, and the slot before is read
         issue();
         do_step<BITS, NP, true>(slot, zeros, a.down.z != nullptr, pairs, y);
-        slot = slot == base + (RING - 1) * S::kBytes ? base : slot + S::kBytes;
+        slot = slot == own + (RING - 1) * S::kBytes ? own : slot + S::kBytes;
         if (++step == steps) {
             finish();
             step = 0;
