@@ -1,16 +1,18 @@
 // moe.cu -- a mixture-of-experts layer of block-quantized gated MLPs for up to 16 tokens
-// (mnb_moe): three kernels, each started before the one ahead of it ends.
+// (mnb_moe): four kernels, each started before the one ahead of it ends.
 //
 //   router   logits x . r_e, one CTA an expert and four tokens.  Which expert comes first decides the
 //            output, so the sums are held in two FP32 words each (products of FP16 are exact).
-//   up       every CTA picks the experts again from the logits (a warp a token), makes the
-//            list of (expert, some of its tokens) and takes units of 32 features of one
-//            item: gate and up rows, a warp 16 rows by a slice of the inputs.
-//   down     a cluster takes 16 outputs over all items, so the sum over experts stays in it.
+//   choose   one CTA: a warp picks a token's experts; the list of (expert, some of its tokens).
+//   up       units of 32 features of one item: gate and up rows; the four warps of a CTA share the
+//            inputs of a unit.
+//   down     a cluster takes 32 outputs over all items, so the sum over experts stays in it.
 //
 // Every warp streams its own weights and inputs into a ring of steps in shared memory (cp.async: prefetched in
 // registers, 16 warps an SM waited for loads half of the time, since a short load's scoreboard is the
-// long ones' too).  A lane takes 16 bytes of codes a row: a quad's lanes hold four neighbouring blocks of 32 inputs.  A lane takes the zero point of its own
+// long ones' too).  A step is four blocks of 32 inputs by 32 rows (up: 32 gate and 32 up rows, so the inputs are
+// copied once for both).  A lane takes 16 bytes of codes a row: a quad's lanes hold the four blocks.
+// A lane takes the zero point of its own
 // block off (exact in FP16) and the rows go to the MMA (m16n8k16) as its left operand.
 // A step's columns are two tokens by the quad's four blocks: the right operand is zero
 // but where a column's block is the lane's own, so each column sums one block of one
@@ -44,12 +46,16 @@ struct MoeWeight {
     const uint8_t* z;
 };
 
-// The items of a call: an expert and some of its tokens each.
+// An item: an expert and some of its tokens.
+struct __align__(64) MoeItem {
+    int expert, n;
+    uint16_t row[kMostItem];               // token * top_k + slot
+    uint8_t token[kMostItem];
+    float weight[kMostItem];
+};
 struct MoeTable {
+    MoeItem item[kMaxItems];
     int count;
-    uint16_t expert[kMaxItems];
-    uint16_t n[kMaxItems];                 // tokens of the item
-    uint16_t row[kMaxItems][kMostItem];    // token | slot << 8
 };
 
 struct MoeArgs {
@@ -134,10 +140,13 @@ __global__ void __launch_bounds__(kRouterThreads) moe_router_kernel(const MoeArg
 #pragma unroll
     for (int t = 0; t < kRouterTokens; ++t) {
         if (t >= n) break;
-        double d = (double)s[t] + (double)c[t];
 #pragma unroll
-        for (int m = 16; m > 0; m >>= 1) d += __shfl_xor_sync(0xffffffffu, d, m);
-        if (lane == 0) part[tid >> 5][t] = d;
+        for (int m = 16; m > 0; m >>= 1) {
+            const float os = __shfl_xor_sync(0xffffffffu, s[t], m), oc = __shfl_xor_sync(0xffffffffu, c[t], m);
+            add2(s[t], c[t], os);
+            c[t] = __fadd_rn(c[t], oc);
+        }
+        if (lane == 0) part[tid >> 5][t] = (double)s[t] + (double)c[t];
     }
     __syncthreads();
     if (tid < n) {
@@ -149,14 +158,6 @@ __global__ void __launch_bounds__(kRouterThreads) moe_router_kernel(const MoeArg
 }
 
 // ---- the choice of experts, and the items ----------------------------------
-
-struct MoeItems {
-    MoeTable t;
-    uint32_t mask[kMaxExperts];            // tokens of an expert
-    uint16_t first[kMaxExperts];           // its first item
-    int32_t sel[kTokens * kMaxTop];
-    float weight[kTokens * kMaxTop];
-};
 
 __device__ __forceinline__ unsigned long long order64(double d) {
     if (d != d) return 1;  // NaN: below every number, still a choice
@@ -227,18 +228,32 @@ __device__ void moe_choose(const MoeArgs& a, int token, int32_t* sel, float* wei
     if (lane < a.top_k) weight[lane] = __fdiv_rn(w, sum);
 }
 
-// The items of the chosen experts (sel in place): by expert number, a.item tokens each. Whole CTA.
-__device__ void moe_items(const MoeArgs& a, MoeItems& it) {
-    const int tid = threadIdx.x, lane = tid & 31, picks = a.tokens * a.top_k;
-    for (int e = tid; e < a.experts; e += blockDim.x) it.mask[e] = 0;
+constexpr int kChooseThreads = kTokens * 32;
+
+// A warp a token; then the items, by expert number, a.item tokens each.
+__global__ void __launch_bounds__(kChooseThreads) moe_choose_kernel(const MoeArgs a) {
+    __shared__ uint32_t mask[kMaxExperts];   // tokens of an expert
+    __shared__ uint16_t first[kMaxExperts];  // its first item
+    __shared__ int32_t sel[kTokens * kMaxTop];
+    __shared__ float weight[kTokens * kMaxTop];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, picks = a.tokens * a.top_k;
+    for (int e = tid; e < a.experts; e += kChooseThreads) mask[e] = 0;
+    pdl_wait();
+    pdl_launch_dependents();
+    if (warp < a.tokens) moe_choose(a, warp, sel + warp * a.top_k, weight + warp * a.top_k);
     __syncthreads();
-    if (tid < picks) atomicOr(&it.mask[it.sel[tid]], 1u << (tid / a.top_k));
+    const int t = tid / a.top_k, e = tid < picks ? sel[tid] : 0;
+    if (tid < picks) {
+        atomicOr(&mask[e], 1u << t);
+        if (a.ids) a.ids[tid] = e;
+        if (a.weights) a.weights[tid] = weight[tid];
+    }
     __syncthreads();
-    if (tid < 32) {
+    if (warp == 0) {
         int at = 0;
         for (int e0 = 0; e0 < a.experts; e0 += 32) {
-            const int e = e0 + lane;
-            int n = e < a.experts ? __popc(it.mask[e]) : 0;
+            const int x = e0 + lane;
+            int n = x < a.experts ? __popc(mask[x]) : 0;
             const int items = (n + a.item - 1) / a.item;
             int run = items;
 #pragma unroll
@@ -246,23 +261,34 @@ __device__ void moe_items(const MoeArgs& a, MoeItems& it) {
                 const int o = __shfl_up_sync(0xffffffffu, run, d);
                 if (lane >= d) run += o;
             }
-            const int first = at + run - items;
-            if (e < a.experts) it.first[e] = (uint16_t)first;
+            const int f = at + run - items;
+            if (x < a.experts) first[x] = (uint16_t)f;
             for (int i = 0; i < items; ++i, n -= a.item) {
-                it.t.expert[first + i] = (uint16_t)e;
-                it.t.n[first + i] = (uint16_t)min(n, a.item);
+                a.table->item[f + i].expert = x;
+                a.table->item[f + i].n = min(n, a.item);
             }
             at += __shfl_sync(0xffffffffu, run, 31);
         }
-        if (lane == 0) it.t.count = at;
+        if (lane == 0) a.table->count = at;
     }
     __syncthreads();
     if (tid < picks) {
-        const int t = tid / a.top_k, e = it.sel[tid];
-        const int at = __popc(it.mask[e] & ((1u << t) - 1u));
-        it.t.row[it.first[e] + at / a.item][at % a.item] = (uint16_t)(t | (tid - t * a.top_k) << 8);
+        const int at = __popc(mask[e] & ((1u << t) - 1u)), i = at % a.item;
+        MoeItem& it = a.table->item[first[e] + at / a.item];
+        it.row[i] = (uint16_t)tid;
+        it.token[i] = (uint8_t)t;
+        it.weight[i] = weight[tid];
     }
+}
+
+// The items into shared memory, once the choice is there. Whole CTA.
+__device__ __forceinline__ int load_items(const MoeTable* table, MoeItem* items) {
+    const int count = table->count;
+    const uint4* from = reinterpret_cast<const uint4*>(table->item);
+    for (int i = threadIdx.x; i < count * (int)(sizeof(MoeItem) / 16); i += blockDim.x)
+        reinterpret_cast<uint4*>(items)[i] = from[i];
     __syncthreads();
+    return count;
 }
 
 // ---- 16 rows of weights times an item's tokens -------------------------------
@@ -277,68 +303,64 @@ __device__ __forceinline__ void copy16_l1(uint32_t dst, const void* src) {
 __device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
+__device__ __forceinline__ void copy8(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void copies_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-// A step in the ring: 16 rows by four blocks of codes (each lane's pieces behind one another's), scales [16][4], zero points
-// [16][4], inputs (256 bytes a token), the tokens' factors [4].
-template <int BITS, int NP>
+// A step in the ring: HALVES times 32 rows by four blocks: codes (the lanes' pieces of 8 rows behind one another's), scales
+// [32][4], zero points [32][4]; then inputs (256 bytes a token) and the tokens' factors [4].
+template <int BITS, int HALVES, int NP>
 struct Slot {
-    static constexpr int kScales = 256 * BITS, kZeros = kScales + 128, kInputs = kZeros + 64,
+    static constexpr int kScales = 512 * BITS, kZeros = kScales + 256, kHalf = kZeros + 128, kInputs = HALVES * kHalf,
                          kFactors = kInputs + NP * 512, kBytes = kFactors + NP * 32;
 };
 
-// Where a lane's copies of a tile come from, moved on step by step: its codes' block of row lane / 4 and of the one eight
-// behind, two scales of row lane / 2, four zero points of row lane (lanes 0 to 15).
+// Where a lane's copies of 32 rows come from, moved on step by step: its codes' block of row lane / 4 (of four of
+// them, eight rows apart), four scales and four zero points of row lane.
 struct TilePtr {
-    const uint8_t *q, *q8, *s, *z;
+    const uint8_t *q, *s, *z;
 };
 
 template <int BITS>
 __device__ __forceinline__ TilePtr tile_at(const MoeWeight& w, int64_t row, int step, int nblk) {
     const int lane = threadIdx.x & 31;
-    const uint8_t* q = w.q + ((row + (lane >> 2)) * nblk + step * 4 + (lane & 3)) * (4 * BITS);
-    return {q, q + nblk * (32 * BITS),
-            reinterpret_cast<const uint8_t*>(w.s + (row + (lane >> 1)) * nblk + step * 4 + (lane & 1) * 2),
-            w.z + (w.z ? (row + (lane & 15)) * nblk + step * 4 : 0)};
+    const int64_t at = (row + lane) * nblk + step * 4;
+    return {w.q + ((row + (lane >> 2)) * nblk + step * 4 + (lane & 3)) * (4 * BITS),
+            reinterpret_cast<const uint8_t*>(w.s + at), w.z ? w.z + at : nullptr};
 }
 
-// Copies of a step's weights; blocks past the row's end (`left` of them are there) are zeros.  words: rows of scales and zero
-// points begin at a word, and all steps are whole.
-template <int BITS, int NP>
-__device__ __forceinline__ void copy_weights(uint32_t slot, TilePtr& p, bool words, int left) {
-    using S = Slot<BITS, NP>;
+// Copies of 32 rows' weights for a step; blocks past the row's end (`left` of them are there) are zeros.  words: rows of scales
+// and zero points begin at a word, and all steps are whole.  eight: bytes of eight rows.
+template <int BITS>
+__device__ __forceinline__ void copy_weights(uint32_t slot, TilePtr& p, int eight, bool words, int left) {
+    constexpr int kScales = 512 * BITS, kZeros = kScales + 256;
     const int lane = threadIdx.x & 31;
+    const bool there = words || (lane & 3) < left;
+    const uint8_t* q = p.q - (there ? 0 : (lane & 3) * (4 * BITS));  // a block that is there
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+#pragma unroll
+        for (int i = 0; i < BITS / 4; ++i) copy16(slot + lane * 16 + (r * (BITS / 4) + i) * 512, q + i * 16, there);
+        q += eight;
+    }
     if (words) {
-#pragma unroll
-        for (int i = 0; i < BITS / 4; ++i) {
-            copy16(slot + lane * 16 + i * 1024, p.q + i * 16, true);
-            copy16(slot + lane * 16 + i * 1024 + 512, p.q8 + i * 16, true);
-        }
-        copy4(slot + S::kScales + lane * 4, p.s);
-        if (p.z) copy4(slot + S::kZeros + (lane & 15) * 4, p.z);  // (twice the same)
+        copy8(slot + kScales + lane * 8, p.s);
+        if (p.z) copy4(slot + kZeros + lane * 4, p.z);
     } else {
-        const bool there = (lane & 3) < left;
-        const int64_t back = there ? 0 : -(int64_t)(lane & 3) * (4 * BITS);  // a block that is there
-#pragma unroll
-        for (int i = 0; i < BITS / 4; ++i) {
-            copy16(slot + lane * 16 + i * 1024, p.q + back + i * 16, there);
-            copy16(slot + lane * 16 + i * 1024 + 512, p.q8 + back + i * 16, there);
-        }
-        const int b = (lane & 1) * 2;
         const __half* s = reinterpret_cast<const __half*>(p.s);
-        const uint32_t lo = b < left ? __half_as_ushort(s[0]) : 0, hi = b + 1 < left ? __half_as_ushort(s[1]) : 0;
-        asm volatile("st.shared.u32 [%0], %1;" ::"r"(slot + S::kScales + lane * 4), "r"(lo | hi << 16) : "memory");
-        if (p.z && lane < 16) {
-            uint32_t v = 0;
-            for (int i = 0; i < 4 && i < left; ++i) v |= (uint32_t)p.z[i] << (8 * i);
-            asm volatile("st.shared.u32 [%0], %1;" ::"r"(slot + S::kZeros + lane * 4), "r"(v) : "memory");
+        uint32_t v[2] = {0, 0}, z = 0;
+        for (int i = 0; i < 4 && i < left; ++i) {
+            v[i >> 1] |= (uint32_t)__half_as_ushort(s[i]) << (16 * (i & 1));
+            if (p.z) z |= (uint32_t)p.z[i] << (8 * i);
         }
+        asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(slot + kScales + lane * 8), "r"(v[0]), "r"(v[1]) : "memory");
+        asm volatile("st.shared.u32 [%0], %1;" ::"r"(slot + kZeros + lane * 4), "r"(z) : "memory");
     }
     p.q += 16 * BITS;
-    p.q8 += 16 * BITS;
     p.s += 8;
     if (p.z) p.z += 4;
 }
@@ -363,107 +385,107 @@ __device__ __forceinline__ void codes8(uint32_t lo, uint32_t hi, uint32_t c, uin
     o[3] = hsub2_rn(prmt(hi, 0x64646464u, 0x4342u), c);
 }
 
-// Adds a step (four blocks of 16 rows) times 2 P tokens: y[p][0], y[p][1] are rows g and
-// g + 8 of token 2 p + (lane & 3) / 2, blocks 2 (lane & 1) and the one behind it.  zeros: NP * 512 bytes of zeros, the inputs of
-// lanes that have none: column g = lane / 4 is token g / 4, block g % 4, and only the lanes that hold that block have any.
+// Adds a step of 32 rows times 2 P tokens: y[m][p][r] is row 16 m + 8 r + g of token 2 p + (lane & 3) / 2, blocks 2 (lane & 1) and
+// the one behind it.  zeros: NP * 512 bytes of zeros, the inputs of lanes that have none: column g = lane / 4 is token
+// g / 4, block g % 4, and only the lanes that hold that block have any.
 template <int BITS, int NP, int P, bool FACTORS>
-__device__ __forceinline__ void step_of(const uint8_t* slot, const uint8_t* zeros, bool zp, float (*y)[2]) {
-    using S = Slot<BITS, NP>;
+__device__ __forceinline__ void step_of(const uint8_t* half, const uint8_t* inputs, const uint8_t* zeros, bool zp,
+                                        float (*y)[NP][2]) {
+    constexpr int kScales = 512 * BITS, kZeros = kScales + 256, W = BITS / 4;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    uint32_t za = 1u << (BITS - 1), zb = za;
-    if (zp) {
-        za = slot[S::kZeros + lane];
-        zb = slot[S::kZeros + 32 + lane];
-    }
-    const uint4* codes = reinterpret_cast<const uint4*>(slot) + lane;
-    uint4 ra[BITS / 4], rb[BITS / 4];
+    const uint4* codes = reinterpret_cast<const uint4*>(half) + lane;
+    const uint8_t* x = (g & 3) == t ? inputs + (g >> 2) * 256 + t * 16 : zeros;
+    uint32_t c0[4], d0[4];  // of the rows g, g + 8, g + 16, g + 24
 #pragma unroll
-    for (int i = 0; i < BITS / 4; ++i) {
-        ra[i] = codes[i * 64];
-        rb[i] = codes[i * 64 + 32];
+    for (int r = 0; r < 4; ++r) {
+        const uint32_t z = zp ? half[kZeros + r * 32 + lane] : 1u << (BITS - 1);
+        c0[r] = kMagic1024x2 | z * 0x00010001u;
+        d0[r] = hsub2_rn(kHalf960x2, c0[r]);
     }
-    const uint8_t* x = (g & 3) == t ? slot + S::kInputs + (g >> 2) * 256 + t * 16 : zeros;
-    const uint32_t ca = kMagic1024x2 | za * 0x00010001u, cb = kMagic1024x2 | zb * 0x00010001u;
-    const uint32_t da = hsub2_rn(kHalf960x2, ca), db = hsub2_rn(kHalf960x2, cb);
-    float c[P][4];
+    float c[2][P][4];
+    uint4 raw[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        uint32_t A[4], B[4];
-        if (BITS == 4) {
-            codes4(word(ra[0], j), ca, da, A);
-            codes4(word(rb[0], j), cb, db, B);
-        } else {
-            constexpr int kHi = BITS / 4 - 1;
-            codes8(word(ra[j / 2 * kHi], 2 * j % 4), word(ra[j / 2 * kHi], (2 * j + 1) % 4), ca, A);
-            codes8(word(rb[j / 2 * kHi], 2 * j % 4), word(rb[j / 2 * kHi], (2 * j + 1) % 4), cb, B);
-        }
+        if (BITS == 4 ? j == 0 : (j & 1) == 0) {
 #pragma unroll
-        for (int p = 0; p < P; ++p) {
-            const uint4 v = *reinterpret_cast<const uint4*>(x + p * 512 + j * 64);
-            if (j == 0)
-                mma_16816_z(c[p], A[0], B[0], A[1], B[1], v.x, v.y);
-            else
-                mma_16816(c[p], A[0], B[0], A[1], B[1], v.x, v.y);
-            mma_16816(c[p], A[2], B[2], A[3], B[3], v.z, v.w);
+            for (int r = 0; r < 4; ++r) raw[r] = codes[(r * W + (BITS == 4 ? 0 : j >> 1)) * 32];
+        }
+        uint4 v[P];
+#pragma unroll
+        for (int p = 0; p < P; ++p) v[p] = *reinterpret_cast<const uint4*>(x + p * 512 + j * 64);
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            uint32_t A[4], B[4];
+            if (BITS == 4) {
+                codes4(word(raw[2 * m], j), c0[2 * m], d0[2 * m], A);
+                codes4(word(raw[2 * m + 1], j), c0[2 * m + 1], d0[2 * m + 1], B);
+            } else {
+                codes8(word(raw[2 * m], 2 * j % 4), word(raw[2 * m], (2 * j + 1) % 4), c0[2 * m], A);
+                codes8(word(raw[2 * m + 1], 2 * j % 4), word(raw[2 * m + 1], (2 * j + 1) % 4), c0[2 * m + 1], B);
+            }
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+                if (j == 0)
+                    mma_16816_z(c[m][p], A[0], B[0], A[1], B[1], v[p].x, v[p].y);
+                else
+                    mma_16816(c[m][p], A[0], B[0], A[1], B[1], v[p].x, v[p].y);
+                mma_16816(c[m][p], A[2], B[2], A[3], B[3], v[p].z, v[p].w);
+            }
         }
     }
     // scales of the two blocks that this lane holds sums of
-    const __half2* scales = reinterpret_cast<const __half2*>(slot + S::kScales + g * 8 + (t & 1) * 4);
-    const float2 f0 = __half22float2(scales[0]), f1 = __half22float2(scales[16]);
+    float2 f[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+        f[r] = __half22float2(*reinterpret_cast<const __half2*>(half + kScales + (r * 8 + g) * 8 + (t & 1) * 4));
 #pragma unroll
     for (int p = 0; p < P; ++p) {
-        if (FACTORS) {
-            const float2 f = *reinterpret_cast<const float2*>(slot + S::kFactors + (2 * p + (t >> 1)) * 16 + (t & 1) * 8);
-            y[p][0] = fmaf(f0.y * f.y, c[p][1], fmaf(f0.x * f.x, c[p][0], y[p][0]));
-            y[p][1] = fmaf(f1.y * f.y, c[p][3], fmaf(f1.x * f.x, c[p][2], y[p][1]));
-        } else {
-            y[p][0] = fmaf(f0.y, c[p][1], fmaf(f0.x, c[p][0], y[p][0]));
-            y[p][1] = fmaf(f1.y, c[p][3], fmaf(f1.x, c[p][2], y[p][1]));
-        }
+        float2 e = make_float2(1.f, 1.f);
+        if (FACTORS) e = *reinterpret_cast<const float2*>(inputs + NP * 512 + (2 * p + (t >> 1)) * 16 + (t & 1) * 8);
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const float2 q = f[2 * m + r];
+                y[m][p][r] = fmaf(FACTORS ? q.y * e.y : q.y, c[m][p][2 * r + 1],
+                                  fmaf(FACTORS ? q.x * e.x : q.x, c[m][p][2 * r], y[m][p][r]));
+            }
     }
 }
 
 // The step for so many pairs (three are done as four): one branch, not one at every product.
 template <int BITS, int NP, bool FACTORS>
-__device__ __forceinline__ void do_step(const uint8_t* slot, const uint8_t* zeros, bool zp, int pairs, float (*y)[2]) {
+__device__ __forceinline__ void do_step(const uint8_t* half, const uint8_t* inputs, const uint8_t* zeros, bool zp, int pairs,
+                                        float (*y)[NP][2]) {
     if (NP == 1 || pairs == 1)
-        step_of<BITS, NP, 1, FACTORS>(slot, zeros, zp, y);
+        step_of<BITS, NP, 1, FACTORS>(half, inputs, zeros, zp, y);
     else if (NP == 2 || pairs == 2)
-        step_of<BITS, NP, (NP < 2 ? NP : 2), FACTORS>(slot, zeros, zp, y);
+        step_of<BITS, NP, (NP < 2 ? NP : 2), FACTORS>(half, inputs, zeros, zp, y);
     else
-        step_of<BITS, NP, NP, FACTORS>(slot, zeros, zp, y);
+        step_of<BITS, NP, NP, FACTORS>(half, inputs, zeros, zp, y);
 }
+
+constexpr int kWarps = 4;
 
 // ---- gate and up -------------------------------------------------------------
 
-// Variants: NP, pairs of tokens of an item, and SLICES, warps that share a row's inputs; RING steps in shared memory.
-template <int BITS, int NP, int SLICES, int RING, int CTAS>
-__global__ void __launch_bounds__(SLICES * 128, CTAS) moe_up_kernel(const MoeArgs a) {
-    using S = Slot<BITS, NP>;
+// Variants: NP, pairs of tokens of an item; RING steps in shared memory.
+template <int BITS, int NP, int RING, int CTAS>
+__global__ void __launch_bounds__(kWarps * 32, CTAS) moe_up_kernel(const MoeArgs a) {
+    using S = Slot<BITS, 2, NP>;
     extern __shared__ __align__(16) uint8_t ring[];
-    __shared__ MoeItems it;
-    __shared__ float red[2][SLICES][4][16][2 * NP + 1];
+    __shared__ MoeItem it[NP == 1 ? 2 * kMaxTop : kMaxItems];  // (one pair: there are two tokens at most)
+    __shared__ float red[2][kWarps][64][2 * NP + 1];
     __shared__ uint4 zero[NP * 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid < NP * 32) zero[tid] = make_uint4(0, 0, 0, 0);
     pdl_wait();
     pdl_launch_dependents();
-    for (int t = warp; t < a.tokens; t += SLICES * 4)
-        moe_choose(a, t, it.sel + t * a.top_k, it.weight + t * a.top_k);
-    __syncthreads();
-    if (blockIdx.x == 0 && tid < a.tokens * a.top_k) {
-        if (a.ids) a.ids[tid] = it.sel[tid];
-        if (a.weights) a.weights[tid] = it.weight[tid];
-    }
-    moe_items(a, it);
-    if (blockIdx.x == 0) {
-        const uint32_t* from = reinterpret_cast<const uint32_t*>(&it.t);
-        for (int i = tid; i < (int)sizeof(MoeTable) / 4; i += SLICES * 128) reinterpret_cast<uint32_t*>(a.table)[i] = from[i];
-    }
+    const int count = load_items(a.table, it);
 
     const int nblk = a.hidden >> 5, steps = (nblk + 3) >> 2, tiles = a.inter / kTile;
-    const int q = warp & 3, slice = warp >> 2;  // gate, gate + 16, up, up + 16; which part of the inputs
-    const int s0 = steps * slice / SLICES, s1 = steps * (slice + 1) / SLICES;
+    const int s0 = steps * warp / kWarps, s1 = steps * (warp + 1) / kWarps;  // the warp's share of the inputs
+    const int eight = nblk * (32 * BITS);
     const int64_t pitch = row_bytes(a.hidden), hpitch = row_bytes(a.inter);
     const bool words = !(nblk & 3);
     // the CTA's units, one every gridDim.x: item and tile without a division each
@@ -477,29 +499,31 @@ __global__ void __launch_bounds__(SLICES * 128, CTAS) moe_up_kernel(const MoeArg
         u.tile += by_tile;
         if (u.tile >= tiles) u.tile -= tiles, ++u.item;
     };
-    const int64_t row0 = (int64_t)(q >> 1) * a.inter + (q & 1) * 16;
     uint8_t* const own = ring + warp * (RING * S::kBytes);
     const uint32_t base = smem_u32(own);
     const uint8_t* const zeros = reinterpret_cast<const uint8_t*>(zero);
     Unit lu = first;  // what is copied next
     int ls = s0, lpairs = 0;
-    bool more = s0 < s1 && lu.item < it.t.count;
+    bool more = s0 < s1 && lu.item < count;
     uint32_t lslot = base;
-    TilePtr lp;
+    TilePtr lp[2];
     const char* lx[NP];
     auto aim = [&] {
-        lp = tile_at<BITS>(a.up, (int64_t)it.t.expert[lu.item] * 2 * a.inter + row0 + lu.tile * kTile, s0, nblk);
-        const int n = it.t.n[lu.item];
-        lpairs = (n + 1) >> 1;
+        const MoeItem& i = it[lu.item];
+        const int64_t row = (int64_t)i.expert * 2 * a.inter + lu.tile * kTile;
+        lp[0] = tile_at<BITS>(a.up, row, s0, nblk);
+        lp[1] = tile_at<BITS>(a.up, row + a.inter, s0, nblk);
+        lpairs = (i.n + 1) >> 1;
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
-            const int i = 2 * p + (lane >> 4);
-            lx[p] = a.xs + (i < n ? it.t.row[lu.item][i] & 255 : a.tokens) * pitch + s0 * 256 + (lane & 15) * 16;
+            const int k = 2 * p + (lane >> 4);
+            lx[p] = a.xs + (k < i.n ? i.token[k] : a.tokens) * pitch + s0 * 256 + (lane & 15) * 16;
         }
     };
     auto issue = [&] {
         if (more) {
-            copy_weights<BITS, NP>(lslot, lp, words, nblk - ls * 4);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) copy_weights<BITS>(lslot + h * S::kHalf, lp[h], eight, words, nblk - ls * 4);
 #pragma unroll
             for (int p = 0; p < NP; ++p) {
                 if (p < lpairs) copy16_l1(lslot + S::kInputs + p * 512 + lane * 16, lx[p]);
@@ -508,7 +532,7 @@ __global__ void __launch_bounds__(SLICES * 128, CTAS) moe_up_kernel(const MoeArg
             if (++ls == s1) {
                 ls = s0;
                 next(lu);
-                more = lu.item < it.t.count;
+                more = lu.item < count;
                 if (more) aim();
             }
         }
@@ -520,36 +544,40 @@ __global__ void __launch_bounds__(SLICES * 128, CTAS) moe_up_kernel(const MoeArg
     for (int i = 0; i < RING - 1; ++i) issue();
     int buf = 0;
     const uint8_t* slot = own;
-    for (Unit u = first; u.item < it.t.count; next(u), buf ^= 1) {
-        const int item = u.item, tile = u.tile, n = it.t.n[item], pairs = (n + 1) >> 1;
-        float y[NP][2];
+    for (Unit u = first; u.item < count; next(u), buf ^= 1) {
+        const MoeItem& i = it[u.item];
+        const int n = i.n, pairs = (n + 1) >> 1;
+        float y[2][2][NP][2];
 #pragma unroll
-        for (int p = 0; p < NP; ++p) y[p][0] = y[p][1] = 0.f;
+        for (int v = 0; v < 8 * NP; ++v) (&y[0][0][0][0])[v] = 0.f;
         for (int s = s0; s < s1; ++s) {
             copies_wait<RING - 2>();
             __syncwarp();  // everyone's copies are there, and the slot before is read
             issue();
-            do_step<BITS, NP, false>(slot, zeros, a.up.z != nullptr, pairs, y);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                do_step<BITS, NP, false>(slot + h * S::kHalf, slot + S::kInputs, zeros, a.up.z != nullptr, pairs, y[h]);
             slot = slot == own + (RING - 1) * S::kBytes ? own : slot + S::kBytes;
         }
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
             if (p >= pairs) break;
-            const float v0 = y[p][0] + __shfl_xor_sync(0xffffffffu, y[p][0], 1);
-            const float v1 = y[p][1] + __shfl_xor_sync(0xffffffffu, y[p][1], 1);
-            if (!(lane & 1)) {
-                red[buf][slice][q][lane >> 2][2 * p + ((lane & 3) >> 1)] = v0;
-                red[buf][slice][q][(lane >> 2) + 8][2 * p + ((lane & 3) >> 1)] = v1;
-            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    float v = y[h][m >> 1][p][m & 1];
+                    v += __shfl_xor_sync(0xffffffffu, v, 1);
+                    if (!(lane & 1)) red[buf][warp][h * 32 + m * 8 + (lane >> 2)][2 * p + ((lane & 3) >> 1)] = v;
+                }
         }
         __syncthreads();
-        for (int w = warp; w < n; w += SLICES * 4) {  // a warp a token, a lane a feature
-            const int f = lane;
+        for (int w = warp; w < n; w += kWarps) {  // a warp a token, a lane a feature
             float gate = 0.f, up = 0.f;
 #pragma unroll
-            for (int i = 0; i < SLICES; ++i) {
-                gate += red[buf][i][f >> 4][f & 15][w];
-                up += red[buf][i][2 + (f >> 4)][f & 15][w];
+            for (int v = 0; v < kWarps; ++v) {
+                gate += red[buf][v][lane][w];
+                up += red[buf][v][32 + lane][w];
             }
             const float h = gate / (1.f + expf(-gate)) * up;
             float m = fabsf(h);
@@ -558,14 +586,14 @@ __global__ void __launch_bounds__(SLICES * 128, CTAS) moe_up_kernel(const MoeArg
             // FP16 holds the block about its largest value, whatever that is: 2^e <= m < 2^(e + 1)
             uint32_t e = __float_as_uint(m) & 0x7F800000u;
             e = e == 0 || e >= 0x7F000000u ? 0x3F800000u : e;
-            const int row = it.t.row[item][w], at = (row & 255) * a.top_k + (row >> 8);
-            // feature f of the tile's block, as the MMA takes it
-            char* to = a.h + at * hpitch + (tile >> 2) * 256 + (f >> 3) * 64 + (tile & 3) * 16;
-            const int in = BITS == 8 ? f & 7 : (f & 3) * 2 + ((f >> 2) & 1);
+            const int at = i.row[w];
+            // feature `lane` of the tile's block, as the MMA takes it
+            char* to = a.h + at * hpitch + (u.tile >> 2) * 256 + (lane >> 3) * 64 + (u.tile & 3) * 16;
+            const int in = BITS == 8 ? lane & 7 : (lane & 3) * 2 + ((lane >> 2) & 1);
             reinterpret_cast<__half*>(to)[in] = __float2half_rn(h * __uint_as_float(0x7F000000u - e));
             float* fe = a.he + (int64_t)at * ((tiles + 3) & ~3);
-            if (lane == 0) fe[tile] = it.weight[at] * __uint_as_float(e);
-            if (tile == tiles - 1)  // zeros up to a whole step
+            if (lane == 0) fe[u.tile] = i.weight[w] * __uint_as_float(e);
+            if (u.tile == tiles - 1)  // zeros up to a whole step
                 for (int b = tiles; b < ((tiles + 3) & ~3); ++b) {
                     if (lane < 4)
                         *reinterpret_cast<uint4*>(a.h + at * hpitch + (b >> 2) * 256 + lane * 64 + (b & 3) * 16) =
@@ -578,29 +606,29 @@ __global__ void __launch_bounds__(SLICES * 128, CTAS) moe_up_kernel(const MoeArg
 
 // ---- down ----------------------------------------------------------------------
 
-constexpr int kDownWarps = 4;
+constexpr int kDownRows = 32;
 
 template <int BITS, int NP, int RING, int CTAS>
-__global__ void __launch_bounds__(kDownWarps * 32, CTAS) moe_down_kernel(const MoeArgs a) {
-    using S = Slot<BITS, NP>;
+__global__ void __launch_bounds__(kWarps * 32, CTAS) moe_down_kernel(const MoeArgs a) {
+    using S = Slot<BITS, 1, NP>;
     extern __shared__ __align__(16) uint8_t ring[];
-    __shared__ float acc[kDownWarps][kTokens][17];
+    __shared__ MoeItem it[NP == 1 ? 2 * kMaxTop : kMaxItems];  // (one pair: there are two tokens at most)
+    __shared__ float acc[kWarps][kTokens][kDownRows + 1];
     __shared__ uint4 zero[NP * 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid < NP * 32) zero[tid] = make_uint4(0, 0, 0, 0);
-    // a cluster (along z) takes 16 rows; its warps share the steps of all items
-    const int parts = gridDim.z, worker = blockIdx.z * kDownWarps + warp;
-    for (int i = lane; i < kTokens * 17; i += 32) acc[warp][0][i] = 0.f;
+    // a cluster (along z) takes 32 rows; its warps share the steps of all items
+    const int parts = gridDim.z, worker = blockIdx.z * kWarps + warp;
+    for (int i = lane; i < kTokens * (kDownRows + 1); i += 32) acc[warp][0][i] = 0.f;
     pdl_wait();
     pdl_launch_dependents();
-    const MoeTable& it = *a.table;
-    const int nblk = a.inter >> 5, steps = (nblk + 3) >> 2, row0 = blockIdx.x * 16;
+    const int count = load_items(a.table, it);
+    const bool words = !((a.inter >> 5) & 3);
+    const int nblk = a.inter >> 5, steps = (nblk + 3) >> 2, row0 = blockIdx.x * kDownRows, eight = nblk * (32 * BITS);
     const int64_t pitch = row_bytes(a.inter);
-    const int total = it.count * steps;
-    const int f0 = (int)((int64_t)total * worker / (parts * kDownWarps)),
-              f1 = (int)((int64_t)total * (worker + 1) / (parts * kDownWarps));
-    __syncthreads();  // the zeros
-    const bool words = !(nblk & 3);
+    const int total = count * steps;
+    const int f0 = (int)((int64_t)total * worker / (parts * kWarps)),
+              f1 = (int)((int64_t)total * (worker + 1) / (parts * kWarps));
     uint8_t* const own = ring + warp * (RING * S::kBytes);
     const uint32_t base = smem_u32(own);
     const uint8_t* const zeros = reinterpret_cast<const uint8_t*>(zero);
@@ -611,24 +639,20 @@ __global__ void __launch_bounds__(kDownWarps * 32, CTAS) moe_down_kernel(const M
     const float* le;  // factors of token `lane` of the item
     auto aim = [&] {
         if (lf >= f1) return;
-        lp = tile_at<BITS>(a.down, (int64_t)it.expert[li] * a.hidden + row0, ls, nblk);
-        const int n = it.n[li];
-        lpairs = (n + 1) >> 1;
-        auto at = [&](int i) {
-            const int row = it.row[li][i];
-            return (row & 255) * a.top_k + (row >> 8);
-        };
+        const MoeItem& i = it[li];
+        lp = tile_at<BITS>(a.down, (int64_t)i.expert * a.hidden + row0, ls, nblk);
+        lpairs = (i.n + 1) >> 1;
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
-            const int i = 2 * p + (lane >> 4);
-            lx[p] = a.h + (i < n ? at(i) : a.tokens * a.top_k) * pitch + ls * 256 + (lane & 15) * 16;
+            const int k = 2 * p + (lane >> 4);
+            lx[p] = a.h + (k < i.n ? i.row[k] : a.tokens * a.top_k) * pitch + ls * 256 + (lane & 15) * 16;
         }
         // (a token that is not there: any factors, its sums are not used)
-        le = a.he + ((int64_t)at(lane < n ? lane : 0) * steps + ls) * 4;
+        le = a.he + ((int64_t)i.row[lane < i.n ? lane : 0] * steps + ls) * 4;
     };
     auto issue = [&] {
         if (lf < f1) {
-            copy_weights<BITS, NP>(lslot, lp, words, nblk - ls * 4);
+            copy_weights<BITS>(lslot, lp, eight, words, nblk - ls * 4);
 #pragma unroll
             for (int p = 0; p < NP; ++p) {
                 if (p < lpairs) copy16(lslot + S::kInputs + p * 512 + lane * 16, lx[p], true);
@@ -650,25 +674,25 @@ __global__ void __launch_bounds__(kDownWarps * 32, CTAS) moe_down_kernel(const M
 #pragma unroll
     for (int i = 0; i < RING - 1; ++i) issue();
     int item = f0 / steps, step = f0 - item * steps, n = 0, pairs = 0;
-    float y[NP][2];
+    float y[2][NP][2];
     auto begin = [&] {
-        n = it.n[item];
+        n = it[item].n;
         pairs = (n + 1) >> 1;
 #pragma unroll
-        for (int p = 0; p < NP; ++p) y[p][0] = y[p][1] = 0.f;
+        for (int v = 0; v < 4 * NP; ++v) (&y[0][0][0])[v] = 0.f;
     };
     auto finish = [&] {
         __syncwarp();
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
             if (p >= pairs) break;
-            const float v0 = y[p][0] + __shfl_xor_sync(0xffffffffu, y[p][0], 1);
-            const float v1 = y[p][1] + __shfl_xor_sync(0xffffffffu, y[p][1], 1);
             const int k = 2 * p + ((lane & 3) >> 1);
-            if (!(lane & 1) && k < n) {
-                const int t = it.row[item][k] & 255;
-                acc[warp][t][lane >> 2] += v0;
-                acc[warp][t][(lane >> 2) + 8] += v1;
+            const int t = it[item].token[k & (kMostItem - 1)];
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                float v = y[m >> 1][p][m & 1];
+                v += __shfl_xor_sync(0xffffffffu, v, 1);
+                if (!(lane & 1) && k < n) acc[warp][t][m * 8 + (lane >> 2)] += v;
             }
         }
     };
@@ -678,7 +702,7 @@ __global__ void __launch_bounds__(kDownWarps * 32, CTAS) moe_down_kernel(const M
         copies_wait<RING - 2>();
         __syncwarp();  // everyone's copies are there, and the slot before is read
         issue();
-        do_step<BITS, NP, true>(slot, zeros, a.down.z != nullptr, pairs, y);
+        do_step<BITS, NP, true>(slot, slot + S::kInputs, zeros, a.down.z != nullptr, pairs, y);
         slot = slot == own + (RING - 1) * S::kBytes ? own : slot + S::kBytes;
         if (++step == steps) {
             finish();
@@ -690,24 +714,24 @@ __global__ void __launch_bounds__(kDownWarps * 32, CTAS) moe_down_kernel(const M
     if (f0 < f1 && step != 0) finish();
     __syncthreads();
     // the warps' sums in order, then the CTAs'
-    for (int i = tid; i < a.tokens * 16; i += kDownWarps * 32) {
-        const int t = i >> 4, r = i & 15;
+    for (int i = tid; i < a.tokens * kDownRows; i += kWarps * 32) {
+        const int t = i / kDownRows, r = i % kDownRows;
         float v = acc[0][t][r];
 #pragma unroll
-        for (int w = 1; w < kDownWarps; ++w) v += acc[w][t][r];
+        for (int w = 1; w < kWarps; ++w) v += acc[w][t][r];
         acc[0][t][r] = v;
         if (parts == 1) a.y[(int64_t)t * a.hidden + row0 + r] = __float2half_rn(v);
     }
     if (parts > 1) {
+        __syncwarp();
         asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
         asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-        if (blockIdx.z == 0) {
-            for (int i = tid; i < a.tokens * 16; i += kDownWarps * 32) {
-                const int t = i >> 4, r = i & 15;
-                float v = acc[0][t][r];
-                for (int c = 1; c < parts; ++c) v += ld_peer_f32(smem_u32(&acc[0][t][r]), c);
-                a.y[(int64_t)t * a.hidden + row0 + r] = __float2half_rn(v);
-            }
+        // each CTA takes its share of the tokens' rows
+        for (int i = blockIdx.z * kWarps * 32 + tid; i < a.tokens * kDownRows; i += parts * kWarps * 32) {
+            const int t = i / kDownRows, r = i % kDownRows;
+            float v = 0.f;
+            for (int c = 0; c < parts; ++c) v += ld_peer_f32(smem_u32(&acc[0][t][r]), c);
+            a.y[(int64_t)t * a.hidden + row0 + r] = __float2half_rn(v);
         }
         __syncwarp();
         asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
@@ -743,71 +767,64 @@ int moe_check(const mnb_moe_layer* l, int64_t M) {
     return MNB_OK;
 }
 
-// Dynamic shared memory of the rings; above 48 KB a kernel has to be allowed it (moe_prepare).
-template <int BITS, int NP, int WARPS, int RING>
-constexpr size_t kRingBytes = (size_t)WARPS * RING * Slot<BITS, NP>::kBytes;
-
 // The up kernel's grid: as many CTAs as run at once, or as there can be units.
-template <int BITS, int NP, int SLICES, int RING, int CTAS>
-cudaError_t up_launch(const MoeArgs* a, int64_t units, int sms, cudaStream_t st) {
-    constexpr size_t smem = kRingBytes<BITS, NP, SLICES * 4, RING>;
-    const auto kernel = moe_up_kernel<BITS, NP, SLICES, RING, CTAS>;
-    if (!a) return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    const int64_t slots = (int64_t)CTAS * sms;
-    return launch_pdl(kernel, dim3((unsigned)(units < slots ? units : slots)), dim3(SLICES * 128), smem, st, *a);
+template <int BITS, int NP, int RING, int CTAS>
+cudaError_t up_launch(const MoeArgs* a, int sms, cudaStream_t st) {
+    constexpr int smem = kWarps * RING * Slot<BITS, 2, NP>::kBytes;
+    const auto kernel = moe_up_kernel<BITS, NP, RING, CTAS>;
+    if (!a) return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const int64_t slots = (int64_t)CTAS * sms, units = (int64_t)a->tokens * a->top_k * (a->inter / kTile);
+    return launch_pdl(kernel, dim3((unsigned)(units < slots ? units : slots)), dim3(kWarps * 32), smem, st, *a);
 }
 
 template <int BITS, int NP, int RING, int CTAS>
 cudaError_t down_launch(const MoeArgs* a, int sms, cudaStream_t st) {
-    constexpr size_t smem = kRingBytes<BITS, NP, kDownWarps, RING>;
+    constexpr int smem = kWarps * RING * Slot<BITS, 1, NP>::kBytes;
     const auto kernel = moe_down_kernel<BITS, NP, RING, CTAS>;
-    if (!a) return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    const int tiles = a->hidden / 16;
-    int parts = CTAS * sms / tiles;  // CTAs of 16 rows: as many as fit, at most eight
+    if (!a) return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const int tiles = a->hidden / kDownRows;
+    int parts = CTAS * sms / tiles;  // CTAs of 32 rows: as many as fit, at most eight
     parts = parts < 1 ? 1 : parts > 8 ? 8 : parts;
-    return launch_pdl(kernel, dim3(tiles, 1, parts), dim3(kDownWarps * 32), smem, st, *a, parts);
+    return launch_pdl(kernel, dim3(tiles, 1, parts), dim3(kWarps * 32), smem, st, *a, parts);
 }
 
 // The two kernels for items of `item` tokens; without arguments, what has to be set up for them.
 template <int BITS>
-cudaError_t moe_kernels(const MoeArgs* a, int item, bool few, int64_t units, int sms, cudaStream_t st) {
+cudaError_t moe_kernels(const MoeArgs* a, int item, int sms, cudaStream_t st) {
+    constexpr bool Q4 = BITS == 4;
     cudaError_t e;
     if (item == 2) {
-        // few units: four warps share a row's inputs, so that there are loads enough on their way
-        e = few ? up_launch<BITS, 1, 4, 3, BITS == 4 ? 2 : 1>(a, units, sms, st)
-                : up_launch<BITS, 1, 2, BITS == 4 ? 4 : 3, BITS == 4 ? 3 : 2>(a, units, sms, st);
-        return e != cudaSuccess ? e : down_launch<BITS, 1, 4, BITS == 4 ? 6 : 4>(a, sms, st);
+        e = up_launch<BITS, 1, Q4 ? 3 : 2, 3>(a, sms, st);
+        return e != cudaSuccess ? e : down_launch<BITS, 1, Q4 ? 4 : 3, 3>(a, sms, st);
     }
     if (item == 4) {
-        e = up_launch<BITS, 2, 2, 3, BITS == 4 ? 3 : 2>(a, units, sms, st);
-        return e != cudaSuccess ? e : down_launch<BITS, 2, 3, BITS == 4 ? 6 : 4>(a, sms, st);
+        e = up_launch<BITS, 2, Q4 ? 3 : 2, 2>(a, sms, st);
+        return e != cudaSuccess ? e : down_launch<BITS, 2, 3, Q4 ? 3 : 2>(a, sms, st);
     }
-    e = up_launch<BITS, 4, 2, 3, BITS == 4 ? 2 : 1>(a, units, sms, st);
-    return e != cudaSuccess ? e : down_launch<BITS, 4, 3, BITS == 4 ? 4 : 3>(a, sms, st);
+    e = up_launch<BITS, 4, Q4 ? 3 : 2, 1>(a, sms, st);
+    return e != cudaSuccess ? e : down_launch<BITS, 4, 3, 2>(a, sms, st);
 }
 
 cudaError_t moe_launch(MoeArgs& a, int sms, cudaStream_t st) {
-    const cudaError_t e = launch_pdl(moe_router_kernel, dim3(a.experts + 1, (a.tokens + kRouterTokens - 1) / kRouterTokens),
-                                     dim3(kRouterThreads), 0, st, a);
+    cudaError_t e = launch_pdl(moe_router_kernel, dim3(a.experts + 1, (a.tokens + kRouterTokens - 1) / kRouterTokens),
+                               dim3(kRouterThreads), 0, st, a);
     if (e != cudaSuccess) return e;
     // tokens of an item: two where there are no more; four where an expert gets two on average, since more cost
     // registers and a rare expert of many is read again from the cache; else eight
-    const int picks = a.tokens * a.top_k;
-    a.item = a.tokens <= 2 ? 2 : picks <= 2 * a.experts ? 4 : 8;
-    const int64_t units = (int64_t)picks * (a.inter / kTile);
-    const bool few = units <= 2 * (int64_t)sms;
-    return a.bits == 4 ? moe_kernels<4>(&a, a.item, few, units, sms, st) : moe_kernels<8>(&a, a.item, few, units, sms, st);
+    a.item = a.tokens <= 2 ? 2 : a.tokens * a.top_k <= 2 * a.experts ? 4 : 8;
+    e = launch_pdl(moe_choose_kernel, dim3(1), dim3(kChooseThreads), 0, st, a);
+    if (e != cudaSuccess) return e;
+    return a.bits == 4 ? moe_kernels<4>(&a, a.item, sms, st) : moe_kernels<8>(&a, a.item, sms, st);
 }
 
 }  // namespace
 
 cudaError_t moe_prepare() {
-    for (int item = 2; item <= 8; item *= 2)
-        for (int few = 0; few <= (item == 2); ++few) {
-            cudaError_t e = moe_kernels<4>(nullptr, item, few != 0, 0, 0, nullptr);
-            if (e == cudaSuccess) e = moe_kernels<8>(nullptr, item, few != 0, 0, 0, nullptr);
-            if (e != cudaSuccess) return e;
-        }
+    for (int item = 2; item <= 8; item *= 2) {
+        cudaError_t e = moe_kernels<4>(nullptr, item, 0, nullptr);
+        if (e == cudaSuccess) e = moe_kernels<8>(nullptr, item, 0, nullptr);
+        if (e != cudaSuccess) return e;
+    }
     return cudaSuccess;
 }
 
