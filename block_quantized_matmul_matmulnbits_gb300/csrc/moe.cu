@@ -4,14 +4,16 @@
 //   router   logits x . r_e, one CTA an expert and four tokens.  Which expert comes first decides the
 //            output, so the sums are held in two FP32 words each (products of FP16 are exact).
 //   choose   one CTA: a warp picks a token's experts; the list of (expert, some of its tokens).
-//   up       units of 32 features of one item: gate and up rows; the four warps of a CTA share the
-//            inputs of a unit.
+//   up       units of 32 features of one item, a CTA each; a warp takes 16 gate and 16 up rows by a quarter
+//            of the inputs.
 //   down     a cluster takes 32 outputs over all items, so the sum over experts stays in it.
 //
 // Every warp streams its own weights and inputs into a ring of steps in shared memory (cp.async: prefetched in
 // registers, 16 warps an SM waited for loads half of the time, since a short load's scoreboard is the
-// long ones' too).  A step is four blocks of 32 inputs by 32 rows (up: 32 gate and 32 up rows, so the inputs are
-// copied once for both).  A lane takes 16 bytes of codes a row: a quad's lanes hold the four blocks.
+// long ones' too).  A step is four blocks of 32 inputs by two tiles of 16 rows, two steps a ring: what bounds these
+// kernels is the instructions between memory and MMA, so many warps count for more than deep rings (gate and up of
+// 16 tokens: 24 warps an SM with two steps of 32 rows @T1@ us, 8 with three of 64 48).
+// A lane takes 16 bytes of codes a row: a quad's lanes hold the four blocks.
 // A lane takes the zero point of its own
 // block off (exact in FP16) and the rows go to the MMA (m16n8k16) as its left operand.
 // A step's columns are two tokens by the quad's four blocks: the right operand is zero
@@ -47,11 +49,10 @@ struct MoeWeight {
 };
 
 // An item: an expert and some of its tokens.
-struct __align__(64) MoeItem {
-    int expert, n;
-    uint16_t row[kMostItem];               // token * top_k + slot
+struct __align__(16) MoeItem {
+    uint16_t expert, n;
     uint8_t token[kMostItem];
-    float weight[kMostItem];
+    uint8_t row[kMostItem];                // token * top_k + slot
 };
 struct MoeTable {
     MoeItem item[kMaxItems];
@@ -65,6 +66,7 @@ struct MoeArgs {
     MoeWeight up, down;
     int item;             // tokens of an item
     double* logits;       // [tokens, experts]
+    float* w;             // [tokens, top_k]: the experts' weights
     MoeTable* table;      // the items, for the down kernel
     char* xs;             // [tokens + 1] rows of x, the last of zeros
     char* h;              // [tokens * top_k + 1] rows of silu(gate) up / 2^e, e of each 32; the last of zeros
@@ -246,6 +248,7 @@ __global__ void __launch_bounds__(kChooseThreads) moe_choose_kernel(const MoeArg
     if (tid < picks) {
         atomicOr(&mask[e], 1u << t);
         if (a.ids) a.ids[tid] = e;
+        a.w[tid] = weight[tid];
         if (a.weights) a.weights[tid] = weight[tid];
     }
     __syncthreads();
@@ -264,8 +267,8 @@ __global__ void __launch_bounds__(kChooseThreads) moe_choose_kernel(const MoeArg
             const int f = at + run - items;
             if (x < a.experts) first[x] = (uint16_t)f;
             for (int i = 0; i < items; ++i, n -= a.item) {
-                a.table->item[f + i].expert = x;
-                a.table->item[f + i].n = min(n, a.item);
+                a.table->item[f + i].expert = (uint16_t)x;
+                a.table->item[f + i].n = (uint16_t)min(n, a.item);
             }
             at += __shfl_sync(0xffffffffu, run, 31);
         }
@@ -275,9 +278,8 @@ __global__ void __launch_bounds__(kChooseThreads) moe_choose_kernel(const MoeArg
     if (tid < picks) {
         const int at = __popc(mask[e] & ((1u << t) - 1u)), i = at % a.item;
         MoeItem& it = a.table->item[first[e] + at / a.item];
-        it.row[i] = (uint16_t)tid;
+        it.row[i] = (uint8_t)tid;
         it.token[i] = (uint8_t)t;
-        it.weight[i] = weight[tid];
     }
 }
 
@@ -300,69 +302,83 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there
 __device__ __forceinline__ void copy16_l1(uint32_t dst, const void* src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool there) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(there ? 4 : 0) : "memory");
 }
-__device__ __forceinline__ void copy8(uint32_t dst, const void* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+__device__ __forceinline__ void copy8(uint32_t dst, const void* src, bool there) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(there ? 8 : 0) : "memory");
 }
 __device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void copies_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-// A step in the ring: HALVES times 32 rows by four blocks: codes (the lanes' pieces of 8 rows behind one another's), scales
-// [32][4], zero points [32][4]; then inputs (256 bytes a token) and the tokens' factors [4].
-template <int BITS, int HALVES, int NP>
+// A warp's shared memory: RING steps of codes (two tiles of 16 rows by four blocks, the lanes' pieces of 8 rows behind one
+// another's), inputs (256 bytes a token) and the tokens' factors [4]; then RING buffers of scales [32][16] and zero
+// points [32][16], four steps each (fewer where a warp's share of a row ends): 8 and 4 bytes of each row a step would take as long as its codes, a tag look-up a row.
+template <int BITS, int NP>
 struct Slot {
-    static constexpr int kScales = 512 * BITS, kZeros = kScales + 256, kHalf = kZeros + 128, kInputs = HALVES * kHalf,
-                         kFactors = kInputs + NP * 512, kBytes = kFactors + NP * 32;
+    static constexpr int kInputs = 512 * BITS, kFactors = kInputs + NP * 512, kBytes = kFactors + NP * 32;
+    static constexpr int kZeros = 1024, kQuad = 1536;
+    __host__ __device__ static constexpr int warp_bytes(int ring) { return ring * (kBytes + kQuad); }
 };
 
-// Where a lane's copies of 32 rows come from, moved on step by step: its codes' block of row lane / 4 (of four of
-// them, eight rows apart), four scales and four zero points of row lane.
+// Where a lane's copies of two tiles come from.  Codes: its block of row lane / 4 of the first tile, moved on step by step.
+// Scales and zero points: row lane / 4 too, four blocks from 4 (lane % 4) on of the row's.
 struct TilePtr {
     const uint8_t *q, *s, *z;
 };
 
 template <int BITS>
-__device__ __forceinline__ TilePtr tile_at(const MoeWeight& w, int64_t row, int step, int nblk) {
+__device__ __forceinline__ TilePtr tiles_at(const MoeWeight& w, int64_t row, int step, int nblk) {
     const int lane = threadIdx.x & 31;
-    const int64_t at = (row + lane) * nblk + step * 4;
-    return {w.q + ((row + (lane >> 2)) * nblk + step * 4 + (lane & 3)) * (4 * BITS),
-            reinterpret_cast<const uint8_t*>(w.s + at), w.z ? w.z + at : nullptr};
+    const int64_t at = (row + (lane >> 2)) * nblk;
+    return {w.q + (at + step * 4 + (lane & 3)) * (4 * BITS), reinterpret_cast<const uint8_t*>(w.s + at + (lane & 3) * 4),
+            w.z ? w.z + at + (lane & 3) * 4 : nullptr};
 }
 
-// Copies of 32 rows' weights for a step; blocks past the row's end (`left` of them are there) are zeros.  words: rows of scales
-// and zero points begin at a word, and all steps are whole.  eight: bytes of eight rows.
+// Copies of a step's codes; blocks past the row's end (`left` of them are there) are zeros.  eight: blocks of eight rows; second: from
+// the first tile to the other.
 template <int BITS>
-__device__ __forceinline__ void copy_weights(uint32_t slot, TilePtr& p, int eight, bool words, int left) {
-    constexpr int kScales = 512 * BITS, kZeros = kScales + 256;
+__device__ __forceinline__ void copy_codes(uint32_t slot, TilePtr& p, int eight, int64_t second, int left) {
     const int lane = threadIdx.x & 31;
-    const bool there = words || (lane & 3) < left;
+    const bool there = (lane & 3) < left;
     const uint8_t* q = p.q - (there ? 0 : (lane & 3) * (4 * BITS));  // a block that is there
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
+        const uint8_t* from = q + ((r >> 1 ? second : 0) + (r & 1 ? eight : 0)) * (4 * BITS);
 #pragma unroll
-        for (int i = 0; i < BITS / 4; ++i) copy16(slot + lane * 16 + (r * (BITS / 4) + i) * 512, q + i * 16, there);
-        q += eight;
-    }
-    if (words) {
-        copy8(slot + kScales + lane * 8, p.s);
-        if (p.z) copy4(slot + kZeros + lane * 4, p.z);
-    } else {
-        const __half* s = reinterpret_cast<const __half*>(p.s);
-        uint32_t v[2] = {0, 0}, z = 0;
-        for (int i = 0; i < 4 && i < left; ++i) {
-            v[i >> 1] |= (uint32_t)__half_as_ushort(s[i]) << (16 * (i & 1));
-            if (p.z) z |= (uint32_t)p.z[i] << (8 * i);
-        }
-        asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(slot + kScales + lane * 8), "r"(v[0]), "r"(v[1]) : "memory");
-        asm volatile("st.shared.u32 [%0], %1;" ::"r"(slot + kZeros + lane * 4), "r"(z) : "memory");
+        for (int i = 0; i < BITS / 4; ++i) copy16(slot + lane * 16 + (r * (BITS / 4) + i) * 512, from + i * 16, there);
     }
     p.q += 16 * BITS;
-    p.s += 8;
-    if (p.z) p.z += 4;
+}
+
+// Copies of the scales and zero points of the four steps that begin with block `first`; those past the row's end are zeros.
+// words: all rows begin at a word of four.
+__device__ __forceinline__ void copy_scales(uint32_t quad, const TilePtr& p, int first, int eight, int64_t second, bool words,
+                                            int nblk) {
+    constexpr int kZeros = Slot<4, 1>::kZeros;
+    const int lane = threadIdx.x & 31, left = nblk - first - (lane & 3) * 4;  // blocks from the lane's on
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const int64_t at = first + (r >> 1 ? second : 0) + (r & 1 ? eight : 0);
+        const uint32_t to = quad + (r * 8 + (lane >> 2)) * 32 + (lane & 3) * 8;
+        const uint32_t tz = quad + kZeros + (r * 8 + (lane >> 2)) * 16 + (lane & 3) * 4;
+        if (words) {
+            const int64_t in = left > 0 ? at : (r >> 1 ? second : 0) - (lane & 3) * 4;  // a place that is there
+            copy8(to, p.s + in * 2, left > 0);
+            if (p.z) copy4(tz, p.z + in, left > 0);
+        } else {
+            const __half* s = reinterpret_cast<const __half*>(p.s) + at;
+            uint32_t v[2] = {0, 0}, z = 0;
+            for (int i = 0; i < 4 && i < left; ++i) {
+                v[i >> 1] |= (uint32_t)__half_as_ushort(s[i]) << (16 * (i & 1));
+                if (p.z) z |= (uint32_t)p.z[at + i] << (8 * i);
+            }
+            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(to), "r"(v[0]), "r"(v[1]) : "memory");
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(tz), "r"(z) : "memory");
+        }
+    }
 }
 
 __device__ __forceinline__ uint32_t word(const uint4& v, int i) {
@@ -385,20 +401,23 @@ __device__ __forceinline__ void codes8(uint32_t lo, uint32_t hi, uint32_t c, uin
     o[3] = hsub2_rn(prmt(hi, 0x64646464u, 0x4342u), c);
 }
 
-// Adds a step of 32 rows times 2 P tokens: y[m][p][r] is row 16 m + 8 r + g of token 2 p + (lane & 3) / 2, blocks 2 (lane & 1) and
+// Adds a step (the one after `step` others of its four) times 2 P tokens: y[m][p][r] is row 8 r + g of tile m and token 2 p + (lane & 3) / 2, blocks 2 (lane & 1) and
 // the one behind it.  zeros: NP * 512 bytes of zeros, the inputs of lanes that have none: column g = lane / 4 is token
 // g / 4, block g % 4, and only the lanes that hold that block have any.
 template <int BITS, int NP, int P, bool FACTORS>
-__device__ __forceinline__ void step_of(const uint8_t* half, const uint8_t* inputs, const uint8_t* zeros, bool zp,
+__device__ __forceinline__ void step_of(const uint8_t* slot, const uint8_t* quad, int step, const uint8_t* zeros, bool zp,
                                         float (*y)[NP][2]) {
-    constexpr int kScales = 512 * BITS, kZeros = kScales + 256, W = BITS / 4;
+    using S = Slot<BITS, NP>;
+    constexpr int W = BITS / 4;
+    const uint8_t* inputs = slot + S::kInputs;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const uint4* codes = reinterpret_cast<const uint4*>(half) + lane;
+    const uint4* codes = reinterpret_cast<const uint4*>(slot) + lane;
     const uint8_t* x = (g & 3) == t ? inputs + (g >> 2) * 256 + t * 16 : zeros;
-    uint32_t c0[4], d0[4];  // of the rows g, g + 8, g + 16, g + 24
+    const uint8_t* zps = quad + S::kZeros + step * 4;
+    uint32_t c0[4], d0[4];  // of the rows g and g + 8 of both tiles
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-        const uint32_t z = zp ? half[kZeros + r * 32 + lane] : 1u << (BITS - 1);
+        const uint32_t z = zp ? zps[(r * 8 + g) * 16 + t] : 1u << (BITS - 1);
         c0[r] = kMagic1024x2 | z * 0x00010001u;
         d0[r] = hsub2_rn(kHalf960x2, c0[r]);
     }
@@ -437,7 +456,7 @@ __device__ __forceinline__ void step_of(const uint8_t* half, const uint8_t* inpu
     float2 f[4];
 #pragma unroll
     for (int r = 0; r < 4; ++r)
-        f[r] = __half22float2(*reinterpret_cast<const __half2*>(half + kScales + (r * 8 + g) * 8 + (t & 1) * 4));
+        f[r] = __half22float2(*reinterpret_cast<const __half2*>(quad + (r * 8 + g) * 32 + step * 8 + (t & 1) * 4));
 #pragma unroll
     for (int p = 0; p < P; ++p) {
         float2 e = make_float2(1.f, 1.f);
@@ -455,27 +474,27 @@ __device__ __forceinline__ void step_of(const uint8_t* half, const uint8_t* inpu
 
 // The step for so many pairs (three are done as four): one branch, not one at every product.
 template <int BITS, int NP, bool FACTORS>
-__device__ __forceinline__ void do_step(const uint8_t* half, const uint8_t* inputs, const uint8_t* zeros, bool zp, int pairs,
-                                        float (*y)[NP][2]) {
+__device__ __forceinline__ void do_step(const uint8_t* slot, const uint8_t* quad, int step, const uint8_t* zeros, bool zp,
+                                        int pairs, float (*y)[NP][2]) {
     if (NP == 1 || pairs == 1)
-        step_of<BITS, NP, 1, FACTORS>(half, inputs, zeros, zp, y);
+        step_of<BITS, NP, 1, FACTORS>(slot, quad, step, zeros, zp, y);
     else if (NP == 2 || pairs == 2)
-        step_of<BITS, NP, (NP < 2 ? NP : 2), FACTORS>(half, inputs, zeros, zp, y);
+        step_of<BITS, NP, (NP < 2 ? NP : 2), FACTORS>(slot, quad, step, zeros, zp, y);
     else
-        step_of<BITS, NP, NP, FACTORS>(half, inputs, zeros, zp, y);
+        step_of<BITS, NP, NP, FACTORS>(slot, quad, step, zeros, zp, y);
 }
 
-constexpr int kWarps = 4;
+constexpr int kUpWarps = 8, kSlices = kUpWarps / 2, kDownWarps = 4;
 
 // ---- gate and up -------------------------------------------------------------
 
 // Variants: NP, pairs of tokens of an item; RING steps in shared memory.
 template <int BITS, int NP, int RING, int CTAS>
-__global__ void __launch_bounds__(kWarps * 32, CTAS) moe_up_kernel(const MoeArgs a) {
-    using S = Slot<BITS, 2, NP>;
+__global__ void __launch_bounds__(kUpWarps * 32, CTAS) moe_up_kernel(const MoeArgs a) {
+    using S = Slot<BITS, NP>;
     extern __shared__ __align__(16) uint8_t ring[];
     __shared__ MoeItem it[NP == 1 ? 2 * kMaxTop : kMaxItems];  // (one pair: there are two tokens at most)
-    __shared__ float red[2][kWarps][64][2 * NP + 1];
+    __shared__ float red[2][kSlices][64][2 * NP + 1];  // rows: gate 0 .. 31, up 0 .. 31
     __shared__ uint4 zero[NP * 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid < NP * 32) zero[tid] = make_uint4(0, 0, 0, 0);
@@ -484,8 +503,10 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) moe_up_kernel(const MoeArgs
     const int count = load_items(a.table, it);
 
     const int nblk = a.hidden >> 5, steps = (nblk + 3) >> 2, tiles = a.inter / kTile;
-    const int s0 = steps * warp / kWarps, s1 = steps * (warp + 1) / kWarps;  // the warp's share of the inputs
-    const int eight = nblk * (32 * BITS);
+    // the warp's features of a unit, and its share of the inputs
+    const int part = warp & 1, slice = warp >> 1, s0 = steps * slice / kSlices, s1 = steps * (slice + 1) / kSlices;
+    const int eight = 8 * nblk;
+    const int64_t second = (int64_t)a.inter * nblk;
     const int64_t pitch = row_bytes(a.hidden), hpitch = row_bytes(a.inter);
     const bool words = !(nblk & 3);
     // the CTA's units, one every gridDim.x: item and tile without a division each
@@ -499,20 +520,18 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) moe_up_kernel(const MoeArgs
         u.tile += by_tile;
         if (u.tile >= tiles) u.tile -= tiles, ++u.item;
     };
-    uint8_t* const own = ring + warp * (RING * S::kBytes);
-    const uint32_t base = smem_u32(own);
+    uint8_t* const own = ring + warp * S::warp_bytes(RING);
+    const uint32_t base = smem_u32(own), quads = base + RING * S::kBytes;
     const uint8_t* const zeros = reinterpret_cast<const uint8_t*>(zero);
     Unit lu = first;  // what is copied next
     int ls = s0, lpairs = 0;
     bool more = s0 < s1 && lu.item < count;
-    uint32_t lslot = base;
-    TilePtr lp[2];
+    uint32_t lslot = base, lquad = quads;
+    TilePtr lp;
     const char* lx[NP];
     auto aim = [&] {
         const MoeItem& i = it[lu.item];
-        const int64_t row = (int64_t)i.expert * 2 * a.inter + lu.tile * kTile;
-        lp[0] = tile_at<BITS>(a.up, row, s0, nblk);
-        lp[1] = tile_at<BITS>(a.up, row + a.inter, s0, nblk);
+        lp = tiles_at<BITS>(a.up, (int64_t)i.expert * 2 * a.inter + lu.tile * kTile + part * 16, s0, nblk);
         lpairs = (i.n + 1) >> 1;
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
@@ -522,8 +541,11 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) moe_up_kernel(const MoeArgs
     };
     auto issue = [&] {
         if (more) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) copy_weights<BITS>(lslot + h * S::kHalf, lp[h], eight, words, nblk - ls * 4);
+            copy_codes<BITS>(lslot, lp, eight, second, nblk - ls * 4);
+            if (ls == s0 || !(ls & 3)) {
+                copy_scales(lquad, lp, (ls & ~3) * 4, eight, second, words, nblk);
+                lquad = lquad == quads + (RING - 1) * S::kQuad ? quads : lquad + S::kQuad;
+            }
 #pragma unroll
             for (int p = 0; p < NP; ++p) {
                 if (p < lpairs) copy16_l1(lslot + S::kInputs + p * 512 + lane * 16, lx[p]);
@@ -543,39 +565,38 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) moe_up_kernel(const MoeArgs
 #pragma unroll
     for (int i = 0; i < RING - 1; ++i) issue();
     int buf = 0;
-    const uint8_t* slot = own;
+    const uint8_t *slot = own, *const last = own + RING * S::kBytes + (RING - 1) * S::kQuad, *quad = last;
     for (Unit u = first; u.item < count; next(u), buf ^= 1) {
         const MoeItem& i = it[u.item];
         const int n = i.n, pairs = (n + 1) >> 1;
-        float y[2][2][NP][2];
+        float y[2][NP][2];
 #pragma unroll
-        for (int v = 0; v < 8 * NP; ++v) (&y[0][0][0][0])[v] = 0.f;
+        for (int v = 0; v < 4 * NP; ++v) (&y[0][0][0])[v] = 0.f;
         for (int s = s0; s < s1; ++s) {
             copies_wait<RING - 2>();
             __syncwarp();  // everyone's copies are there, and the slot before is read
             issue();
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                do_step<BITS, NP, false>(slot + h * S::kHalf, slot + S::kInputs, zeros, a.up.z != nullptr, pairs, y[h]);
+            if (s == s0 || !(s & 3)) quad = quad == last ? own + RING * S::kBytes : quad + S::kQuad;
+            do_step<BITS, NP, false>(slot, quad, s & 3, zeros, a.up.z != nullptr, pairs, y);
             slot = slot == own + (RING - 1) * S::kBytes ? own : slot + S::kBytes;
         }
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
             if (p >= pairs) break;
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    float v = y[h][m >> 1][p][m & 1];
-                    v += __shfl_xor_sync(0xffffffffu, v, 1);
-                    if (!(lane & 1)) red[buf][warp][h * 32 + m * 8 + (lane >> 2)][2 * p + ((lane & 3) >> 1)] = v;
-                }
+            for (int m = 0; m < 4; ++m) {
+                float v = y[m >> 1][p][m & 1];
+                v += __shfl_xor_sync(0xffffffffu, v, 1);
+                if (!(lane & 1))
+                    red[buf][slice][(m >> 1) * 32 + part * 16 + (m & 1) * 8 + (lane >> 2)][2 * p + ((lane & 3) >> 1)] = v;
+            }
         }
         __syncthreads();
-        for (int w = warp; w < n; w += kWarps) {  // a warp a token, a lane a feature
+        if (warp < n) {  // a warp a token, a lane a feature
+            const int w = warp;
             float gate = 0.f, up = 0.f;
 #pragma unroll
-            for (int v = 0; v < kWarps; ++v) {
+            for (int v = 0; v < kSlices; ++v) {
                 gate += red[buf][v][lane][w];
                 up += red[buf][v][32 + lane][w];
             }
@@ -592,7 +613,7 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) moe_up_kernel(const MoeArgs
             const int in = BITS == 8 ? lane & 7 : (lane & 3) * 2 + ((lane >> 2) & 1);
             reinterpret_cast<__half*>(to)[in] = __float2half_rn(h * __uint_as_float(0x7F000000u - e));
             float* fe = a.he + (int64_t)at * ((tiles + 3) & ~3);
-            if (lane == 0) fe[u.tile] = i.weight[w] * __uint_as_float(e);
+            if (lane == 0) fe[u.tile] = a.w[at] * __uint_as_float(e);
             if (u.tile == tiles - 1)  // zeros up to a whole step
                 for (int b = tiles; b < ((tiles + 3) & ~3); ++b) {
                     if (lane < 4)
@@ -609,38 +630,39 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) moe_up_kernel(const MoeArgs
 constexpr int kDownRows = 32;
 
 template <int BITS, int NP, int RING, int CTAS>
-__global__ void __launch_bounds__(kWarps * 32, CTAS) moe_down_kernel(const MoeArgs a) {
-    using S = Slot<BITS, 1, NP>;
+__global__ void __launch_bounds__(kDownWarps * 32, CTAS) moe_down_kernel(const MoeArgs a) {
+    using S = Slot<BITS, NP>;
     extern __shared__ __align__(16) uint8_t ring[];
-    __shared__ MoeItem it[NP == 1 ? 2 * kMaxTop : kMaxItems];  // (one pair: there are two tokens at most)
-    __shared__ float acc[kWarps][kTokens][kDownRows + 1];
+    __shared__ float acc[kDownWarps][kTokens][kDownRows + 1];
     __shared__ uint4 zero[NP * 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid < NP * 32) zero[tid] = make_uint4(0, 0, 0, 0);
     // a cluster (along z) takes 32 rows; its warps share the steps of all items
-    const int parts = gridDim.z, worker = blockIdx.z * kWarps + warp;
+    const int parts = gridDim.z, worker = blockIdx.z * kDownWarps + warp;
     for (int i = lane; i < kTokens * (kDownRows + 1); i += 32) acc[warp][0][i] = 0.f;
     pdl_wait();
     pdl_launch_dependents();
-    const int count = load_items(a.table, it);
+    const MoeItem* const it = a.table->item;
+    const int count = a.table->count;
+    __syncthreads();  // the zeros
     const bool words = !((a.inter >> 5) & 3);
-    const int nblk = a.inter >> 5, steps = (nblk + 3) >> 2, row0 = blockIdx.x * kDownRows, eight = nblk * (32 * BITS);
+    const int nblk = a.inter >> 5, steps = (nblk + 3) >> 2, row0 = blockIdx.x * kDownRows, eight = 8 * nblk;
     const int64_t pitch = row_bytes(a.inter);
     const int total = count * steps;
-    const int f0 = (int)((int64_t)total * worker / (parts * kWarps)),
-              f1 = (int)((int64_t)total * (worker + 1) / (parts * kWarps));
-    uint8_t* const own = ring + warp * (RING * S::kBytes);
-    const uint32_t base = smem_u32(own);
+    const int f0 = (int)((int64_t)total * worker / (parts * kDownWarps)),
+              f1 = (int)((int64_t)total * (worker + 1) / (parts * kDownWarps));
+    uint8_t* const own = ring + warp * S::warp_bytes(RING);
+    const uint32_t base = smem_u32(own), quads = base + RING * S::kBytes;
     const uint8_t* const zeros = reinterpret_cast<const uint8_t*>(zero);
     int li = f0 / steps, ls = f0 - li * steps, lf = f0, lpairs = 0;  // what is copied next
-    uint32_t lslot = base;
+    uint32_t lslot = base, lquad = quads;
     TilePtr lp;
     const char* lx[NP];
     const float* le;  // factors of token `lane` of the item
     auto aim = [&] {
         if (lf >= f1) return;
         const MoeItem& i = it[li];
-        lp = tile_at<BITS>(a.down, (int64_t)i.expert * a.hidden + row0, ls, nblk);
+        lp = tiles_at<BITS>(a.down, (int64_t)i.expert * a.hidden + row0, ls, nblk);
         lpairs = (i.n + 1) >> 1;
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
@@ -652,7 +674,11 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) moe_down_kernel(const MoeAr
     };
     auto issue = [&] {
         if (lf < f1) {
-            copy_weights<BITS>(lslot, lp, eight, words, nblk - ls * 4);
+            copy_codes<BITS>(lslot, lp, eight, 2 * eight, nblk - ls * 4);
+            if (lf == f0 || !(ls & 3)) {
+                copy_scales(lquad, lp, (ls & ~3) * 4, eight, 2 * eight, words, nblk);
+                lquad = lquad == quads + (RING - 1) * S::kQuad ? quads : lquad + S::kQuad;
+            }
 #pragma unroll
             for (int p = 0; p < NP; ++p) {
                 if (p < lpairs) copy16(lslot + S::kInputs + p * 512 + lane * 16, lx[p], true);
@@ -697,12 +723,13 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) moe_down_kernel(const MoeAr
         }
     };
     if (f0 < f1) begin();
-    const uint8_t* slot = own;
+    const uint8_t *slot = own, *const last = own + RING * S::kBytes + (RING - 1) * S::kQuad, *quad = last;
     for (int f = f0; f < f1; ++f) {
         copies_wait<RING - 2>();
         __syncwarp();  // everyone's copies are there, and the slot before is read
         issue();
-        do_step<BITS, NP, true>(slot, slot + S::kInputs, zeros, a.down.z != nullptr, pairs, y);
+        if (f == f0 || !(step & 3)) quad = quad == last ? own + RING * S::kBytes : quad + S::kQuad;
+        do_step<BITS, NP, true>(slot, quad, step & 3, zeros, a.down.z != nullptr, pairs, y);
         slot = slot == own + (RING - 1) * S::kBytes ? own : slot + S::kBytes;
         if (++step == steps) {
             finish();
@@ -714,11 +741,11 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) moe_down_kernel(const MoeAr
     if (f0 < f1 && step != 0) finish();
     __syncthreads();
     // the warps' sums in order, then the CTAs'
-    for (int i = tid; i < a.tokens * kDownRows; i += kWarps * 32) {
+    for (int i = tid; i < a.tokens * kDownRows; i += kDownWarps * 32) {
         const int t = i / kDownRows, r = i % kDownRows;
         float v = acc[0][t][r];
 #pragma unroll
-        for (int w = 1; w < kWarps; ++w) v += acc[w][t][r];
+        for (int w = 1; w < kDownWarps; ++w) v += acc[w][t][r];
         acc[0][t][r] = v;
         if (parts == 1) a.y[(int64_t)t * a.hidden + row0 + r] = __float2half_rn(v);
     }
@@ -727,7 +754,7 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) moe_down_kernel(const MoeAr
         asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
         asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
         // each CTA takes its share of the tokens' rows
-        for (int i = blockIdx.z * kWarps * 32 + tid; i < a.tokens * kDownRows; i += parts * kWarps * 32) {
+        for (int i = blockIdx.z * kDownWarps * 32 + tid; i < a.tokens * kDownRows; i += parts * kDownWarps * 32) {
             const int t = i / kDownRows, r = i % kDownRows;
             float v = 0.f;
             for (int c = 0; c < parts; ++c) v += ld_peer_f32(smem_u32(&acc[0][t][r]), c);
@@ -743,13 +770,14 @@ bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p
 
 // Offsets of the workspace's parts, 256-byte aligned.
 struct MoeLayout {
-    int64_t table, xs, h, he, bytes;
+    int64_t w, table, xs, h, he, bytes;
 };
 
 MoeLayout moe_layout(const mnb_moe_layer* l, int64_t M) {
     auto up = [](int64_t n) { return (n + 255) & ~(int64_t)255; };
     MoeLayout o;
-    o.table = up(M * l->experts * 8);
+    o.w = up(M * l->experts * 8);
+    o.table = o.w + up(M * l->top_k * 4);
     o.xs = o.table + up(sizeof(MoeTable));
     o.h = o.xs + (M + 1) * row_bytes(l->hidden);
     o.he = o.h + (M * l->top_k + 1) * row_bytes(l->inter);
@@ -770,22 +798,22 @@ int moe_check(const mnb_moe_layer* l, int64_t M) {
 // The up kernel's grid: as many CTAs as run at once, or as there can be units.
 template <int BITS, int NP, int RING, int CTAS>
 cudaError_t up_launch(const MoeArgs* a, int sms, cudaStream_t st) {
-    constexpr int smem = kWarps * RING * Slot<BITS, 2, NP>::kBytes;
+    constexpr int smem = kUpWarps * Slot<BITS, NP>::warp_bytes(RING);
     const auto kernel = moe_up_kernel<BITS, NP, RING, CTAS>;
     if (!a) return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     const int64_t slots = (int64_t)CTAS * sms, units = (int64_t)a->tokens * a->top_k * (a->inter / kTile);
-    return launch_pdl(kernel, dim3((unsigned)(units < slots ? units : slots)), dim3(kWarps * 32), smem, st, *a);
+    return launch_pdl(kernel, dim3((unsigned)(units < slots ? units : slots)), dim3(kUpWarps * 32), smem, st, *a);
 }
 
 template <int BITS, int NP, int RING, int CTAS>
 cudaError_t down_launch(const MoeArgs* a, int sms, cudaStream_t st) {
-    constexpr int smem = kWarps * RING * Slot<BITS, 1, NP>::kBytes;
+    constexpr int smem = kDownWarps * Slot<BITS, NP>::warp_bytes(RING);
     const auto kernel = moe_down_kernel<BITS, NP, RING, CTAS>;
     if (!a) return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     const int tiles = a->hidden / kDownRows;
     int parts = CTAS * sms / tiles;  // CTAs of 32 rows: as many as fit, at most eight
     parts = parts < 1 ? 1 : parts > 8 ? 8 : parts;
-    return launch_pdl(kernel, dim3(tiles, 1, parts), dim3(kWarps * 32), smem, st, *a, parts);
+    return launch_pdl(kernel, dim3(tiles, 1, parts), dim3(kDownWarps * 32), smem, st, *a, parts);
 }
 
 // The two kernels for items of `item` tokens; without arguments, what has to be set up for them.
@@ -794,15 +822,15 @@ cudaError_t moe_kernels(const MoeArgs* a, int item, int sms, cudaStream_t st) {
     constexpr bool Q4 = BITS == 4;
     cudaError_t e;
     if (item == 2) {
-        e = up_launch<BITS, 1, Q4 ? 3 : 2, 3>(a, sms, st);
-        return e != cudaSuccess ? e : down_launch<BITS, 1, Q4 ? 4 : 3, 3>(a, sms, st);
+        e = up_launch<BITS, 1, Q4 ? 3 : 2, 2>(a, sms, st);
+        return e != cudaSuccess ? e : down_launch<BITS, 1, 2, Q4 ? 5 : 3>(a, sms, st);
     }
     if (item == 4) {
-        e = up_launch<BITS, 2, Q4 ? 3 : 2, 2>(a, sms, st);
-        return e != cudaSuccess ? e : down_launch<BITS, 2, 3, Q4 ? 3 : 2>(a, sms, st);
+        e = up_launch<BITS, 2, Q4 ? 2 : 3, Q4 ? 2 : 1>(a, sms, st);
+        return e != cudaSuccess ? e : down_launch<BITS, 2, 2, Q4 ? 4 : 3>(a, sms, st);
     }
-    e = up_launch<BITS, 4, Q4 ? 3 : 2, 1>(a, sms, st);
-    return e != cudaSuccess ? e : down_launch<BITS, 4, 3, 2>(a, sms, st);
+    e = up_launch<BITS, 4, Q4 ? 4 : 3, 1>(a, sms, st);
+    return e != cudaSuccess ? e : down_launch<BITS, 4, 2, 3>(a, sms, st);
 }
 
 cudaError_t moe_launch(MoeArgs& a, int sms, cudaStream_t st) {
@@ -870,6 +898,7 @@ extern "C" int mnb_moe(const mnb_moe_layer* layer, const void* X, int64_t M, voi
     a.down = {static_cast<const uint8_t*>(l.down_Wq), static_cast<const __half*>(l.down_scales),
               static_cast<const uint8_t*>(l.down_zp)};
     a.logits = reinterpret_cast<double*>(w);
+    a.w = reinterpret_cast<float*>(w + o.w);
     a.table = reinterpret_cast<MoeTable*>(w + o.table);
     a.xs = w + o.xs;
     a.h = w + o.h;
