@@ -313,17 +313,19 @@ template <int N>
 __device__ __forceinline__ void copies_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-// A warp's shared memory: RING steps of codes (two tiles of 16 rows by four blocks, the lanes' pieces of 8 rows behind one
-// another's), inputs (256 bytes a token) and the tokens' factors [4]; then RING buffers of scales [32][16] and zero
+// A warp's shared memory: RING steps of codes (two tiles of 16 rows by four blocks, 64 bytes of each of 8 rows behind one
+// another; the second 64 of 8-bit codes 16 further, so that a quad's reads of a block each meet no bank twice), inputs (256 bytes a token) and the tokens' factors [4]; then RING buffers of scales [32][16] and zero
 // points [32][16], four steps each (fewer where a warp's share of a row ends): 8 and 4 bytes of each row a step would take as long as its codes, a tag look-up a row.
 template <int BITS, int NP>
 struct Slot {
-    static constexpr int kInputs = 512 * BITS, kFactors = kInputs + NP * 512, kBytes = kFactors + NP * 32;
+    static constexpr int kPiece = BITS == 4 ? 512 : 528, kRows = kPiece * (BITS / 4);  // 64 bytes of 8 rows; 8 rows
+    static constexpr int kInputs = 4 * kRows, kFactors = kInputs + NP * 512, kBytes = kFactors + NP * 32;
     static constexpr int kZeros = 1024, kQuad = 1536;
     __host__ __device__ static constexpr int warp_bytes(int ring) { return ring * (kBytes + kQuad); }
 };
 
-// Where a lane's copies of two tiles come from.  Codes: its block of row lane / 4 of the first tile, moved on step by step.
+// Where a lane's copies of two tiles come from.  Codes: 16 bytes from 16 (lane % 4) on of row lane / 4 of the first tile, moved
+// on step by step (64 bytes of a row at a time: less than whole 32-byte sectors would be read twice).
 // Scales and zero points: row lane / 4 too, four blocks from 4 (lane % 4) on of the row's.
 struct TilePtr {
     const uint8_t *q, *s, *z;
@@ -333,7 +335,7 @@ template <int BITS>
 __device__ __forceinline__ TilePtr tiles_at(const MoeWeight& w, int64_t row, int step, int nblk) {
     const int lane = threadIdx.x & 31;
     const int64_t at = (row + (lane >> 2)) * nblk;
-    return {w.q + (at + step * 4 + (lane & 3)) * (4 * BITS), reinterpret_cast<const uint8_t*>(w.s + at + (lane & 3) * 4),
+    return {w.q + (at + step * 4) * (4 * BITS) + (lane & 3) * 16, reinterpret_cast<const uint8_t*>(w.s + at + (lane & 3) * 4),
             w.z ? w.z + at + (lane & 3) * 4 : nullptr};
 }
 
@@ -341,14 +343,17 @@ __device__ __forceinline__ TilePtr tiles_at(const MoeWeight& w, int64_t row, int
 // the first tile to the other.
 template <int BITS>
 __device__ __forceinline__ void copy_codes(uint32_t slot, TilePtr& p, int eight, int64_t second, int left) {
+    using S = Slot<BITS, 1>;
     const int lane = threadIdx.x & 31;
-    const bool there = (lane & 3) < left;
-    const uint8_t* q = p.q - (there ? 0 : (lane & 3) * (4 * BITS));  // a block that is there
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        const uint8_t* from = q + ((r >> 1 ? second : 0) + (r & 1 ? eight : 0)) * (4 * BITS);
+    for (int i = 0; i < BITS / 4; ++i) {
+        const int block = BITS == 4 ? lane & 3 : 2 * i + ((lane & 3) >> 1);
+        const bool there = block < left;
+        const uint8_t* q = there ? p.q + i * 64 : p.q - (lane & 3) * 16;  // bytes that are there
 #pragma unroll
-        for (int i = 0; i < BITS / 4; ++i) copy16(slot + lane * 16 + (r * (BITS / 4) + i) * 512, from + i * 16, there);
+        for (int r = 0; r < 4; ++r)
+            copy16(slot + r * S::kRows + i * S::kPiece + lane * 16,
+                   q + ((r >> 1 ? second : 0) + (r & 1 ? eight : 0)) * (4 * BITS), there);
     }
     p.q += 16 * BITS;
 }
@@ -408,10 +413,10 @@ template <int BITS, int NP, int P, bool FACTORS>
 __device__ __forceinline__ void step_of(const uint8_t* slot, const uint8_t* quad, int step, const uint8_t* zeros, bool zp,
                                         float (*y)[NP][2]) {
     using S = Slot<BITS, NP>;
-    constexpr int W = BITS / 4;
     const uint8_t* inputs = slot + S::kInputs;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const uint4* codes = reinterpret_cast<const uint4*>(slot) + lane;
+    // this lane's block of row g
+    const uint8_t* codes = slot + (BITS == 4 ? lane * 16 : (t >> 1) * S::kPiece + g * 64 + (t & 1) * 32);
     const uint8_t* x = (g & 3) == t ? inputs + (g >> 2) * 256 + t * 16 : zeros;
     const uint8_t* zps = quad + S::kZeros + step * 4;
     uint32_t c0[4], d0[4];  // of the rows g and g + 8 of both tiles
@@ -427,7 +432,8 @@ __device__ __forceinline__ void step_of(const uint8_t* slot, const uint8_t* quad
     for (int j = 0; j < 4; ++j) {
         if (BITS == 4 ? j == 0 : (j & 1) == 0) {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) raw[r] = codes[(r * W + (BITS == 4 ? 0 : j >> 1)) * 32];
+            for (int r = 0; r < 4; ++r)
+                raw[r] = *reinterpret_cast<const uint4*>(codes + r * S::kRows + (BITS == 4 ? 0 : (j >> 1) * 16));
         }
         uint4 v[P];
 #pragma unroll
