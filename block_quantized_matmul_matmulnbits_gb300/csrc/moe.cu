@@ -172,58 +172,57 @@ __device__ __forceinline__ float exp_of(double d) {  // d <= 0, or NaN
     return expf(hi) * (1.f + (isfinite(hi) ? (float)(d - (double)hi) : 0.f));
 }
 
-// The top_k experts of a token, by the whole warp: the largest logit top_k times.
-__device__ void moe_choose(const MoeArgs& a, int token, int32_t* sel, float* weight) {
+// The top_k experts of a token, by the whole warp: the largest logit top_k times.  Every lane knows the best of its own; a round
+// is the largest of their upper words, and only the lane that holds it looks at its others again.
+__device__ void moe_choose(const MoeArgs& a, int token, int32_t* sel, float* weight, double* chosen) {
     constexpr int kEach = kMaxExperts / 32;
     const int lane = threadIdx.x & 31;
     const double* l = a.logits + (int64_t)token * a.experts;
     unsigned long long key[kEach];
-    double v[kEach];
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
         const int e = i * 32 + lane;
         key[i] = 0;
-        v[i] = 0.0;
-        if (i * 32 >= a.experts) continue;
-        if (e < a.experts) {
-            v[i] = l[e];
-            key[i] = order64(v[i]);
-        }
+        if (i * 32 < a.experts && e < a.experts) key[i] = order64(l[e]);
     }
-    double top = 0.0, mine = 0.0;
-    for (int r = 0; r < a.top_k; ++r) {
-        unsigned long long best = key[0];
-        double bv = v[0];
-        int be = lane;
+    unsigned long long best = 0;
+    int be = lane;
+    auto look = [&] {
+        best = key[0];
+        be = lane;
 #pragma unroll
         for (int i = 1; i < kEach; ++i) {
             if (i * 32 >= a.experts) break;
-            if (key[i] > best) best = key[i], bv = v[i], be = i * 32 + lane;
+            if (key[i] > best) best = key[i], be = i * 32 + lane;
         }
+    };
+    look();
+    for (int r = 0; r < a.top_k; ++r) {
         const unsigned hi = (unsigned)(best >> 32), m = __reduce_max_sync(0xffffffffu, hi);
-        const unsigned lo = hi == m ? (unsigned)best : 0u, m2 = __reduce_max_sync(0xffffffffu, lo);
-        const int e = __reduce_min_sync(0xffffffffu, hi == m && lo == m2 ? be : INT32_MAX);
-        const double chosen = __shfl_sync(0xffffffffu, bv, e & 31);
-        if (r == 0) top = chosen;
-        if (lane == r) {
-            mine = chosen;
-            sel[r] = e;
+        bool mine = hi == m;
+        if (__popc(__ballot_sync(0xffffffffu, mine)) > 1) {  // then the lower words, then the lower number
+            const unsigned lo = mine ? (unsigned)best : 0u, m2 = __reduce_max_sync(0xffffffffu, lo);
+            mine = mine && lo == m2;
+            const int e = __reduce_min_sync(0xffffffffu, mine ? be : INT32_MAX);
+            mine = mine && be == e;
         }
+        if (mine) {
+            sel[r] = be;
+            chosen[r] = l[be];
 #pragma unroll
-        for (int i = 0; i < kEach; ++i) {
-            if (i * 32 >= a.experts) break;
-            if (e == i * 32 + lane) key[i] = 0;
+            for (int i = 0; i < kEach; ++i)
+                if (be == i * 32 + lane) key[i] = 0;
+            look();
         }
     }
-    float w = lane < a.top_k ? exp_of(mine - top) : 0.f, sum = 0.f;
+    __syncwarp();
+    const double top = chosen[0];
+    float w = lane < a.top_k ? exp_of(chosen[lane] - top) : 0.f, sum = 0.f;
     if (a.normalize) {
         sum = w;
     } else {
-#pragma unroll
-        for (int i = 0; i < kEach; ++i) {
-            if (i * 32 >= a.experts) break;
-            if (i * 32 + lane < a.experts) sum += exp_of(v[i] - top);
-        }
+#pragma unroll 1
+        for (int e = lane; e < a.experts; e += 32) sum += exp_of(l[e] - top);
     }
 #pragma unroll
     for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
@@ -238,11 +237,12 @@ __global__ void __launch_bounds__(kChooseThreads) moe_choose_kernel(const MoeArg
     __shared__ uint16_t first[kMaxExperts];  // its first item
     __shared__ int32_t sel[kTokens * kMaxTop];
     __shared__ float weight[kTokens * kMaxTop];
+    __shared__ double chosen[kTokens * kMaxTop];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, picks = a.tokens * a.top_k;
     for (int e = tid; e < a.experts; e += kChooseThreads) mask[e] = 0;
     pdl_wait();
     pdl_launch_dependents();
-    if (warp < a.tokens) moe_choose(a, warp, sel + warp * a.top_k, weight + warp * a.top_k);
+    if (warp < a.tokens) moe_choose(a, warp, sel + warp * a.top_k, weight + warp * a.top_k, chosen + warp * a.top_k);
     __syncthreads();
     const int t = tid / a.top_k, e = tid < picks ? sel[tid] : 0;
     if (tid < picks) {
@@ -283,11 +283,12 @@ __global__ void __launch_bounds__(kChooseThreads) moe_choose_kernel(const MoeArg
     }
 }
 
-// The items into shared memory, once the choice is there. Whole CTA.
-__device__ __forceinline__ int load_items(const MoeTable* table, MoeItem* items) {
-    const int count = table->count;
-    const uint4* from = reinterpret_cast<const uint4*>(table->item);
-    for (int i = threadIdx.x; i < count * (int)(sizeof(MoeItem) / 16); i += blockDim.x)
+// The items into shared memory, once the choice is there: as many as there can be, without waiting for their number.
+// Whole CTA.
+__device__ __forceinline__ int load_items(const MoeArgs& a, MoeItem* items) {
+    const int count = a.table->count;
+    const uint4* from = reinterpret_cast<const uint4*>(a.table->item);
+    for (int i = threadIdx.x; i < a.tokens * a.top_k * (int)(sizeof(MoeItem) / 16); i += blockDim.x)
         reinterpret_cast<uint4*>(items)[i] = from[i];
     __syncthreads();
     return count;
@@ -490,27 +491,27 @@ __device__ __forceinline__ void do_step(const uint8_t* slot, const uint8_t* quad
         step_of<BITS, NP, NP, FACTORS>(slot, quad, step, zeros, zp, y);
 }
 
-constexpr int kUpWarps = 8, kSlices = kUpWarps / 2, kDownWarps = 4;
+constexpr int kDownWarps = 4;
 
 // ---- gate and up -------------------------------------------------------------
 
-// Variants: NP, pairs of tokens of an item; RING steps in shared memory.
-template <int BITS, int NP, int RING, int CTAS>
-__global__ void __launch_bounds__(kUpWarps * 32, CTAS) moe_up_kernel(const MoeArgs a) {
+// Variants: NP, pairs of tokens of an item; SLICES, warps that share a row's inputs; RING steps in shared memory.
+template <int BITS, int NP, int SLICES, int RING, int CTAS>
+__global__ void __launch_bounds__(SLICES * 64, CTAS) moe_up_kernel(const MoeArgs a) {
     using S = Slot<BITS, NP>;
     extern __shared__ __align__(16) uint8_t ring[];
     __shared__ MoeItem it[NP == 1 ? 2 * kMaxTop : kMaxItems];  // (one pair: there are two tokens at most)
-    __shared__ float red[2][kSlices][64][2 * NP + 1];  // rows: gate 0 .. 31, up 0 .. 31
+    __shared__ float red[2][SLICES][64][2 * NP + 1];  // rows: gate 0 .. 31, up 0 .. 31
     __shared__ uint4 zero[NP * 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid < NP * 32) zero[tid] = make_uint4(0, 0, 0, 0);
     pdl_wait();
     pdl_launch_dependents();
-    const int count = load_items(a.table, it);
+    const int count = load_items(a, it);
 
     const int nblk = a.hidden >> 5, steps = (nblk + 3) >> 2, tiles = a.inter / kTile;
     // the warp's features of a unit, and its share of the inputs
-    const int part = warp & 1, slice = warp >> 1, s0 = steps * slice / kSlices, s1 = steps * (slice + 1) / kSlices;
+    const int part = warp & 1, slice = warp >> 1, s0 = steps * slice / SLICES, s1 = steps * (slice + 1) / SLICES;
     const int eight = 8 * nblk;
     const int64_t second = (int64_t)a.inter * nblk;
     const int64_t pitch = row_bytes(a.hidden), hpitch = row_bytes(a.inter);
@@ -598,11 +599,10 @@ __global__ void __launch_bounds__(kUpWarps * 32, CTAS) moe_up_kernel(const MoeAr
             }
         }
         __syncthreads();
-        if (warp < n) {  // a warp a token, a lane a feature
-            const int w = warp;
+        for (int w = warp; w < n; w += 2 * SLICES) {  // a warp a token, a lane a feature
             float gate = 0.f, up = 0.f;
 #pragma unroll
-            for (int v = 0; v < kSlices; ++v) {
+            for (int v = 0; v < SLICES; ++v) {
                 gate += red[buf][v][lane][w];
                 up += red[buf][v][32 + lane][w];
             }
@@ -802,13 +802,13 @@ int moe_check(const mnb_moe_layer* l, int64_t M) {
 }
 
 // The up kernel's grid: as many CTAs as run at once, or as there can be units.
-template <int BITS, int NP, int RING, int CTAS>
+template <int BITS, int NP, int SLICES, int RING, int CTAS>
 cudaError_t up_launch(const MoeArgs* a, int sms, cudaStream_t st) {
-    constexpr int smem = kUpWarps * Slot<BITS, NP>::warp_bytes(RING);
-    const auto kernel = moe_up_kernel<BITS, NP, RING, CTAS>;
+    constexpr int smem = SLICES * 2 * Slot<BITS, NP>::warp_bytes(RING);
+    const auto kernel = moe_up_kernel<BITS, NP, SLICES, RING, CTAS>;
     if (!a) return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     const int64_t slots = (int64_t)CTAS * sms, units = (int64_t)a->tokens * a->top_k * (a->inter / kTile);
-    return launch_pdl(kernel, dim3((unsigned)(units < slots ? units : slots)), dim3(kUpWarps * 32), smem, st, *a);
+    return launch_pdl(kernel, dim3((unsigned)(units < slots ? units : slots)), dim3(SLICES * 64), smem, st, *a);
 }
 
 template <int BITS, int NP, int RING, int CTAS>
@@ -828,14 +828,14 @@ cudaError_t moe_kernels(const MoeArgs* a, int item, int sms, cudaStream_t st) {
     constexpr bool Q4 = BITS == 4;
     cudaError_t e;
     if (item == 2) {
-        e = up_launch<BITS, 1, Q4 ? 3 : 2, 2>(a, sms, st);
+        e = up_launch<BITS, 1, 4, Q4 ? 3 : 2, 2>(a, sms, st);
         return e != cudaSuccess ? e : down_launch<BITS, 1, 2, Q4 ? 5 : 3>(a, sms, st);
     }
     if (item == 4) {
-        e = up_launch<BITS, 2, Q4 ? 2 : 3, Q4 ? 2 : 1>(a, sms, st);
+        e = up_launch<BITS, 2, Q4 ? 2 : 4, Q4 ? 2 : 3, Q4 ? 4 : 1>(a, sms, st);
         return e != cudaSuccess ? e : down_launch<BITS, 2, 2, Q4 ? 4 : 3>(a, sms, st);
     }
-    e = up_launch<BITS, 4, Q4 ? 4 : 3, 1>(a, sms, st);
+    e = up_launch<BITS, 4, 2, Q4 ? 2 : 2, Q4 ? 3 : 2>(a, sms, st);
     return e != cudaSuccess ? e : down_launch<BITS, 4, 2, 3>(a, sms, st);
 }
 
