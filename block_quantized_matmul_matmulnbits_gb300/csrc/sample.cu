@@ -34,7 +34,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kMaxVocab = 1 << 24;
 constexpr int kBins = 4096;              // places of the window
-constexpr int kList = 1024;              // logits of the first window whose ids are kept
+constexpr int kEach = 128, kList = kEach * kWarps;  // logits of the first window: a warp's, a CTA's
 constexpr int kMaxWindows = 65536 / kBins + 2;
 constexpr uint32_t kLowest = 0x0400;     // order of -65504, the lowest logit that can be drawn
 constexpr uint32_t kInfinite = 0xFC00;   // order of +infinity; NaN lies above
@@ -103,6 +103,7 @@ __device__ __forceinline__ float ex2f(float x) {
 struct Scale {
     float top, c, c_low;  // c in two words
     int places;
+    uint32_t order;       // top's
 };
 
 // log2 of the weight of a logit, in two words.
@@ -132,13 +133,34 @@ __device__ __forceinline__ Power exp2_of(float2 p) {
     return {__umul64hi(kRoots[(int)j + 32], x), (int)n};
 }
 
+// Ratios 2^(-c j u) of neighbouring logits' weights: 2^62 of them for j places of u, FP16's unit of exponent e.
+struct Ratios {
+    u64 of[32][16];
+};
+
 // (One copy: what the search costs is mostly the way of its instructions into the SM.)
-__device__ __noinline__ u64 weight_of(Scale k, uint32_t order) {
-    const float2 p = power_of(k, value_of(order));
-    if (!(p.x > -70.f)) return 0;
-    const Power w = exp2_of(p);
-    const int shift = 60 - k.places - w.n;
-    return shift > 62 ? 0 : shift > 0 ? (w.m + (1ull << (shift - 1))) >> shift : w.m;
+__device__ __noinline__ u64 ratio_of(Scale k, int e, int j) {
+    const float a = (float)j * __uint_as_float((uint32_t)(max(e, 1) - 25 + 127) << 23), p = __fmul_rn(-a, k.c);
+    if (!(p > -70.f)) return 0;
+    const Power w = exp2_of(make_float2(p, __fmaf_rn(-a, k.c, -p) - a * k.c_low));
+    return w.n < -61 ? 0 : (w.m << 2) >> -w.n;
+}
+
+// A weight as the sums take it.  Sixteen orders that differ in their last four bits lie u apart: the largest of them (or the row's, if
+// that is one of them) times a ratio.
+__device__ __forceinline__ uint32_t block_of(uint32_t order, uint32_t top) { return min(order | 15u, top); }
+__device__ __forceinline__ u64 weight_in(const Power& base, u64 ratio, int places) {
+    const u64 m = __umul64hi(base.m, ratio) << 2;
+    const int shift = 60 - places - base.n;
+    return shift > 62 ? 0 : shift > 0 ? (m + (1ull << (shift - 1))) >> shift : m;
+}
+__device__ __noinline__ Power block_power(Scale k, uint32_t block) {
+    const float2 p = power_of(k, value_of(block));
+    return p.x > -70.f ? exp2_of(p) : Power{0, 0};
+}
+__device__ __forceinline__ u64 weight_of(const Scale& k, const Ratios& r, uint32_t order) {
+    const uint32_t block = block_of(order, k.order);
+    return weight_in(block_power(k, block), r.of[unorder16(order) >> 10 & 31][block - order], k.places);
 }
 
 // Whether a logit's weight is at least m times the largest's.
@@ -214,14 +236,14 @@ __device__ __forceinline__ uint32_t window_low(uint32_t high) {
 
 // ---- shared state ---------------------------------------------------------------
 
-enum { kDone, kFirst, kWindow, kTie, kScan };
-enum { kNoRest, kRest, kExactRest };  // what lies below a window: left out, summed in FP32, or as the search's weights
+enum { kDone, kFirst, kWindow, kRestOf, kTie, kScan };
 
 struct Command {
     uint32_t op;         // kFirst: the first window, its counts and logits gathered in the first CTA; kWindow: another,
-                         // counts in each CTA; kTie, kScan: the drawn logit's tokens
+                         // counts in each CTA; kRestOf: the weight below
+                         // the loaded window to its last place; kTie, kScan: the drawn logit's tokens
     uint32_t high, low;  // the orders from `high` down to `low`
-    uint32_t rest;       // kWindow: what is done with what lies below
+    uint32_t rest;       // kWindow: whether what lies below is summed in FP32
     uint32_t order;      // kTie, kScan: the order looked for
     uint32_t skip;       // kTie: of its tokens the one after so many; kScan: of those in this warp ...
     uint32_t who;        // ... of the cluster
@@ -249,26 +271,28 @@ struct Ending {     // what one end of the bound gives
 
 struct __align__(16) SampleShared {
     uint32_t count[kBins];
-    uint2 list[kList];                  // the first window's logits: order and id
-    uint32_t listed;
+    uint2 list[kWarps][kEach];          // the warps' largest logits: order and id
+    int listed[kWarps];
+    uint2 others[kList];                // first CTA: those of the other CTAs' that are in the window
+    uint32_t others_listed;
     u64 sum_to[kThreads];               // weight and tokens up to each thread's last bin
     int count_to[kThreads];
     u64 warp_sum[kWarps];
     int warp_count[kWarps];
     u64 rest[kMaxCluster];              // first CTA: every CTA's sum below the window (kFirst: of all its logits)
     uint32_t below[kMaxCluster];        // ... and the largest order there
-    uint32_t top[kMaxCluster], reach[kMaxCluster];  // all CTAs: every CTA's largest order, its n-th largest thread
+    uint32_t top[kMaxCluster], reach[kMaxCluster];  // all CTAs: every CTA's largest order, and how far down its list is whole
     uint32_t ties[kMaxCluster * kWarps];
     uint32_t warp_word[kWarps];
     Command cmd, next;
     Scale scale;                        // what the search works with
+    Ratios ratios;
     Window window;
     Found found[4];                     // two ends of a bound: a place, the last kept
     Ending ending[2];
-    int work[2 * kThreads];             // first pieces of groups to look at again
-    int works;
     u64 before_sum;                     // weight and tokens above the window that is loaded
     int before_count;
+    uint32_t under;                     // the largest order below the last window
     int trying;                         // whether the window is a try's
     u64 win_sum[kMaxWindows];           // the search to the end: weight and tokens above each window,
     int win_count[kMaxWindows];         // and its bounds
@@ -327,33 +351,26 @@ __device__ __forceinline__ __half2 max_of(const uint4& q) {
     return __hmax2_nan(__hmax2_nan(as_half2(q.x), as_half2(q.y)), __hmax2_nan(as_half2(q.z), as_half2(q.w)));
 }
 
-// What a thread keeps of the first look: the largest of its groups of pieces and where the two best were, and the sum
-// of 2^(c x - r) about a reference r that moves when a value passes it by kMove.
-constexpr int kGroup = 3;
-constexpr int kHead = -2, kTail = -3, kNone = -1;  // the row's ends as groups
+// What a thread keeps of the first look: its largest logit and the sum of 2^(c x - r) about a reference r that moves when
+// a value passes it by kMove.
+constexpr int kGroup = 3;  // pieces of a group
 constexpr float kMove = 8.f;
 
 struct Look {
-    float best = -INFINITY, second = -INFINITY, third = -INFINITY;
-    int at = kNone, second_at = kNone;
-    float r = -INFINITY;
+    float best = -INFINITY, r = -INFINITY;
     u64 z = 0;
     bool bad = false;  // NaN
 
-    // sum: whether the weights are wanted; low: -infinity has to be told from FP16's lowest value
+    // sum: whether the weights are wanted; returns the group's largest, two logits' places apart
     template <int N>
-    __device__ __forceinline__ void add(const uint4 (&q)[N], int v, bool sum, bool low, float c) {
+    __device__ __forceinline__ __half2 add(const uint4 (&q)[N], bool sum, float c) {
         __half2 m2 = max_of(q[0]);
 #pragma unroll
         for (int i = 1; i < N; ++i) m2 = __hmax2_nan(m2, max_of(q[i]));
         const float x = __half2float(__hmax_nan(__low2half(m2), __high2half(m2)));
         bad |= x != x;
-        third = fmaxf(third, fminf(second, x));
-        second_at = x > best ? at : (x > second ? v : second_at);
-        second = fmaxf(second, fminf(best, x));
-        at = x > best ? v : at;
         best = fmaxf(best, x);
-        if (!sum) return;
+        if (!sum) return m2;
         const float to = x * c;
         if (to > r + kMove) {
             const float2 zz = unpair(z);
@@ -363,14 +380,18 @@ struct Look {
         }
         const float ref = r == -INFINITY ? 0.f : -r;
         const u64 r2 = pair(ref, ref), c2 = pair(c, c);
+        u64 part = 0;
 #pragma unroll
         for (int i = 0; i < N; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const float2 f = __half22float2(as_half2(word_at(q[i], j)));
                 const float2 y = unpair(fma2(pair(f.x, f.y), c2, r2));
-                z = add2(z, pair(ex2f(y.x), ex2f(y.y)));
+                const u64 e = pair(ex2f(y.x), ex2f(y.y));
+                part = i + j ? add2(part, e) : e;
             }
+        z = add2(z, part);
+        return m2;
     }
 };
 
@@ -400,11 +421,6 @@ __device__ __forceinline__ void each_piece(const Slice& s, F f) {
     }
 }
 
-__device__ __forceinline__ uint32_t half_at(const uint4& v, int i) {
-    const uint32_t w = word_at(v, i >> 1);
-    return i & 1 ? w >> 16 : w & 0xFFFFu;
-}
-
 __device__ __forceinline__ uint32_t block_max(SampleShared& sh, uint32_t v) {
     v = __reduce_max_sync(kFull, v);
     if ((threadIdx.x & 31) == 0) sh.warp_word[threadIdx.x >> 5] = v;
@@ -415,7 +431,7 @@ __device__ __forceinline__ uint32_t block_max(SampleShared& sh, uint32_t v) {
 // One look of a CTA for a window: counts of the orders from `high` down to `low` (cleared before) by shared-memory atomics;
 // returns the largest order below, a thread's, and adds the weight there to *weight.  The orders and what is
 // masked for the sum are worked out two logits at a time.
-template <int REST, bool APART>
+template <bool REST, bool APART>
 __device__ __forceinline__ uint32_t count_window(const Slice& s, const Scale& k, uint32_t high, uint32_t low,
                                                  uint32_t counts, u64* weight) {
     const __half low_h = __ushort_as_half((unsigned short)unorder16(low));
@@ -436,7 +452,7 @@ __device__ __forceinline__ uint32_t count_window(const Slice& s, const Scale& k,
             in[i] = __hge2_mask(as_half2(w), low2);
             const uint32_t under = (w & ~in[i]) | (in[i] & 0xFC00FC00u);  // -infinity in place of the window's
             b2 = __hmax2(b2, as_half2(under));
-            if (REST == kRest) {
+            if (REST) {
                 const float2 f = __half22float2(__hmax2(as_half2(under), as_half2(0xFBFFFBFFu)));
                 const u64 x = pair(f.x, f.y);
                 const float2 t = unpair(add2(fma2(x, c2, t2), fma2(x, cl2, tl2)));
@@ -447,15 +463,8 @@ __device__ __forceinline__ uint32_t count_window(const Slice& s, const Scale& k,
                 }
                 part = i ? add2(part, pair(e.x, e.y)) : pair(e.x, e.y);
             }
-            if (REST == kExactRest) {
-#pragma unroll 1
-                for (int j = 0; j < 2; ++j) {
-                    const uint32_t o = order16((under >> (16 * j)) & 0xFFFFu);
-                    if (o >= kLowest) sum += weight_of(k, o);
-                }
-            }
         }
-        if (REST == kRest) {
+        if (REST) {
             const float2 f = unpair(part);
             sum += __float2ull_rn((f.x + f.y) * unit);
         }
@@ -475,6 +484,28 @@ __device__ __forceinline__ uint32_t count_window(const Slice& s, const Scale& k,
     return max(order16(as_word(b2) & 0xFFFFu), order16(as_word(b2) >> 16));
 }
 
+// The weight of the CTA's logits below `low`, a thread's, each to 2^-40 of it.
+__device__ __forceinline__ u64 exact_rest(const Slice& s, const Scale& k, uint32_t low) {
+    const __half low_h = __ushort_as_half((unsigned short)unorder16(low));
+    const __half2 low2 = __halves2half2(low_h, low_h);
+    u64 sum = 0;
+    each_piece(s, [&](const uint4& v, int) {
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t w = word_at(v, i), in = __hge2_mask(as_half2(w), low2);
+            const float2 f = __half22float2(as_half2((w & ~in) | (in & 0xFC00FC00u)));
+            const float2 p0 = power_of(k, f.x), p1 = power_of(k, f.y);  // (-infinity, or NaN, for -infinity)
+            const bool t0 = p0.x > -70.f, t1 = p1.x > -70.f;
+            const Power a = exp2_of(t0 ? p0 : make_float2(0.f, 0.f)), b = exp2_of(t1 ? p1 : make_float2(0.f, 0.f));
+            const int sa = 60 - k.places - a.n, sb = 60 - k.places - b.n;
+            const u64 wa = sa > 62 ? 0 : sa > 0 ? (a.m + (1ull << (sa - 1))) >> sa : a.m;
+            const u64 wb = sb > 62 ? 0 : sb > 0 ? (b.m + (1ull << (sb - 1))) >> sb : b.m;
+            sum += (t0 ? wa : 0) + (t1 ? wb : 0);
+        }
+    });
+    return sum;
+}
+
 // ---- the first CTA's search in the window -----------------------------------------
 
 // Sums up to every thread's bins. The whole CTA.
@@ -485,11 +516,14 @@ __device__ __forceinline__ void window_sums(SampleShared& sh, uint32_t high, uin
     const int lo = min(tid * own, bins), hi = min(lo + own, bins);
     int n = 0;
     u64 w = 0;
+    uint32_t block = 0;
+    Power base = {0, 0};
     for (int i = lo; i < hi; ++i) {
-        const uint32_t c = sh.count[i];
+        const uint32_t c = sh.count[i], order = high - i;
         if (c) {
+            if (block_of(order, k.order) != block) base = block_power(k, block = block_of(order, k.order));
             n += (int)c;
-            w += c * weight_of(k, high - i);
+            w += c * weight_in(base, sh.ratios.of[unorder16(order) >> 10 & 31][block - order], k.places);
         }
     }
 #pragma unroll
@@ -535,7 +569,7 @@ __device__ __noinline__ void find(const SampleShared& sh, int how, int n, u64 s,
     const u64 s0 = thread ? sh.sum_to[thread - 1] : w.above;
     const int bins = (int)(w.high - w.low) + 1, i = thread * w.own + lane;
     const int c = lane < w.own && i < bins ? (int)sh.count[i] : 0;  // own is 16 at most
-    const u64 weight = c ? weight_of(sh.scale, w.high - i) : 0;
+    const u64 weight = c ? weight_of(sh.scale, sh.ratios, w.high - i) : 0;
     int ni = c;
     u64 si = c * weight;
 #pragma unroll 1
@@ -581,7 +615,7 @@ __device__ __noinline__ bool find_min(const SampleShared& sh, float m, Found* ou
     int n = thread ? sh.count_to[thread - 1] : w.before;
     u64 s = thread ? sh.sum_to[thread - 1] : w.above;
     const int c = i < lo && lane < w.own ? (int)sh.count[i] : 0;
-    u64 si = c ? c * weight_of(sh.scale, w.high - i) : 0;
+    u64 si = c ? c * weight_of(sh.scale, sh.ratios, w.high - i) : 0;
     n += (int)__reduce_add_sync(kFull, (unsigned)c);
 #pragma unroll 1
     for (int d = 16; d > 0; d >>= 1) si += __shfl_xor_sync(kFull, si, d);
@@ -657,8 +691,8 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
     };
     if (rank == 0) {
         clear(kBins);
-        if (tid == 0) sh.listed = 0;
     }
+    if (tid == 0) sh.others_listed = 0;
     pdl_wait();
     pdl_launch_dependents();
 
@@ -695,81 +729,101 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
         k.places = a.places;
     }
 
-    // look 1
-    const bool all = wish.k == kAll && !(wish.p < 1.f) && !(wish.m > 0.f);
-    const bool sum = wish.k == kAll && wish.p < 1.f;
+    // look 1: the row's largest logit, its weight where a limit or the draw needs it, and a list of its largest logits.  How
+    // far down the list reaches is taken from the first group of every thread: its r-th largest maximum, r such that the whole
+    // slice will give a few hundred (with a top-k three times as many as it, which is enough but for some).
+    const bool sum = wish.k == kAll && (wish.p < 1.f || !(wish.m > 0.f));
     Look look;
+    uint32_t reach = 0;
     {
         const uint4* pc = reinterpret_cast<const uint4*>(s.row + s.head);
         const float c = fminf(k.c, 1e30f);  // times a logit it stays finite
         constexpr int kStep = kGroup * kThreads;
+        const uint4 none = make_uint4(0xFC00FC00u, 0xFC00FC00u, 0xFC00FC00u, 0xFC00FC00u);  // -infinity
         uint4 q[2][kGroup];  // a group, and the next one on its way
         auto fetch = [&](uint4(&to)[kGroup], int v) {
-            if (v + (kGroup - 1) * kThreads < s.p1) {
 #pragma unroll
-                for (int j = 0; j < kGroup; ++j) to[j] = pc[v + j * kThreads];
+            for (int j = 0; j < kGroup; ++j) {
+                to[j] = none;
+                if (v + j * kThreads < s.p1) to[j] = pc[v + j * kThreads];
             }
         };
-        int v = s.p0 + tid;
+        int v = s.p0 + tid, edge_id = 0;
         fetch(q[0], v);
-        while (v + (kGroup - 1) * kThreads < s.p1) {
-            fetch(q[1], v + kStep);
-            look.add(q[0], v, sum, false, c);
-            v += kStep;
-            if (v + (kGroup - 1) * kThreads >= s.p1) break;
-            fetch(q[0], v + kStep);
-            look.add(q[1], v, sum, false, c);
-            v += kStep;
-        }
-        // fewer than a group are left, and the row's ends
-        uint4 rest[kGroup + 1];
-        int at[kGroup + 1], id;
+        fetch(q[1], v + kStep);
+        uint4 edge[1] = {none};
+        if (s.first && s.head && tid == kThreads - 1) edge[0] = edge_piece(s, 0, &edge_id);
+        if (s.last && s.tail && tid == kThreads - 2) edge[0] = edge_piece(s, 1, &edge_id);
+        if (rank == 0)
+            for (int i = tid; i < 32 * 16; i += kThreads) sh.ratios.of[i >> 4][i & 15] = ratio_of(k, i >> 4, i & 15);
+        look.add(q[0], sum, c);
+        if (tid >= kThreads - 2) look.add(edge, sum, c);
+        {
+            const int mean = greedy ? 8 : wish.k != kAll ? min(3 * wish.k + 64, 4 * kList) : 320;
+            const int mine = min((mean + a.cluster - 1) / a.cluster, kList * 5 / 8);
+            // (the 200th of 256 maxima: 390 logits)
+            const int r = min((mine * kStep + s.p1 - s.p0) / max(s.p1 - s.p0, kStep), 200);
+            const uint32_t best = order16(__half_as_ushort(__float2half_rn(look.best)));
 #pragma unroll
-        for (int j = 0; j < kGroup - 1; ++j) {
-            at[j] = v + j * kThreads < s.p1 ? v + j * kThreads : kNone;
-            if (at[j] != kNone) rest[j] = pc[at[j]];
+            for (int bit = 15; bit >= 0; --bit) {
+                const uint32_t t = reach | 1u << bit;
+                if (__syncthreads_count(best >= t) >= r) reach = t;
+            }
+            reach = min(max(reach, kLowest), kInfinite - 1);
         }
-        at[kGroup - 1] = s.first && s.head && tid == kThreads - 1 ? kHead : kNone;
-        at[kGroup] = s.last && s.tail && tid == kThreads - 2 ? kTail : kNone;
-        if (at[kGroup - 1] != kNone) rest[kGroup - 1] = edge_piece(s, 0, &id);
-        if (at[kGroup] != kNone) rest[kGroup] = edge_piece(s, 1, &id);
+        const __half least = __ushort_as_half((unsigned short)unorder16(reach));
+        const __half2 least2 = __halves2half2(least, least);
+        // a piece's logits that reach `least`, by the whole warp
+        int listed = 0;
+        auto list = [&](const uint4& x, int id) {
 #pragma unroll 1
-        for (int j = 0; j <= kGroup; ++j) {
-            uint4 one[1] = {rest[0]};
-            int from = at[0];
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t w = j < 2 ? (j ? x.y : x.x) : (j == 2 ? x.z : x.w), in = __hge2_mask(as_half2(w), least2);
 #pragma unroll
-            for (int i = 1; i <= kGroup; ++i)
-                if (j == i) one[0] = rest[i], from = at[i];
-            if (from != kNone) look.add(one, from, sum, false, c);
+                for (int h = 0; h < 2; ++h) {
+                    const bool mine = in >> (16 * h) & 1;
+                    const unsigned all = __ballot_sync(kFull, mine);
+                    const int at = listed + __popc(all & ((1u << lane) - 1u));
+                    if (mine && at < kEach) sh.list[warp][at] = make_uint2(order16(w >> (16 * h) & 0xFFFFu), (uint32_t)(id + 2 * j + h));
+                    listed += __popc(all);
+                }
+            }
+        };
+        auto list_group = [&](const uint4(&x)[kGroup], int v, __half2 m2) {
+            if (!__any_sync(kFull, __hge2_mask(m2, least2) != 0)) return;
+#pragma unroll 1
+            for (int j = 0; j < kGroup; ++j) {
+                const uint4 y = j == 0 ? x[0] : j == 1 ? x[1] : x[2];
+                if (__any_sync(kFull, __hge2_mask(max_of(y), least2) != 0)) list(y, s.head + (v + j * kThreads) * 8);
+            }
+        };
+        list_group(q[0], v, as_half2(0x7C007C00u));
+        if (warp == kWarps - 1) list(edge[0], edge_id);
+        for (int w = v - lane + kStep; w < s.p1; w += kStep) {  // a warp together
+            v += kStep;
+            fetch(q[0], v + kStep);
+            list_group(q[1], v, look.add(q[1], sum, c));
+            w += kStep;
+            if (w >= s.p1) break;
+            v += kStep;
+            fetch(q[1], v + kStep);
+            list_group(q[0], v, look.add(q[0], sum, c));
         }
+        if (lane == 0) sh.listed[warp] = listed;
     }
-    const uint32_t mine = look.bad ? 0xFFFFu : order16(__half_as_ushort(__float2half_rn(look.best)));
-    const uint32_t cta_top = block_max(sh, mine);
-    // The window's reach: with a top-k the k-th largest of the threads' maxima (k logits reach it at least), else the
-    // 128th, which holds the likely tokens of a trained model's row; without any limit, and for more than there are
-    // threads, all of the histogram.
-    const int want = ((wish.k != kAll ? min(wish.k, kThreads * a.cluster + 1) : 128) + a.cluster - 1) / a.cluster;
-    uint32_t reach = 0;
-    if (greedy) {
-        reach = cta_top;
-    } else if (!all && want <= kThreads) {
-#pragma unroll
-        for (int bit = 15; bit >= 0; --bit) {
-            const uint32_t t = reach | 1u << bit;
-            if (__syncthreads_count(mine >= t) >= want) reach = t;
-        }
-    }
+    const uint32_t cta_top = block_max(sh, look.bad ? 0xFFFFu : order16(__half_as_ushort(__float2half_rn(look.best))));
+    // (the barrier of the maximum lies behind the lists' last entries)
+    if (__reduce_max_sync(kFull, sh.listed[lane & (kWarps - 1)]) > kEach) reach = 0xFFFFu;
     if (tid < a.cluster) {
         st_cluster(in_cta(smem_u32(&sh.top[rank]), tid), cta_top);
         st_cluster(in_cta(smem_u32(&sh.reach[rank]), tid), reach);
     }
     cluster_sync();
-    uint32_t top = 0, low = 0xFFFFu;
+    uint32_t top = 0, low = 0;
     for (int i = 0; i < a.cluster; ++i) {
         top = max(top, sh.top[i]);
-        low = min(low, sh.reach[i]);
+        low = max(low, sh.reach[i]);
     }
-    if (greedy) low = top;
     if (top >= kInfinite || top < kLowest) {  // NaN or +infinity; nothing that can be drawn
         if (rank == 0 && tid == 0) {
             a.token[row] = -1;
@@ -778,12 +832,12 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
         return;
     }
     k.top = value_of(top);
-    Command cmd = {kFirst, top, max(low, window_low(top)), kNoRest, 0, 0, 0};
-    const uint32_t rest_of = wish.k == kAll ? kRest : kNoRest;
-    // many logits are counted in each CTA and gathered then, few where they are wanted
-    if (cmd.low == window_low(top) && !greedy) cmd.op = kWindow, cmd.rest = rest_of;
+    k.order = top;
+    low = max(low, window_low(top));
+    Command cmd = {kFirst, top, low, 0, 0, 0, 0};
+    if (low > top) cmd = {kWindow, top, window_low(top), wish.k == kAll, 0, 0, 0};  // a list is not whole
 
-    if (tid == 0) sh.before_count = 0, sh.before_sum = 0, sh.works = 0, sh.trying = 1, sh.scale = k;
+    if (tid == 0) sh.before_count = 0, sh.before_sum = 0, sh.trying = 1, sh.scale = k;
     __syncthreads();
 
     // first CTA, first warp: where the search is
@@ -811,57 +865,24 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
 
     for (;;) {
         if (cmd.op == kFirst) {
-            // The groups that hold logits of the window, a piece a thread; all of a thread's pieces where a third of its
-            // groups does.
-            const uint32_t counts = in_cta(smem_u32(sh.count), 0), list = in_cta(smem_u32(sh.list), 0),
-                           listed = in_cta(smem_u32(&sh.listed), 0);
-            const uint4* pc = reinterpret_cast<const uint4*>(s.row + s.head);
-            auto take = [&](const uint4& v, int id) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const uint32_t o = order16(half_at(v, i));
-                    if (o >= cmd.low) {
-                        add_cluster(counts + (cmd.high - o) * 4, 1u);
-                        const uint32_t at = next_cluster(listed);
-                        if (at < kList) st_cluster(list + at * 8, (u64)(uint32_t)(id + i) << 32 | o);
-                    }
-                }
-            };
-            const float least = value_of(cmd.low);
-            const bool reaches = look.best >= least, two = look.second >= least, three = look.third >= least;
-            if (reaches && !three) {
-                const int i = atomicAdd(&sh.works, two ? 2 : 1);
-                sh.work[i] = look.at;
-                if (two) sh.work[i + 1] = look.second_at;
-            }
-            __syncthreads();
-            for (int i = tid; i < sh.works * kGroup; i += kThreads) {
-                const int from = sh.work[i / kGroup], j = i % kGroup;
-                int id;
-                if (from < 0) {
-                    if (j) continue;
-                    const uint4 v = edge_piece(s, from == kTail, &id);
-                    take(v, id);
-                } else if (j == 0 || from + (kGroup - 1) * kThreads < s.p1) {  // an entry is a group, or one of the last pieces
-                    take(pc[from + j * kThreads], s.head + (from + j * kThreads) * 8);
-                }
-            }
-            for (unsigned left = __ballot_sync(kFull, three); left; left &= left - 1) {  // by its warp
-                const int from = warp * 32 + __ffs(left) - 1;
-                for (int v = s.p0 + from + lane * kThreads; v < s.p1; v += 32 * kThreads) take(pc[v], s.head + v * 8);
-                int id;
-                if (lane == 0 && from == kThreads - 1 && s.first && s.head) {
-                    const uint4 v = edge_piece(s, 0, &id);
-                    take(v, id);
-                }
-                if (lane == 0 && from == kThreads - 2 && s.last && s.tail) {
-                    const uint4 v = edge_piece(s, 1, &id);
-                    take(v, id);
+            // the lists' logits that are in the window: their counts, and the first CTA's list of them
+            const uint32_t counts = in_cta(smem_u32(sh.count), 0), list = in_cta(smem_u32(sh.others), 0),
+                           listed = in_cta(smem_u32(&sh.others_listed), 0);
+            for (int i = lane; i < sh.listed[warp]; i += 32) {
+                const uint2 x = sh.list[warp][i];
+                if (x.x < cmd.low) continue;
+                add_cluster(counts + (cmd.high - x.x) * 4, 1u);
+                if (rank) {
+                    const uint32_t at = next_cluster(listed);
+                    if (at < kList) st_cluster(list + at * 8, (u64)x.y << 32 | x.x);
                 }
             }
             if (sum) {
+                // r and c top are rounded alike; what top's product leaves over is taken off
                 const float2 z = unpair(look.z);
-                const float f = (z.x + z.y) * ex2f(fmaxf(look.r - k.top * fminf(k.c, 1e30f), -1000.f));
+                const float c = fminf(k.c, 1e30f), tc = __fmul_rn(k.top, c);
+                const float tl = k.c < 1e30f ? __fmaf_rn(k.top, c, -tc) : 0.f;
+                const float f = (z.x + z.y) * ex2f(fmaxf(look.r - tc, -1000.f) - tl);
                 send_rest(__float2ull_rn(f * __uint_as_float((uint32_t)(k.places + 127) << 23)), kLowest);
             }
         } else if (cmd.op == kWindow) {
@@ -871,14 +892,14 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
             uint32_t under;
             // -infinity stands for FP16's lowest value where that has no weight; else it is told apart
             const bool apart = (-65504.f - k.top) * k.c > -200.f;
-            if (cmd.rest == kRest)
-                under = apart ? count_window<kRest, true>(s, k, cmd.high, cmd.low, smem_u32(sh.count), &exact)
-                              : count_window<kRest, false>(s, k, cmd.high, cmd.low, smem_u32(sh.count), &exact);
-            else if (cmd.rest == kExactRest)
-                under = count_window<kExactRest, false>(s, k, cmd.high, cmd.low, smem_u32(sh.count), &exact);
+            if (cmd.rest)
+                under = apart ? count_window<true, true>(s, k, cmd.high, cmd.low, smem_u32(sh.count), &exact)
+                              : count_window<true, false>(s, k, cmd.high, cmd.low, smem_u32(sh.count), &exact);
             else
-                under = count_window<kNoRest, false>(s, k, cmd.high, cmd.low, smem_u32(sh.count), &exact);
+                under = count_window<false, false>(s, k, cmd.high, cmd.low, smem_u32(sh.count), &exact);
             send_rest(exact, under);
+        } else if (cmd.op == kRestOf) {
+            send_rest(exact_rest(s, k, cmd.low), kLowest);
         } else {  // tokens of one logit, warp by warp in the order of their ids
             const int n = s.p1 - s.p0, w0 = s.p0 + (int)((int64_t)n * warp / kWarps),
                       w1 = s.p0 + (int)((int64_t)n * (warp + 1) / kWarps);
@@ -968,12 +989,14 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
                 }
                 uint32_t below = 0;
                 u64 rest = 0;
-                if (cmd.op == kWindow || sum)
+                if (cmd.op != kFirst || sum)
                     for (int i = 0; i < a.cluster; ++i) {
                         below = max(below, sh.below[i]);
                         rest += sh.rest[i];
                     }
-                window_sums(sh, cmd.high, cmd.low, sh.before_count, sh.before_sum);
+                if (cmd.op != kRestOf) window_sums(sh, cmd.high, cmd.low, sh.before_count, sh.before_sum);
+                if (cmd.op == kWindow && tid == 0) sh.under = below;
+                if (cmd.op == kRestOf) below = sh.under;
                 const Window& w = sh.window;
                 // the first tries: the two ends of the bound, a warp each
                 bool more = below >= kLowest;
@@ -983,17 +1006,18 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
                     // The error of a weight below the window, in steps of 2^-24: of a piece's sum, 3; of the power, 4; of
                     // its exponent t, two roundings of half a step of |t| ln 2: 17 for |t| up to 24, and for
                     // smaller weights (2^-24 at most, vocab of them) up to 42, all those under 2^-60 together being
-                    // under 2^-36 of the largest's; and a place for each piece.  In the first look a thread's sums
-                    // of its pieces come in place of one piece's, and the exponent's roundings are those of c logit
-                    // and c top, |c top| + 60 at most.
+                    // under 2^-36 of the largest's; and a place for each piece.  In the first look, of all of the row's
+                    // weight: a group's sum, 12, and its thread's of them; the power's 4 and its reference's
+                    // 4; of the exponent its rounding, 68 ln 2 / 2, and the low word of c, which the difference from the
+                    // largest is not multiplied with, 60 ln 2 / 2.
                     u64 error = 0;
                     const u64 spare = ((u64)a.vocab << k.places >> 42) + ((u64)a.vocab >> (60 - k.places)) +
                                       (u64)s.pieces + kThreads * kMaxCluster + 64;
                     if (cmd.op == kFirst) {
-                        const u64 units = (u64)((s.p1 - s.p0) / kThreads + 3.f * fminf(fabsf(k.top) * k.c, 1e9f)) + 400;
+                        const u64 units = (u64)((s.p1 - s.p0) / (kGroup * kThreads)) + 80;
                         error = sum ? (rest >> 24) * units + units + spare : 1ull << 61;  // (not known)
                         rest = !sum ? error : rest > w.sum ? rest - w.sum : 0;
-                    } else if (cmd.rest == kRest) {
+                    } else if (cmd.op == kWindow && cmd.rest) {
                         error = (rest >> 24) * 24 + spare;
                     }
                     if (!more) rest = error = 0;
@@ -1005,7 +1029,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
                         const Ending x = sh.ending[0], y = sh.ending[1];
                         // the same kept tokens, the same place, and a probability that is certain enough
                         const u64 apart = x.total > y.total ? x.total - y.total : y.total - x.total;
-                        sh.ending[0].ok = x.ok && y.ok && x.kept == y.kept && x.at.n == y.at.n && apart <= x.total >> 14;
+                        sh.ending[0].ok = x.ok && y.ok && x.kept == y.kept && x.at.n == y.at.n && apart <= x.total >> 15;
                         sh.ending[0].total = min(x.total, y.total) + apart / 2;
                     }
                     __syncwarp();
@@ -1022,12 +1046,12 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
                         if (!done) {
                             // all of the histogram, then what lies below it exactly
                             if (cmd.op == kFirst)
-                                next = {kWindow, top, window_low(top), rest_of, 0, 0, 0};
-                            else if (cmd.rest == kRest && more)
-                                next = {kWindow, top, window_low(top), kExactRest, 0, 0, 0};
+                                next = {kWindow, top, window_low(top), wish.k == kAll, 0, 0, 0};
+                            else if (cmd.op == kWindow && cmd.rest && more)
+                                next = {kRestOf, top, cmd.low, 0, 0, 0, 0};
                             else
                                 stage = kCollect;
-                            if (cmd.rest == kExactRest || !more) whole = w.sum + rest;
+                            if (cmd.op == kRestOf || !more) whole = w.sum + rest;
                         }
                     }
                     if (stage >= kCollect) {
@@ -1116,15 +1140,29 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
                             a.logprob[row] = fminf((float)((((double)t.x + (double)t.y) - log2_of(total, k.places)) *
                                                            0.69314718055994530942), 0.f);
                         }
-                        if (cmd.op == kFirst && sh.listed <= kList) {
-                            // the id that so many of the same logit lie before
-                            const int n = (int)sh.listed;
-                            for (int i = lane; i < n; i += 32) {
-                                if (sh.list[i].x != at.order) continue;
+                        if (at.order >= low && sh.others_listed <= (uint32_t)kList) {
+                            // of the listed ids of the drawn logit the one that so many lie before
+                            int n = 0;
+                            uint32_t id = 0;  // this lane's share of them: at most one, or the search below
+                            bool many = false;
+                            auto look_at = [&](const uint2& x) {
+                                if (x.x != at.order) return;
+                                many |= n > 0;
+                                id = x.y;
+                                ++n;
+                            };
+                            for (int v = 0; v < kWarps; ++v)
+                                for (int i = lane; i < sh.listed[v]; i += 32) look_at(sh.list[v][i]);
+                            for (int i = lane; i < (int)sh.others_listed; i += 32) look_at(sh.others[i]);
+                            if (!__any_sync(kFull, many)) {
                                 int before = 0;
-                                for (int j = 0; j < n; ++j)
-                                    before += sh.list[j].x == at.order && sh.list[j].y < sh.list[i].y;
-                                if (before == at.tie) a.token[row] = (int64_t)sh.list[i].y;
+                                for (int l = 0; l < 32; ++l) {
+                                    const uint32_t other = __shfl_sync(kFull, id, l);
+                                    before += __shfl_sync(kFull, n, l) && other < id;
+                                }
+                                if (n && before == at.tie) a.token[row] = (int64_t)id;
+                            } else {
+                                next = {kTie, 0, 0, 0, at.order, (uint32_t)at.tie, 0};
                             }
                         } else {
                             next = {kTie, 0, 0, 0, at.order, (uint32_t)at.tie, 0};
