@@ -272,7 +272,7 @@ struct Ending {     // what one end of the bound gives
 struct __align__(16) SampleShared {
     uint32_t count[kBins];
     uint2 list[kWarps][kEach];          // the warps' largest logits: order and id
-    int listed[kWarps];
+    int listed[kWarps], hits[kWarps][kEach];  // ... and the first pieces of the groups that hold some
     uint2 others[kList];                // first CTA: those of the other CTAs' that are in the window
     uint32_t others_listed;
     u64 sum_to[kThreads];               // weight and tokens up to each thread's last bin
@@ -491,16 +491,22 @@ __device__ __forceinline__ u64 exact_rest(const Slice& s, const Scale& k, uint32
     u64 sum = 0;
     each_piece(s, [&](const uint4& v, int) {
 #pragma unroll 1
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t w = word_at(v, i), in = __hge2_mask(as_half2(w), low2);
-            const float2 f = __half22float2(as_half2((w & ~in) | (in & 0xFC00FC00u)));
-            const float2 p0 = power_of(k, f.x), p1 = power_of(k, f.y);  // (-infinity, or NaN, for -infinity)
-            const bool t0 = p0.x > -70.f, t1 = p1.x > -70.f;
-            const Power a = exp2_of(t0 ? p0 : make_float2(0.f, 0.f)), b = exp2_of(t1 ? p1 : make_float2(0.f, 0.f));
-            const int sa = 60 - k.places - a.n, sb = 60 - k.places - b.n;
-            const u64 wa = sa > 62 ? 0 : sa > 0 ? (a.m + (1ull << (sa - 1))) >> sa : a.m;
-            const u64 wb = sb > 62 ? 0 : sb > 0 ? (b.m + (1ull << (sb - 1))) >> sb : b.m;
-            sum += (t0 ? wa : 0) + (t1 ? wb : 0);
+        for (int i = 0; i < 2; ++i) {
+            float x[4];
+            const uint32_t w0 = i ? v.z : v.x, w1 = i ? v.w : v.y;
+            const uint32_t in0 = __hge2_mask(as_half2(w0), low2), in1 = __hge2_mask(as_half2(w1), low2);
+            const float2 f0 = __half22float2(as_half2((w0 & ~in0) | (in0 & 0xFC00FC00u)));
+            const float2 f1 = __half22float2(as_half2((w1 & ~in1) | (in1 & 0xFC00FC00u)));
+            x[0] = f0.x, x[1] = f0.y, x[2] = f1.x, x[3] = f1.y;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {  // (side by side: the power's steps wait for one another)
+                const float2 p = power_of(k, x[j]);  // -infinity, or NaN, for -infinity
+                const bool there = p.x > -70.f;
+                const Power a = exp2_of(there ? p : make_float2(0.f, 0.f));
+                const int shift = 60 - k.places - a.n;
+                const u64 weight = shift > 62 ? 0 : shift > 0 ? (a.m + (1ull << (shift - 1))) >> shift : a.m;
+                sum += there ? weight : 0;
+            }
         }
     });
     return sum;
@@ -756,7 +762,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
         if (s.last && s.tail && tid == kThreads - 2) edge[0] = edge_piece(s, 1, &edge_id);
         if (rank == 0)
             for (int i = tid; i < 32 * 16; i += kThreads) sh.ratios.of[i >> 4][i & 15] = ratio_of(k, i >> 4, i & 15);
-        look.add(q[0], sum, c);
+        const __half2 first2 = look.add(q[0], sum, c);
         if (tid >= kThreads - 2) look.add(edge, sum, c);
         {
             const int mean = greedy ? 8 : wish.k != kAll ? min(3 * wish.k + 64, 4 * kList) : 320;
@@ -773,12 +779,33 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
         }
         const __half least = __ushort_as_half((unsigned short)unorder16(reach));
         const __half2 least2 = __halves2half2(least, least);
-        // a piece's logits that reach `least`, by the whole warp
-        int listed = 0;
+        // A group that holds logits which reach `least` is noted, and looked at again at the end: one in hundreds does.
+        int hits = 0, listed = 0;
+        auto note = [&](int v, __half2 m2) {
+            const bool hit = __hge2_mask(m2, least2) != 0;
+            const unsigned all = __ballot_sync(kFull, hit);
+            if (!all) return;
+            const int at = hits + __popc(all & ((1u << lane) - 1u));
+            if (hit && at < kEach) sh.hits[warp][at] = v;
+            hits += __popc(all);
+        };
+        note(v, first2);
+        for (int w = v - lane + kStep; w < s.p1; w += kStep) {  // a warp together
+            v += kStep;
+            fetch(q[0], v + kStep);
+            note(v, look.add(q[1], sum, c));
+            w += kStep;
+            if (w >= s.p1) break;
+            v += kStep;
+            fetch(q[1], v + kStep);
+            note(v, look.add(q[0], sum, c));
+        }
+        // a piece's logits that reach it, by the whole warp
         auto list = [&](const uint4& x, int id) {
-#pragma unroll 1
+            if (!__any_sync(kFull, __hge2_mask(max_of(x), least2) != 0)) return;
+#pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const uint32_t w = j < 2 ? (j ? x.y : x.x) : (j == 2 ? x.z : x.w), in = __hge2_mask(as_half2(w), least2);
+                const uint32_t w = word_at(x, j), in = __hge2_mask(as_half2(w), least2);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const bool mine = in >> (16 * h) & 1;
@@ -789,26 +816,26 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
                 }
             }
         };
-        auto list_group = [&](const uint4(&x)[kGroup], int v, __half2 m2) {
-            if (!__any_sync(kFull, __hge2_mask(m2, least2) != 0)) return;
-#pragma unroll 1
-            for (int j = 0; j < kGroup; ++j) {
-                const uint4 y = j == 0 ? x[0] : j == 1 ? x[1] : x[2];
-                if (__any_sync(kFull, __hge2_mask(max_of(y), least2) != 0)) list(y, s.head + (v + j * kThreads) * 8);
+        __syncwarp();
+        const int pieces = hits <= kEach ? hits * kGroup : 0;
+        if (hits > kEach) listed = kEach + 1;  // (it is not whole)
+        for (int i0 = 0; i0 < pieces; i0 += 64) {
+            uint4 x[2];
+            int at[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int i = i0 + u * 32 + lane;
+                x[u] = none;
+                at[u] = 0;
+                if (i < pieces) {
+                    at[u] = sh.hits[warp][i / kGroup] + i % kGroup * kThreads;
+                    if (at[u] < s.p1) x[u] = pc[at[u]];
+                }
             }
-        };
-        list_group(q[0], v, as_half2(0x7C007C00u));
-        if (warp == kWarps - 1) list(edge[0], edge_id);
-        for (int w = v - lane + kStep; w < s.p1; w += kStep) {  // a warp together
-            v += kStep;
-            fetch(q[0], v + kStep);
-            list_group(q[1], v, look.add(q[1], sum, c));
-            w += kStep;
-            if (w >= s.p1) break;
-            v += kStep;
-            fetch(q[1], v + kStep);
-            list_group(q[0], v, look.add(q[0], sum, c));
+#pragma unroll 1
+            for (int u = 0; u < 2; ++u) list(u ? x[1] : x[0], s.head + (u ? at[1] : at[0]) * 8);
         }
+        if (warp == kWarps - 1) list(edge[0], edge_id);
         if (lane == 0) sh.listed[warp] = listed;
     }
     const uint32_t cta_top = block_max(sh, look.bad ? 0xFFFFu : order16(__half_as_ushort(__float2half_rn(look.best))));
@@ -861,6 +888,12 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
             st_cluster(in_cta(smem_u32(&sh.rest[rank]), 0), exact);
             st_cluster(in_cta(smem_u32(&sh.below[rank]), 0), below);
         }
+    };
+
+    auto write_logprob = [&](uint32_t order, u64 total) {
+        if (!a.logprob) return;
+        const float2 t = power_of(k, value_of(order));
+        a.logprob[row] = fminf((float)((((double)t.x + (double)t.y) - log2_of(total, k.places)) * 0.69314718055994530942), 0.f);
     };
 
     for (;;) {
@@ -1032,7 +1065,8 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
                         sh.ending[0].ok = x.ok && y.ok && x.kept == y.kept && x.at.n == y.at.n && apart <= x.total >> 15;
                         sh.ending[0].total = min(x.total, y.total) + apart / 2;
                     }
-                    __syncwarp();
+                    __syncthreads();
+                    if (tid == 32 && sh.ending[0].ok) write_logprob(sh.ending[0].at.order, sh.ending[0].total);
                 }
                 if (warp == 0) {  // the search is one warp's
                     Found at = {};
@@ -1135,11 +1169,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
                         }
                     }
                     if (done) {
-                        if (lane == 0 && a.logprob) {
-                            const float2 t = power_of(k, value_of(at.order));
-                            a.logprob[row] = fminf((float)((((double)t.x + (double)t.y) - log2_of(total, k.places)) *
-                                                           0.69314718055994530942), 0.f);
-                        }
+                        if (stage != kTry && lane == 0) write_logprob(at.order, total);
                         if (at.order >= low && sh.others_listed <= (uint32_t)kList) {
                             // of the listed ids of the drawn logit the one that so many lie before
                             int n = 0;
