@@ -55,7 +55,7 @@ struct SampleArgs {
     float* logprob;
 };
 
-// 2^(j / 64) 2^62, j = -32 .. 32
+// 2^(j / 64) 2^62, j = -32 .. 32; read from shared memory, since constant memory gives one address at a time
 __constant__ u64 kRoots[65] = {
     0x2d413cccfe779921ull, 0x2dbf6478ca345de4ull, 0x2e3eebd1d8bee7baull, 0x2ebfd6ac84cf917full,
     0x2f4228e7d6030db0ull, 0x2fc5e66d9e9cc421ull, 0x304b1332999c2516ull, 0x30d1b3368925d902ull,
@@ -104,6 +104,7 @@ struct Scale {
     float top, c, c_low;  // c in two words
     int places;
     uint32_t order;       // top's
+    const u64* roots;     // kRoots in shared memory
 };
 
 // log2 of the weight of a logit, in two words.
@@ -121,7 +122,7 @@ struct Power {
     u64 m;
     int n;
 };
-__device__ __forceinline__ Power exp2_of(float2 p) {
+__device__ __forceinline__ Power exp2_of(const u64* roots, float2 p) {
     const float n = rintf(p.x), f = p.x - n;  // exact
     const float j = rintf(f * 64.f), g = __fmaf_rn(j, -0.015625f, f);  // exact
     const float h = __fmul_rn(g, 0.6931471824645996f);
@@ -130,7 +131,7 @@ __device__ __forceinline__ Power exp2_of(float2 p) {
     const float z = h + l;
     const float q = z * z * (0.5f + z * (0.16666667f + z * (0.041666668f + z * 0.008333334f)));
     const u64 x = (1ull << 62) + (u64)(__float2ll_rn(h * 0x1p62f) + __float2ll_rn((l + q) * 0x1p62f));
-    return {__umul64hi(kRoots[(int)j + 32], x), (int)n};
+    return {__umul64hi(roots[(int)j + 32], x), (int)n};
 }
 
 // Ratios 2^(-c j u) of neighbouring logits' weights: 2^62 of them for j places of u, FP16's unit of exponent e.
@@ -142,7 +143,7 @@ struct Ratios {
 __device__ __noinline__ u64 ratio_of(Scale k, int e, int j) {
     const float a = (float)j * __uint_as_float((uint32_t)(max(e, 1) - 25 + 127) << 23), p = __fmul_rn(-a, k.c);
     if (!(p > -70.f)) return 0;
-    const Power w = exp2_of(make_float2(p, __fmaf_rn(-a, k.c, -p) - a * k.c_low));
+    const Power w = exp2_of(k.roots, make_float2(p, __fmaf_rn(-a, k.c, -p) - a * k.c_low));
     return w.n < -61 ? 0 : (w.m << 2) >> -w.n;
 }
 
@@ -156,7 +157,7 @@ __device__ __forceinline__ u64 weight_in(const Power& base, u64 ratio, int place
 }
 __device__ __noinline__ Power block_power(Scale k, uint32_t block) {
     const float2 p = power_of(k, value_of(block));
-    return p.x > -70.f ? exp2_of(p) : Power{0, 0};
+    return p.x > -70.f ? exp2_of(k.roots, p) : Power{0, 0};
 }
 __device__ __forceinline__ u64 weight_of(const Scale& k, const Ratios& r, uint32_t order) {
     const uint32_t block = block_of(order, k.order);
@@ -167,16 +168,16 @@ __device__ __forceinline__ u64 weight_of(const Scale& k, const Ratios& r, uint32
 __device__ __noinline__ bool at_least(Scale k, uint32_t order, float m) {
     const float2 p = power_of(k, value_of(order));
     if (!(p.x > -200.f)) return false;
-    const Power w = exp2_of(p);
+    const Power w = exp2_of(k.roots, p);
     return (double)w.m * __longlong_as_double((long long)(w.n - 60 + 1023) << 52) >= (double)m;
 }
 
 // log2 of s 2^-places, to FP32's places and more: log2f, and one step of Newton's method about it.
-__device__ __forceinline__ double log2_of(u64 s, int places) {
+__device__ __forceinline__ double log2_of(const u64* roots, u64 s, int places) {
     const int lead = 63 - __clzll((long long)s);
     const u64 m = lead >= 60 ? s >> (lead - 60) : s << (60 - lead);  // in [2^60, 2^61)
     const float y = log2f((float)m * 0x1p-60f);
-    const Power w = exp2_of(make_float2(y, 0.f));
+    const Power w = exp2_of(roots, make_float2(y, 0.f));
     const long long d = (long long)(m - (w.n > 0 ? w.m << 1 : w.m));
     return (double)(lead - places) + (double)y + (double)((float)d / (float)m * 1.44269504f);
 }
@@ -287,6 +288,7 @@ struct __align__(16) SampleShared {
     Command cmd, next;
     Scale scale;                        // what the search works with
     Ratios ratios;
+    u64 roots[65];
     Window window;
     Found found[4];                     // two ends of a bound: a place, the last kept
     Ending ending[2];
@@ -502,7 +504,7 @@ __device__ __forceinline__ u64 exact_rest(const Slice& s, const Scale& k, uint32
             for (int j = 0; j < 4; ++j) {  // (side by side: the power's steps wait for one another)
                 const float2 p = power_of(k, x[j]);  // -infinity, or NaN, for -infinity
                 const bool there = p.x > -70.f;
-                const Power a = exp2_of(there ? p : make_float2(0.f, 0.f));
+                const Power a = exp2_of(k.roots, there ? p : make_float2(0.f, 0.f));
                 const int shift = 60 - k.places - a.n;
                 const u64 weight = shift > 62 ? 0 : shift > 0 ? (a.m + (1ull << (shift - 1))) >> shift : a.m;
                 sum += there ? weight : 0;
@@ -699,6 +701,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
         clear(kBins);
     }
     if (tid == 0) sh.others_listed = 0;
+    if (tid < 65) sh.roots[tid] = kRoots[tid];
     pdl_wait();
     pdl_launch_dependents();
 
@@ -733,6 +736,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
         k.c = __fdiv_rn(1.44269502162933349609f, t);
         k.c_low = __fdiv_rn(__fmaf_rn(-k.c, t, 1.44269502162933349609f) + 1.9259629911266174681e-8f, t);
         k.places = a.places;
+        k.roots = sh.roots;
     }
 
     // look 1: the row's largest logit, its weight where a limit or the draw needs it, and a list of its largest logits.  How
@@ -758,6 +762,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
         fetch(q[0], v);
         fetch(q[1], v + kStep);
         uint4 edge[1] = {none};
+        __syncthreads();  // the roots
         if (s.first && s.head && tid == kThreads - 1) edge[0] = edge_piece(s, 0, &edge_id);
         if (s.last && s.tail && tid == kThreads - 2) edge[0] = edge_piece(s, 1, &edge_id);
         if (rank == 0)
@@ -893,7 +898,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
     auto write_logprob = [&](uint32_t order, u64 total) {
         if (!a.logprob) return;
         const float2 t = power_of(k, value_of(order));
-        a.logprob[row] = fminf((float)((((double)t.x + (double)t.y) - log2_of(total, k.places)) * 0.69314718055994530942), 0.f);
+        a.logprob[row] = fminf((float)((((double)t.x + (double)t.y) - log2_of(k.roots, total, k.places)) * 0.69314718055994530942), 0.f);
     };
 
     for (;;) {
@@ -1227,9 +1232,12 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-// CTAs of a row: enough for two on every SM (four fit), of at least 4096 logits each.
+// CTAs of a row: enough for two on every SM (four fit), of at least 4096 logits each; two at least for a long row, which
+// has to be gone through three times or more where its limits lie far down, and is what the call then ends with (512 rows of
+// 151,936 with top-p 0.7 to 0.98 and temperatures 0.6 to 1.2: 191 us with two, 285 with one; with none but likely
+// tokens kept 70 and 56).
 int cluster_for(int64_t rows, int64_t vocab, int sms) {
-    int c = 1;
+    int c = vocab > 1 << 17 ? 2 : 1;
     while (c < kMaxCluster && rows * c < (int64_t)sms * 2 && vocab >= (int64_t)c * 2 * 4096) c *= 2;
     return c;
 }
