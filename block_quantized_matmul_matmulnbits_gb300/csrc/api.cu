@@ -85,7 +85,7 @@ int device_setup(int* sm_count, unsigned int** status = nullptr) {
         if (mnb::gemv_prepare() != cudaSuccess || mnb::gemm_prepare() != cudaSuccess ||
             mnb::lora_down_prepare() != cudaSuccess || mnb::decode_prepare() != cudaSuccess ||
             mnb::decode_mt_prepare() != cudaSuccess || mnb::attn_prepare() != cudaSuccess ||
-            mnb::moe_prepare() != cudaSuccess ||
+            mnb::moe_prepare() != cudaSuccess || mnb::sample_prepare() != cudaSuccess ||
             cudaGetSymbolAddress(&st, mnb::g_status) != cudaSuccess) {
             cudaGetLastError();
             return MNB_ERR_CUDA;

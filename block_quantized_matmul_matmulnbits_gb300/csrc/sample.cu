@@ -155,13 +155,10 @@ __device__ __forceinline__ u64 weight_in(const Power& base, u64 ratio, int place
     const int shift = 60 - places - base.n;
     return shift > 62 ? 0 : shift > 0 ? (m + (1ull << (shift - 1))) >> shift : m;
 }
-__device__ __noinline__ Power block_power(Scale k, uint32_t block) {
+__device__ __forceinline__ Power block_power(const Scale& k, uint32_t block) {
     const float2 p = power_of(k, value_of(block));
-    return p.x > -70.f ? exp2_of(k.roots, p) : Power{0, 0};
-}
-__device__ __forceinline__ u64 weight_of(const Scale& k, const Ratios& r, uint32_t order) {
-    const uint32_t block = block_of(order, k.order);
-    return weight_in(block_power(k, block), r.of[unorder16(order) >> 10 & 31][block - order], k.places);
+    const Power w = exp2_of(k.roots, p.x > -70.f ? p : make_float2(0.f, 0.f));
+    return p.x > -70.f ? w : Power{0, 0};
 }
 
 // Whether a logit's weight is at least m times the largest's.
@@ -276,8 +273,11 @@ struct __align__(16) SampleShared {
     int listed[kWarps], hits[kWarps][kEach];  // ... and the first pieces of the groups that hold some
     uint2 others[kList];                // first CTA: those of the other CTAs' that are in the window
     uint32_t others_listed;
+    uint32_t same[32];                  // ids of the drawn logit
+    int sames;
     u64 sum_to[kThreads];               // weight and tokens up to each thread's last bin
     int count_to[kThreads];
+    Power base[2][kThreads];            // of the (two at most) blocks of its bins
     u64 warp_sum[kWarps];
     int warp_count[kWarps];
     u64 rest[kMaxCluster];              // first CTA: every CTA's sum below the window (kFirst: of all its logits)
@@ -524,14 +524,18 @@ __device__ __forceinline__ void window_sums(SampleShared& sh, uint32_t high, uin
     const int lo = min(tid * own, bins), hi = min(lo + own, bins);
     int n = 0;
     u64 w = 0;
-    uint32_t block = 0;
-    Power base = {0, 0};
+    // a thread's bins, 16 at most, lie in two blocks at most
+    const uint32_t block0 = block_of(high - lo, k.order), block1 = block_of(high - max(hi - 1, lo), k.order);
+    const Power base0 = block_power(k, block0), base1 = block_power(k, block1);
+    sh.base[0][tid] = base0;
+    sh.base[1][tid] = base1;
     for (int i = lo; i < hi; ++i) {
         const uint32_t c = sh.count[i], order = high - i;
         if (c) {
-            if (block_of(order, k.order) != block) base = block_power(k, block = block_of(order, k.order));
+            const bool one = block_of(order, k.order) != block0;
             n += (int)c;
-            w += c * weight_in(base, sh.ratios.of[unorder16(order) >> 10 & 31][block - order], k.places);
+            w += c * weight_in(one ? base1 : base0,
+                               sh.ratios.of[unorder16(order) >> 10 & 31][(one ? block1 : block0) - order], k.places);
         }
     }
 #pragma unroll
@@ -553,6 +557,13 @@ __device__ __forceinline__ void window_sums(SampleShared& sh, uint32_t high, uin
     sh.sum_to[tid] = w;
     if (tid == 0) sh.window = o;
     __syncthreads();
+}
+
+// The weight of a logit of bin i, one of `thread`'s.
+__device__ __forceinline__ u64 bin_weight(const SampleShared& sh, const Window& w, int thread, int i) {
+    const uint32_t order = w.high - (uint32_t)i, top = sh.scale.order, block = block_of(order, top);
+    const bool one = block != block_of(w.high - (uint32_t)(thread * w.own), top);
+    return weight_in(sh.base[one][thread], sh.ratios.of[unorder16(order) >> 10 & 31][block - order], sh.scale.places);
 }
 
 enum { kByCount, kReach, kPass };  // the n-th token; the first at which the weight reaches, or passes, s
@@ -577,7 +588,7 @@ __device__ __noinline__ void find(const SampleShared& sh, int how, int n, u64 s,
     const u64 s0 = thread ? sh.sum_to[thread - 1] : w.above;
     const int bins = (int)(w.high - w.low) + 1, i = thread * w.own + lane;
     const int c = lane < w.own && i < bins ? (int)sh.count[i] : 0;  // own is 16 at most
-    const u64 weight = c ? weight_of(sh.scale, sh.ratios, w.high - i) : 0;
+    const u64 weight = c ? bin_weight(sh, w, thread, i) : 0;
     int ni = c;
     u64 si = c * weight;
 #pragma unroll 1
@@ -623,7 +634,7 @@ __device__ __noinline__ bool find_min(const SampleShared& sh, float m, Found* ou
     int n = thread ? sh.count_to[thread - 1] : w.before;
     u64 s = thread ? sh.sum_to[thread - 1] : w.above;
     const int c = i < lo && lane < w.own ? (int)sh.count[i] : 0;
-    u64 si = c ? c * weight_of(sh.scale, sh.ratios, w.high - i) : 0;
+    u64 si = c ? c * bin_weight(sh, w, thread, i) : 0;
     n += (int)__reduce_add_sync(kFull, (unsigned)c);
 #pragma unroll 1
     for (int d = 16; d > 0; d >>= 1) si += __shfl_xor_sync(kFull, si, d);
@@ -690,7 +701,8 @@ __device__ __noinline__ void decide(SampleShared& sh, const Wish& wish, bool mor
 // ---- the kernel ---------------------------------------------------------------------
 
 __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a) {
-    __shared__ SampleShared sh;
+    extern __shared__ __align__(16) char smem[];
+    SampleShared& sh = *reinterpret_cast<SampleShared*>(smem);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t rank = a.cluster > 1 ? cluster_rank() : 0;
     const int64_t row = blockIdx.x / (unsigned)a.cluster;
@@ -869,7 +881,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
     Command cmd = {kFirst, top, low, 0, 0, 0, 0};
     if (low > top) cmd = {kWindow, top, window_low(top), wish.k == kAll, 0, 0, 0};  // a list is not whole
 
-    if (tid == 0) sh.before_count = 0, sh.before_sum = 0, sh.trying = 1, sh.scale = k;
+    if (tid == 0) sh.before_count = 0, sh.before_sum = 0, sh.trying = 1, sh.sames = 0, sh.scale = k;
     __syncthreads();
 
     // first CTA, first warp: where the search is
@@ -1071,7 +1083,19 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
                         sh.ending[0].total = min(x.total, y.total) + apart / 2;
                     }
                     __syncthreads();
+                    if (sh.ending[0].ok && sh.ending[0].at.order >= low && sh.others_listed <= (uint32_t)kList) {
+                        // the listed ids of the drawn logit
+                        const uint32_t order = sh.ending[0].at.order;
+                        auto look_at = [&](const uint2& x) {
+                            if (x.x != order) return;
+                            const int i = atomicAdd(&sh.sames, 1);
+                            if (i < 32) sh.same[i] = x.y;
+                        };
+                        for (int i = lane; i < sh.listed[warp]; i += 32) look_at(sh.list[warp][i]);
+                        for (int i = tid; i < (int)sh.others_listed; i += kThreads) look_at(sh.others[i]);
+                    }
                     if (tid == 32 && sh.ending[0].ok) write_logprob(sh.ending[0].at.order, sh.ending[0].total);
+                    __syncthreads();
                 }
                 if (warp == 0) {  // the search is one warp's
                     Found at = {};
@@ -1175,30 +1199,13 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
                     }
                     if (done) {
                         if (stage != kTry && lane == 0) write_logprob(at.order, total);
-                        if (at.order >= low && sh.others_listed <= (uint32_t)kList) {
+                        const int n = sh.sames;
+                        if (stage == kTry && n > 0 && n <= 32) {
                             // of the listed ids of the drawn logit the one that so many lie before
-                            int n = 0;
-                            uint32_t id = 0;  // this lane's share of them: at most one, or the search below
-                            bool many = false;
-                            auto look_at = [&](const uint2& x) {
-                                if (x.x != at.order) return;
-                                many |= n > 0;
-                                id = x.y;
-                                ++n;
-                            };
-                            for (int v = 0; v < kWarps; ++v)
-                                for (int i = lane; i < sh.listed[v]; i += 32) look_at(sh.list[v][i]);
-                            for (int i = lane; i < (int)sh.others_listed; i += 32) look_at(sh.others[i]);
-                            if (!__any_sync(kFull, many)) {
-                                int before = 0;
-                                for (int l = 0; l < 32; ++l) {
-                                    const uint32_t other = __shfl_sync(kFull, id, l);
-                                    before += __shfl_sync(kFull, n, l) && other < id;
-                                }
-                                if (n && before == at.tie) a.token[row] = (int64_t)id;
-                            } else {
-                                next = {kTie, 0, 0, 0, at.order, (uint32_t)at.tie, 0};
-                            }
+                            const uint32_t id = sh.same[min(lane, n - 1)];
+                            int before = 0;
+                            for (int l = 0; l < n; ++l) before += sh.same[l] < id;
+                            if (lane < n && before == at.tie) a.token[row] = (int64_t)id;
                         } else {
                             next = {kTie, 0, 0, 0, at.order, (uint32_t)at.tie, 0};
                         }
@@ -1244,6 +1251,10 @@ int cluster_for(int64_t rows, int64_t vocab, int sms) {
 
 }  // namespace
 
+cudaError_t sample_prepare() {
+    return cudaFuncSetAttribute(sample_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(SampleShared));
+}
+
 }  // namespace mnb
 
 extern "C" int mnb_sample(const void* logits, int64_t rows, int64_t vocab, int64_t row_stride, const float* u,
@@ -1280,6 +1291,7 @@ extern "C" int mnb_sample(const void* logits, int64_t rows, int64_t vocab, int64
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(rows * a.cluster));
     cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = sizeof(SampleShared);
     cfg.stream = reinterpret_cast<cudaStream_t>(stream);
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;
