@@ -24,7 +24,7 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kRing = 4;   // 16-byte pieces a thread has on their way
-constexpr int kChunk = 8;  // tokens of a CTA, at most
+constexpr int kChunk = 4;  // tokens of a CTA, at most (8: 73 us in the case above, 16: 82)
 
 struct RopeArgs {
     KvArgs b;                  // q_start, kv_len, seqs, tokens (where positions is NULL)
@@ -39,6 +39,30 @@ struct RopeArgs {
     int64_t q_stride, k_stride, q_out_stride, k_out_stride;
 };
 
+typedef unsigned long long u64;
+
+// Pairs of FP32 values in one 64-bit register: one instruction for two.
+__device__ __forceinline__ u64 pair(float2 v) {
+    u64 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(v.x), "f"(v.y));
+    return r;
+}
+__device__ __forceinline__ float2 unpair(u64 v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c) {
+    u64 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ u64 mul2(u64 a, u64 b) {
+    u64 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
 // f / 2 pi as a fraction of a turn, times 2^64.
 __device__ __forceinline__ unsigned long long turn_of(float f) {
     const double d = (double)f, hi = 0.15915494309189534561, lo = -9.839338337591243e-18;  // 1 / 2 pi
@@ -48,13 +72,22 @@ __device__ __forceinline__ unsigned long long turn_of(float f) {
            (unsigned long long)__double2ll_rn(e * 18446744073709551616.0);
 }
 
-// Position of token t, or -1.  The whole warp.
-__device__ __forceinline__ int position_of(const RopeArgs& a, int t) {
-    if (a.positions) return a.positions[t];
-    int64_t first;
-    const KvSeq s = kv_find_seq(a.b, t, KvSplit{1, 0, 0}, &first);
-    const int i = t - s.row0;
-    return i >= 0 && i < s.n ? s.len - s.n + i : -1;
+// Positions of the n tokens from t0 on (32 at most), or -1: a lane's.  The whole warp; a look for each sequence that
+// the tokens belong to.
+__device__ __forceinline__ int position_of(const RopeArgs& a, int t0, int n) {
+    const int lane = threadIdx.x & 31, t = t0 + lane;
+    if (a.positions) return lane < n ? a.positions[t] : -1;
+    int pos = -1;
+    unsigned left = n < 32 ? (1u << n) - 1u : 0xffffffffu;
+    while (left) {
+        int64_t first;
+        const KvSeq s = kv_find_seq(a.b, t0 + __ffs(left) - 1, KvSplit{1, 0, 0}, &first);
+        const int i = t - s.row0;
+        const bool mine = i >= 0 && i < s.n;
+        if (mine) pos = s.len - s.n + i;
+        left &= ~(__ballot_sync(0xffffffffu, mine) | (left & -left));  // (the one looked for: it may be no sequence's)
+    }
+    return pos;
 }
 
 template <int D, bool NORM>
@@ -96,9 +129,9 @@ __global__ void __launch_bounds__(kThreads, 6) qk_rope_kernel(const RopeArgs a) 
             gain[i / D][i % D] = g ? __half2float(g[i % D]) : 1.f;
         }
     }
-    for (int i = warp; i < nt; i += kThreads / 32) {
-        const int pos = position_of(a, t0 + i);
-        if ((tid & 31) == 0) position[i] = pos;
+    if (warp == kThreads / 32 - 1) {  // (the first warps take the frequencies)
+        const int pos = position_of(a, t0, nt);
+        if ((tid & 31) < nt) position[tid & 31] = pos;
     }
     __syncthreads();
     for (int i = tid; i < nt * half; i += kThreads) {
@@ -115,7 +148,7 @@ __global__ void __launch_bounds__(kThreads, 6) qk_rope_kernel(const RopeArgs a) 
     const int other = (tid & 31) + (a.interleaved || !turned ? 0 : second ? -lanes : lanes);
     const int pair0 = a.interleaved ? j * 4 : (second ? j - lanes : j) * 8;
     const int other8 = (j + other - (tid & 31)) * 8;
-    float c[8], s[8];  // what a value and its other one are multiplied with, weights included
+    u64 c2[4], s2[4];  // what two values and their other ones are multiplied with, weights included
     int have = -1;     // for which token and kind of head
     int t = 0, h = h0;
     for (int q = 0; q < passes; q += kRing) {
@@ -126,6 +159,7 @@ __global__ void __launch_bounds__(kThreads, 6) qk_rope_kernel(const RopeArgs a) 
             const bool key = h >= a.q_heads, normed = NORM && (key ? a.k_weight != nullptr : a.q_weight != nullptr);
             if (have != 2 * t + key) {
                 have = 2 * t + key;
+                float c[8], s[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     c[i] = 1.f;
@@ -140,6 +174,11 @@ __global__ void __launch_bounds__(kThreads, 6) qk_rope_kernel(const RopeArgs a) 
                         if (turned) s[i] *= gain[key][a.interleaved ? j * 8 + (i ^ 1) : other8 + i];
                     }
                 }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    c2[i] = pair(make_float2(c[2 * i], c[2 * i + 1]));
+                    s2[i] = pair(make_float2(s[2 * i], s[2 * i + 1]));
+                }
             }
             uint4 y;  // the other values of the pairs
             if (a.interleaved) {
@@ -152,30 +191,30 @@ __global__ void __launch_bounds__(kThreads, 6) qk_rope_kernel(const RopeArgs a) 
                 y.w = __shfl_sync(0xffffffffu, x[u].w, other);
             }
             if (!turned) y = make_uint4(0, 0, 0, 0);  // not an infinity times 0
-            float v[8];
+            u64 v[4];
             const __half2* xp = reinterpret_cast<const __half2*>(&x[u]);
             const __half2* yp = reinterpret_cast<const __half2*>(&y);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 f = __half22float2(xp[i]);
-                v[2 * i] = f.x, v[2 * i + 1] = f.y;
-            }
+            for (int i = 0; i < 4; ++i) v[i] = pair(__half22float2(xp[i]));
             float rms = 1.f;
             if (NORM) {
-                float sum = 0.f;
+                u64 part = 0;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) sum = fmaf(v[i], v[i], sum);
+                for (int i = 0; i < 4; ++i) part = fma2(v[i], v[i], part);
+                const float2 two = unpair(part);
+                float sum = two.x + two.y;
 #pragma unroll
                 for (int m = LPH / 2; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
                 if (normed) rms = rsqrtf(fmaf(sum, 1.f / D, a.eps));
             }
+            const u64 rms2 = pair(make_float2(rms, rms));
             uint32_t out[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float2 o = __half22float2(yp[i]);
-                const float lo = rms * fmaf(v[2 * i], c[2 * i], o.x * s[2 * i]);
-                const float hi = rms * fmaf(v[2 * i + 1], c[2 * i + 1], o.y * s[2 * i + 1]);
-                const __half2 p = __floats2half2_rn(lo, hi);
+                u64 r = fma2(v[i], c2[i], mul2(pair(__half22float2(yp[i])), s2[i]));
+                if (NORM) r = mul2(r, rms2);
+                const float2 f = unpair(r);
+                const __half2 p = __floats2half2_rn(f.x, f.y);
                 out[i] = *reinterpret_cast<const uint32_t*>(&p);
             }
             if (h < a.heads && pos >= 0) {
@@ -254,7 +293,7 @@ extern "C" int mnb_qk_rope(const mnb_rope* rope, const mnb_kv_batch* batch, cons
     a.k_stride = k_stride;
     a.q_out_stride = q_out_stride;
     a.k_out_stride = k_out_stride;
-    // tokens of a CTA: eight where that leaves six CTAs an SM and more
+    // tokens of a CTA: as many as leave six CTAs an SM and more
     a.chunk = (int)(tokens / ((int64_t)sms * 6));
     a.chunk = a.chunk < 1 ? 1 : a.chunk > kChunk ? kChunk : a.chunk;
     const dim3 grid((unsigned)((tokens + a.chunk - 1) / a.chunk)), block(kThreads);

@@ -533,41 +533,47 @@ class Rope:
         self.ref = ctypes.byref(self.desc)
 
 
-def _heads(x, out, tokens: int, dim: int, device: int, what: str):
-    """(address, stride, heads, address, stride) of token tensors, zeros without one."""
-    if x is None:
-        _want(out is None, f"{what}_out without {what}")
-        return None, 0, 0, None, 0
-    shape = x.shape
-    _want(len(shape) in (2, 3) and (len(shape) == 3 or shape[1] % dim == 0), f"{what}: [tokens, heads, head_dim]")
-    heads = shape[1] if len(shape) == 3 else shape[1] // dim
-    stride = _rows(x, shape, x.stride(), heads, dim, tokens, what)
+def _heads(x, tokens: int, dim: int, device: int, what: str):
+    """(address, row stride, heads) of a token tensor."""
+    shape, s = x.shape, x.stride()
+    if len(shape) == 3:
+        heads = shape[1]
+        ok = shape[2] == dim and s[2] == 1 and (s[1] == dim or heads == 1)
+    else:
+        heads = shape[1] // dim if len(shape) == 2 else 0
+        ok = len(shape) == 2 and shape[1] == heads * dim and s[1] == 1
+    if not ok or shape[0] != tokens or x.dtype is not _half:
+        raise ValueError(f"{what}: fp16 [tokens, heads, head_dim], whole rows")
     if x.get_device() != device:
         raise _not_there("mnb_qk_rope")
-    if out is None or out is x:
-        return x.data_ptr(), stride, heads, x.data_ptr(), stride
-    out_stride = _rows(out, out.shape, out.stride(), heads, dim, tokens, what + "_out")
-    if out.get_device() != device:
-        raise _not_there("mnb_qk_rope")
-    return x.data_ptr(), stride, heads, out.data_ptr(), out_stride
+    return x.data_ptr(), s[0] if tokens > 1 else heads * dim, heads  # a single row has no stride
 
 
 def mnb_qk_rope(rope: Rope, where, Q, K=None, Q_out=None, K_out=None, stream=None) -> None:
     """Norm and rotate heads by their tokens' positions: Q fp16 [tokens, q_heads, head_dim], K alike (either may be
     None), into Q_out, K_out (None: in place).  ``where``: a KVBatch, or int32 positions [tokens] (negative: left
     as they are)."""
-    device = where.device if isinstance(where, KVBatch) else where.get_device()
-    if device < 0 or (rope.device is not None and rope.device != device):
-        raise _not_there("mnb_qk_rope")
-    if isinstance(where, KVBatch):
-        batch, positions, tokens = where.ref, None, where.tokens
+    if where.__class__ is KVBatch:
+        device, batch, positions, tokens = where.device, where.ref, None, where.tokens
     else:
-        _fp16()
         _want(where.dtype is _int32 and where.dim() == 1 and where.is_contiguous(),
               "positions: contiguous int32 [tokens]")
-        batch, positions, tokens = None, where.data_ptr(), where.shape[0]
-    q, qs, qh, qo, qos = _heads(Q, Q_out, tokens, rope.head_dim, device, "Q")
-    k, ks, kh, ko, kos = _heads(K, K_out, tokens, rope.head_dim, device, "K")
+        device, batch, positions, tokens = where.get_device(), None, where.data_ptr(), where.shape[0]
+    if device < 0 or (rope.device != device and rope.device is not None):
+        raise _not_there("mnb_qk_rope")
+    dim = rope.head_dim
+    q = k = qo = ko = None
+    qs = ks = qos = kos = qh = kh = 0
+    if Q is not None:
+        q, qs, qh = qo, qos, _ = _heads(Q, tokens, dim, device, "Q")
+    if K is not None:
+        k, ks, kh = ko, kos, _ = _heads(K, tokens, dim, device, "K")
+    if Q_out is not None:
+        qo, qos, heads = _heads(Q_out, tokens, dim, device, "Q_out")
+        _want(heads == qh, "Q_out: heads of Q")
+    if K_out is not None:
+        ko, kos, heads = _heads(K_out, tokens, dim, device, "K_out")
+        _want(heads == kh, "K_out: heads of K")
     rc = (_lib or lib()).mnb_qk_rope(rope.ref, batch, positions, tokens, q, qs, qh, k, ks, kh, qo, qos, ko, kos,
                                      _current_stream() if stream is None else _stream(stream))
     if rc:
