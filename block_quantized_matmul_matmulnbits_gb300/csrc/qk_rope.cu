@@ -93,9 +93,11 @@ __device__ __forceinline__ int position_of(const RopeArgs& a, int t0, int n) {
 template <int D, bool NORM>
 __global__ void __launch_bounds__(kThreads, 6) qk_rope_kernel(const RopeArgs a) {
     constexpr int LPH = D / 8, STEP = kThreads / LPH;  // threads of a head, heads of a pass
-    __shared__ float2 turn[kChunk][D / 2];             // cosine and sine of a token's pairs
+    // Cosine and sine of a token's pairs, and the weights of queries and of keys.  The i-th value of all threads of a
+    // head lies together, so that they are read without meeting in a bank.
+    __shared__ float2 turn[kChunk][D / 2];
     __shared__ unsigned long long step[D / 2];
-    __shared__ float gain[2][D];                       // weights of queries and of keys
+    __shared__ float gain[2][D];
     __shared__ int position[kChunk];
     const int tid = threadIdx.x, warp = tid >> 5, j = tid % LPH, h0 = tid / LPH;
     const int half = a.rotary >> 1, lanes = a.rotary >> 4;  // pairs; threads of half of the turned values
@@ -126,7 +128,7 @@ __global__ void __launch_bounds__(kThreads, 6) qk_rope_kernel(const RopeArgs a) 
     if (NORM) {
         for (int i = tid; i < 2 * D; i += kThreads) {
             const __half* g = i < D ? a.q_weight : a.k_weight;
-            gain[i / D][i % D] = g ? __half2float(g[i % D]) : 1.f;
+            gain[i / D][(i & 7) * LPH + (i % D >> 3)] = g ? __half2float(g[i % D]) : 1.f;
         }
     }
     if (warp == kThreads / 32 - 1) {  // (the first warps take the frequencies)
@@ -139,15 +141,15 @@ __global__ void __launch_bounds__(kThreads, 6) qk_rope_kernel(const RopeArgs a) 
         const int r = (int)(((unsigned long long)(unsigned)position[t] * step[p]) >> 32);
         float s, c;
         sincospif((float)r * 4.656612873077392578125e-10f, &s, &c);  // r 2^-31: half turns
-        turn[t][p] = make_float2(c, s);
+        turn[t][a.interleaved ? (p & 3) * (half >> 2) + (p >> 2) : (p & 7) * lanes + (p >> 3)] = make_float2(c, s);
     }
     __syncthreads();
 
     const bool turned = j * 8 < a.rotary, second = !a.interleaved && j >= lanes;
     // the thread that holds the other values of this one's pairs
     const int other = (tid & 31) + (a.interleaved || !turned ? 0 : second ? -lanes : lanes);
-    const int pair0 = a.interleaved ? j * 4 : (second ? j - lanes : j) * 8;
-    const int other8 = (j + other - (tid & 31)) * 8;
+    const int pair0 = second ? j - lanes : j, pairs = a.interleaved ? half >> 2 : lanes;
+    const int oj = j + other - (tid & 31);
     u64 c2[4], s2[4];  // what two values and their other ones are multiplied with, weights included
     int have = -1;     // for which token and kind of head
     int t = 0, h = h0;
@@ -165,13 +167,13 @@ __global__ void __launch_bounds__(kThreads, 6) qk_rope_kernel(const RopeArgs a) 
                     c[i] = 1.f;
                     s[i] = 0.f;
                     if (turned) {
-                        const float2 cs = turn[t][pair0 + (a.interleaved ? i >> 1 : i)];
+                        const float2 cs = turn[t][pair0 + (a.interleaved ? i >> 1 : i) * pairs];
                         c[i] = cs.x;
                         s[i] = (a.interleaved ? (i & 1) : second) ? cs.y : -cs.y;
                     }
                     if (NORM) {
-                        c[i] *= gain[key][j * 8 + i];
-                        if (turned) s[i] *= gain[key][a.interleaved ? j * 8 + (i ^ 1) : other8 + i];
+                        c[i] *= gain[key][i * LPH + j];
+                        if (turned) s[i] *= gain[key][a.interleaved ? (i ^ 1) * LPH + j : i * LPH + oj];
                     }
                 }
 #pragma unroll
