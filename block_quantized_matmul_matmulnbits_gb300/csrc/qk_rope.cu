@@ -258,6 +258,9 @@ extern "C" int mnb_qk_rope(const mnb_rope* rope, const mnb_kv_batch* batch, cons
         (kv_heads && (k_stride % 8 != 0 || k_out_stride % 8 != 0)))
         return MNB_ERR_ALIGN;
     if (tokens == 0 || q_heads + kv_heads == 0 || (batch && batch->seqs == 0)) return MNB_OK;
+    // in place means row by row
+    if (tokens > 1 && ((q_heads && Q == Q_out && q_stride != q_out_stride) || (kv_heads && K == K_out && k_stride != k_out_stride)))
+        return MNB_ERR_ARG;
     if ((q_heads && (!Q || !Q_out)) || (kv_heads && (!K || !K_out)) || (rope->rotary_dim && !rope->inv_freq) ||
         (batch ? !batch->kv_len || !batch->q_start : !positions))
         return MNB_ERR_ARG;

@@ -514,14 +514,14 @@ typedef struct {
  * made them and mnb_kv_write / mnb_attn.
  *   batch       the sequences: token i of sequence s has position
  *               kv_len[s] - n + i, as in mnb_attn (its page table is not read); or NULL:
- *   positions   int32 [tokens] (device), used where batch is NULL.  A row
- *               with a negative position, and with a batch a row that no sequence owns,
- *               is not read and its outputs are left as they are.
+ *   positions   int32 [tokens] (device), used where batch is NULL.  The outputs of a row
+ *               with a negative position, and with a batch of a row that no sequence
+ *               owns, are left as they are.
  *   tokens      rows of Q and K (batch->tokens where there is a batch)
  *   Q, K        fp16, row t at Q + t * q_stride, [q_heads, head_dim] (K alike);
  *               heads may be 0, the pointers then NULL.  q_heads + kv_heads <= 65536
  *   Q_out, K_out   the same with strides of their own; each may be its input
- *               (in place) and overlaps nothing else of the call
+ *               (in place, with its stride) and overlaps nothing else of the call
  * Strides are in elements, multiples of 8, at least heads * head_dim; the sums of
  * squares are in binary32, the angle's turns are exact to 2^-32 at every position, one
  * rounding to fp16 at the end.  Values from rotary_dim on are normed only.
@@ -565,20 +565,20 @@ typedef struct {
     const void* down_zp;
 } mnb_moe_layer;
 
-/* The layer for a few tokens (a decode step): each expert that some token takes is read
- * once (twice beyond 8 tokens of one expert).
+/* The layer for a few tokens (a decode step): the weights of each expert that some token takes
+ * are read from memory once, and once more from the cache for every 2, 4 or 8 of its tokens
+ * (with up to 2 tokens, up to two an expert on average, more).
  *   X        fp16 [M, hidden], M at most MNB_MOE_MAX_TOKENS
  *   Y        fp16 [M, hidden]; not X
  *   ids      int32 [M, top_k] or NULL: the experts taken, by falling logit
  *   weights  float [M, top_k] or NULL: their w_e
  *   ws       workspace of at least mnb_moe_workspace bytes, 16-byte aligned; it needs no
  *            clearing and holds nothing between calls; calls that may overlap need one each
- * Router logits are sums of exact products held to more than 64-bit floating point needs to
- * tell two experts apart by 2^-40 of their terms; the expert sums are in binary32 with
- * exact codes, the products silu(gate) * up enter the down projection in fp16 scaled by
- * a power of two per 32.  Each token's result is independent of the others in the call.
- * A token with NaN or infinity takes some valid experts and gives NaN or infinity.
- * Deterministic.  Errors: MNB_ERR_ARG (also a workspace that is too small),
+ * Router logits are sums of exact products in two binary32 words, which tell experts apart that
+ * differ by 2^-40 of their terms; the expert sums are in binary32 with exact codes, the
+ * products silu(gate) * up enter the down projection in fp16 scaled by a power of two
+ * per 32.  A token with NaN or infinity takes some valid experts and gives NaN or
+ * infinity; it does not touch the others.  Deterministic for given arguments.  Errors: MNB_ERR_ARG (also a workspace that is too small),
  * MNB_ERR_UNSUPPORTED (sizes beyond the above, bits, M), MNB_ERR_ALIGN (16 bytes; zero
  * points, ids and weights 4), MNB_ERR_NO_DEVICE, MNB_ERR_CUDA. */
 int mnb_moe(const mnb_moe_layer* layer, const void* X, int64_t M, void* Y, int32_t* ids, float* weights, void* ws,

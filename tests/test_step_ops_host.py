@@ -47,7 +47,7 @@ def child_rope_checks():
     E = mnb
     for kw in (dict(r=None), dict(tokens=-1), dict(qh=-1), dict(kh=-1), dict(rotary_dim=-16), dict(rotary_dim=80),
                dict(interleaved=2), dict(eps=-1.0), dict(eps=NAN), dict(eps=INF), dict(b=batch(tokens=4)),
-               dict(b=batch(tokens=5, seqs=-1)), dict(qs=248), dict(qos=248), dict(ks=120), dict(kos=120), dict(Q=None),
+               dict(b=batch(tokens=5, seqs=-1)), dict(qs=248), dict(qos=248), dict(qs=512), dict(kos=512), dict(ks=120), dict(kos=120), dict(Q=None),
                dict(Qo=None), dict(K=None), dict(Ko=None), dict(inv_freq=None), dict(positions=None),
                dict(b=batch(tokens=5, kv_len=None)), dict(b=batch(tokens=5, q_start=None))):
         assert rope(**kw) == E.MNB_ERR_ARG, kw
@@ -60,7 +60,8 @@ def child_rope_checks():
     for kw in (dict(tokens=0, Q=None), dict(qh=0, kh=0, Q=None), dict(b=batch(tokens=5, seqs=0))):
         assert rope(**kw) == E.MNB_OK, kw
     for kw in (dict(), dict(b=batch(tokens=5, page_table=None, max_pages=0), positions=None), dict(kh=0, K=None, Ko=None),
-               dict(qh=0, Q=None, Qo=None), dict(rotary_dim=0, inv_freq=None), dict(qh=65534, qs=1 << 23, qos=1 << 23)):
+               dict(qh=0, Q=None, Qo=None), dict(rotary_dim=0, inv_freq=None), dict(qh=65534, qs=1 << 23, qos=1 << 23), dict(qs=512, Qo=2 * A),
+               dict(tokens=1, qs=512, b=batch(tokens=1)), dict(qs=512, qos=512)):
         assert rope(**kw) == E.MNB_ERR_NO_DEVICE, kw
 
 
