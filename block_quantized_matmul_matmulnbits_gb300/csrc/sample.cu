@@ -683,7 +683,11 @@ __device__ __noinline__ void decide(SampleShared& sh, const Wish& wish, bool mor
     }
     if (wish.m > 0.f) {
         const bool end = find_min(sh, wish.m, &f[0]);
-        if (!(end && more) && f[0].n < kept) kept = f[0].n, total = f[0].sum;
+        if (end && more) {
+            if (kept == kAll) kept = kBeyond;
+        } else if (f[0].n < kept) {
+            kept = f[0].n, total = f[0].sum;
+        }
     }
     if (kept == kBeyond) return;
     __syncwarp();
@@ -879,7 +883,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
     k.order = top;
     low = max(low, window_low(top));
     Command cmd = {kFirst, top, low, 0, 0, 0, 0};
-    if (low > top) cmd = {kWindow, top, window_low(top), wish.k == kAll, 0, 0, 0};  // a list is not whole
+    if (low > top) cmd = {kWindow, top, window_low(top), sum, 0, 0, 0};  // a list is not whole
 
     if (tid == 0) sh.before_count = 0, sh.before_sum = 0, sh.trying = 1, sh.sames = 0, sh.scale = k;
     __syncthreads();
@@ -1065,8 +1069,8 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
                                       (u64)s.pieces + kThreads * kMaxCluster + 64;
                     if (cmd.op == kFirst) {
                         const u64 units = (u64)((s.p1 - s.p0) / (kGroup * kThreads)) + 80;
-                        error = sum ? (rest >> 24) * units + units + spare : 1ull << 61;  // (not known)
-                        rest = !sum ? error : rest > w.sum ? rest - w.sum : 0;
+                        error = sum ? (rest >> 24) * units + units + spare : 0;
+                        rest = rest > w.sum ? rest - w.sum : 0;
                     } else if (cmd.op == kWindow && cmd.rest) {
                         error = (rest >> 24) * 24 + spare;
                     }
@@ -1109,7 +1113,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
                         if (!done) {
                             // all of the histogram, then what lies below it exactly
                             if (cmd.op == kFirst)
-                                next = {kWindow, top, window_low(top), wish.k == kAll, 0, 0, 0};
+                                next = {kWindow, top, window_low(top), sum, 0, 0, 0};
                             else if (cmd.op == kWindow && cmd.rest && more)
                                 next = {kRestOf, top, cmd.low, 0, 0, 0, 0};
                             else

@@ -128,6 +128,20 @@ def test_runs_of_equal_logits_far_apart():
     check(x, u, top_p=[0.1, 0.2, 0.3, 0.9, 0.95, 0.99])
 
 
+def test_min_p_whose_place_lies_far_down():
+    # the last kept logit lies more orders below the largest than the first histogram holds
+    r = np.random.default_rng(83)
+    two = np.where(r.random((40, 77)) < 0.5, 1.0, -1.0).astype(np.float16)
+    ties = np.round(r.standard_normal((40, 4999)) * 2).astype(np.float16)
+    flat = (r.standard_normal((40, 20011)) * 0.5).astype(np.float16)
+    for x in (two, ties, flat):
+        for m in (0.5, 0.1, 0.001, 1e-6):
+            u, t = r.uniform(0, 1, 40), r.uniform(0.4, 3, 40)
+            check(x, u, t, min_p=np.full(40, m))
+            check(x, u, t, min_p=np.full(40, m), top_p=np.full(40, 0.99))
+            check(x, u, t, min_p=np.full(40, m), top_k=np.full(40, 3000))
+
+
 def test_odd_strides_and_another_stream():
     r, x = logits(80, 6, 1003)
     u = r.uniform(0, 1, 6)
