@@ -241,7 +241,7 @@ struct Command {
                          // counts in each CTA; kRestOf: the weight below
                          // the loaded window to its last place; kTie, kScan: the drawn logit's tokens
     uint32_t high, low;  // the orders from `high` down to `low`
-    uint32_t rest;       // kWindow: whether what lies below is summed in FP32
+    uint32_t rest;       // kWindow: whether what lies below is summed in FP32; kRestOf: whether it is summed quickly
     uint32_t order;      // kTie, kScan: the order looked for
     uint32_t skip;       // kTie: of its tokens the one after so many; kScan: of those in this warp ...
     uint32_t who;        // ... of the cluster
@@ -261,8 +261,11 @@ struct Found {      // a place in the order
     u64 sum;        // weight up to and with it
 };
 
+// kBelow: the drawn token, or what its probability wants, lies below the window; kAbove: it lies above, what is kept is known
+enum { kNo, kYes, kBelow, kAbove };
+
 struct Ending {     // what one end of the bound gives
-    int ok, kept;
+    int ok, kept;   // ok: of the above
     u64 total;      // the kept weight
     Found at;       // the drawn place
 };
@@ -292,6 +295,8 @@ struct __align__(16) SampleShared {
     Window window;
     Found found[4];                     // two ends of a bound: a place, the last kept
     Ending ending[2];
+    Found drawn;                        // the drawn token, where only its probability is wanted
+    u64 fixed[2];                       // the two ends' kept weight, where only the drawn token is wanted (else 0)
     u64 before_sum;                     // weight and tokens above the window that is loaded
     int before_count;
     uint32_t under;                     // the largest order below the last window
@@ -486,6 +491,76 @@ __device__ __forceinline__ uint32_t count_window(const Slice& s, const Scale& k,
     return max(order16(as_word(b2) & 0xFFFFu), order16(as_word(b2) >> 16));
 }
 
+// Whether quick_rest may be asked: 64 c logit of all logits that have a weight is at most 2^14.
+__device__ __forceinline__ bool quick_fits(const Scale& k) { return k.c * fabsf(k.top) + 70.f <= 256.f; }
+
+// More places of a thread's sum there: of 2^13 logits and more it has a 128th at most.
+__device__ __forceinline__ int quick_places(int places) { return places <= 48 ? 8 : 0; }
+
+// The weight of the CTA's logits below `low`, a thread's, to 2^-26 of it and a place, and each to one of the last places.
+// 64 c logit less 64 c top is a whole number m and r, |r| <= 1/2, and the weight the root 2^(m / 64), which is added as an
+// integer, and its product with 2^(r / 64) - 1, which is below 2^-7 and so is right to 2^-29 in FP32.  c is in two words, the
+// products with the upper one (12 bits) exact: r is off by the lower one's last place times 2^14 (2^-22 for the logit, as
+// much for the largest: 2^-27.5 of the weight) and by three roundings.
+__device__ __forceinline__ u64 quick_rest(const Slice& s, const Scale& k, uint32_t low) {
+    const __half low_h = __ushort_as_half((unsigned short)unorder16(low));
+    const __half2 low2 = __halves2half2(low_h, low_h);
+    const float c64 = k.c * 64.f, ch = __uint_as_float(__float_as_uint(c64) & 0xFFFFF000u);
+    const float cl = __fadd_rn(__fsub_rn(c64, ch), k.c_low * 64.f);
+    const float top_a = __fmul_rn(k.top, ch), top_m = rintf(__fmaf_rn(k.top, cl, top_a));
+    const float top_r = __fmaf_rn(k.top, cl, __fsub_rn(top_a, top_m));
+    constexpr float kMagic = 12582912.f;  // 1.5 2^23: a sum with it is a whole number
+    const u64 ch2 = pair(ch, ch), cl2 = pair(cl, cl), zero2 = 0, rt2 = pair(-top_r, -top_r), mt2 = pair(-top_m, -top_m);
+    const u64 up2 = pair(kMagic, kMagic), down2 = pair(-kMagic, -kMagic), minus2 = pair(-1.f, -1.f);
+    // 2^(r / 64) - 1, to r^3
+    const u64 p1 = pair(0.010830424696f, 0.010830424696f), p2 = pair(5.86490495e-05f, 5.86490495e-05f),
+              p3 = pair(2.11731324e-07f, 2.11731324e-07f), by64 = pair(0.015625f, 0.015625f);
+    const int more = quick_places(k.places), places = k.places + more;
+    const float unit = __uint_as_float((uint32_t)(places + 127) << 23);
+    const uint4 none = make_uint4(0xFC00FC00u, 0xFC00FC00u, 0xFC00FC00u, 0xFC00FC00u);
+    const uint4* pc = reinterpret_cast<const uint4*>(s.row + s.head);
+    const int tid = threadIdx.x;
+    auto load = [&](int i) { return i < s.p1 ? pc[i] : none; };
+    uint4 q0 = load(s.p0 + tid), q1 = load(s.p0 + tid + kThreads);
+    u64 sum = 0;
+    int id;
+    for (int i = s.p0 + tid;; i += kThreads) {
+        uint4 v = q0;
+        const bool ends = i - tid >= s.p1;  // the row's ends, last
+        if (ends) {
+            if (s.first && s.head && tid == kThreads - 1) v = edge_piece(s, 0, &id);
+            if (s.last && s.tail && tid == kThreads - 2) v = edge_piece(s, 1, &id);
+        } else {
+            q0 = q1;
+            q1 = load(i + 2 * kThreads);
+        }
+        u64 part = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t w = word_at(v, j), in = __hge2_mask(as_half2(w), low2);
+            const float2 f = __half22float2(as_half2((w & ~in) | (in & 0xFC00FC00u)));  // (-infinity: no weight)
+            const u64 x = pair(f.x, f.y), a = fma2(x, ch2, zero2);
+            const u64 m = add2(add2(fma2(x, cl2, add2(a, rt2)), up2), down2);
+            const u64 r = add2(fma2(x, cl2, fma2(m, minus2, a)), rt2);
+            const u64 t = fma2(r, fma2(r, fma2(r, p3, p2), p1), zero2);
+            const float2 mm = unpair(add2(m, mt2));
+            const float m0 = fmaxf(mm.x, -4480.f), m1 = fmaxf(mm.y, -4480.f);  // (NaN too)
+            const u64 n = pair(m0, m1);
+            const float2 g = unpair(add2(n, up2)), e = unpair(fma2(n, by64, zero2));
+            float2 y = unpair(t);
+            if (!(mm.x > -4480.f)) y.x = 0.f;
+            if (!(mm.y > -4480.f)) y.y = 0.f;
+            part = fma2(pair(ex2f(e.x), ex2f(e.y)), pair(y.x, y.y), part);
+            const int i0 = __float_as_int(g.x) - __float_as_int(kMagic) + 32, i1 = __float_as_int(g.y) - __float_as_int(kMagic) + 32;
+            sum += k.roots[i0 & 63] >> min(62 - places - (i0 >> 6), 63);
+            sum += k.roots[i1 & 63] >> min(62 - places - (i1 >> 6), 63);
+        }
+        const float2 f = unpair(part);
+        sum += (u64)__float2ll_rn((f.x + f.y) * unit);
+        if (ends) return sum >> more;
+    }
+}
+
 // The weight of the CTA's logits below `low`, a thread's, each to 2^-40 of it.
 __device__ __forceinline__ u64 exact_rest(const Slice& s, const Scale& k, uint32_t low) {
     const __half low_h = __ushort_as_half((unsigned short)unorder16(low));
@@ -660,45 +735,70 @@ __device__ __forceinline__ void find_top_p(const SampleShared& sh, float p, u64 
     find(sh, s ? kReach : kByCount, 1, s, out);  // the first is always kept
 }
 
-// What the window from the row's maximum down gives, `below` being the weight that lies under it (more: anything
-// does): ok = 0 where it does not say.  One warp, with two places of its own.
-__device__ __noinline__ void decide(SampleShared& sh, const Wish& wish, bool more, u64 below, Found* f, Ending* out) {
+// What the window gives, `below` being the weight that lies under it (more: anything does); the upper or the lower end of a
+// bound.  Where a row has no limit but a top-p that lies below the window, its kept weight is the limit's and at most one of the
+// tokens down there more, which leaves few draws in doubt.  One warp, with two places of its own.
+__device__ __noinline__ void decide(SampleShared& sh, const Wish& wish, bool more, bool upper, u64 below, Found* f,
+                                    Ending* out) {
     const int lane = threadIdx.x & 31;
     const int count = sh.window.count;
-    if (lane == 0) out->ok = 0;
+    if (lane == 0) out->ok = kNo;
     int kept = kAll;  // tokens kept, kAll: all of the row
     u64 total = sh.window.sum + below;
-    if (wish.k <= count || !more) {
-        kept = min(wish.k, count);
-        find(sh, kByCount, kept, 0, &f[1]);
-        total = f[1].sum;
-    } else if (wish.k != kAll) {
-        return;  // the k-th lies below
-    }
-    if (wish.p < 1.f) {
-        find_top_p(sh, wish.p, total, &f[0]);
-        const int n = f[0].n;
-        if (!n) kept = kBeyond;
-        else if (n <= kept) kept = n, total = f[0].sum;
-    }
-    if (wish.m > 0.f) {
-        const bool end = find_min(sh, wish.m, &f[0]);
-        if (end && more) {
-            if (kept == kAll) kept = kBeyond;
-        } else if (f[0].n < kept) {
-            kept = f[0].n, total = f[0].sum;
+    bool open = wish.k == kAll && more && !(wish.m > 0.f);  // whether what lies below the window is known well enough
+    if (sh.fixed[0]) {
+        kept = kBeyond, total = sh.fixed[upper];
+    } else {
+        if (wish.k <= count || !more) {
+            kept = min(wish.k, count);
+            find(sh, kByCount, kept, 0, &f[1]);
+            total = f[1].sum;
+        } else if (wish.k != kAll) {
+            return;  // the k-th lies below
+        }
+        if (wish.p < 1.f) {
+            const u64 s = times(wish.p, total, true);
+            if (s <= sh.window.above && sh.window.before) return;  // above this window
+            find_top_p(sh, wish.p, total, &f[0]);
+            const int n = f[0].n;
+            if (!n) {
+                kept = kBeyond;
+                const Window& w = sh.window;
+                const int last = (int)(w.high - w.low);
+                total = s + (upper ? bin_weight(sh, w, last / w.own, last) : 0);
+            } else if (n <= kept) {
+                kept = n, total = f[0].sum;
+            }
+            open = open && !n;
+        }
+        if (wish.m > 0.f) {
+            const bool end = find_min(sh, wish.m, &f[0]);
+            if (end && more) {
+                if (kept == kAll) kept = kBeyond;
+            } else if (f[0].n < kept) {
+                kept = f[0].n, total = f[0].sum;
+            }
         }
     }
-    if (kept == kBeyond) return;
+    const bool known = sh.drawn.n != 0;
+    if (kept == kBeyond && !open) return;
     __syncwarp();
-    if (lane == 0) f[0].n = 0;
+    if (lane == 0) f[0] = sh.drawn;
     __syncwarp();
-    if (wish.u < 1.f) find(sh, kPass, 0, times(wish.u, total, false), &f[0]);
-    if (kept != kAll && (!f[0].n || f[0].n > kept)) {
+    if (wish.u < 1.f && !known) {
+        const u64 target = times(wish.u, total, false);
+        if (target < sh.window.above && sh.window.before) {
+            if (lane == 0) out->ok = kAbove, out->kept = kept, out->total = total;
+            __syncwarp();
+            return;
+        }
+        find(sh, kPass, 0, target, &f[0]);
+    }
+    if (kept < kBeyond && !known && (!f[0].n || f[0].n > kept)) {
         __syncwarp();
         find(sh, kByCount, kept, 0, &f[0]);
     }
-    if (lane == 0) *out = {f[0].n != 0, kept, total, f[0]};
+    if (lane == 0) *out = {f[0].n ? kYes : open && wish.u < 1.f ? kBelow : kNo, kept, total, f[0]};
     __syncwarp();
 }
 
@@ -885,7 +985,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
     Command cmd = {kFirst, top, low, 0, 0, 0, 0};
     if (low > top) cmd = {kWindow, top, window_low(top), sum, 0, 0, 0};  // a list is not whole
 
-    if (tid == 0) sh.before_count = 0, sh.before_sum = 0, sh.trying = 1, sh.sames = 0, sh.scale = k;
+    if (tid == 0) sh.before_count = 0, sh.before_sum = 0, sh.trying = 1, sh.sames = 0, sh.drawn.n = 0, sh.fixed[0] = 0, sh.scale = k;
     __syncthreads();
 
     // first CTA, first warp: where the search is
@@ -917,7 +1017,9 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
         a.logprob[row] = fminf((float)((((double)t.x + (double)t.y) - log2_of(k.roots, total, k.places)) * 0.69314718055994530942), 0.f);
     };
 
-    for (;;) {
+    // The tries go down window by window, from the top once more at most, and to the end from the top once and back: it
+    // ends far below this number of steps.
+    for (int steps = 0; steps < 8 * kMaxWindows; ++steps) {
         if (cmd.op == kFirst) {
             // the lists' logits that are in the window: their counts, and the first CTA's list of them
             const uint32_t counts = in_cta(smem_u32(sh.count), 0), list = in_cta(smem_u32(sh.others), 0),
@@ -953,7 +1055,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
                 under = count_window<false, false>(s, k, cmd.high, cmd.low, smem_u32(sh.count), &exact);
             send_rest(exact, under);
         } else if (cmd.op == kRestOf) {
-            send_rest(exact_rest(s, k, cmd.low), kLowest);
+            send_rest(cmd.rest ? quick_rest(s, k, cmd.low) : exact_rest(s, k, cmd.low), kLowest);
         } else {  // tokens of one logit, warp by warp in the order of their ids
             const int n = s.p1 - s.p0, w0 = s.p0 + (int)((int64_t)n * warp / kWarps),
                       w1 = s.p0 + (int)((int64_t)n * (warp + 1) / kWarps);
@@ -1065,29 +1167,51 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
                     // 4; of the exponent its rounding, 68 ln 2 / 2, and the low word of c, which the difference from the
                     // largest is not multiplied with, 60 ln 2 / 2.
                     u64 error = 0;
-                    const u64 spare = ((u64)a.vocab << k.places >> 42) + ((u64)a.vocab >> (60 - k.places)) +
-                                      (u64)s.pieces + kThreads * kMaxCluster + 64;
+                    const u64 small = (u64)a.vocab << k.places >> 42;
+                    const u64 spare = ((u64)a.vocab >> (60 - k.places)) + (u64)s.pieces + kThreads * kMaxCluster + 64;
                     if (cmd.op == kFirst) {
                         const u64 units = (u64)((s.p1 - s.p0) / (kGroup * kThreads)) + 80;
-                        error = sum ? (rest >> 24) * units + units + spare : 0;
+                        error = sum ? (rest >> 24) * units + units + small + spare : 0;
                         rest = rest > w.sum ? rest - w.sum : 0;
                     } else if (cmd.op == kWindow && cmd.rest) {
-                        error = (rest >> 24) * 24 + spare;
+                        error = min((rest >> 24) * 24 + small, (rest >> 24) * 42) + spare;
+                    } else if (cmd.op == kRestOf && cmd.rest) {
+                        error = (rest >> 26) + ((u64)a.vocab * 2 >> quick_places(k.places)) + kThreads * kMaxCluster;
                     }
                     if (!more) rest = error = 0;
                     if (warp < 2 && (warp == 0 || error))
-                        decide(sh, wish, more, warp ? rest + error : rest > error ? rest - error : 0, &sh.found[2 * warp],
-                               &sh.ending[warp]);
+                        decide(sh, wish, more, warp, warp ? rest + error : rest > error ? rest - error : 0,
+                               &sh.found[2 * warp], &sh.ending[warp]);
                     __syncthreads();
                     if (tid == 0 && error) {
                         const Ending x = sh.ending[0], y = sh.ending[1];
-                        // the same kept tokens, the same place, and a probability that is certain enough
+                        // The row's weight lies between the two ends, so what both draw is the token.  Its probability has
+                        // to be certain enough: where the limits are certain, the ends lie much farther from it than it is
+                        // from their middle; where a top-p's lies below the window, the next one gives it.
                         const u64 apart = x.total > y.total ? x.total - y.total : y.total - x.total;
-                        sh.ending[0].ok = x.ok && y.ok && x.kept == y.kept && x.at.n == y.at.n && apart <= x.total >> 15;
+                        const bool yes = x.ok == kYes && y.ok == kYes, same = yes && x.at.n == y.at.n, fixed = sh.fixed[0] != 0;
+                        const bool below_it = yes && !fixed && x.kept == kBeyond && y.kept == kBeyond;
+                        int ok = kNo;
+                        if (same && apart <= x.total >> (x.kept == y.kept && (x.kept != kBeyond || fixed) ? 15 : 19)) {
+                            ok = kYes;
+                        } else if (below_it || (x.ok == kBelow && y.ok == kBelow)) {
+                            ok = kBelow;
+                            if (same) sh.drawn = x.at;
+                        } else if (x.ok == kAbove && y.ok == kAbove && !fixed && apart <= x.total >> 19) {
+                            ok = kAbove;
+                            sh.fixed[0] = x.total, sh.fixed[1] = y.total;
+                        }
+                        sh.ending[0].ok = ok;
                         sh.ending[0].total = min(x.total, y.total) + apart / 2;
+                    } else if (tid == 0) {  // there is one end: the weight below is exact, or not asked for
+                        Ending& x = sh.ending[0];
+                        if ((more && sum && x.kept == kBeyond) || sh.fixed[0])
+                            x.ok = kNo;
+                        else if (x.ok == kAbove)
+                            sh.fixed[0] = sh.fixed[1] = x.total;
                     }
                     __syncthreads();
-                    if (sh.ending[0].ok && sh.ending[0].at.order >= low && sh.others_listed <= (uint32_t)kList) {
+                    if (sh.ending[0].ok == kYes && sh.ending[0].at.order >= low && sh.others_listed <= (uint32_t)kList) {
                         // the listed ids of the drawn logit
                         const uint32_t order = sh.ending[0].at.order;
                         auto look_at = [&](const uint2& x) {
@@ -1098,7 +1222,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
                         for (int i = lane; i < sh.listed[warp]; i += 32) look_at(sh.list[warp][i]);
                         for (int i = tid; i < (int)sh.others_listed; i += kThreads) look_at(sh.others[i]);
                     }
-                    if (tid == 32 && sh.ending[0].ok) write_logprob(sh.ending[0].at.order, sh.ending[0].total);
+                    if (tid == 32 && sh.ending[0].ok == kYes) write_logprob(sh.ending[0].at.order, sh.ending[0].total);
                     __syncthreads();
                 }
                 if (warp == 0) {  // the search is one warp's
@@ -1107,21 +1231,30 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
                     bool done = false;
                     Found* const f = sh.found;
                     if (stage == kTry) {
-                        done = sh.ending[0].ok;
+                        done = sh.ending[0].ok == kYes;
                         at = sh.ending[0].at;
                         total = sh.ending[0].total;
                         if (!done) {
-                            // all of the histogram, then what lies below it exactly
+                            // all of the histogram; the next one, where the place lies there; what lies below: quickly,
+                            // exactly; all of them from the first on
+                            const bool exact = cmd.op == kRestOf && !cmd.rest;
                             if (cmd.op == kFirst)
                                 next = {kWindow, top, window_low(top), sum, 0, 0, 0};
+                            else if (sh.ending[0].ok == kAbove && !exact)
+                                next = {kWindow, top, window_low(top), 1, 0, 0, 0};
+                            else if (sh.ending[0].ok == kBelow && !exact)
+                                next = {kWindow, below, window_low(below), 1, 0, 0, 0};
                             else if (cmd.op == kWindow && cmd.rest && more)
+                                next = {kRestOf, top, cmd.low, quick_fits(k), 0, 0, 0};
+                            else if (cmd.op == kRestOf && cmd.rest)
                                 next = {kRestOf, top, cmd.low, 0, 0, 0, 0};
                             else
                                 stage = kCollect;
-                            if (cmd.op == kRestOf || !more) whole = w.sum + rest;
+                            if (exact || !more) whole = w.sum + rest;
+                            if (stage == kCollect && w.before) next = {kWindow, top, window_low(top), 0, 0, 0, 0};
                         }
                     }
-                    if (stage >= kCollect) {
+                    if (stage >= kCollect && next.op == kDone) {
                         // Window by window, to the k-th token or as far as the row's weight, which is exact now, says
                         // that a limit or the drawn token lies.  Then the places of top-p, min-p and the drawn token,
                         // each in the window that holds it.
@@ -1224,8 +1357,9 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
                     if (next.op == kWindow) {
                         sh.trying = stage == kTry;
                         const int v = stage == kTry ? 0 : stage == kCollect ? windows : win;
-                        sh.before_count = v ? sh.win_count[v] : 0;
-                        sh.before_sum = v ? sh.win_sum[v] : 0;
+                        const bool on = stage == kTry && next.high != top;
+                        sh.before_count = on ? sh.window.count : v ? sh.win_count[v] : 0;
+                        sh.before_sum = on ? sh.window.sum : v ? sh.win_sum[v] : 0;
                     }
                 }
                 __syncwarp();
@@ -1239,6 +1373,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
         cmd = sh.cmd;
         if (cmd.op == kDone) return;
     }
+    if (rank == 0 && tid == 0) a.token[row] = -1;
 }
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }

@@ -142,6 +142,21 @@ def test_min_p_whose_place_lies_far_down():
             check(x, u, t, min_p=np.full(40, m), top_k=np.full(40, 3000))
 
 
+@pytest.mark.parametrize("vocab", [700, 20011, 90001])
+def test_limits_and_draws_in_lower_windows(vocab):
+    # flat rows: the limit, the drawn token or both lie one window or more below the first, some rows end in the second
+    r = np.random.default_rng(vocab)
+    for x in (r.standard_normal((24, vocab)) * 2.5, r.standard_normal((24, vocab)) * 0.4, r.uniform(0, 12, (24, vocab)),
+              np.abs(r.standard_normal((24, vocab))) * 2.0 ** -r.integers(0, 12, (24, vocab))):
+        x = x.astype(np.float16)
+        u = r.uniform(0, 1, 24)
+        u[:4] = 0.999, 0.99999, 0.0, 1.0
+        t = r.uniform(0.7, 4, 24)
+        check(x, u, t)
+        check(x, u, t, top_p=r.uniform(0.9, 1, 24))
+        check(x, u, t, top_p=r.uniform(0, 1, 24), min_p=r.choice([0.0, 1e-4], 24))
+
+
 def test_odd_strides_and_another_stream():
     r, x = logits(80, 6, 1003)
     u = r.uniform(0, 1, 6)
