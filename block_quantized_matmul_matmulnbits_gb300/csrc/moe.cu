@@ -3,24 +3,31 @@
 //
 //   router   logits x . r_e, one CTA an expert and four tokens.  Which expert comes first decides the
 //            output, so the sums are held in two FP32 words each (products of FP16 are exact).
-//   choose   one CTA: a warp picks a token's experts; the list of (expert, some of its tokens).
-//   up       units of 32 features of one item, a CTA each; a warp takes 16 gate and 16 up rows by a quarter
-//            of the inputs.
+//   choose   one CTA: a warp picks a token's experts; the list of (expert, some of its tokens).  (Worked out
+//            by every CTA of the next kernel instead: 87 us for 80 in the case below, 24 for 23 with one token.)
+//   up       units of 32 features of one item, a CTA each; a warp takes 16 gate and 16 up rows by a half or a
+//            quarter of the inputs.
 //   down     a cluster takes 32 outputs over all items, so the sum over experts stays in it.
 //
 // Every warp streams its own weights and inputs into a ring of steps in shared memory (cp.async: prefetched in
 // registers, 16 warps an SM waited for loads half of the time, since a short load's scoreboard is the
-// long ones' too).  A step is four blocks of 32 inputs by two tiles of 16 rows, two steps a ring: what bounds these
-// kernels is the instructions between memory and MMA, so many warps count for more than deep rings (gate and up of
-// 16 tokens: 24 warps an SM with two steps of 32 rows @T1@ us, 8 with three of 64 48).
-// A lane takes 16 bytes of codes a row: a quad's lanes hold the four blocks.
-// A lane takes the zero point of its own
-// block off (exact in FP16) and the rows go to the MMA (m16n8k16) as its left operand.
-// A step's columns are two tokens by the quad's four blocks: the right operand is zero
-// but where a column's block is the lane's own, so each column sums one block of one
-// token, exact codes times FP16 inputs in FP32, and the block's scale multiplies its sum in FP32.
-// No code is rounded and no sum over K is needed for the zero points.  Two tokens a
-// step use a quarter of the MMA's work; an expert of a few tokens' step has one or two.
+// long ones' too).  A step is four blocks of 32 inputs by two tiles of 16 rows.  Where an expert has one or two
+// tokens, the chain from a step's copy over its codes to the MMAs is as long as the copy, so many warps count for
+// more than deep rings.  16 tokens, 8 of 64 experts, 2048 inputs, 1024 wide, 4 bits: 78 us in CTAs of 4 warps, 16
+// an SM with two steps each; CTAs of 2 warps 82, of 16 99; 12 warps with three steps 2 % more.
+//
+// A lane takes 16 bytes of codes a row: a quad's lanes hold the four blocks.  It takes the zero point of its own
+// block off (exact in FP16) and the rows go to the MMA (m16n8k16) as its left operand.  A step's columns are two
+// tokens by the quad's four blocks: the right operand is zero but where a column's block is the lane's own, so each
+// column sums one block of one token, exact codes times FP16 inputs in FP32, and the block's scale multiplies its
+// sum in FP32.  No code is rounded and no sum over K is needed for the zero points (with such sums, and codes as FP16
+// values without an exponent, there are a tenth fewer instructions, but 85 us, and a weight of zero gives zero to
+// FP32's rounding only).  Two tokens a step use a quarter of the MMA's work; an expert of a few tokens' step has one or two.
+//
+// What bounds it.  5 tokens, 2 of 8 experts, 4096 by 14336, 8 bits: 242 us for 1.14 GB (4.7 TB/s; gate and up alone
+// 5.8), memory and the ends of three waits.  The layer above reads 211 MB in 80 us: router 5, choice 5, gate and up 42
+// (3.6 TB/s), down 26; half of the issue slots are taken, of the stalls a third are fixed latencies, the others
+// full pipes and copies.  With one token 21 us: the four kernels' chains, 2, 4, 8 and 7 us.
 //
 // The inputs lie in the workspace as the MMA takes them (router and up kernel write them so): 256 bytes
 // a step, first the quad's first quarter blocks and so on, each in the order of the codes, a
@@ -314,9 +321,11 @@ template <int N>
 __device__ __forceinline__ void copies_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-// A warp's shared memory: RING steps of codes (two tiles of 16 rows by four blocks, 64 bytes of each of 8 rows behind one
-// another; the second 64 of 8-bit codes 16 further, so that a quad's reads of a block each meet no bank twice), inputs (256 bytes a token) and the tokens' factors [4]; then RING buffers of scales [32][16] and zero
-// points [32][16], four steps each (fewer where a warp's share of a row ends): 8 and 4 bytes of each row a step would take as long as its codes, a tag look-up a row.
+// A warp's shared memory: RING steps of codes (two tiles of 16 rows by four blocks, 64 bytes of each of 8 rows behind
+// one another; the second 64 of 8-bit codes 16 further, so that a quad's reads of a block each meet no bank twice),
+// inputs (256 bytes a token) and the tokens' factors [4]; then RING buffers of scales [32][16] and zero points [32][16],
+// four steps each (fewer where a warp's share of a row ends): 8 and 4 bytes of each row a step would take as long as
+// its codes, a tag look-up a row.
 template <int BITS, int NP>
 struct Slot {
     static constexpr int kPiece = BITS == 4 ? 512 : 528, kRows = kPiece * (BITS / 4);  // 64 bytes of 8 rows; 8 rows
@@ -340,8 +349,8 @@ __device__ __forceinline__ TilePtr tiles_at(const MoeWeight& w, int64_t row, int
             w.z ? w.z + at + (lane & 3) * 4 : nullptr};
 }
 
-// Copies of a step's codes; blocks past the row's end (`left` of them are there) are zeros.  eight: blocks of eight rows; second: from
-// the first tile to the other.
+// Copies of a step's codes; blocks past the row's end (`left` of them are there) are zeros.  eight: blocks of eight rows;
+// second: from the first tile to the other.
 template <int BITS>
 __device__ __forceinline__ void copy_codes(uint32_t slot, TilePtr& p, int eight, int64_t second, int left) {
     using S = Slot<BITS, 1>;
@@ -407,9 +416,9 @@ __device__ __forceinline__ void codes8(uint32_t lo, uint32_t hi, uint32_t c, uin
     o[3] = hsub2_rn(prmt(hi, 0x64646464u, 0x4342u), c);
 }
 
-// Adds a step (the one after `step` others of its four) times 2 P tokens: y[m][p][r] is row 8 r + g of tile m and token 2 p + (lane & 3) / 2, blocks 2 (lane & 1) and
-// the one behind it.  zeros: NP * 512 bytes of zeros, the inputs of lanes that have none: column g = lane / 4 is token
-// g / 4, block g % 4, and only the lanes that hold that block have any.
+// Adds a step (the one after `step` others of its four) times 2 P tokens: y[m][p][r] is row 8 r + g of tile m and token
+// 2 p + (lane & 3) / 2, blocks 2 (lane & 1) and the one behind it.  zeros: NP * 512 bytes of zeros, the inputs of lanes
+// that have none: column g = lane / 4 is token g / 4, block g % 4, and only the lanes that hold that block have any.
 template <int BITS, int NP, int P, bool FACTORS>
 __device__ __forceinline__ void step_of(const uint8_t* slot, const uint8_t* quad, int step, const uint8_t* zeros, bool zp,
                                         float (*y)[NP][2]) {
@@ -822,7 +831,8 @@ cudaError_t down_launch(const MoeArgs* a, int sms, cudaStream_t st) {
     return launch_pdl(kernel, dim3(tiles, 1, parts), dim3(kDownWarps * 32), smem, st, *a, parts);
 }
 
-// The two kernels for items of `item` tokens; without arguments, what has to be set up for them.
+// The two kernels for items of `item` tokens; without arguments, what has to be set up for them.  Warps that share a row's
+// inputs, steps of a ring and CTAs an SM fill the registers and shared memory that so many tokens leave.
 template <int BITS>
 cudaError_t moe_kernels(const MoeArgs* a, int item, int sms, cudaStream_t st) {
     constexpr bool Q4 = BITS == 4;
@@ -843,9 +853,13 @@ cudaError_t moe_launch(MoeArgs& a, int sms, cudaStream_t st) {
     cudaError_t e = launch_pdl(moe_router_kernel, dim3(a.experts + 1, (a.tokens + kRouterTokens - 1) / kRouterTokens),
                                dim3(kRouterThreads), 0, st, a);
     if (e != cudaSuccess) return e;
-    // tokens of an item: two where there are no more; four where an expert gets two on average, since more cost
-    // registers and a rare expert of many is read again from the cache; else eight
-    a.item = a.tokens <= 2 ? 2 : a.tokens * a.top_k <= 2 * a.experts ? 4 : 8;
+    // Tokens of an item: two where there are no more; four where an expert gets few on average, since more cost
+    // registers, and an expert of many is read again from the cache; else eight.  us with items of four and eight:
+    //   4 bits, hidden 2048, inter 1024   2 an expert (64 experts)    78   97;    4 (32)   65   74;    8 (8)   37   41
+    //   4 bits, 4096, 14336               4 an expert (8)            276  282;    8 (8)   468  417;   16 (8)  785  618
+    //   8 bits, 4096, 14336            1.25 an expert (8)            231  256;    4 (8)   373  332;    8 (8)  634  479
+    // and one token with items of two 20, of four 21.
+    a.item = a.tokens <= 2 ? 2 : a.tokens * a.top_k <= (a.bits == 4 ? 4 : 2) * a.experts ? 4 : 8;
     e = launch_pdl(moe_choose_kernel, dim3(1), dim3(kChooseThreads), 0, st, a);
     if (e != cudaSuccess) return e;
     return a.bits == 4 ? moe_kernels<4>(&a, a.item, sms, st) : moe_kernels<8>(&a, a.item, sms, st);

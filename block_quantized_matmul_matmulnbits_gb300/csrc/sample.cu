@@ -4,22 +4,29 @@
 // The tokens of a row are ordered by falling logit, equal ones by rising id; every limit keeps a
 // prefix of that order, and the drawn token is the first whose cumulative weight passes u times
 // the kept weight.  So three places in one order are wanted, each "the first at which a running sum
-// reaches a target", and nothing has to be sorted: FP16 logits have few distinct values,
-// and equal ones weigh the same.  A histogram over the 16-bit order of the logits, from
-// the largest down (the window), gives counts and lowest ids; with one weight a distinct value, taken to
-// 2^-40, the sums are those that 64-bit arithmetic gives.
+// reaches a target", and nothing has to be sorted: FP16 logits have few distinct values, and equal ones weigh
+// the same.  A histogram over the 16-bit order of the logits, from the largest down (a window of it), gives counts;
+// with one weight a distinct value, taken to 2^-40 and held as an integer, sums are those of 64-bit arithmetic,
+// whatever their order.  (FP64 itself runs at two operations a clock and SM.)
 //
-//   look 1   the row's maximum, and how far down the window has to reach: to the n-th largest of
-//            the threads' maxima, so at least n logits are in it (or to the histogram's end)
-//   look 2   the histogram; what lies below the window enters as a sum in FP32 with a bound
-//            of its error.  With a top-k it is not needed.
-// Where the two ends of that bound give the same token, it is the token.  Else the window is widened
-// to all of the histogram's places, and after that the row is gone through window by window to its end,
-// which leaves nothing inexact.  A drawn value that several tokens share takes one more
-// look for the id.
+//   look 1      the row's maximum, its weight in FP32 about a moving reference, and a list of its largest
+//               logits: groups of 24 that hold one above a bound from the first groups' maxima are noted and looked
+//               at again.  The list is the first window; what lies below it is the weight less the list's, with a
+//               bound of its error.  Most rows end here.
+//   window      a histogram of 4096 orders by shared-memory atomics, what lies below in FP32 with a bound
+//   next ones   where the token, or a top-p, lies lower, with the counts and the weight above them known; a token above
+//               the window that the limit lies in is looked for from the first one with the kept weight
+//   rest        where the two ends of the bound leave a doubt: the weight below the window to 2^-26, then to 2^-40,
+//               and with that window by window to the end, which leaves nothing inexact
+// A token is taken where both ends of the bound give it.  A drawn value whose ids the list has not takes one more
+// look for the id.  A cluster of up to eight CTAs takes a row; its first one searches, in its shared memory, where
+// the others' lists are counted with remote atomics (integers: their order does not matter).
 //
-// A cluster of up to eight CTAs takes a row; the histogram is in its first one's shared memory, where the
-// others add with remote atomics (integers: their order does not matter).
+// What bounds it: the chain of a row, not the memory.  512 rows of 151,936 with top-p 0.7 to 0.98 and temperatures
+// 0.6 to 1.2: 121 us (a read of them 23); the first look 25, the search in the list 8 to 14, twice, since the rows' CTAs
+// fill the GPU 1.7 times; 120 rows have a window more, 40 us beside one another, and the call ends with the one that has
+// two or three (179 us where those took the exact rest).  128 rows with mixed limits 51, 300 of 50,257 without any 49,
+// one of 49,152 14, of which the look is 3.
 #include <cuda_fp16.h>
 
 #include "common.cuh"
@@ -147,8 +154,8 @@ __device__ __noinline__ u64 ratio_of(Scale k, int e, int j) {
     return w.n < -61 ? 0 : (w.m << 2) >> -w.n;
 }
 
-// A weight as the sums take it.  Sixteen orders that differ in their last four bits lie u apart: the largest of them (or the row's, if
-// that is one of them) times a ratio.
+// A weight as the sums take it.  Sixteen orders that differ in their last four bits lie u apart: the largest of them (or
+// the row's, if that is one of them) times a ratio.
 __device__ __forceinline__ uint32_t block_of(uint32_t order, uint32_t top) { return min(order | 15u, top); }
 __device__ __forceinline__ u64 weight_in(const Power& base, u64 ratio, int places) {
     const u64 m = __umul64hi(base.m, ratio) << 2;
@@ -1378,10 +1385,10 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-// CTAs of a row: enough for two on every SM (four fit), of at least 4096 logits each; two at least for a long row, which
-// has to be gone through three times or more where its limits lie far down, and is what the call then ends with (512 rows of
-// 151,936 with top-p 0.7 to 0.98 and temperatures 0.6 to 1.2: 191 us with two, 285 with one; with none but likely
-// tokens kept 70 and 56).
+// CTAs of a row: enough for two on every SM (four fit), of at least 4096 logits each (128 rows of 151,936 with mixed limits:
+// 52 us, enough for one 67, for three 52); two at least for a long row, which has to be gone through again where its
+// limits lie far down, and is what the call then ends with (512 rows of 151,936 with top-p: 122 us with two, 160 with
+// one, 141 with four; with none but likely tokens kept 58, 48 and 78).
 int cluster_for(int64_t rows, int64_t vocab, int sms) {
     int c = vocab > 1 << 17 ? 2 : 1;
     while (c < kMaxCluster && rows * c < (int64_t)sms * 2 && vocab >= (int64_t)c * 2 * 4096) c *= 2;

@@ -567,7 +567,7 @@ typedef struct {
 
 /* The layer for a few tokens (a decode step): the weights of each expert that some token takes
  * are read from memory once, and once more from the cache for every 2, 4 or 8 of its tokens
- * (with up to 2 tokens, up to two an expert on average, more).
+ * (where there are at most 2; where an expert gets few on average; else).
  *   X        fp16 [M, hidden], M at most MNB_MOE_MAX_TOKENS
  *   Y        fp16 [M, hidden]; not X
  *   ids      int32 [M, top_k] or NULL: the experts taken, by falling logit
