@@ -13,7 +13,7 @@
 // fraction of a turn, and position times that, modulo 2^64, is the angle's turn: one integer
 // product, exact to 2^-32 turns at the largest position.
 //
-// What bounds it: 10,780 tokens of 32 + 8 heads of 128 with norms take 53.4 us, 4.1 TB/s of reads and writes (the rate of
+// What bounds it: 10,778 tokens of 32 + 8 heads of 128 with norms take 53.4 us, 4.1 TB/s of reads and writes (the rate of
 // a copy gives 33); two thirds of the issue slots are taken, conversions and shuffles beside the arithmetic, which is
 // packed for that reason (73 to 65 us).  The tables are read without conflicts of banks (65 to 54).  127 tokens take
 // 4.6 us, one of 9 + 3 heads of 64 2.2, the chain from the lengths over the angle to the stores.
