@@ -95,7 +95,7 @@ __device__ __forceinline__ int position_of(const RopeArgs& a, int t0, int n) {
     return pos;
 }
 
-template <int D, bool NORM>
+template <int D, bool NORM, bool INTER>
 __global__ void __launch_bounds__(kThreads, 6) qk_rope_kernel(const RopeArgs a) {
     constexpr int LPH = D / 8, STEP = kThreads / LPH;  // threads of a head, heads of a pass
     // Cosine and sine of a token's pairs, and the weights of queries and of keys.  The i-th value of all threads of a
@@ -112,17 +112,23 @@ __global__ void __launch_bounds__(kThreads, 6) qk_rope_kernel(const RopeArgs a) 
 
     // passes of STEP heads, a token's behind the other's; their pieces are on their way kRing ahead
     const int per = (a.heads + STEP - 1) / STEP, passes = nt * per;
+    // Where a thread's piece of head 0 of a token lies, and of the key head that head would be were it a key.
+    struct Rows {
+        const char *q, *k;
+    };
+    auto rows = [&](const __half* q, int64_t qs, const __half* k, int64_t ks) {
+        return Rows{reinterpret_cast<const char*>(q + (int64_t)t0 * qs + j * 8),
+                    reinterpret_cast<const char*>(k + (int64_t)t0 * ks + j * 8) - a.q_heads * (D * 2)};
+    };
     uint4 x[kRing];
-    int lt = 0, lh = h0;  // what is loaded next
+    Rows from = rows(a.q, a.q_stride, a.k, a.k_stride), to = rows(a.q_out, a.q_out_stride, a.k_out, a.k_out_stride);
+    int left = passes, lh = h0;  // what is loaded next
     auto fetch = [&](uint4& v) {
-        if (lt < nt && lh < a.heads) {
-            const int t = t0 + lt;
-            v = *reinterpret_cast<const uint4*>((lh < a.q_heads ? a.q + (int64_t)t * a.q_stride + lh * D
-                                                                : a.k + (int64_t)t * a.k_stride + (lh - a.q_heads) * D) +
-                                                j * 8);
-        }
+        if (left > 0 && lh < a.heads)
+            v = *reinterpret_cast<const uint4*>((lh < a.q_heads ? from.q : from.k) + lh * (D * 2));
+        --left;
         lh += STEP;
-        if (lh >= h0 + per * STEP) lh = h0, ++lt;
+        if (lh >= h0 + per * STEP) lh = h0, from.q += a.q_stride * 2, from.k += a.k_stride * 2;
     };
 #pragma unroll
     for (int i = 0; i < kRing; ++i) {
@@ -146,14 +152,14 @@ __global__ void __launch_bounds__(kThreads, 6) qk_rope_kernel(const RopeArgs a) 
         const int r = (int)(((unsigned long long)(unsigned)position[t] * step[p]) >> 32);
         float s, c;
         sincospif((float)r * 4.656612873077392578125e-10f, &s, &c);  // r 2^-31: half turns
-        turn[t][a.interleaved ? (p & 3) * (half >> 2) + (p >> 2) : (p & 7) * lanes + (p >> 3)] = make_float2(c, s);
+        turn[t][INTER ? (p & 3) * (half >> 2) + (p >> 2) : (p & 7) * lanes + (p >> 3)] = make_float2(c, s);
     }
     __syncthreads();
 
-    const bool turned = j * 8 < a.rotary, second = !a.interleaved && j >= lanes;
+    const bool turned = j * 8 < a.rotary, second = !INTER && j >= lanes;
     // the thread that holds the other values of this one's pairs
-    const int other = (tid & 31) + (a.interleaved || !turned ? 0 : second ? -lanes : lanes);
-    const int pair0 = second ? j - lanes : j, pairs = a.interleaved ? half >> 2 : lanes;
+    const int other = (tid & 31) + (INTER || !turned ? 0 : second ? -lanes : lanes);
+    const int pair0 = second ? j - lanes : j, pairs = INTER ? half >> 2 : lanes;
     const int oj = j + other - (tid & 31);
     u64 c2[4], s2[4];  // what two values and their other ones are multiplied with, weights included
     int have = -1;     // for which token and kind of head
@@ -172,13 +178,13 @@ __global__ void __launch_bounds__(kThreads, 6) qk_rope_kernel(const RopeArgs a) 
                     c[i] = 1.f;
                     s[i] = 0.f;
                     if (turned) {
-                        const float2 cs = turn[t][pair0 + (a.interleaved ? i >> 1 : i) * pairs];
+                        const float2 cs = turn[t][pair0 + (INTER ? i >> 1 : i) * pairs];
                         c[i] = cs.x;
-                        s[i] = (a.interleaved ? (i & 1) : second) ? cs.y : -cs.y;
+                        s[i] = (INTER ? (i & 1) : second) ? cs.y : -cs.y;
                     }
                     if (NORM) {
                         c[i] *= gain[key][i * LPH + j];
-                        if (turned) s[i] *= gain[key][a.interleaved ? (i ^ 1) * LPH + j : i * LPH + oj];
+                        if (turned) s[i] *= gain[key][INTER ? (i ^ 1) * LPH + j : i * LPH + oj];
                     }
                 }
 #pragma unroll
@@ -188,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, 6) qk_rope_kernel(const RopeArgs a) 
                 }
             }
             uint4 y;  // the other values of the pairs
-            if (a.interleaved) {
+            if (INTER) {
                 y = make_uint4(prmt(x[u].x, 0, 0x1032), prmt(x[u].y, 0, 0x1032), prmt(x[u].z, 0, 0x1032),
                                prmt(x[u].w, 0, 0x1032));
             } else {
@@ -224,15 +230,12 @@ __global__ void __launch_bounds__(kThreads, 6) qk_rope_kernel(const RopeArgs a) 
                 const __half2 p = __floats2half2_rn(f.x, f.y);
                 out[i] = *reinterpret_cast<const uint32_t*>(&p);
             }
-            if (h < a.heads && pos >= 0) {
-                const int64_t row = t0 + t;
-                __half* to = key ? a.k_out + row * a.k_out_stride + (h - a.q_heads) * D
-                                 : a.q_out + row * a.q_out_stride + h * D;
-                *reinterpret_cast<uint4*>(to + j * 8) = make_uint4(out[0], out[1], out[2], out[3]);
-            }
+            if (h < a.heads && pos >= 0)
+                *reinterpret_cast<uint4*>(const_cast<char*>(key ? to.k : to.q) + h * (D * 2)) =
+                    make_uint4(out[0], out[1], out[2], out[3]);
             fetch(x[u]);
             h += STEP;
-            if (h >= h0 + per * STEP) h = h0, ++t;
+            if (h >= h0 + per * STEP) h = h0, ++t, to.q += a.q_out_stride * 2, to.k += a.k_out_stride * 2;
         }
     }
 }
@@ -308,8 +311,10 @@ extern "C" int mnb_qk_rope(const mnb_rope* rope, const mnb_kv_batch* batch, cons
     a.chunk = a.chunk < 1 ? 1 : a.chunk > kChunk ? kChunk : a.chunk;
     const dim3 grid((unsigned)((tokens + a.chunk - 1) / a.chunk)), block(kThreads);
     const bool norm = a.q_weight || a.k_weight;
-    const auto kernel = dim == 64 ? (norm ? qk_rope_kernel<64, true> : qk_rope_kernel<64, false>)
-                                  : (norm ? qk_rope_kernel<128, true> : qk_rope_kernel<128, false>);
+    const auto kernel = a.interleaved ? (dim == 64 ? (norm ? qk_rope_kernel<64, true, true> : qk_rope_kernel<64, false, true>)
+                                                   : (norm ? qk_rope_kernel<128, true, true> : qk_rope_kernel<128, false, true>))
+                                      : (dim == 64 ? (norm ? qk_rope_kernel<64, true, false> : qk_rope_kernel<64, false, false>)
+                                                   : (norm ? qk_rope_kernel<128, true, false> : qk_rope_kernel<128, false, false>));
     return launch_pdl(kernel, grid, block, 0, reinterpret_cast<cudaStream_t>(stream), a) == cudaSuccess ? MNB_OK
                                                                                                         : MNB_ERR_CUDA;
 }
