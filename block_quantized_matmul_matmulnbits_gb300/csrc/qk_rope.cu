@@ -95,7 +95,7 @@ __device__ __forceinline__ int position_of(const RopeArgs& a, int t0, int n) {
     return pos;
 }
 
-template <int D, bool NORM, bool INTER>
+template <int D, bool NORM, bool INTER, bool WHOLE>
 __global__ void __launch_bounds__(kThreads, 6) qk_rope_kernel(const RopeArgs a) {
     constexpr int LPH = D / 8, STEP = kThreads / LPH;  // threads of a head, heads of a pass
     // Cosine and sine of a token's pairs, and the weights of queries and of keys.  The i-th value of all threads of a
@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(kThreads, 6) qk_rope_kernel(const RopeArgs a) 
     __shared__ float gain[2][D];
     __shared__ int position[kChunk];
     const int tid = threadIdx.x, warp = tid >> 5, j = tid % LPH, h0 = tid / LPH;
-    const int half = a.rotary >> 1, lanes = a.rotary >> 4;  // pairs; threads of half of the turned values
+    const int half = WHOLE ? D / 2 : a.rotary >> 1, lanes = WHOLE ? D / 16 : a.rotary >> 4;  // pairs; threads of half of the turned values
     const int t0 = blockIdx.x * a.chunk, nt = min(a.chunk, a.tokens - t0);
     pdl_wait();
     pdl_launch_dependents();
@@ -156,22 +156,26 @@ __global__ void __launch_bounds__(kThreads, 6) qk_rope_kernel(const RopeArgs a) 
     }
     __syncthreads();
 
-    const bool turned = j * 8 < a.rotary, second = !INTER && j >= lanes;
+    const bool turned = WHOLE || j * 8 < a.rotary, second = !INTER && j >= lanes;
     // the thread that holds the other values of this one's pairs
     const int other = (tid & 31) + (INTER || !turned ? 0 : second ? -lanes : lanes);
     const int pair0 = second ? j - lanes : j, pairs = INTER ? half >> 2 : lanes;
     const int oj = j + other - (tid & 31);
     u64 c2[4], s2[4];  // what two values and their other ones are multiplied with, weights included
     int have = -1;     // for which token and kind of head
+    bool there = false, normed = false;
+    char* out_row = nullptr;
     int t = 0, h = h0;
     for (int q = 0; q < passes; q += kRing) {
 #pragma unroll
         for (int u = 0; u < kRing; ++u) {
             if (q + u >= passes) break;
-            const int pos = position[t];
-            const bool key = h >= a.q_heads, normed = NORM && (key ? a.k_weight != nullptr : a.q_weight != nullptr);
+            const bool key = h >= a.q_heads;
             if (have != 2 * t + key) {
                 have = 2 * t + key;
+                there = position[t] >= 0;
+                normed = NORM && (key ? a.k_weight != nullptr : a.q_weight != nullptr);
+                out_row = const_cast<char*>(key ? to.k : to.q);
                 float c[8], s[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
@@ -203,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, 6) qk_rope_kernel(const RopeArgs a) 
                 y.z = __shfl_sync(0xffffffffu, x[u].z, other);
                 y.w = __shfl_sync(0xffffffffu, x[u].w, other);
             }
-            if (!turned) y = make_uint4(0, 0, 0, 0);  // not an infinity times 0
+            if (!WHOLE && !turned) y = make_uint4(0, 0, 0, 0);  // not an infinity times 0
             u64 v[4];
             const __half2* xp = reinterpret_cast<const __half2*>(&x[u]);
             const __half2* yp = reinterpret_cast<const __half2*>(&y);
@@ -230,14 +234,26 @@ __global__ void __launch_bounds__(kThreads, 6) qk_rope_kernel(const RopeArgs a) 
                 const __half2 p = __floats2half2_rn(f.x, f.y);
                 out[i] = *reinterpret_cast<const uint32_t*>(&p);
             }
-            if (h < a.heads && pos >= 0)
-                *reinterpret_cast<uint4*>(const_cast<char*>(key ? to.k : to.q) + h * (D * 2)) =
-                    make_uint4(out[0], out[1], out[2], out[3]);
+            if (h < a.heads && there)
+                *reinterpret_cast<uint4*>(out_row + h * (D * 2)) = make_uint4(out[0], out[1], out[2], out[3]);
             fetch(x[u]);
             h += STEP;
             if (h >= h0 + per * STEP) h = h0, ++t, to.q += a.q_out_stride * 2, to.k += a.k_out_stride * 2;
         }
     }
+}
+
+using RopeKernel = void (*)(RopeArgs);
+
+template <int D, bool NORM>
+RopeKernel rope_kernel(bool interleaved, bool whole) {
+    return interleaved ? (whole ? qk_rope_kernel<D, NORM, true, true> : qk_rope_kernel<D, NORM, true, false>)
+                       : (whole ? qk_rope_kernel<D, NORM, false, true> : qk_rope_kernel<D, NORM, false, false>);
+}
+
+RopeKernel rope_kernel(int dim, bool norm, bool interleaved, bool whole) {
+    return dim == 64 ? (norm ? rope_kernel<64, true>(interleaved, whole) : rope_kernel<64, false>(interleaved, whole))
+                     : (norm ? rope_kernel<128, true>(interleaved, whole) : rope_kernel<128, false>(interleaved, whole));
 }
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -311,10 +327,7 @@ extern "C" int mnb_qk_rope(const mnb_rope* rope, const mnb_kv_batch* batch, cons
     a.chunk = a.chunk < 1 ? 1 : a.chunk > kChunk ? kChunk : a.chunk;
     const dim3 grid((unsigned)((tokens + a.chunk - 1) / a.chunk)), block(kThreads);
     const bool norm = a.q_weight || a.k_weight;
-    const auto kernel = a.interleaved ? (dim == 64 ? (norm ? qk_rope_kernel<64, true, true> : qk_rope_kernel<64, false, true>)
-                                                   : (norm ? qk_rope_kernel<128, true, true> : qk_rope_kernel<128, false, true>))
-                                      : (dim == 64 ? (norm ? qk_rope_kernel<64, true, false> : qk_rope_kernel<64, false, false>)
-                                                   : (norm ? qk_rope_kernel<128, true, false> : qk_rope_kernel<128, false, false>));
+    const auto kernel = rope_kernel(dim, norm, a.interleaved != 0, a.rotary == dim);
     return launch_pdl(kernel, grid, block, 0, reinterpret_cast<cudaStream_t>(stream), a) == cudaSuccess ? MNB_OK
                                                                                                         : MNB_ERR_CUDA;
 }
