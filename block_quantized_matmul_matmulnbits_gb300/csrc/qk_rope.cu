@@ -13,10 +13,11 @@
 // fraction of a turn, and position times that, modulo 2^64, is the angle's turn: one integer
 // product, exact to 2^-32 turns at the largest position.
 //
-// What bounds it: 10,778 tokens of 32 + 8 heads of 128 with norms take 53.4 us, 4.1 TB/s of reads and writes (the rate of
-// a copy gives 33); two thirds of the issue slots are taken, conversions and shuffles beside the arithmetic, which is
-// packed for that reason (73 to 65 us).  The tables are read without conflicts of banks (65 to 54).  127 tokens take
-// 4.6 us, one of 9 + 3 heads of 64 2.2, the chain from the lengths over the angle to the stores.
+// What bounds it: 10,778 tokens of 32 + 8 heads of 128 with norms take 42.5 us, 5.2 TB/s of reads and writes (the rate of
+// a copy gives 33); 63 % of the issue slots are taken, conversions and shuffles beside the arithmetic, which is
+// packed for that reason (73 to 65 us).  The tables are read without conflicts of banks (65 to 53); what a call's heads have
+// in common is fixed when the kernel is compiled and addresses move on by a step (53 to 42.5).  127 tokens take
+// 3.5 us, one of 9 + 3 heads of 64 1.9: the chain from the lengths over the angle to the stores.
 #include <cuda_fp16.h>
 
 #include "common.cuh"
@@ -28,8 +29,8 @@ namespace mnb {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kRing = 4;   // 16-byte pieces a thread has on their way
-constexpr int kChunk = 4;  // tokens of a CTA, at most, which share the frequencies (1: 62 us in the case above, 2: 55, 8: 57)
+constexpr int kRing = 4;   // 16-byte pieces a thread has on their way (3 with seven CTAs an SM: 44 us, 6 with five 44)
+constexpr int kChunk = 4;  // tokens of a CTA, at most, which share the frequencies (1: 47 us in the case above, 2: 44, 8: 47)
 
 struct RopeArgs {
     KvArgs b;                  // q_start, kv_len, seqs, tokens (where positions is NULL)
@@ -95,6 +96,7 @@ __device__ __forceinline__ int position_of(const RopeArgs& a, int t0, int n) {
     return pos;
 }
 
+// NORM: some heads are normed; INTER: neighbours are pairs; WHOLE: all values of a head are turned.
 template <int D, bool NORM, bool INTER, bool WHOLE>
 __global__ void __launch_bounds__(kThreads, 6) qk_rope_kernel(const RopeArgs a) {
     constexpr int LPH = D / 8, STEP = kThreads / LPH;  // threads of a head, heads of a pass
