@@ -603,7 +603,8 @@ int64_t mnb_moe_workspace(const mnb_moe_layer* layer, int64_t M);
  *   top_p        float [rows] or NULL; 1, above and NaN: no limit; the first is always kept
  *   min_p        float [rows] or NULL; 0, below and NaN: no limit; the first is always kept
  *   token        int64 [rows]
- *   logprob      float [rows] or NULL: log of its weight over the sum of the kept
+ *   logprob      float [rows] or NULL: log of its weight over the sum of the kept, to 2^-18 and
+ *                binary32's places
  * All are device arrays, read when the call runs: a captured call can be replayed
  * with other settings.  Logits of -infinity are never drawn; a row of nothing else
  * gives token -1 and logprob -infinity, a row with NaN or +infinity -1 and NaN.
