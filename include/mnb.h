@@ -578,9 +578,10 @@ typedef struct {
  * differ by 2^-40 of their terms; the expert sums are in binary32 with exact codes, the
  * products silu(gate) * up enter the down projection in fp16 scaled by a power of two
  * per 32.  A token with NaN or infinity takes some valid experts and gives NaN or
- * infinity; it does not touch the others.  Deterministic for given arguments.  Errors: MNB_ERR_ARG (also a workspace that is too small),
- * MNB_ERR_UNSUPPORTED (sizes beyond the above, bits, M), MNB_ERR_ALIGN (16 bytes; zero
- * points, ids and weights 4), MNB_ERR_NO_DEVICE, MNB_ERR_CUDA. */
+ * infinity; it does not touch the others.  Deterministic for given arguments.
+ * Errors: MNB_ERR_ARG (also a workspace that is too small), MNB_ERR_UNSUPPORTED (sizes
+ * beyond the above, bits, M), MNB_ERR_ALIGN (16 bytes; zero points, ids and weights 4),
+ * MNB_ERR_NO_DEVICE, MNB_ERR_CUDA. */
 int mnb_moe(const mnb_moe_layer* layer, const void* X, int64_t M, void* Y, int32_t* ids, float* weights, void* ws,
             int64_t ws_bytes, void* stream);
 
@@ -603,8 +604,8 @@ int64_t mnb_moe_workspace(const mnb_moe_layer* layer, int64_t M);
  *   top_p        float [rows] or NULL; 1, above and NaN: no limit; the first is always kept
  *   min_p        float [rows] or NULL; 0, below and NaN: no limit; the first is always kept
  *   token        int64 [rows]
- *   logprob      float [rows] or NULL: log of its weight over the sum of the kept, to 2^-18 and
- *                binary32's places
+ *   logprob      float [rows] or NULL: log of its weight over the sum of the kept, to 2^-16
+ *                at most, far less as a rule
  * All are device arrays, read when the call runs: a captured call can be replayed
  * with other settings.  Logits of -infinity are never drawn; a row of nothing else
  * gives token -1 and logprob -infinity, a row with NaN or +infinity -1 and NaN.
