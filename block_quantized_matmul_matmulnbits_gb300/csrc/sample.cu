@@ -277,6 +277,14 @@ struct Ending {     // what one end of the bound gives
     Found at;       // the drawn place
 };
 
+// What a row asks for.
+struct Wish {
+    int k;     // kAll: no limit
+    float p;   // 1: no top-p
+    float m;   // 0: no min-p
+    float u;   // 1: the last
+};
+
 struct __align__(16) SampleShared {
     uint32_t count[kBins];
     uint2 list[kWarps][kEach];          // the warps' largest logits: order and id
@@ -296,7 +304,8 @@ struct __align__(16) SampleShared {
     uint32_t ties[kMaxCluster * kWarps];
     uint32_t warp_word[kWarps];
     Command cmd, next;
-    Scale scale;                        // what the search works with
+    Scale scale;                        // what the search works with: here, since what a thread keeps on its stack would
+    Wish wish;                          // come back from L2 word by word
     Ratios ratios;
     u64 roots[65];
     Window window;
@@ -446,7 +455,7 @@ __device__ __forceinline__ uint32_t block_max(SampleShared& sh, uint32_t v) {
 // returns the largest order below, a thread's, and adds the weight there to *weight.  The orders and what is
 // masked for the sum are worked out two logits at a time.
 template <bool REST, bool APART>
-__device__ __forceinline__ uint32_t count_window(const Slice& s, const Scale& k, uint32_t high, uint32_t low,
+__device__ __forceinline__ uint32_t count_window(const Slice& s, const Scale k, uint32_t high, uint32_t low,
                                                  uint32_t counts, u64* weight) {
     const __half low_h = __ushort_as_half((unsigned short)unorder16(low));
     const __half2 low2 = __halves2half2(low_h, low_h);
@@ -509,7 +518,7 @@ __device__ __forceinline__ int quick_places(int places) { return places <= 48 ? 
 // integer, and its product with 2^(r / 64) - 1, which is below 2^-7 and so is right to 2^-29 in FP32.  c is in two words, the
 // products with the upper one (12 bits) exact: r is off by the lower one's last place times 2^14 (2^-22 for the logit, as
 // much for the largest: 2^-27.5 of the weight) and by three roundings.
-__device__ __forceinline__ u64 quick_rest(const Slice& s, const Scale& k, uint32_t low) {
+__device__ __forceinline__ u64 quick_rest(const Slice& s, const Scale k, uint32_t low) {
     const __half low_h = __ushort_as_half((unsigned short)unorder16(low));
     const __half2 low2 = __halves2half2(low_h, low_h);
     const float c64 = k.c * 64.f, ch = __uint_as_float(__float_as_uint(c64) & 0xFFFFF000u);
@@ -569,7 +578,7 @@ __device__ __forceinline__ u64 quick_rest(const Slice& s, const Scale& k, uint32
 }
 
 // The weight of the CTA's logits below `low`, a thread's, each to 2^-40 of it.
-__device__ __forceinline__ u64 exact_rest(const Slice& s, const Scale& k, uint32_t low) {
+__device__ __forceinline__ u64 exact_rest(const Slice& s, const Scale k, uint32_t low) {
     const __half low_h = __ushort_as_half((unsigned short)unorder16(low));
     const __half2 low2 = __halves2half2(low_h, low_h);
     u64 sum = 0;
@@ -674,7 +683,7 @@ __device__ __noinline__ void find(const SampleShared& sh, int how, int n, u64 s,
     int ni = c;
     u64 si = c * weight;
 #pragma unroll 1
-    for (int d = 1; d < 16; d <<= 1) {
+    for (int d = 1; d < w.own; d <<= 1) {
         const int pn = __shfl_up_sync(kFull, ni, d);
         const u64 ps = __shfl_up_sync(kFull, si, d);
         if (lane >= d) ni += pn, si += ps;
@@ -687,7 +696,8 @@ __device__ __noinline__ void find(const SampleShared& sh, int how, int n, u64 s,
         const u64 from_s = si - c * weight;
         // with a target by weight the bin has one, or the target is 0
         int m = n - from_n;
-        if (how != kByCount) m = weight ? (int)((s - from_s + (how == kReach ? weight - 1 : weight)) / weight) : 1;
+        if (c == 1) m = 1;  // (as a rule: no division)
+        else if (how != kByCount) m = weight ? (int)((s - from_s + (how == kReach ? weight - 1 : weight)) / weight) : 1;
         m = max(m, 1);
         *out = {from_n + m, w.high - (uint32_t)i, m - 1, from_s + m * weight};
     }
@@ -700,6 +710,15 @@ __device__ __noinline__ bool find_min(const SampleShared& sh, float m, Found* ou
     const Window w = sh.window;
     const int lane = threadIdx.x & 31, bins = (int)(w.high - w.low) + 1;
     int lo = 0, hi = bins;  // the first bin that is not kept lies in [lo, hi]
+    {
+        // most likely it is among the 32 about the logit where the weight in FP32 is m
+        const float x = fminf(fmaxf(__fadd_rn(sh.scale.top, __fdividef(log2f(m), sh.scale.c)), -65504.f), 65504.f);
+        const int first = (int)w.high - (int)order16(__half_as_ushort(__float2half_rn(x))) - 16, i = first + lane;
+        const unsigned kept = __ballot_sync(kFull, i < 0 || (i < bins && at_least(sh.scale, w.high - i, m)));
+        const int n = __popc(kept);  // the kept ones come first
+        if (n > 0) lo = min(max(first + n, 0), bins);
+        if (n < 32) hi = min(max(first + n, 0), bins);
+    }
     while (lo < hi) {
         const int step = (hi - lo + 31) >> 5, i = lo + lane * step;
         const unsigned kept = __ballot_sync(kFull, i < hi && at_least(sh.scale, w.high - i, m));
@@ -729,14 +748,6 @@ __device__ __noinline__ bool find_min(const SampleShared& sh, float m, Found* ou
     return lo == bins;
 }
 
-// What a row asks for.
-struct Wish {
-    int k;     // kAll: no limit
-    float p;   // 1: no top-p
-    float m;   // 0: no min-p
-    float u;   // 1: the last
-};
-
 __device__ __forceinline__ void find_top_p(const SampleShared& sh, float p, u64 sum, Found* out) {
     const u64 s = times(p, sum, true);
     find(sh, s ? kReach : kByCount, 1, s, out);  // the first is always kept
@@ -745,10 +756,11 @@ __device__ __forceinline__ void find_top_p(const SampleShared& sh, float p, u64 
 // What the window gives, `below` being the weight that lies under it (more: anything does); the upper or the lower end of a
 // bound.  Where a row has no limit but a top-p that lies below the window, its kept weight is the limit's and at most one of the
 // tokens down there more, which leaves few draws in doubt.  One warp, with two places of its own.
-__device__ __noinline__ void decide(SampleShared& sh, const Wish& wish, bool more, bool upper, u64 below, Found* f,
+__device__ __noinline__ void decide(SampleShared& sh, bool more, bool upper, u64 below, Found* f,
                                     Ending* out) {
     const int lane = threadIdx.x & 31;
     const int count = sh.window.count;
+    const Wish wish = sh.wish;
     if (lane == 0) out->ok = kNo;
     int kept = kAll;  // tokens kept, kAll: all of the row
     u64 total = sh.window.sum + below;
@@ -992,7 +1004,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
     Command cmd = {kFirst, top, low, 0, 0, 0, 0};
     if (low > top) cmd = {kWindow, top, window_low(top), sum, 0, 0, 0};  // a list is not whole
 
-    if (tid == 0) sh.before_count = 0, sh.before_sum = 0, sh.trying = 1, sh.sames = 0, sh.drawn.n = 0, sh.fixed[0] = 0, sh.scale = k;
+    if (tid == 0) sh.before_count = 0, sh.before_sum = 0, sh.trying = 1, sh.sames = 0, sh.drawn.n = 0, sh.fixed[0] = 0, sh.scale = k, sh.wish = wish;
     __syncthreads();
 
     // first CTA, first warp: where the search is
@@ -1020,8 +1032,8 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
 
     auto write_logprob = [&](uint32_t order, u64 total) {
         if (!a.logprob) return;
-        const float2 t = power_of(k, value_of(order));
-        a.logprob[row] = fminf((float)((((double)t.x + (double)t.y) - log2_of(k.roots, total, k.places)) * 0.69314718055994530942), 0.f);
+        const float2 t = power_of(sh.scale, value_of(order));
+        a.logprob[row] = fminf((float)((((double)t.x + (double)t.y) - log2_of(sh.scale.roots, total, sh.scale.places)) * 0.69314718055994530942), 0.f);
     };
 
     // The tries go down window by window, from the top once more at most, and to the end from the top once and back: it
@@ -1043,10 +1055,10 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
             if (sum) {
                 // r and c top are rounded alike; what top's product leaves over is taken off
                 const float2 z = unpair(look.z);
-                const float c = fminf(k.c, 1e30f), tc = __fmul_rn(k.top, c);
-                const float tl = k.c < 1e30f ? __fmaf_rn(k.top, c, -tc) : 0.f;
+                const float c = fminf(sh.scale.c, 1e30f), tc = __fmul_rn(sh.scale.top, c);
+                const float tl = sh.scale.c < 1e30f ? __fmaf_rn(sh.scale.top, c, -tc) : 0.f;
                 const float f = (z.x + z.y) * ex2f(fmaxf(look.r - tc, -1000.f) - tl);
-                send_rest(__float2ull_rn(f * __uint_as_float((uint32_t)(k.places + 127) << 23)), kLowest);
+                send_rest(__float2ull_rn(f * __uint_as_float((uint32_t)(sh.scale.places + 127) << 23)), kLowest);
             }
         } else if (cmd.op == kWindow) {
             clear((int)(cmd.high - cmd.low) + 1);
@@ -1054,15 +1066,15 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
             u64 exact = 0;
             uint32_t under;
             // -infinity stands for FP16's lowest value where that has no weight; else it is told apart
-            const bool apart = (-65504.f - k.top) * k.c > -200.f;
+            const bool apart = (-65504.f - sh.scale.top) * sh.scale.c > -200.f;
             if (cmd.rest)
-                under = apart ? count_window<true, true>(s, k, cmd.high, cmd.low, smem_u32(sh.count), &exact)
-                              : count_window<true, false>(s, k, cmd.high, cmd.low, smem_u32(sh.count), &exact);
+                under = apart ? count_window<true, true>(s, sh.scale, cmd.high, cmd.low, smem_u32(sh.count), &exact)
+                              : count_window<true, false>(s, sh.scale, cmd.high, cmd.low, smem_u32(sh.count), &exact);
             else
-                under = count_window<false, false>(s, k, cmd.high, cmd.low, smem_u32(sh.count), &exact);
+                under = count_window<false, false>(s, sh.scale, cmd.high, cmd.low, smem_u32(sh.count), &exact);
             send_rest(exact, under);
         } else if (cmd.op == kRestOf) {
-            send_rest(cmd.rest ? quick_rest(s, k, cmd.low) : exact_rest(s, k, cmd.low), kLowest);
+            send_rest(cmd.rest ? quick_rest(s, sh.scale, cmd.low) : exact_rest(s, sh.scale, cmd.low), kLowest);
         } else {  // tokens of one logit, warp by warp in the order of their ids
             const int n = s.p1 - s.p0, w0 = s.p0 + (int)((int64_t)n * warp / kWarps),
                       w1 = s.p0 + (int)((int64_t)n * (warp + 1) / kWarps);
@@ -1174,8 +1186,8 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
                     // 4; of the exponent its rounding, 68 ln 2 / 2, and the low word of c, which the difference from the
                     // largest is not multiplied with, 60 ln 2 / 2.
                     u64 error = 0;
-                    const u64 small = (u64)a.vocab << k.places >> 42;
-                    const u64 spare = ((u64)a.vocab >> (60 - k.places)) + (u64)s.pieces + kThreads * kMaxCluster + 64;
+                    const u64 small = (u64)a.vocab << sh.scale.places >> 42;
+                    const u64 spare = ((u64)a.vocab >> (60 - sh.scale.places)) + (u64)s.pieces + kThreads * kMaxCluster + 64;
                     if (cmd.op == kFirst) {
                         const u64 units = (u64)((s.p1 - s.p0) / (kGroup * kThreads)) + 80;
                         error = sum ? (rest >> 24) * units + units + small + spare : 0;
@@ -1183,11 +1195,11 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
                     } else if (cmd.op == kWindow && cmd.rest) {
                         error = min((rest >> 24) * 24 + small, (rest >> 24) * 42) + spare;
                     } else if (cmd.op == kRestOf && cmd.rest) {
-                        error = (rest >> 26) + ((u64)a.vocab * 2 >> quick_places(k.places)) + kThreads * kMaxCluster;
+                        error = (rest >> 26) + ((u64)a.vocab * 2 >> quick_places(sh.scale.places)) + kThreads * kMaxCluster;
                     }
                     if (!more) rest = error = 0;
                     if (warp < 2 && (warp == 0 || error))
-                        decide(sh, wish, more, warp, warp ? rest + error : rest > error ? rest - error : 0,
+                        decide(sh, more, warp, warp ? rest + error : rest > error ? rest - error : 0,
                                &sh.found[2 * warp], &sh.ending[warp]);
                     __syncthreads();
                     if (tid == 0 && error) {
@@ -1252,7 +1264,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
                             else if (sh.ending[0].ok == kBelow && !exact)
                                 next = {kWindow, below, window_low(below), 1, 0, 0, 0};
                             else if (cmd.op == kWindow && cmd.rest && more)
-                                next = {kRestOf, top, cmd.low, quick_fits(k), 0, 0, 0};
+                                next = {kRestOf, top, cmd.low, quick_fits(sh.scale), 0, 0, 0};
                             else if (cmd.op == kRestOf && cmd.rest)
                                 next = {kRestOf, top, cmd.low, 0, 0, 0, 0};
                             else
@@ -1273,63 +1285,63 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
                             sh.win_sum[windows + 1] = w.sum;
                             __syncwarp();
                             win = windows++;
-                            bool on = more && w.count < wish.k;
-                            if (on && wish.k == kAll) {
-                                if (wish.p < 1.f) on = w.sum < times(wish.p, whole, true);
-                                else if (!(wish.m > 0.f)) on = !(wish.u < 1.f) || w.sum <= times(wish.u, whole, false);
-                                on = on && !(wish.m > 0.f && !at_least(k, cmd.low, wish.m));
+                            bool on = more && w.count < sh.wish.k;
+                            if (on && sh.wish.k == kAll) {
+                                if (sh.wish.p < 1.f) on = w.sum < times(sh.wish.p, whole, true);
+                                else if (!(sh.wish.m > 0.f)) on = !(sh.wish.u < 1.f) || w.sum <= times(sh.wish.u, whole, false);
+                                on = on && !(sh.wish.m > 0.f && !at_least(sh.scale, cmd.low, sh.wish.m));
                             }
                             if (on) {
                                 next = {kWindow, below, window_low(below), 0, 0, 0, 0};
                             } else {
-                                kept = wish.k <= w.count || !more ? min(wish.k, w.count) : kAll;
+                                kept = sh.wish.k <= w.count || !more ? min(sh.wish.k, w.count) : kAll;
                                 kept_sum = kept == kAll ? whole : (find(sh, kByCount, kept, 0, f), f->sum);
                                 stage = kTopP;
                             }
                         }
                         while (next.op == kDone && !done && need < 0) {
                             if (stage == kTopP) {
-                                if (!(wish.p < 1.f)) {
+                                if (!(sh.wish.p < 1.f)) {
                                     stage = kMinP;
                                     continue;
                                 }
-                                const u64 target = times(wish.p, kept_sum, true);
+                                const u64 target = times(sh.wish.p, kept_sum, true);
                                 int v = 0;
                                 while (v + 1 < windows && sh.win_sum[v + 1] < target) ++v;
                                 if (v != win) {
                                     need = v;
                                     continue;
                                 }
-                                find_top_p(sh, wish.p, kept_sum, f);
+                                find_top_p(sh, sh.wish.p, kept_sum, f);
                                 if (f->n && f->n <= kept) kept = f->n, kept_sum = f->sum;
                                 __syncwarp();
                                 stage = kMinP;
                             } else if (stage == kMinP) {
-                                if (!(wish.m > 0.f)) {
+                                if (!(sh.wish.m > 0.f)) {
                                     stage = kPick;
                                     continue;
                                 }
                                 int v = 0;
-                                while (v + 1 < windows && at_least(k, sh.win_high[v + 1], wish.m)) ++v;
+                                while (v + 1 < windows && at_least(sh.scale, sh.win_high[v + 1], sh.wish.m)) ++v;
                                 if (v != win) {
                                     need = v;
                                     continue;
                                 }
-                                find_min(sh, wish.m, f);
+                                find_min(sh, sh.wish.m, f);
                                 if (f->n < kept) kept = f->n, kept_sum = f->sum;
                                 __syncwarp();
                                 stage = kPick;
                             } else {
-                                const u64 target = times(wish.u, kept_sum, false);
+                                const u64 target = times(sh.wish.u, kept_sum, false);
                                 int v_last = 0, v = 0;
                                 while (v_last + 1 < windows && sh.win_count[v_last + 1] < kept) ++v_last;
                                 while (v < v_last && sh.win_sum[v + 1] <= target) ++v;
-                                if (!(wish.u < 1.f)) v = v_last;
+                                if (!(sh.wish.u < 1.f)) v = v_last;
                                 if (v != win) {
                                     need = v;
                                     continue;
                                 }
-                                if (wish.u < 1.f) find(sh, kPass, 0, target, f), at = *f;
+                                if (sh.wish.u < 1.f) find(sh, kPass, 0, target, f), at = *f;
                                 __syncwarp();
                                 if (!at.n || at.n > kept) find(sh, kByCount, min(kept, w.count), 0, f), at = *f;
                                 total = kept_sum;
