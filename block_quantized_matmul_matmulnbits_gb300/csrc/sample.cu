@@ -234,6 +234,13 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// Another CTA's shared memory is there once it has started: said at the start, waited for before the first store to it.
+__device__ __forceinline__ void cluster_started() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait_started() {
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 // The lowest order of a window from `high` down.
 __device__ __forceinline__ uint32_t window_low(uint32_t high) {
     return high >= kLowest + kBins ? high - (kBins - 1) : kLowest;
@@ -829,6 +836,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t rank = a.cluster > 1 ? cluster_rank() : 0;
     const int64_t row = blockIdx.x / (unsigned)a.cluster;
+    cluster_started();
     auto clear = [&](int bins) {
         for (int i = tid; i < bins; i += kThreads) sh.count[i] = 0;
     };
@@ -981,6 +989,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
     const uint32_t cta_top = block_max(sh, look.bad ? 0xFFFFu : order16(__half_as_ushort(__float2half_rn(look.best))));
     // (the barrier of the maximum lies behind the lists' last entries)
     if (__reduce_max_sync(kFull, sh.listed[lane & (kWarps - 1)]) > kEach) reach = 0xFFFFu;
+    cluster_wait_started();
     if (tid < a.cluster) {
         st_cluster(in_cta(smem_u32(&sh.top[rank]), tid), cta_top);
         st_cluster(in_cta(smem_u32(&sh.reach[rank]), tid), reach);
