@@ -23,10 +23,10 @@
 // the others' lists are counted with remote atomics (integers: their order does not matter).
 //
 // What bounds it: the chain of a row, not the memory.  512 rows of 151,936 with top-p 0.7 to 0.98 and temperatures
-// 0.6 to 1.2: 121 us (a read of them 23); the first look 25, the search in the list 8 to 14, twice, since the rows' CTAs
+// 0.6 to 1.2: 120 us (a read of them 23); the first look 25, the search in the list 7 to 12, twice, since the rows' CTAs
 // fill the GPU 1.7 times; 120 rows have a window more, 40 us beside one another, and the call ends with the one that has
-// two or three (179 us where those took the exact rest).  128 rows with mixed limits 51, 300 of 50,257 without any 49,
-// one of 49,152 14, of which the look is 3.
+// two or three (179 us where those took the exact rest).  128 rows with mixed limits 50, 300 of 50,257 without any 48,
+// one of 49,152 13, of which the look is 3, barriers of the cluster 3 and the search 5.
 #include <cuda_fp16.h>
 
 #include "common.cuh"
@@ -1407,9 +1407,9 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 // CTAs of a row: enough for two on every SM (four fit), of at least 4096 logits each (128 rows of 151,936 with mixed limits:
-// 52 us, enough for one 67, for three 52); two at least for a long row, which has to be gone through again where its
-// limits lie far down, and is what the call then ends with (512 rows of 151,936 with top-p: 122 us with two, 160 with
-// one, 141 with four; with none but likely tokens kept 58, 48 and 78).
+// 50 us, enough for one 66, for three 50); two at least for a long row, which has to be gone through again where its
+// limits lie far down, and is what the call then ends with (512 rows of 151,936 with top-p: 120 us with two, 156 with
+// one, 141 with four; with none but likely tokens kept 55, 45 and 72).
 int cluster_for(int64_t rows, int64_t vocab, int sms) {
     int c = vocab > 1 << 17 ? 2 : 1;
     while (c < kMaxCluster && rows * c < (int64_t)sms * 2 && vocab >= (int64_t)c * 2 * 4096) c *= 2;
