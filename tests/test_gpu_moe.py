@@ -120,3 +120,27 @@ def test_repeats_give_the_same_bits_and_streams_and_graphs_work():
         torch.cuda.synchronize()
         ref = ex.ref(X, 4, True)
         assert np.all(np.abs(y.cpu().numpy() - ref[2]) <= ref[3])
+
+
+def test_offsets_past_32_bits():
+    K, I, E, where = 4096, 2048, 256, [3, 255]
+    ex = Experts(16, K, I, 2, 8, True)
+    small = ex.layer(torch, mnb, 2, True)
+
+    def spread(t):
+        big = torch.zeros(E, *t.shape[1:], dtype=t.dtype, device="cuda")
+        big[where] = t
+        return big
+
+    router, *weights = small.kept
+    router, weights = spread(router), [spread(t) for t in weights]
+    rest = torch.ones(E, dtype=torch.bool)
+    rest[where] = False
+    router[rest.cuda()] = -0.1  # far below, of positive inputs
+    uw, us, uz, dw, ds, dz = weights
+    layer = mnb.MoE(router, uw, us, dw, ds, top_k=2, bits=8, up_zp=uz, down_zp=dz, normalize=True)
+    X = np.abs(ex.rng.standard_normal((3, K))).astype(np.float16)
+    ids, w, y = run(layer, X)
+    want = ex.ref(X, 2, True)
+    assert np.array_equal(ids, np.array(where)[want[0]])
+    assert np.all(np.abs(y - want[2]) <= want[3])

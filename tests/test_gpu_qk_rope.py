@@ -155,3 +155,17 @@ def test_many_tokens_and_many_sequences():
     q = dev(Q)
     mnb.mnb_qk_rope(mnb.Rope(D, dev(f), True), b, q)
     near(q, rope_ref(Q, pos, f, True))
+
+
+@pytest.mark.parametrize("tokens,stride", [(5, (1 << 29) + 8), (4001, (1 << 20) + 8)])
+def test_offsets_past_32_bits(tokens, stride):
+    # one token a CTA and several
+    r = np.random.default_rng(tokens)
+    Q, K = half(r, tokens, 3, 64), half(r, tokens, 1, 64)
+    flat = torch.empty((tokens - 1) * stride + 256, dtype=torch.float16, device="cuda")
+    q, k = flat.as_strided((tokens, 3, 64), (stride, 64, 1)), flat[192:].as_strided((tokens, 1, 64), (stride, 64, 1))
+    q.copy_(torch.from_numpy(Q)), k.copy_(torch.from_numpy(K))
+    pos, f, gain = np.arange(tokens) * 7, freqs(32), half(r, 64) + np.float16(1)
+    mnb.mnb_qk_rope(mnb.Rope(64, dev(f), q_weight=dev(gain)), dev(np.int32(pos)), q, k)
+    for x, o, g in ((Q, q, gain), (K, k, None)):
+        near(o.contiguous(), rope_ref(x, pos, f, False, g))

@@ -195,3 +195,12 @@ def test_a_replayed_graph_takes_new_settings():
         graph.replay()
         torch.cuda.synchronize()
         assert token.tolist() == [sample_ref(x[i], us[i], ts[i], ks[i])[0] for i in range(4)]
+
+
+def test_offsets_past_32_bits():
+    r, x = logits(84, 3, 1000)
+    stride = (1 << 30) + 5
+    flat = torch.empty(2 * stride + 1000, dtype=torch.float16, device="cuda")
+    rows = flat.as_strided((3, 1000), (stride, 1))
+    rows.copy_(torch.from_numpy(x))
+    check(x, r.uniform(0, 1, 3), top_p=[0.9, 1.0, 0.5], xd=rows)
