@@ -140,3 +140,44 @@ def test_the_example_with_experts_and_drawn_tokens(kw):
     assert tokens.shape == (40, 4) and tokens.min() >= 0 and tokens.max() < 1000 and ms > 0
     assert torch.all(torch.isfinite(logps)) and torch.all(logps < 0)
     assert apart.abs().median().item() < 0.25
+
+
+def test_calls_on_two_streams_at_once():
+    r = np.random.default_rng(77)
+    ex = Experts(78, 512, 256, 16, 4, True)
+    layer = ex.layer(torch, mnb, 4, True)
+    dev = lambda a: torch.from_numpy(a).cuda()  # noqa: E731
+    rope = mnb.Rope(64, dev((10000.0 ** (-np.arange(32) / 32)).astype(np.float32)))
+
+    class Lane:
+        def __init__(self, tokens):
+            self.x, self.y = dev(r.standard_normal((tokens, 512)).astype(np.float16)), None
+            self.pos = torch.arange(tokens, dtype=torch.int32, device="cuda") * 1000
+            self.turned, self.y = torch.empty(tokens, 8, 64, dtype=torch.float16, device="cuda"), torch.empty_like(self.x)
+            self.ws = mnb.moe_workspace(layer, tokens)
+            self.logits = dev((r.standard_normal((tokens, 40003)) * 2).astype(np.float16))
+            self.u, self.p = (dev(r.uniform(0, 1, tokens).astype(np.float32)) for _ in range(2))
+            self.token = torch.empty(tokens, dtype=torch.int64, device="cuda")
+
+        def run(self):
+            mnb.mnb_qk_rope(rope, self.pos, self.x.view(-1, 8, 64), Q_out=self.turned)
+            mnb.mnb_moe(layer, self.turned.view(-1, 512), self.y, ws=self.ws)
+            mnb.mnb_sample(self.logits, self.u, self.token, top_p=self.p)
+            return self.turned, self.y, self.token
+
+    lanes = [Lane(3), Lane(16)]
+    torch.cuda.synchronize()
+    want = [[t.clone() for t in lane.run()] for lane in lanes]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in lanes]
+    for _ in range(20):
+        for lane, s in zip(lanes, streams):
+            for t in (lane.turned, lane.y):
+                t.zero_()
+        torch.cuda.synchronize()
+        for lane, s in zip(lanes, streams):
+            with torch.cuda.stream(s):
+                lane.run()
+        torch.cuda.synchronize()
+        for lane, w in zip(lanes, want):
+            assert all(torch.equal(a, b) for a, b in zip((lane.turned, lane.y, lane.token), w))
